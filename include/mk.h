@@ -36,10 +36,12 @@ typedef enum {
   MK_ERR_CUDA = 3,       /* a CUDA runtime call failed                                   */
   MK_ERR_TIMEOUT = 4,    /* a device-side wait ran past its limit; the step was abandoned */
   MK_ERR_STATE = 5,      /* context unusable until mk_reset (after a timeout)            */
-  MK_ERR_NAN = 6         /* a logit was NaN; the returned token is meaningless           */
+  MK_ERR_NAN = 6,        /* a logit was NaN; the returned token is meaningless           */
+  MK_ERR_PAGES = 7       /* paged cache: a bad page, row, length or parent, or no free page */
 } mk_status;
 
-typedef enum { MK_F16 = 0, MK_BF16 = 1 } mk_dtype;
+/* MK_F32 is a type of the paged operators' vectors and logits only, not of a model. */
+typedef enum { MK_F16 = 0, MK_BF16 = 1, MK_F32 = 2 } mk_dtype;
 typedef enum { MK_SYNC_COUNTER = 0, MK_SYNC_SENTINEL = 1 } mk_sync_mode;
 /* MK_EXEC_GRAPH: the multi-launch control captured once per batch size into a CUDA graph
  * whose launches are programmatic dependent launches (each grid's loader streams its
@@ -314,6 +316,178 @@ mk_status mk_decode_step_noalloc(const mk_model_desc *desc, const mk_weights *we
  * three timed runs.  Allocates total_bytes of device memory for the run (hint bit 1:
  * total_bytes / #SM). */
 mk_status mk_stream_bench(int page_bytes, int n_pages, int mode, int hint, long long total_bytes, double *gbps);
+
+/* ---------------------------------------------------------------------------------------
+ * Operators over a paged KV cache, and the selection of a beam search.
+ *
+ * A layer's keys and values lie in pages [n_kv_heads][page_size][head_dim]; a page table
+ * row per sequence names its pages in order: position t of row r is row t % page_size of
+ * page table[r][t / page_size].  Rows may share pages (a common prompt, beams); refs counts
+ * the holders of each page, and a page nobody holds (0) is free.
+ *
+ * Every call below enqueues kernels on `stream` (a cudaStream_t; NULL = legacy) of the
+ * current device and returns at once; it allocates nothing, copies nothing to the host and
+ * can be captured into a graph.  All pointers are device memory of that device.  Workspaces
+ * are the caller's: a call may overwrite its workspace, needs nothing in it beforehand, and
+ * calls that may run at the same time need one each.
+ *
+ * What only the device can see is reported through `status`, a device int32[4] the caller
+ * zeroes (NULL: not reported): the first error found is kept as {mk_status, operator, row,
+ * value} (operator: 1 append, 2 attention, 3 update, 4 compaction, 5 selection) and
+ * mk_paged_status reads it back.  A bad index is never followed: each call says what it
+ * does instead. */
+typedef struct {
+  void *k, *v;             /* one layer's pages, 16-byte aligned                            */
+  long long page_stride;   /* elements from one page to the next, a multiple of 8           */
+  int n_pages, n_kv_heads, page_size, head_dim;  /* page_size a multiple of 16 up to 1024;
+                              head_dim 64 or 128                                            */
+  int dtype;               /* MK_F16 or MK_BF16                                             */
+  const int32_t* table;    /* [n_rows][table_stride], the first table_width entries used    */
+  int n_rows, table_width;
+  long long table_stride;
+} mk_page_view;
+
+/* Rotary frequencies.  Pair i of the rotated part (n_rot elements of a head) turns by
+ * position * theta^(-2i / n_rot), scaled for contexts longer than `original` positions:
+ *   0 none; 1 linear: every frequency / factor; 2 base: theta * factor^(n_rot / (n_rot - 2));
+ *   3 blended: pairs that turn more than beta_fast times within `original` positions keep
+ *     their frequency, those below beta_slow are divided by factor, between them the two
+ *     are mixed linearly in the pair index; cos and sin get the factor 0.1 ln(factor) + 1;
+ *   4 by wavelength: pairs that turn more than beta_fast times within `original` positions
+ *     keep their frequency, those below beta_slow are divided by factor, between them the
+ *     two are mixed linearly in the number of turns.                                      */
+typedef struct {
+  double theta;
+  int n_rot;               /* even, in [2, 128] (kind 2: at least 4)                        */
+  int kind;
+  double factor;           /* >= 1                                                          */
+  double original, beta_fast, beta_slow;  /* kinds 3 (0: 32 and 1) and 4 (0: 4 and 1)       */
+} mk_rope_desc;
+/* freqs host [n_rot / 2] and the factor of cos and sin (host only, no GPU needed). */
+mk_status mk_rope_freqs(const mk_rope_desc* desc, double* freqs, float* mscale);
+
+/* Rotary positions and append: token t (position positions[t] of table row rows[t]) has its
+ * key rotated and written to its page, its value written beside it, and its query rotated
+ * into q_out.  Angles are reduced in 64 bits (positions up to 2^31 - 1), the rotation is
+ * done in 32 bits and rounded once.  A token whose position is negative is skipped: neither
+ * the cache nor its row of q_out is written.  A row outside the table, a position past
+ * table_width * page_size or a bad page is reported (MK_ERR_PAGES) and nothing is cached
+ * for that token; its query is rotated all the same.  Two tokens of one call at the same
+ * position of the same page leave one of the two vectors' values, element by element. */
+typedef struct {
+  const void *q, *k, *v;   /* [n_tokens][heads][head_dim], element strides below; q and
+                              q_out NULL: no queries                                        */
+  void* q_out;             /* may be q itself (same strides)                                */
+  int dtype;               /* of q, k, v and q_out: MK_F16, MK_BF16 or MK_F32               */
+  int n_tokens, n_heads;
+  long long q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
+  const int32_t* positions;
+  const int32_t* rows;     /* NULL: token t is row t                                        */
+  const double* freqs;     /* [n_freqs]: radians per position of each pair                  */
+  int n_freqs;             /* rotated pairs; 2 n_freqs <= head_dim; 0: nothing is rotated   */
+  int interleaved;         /* 0: pairs (i, i + n_freqs); 1: pairs (2i, 2i + 1)              */
+  float mscale;            /* factor of cos and sin                                         */
+} mk_append_args;
+mk_status mk_rope_append(const mk_append_args* args, const mk_page_view* cache, int32_t* status, void* stream);
+
+/* Attention of one new query per row over its paged positions:
+ *   s_t = cap(scale * q . k_t),  cap(x) = softcap * tanh(x / softcap) (softcap 0: x),
+ *   out = sum_t e^(s_t) v_t / sum_t e^(s_t),  lse = log sum_t e^(s_t)   (natural log)
+ * over t in [max(0, n - window), n) (window 0: [0, n)), n = lens[r] + len_add.  Query head h
+ * reads kv head h / (n_heads / n_kv_heads).  A row without positions (n <= 0) or whose
+ * scores are all -inf gets zeros and lse -inf.  Nothing outside that range is read for its
+ * value: whatever lies there, NaN included, has no effect.  A row outside the table counts
+ * as empty, positions past the table are dropped and those on a bad page masked, each of
+ * them reported (MK_ERR_PAGES).  A query that is not of the cache's type must lie within
+ * the cache type's range.  Results do not depend on timing. */
+typedef struct {
+  const void* q;           /* [n_rows][n_heads][head_dim], element strides below            */
+  void* out;
+  float* lse;              /* [n_rows][n_heads] or NULL                                     */
+  int dtype;               /* of q and out: MK_F16, MK_BF16 or MK_F32                       */
+  int n_rows, n_heads;     /* n_heads / n_kv_heads: 1..16                                   */
+  long long q_row, q_head, o_row, o_head;
+  const int32_t* lens;
+  int len_add;
+  const int32_t* rows;     /* table row of each query; NULL: query r is row r               */
+  float scale, softcap;
+  int window;
+  void* workspace;         /* 16-byte aligned                                               */
+  size_t workspace_bytes;
+} mk_attend_args;
+mk_status mk_paged_attention(const mk_attend_args* args, const mk_page_view* cache, int32_t* status, void* stream);
+/* Bytes of workspace a call needs on the current device; depends on head_dim and on
+ * n_heads / n_kv_heads, not on rows or lengths. */
+mk_status mk_paged_attention_workspace(int n_heads, int n_kv_heads, int head_dim, size_t* bytes);
+
+/* Pages of every layer: planes (layer, k or v) of n_pages pages each. */
+typedef struct {
+  void *k, *v;             /* 16-byte aligned                                               */
+  int n_layers, n_pages, page_size;
+  long long page_bytes;    /* bytes of one page of one plane, a multiple of 16              */
+  long long page_stride, layer_stride;  /* bytes, multiples of 16                           */
+  int32_t* table;          /* [n_rows][table_stride]; entries below 0 hold no page          */
+  int n_rows, table_width;
+  long long table_stride;
+  int32_t* refs;           /* [n_pages] holders of each page; 0: free                       */
+} mk_page_pool;
+
+/* Fork, free and reserve in one step (all rows at once, from the state before the call).
+ * Row r continues the sequence of row parents[r] (NULL: its own; -1: it is freed): it takes
+ * over that row's lens and the pages of its positions, and releases every other page it
+ * held.  With reserve[r] = m > 0 the row then gets what the next m positions need: a partly
+ * filled last page that another holder shares is copied (in every layer) to a page of its
+ * own -- of the rows that share it, the last one keeps it if nobody else holds it -- and
+ * new pages follow.  reserve[r] = 0 (NULL: all 0) only shares.  Pages are taken lowest free
+ * first, rows in order, a row's copy before its new pages; pages this call released count
+ * as free.  If a parent is out of range, a row would outgrow the table, or the free pages
+ * do not suffice, nothing is changed and status reports MK_ERR_PAGES.  A table entry that
+ * names no page is reported and treated as -1.  n_rows at most 4096. */
+typedef struct {
+  int32_t* lens;           /* [n_rows] in and out: positions in each row                    */
+  const int32_t* parents;
+  const int32_t* reserve;
+  void* workspace;         /* 16-byte aligned                                               */
+  size_t workspace_bytes;
+} mk_update_args;
+mk_status mk_update_pages(const mk_update_args* args, const mk_page_pool* pool, int32_t* status, void* stream);
+/* Compaction: with u pages held, the held pages at u and above move, in order, to the lowest
+ * free pages (in every layer; the table and refs follow), so that the pages from u on are
+ * free.  Holders outside this table are not renamed: compact only what one table names. */
+mk_status mk_compact_pages(const mk_page_pool* pool, void* workspace, size_t workspace_bytes, int32_t* status,
+                           void* stream);
+/* Bytes of workspace mk_update_pages and mk_compact_pages need. */
+mk_status mk_update_pages_workspace(int n_rows, int table_width, int n_pages, size_t* bytes);
+
+/* One step of a beam search.  Group g has `beams` rows of logits (row g * beams + b), each
+ * with the sum of log probabilities so far (scores) and a flag that it has ended.  A beam
+ * that has not ended offers every token at scores + log softmax(logits); one that has ended
+ * offers token `eos` at its own score.  The `beams` best of the group are chosen, best
+ * first: tokens, parents (the row chosen from: what mk_update_pages takes), scores, ended.
+ * Within a beam the order is by logit, ties to the lowest token; between beams by the score
+ * in 64 bits, ties to the lower beam.  A NaN or +inf logit is reported (MK_ERR_NAN) and
+ * counts as -inf, as does a NaN score; a token at -inf is only chosen when nothing else is
+ * left.  Outputs must not overlap the inputs. */
+typedef struct {
+  const void* logits;      /* [groups * beams][row_stride], the first vocab entries used    */
+  int dtype;               /* MK_F16, MK_BF16 or MK_F32                                     */
+  long long row_stride;    /* elements                                                      */
+  int groups, beams, vocab;  /* beams 1..32, at most vocab                                  */
+  int eos;                 /* the token that ends a beam, or -1: none does                  */
+  const float* scores;     /* [groups][beams]                                               */
+  const int32_t* ended;    /* [groups][beams]                                               */
+  int32_t *out_tokens, *out_parents;
+  float* out_scores;
+  int32_t* out_ended;
+  void* workspace;         /* 16-byte aligned                                               */
+  size_t workspace_bytes;
+} mk_select_args;
+mk_status mk_beam_select(const mk_select_args* args, int32_t* status, void* stream);
+mk_status mk_beam_select_workspace(int groups, int beams, int vocab, size_t* bytes);
+
+/* Reads the device status word back (synchronises the stream): MK_OK, or the code found,
+ * with its text in mk_last_error.  The word is cleared. */
+mk_status mk_paged_status(int32_t* status, void* stream);
 
 const char *mk_last_error(void);
 const char *mk_status_string(mk_status s);

@@ -19,8 +19,8 @@ if not os.path.exists(LIB_PATH):
         f"{LIB_PATH} is missing: build it with __graft_entry__.build(); the decode path has no CPU fallback")
 lib = ctypes.CDLL(LIB_PATH)
 
-MK_OK, MK_ERR_INVALID, MK_ERR_OCCUPANCY, MK_ERR_CUDA, MK_ERR_TIMEOUT, MK_ERR_STATE, MK_ERR_NAN = range(7)
-MK_F16, MK_BF16 = 0, 1
+MK_OK, MK_ERR_INVALID, MK_ERR_OCCUPANCY, MK_ERR_CUDA, MK_ERR_TIMEOUT, MK_ERR_STATE, MK_ERR_NAN, MK_ERR_PAGES = range(8)
+MK_F16, MK_BF16, MK_F32 = 0, 1, 2
 MK_SYNC_COUNTER, MK_SYNC_SENTINEL = 0, 1
 MK_EXEC_PERSISTENT, MK_EXEC_MULTILAUNCH, MK_EXEC_GRAPH = 0, 1, 2
 
@@ -67,6 +67,53 @@ class mk_trace_rec(ctypes.Structure):
                 ("t_end", ctypes.c_uint64)]
 
 
+c_ll, c_size_t = ctypes.c_longlong, ctypes.c_size_t
+
+
+class mk_page_view(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("page_stride", c_ll), ("n_pages", c_int), ("n_kv_heads", c_int),
+                ("page_size", c_int), ("head_dim", c_int), ("dtype", c_int), ("table", c_void_p), ("n_rows", c_int),
+                ("table_width", c_int), ("table_stride", c_ll)]
+
+
+class mk_rope_desc(ctypes.Structure):
+    _fields_ = [("theta", c_double), ("n_rot", c_int), ("kind", c_int), ("factor", c_double), ("original", c_double),
+                ("beta_fast", c_double), ("beta_slow", c_double)]
+
+
+class mk_append_args(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("q_out", c_void_p), ("dtype", c_int),
+                ("n_tokens", c_int), ("n_heads", c_int), ("q_token", c_ll), ("q_head", c_ll), ("k_token", c_ll),
+                ("k_head", c_ll), ("v_token", c_ll), ("v_head", c_ll), ("o_token", c_ll), ("o_head", c_ll),
+                ("positions", c_void_p), ("rows", c_void_p), ("freqs", c_void_p), ("n_freqs", c_int),
+                ("interleaved", c_int), ("mscale", c_float)]
+
+
+class mk_attend_args(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("out", c_void_p), ("lse", c_void_p), ("dtype", c_int), ("n_rows", c_int),
+                ("n_heads", c_int), ("q_row", c_ll), ("q_head", c_ll), ("o_row", c_ll), ("o_head", c_ll),
+                ("lens", c_void_p), ("len_add", c_int), ("rows", c_void_p), ("scale", c_float), ("softcap", c_float),
+                ("window", c_int), ("workspace", c_void_p), ("workspace_bytes", c_size_t)]
+
+
+class mk_page_pool(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("n_layers", c_int), ("n_pages", c_int), ("page_size", c_int),
+                ("page_bytes", c_ll), ("page_stride", c_ll), ("layer_stride", c_ll), ("table", c_void_p),
+                ("n_rows", c_int), ("table_width", c_int), ("table_stride", c_ll), ("refs", c_void_p)]
+
+
+class mk_update_args(ctypes.Structure):
+    _fields_ = [("lens", c_void_p), ("parents", c_void_p), ("reserve", c_void_p), ("workspace", c_void_p),
+                ("workspace_bytes", c_size_t)]
+
+
+class mk_select_args(ctypes.Structure):
+    _fields_ = [("logits", c_void_p), ("dtype", c_int), ("row_stride", c_ll), ("groups", c_int), ("beams", c_int),
+                ("vocab", c_int), ("eos", c_int), ("scores", c_void_p), ("ended", c_void_p), ("out_tokens", c_void_p),
+                ("out_parents", c_void_p), ("out_scores", c_void_p), ("out_ended", c_void_p), ("workspace", c_void_p),
+                ("workspace_bytes", c_size_t)]
+
+
 def _fn(name, argtypes, restype=c_int):
     f = getattr(lib, name)
     f.argtypes = argtypes
@@ -99,6 +146,18 @@ mk_stream_bench = _fn("mk_stream_bench", [c_int, c_int, c_int, c_int, ctypes.c_l
 mk_decode_step_noalloc = _fn("mk_decode_step_noalloc", [ctypes.POINTER(mk_model_desc), ctypes.POINTER(mk_weights),
                                                         ctypes.POINTER(mk_kv), P_i32, P_i32, c_int, P_i32, c_void_p,
                                                         c_void_p])
+P_size = ctypes.POINTER(c_size_t)
+mk_rope_freqs = _fn("mk_rope_freqs", [ctypes.POINTER(mk_rope_desc), ctypes.POINTER(c_double), P_f32])
+mk_rope_append = _fn("mk_rope_append", [ctypes.POINTER(mk_append_args), ctypes.POINTER(mk_page_view), c_void_p, c_void_p])
+mk_paged_attention = _fn("mk_paged_attention", [ctypes.POINTER(mk_attend_args), ctypes.POINTER(mk_page_view), c_void_p,
+                                                c_void_p])
+mk_paged_attention_workspace = _fn("mk_paged_attention_workspace", [c_int, c_int, c_int, P_size])
+mk_update_pages = _fn("mk_update_pages", [ctypes.POINTER(mk_update_args), ctypes.POINTER(mk_page_pool), c_void_p, c_void_p])
+mk_compact_pages = _fn("mk_compact_pages", [ctypes.POINTER(mk_page_pool), c_void_p, c_size_t, c_void_p, c_void_p])
+mk_update_pages_workspace = _fn("mk_update_pages_workspace", [c_int, c_int, c_int, P_size])
+mk_beam_select = _fn("mk_beam_select", [ctypes.POINTER(mk_select_args), c_void_p, c_void_p])
+mk_beam_select_workspace = _fn("mk_beam_select_workspace", [c_int, c_int, c_int, P_size])
+mk_paged_status = _fn("mk_paged_status", [c_void_p, c_void_p])
 mk_last_error = _fn("mk_last_error", [], ctypes.c_char_p)
 mk_status_string = _fn("mk_status_string", [c_int], ctypes.c_char_p)
 

@@ -423,6 +423,7 @@ const char* mk_status_string(mk_status s) {
     case MK_ERR_TIMEOUT: return "MK_ERR_TIMEOUT";
     case MK_ERR_STATE: return "MK_ERR_STATE";
     case MK_ERR_NAN: return "MK_ERR_NAN";
+    case MK_ERR_PAGES: return "MK_ERR_PAGES";
   }
   return "MK_ERR_UNKNOWN";
 }

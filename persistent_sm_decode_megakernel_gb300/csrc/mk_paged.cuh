@@ -1,0 +1,102 @@
+// Shared by the paged-cache operators (append, attention, page updates, beam selection):
+// launches as programmatic dependents, the device status word, type conversions.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <string>
+
+#include "../../include/mk.h"
+
+namespace mk {
+
+void set_last_error(const std::string& msg);  // defined beside mk_last_error
+
+enum PagedOp : int { PO_APPEND = 1, PO_ATTEND = 2, PO_UPDATE = 3, PO_COMPACT = 4, PO_SELECT = 5 };
+
+inline mk_status paged_fail(mk_status s, const std::string& m) {
+  set_last_error(m);
+  return s;
+}
+
+inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+inline size_t round16(size_t x) { return (x + 15) & ~size_t(15); }
+
+// Every kernel of these operators is launched as a programmatic dependent of what precedes
+// it in the stream and waits for that (pdl_wait) before it touches memory: its launch
+// overlaps the previous kernel's tail, the order of the data stays the stream's.
+template <typename... Params, typename... Args>
+inline mk_status launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, void* stream,
+                                  const char* what, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) return paged_fail(MK_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+  return MK_OK;
+}
+
+// multiprocessors of the current device (looked up once per device)
+mk_status sm_count(int* n);
+// the checks on a page view that every operator over pages applies: "" when usable
+std::string check_view(const mk_page_view* c);
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// keeps the first error found (of several found at the same time, one of them)
+__device__ __noinline__ static void report(int32_t* status, int code, int op, int row, int value) {
+  if (status != nullptr && atomicCAS(status, 0, code) == 0) {
+    status[1] = op;
+    status[2] = row;
+    status[3] = value;
+  }
+}
+
+template <typename T>
+struct Conv;
+template <>
+struct Conv<float> {
+  static __device__ __forceinline__ float up(float x) { return x; }
+  static __device__ __forceinline__ float down(float x) { return x; }
+};
+template <>
+struct Conv<__half> {
+  static __device__ __forceinline__ float up(__half x) { return __half2float(x); }
+  static __device__ __forceinline__ __half down(float x) { return __float2half_rn(x); }
+};
+template <>
+struct Conv<__nv_bfloat16> {
+  static __device__ __forceinline__ float up(__nv_bfloat16 x) { return __bfloat162float(x); }
+  static __device__ __forceinline__ __nv_bfloat16 down(float x) { return __float2bfloat16_rn(x); }
+};
+
+// 8 consecutive elements between memory (16-byte aligned) and floats
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+  alignas(16) T raw[8];
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(raw)[i] = reinterpret_cast<const uint4*>(p)[i];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = Conv<T>::up(raw[i]);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
+  alignas(16) T raw[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) raw[i] = Conv<T>::down(x[i]);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(raw)[i];
+}
+#endif
+
+}  // namespace mk

@@ -1,0 +1,422 @@
+// Page table updates of a paged KV cache (mk_update_pages: fork, free, reserve) and its
+// compaction (mk_compact_pages), with the copies of pages over all layers.
+//
+// Both are a plan of integers and a copy.  mk_update_pages takes three launches: `count`
+// (a CTA per row) moves the holders' counts from the old table to the shared part of the new
+// one and saves the old table; `plan` (one CTA) decides who copies a page, takes the lowest
+// free pages by a scan of the counts and commits, or finds that it cannot; `apply` (all SMs)
+// writes the table rows and copies the pages -- or, after a refusal, gives the counts back.
+// The counts are integer sums, so the order of their atomics does not show.
+#include <algorithm>
+
+#include "mk_paged.cuh"
+
+namespace mk {
+namespace {
+
+constexpr int kMaxRows = 4096;
+constexpr int kPlanThreads = 1024;
+constexpr int kRowThreads = 256;
+constexpr int kCopyThreads = 256;
+constexpr int kUnitBytes = kCopyThreads * 16;  // a copy's unit: one 16-byte access per thread
+constexpr int kInFlight = 4;                   // units a thread has in flight
+constexpr int kCopyCtasPerSm = 4;
+constexpr int kMost = (1 << 30) - 1;           // counts of pages saturate here
+
+struct PoolArgs {
+  char *k, *v;
+  int32_t *table, *refs, *lens, *status;
+  const int32_t *parents, *reserve;
+  long long page_bytes, page_stride, layer_stride, table_stride;
+  int n_layers, n_pages, page_size, n_rows, width;
+  // workspace
+  int32_t *head;                     // [0] refused, [1] copies
+  int32_t *held, *ends, *at, *copy;  // per row: pages taken over, pages after, first fresh page, copies its last
+  int32_t *snap;                     // [n_rows][width]: the old table, entries that name no page as -1
+  int32_t *fresh;                    // fresh pages in order (compaction: destinations)
+  int32_t *src, *dst;                // the copies (compaction: sources in src, destinations in fresh)
+  int32_t *rank;                     // compaction: [n_pages] a moved page's place in src, or -1
+};
+
+// what the workspace holds, in order
+size_t lay_out(PoolArgs* a, void* ws, long long rows, long long width, long long pages) {
+  char* p = static_cast<char*>(ws);
+  size_t at = 0;
+  auto take = [&](int32_t** out, long long n) {
+    *out = reinterpret_cast<int32_t*>(p + at);
+    at += round16(sizeof(int32_t) * (size_t)n);
+  };
+  take(&a->head, 4);
+  take(&a->held, rows);
+  take(&a->ends, rows);
+  take(&a->at, rows);
+  take(&a->copy, rows);
+  take(&a->src, std::max(rows, pages));
+  take(&a->dst, rows);
+  take(&a->fresh, pages);
+  take(&a->rank, pages);
+  take(&a->snap, rows * width);
+  return at;
+}
+
+// What row r takes over: its parent, the parent's positions and pages; false when the
+// parent or its length cannot be (the whole call is then refused).
+struct Take {
+  int parent, len, held;
+};
+__device__ __forceinline__ bool take_of(const PoolArgs& a, int r, Take* t) {
+  const int p = a.parents ? a.parents[r] : r;
+  t->parent = p;
+  t->len = t->held = 0;
+  if (p == -1) return true;
+  if ((unsigned)p >= (unsigned)a.n_rows) return false;
+  const int n = a.lens[p];
+  if (n < 0 || n > (long long)a.width * a.page_size) return false;
+  t->len = n;
+  t->held = (int)(((long long)n + a.page_size - 1) / a.page_size);
+  return true;
+}
+
+__device__ __forceinline__ int page_or_none(const PoolArgs& a, int id) { return (unsigned)id < (unsigned)a.n_pages ? id : -1; }
+
+__global__ void __launch_bounds__(kRowThreads) count_kernel(const __grid_constant__ PoolArgs a) {
+  pdl_wait();
+  pdl_launch();
+  const int r = blockIdx.x;
+  Take t;
+  const bool ok = take_of(a, r, &t);
+  const int32_t* old = a.table + (long long)r * a.table_stride;
+  const int32_t* from = a.table + (long long)(ok ? max(t.parent, 0) : r) * a.table_stride;
+  for (int i = threadIdx.x; i < a.width; i += kRowThreads) {
+    const int raw = old[i], o = page_or_none(a, raw);
+    if (raw >= a.n_pages) report(a.status, MK_ERR_PAGES, PO_UPDATE, r, raw);
+    a.snap[(long long)r * a.width + i] = o;
+    if (!ok) continue;
+    const int n = i < t.held ? page_or_none(a, from[i]) : -1;
+    if (o == n) continue;
+    if (o >= 0) atomicSub(a.refs + o, 1);
+    if (n >= 0) atomicAdd(a.refs + n, 1);
+  }
+}
+
+__device__ __forceinline__ int add_sat(int x, int y) { return min(x + y, kMost); }
+// exclusive prefix sum of one int in [0, kMost] per thread over the CTA; the total in *total
+// (with a saturated total the prefixes say nothing: the call is refused)
+__device__ __forceinline__ int block_scan(int x, int* sums, int* total) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc = add_sat(inc, y);
+  }
+  if (lane == 31) sums[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    int s = sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s = add_sat(s, y);
+    }
+    sums[lane] = s;
+  }
+  __syncthreads();
+  const int base = warp ? sums[warp - 1] : 0;
+  *total = sums[31];
+  __syncthreads();
+  return add_sat(base, inc - x);
+}
+
+// Appends to `out` the ids in [from, to) for which want(refs[id]) holds, ascending, until
+// `most` are found; returns how many were found (at most `most`).
+template <typename Want>
+__device__ __forceinline__ int list_pages(const int32_t* refs, int from, int to, int most, int32_t* out, int* sums,
+                                          Want want) {
+  int found = 0;
+  for (int base = from; base < to && found < most; base += kPlanThreads * 4) {
+    const int p0 = base + (int)threadIdx.x * 4;
+    bool is[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) is[x] = p0 + x < to && want(refs[p0 + x]);
+    int total;
+    int at = found + block_scan(is[0] + is[1] + is[2] + is[3], sums, &total);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (is[x] && at < most) out[at] = p0 + x;
+      at += is[x];
+    }
+    found = min(most, found + total);
+  }
+  return found;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PoolArgs a) {
+  __shared__ int s_sums[32], s_last[kMaxRows], s_bad;
+  const int tid = threadIdx.x;
+  pdl_wait();
+  pdl_launch();
+  if (tid == 0) s_bad = 0;
+  __syncthreads();
+  constexpr int PER = kMaxRows / kPlanThreads;
+  const int per = (a.n_rows + kPlanThreads - 1) / kPlanThreads;
+  const int r0 = min(a.n_rows, tid * per), r1 = min(a.n_rows, r0 + per);
+  int len[PER], held[PER], ends[PER], copies[PER];
+#pragma unroll
+  for (int x = 0; x < PER; ++x) {
+    const int r = r0 + x;
+    len[x] = held[x] = ends[x] = copies[x] = 0;
+    if (r >= r1) continue;
+    Take t;
+    bool ok = take_of(a, r, &t);
+    const int room = ok && t.parent >= 0 && a.reserve ? max(0, a.reserve[r]) : 0;
+    const long long e = ((long long)t.len + room + a.page_size - 1) / a.page_size;
+    if (room > 0 && e > a.width) ok = false;
+    if (!ok) {
+      report(a.status, MK_ERR_PAGES, PO_UPDATE, r, t.parent);
+      s_bad = 1;
+      t.len = t.held = 0;
+    }
+    len[x] = t.len;
+    held[x] = t.held;
+    ends[x] = ok && room > 0 ? (int)e : t.held;
+    // the page this row will write into: its last, when it is partly filled
+    int last = -1;
+    if (ok && room > 0 && t.len % a.page_size) last = a.snap[(long long)t.parent * a.width + t.held - 1];
+    s_last[r] = last;
+  }
+  __syncthreads();
+  // of the rows that write into one page, each copies it while another holder is left
+  int need = 0, mine = 0;
+#pragma unroll
+  for (int x = 0; x < PER; ++x) {
+    const int r = r0 + x;
+    if (r >= r1) continue;
+    const int last = s_last[r];
+    if (last >= 0) {
+      const int holders = a.refs[last];
+      if (holders > 1) {
+        int before = 0;
+        for (int q = 0; q < r; ++q) before += s_last[q] == last;
+        copies[x] = before < holders - 1;
+      }
+    }
+    need = add_sat(need, copies[x] + ends[x] - held[x]);
+    mine += copies[x];
+  }
+  int total, n_copies;
+  int at = block_scan(need, s_sums, &total);
+  int c = block_scan(mine, s_sums, &n_copies);
+  bool refused = s_bad != 0;
+  int found = 0;
+  if (!refused && total > 0)
+    found = list_pages(a.refs, 0, a.n_pages, min(total, a.n_pages), a.fresh, s_sums, [](int n) { return n == 0; });
+  if (!refused && found < total) {
+    refused = true;
+    if (tid == 0) report(a.status, MK_ERR_PAGES, PO_UPDATE, -1, total - found);
+  }
+  if (tid == 0) {
+    a.head[0] = refused;
+    a.head[1] = refused ? 0 : n_copies;
+  }
+  if (refused) return;
+  __syncthreads();  // every read of refs is done, a.fresh is written
+  for (int i = tid; i < total; i += kPlanThreads) a.refs[a.fresh[i]] = 1;
+#pragma unroll
+  for (int x = 0; x < PER; ++x) {
+    const int r = r0 + x;
+    if (r >= r1) continue;
+    a.held[r] = held[x];
+    a.ends[r] = ends[x];
+    a.at[r] = at;
+    a.copy[r] = copies[x];
+    if (copies[x]) {
+      a.src[c] = s_last[r];
+      a.dst[c] = a.fresh[at];
+      atomicSub(a.refs + s_last[r], 1);
+      ++c;
+    }
+    at += copies[x] + ends[x] - held[x];
+    a.lens[r] = len[x];  // every thread has read the old lengths it needs
+  }
+}
+
+// Copies pages src[i] -> dst[i] in every plane: units of 4 KB dealt to the CTAs round robin,
+// so that a few pages still use every SM; a thread has up to four 16-byte loads in flight.
+__device__ __forceinline__ void copy_pages(const PoolArgs& a, const int32_t* src, const int32_t* dst, int n) {
+  const unsigned upp = (unsigned)((a.page_bytes + kUnitBytes - 1) / kUnitBytes);  // units of a page
+  const unsigned planes = 2u * a.n_layers;
+  const unsigned long long units = (unsigned long long)n * planes * upp;
+  for (unsigned long long u0 = blockIdx.x; u0 < units; u0 += (unsigned long long)gridDim.x * kInFlight) {
+    uint4 x[kInFlight];
+    char* to[kInFlight];
+#pragma unroll
+    for (int q = 0; q < kInFlight; ++q) {
+      const unsigned long long u = u0 + (unsigned long long)q * gridDim.x;
+      to[q] = nullptr;
+      if (u >= units) continue;
+      const unsigned long long pl = u / upp;
+      const long long off = (long long)(u - pl * upp) * kUnitBytes + threadIdx.x * 16;
+      if (off >= a.page_bytes) continue;
+      const unsigned i = (unsigned)(pl / planes), p = (unsigned)(pl - (unsigned long long)i * planes);
+      char* base = ((p & 1) ? a.v : a.k) + (long long)(p >> 1) * a.layer_stride + off;
+      x[q] = *reinterpret_cast<const uint4*>(base + (long long)src[i] * a.page_stride);
+      to[q] = base + (long long)dst[i] * a.page_stride;
+    }
+#pragma unroll
+    for (int q = 0; q < kInFlight; ++q)
+      if (to[q]) *reinterpret_cast<uint4*>(to[q]) = x[q];
+  }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) apply_kernel(const __grid_constant__ PoolArgs a) {
+  pdl_wait();
+  pdl_launch();
+  if (a.head[0]) {  // refused: the counts go back to what the table says
+    for (int r = blockIdx.x; r < a.n_rows; r += gridDim.x) {
+      Take t;
+      if (!take_of(a, r, &t)) continue;
+      for (int i = threadIdx.x; i < a.width; i += kCopyThreads) {
+        const int o = a.snap[(long long)r * a.width + i];
+        const int n = i < t.held ? a.snap[(long long)t.parent * a.width + i] : -1;
+        if (o == n) continue;
+        if (o >= 0) atomicAdd(a.refs + o, 1);
+        if (n >= 0) atomicSub(a.refs + n, 1);
+      }
+    }
+    return;
+  }
+  for (int r = blockIdx.x; r < a.n_rows; r += gridDim.x) {
+    const int held = a.held[r], ends = a.ends[r], at = a.at[r], copy = a.copy[r];
+    const int p = a.parents ? a.parents[r] : r;
+    const int32_t* from = a.snap + (long long)max(p, 0) * a.width;
+    for (int i = threadIdx.x; i < a.width; i += kCopyThreads) {
+      int id = -1;
+      if (i < held)
+        id = copy && i == held - 1 ? a.fresh[at] : from[i];
+      else if (i < ends)
+        id = a.fresh[at + copy + i - held];
+      a.table[(long long)r * a.table_stride + i] = id;
+    }
+  }
+  copy_pages(a, a.src, a.dst, a.head[1]);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid_constant__ PoolArgs a) {
+  __shared__ int s_sums[32];
+  const int tid = threadIdx.x;
+  pdl_wait();
+  pdl_launch();
+  int mine = 0, used;
+  for (int i = tid; i < a.n_pages; i += kPlanThreads) {
+    mine += a.refs[i] > 0;
+    a.rank[i] = -1;
+  }
+  block_scan(mine, s_sums, &used);
+  const int n = list_pages(a.refs, used, a.n_pages, a.n_pages, a.src, s_sums, [](int c) { return c > 0; });
+  list_pages(a.refs, 0, used, n, a.fresh, s_sums, [](int c) { return c <= 0; });
+  __syncthreads();  // a.src and a.fresh are written, refs read
+  for (int i = tid; i < n; i += kPlanThreads) {
+    const int s = a.src[i];
+    a.rank[s] = i;
+    a.refs[a.fresh[i]] = a.refs[s];
+    a.refs[s] = 0;
+  }
+  if (tid == 0) a.head[1] = n;
+}
+
+__global__ void __launch_bounds__(kCopyThreads) compact_apply_kernel(const __grid_constant__ PoolArgs a) {
+  pdl_wait();
+  pdl_launch();
+  const long long cells = (long long)a.n_rows * a.width;
+  for (long long x = (long long)blockIdx.x * kCopyThreads + threadIdx.x; x < cells; x += (long long)gridDim.x * kCopyThreads) {
+    const int r = (int)(x / a.width);
+    int32_t* cell = a.table + (long long)r * a.table_stride + (int)(x - (long long)r * a.width);
+    const int id = *cell;
+    if (id < 0) continue;
+    if (id >= a.n_pages) {
+      report(a.status, MK_ERR_PAGES, PO_COMPACT, r, id);
+      continue;
+    }
+    const int k = a.rank[id];
+    if (k >= 0) *cell = a.fresh[k];
+  }
+  copy_pages(a, a.src, a.fresh, a.head[1]);
+}
+
+mk_status fill(PoolArgs* a, const mk_page_pool* p, void* ws, size_t ws_bytes, int32_t* status) {
+  if (!p || !p->k || !p->v || !p->table || !p->refs)
+    return paged_fail(MK_ERR_INVALID, "the page pool or one of its pointers is NULL");
+  if (!aligned_to(p->k, 16) || !aligned_to(p->v, 16)) return paged_fail(MK_ERR_INVALID, "pages must be 16-byte aligned");
+  if (p->n_layers < 1 || p->n_pages < 1 || p->n_rows < 1 || p->table_width < 1)
+    return paged_fail(MK_ERR_INVALID, "n_layers, n_pages, n_rows and table_width must be positive");
+  if (p->n_pages >= kMost) return paged_fail(MK_ERR_INVALID, "n_pages out of range");
+  if (p->n_rows > kMaxRows) return paged_fail(MK_ERR_INVALID, "n_rows must be at most 4096");
+  if (p->page_size < 16 || p->page_size > 1024 || p->page_size % 16)
+    return paged_fail(MK_ERR_INVALID, "page_size must be a multiple of 16 in [16, 1024]");
+  if ((long long)p->table_width * p->page_size > 0x7fffffffLL)
+    return paged_fail(MK_ERR_INVALID, "table_width * page_size must be below 2^31");
+  if (p->table_stride < p->table_width) return paged_fail(MK_ERR_INVALID, "table_stride is smaller than table_width");
+  if (p->page_bytes < 16 || p->page_bytes % 16 || p->page_stride % 16 || p->layer_stride % 16)
+    return paged_fail(MK_ERR_INVALID, "page_bytes, page_stride and layer_stride must be multiples of 16");
+  if (p->page_stride < p->page_bytes || (p->n_layers > 1 && p->layer_stride < p->page_bytes))
+    return paged_fail(MK_ERR_INVALID, "page_stride and layer_stride must hold a page");
+  const size_t need = lay_out(a, ws, p->n_rows, p->table_width, p->n_pages);
+  if (!ws || !aligned_to(ws, 16) || ws_bytes < need)
+    return paged_fail(MK_ERR_INVALID, "the workspace is missing, unaligned or too small (mk_update_pages_workspace)");
+  a->k = static_cast<char*>(p->k); a->v = static_cast<char*>(p->v);
+  a->table = p->table; a->refs = p->refs; a->status = status;
+  a->page_bytes = p->page_bytes; a->page_stride = p->page_stride; a->layer_stride = p->layer_stride;
+  a->table_stride = p->table_stride;
+  a->n_layers = p->n_layers; a->n_pages = p->n_pages; a->page_size = p->page_size; a->n_rows = p->n_rows;
+  a->width = p->table_width;
+  return MK_OK;
+}
+
+}  // namespace
+}  // namespace mk
+
+extern "C" mk_status mk_update_pages_workspace(int n_rows, int table_width, int n_pages, size_t* bytes) {
+  using namespace mk;
+  if (!bytes) return paged_fail(MK_ERR_INVALID, "bytes is NULL");
+  if (n_rows < 1 || n_rows > kMaxRows || table_width < 1 || n_pages < 1)
+    return paged_fail(MK_ERR_INVALID, "n_rows must be in [1, 4096], table_width and n_pages positive");
+  PoolArgs a{};
+  *bytes = lay_out(&a, nullptr, n_rows, table_width, n_pages);
+  return MK_OK;
+}
+
+extern "C" mk_status mk_update_pages(const mk_update_args* args, const mk_page_pool* pool, int32_t* status, void* stream) {
+  using namespace mk;
+  if (!args || !args->lens) return paged_fail(MK_ERR_INVALID, "NULL argument");
+  PoolArgs a{};
+  mk_status s = fill(&a, pool, args->workspace, args->workspace_bytes, status);
+  if (s) return s;
+  a.lens = args->lens;
+  a.parents = args->parents;
+  a.reserve = args->reserve;
+  int n_sm = 0;
+  s = sm_count(&n_sm);
+  if (s) return s;
+  s = launch_dependent(count_kernel, dim3(a.n_rows), dim3(kRowThreads), 0, stream, "mk_update_pages (count)", a);
+  if (s) return s;
+  s = launch_dependent(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, "mk_update_pages (plan)", a);
+  if (s) return s;
+  return launch_dependent(apply_kernel, dim3(n_sm * kCopyCtasPerSm), dim3(kCopyThreads), 0, stream,
+                          "mk_update_pages (apply)", a);
+}
+
+extern "C" mk_status mk_compact_pages(const mk_page_pool* pool, void* workspace, size_t workspace_bytes, int32_t* status,
+                                      void* stream) {
+  using namespace mk;
+  PoolArgs a{};
+  mk_status s = fill(&a, pool, workspace, workspace_bytes, status);
+  if (s) return s;
+  int n_sm = 0;
+  s = sm_count(&n_sm);
+  if (s) return s;
+  s = launch_dependent(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, "mk_compact_pages (plan)", a);
+  if (s) return s;
+  return launch_dependent(compact_apply_kernel, dim3(n_sm * kCopyCtasPerSm), dim3(kCopyThreads), 0, stream,
+                          "mk_compact_pages (apply)", a);
+}
