@@ -399,7 +399,9 @@ mk_status mk_rope_append(const mk_append_args* args, const mk_page_view* cache, 
  * value: whatever lies there, NaN included, has no effect.  A row outside the table counts
  * as empty, positions past the table are dropped and those on a bad page masked, each of
  * them reported (MK_ERR_PAGES).  A query that is not of the cache's type must lie within
- * the cache type's range.  Results do not depend on timing. */
+ * the cache type's range.  A NaN or infinite value inside the range makes that row's results
+ * NaN or infinite, as does a NaN key; an infinite key does, unless the query is of the
+ * cache's type and the scores stay below +inf.  Results do not depend on timing. */
 typedef struct {
   const void* q;           /* [n_rows][n_heads][head_dim], element strides below            */
   void* out;

@@ -347,7 +347,9 @@ __global__ void __launch_bounds__(kAttThreads, HD == 128 ? 3 : 4) attend_kernel(
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int p = 2 * c + (e & 1) + 8 * (e >> 1);
-          float y = WIDE ? s[e >> 1][2 * h + (e & 1)] : s[e >> 1][e & 1] + s[e >> 1][2 + (e & 1)];
+          float y = s[e >> 1][2 * h + (e & 1)];
+          // the second part's row; one part has none, and there 0 times an infinite key is NaN
+          if (!WIDE && NQ > 1) y += s[e >> 1][2 + (e & 1)];
           y *= a.scale;
           if (a.softcap > 0.f) y = a.softcap * tanhf(y / a.softcap);
           x[e] = p >= q0 && p < q1 ? y * kLog2e : -INFINITY;
