@@ -2,7 +2,8 @@
 
 The translation units compile in parallel; the shared library links the CUDA runtime
 statically, so loading it needs no CUDA driver (host-only entry points such as
-mk_plan work on a machine without a GPU).
+mk_plan work on a machine without a GPU).  Beside it a small extension module passes torch
+tensors to the paged operators.
 """
 import os
 import subprocess
@@ -13,6 +14,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_objs")
 LIB = os.path.join(HERE, "libmk.so")
+EXT = os.path.join(HERE, "_mk_torch.so")  # the paged operators on torch tensors (paged.py)
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -42,10 +44,28 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
+def _extension_command(nvcc):
+    """The compile of the torch extension module (host code; torch's headers, libmk.so linked after)."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc)) if os.path.isabs(nvcc) else "/usr/local/cuda", "include")
+    inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"), cuda]
+    obj = os.path.join(OBJ, "mk_torch.o")
+    comp = ["g++", "-O2", "-std=c++17", "-fPIC", "-w", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    comp += [f"-I{d}" for d in inc] + ["-c", os.path.join(CSRC, "mk_torch.cpp"), "-o", obj]
+    lib = os.path.join(root, "lib")
+    link = ["g++", "-shared", obj, "-o", EXT + ".tmp", f"-L{HERE}", "-l:libmk.so", "-Wl,-rpath,$ORIGIN", f"-L{lib}",
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    return comp, link
+
+
 def build(force=False, verbose=False, ptxas_info=False):
     """Compile and link libmk.so if any source changed; returns the library path."""
     deps = _deps()
-    if not force and not _stale(LIB, deps):
+    if not force and not _stale(LIB, deps) and not _stale(EXT, deps):
         return LIB
     os.makedirs(OBJ, exist_ok=True)
     nvcc = _nvcc()
@@ -63,8 +83,12 @@ def build(force=False, verbose=False, ptxas_info=False):
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stdout + r.stderr
 
-    with ThreadPoolExecutor(len(SOURCES)) as ex:
+    ext_compile, ext_link = _extension_command(nvcc)
+    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        ext = ex.submit(subprocess.run, ext_compile, capture_output=True, text=True)
         results = list(ex.map(compile_one, SOURCES))
+        if ext.result().returncode != 0:
+            raise RuntimeError(f"g++ failed on mk_torch.cpp:\n{ext.result().stdout}\n{ext.result().stderr}")
     logs = "".join(r[1] for r in results)
     if verbose and logs:
         print(logs, file=sys.stderr)
@@ -74,6 +98,10 @@ def build(force=False, verbose=False, ptxas_info=False):
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    r = subprocess.run(ext_link, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the torch extension failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(EXT + ".tmp", EXT)
     return (LIB, logs) if ptxas_info else LIB
 
 
