@@ -343,7 +343,7 @@ typedef struct {
                               head_dim 64 or 128                                            */
   int dtype;               /* MK_F16 or MK_BF16                                             */
   const int32_t* table;    /* [n_rows][table_stride], the first table_width entries used    */
-  int n_rows, table_width;
+  int n_rows, table_width; /* table_width * page_size at most 2^30                          */
   long long table_stride;
 } mk_page_view;
 

@@ -33,7 +33,7 @@ std::string check_view(const mk_page_view* c) {
   if (c->n_pages < 1 || c->n_kv_heads < 1 || c->n_rows < 1 || c->table_width < 1)
     return "n_pages, n_kv_heads, n_rows and table_width must be positive";
   if (c->n_kv_heads > 65535) return "n_kv_heads must be at most 65535";
-  if ((long long)c->table_width * c->page_size > 0x7fffffffLL) return "table_width * page_size must be below 2^31";
+  if ((long long)c->table_width * c->page_size > (1LL << 30)) return "table_width * page_size must be at most 2^30";
   if (c->table_stride < c->table_width) return "table_stride is smaller than table_width";
   if (c->page_stride < (long long)c->n_kv_heads * c->page_size * c->head_dim || c->page_stride % 8)
     return "page_stride must hold a page and be a multiple of 8";

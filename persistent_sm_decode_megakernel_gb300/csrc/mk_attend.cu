@@ -17,6 +17,7 @@ namespace {
 constexpr int kTile = 16;               // positions per tile: the k extent of the value product
 constexpr int kAttWarps = 4;
 constexpr int kAttThreads = 32 * kAttWarps;
+constexpr int kCtasPerSm = 3;           // 168 registers a thread
 constexpr int kJoinThreads = 256;
 constexpr int kMaxGroup = 16;           // query heads per kv head
 constexpr float kLog2e = 1.4426950408889634f;
@@ -27,12 +28,16 @@ struct AttendArgs {
   void* out;
   float* lse;
   float* part;                          // [n_cta][2][heads of a group][HD + 4]
+  int4* joins;                          // [n_cta] what to join: first and last CTA, row, kv head
   const int32_t *lens, *rows, *table;
   int32_t* status;
   long long q_row, q_head, o_row, o_head, page_stride, table_stride;
   int n_rows, hq, hkv, group, len_add, window, page_size, n_pages, table_rows, width;
+  int tpp;                              // tiles per page
+  unsigned tpp_inverse;                 // 2^32 / tpp, rounded up
   int n_cta, min_share;
-  float scale, softcap;
+  int by_segment;                       // joins[row * hkv + kv head] (they fit), else joins[first CTA]
+  float scale, softcap;                 // scores to units of log 2: scale s, or softcap tanh(scale s)
 };
 
 // The span of a row: positions [lo, hi) and their tiles [t0, t0 + n).
@@ -58,41 +63,47 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int r, bool tell) {
   return s;
 }
 
-// Sums of the rows' tiles over a CTA of THREADS, thread t taking the rows from t * per:
-// returns the total; *before: the tiles of the rows before this thread's (upto < 0), or of the
-// rows below `upto`.
-template <int THREADS>
-__device__ __forceinline__ long long sum_rows(const AttendArgs& a, long long* sums, bool tell, int upto,
-                                              long long* before) {
+// Of the rows' tiles, times hkv: returns the total; the thread whose rows hold unit `at` leaves
+// that row and the units before it in *row and *before (shared memory; the caller syncs).
+__device__ __forceinline__ long long share_of(const AttendArgs& a, long long units);
+__device__ __forceinline__ long long find_row(const AttendArgs& a, long long* sums, int* row, long long* before) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (a.n_rows + THREADS - 1) / THREADS, r0 = min(a.n_rows, tid * per), r1 = min(a.n_rows, r0 + per);
-  long long mine = 0, below = 0;
-  for (int r = r0; r < r1; ++r) {
-    const int n = span_of(a, r, tell).n;
-    mine += n;
-    if (r < upto) below += n;
-  }
+  const int per = (a.n_rows + kAttThreads - 1) / kAttThreads;
+  const int r0 = min(a.n_rows, tid * per), r1 = min(a.n_rows, r0 + per);
+  long long mine = 0;
+  for (int r = r0; r < r1; ++r) mine += span_of(a, r, blockIdx.x == 0).n;
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long x = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += x;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
   if (lane == 31) sums[warp] = inc;
-  if (lane == 0) sums[THREADS / 32 + warp] = below;
   __syncthreads();
-  long long base = 0, total = 0, bel = 0;
+  long long base = 0, total = 0;
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
+  for (int w = 0; w < kAttWarps; ++w) {
     if (w < warp) base += sums[w];
     total += sums[w];
-    bel += sums[THREADS / 32 + w];
   }
-  __syncthreads();
-  *before = upto >= 0 ? bel : base + inc - mine;
+  total *= a.hkv;
+  const long long at = share_of(a, total) * blockIdx.x;
+  long long b = (base + inc - mine) * a.hkv;
+  if (at >= b && at < b + mine * a.hkv)
+    for (int r = r0; r < r1; ++r) {
+      const long long n = (per == 1 ? mine : (long long)span_of(a, r, false).n) * a.hkv;
+      if (at >= b && at < b + n) {
+        *row = r;
+        *before = b;
+      }
+      b += n;
+    }
   return total;
+}
+
+// the page a tile lies in: t / tpp by a multiplication (exact for t <= 2^26, tpp <= 64)
+__device__ __forceinline__ int page_index(const AttendArgs& a, int t) {
+  return a.tpp == 1 ? t : (int)__umulhi((unsigned)t, a.tpp_inverse);
 }
 
 // units (tiles of one kv head) a CTA takes: equal shares of one wave, but no fewer than
@@ -142,6 +153,13 @@ constexpr float kProbShift = 0.f;
 template <>
 constexpr float kProbShift<__half> = 14.f;
 
+// 2^x by the hardware's approximation (2 ulp; results below the normal range become 0)
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // keys and values are read once: they need not stay in L1
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   uint4 v;
@@ -153,6 +171,11 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
 
 // Shared memory of the kernel: the query as A fragments [part][32-dim chunk][32 lanes][16 B]
 // (WIDE: [part][chunk][2 row halves][32 lanes]), then the warps' partials for the CTA's merge.
+struct AttState {
+  long long at, end, share, before;  // next unit, end of the CTA's units, share; units before `row`
+  long long sums[kAttWarps];
+  int row, head, slot, bad, bad_page;
+};
 template <int HD, bool WIDE, int NQ>
 struct AttSmem {
   static constexpr int kHeads = WIDE ? 16 : 8;
@@ -160,7 +183,7 @@ struct AttSmem {
   static constexpr int kRow = HD + 4;                        // floats per head of a partial
   static constexpr int kPartFloats = kAttWarps * kHeads * kRow;
   static constexpr int kMlFloats = kAttWarps * kHeads * 2;
-  static constexpr int kBytes = kQBytes + 4 * (kPartFloats + kMlFloats) + 16 * kAttWarps + 32;
+  static constexpr int kBytes = kQBytes + 4 * (kPartFloats + kMlFloats) + (int)sizeof(AttState);
 };
 
 // C: the cache's type.  Q: the queries' and outputs' type.  NQ parts of C make up a query
@@ -178,60 +201,94 @@ struct AttSmem {
 // So every load is 16 bytes, a warp's rows are read in whole 64- and 128-byte runs, no
 // barrier stands between the loads and the products, and the warps of an SM hide each
 // other's latency.
+//
+// A warp takes NT tiles at a time: with 64 dims two, so that as many bytes are in flight.
 template <typename C, typename Q, int HD, bool WIDE, int NQ, int NP>
-__global__ void __launch_bounds__(kAttThreads, HD == 128 ? 3 : 4) attend_kernel(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(kAttThreads, kCtasPerSm) attend_kernel(const __grid_constant__ AttendArgs a) {
   using SM = AttSmem<HD, WIDE, NQ>;
-  constexpr int CH = HD / 32, VH = HD / 64, HEADS = SM::kHeads, ROW = SM::kRow;
+  constexpr int CH = HD / 32, VH = HD / 64, HEADS = SM::kHeads, ROW = SM::kRow, NT = HD == 64 ? 2 : 1;
   constexpr int RH = WIDE ? 2 : 1;  // row halves that are heads of their own
   extern __shared__ __align__(16) unsigned char att_smem[];
   uint4* s_q = reinterpret_cast<uint4*>(att_smem);
   float* s_part = reinterpret_cast<float*>(att_smem + SM::kQBytes);
   float* s_ml = s_part + SM::kPartFloats;
-  long long* s_sum = reinterpret_cast<long long*>(s_ml + SM::kMlFloats);  // [2 kAttWarps]
-  long long* s_before = s_sum + 2 * kAttWarps;                            // units before the first row
-  int* s_row = reinterpret_cast<int*>(s_before + 1);                      // the first row
+  AttState* st = reinterpret_cast<AttState*>(s_ml + SM::kMlFloats);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   pdl_wait();
   pdl_launch();
-  long long before;
-  const long long units = sum_rows<kAttThreads>(a, s_sum, blockIdx.x == 0, -1, &before) * a.hkv;
+  const long long units = find_row(a, st->sums, &st->row, &st->before);
   const long long share = share_of(a, units);
-  long long at = share * blockIdx.x;
-  const long long end = min(units, at + share);
-  if (at >= end) return;
-  {  // the row that holds unit `at` is among one thread's rows
-    const int per = (a.n_rows + kAttThreads - 1) / kAttThreads;
-    const int r0 = min(a.n_rows, tid * per), r1 = min(a.n_rows, r0 + per);
-    long long b = before * a.hkv;
-    for (int r = r0; r < r1; ++r) {
-      const long long n = (long long)span_of(a, r, false).n * a.hkv;
-      if (at >= b && at < b + n) {
-        *s_row = r;
-        *s_before = b;
-      }
-      b += n;
+  // rows without positions: zeros
+  for (int r = blockIdx.x; r < a.n_rows; r += gridDim.x) {
+    if (span_of(a, r, false).n != 0) continue;
+    for (int x = tid; x < a.hq * HD; x += kAttThreads)
+      static_cast<Q*>(a.out)[(long long)r * a.o_row + (long long)(x / HD) * a.o_head + x % HD] = Conv<Q>::down(0.f);
+    for (int h = tid; h < a.hq; h += kAttThreads) {
+      if (a.lse) a.lse[(long long)r * a.hq + h] = -INFINITY;
+      if (a.by_segment && h < a.hkv) a.joins[r * a.hkv + h] = make_int4(0, -1, 0, 0);
     }
   }
+  if (tid == 0 && !a.by_segment) a.joins[blockIdx.x] = make_int4(0, -1, 0, 0);
+  if (share * blockIdx.x >= units) return;
   __syncthreads();
-  int r = *s_row;
-  long long rbase = *s_before;  // units before row r
-  while (at < end) {
-    const Span sp = span_of(a, r, false);
-    const long long in_row = at - rbase;
-    if (in_row >= (long long)sp.n * a.hkv) {  // next row (rows without positions have no units)
-      rbase += (long long)sp.n * a.hkv;
-      ++r;
-      continue;
+  // what a piece needs again at its end lives in shared memory: the loop over the tiles has
+  // few registers to spare
+  if (tid == 0) {
+    st->at = share * blockIdx.x;
+    st->end = min(units, share * (blockIdx.x + 1LL));
+    st->share = share;
+    st->bad = 0;
+  }
+  __syncthreads();
+  while (true) {
+    int base, cnt, mine, lo, hi;  // this warp's tiles: base, + kAttWarps, ...
+    const int32_t* trow;
+    {
+      long long rbase = st->before, in_row;
+      int r = st->row;
+      Span sp;
+      while (true) {
+        sp = span_of(a, r, false);
+        in_row = st->at - rbase;
+        if (in_row < (long long)sp.n * a.hkv) break;  // rows without positions have no units
+        rbase += (long long)sp.n * a.hkv;
+        ++r;
+      }
+      const int j = (int)(in_row / sp.n), first = (int)(in_row - (long long)j * sp.n);
+      cnt = (int)min((long long)(sp.n - first), st->end - st->at);  // tiles of this piece
+      __syncthreads();  // the state is read
+      if (tid == 0) {
+        const bool whole = first == 0 && cnt == sp.n;
+        st->row = r;
+        st->before = rbase;
+        st->head = j;
+        st->slot = whole ? 2 : first == 0;  // 0: continues a segment, 1: begins one, 2: is one
+        if (first == 0) {  // the segment's begin knows where it ends
+          const int last = (int)((st->at + sp.n - 1) / st->share);
+          if (a.by_segment)
+            a.joins[r * a.hkv + j] = whole ? make_int4(0, -1, 0, 0) : make_int4(blockIdx.x, last, r, j);
+          else if (!whole)
+            a.joins[blockIdx.x] = make_int4(blockIdx.x, last, r, j);
+        }
+        st->at += cnt;
+      }
+      base = sp.t0 + first + warp;
+      mine = cnt > warp ? (cnt - warp + kAttWarps - 1) / kAttWarps : 0;
+      lo = sp.lo;
+      hi = sp.hi;
+      trow = a.table + (long long)sp.trow * a.table_stride;
     }
-    const int j = (int)(in_row / sp.n), first = (int)(in_row - (long long)j * sp.n);
-    const int cnt = (int)min((long long)(sp.n - first), end - at);  // tiles of this piece
-    // ---- the query's fragments: chunk i, lane (g, c): dims [32 i + 8 c, + 8) of head g
     __syncthreads();
-    for (int x = tid; x < CH * HEADS * 4; x += kAttThreads) {
-      const int cc = x & 3, h = (x >> 2) % HEADS, i = x / (4 * HEADS);
+    // lane i holds the page of this warp's (32 b + i)-th tile; the next 32 are fetched ahead
+    auto page_of = [&](int k) -> int { return k < mine ? trow[page_index(a, base + k * kAttWarps)] : -1; };
+    int pages = page_of(lane), pages_next = -1;
+    // the query's fragments: chunk i, lane (g, c): dims [32 i + 8 c, + 8) of head g
+#pragma unroll 1
+    for (int y = tid; y < CH * HEADS * 4; y += kAttThreads) {
+      const int h = (y >> 2) % HEADS, i = y / (4 * HEADS);
+      const Q* src = static_cast<const Q*>(a.q) + (long long)st->row * a.q_row +
+                     (long long)(st->head * a.group + min(h, a.group - 1)) * a.q_head + 32 * i + 8 * (y & 3);
       float v[8];
-      const Q* src = static_cast<const Q*>(a.q) + (long long)r * a.q_row +
-                     (long long)(j * a.group + min(h, a.group - 1)) * a.q_head + 32 * i + 8 * cc;
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = h < a.group ? Conv<Q>::up(src[e]) : 0.f;
       uint32_t w[4][NQ];
@@ -240,11 +297,53 @@ __global__ void __launch_bounds__(kAttThreads, HD == 128 ? 3 : 4) attend_kernel(
 #pragma unroll
       for (int p = 0; p < NQ; ++p) {
         const int slot = WIDE ? ((p * CH + i) * 2 + (h >> 3)) * 32 : (p * CH + i) * 32;
-        s_q[slot + (h & 7) * 4 + cc] = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+        s_q[slot + (h & 7) * 4 + (y & 3)] = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
       }
     }
-    __syncthreads();
-    // ---- this warp's tiles: first + warp, + kAttWarps, ...
+    const long long plane = (long long)st->head * a.page_size * HD;  // the kv head's part of a page
+    // a tile's offset in the pages, and the positions [p0, p1) of it that count
+    long long off[NT];
+    int p0[NT], p1[NT];
+    auto locate = [&](int k) {
+#pragma unroll
+      for (int x = 0; x < NT; ++x) {
+        const int t = base + (k + x) * kAttWarps;
+        const int page = __shfl_sync(0xffffffffu, pages, (k + x) & 31);
+        p0[x] = max(0, lo - t * kTile);
+        p1[x] = min(kTile, hi - t * kTile);
+        off[x] = (long long)page * a.page_stride + plane + (t - page_index(a, t) * a.tpp) * (kTile * HD);
+        if ((unsigned)page >= (unsigned)a.n_pages || k + x >= mine) {
+          if (k + x < mine) {  // no such page: its positions are masked, and reported at the end
+            st->bad_page = page;
+            st->bad = 1;
+          }
+          p0[x] = p1[x] = 0;
+          off[x] = 0;
+        }
+      }
+    };
+    uint4 kf[NT][2][CH];
+    auto load_k = [&]() {
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int p = n * 8 + g;
+          const C* src = static_cast<const C*>(a.k) + off[x] + p * HD + 8 * c;
+          if (p1[x] - p0[x] == kTile) {  // a whole tile: nothing to fill in
+#pragma unroll
+            for (int i = 0; i < CH; ++i) kf[x][n][i] = ldg_stream(src + 32 * i);
+          } else {
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+              kf[x][n][i] = p >= p0[x] && p < p1[x] ? ldg_stream(src + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+    };
+    if (mine > 0) {
+      locate(0);
+      load_k();
+    }
     float o[VH][8][4];
 #pragma unroll
     for (int h = 0; h < VH; ++h)
@@ -258,62 +357,40 @@ __global__ void __launch_bounds__(kAttThreads, HD == 128 ? 3 : 4) attend_kernel(
       m[h] = -INFINITY;
       l[h] = 0.f;
     }
-    const int32_t* trow = a.table + (long long)sp.trow * a.table_stride;
-    const int tpp = a.page_size / kTile;  // tiles per page
-    const int mine = cnt > warp ? (cnt - warp + kAttWarps - 1) / kAttWarps : 0;
-    // lane i holds the page of this warp's (32 b + i)-th tile; the next 32 are fetched ahead
-    auto page_of = [&](int k) -> int { return k < mine ? trow[(sp.t0 + first + warp + k * kAttWarps) / tpp] : -1; };
-    int pages = page_of(lane), pages_next = -1;
-    const C* kbase = static_cast<const C*>(a.k) + (long long)j * a.page_size * HD;
-    const C* vbase = static_cast<const C*>(a.v) + (long long)j * a.page_size * HD;
-    // a tile's offset in the pages, and the positions [p0, p1) of it that count
-    auto locate = [&](int k, long long* off, int* p0, int* p1) {
-      const int t = sp.t0 + first + warp + k * kAttWarps;
-      const int page = __shfl_sync(0xffffffffu, pages, k & 31);
-      *p0 = max(0, sp.lo - t * kTile);
-      *p1 = min(kTile, sp.hi - t * kTile);
-      *off = (long long)page * a.page_stride + (t % tpp) * (kTile * HD);
-      if ((unsigned)page >= (unsigned)a.n_pages) {
-        if (lane == 0) report(a.status, MK_ERR_PAGES, PO_ATTEND, r, page);
-        *p0 = *p1 = 0;
-        *off = 0;
-      }
-    };
-    uint4 kf[2][CH];
-    auto load_k = [&](long long off, int p0, int p1) {
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int p = n * 8 + g;
-        const C* src = kbase + off + p * HD + 8 * c;
-#pragma unroll
-        for (int i = 0; i < CH; ++i)
-          kf[n][i] = p >= p0 && p < p1 ? ldg_stream(src + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
-      }
-    };
-    long long off = 0;
-    int p0 = 0, p1 = 0;
-    if (mine > 0) {
-      locate(0, &off, &p0, &p1);
-      load_k(off, p0, p1);
-    }
-    for (int k = 0; k < mine; ++k) {
+    __syncthreads();
+    for (int k = 0; k < mine; k += NT) {
       if ((k & 31) == 0) pages_next = page_of(k + 32 + lane);
-      const int q0 = p0, q1 = p1;
-      // values of this tile: in flight while the scores are computed
-      uint4 vf[VH][4];
+      int q0[NT], q1[NT];
+      // values of these tiles: in flight while the scores are computed
+      uint4 vf[NT][VH][4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int p = 2 * c + (x & 1) + 8 * (x >> 1);
-        const C* src = vbase + off + p * HD + 8 * g;
+      for (int x = 0; x < NT; ++x) {
+        q0[x] = p0[x];
+        q1[x] = p1[x];
+        const C* src = static_cast<const C*>(a.v) + off[x] + 2 * c * HD + 8 * g;
+        if (p1[x] - p0[x] == kTile) {
 #pragma unroll
-        for (int h = 0; h < VH; ++h)
-          vf[h][x] = p >= q0 && p < q1 ? ldg_stream(src + 64 * h) : make_uint4(0u, 0u, 0u, 0u);
+          for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int h = 0; h < VH; ++h) vf[x][h][y] = ldg_stream(src + ((y & 1) + 8 * (y >> 1)) * HD + 64 * h);
+        } else {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int p = 2 * c + (y & 1) + 8 * (y >> 1);
+#pragma unroll
+            for (int h = 0; h < VH; ++h)
+              vf[x][h][y] = p >= p0[x] && p < p1[x] ? ldg_stream(src + ((y & 1) + 8 * (y >> 1)) * HD + 64 * h)
+                                                    : make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
       }
-      float s[2][4];
+      float s[NT][2][4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int x = 0; x < NT; ++x)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[x][n][e] = 0.f;
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
 #pragma unroll
@@ -327,39 +404,53 @@ __global__ void __launch_bounds__(kAttThreads, HD == 128 ? 3 : 4) attend_kernel(
             w = p + 1 < NQ ? s_q[((p + 1) * CH + i) * 32 + lane] : make_uint4(0u, 0u, 0u, 0u);
           }
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            Mma<C>::run(s[n], make_uint4(u.x, w.x, u.y, w.y), kf[n][i].x, kf[n][i].y);
-            Mma<C>::run(s[n], make_uint4(u.z, w.z, u.w, w.w), kf[n][i].z, kf[n][i].w);
-          }
+          for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              Mma<C>::run(s[x][n], make_uint4(u.x, w.x, u.y, w.y), kf[x][n][i].x, kf[x][n][i].y);
+              Mma<C>::run(s[x][n], make_uint4(u.z, w.z, u.w, w.w), kf[x][n][i].z, kf[x][n][i].w);
+            }
         }
       }
-      // the next tile's keys
-      if (((k + 1) & 31) == 0) pages = pages_next;
-      if (k + 1 < mine) {
-        locate(k + 1, &off, &p0, &p1);
-        load_k(off, p0, p1);
+      // the next tiles' keys
+      if (((k + NT) & 31) == 0) pages = pages_next;
+      if (k + NT < mine) {
+        locate(k + NT);
+        load_k();
       }
-      // ---- softmax of the tile, in units of log 2; lane (g, c): columns 2c, 2c + 1 of each half
-      uint32_t ph[RH][2][NP];  // [row half][column half][part]
+      // ---- softmax of the tiles, in units of log 2; lane (g, c): columns 2c, 2c + 1 of each half
+      uint32_t ph[NT][RH][2][NP];  // [tile][row half][column half][part]
 #pragma unroll
       for (int h = 0; h < RH; ++h) {
-        float x[4], top = -INFINITY;
+        float x[NT][4], top = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int p = 2 * c + (e & 1) + 8 * (e >> 1);
-          float y = s[e >> 1][2 * h + (e & 1)];
-          // the second part's row; one part has none, and there 0 times an infinite key is NaN
-          if (!WIDE && NQ > 1) y += s[e >> 1][2 + (e & 1)];
-          y *= a.scale;
-          if (a.softcap > 0.f) y = a.softcap * tanhf(y / a.softcap);
-          x[e] = p >= q0 && p < q1 ? y * kLog2e : -INFINITY;
-          top = fmaxf(top, x[e]);
+        for (int z = 0; z < NT; ++z) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float y = s[z][e >> 1][2 * h + (e & 1)];
+            // the second part's row; one part has none, and there 0 times an infinite key is NaN
+            if (!WIDE && NQ > 1) y += s[z][e >> 1][2 + (e & 1)];
+            x[z][e] = y * a.scale;
+          }
+          if (a.softcap > 0.f) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[z][e] = a.softcap * tanhf(x[z][e]);
+          }
+          if (q1[z] - q0[z] != kTile) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int p = 2 * c + (e & 1) + 8 * (e >> 1);
+              if (p < q0[z] || p >= q1[z]) x[z][e] = -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, x[z][e]);
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const float mn = fmaxf(m[h], top), ms = mn == -INFINITY ? 0.f : mn;
         if (__any_sync(0xffffffffu, mn > m[h])) {  // rescale what was summed under a smaller maximum
-          const float f = exp2f(m[h] - ms);
+          const float f = ex2(m[h] - ms);
           l[h] *= f;
 #pragma unroll
           for (int d = 0; d < VH; ++d)
@@ -374,38 +465,44 @@ __global__ void __launch_bounds__(kAttThreads, HD == 128 ? 3 : 4) attend_kernel(
             }
           m[h] = mn;
         }
-        float p[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[e] = exp2f(x[e] - ms + kProbShift<C>);
-          l[h] += p[e];
+        for (int z = 0; z < NT; ++z) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[e] = ex2(x[z][e] - ms + kProbShift<C>);
+            l[h] += p[e];
+          }
+          split2<C, NP>(p[0], p[1], ph[z][h][0]);
+          split2<C, NP>(p[2], p[3], ph[z][h][1]);
         }
-        split2<C, NP>(p[0], p[1], ph[h][0]);
-        split2<C, NP>(p[2], p[3], ph[h][1]);
       }
       // ---- values: pair the positions (2c, 2c + 1) and (2c + 8, 2c + 9) of every dim
 #pragma unroll
-      for (int d = 0; d < VH; ++d) {
-        const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&vf[d][0]);
-        const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&vf[d][1]);
-        const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vf[d][2]);
-        const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&vf[d][3]);
+      for (int z = 0; z < NT; ++z)
 #pragma unroll
-        for (int y = 0; y < 8; ++y) {
-          const uint32_t sel = y & 1 ? 0x7632u : 0x5410u;
-          const uint32_t b0 = __byte_perm(v0[y >> 1], v1[y >> 1], sel), b1 = __byte_perm(v2[y >> 1], v3[y >> 1], sel);
+        for (int d = 0; d < VH; ++d) {
+          const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&vf[z][d][0]);
+          const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&vf[z][d][1]);
+          const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vf[z][d][2]);
+          const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&vf[z][d][3]);
 #pragma unroll
-          for (int p = 0; p < NP; p += WIDE ? 1 : 2) {
-            if (WIDE) {
-              Mma<C>::run(o[d][y], make_uint4(ph[0][0][p], ph[RH - 1][0][p], ph[0][1][p], ph[RH - 1][1][p]), b0, b1);
-            } else {
-              const int p2 = p + 1 < NP ? p + 1 : 0;
-              Mma<C>::run(o[d][y], make_uint4(ph[0][0][p], p2 ? ph[0][0][p2] : 0u, ph[0][1][p], p2 ? ph[0][1][p2] : 0u),
-                          b0, b1);
+          for (int y = 0; y < 8; ++y) {
+            const uint32_t sel = y & 1 ? 0x7632u : 0x5410u;
+            const uint32_t b0 = __byte_perm(v0[y >> 1], v1[y >> 1], sel), b1 = __byte_perm(v2[y >> 1], v3[y >> 1], sel);
+#pragma unroll
+            for (int p = 0; p < NP; p += WIDE ? 1 : 2) {
+              if (WIDE) {
+                Mma<C>::run(o[d][y], make_uint4(ph[z][0][0][p], ph[z][RH - 1][0][p], ph[z][0][1][p], ph[z][RH - 1][1][p]),
+                            b0, b1);
+              } else {
+                const int p2 = p + 1 < NP ? p + 1 : 0;
+                Mma<C>::run(o[d][y], make_uint4(ph[z][0][0][p], p2 ? ph[z][0][0][p2] : 0u, ph[z][0][1][p],
+                                                p2 ? ph[z][0][1][p2] : 0u), b0, b1);
+              }
             }
           }
         }
-      }
     }
     // ---- merge the warps' pieces in shared memory, fixed order
 #pragma unroll
@@ -432,7 +529,11 @@ __global__ void __launch_bounds__(kAttThreads, HD == 128 ? 3 : 4) attend_kernel(
         }
     }
     __syncthreads();
-    const bool whole = first == 0 && cnt == sp.n;
+    const int r = st->row, j = st->head, slot = st->slot;
+    if (tid == 0 && st->bad) {
+      report(a.status, MK_ERR_PAGES, PO_ATTEND, r, st->bad_page);
+      st->bad = 0;
+    }
     for (int x = tid; x < a.group * (HD / 4); x += kAttThreads) {
       const int h = x / (HD / 4), d = (x % (HD / 4)) * 4;
       float M = -INFINITY;
@@ -443,7 +544,7 @@ __global__ void __launch_bounds__(kAttThreads, HD == 128 ? 3 : 4) attend_kernel(
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kAttWarps; ++w) {
-        const float f = exp2f(s_ml[(w * HEADS + h) * 2] - Ms);
+        const float f = ex2(s_ml[(w * HEADS + h) * 2] - Ms);
         const float4 v = *reinterpret_cast<const float4*>(s_part + (w * HEADS + h) * ROW + d);
         L = fmaf(f, s_ml[(w * HEADS + h) * 2 + 1], L);
         acc.x = fmaf(f, v.x, acc.x);
@@ -451,7 +552,7 @@ __global__ void __launch_bounds__(kAttThreads, HD == 128 ? 3 : 4) attend_kernel(
         acc.z = fmaf(f, v.z, acc.z);
         acc.w = fmaf(f, v.w, acc.w);
       }
-      if (whole) {
+      if (slot == 2) {
         const float inv = L == 0.f ? 0.f : 1.f / L;
         Q* dst = static_cast<Q*>(a.out) + (long long)r * a.o_row + (long long)(j * a.group + h) * a.o_head + d;
         dst[0] = Conv<Q>::down(acc.x * inv);
@@ -460,8 +561,8 @@ __global__ void __launch_bounds__(kAttThreads, HD == 128 ? 3 : 4) attend_kernel(
         dst[3] = Conv<Q>::down(acc.w * inv);
         if (d == 0 && a.lse)
           a.lse[(long long)r * a.hq + j * a.group + h] = (Ms - kProbShift<C> + log2f(L)) * kLn2;
-      } else {  // slot 0: a piece that continues a segment, slot 1: one that begins it
-        float* dst = a.part + (((size_t)blockIdx.x * 2 + (first == 0)) * a.group + h) * ROW;
+      } else {
+        float* dst = a.part + (((size_t)blockIdx.x * 2 + slot) * a.group + h) * ROW;
         *reinterpret_cast<float4*>(dst + d) = acc;
         if (d == 0) {
           dst[HD] = M;
@@ -469,33 +570,23 @@ __global__ void __launch_bounds__(kAttThreads, HD == 128 ? 3 : 4) attend_kernel(
         }
       }
     }
-    at += cnt;
+    if (st->at >= st->end) return;
   }
 }
 
-// Joins the pieces of the segments that span CTAs, and writes the rows without positions.
-// One CTA per (row, query head); warps take the pieces in turn, each lane HD / 32 dims.
+// Joins the pieces of the segments that span CTAs: one CTA per (segment, head of its group);
+// warps take the pieces in turn, each lane HD / 32 dims.
 template <typename Q, int HD>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttendArgs a, float shift) {
   constexpr int W = kJoinThreads / 32, E = HD / 32, ROW = HD + 4;
-  __shared__ long long sums[2 * W];
   __shared__ float s_o[W][HD], s_ml[W][2];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int r = blockIdx.x / a.hq, head = blockIdx.x % a.hq, j = head / a.group, h = head % a.group;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y;
   pdl_wait();
   pdl_launch();
-  const Span sp = span_of(a, r, false);
+  const int4 job = a.joins[blockIdx.x];
+  const int c0 = job.x, c1 = job.y, r = job.z, head = job.w * a.group + h;
+  if (c1 < 0) return;  // finished by its CTA
   Q* out = static_cast<Q*>(a.out) + (long long)r * a.o_row + (long long)head * a.o_head;
-  if (sp.n == 0) {
-    for (int d = tid; d < HD; d += kJoinThreads) out[d] = Conv<Q>::down(0.f);
-    if (tid == 0 && a.lse) a.lse[(long long)r * a.hq + head] = -INFINITY;
-    return;
-  }
-  long long before;
-  const long long units = sum_rows<kJoinThreads>(a, sums, false, r, &before) * a.hkv;
-  const long long share = share_of(a, units), from = before * a.hkv + (long long)j * sp.n;
-  const int c0 = (int)(from / share), c1 = (int)((from + sp.n - 1) / share);
-  if (c0 == c1) return;  // finished by its CTA
   float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
@@ -515,7 +606,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     for (int u = 0; u < U; ++u) {
       if (b + u * W > c1) continue;
       const float mn = fmaxf(m, pm[u]), ms = mn == -INFINITY ? 0.f : mn;
-      const float f0 = exp2f(m - ms), f1 = exp2f(pm[u] - ms);
+      const float f0 = ex2(m - ms), f1 = ex2(pm[u] - ms);
       l = l * f0 + pl[u] * f1;
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = o[e] * f0 + po[u][e] * f1;
@@ -536,7 +627,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     const float Ms = M == -INFINITY ? 0.f : M;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const float f = exp2f(s_ml[w][0] - Ms);
+      const float f = ex2(s_ml[w][0] - Ms);
       L = fmaf(f, s_ml[w][1], L);
       acc = fmaf(f, s_o[w][tid], acc);
     }
@@ -544,10 +635,6 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     if (tid == 0 && a.lse) a.lse[(long long)r * a.hq + head] = (Ms - shift + log2f(L)) * kLn2;
   }
 }
-
-// CTAs of one wave: resident per SM by the launch bounds, the same for every instance of a
-// head_dim, so that the workspace's size depends on nothing else
-int ctas_per_sm(int hd) { return hd == 128 ? 3 : 4; }
 
 template <typename C, typename Q, int HD, bool WIDE, int NQ, int NP>
 mk_status launch_attend(const AttendArgs& a, void* stream) {
@@ -559,7 +646,8 @@ mk_status launch_attend(const AttendArgs& a, void* stream) {
   }
   const mk_status s = launch_dependent(k, dim3(a.n_cta), dim3(kAttThreads), smem, stream, "mk_paged_attention", a);
   if (s) return s;
-  return launch_dependent(join_kernel<Q, HD>, dim3((unsigned)(a.n_rows * a.hq)), dim3(kJoinThreads), 0, stream,
+  const int jobs = a.by_segment ? a.n_rows * a.hkv : a.n_cta;
+  return launch_dependent(join_kernel<Q, HD>, dim3(jobs, a.group), dim3(kJoinThreads), 0, stream,
                           "mk_paged_attention (join)", a, kProbShift<C>);
 }
 template <typename C, typename Q, int NQ, int NP>
@@ -581,7 +669,8 @@ extern "C" mk_status mk_paged_attention_workspace(int n_heads, int n_kv_heads, i
   int n_sm = 0;
   const mk_status s = sm_count(&n_sm);
   if (s) return s;
-  *bytes = (size_t)n_sm * ctas_per_sm(head_dim) * 2 * (n_heads / n_kv_heads) * (head_dim + 4) * sizeof(float);
+  const size_t n_cta = (size_t)n_sm * kCtasPerSm;
+  *bytes = n_cta * (sizeof(int4) + 2 * (n_heads / n_kv_heads) * (head_dim + 4) * sizeof(float));
   return MK_OK;
 }
 
@@ -614,16 +703,21 @@ extern "C" mk_status mk_paged_attention(const mk_attend_args* args, const mk_pag
   if (s) return s;
   AttendArgs a{};
   a.q = args->q; a.k = cache->k; a.v = cache->v; a.out = args->out; a.lse = args->lse;
-  a.part = static_cast<float*>(args->workspace);
+  a.joins = static_cast<int4*>(args->workspace);
   a.lens = args->lens; a.rows = args->rows; a.table = cache->table; a.status = status;
   a.q_row = args->q_row; a.q_head = args->q_head; a.o_row = args->o_row; a.o_head = args->o_head;
   a.page_stride = cache->page_stride; a.table_stride = cache->table_stride;
   a.n_rows = args->n_rows; a.hq = args->n_heads; a.hkv = cache->n_kv_heads; a.group = args->n_heads / cache->n_kv_heads;
   a.len_add = args->len_add; a.window = args->window; a.page_size = cache->page_size; a.n_pages = cache->n_pages;
   a.table_rows = cache->n_rows; a.width = cache->table_width;
-  a.n_cta = n_sm * ctas_per_sm(cache->head_dim);
+  a.tpp = a.page_size / kTile;
+  a.tpp_inverse = a.tpp > 1 ? (unsigned)(((1ULL << 32) + a.tpp - 1) / a.tpp) : 0;
+  a.n_cta = n_sm * kCtasPerSm;
+  a.part = reinterpret_cast<float*>(a.joins + a.n_cta);
+  a.by_segment = (long long)a.n_rows * a.hkv <= a.n_cta;
   a.min_share = kAttWarps;
-  a.scale = args->scale; a.softcap = args->softcap;
+  a.scale = args->softcap > 0.f ? args->scale / args->softcap : args->scale * kLog2e;
+  a.softcap = args->softcap * kLog2e;
   // 16-bit queries of the cache's type are exact in one part.  Other queries are split into
   // 2 parts of fp16 (22 bits) or 3 of bf16 (24 bits); probabilities likewise, 2 parts of
   // bf16 (16 bits) being enough for an output of 16 bits.

@@ -354,8 +354,8 @@ mk_status fill(PoolArgs* a, const mk_page_pool* p, void* ws, size_t ws_bytes, in
   if (p->n_rows > kMaxRows) return paged_fail(MK_ERR_INVALID, "n_rows must be at most 4096");
   if (p->page_size < 16 || p->page_size > 1024 || p->page_size % 16)
     return paged_fail(MK_ERR_INVALID, "page_size must be a multiple of 16 in [16, 1024]");
-  if ((long long)p->table_width * p->page_size > 0x7fffffffLL)
-    return paged_fail(MK_ERR_INVALID, "table_width * page_size must be below 2^31");
+  if ((long long)p->table_width * p->page_size > (1LL << 30))
+    return paged_fail(MK_ERR_INVALID, "table_width * page_size must be at most 2^30");
   if (p->table_stride < p->table_width) return paged_fail(MK_ERR_INVALID, "table_stride is smaller than table_width");
   if (p->page_bytes < 16 || p->page_bytes % 16 || p->page_stride % 16 || p->layer_stride % 16)
     return paged_fail(MK_ERR_INVALID, "page_bytes, page_stride and layer_stride must be multiples of 16");

@@ -1,9 +1,9 @@
 // One step of a beam search over beams and vocabulary (mk_beam_select).
 //
 // A row's candidates are ordered by logit alone, so the log-softmax is not needed to choose
-// among them: one pass over the logits yields, per chunk of a row, the maximum, the sum of
-// exponentials and the chunk's `beams` largest logits; a second kernel (one CTA per group)
-// joins the chunks -- lse = M + log sum_c S_c e^(M_c - M), in 64 bits -- and picks the best of
+// among them: one pass over the logits yields, per part of a row, the maximum, the sum of
+// exponentials and the part's `beams` largest logits; a second kernel (one CTA per group)
+// joins the parts -- lse = M + log sum_c S_c e^(M_c - M), in 64 bits -- and picks the best of
 // score + logit - lse over the group's beams.
 //
 // Keys: a logit's bits as an ordered unsigned number, above the complement of its token, so
@@ -22,7 +22,8 @@ constexpr int kScanThreads = 256;
 constexpr int kScanWarps = kScanThreads / 32;
 constexpr int kPickThreads = 256;
 constexpr int kPickWarps = kPickThreads / 32;
-constexpr int kList = 1024;  // candidates of a chunk above its threshold that are ranked at once
+constexpr int kIter = 16 * kScanThreads;  // elements of a step
+constexpr int kList = 1024;               // entries of a CTA's list
 
 using u64 = unsigned long long;
 
@@ -52,111 +53,176 @@ __device__ __forceinline__ u64 warp_max(u64 k) {
   return (u64)hi << 32 | lo;
 }
 
-// One chunk of PER * 256 logits per CTA, all of it in registers.  The `beams` largest are
-// found through a threshold: the beams-th largest of a warp's 32 lane maxima has at least
-// `beams` elements at or above it, the largest such bound over the warps few more (about
-// 60..150 of 8192 for 8 beams); those go to a list in shared memory and each counts how many
-// of the list are above it, which is its place.  Were the list to overflow (logits laid out
-// so that a few lanes hold all the large ones), the beams come out one block maximum at a
-// time.  Bound: the logits' bytes for many rows, the launch and the block steps for few.
-template <typename T, int PER, bool VEC>
-__global__ void __launch_bounds__(kScanThreads) scan_kernel(const __grid_constant__ SelectArgs a) {
+// A CTA reads its part of a row once, kIter elements at a time with the next ones in flight.
+// The `beams` largest are kept in a list in shared memory, entered by what lies above a bound.
+// The first bound comes from the lanes: the beams-th largest of a warp's 32 lane maxima has
+// at least `beams` elements at or above it.  From then on it is the list's beams-th key: the
+// list is cut down to its best after the first elements and whenever it has grown, each entry
+// counting how many are above it, which is its place; of a part in random order about
+// beams / i keys enter at the i-th elements.  Were one step's entries to overflow the list
+// (rising logits), they come out one block maximum at a time.  The sum of exponentials runs
+// against each thread's own maximum: fours in 32 bits, a compensated sum of them, and from
+// there on in 64 bits, so that the sum of any vocabulary is good to a few 2^-24 of its terms.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_constant__ SelectArgs a) {
   __shared__ u64 s_list[kList], s_warp[kScanWarps];
   __shared__ double s_d[kScanWarps];
   __shared__ float s_f[kScanWarps];
-  __shared__ int s_n;
+  __shared__ int s_n[3];  // entries of the step, in turn: one is cleared while one is read
   constexpr int V = VEC ? 16 / (int)sizeof(T) : 1;  // elements of an access
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int PER = kIter / kScanThreads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = a.beams;
   const int row = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks;
   pdl_wait();
   pdl_launch();
   if (a.ended[row]) return;  // it offers one token, whatever its logits
   const T* src = static_cast<const T*>(a.logits) + (long long)row * a.row_stride;
   const int first = chunk * a.chunk, n = min(a.chunk, a.vocab - first);
-  float x[PER];
+  // element i * V + y of step `it` is token first + it * kIter + (i * 256 + tid) * V + y
+  auto at = [&](int it, int i) { return it * kIter + ((i / V) * kScanThreads + tid) * V + i % V; };
+  auto load = [&](int it, float (&x)[PER]) {
 #pragma unroll
-  for (int i = 0; i < PER / V; ++i) {
-    const int e = (i * kScanThreads + tid) * V;
-    if (VEC) {
-      alignas(16) T raw[V];
-      if (e + V <= n) {
+    for (int i = 0; i < PER; i += V) {
+      const int e = at(it, i);
+      if (VEC && e + V <= n) {
+        alignas(16) T raw[V];
         *reinterpret_cast<uint4*>(raw) = *reinterpret_cast<const uint4*>(src + first + e);
 #pragma unroll
-        for (int y = 0; y < V; ++y) x[i * V + y] = Conv<T>::up(raw[y]);
+        for (int y = 0; y < V; ++y) x[i + y] = Conv<T>::up(raw[y]);
       } else {
 #pragma unroll
-        for (int y = 0; y < V; ++y) x[i * V + y] = e + y < n ? Conv<T>::up(src[first + e + y]) : -INFINITY;
+        for (int y = 0; y < V; ++y) x[i + y] = e + y < n ? Conv<T>::up(src[first + e + y]) : -INFINITY;
       }
-    } else {
-      x[i] = e < n ? Conv<T>::up(src[first + e]) : -INFINITY;
     }
-  }
-  // element x[i * V + y] is token first + (i * 256 + tid) * V + y: rising in a thread
-  auto at = [&](int i) { return ((i / V) * kScanThreads + tid) * V + i % V; };
-  float top = -INFINITY;
+  };
+  if (tid < 3) s_n[tid] = 0;
+  float x[PER], next[PER];
+  load(0, next);
+  const int steps = (n + kIter - 1) / kIter;
+  int held = 0;       // entries of the list
+  u64 bound = 0ull;   // keys above it enter
   bool bad = false;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    if (!(x[i] < INFINITY)) {  // NaN or +inf
-      bad = true;
-      x[i] = -INFINITY;
-    }
-    x[i] += 0.f;  // -0 and +0 are one value, and so a tie
-    top = fmaxf(top, x[i]);
-  }
-  if (bad) report(a.status, MK_ERR_NAN, PO_SELECT, row, chunk);
-  // the thread's own largest key: the first element that reaches top (none in an empty tail)
-  int best = -1;
-#pragma unroll
-  for (int i = PER - 1; i >= 0; --i)
-    if (x[i] == top && at(i) < n) best = at(i);
-  const u64 own = best >= 0 ? key_of(top, first + best) : 0ull;
-  // the warp's beams-th largest lane maximum
-  u64 left = own, kth = 0ull;
-  for (int b = 0; b < a.beams; ++b) {
-    kth = warp_max(left);
-    if (kth == 0ull) break;  // fewer lanes with elements than beams: no bound from this warp
-    if (left == kth) left = 0ull;
-  }
-  float wtop = top;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) wtop = fmaxf(wtop, __shfl_xor_sync(0xffffffffu, wtop, o));
-  if (lane == 0) {
-    s_warp[warp] = kth;
-    s_f[warp] = wtop;
-  }
-  if (tid == 0) s_n = 0;
-  __syncthreads();
-  u64 bound = 0ull;
-  float m = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < kScanWarps; ++w) {
-    bound = s_warp[w] > bound ? s_warp[w] : bound;
-    m = fmaxf(m, s_f[w]);
-  }
-  // sum of e^(x - m): fours in 32 bits, a compensated sum of them per thread, and from there
-  // on in 64 bits, so that the sum of any vocabulary is good to a few 2^-24 of its terms
-  float s = 0.f, comp = 0.f;
-  if (m > -INFINITY) {
-#pragma unroll
-    for (int i = 0; i < PER; i += 4) {
-      const float q = (expf(x[i] - m) + expf(x[i + 1] - m)) + (expf(x[i + 2] - m) + expf(x[i + 3] - m));
-      const float t = s + q, r = t - s;  // t + the bracket below is s + q exactly
-      comp += (s - (t - r)) + (q - r);
-      s = t;
-    }
-  }
-  if (own >= bound) {  // its largest is at or above the bound: the others may be
+  float m = -INFINITY, s = 0.f, comp = 0.f;
+  for (int it = 0; it < steps; ++it) {
+    float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      if (at(i) >= n) continue;
-      const u64 k = key_of(x[i], first + at(i));
-      if (k < bound) continue;
-      const int p = atomicAdd(&s_n, 1);
-      if (p < kList) s_list[p] = k;
+      x[i] = next[i];
+      if (!(x[i] < INFINITY)) {  // NaN or +inf
+        bad = true;
+        x[i] = -INFINITY;
+      }
+      x[i] += 0.f;  // -0 and +0 are one value, and so a tie
+      top = fmaxf(top, x[i]);
+    }
+    if (it + 1 < steps) load(it + 1, next);
+    if (it == 0) {
+      // the lane's own largest key: the first element that reaches top (none in an empty tail)
+      int best = -1;
+#pragma unroll
+      for (int i = PER - 1; i >= 0; --i)
+        if (x[i] == top && at(0, i) < n) best = at(0, i);
+      u64 left = best >= 0 ? key_of(top, first + best) : 0ull, kth = 0ull;
+      for (int b = 0; b < K; ++b) {
+        kth = warp_max(left);
+        if (kth == 0ull) break;  // fewer lanes with elements than beams: no bound from this warp
+        if (left == kth) left = 0ull;
+      }
+      if (lane == 0) s_warp[warp] = kth;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kScanWarps; ++w) bound = s_warp[w] > bound ? s_warp[w] : bound;
+      if (bound) --bound;  // that key itself enters
+    }
+    if (orderable(top) >= (uint32_t)(bound >> 32)) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const u64 k = key_of(x[i], first + at(it, i));
+        if (k <= bound || at(it, i) >= n) continue;
+        const int p = held + atomicAdd(&s_n[it % 3], 1);
+        if (p < kList) s_list[p] = k;
+      }
+    }
+    if (top > m) {
+      if (m > -INFINITY) {
+        const float f = expf(m - top);
+        s *= f;
+        comp *= f;
+      }
+      m = top;
+    }
+    if (m > -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < PER; i += 4) {
+        const float q = (expf(x[i] - m) + expf(x[i + 1] - m)) + (expf(x[i + 2] - m) + expf(x[i + 3] - m));
+        const float t = s + q, r = t - s;  // t + the bracket below is s + q exactly
+        comp += (s - (t - r)) + (q - r);
+        s = t;
+      }
+    }
+    if (tid == 0) s_n[(it + 1) % 3] = 0;
+    __syncthreads();
+    int count = held + s_n[it % 3];
+    if (count > kList) {  // the step's entries one by one: the largest below the last one taken
+      u64 last = ~0ull;
+      for (int b = 0; b < K; ++b) {
+        u64 k = 0ull;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const u64 y = key_of(x[i], first + at(it, i));
+          if (at(it, i) < n && y > bound && y < last && y > k) k = y;
+        }
+        k = warp_max(k);
+        __syncthreads();
+        if (lane == 0) s_warp[warp] = k;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kScanWarps; ++w) k = s_warp[w] > k ? s_warp[w] : k;
+        if (tid == 0) s_list[held + b] = k;  // held <= kList / 2
+        last = k;
+      }
+      count = held + K;
+      __syncthreads();
+    }
+    held = count;
+    if (it == 0 || it == steps - 1 || count > kList / 2) {  // the list's best, in order
+      u64 mine[kList / kScanThreads];
+      int place[kList / kScanThreads];
+#pragma unroll
+      for (int q = 0; q < kList / kScanThreads; ++q) {
+        const int e = q * kScanThreads + tid;
+        place[q] = K;
+        mine[q] = 0ull;
+        if (e >= count) continue;
+        mine[q] = s_list[e];
+        int above = 0;
+        for (int f = 0; f < count; ++f) above += s_list[f] > mine[q];
+        place[q] = above;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < kList / kScanThreads; ++q)
+        if (place[q] < K) s_list[place[q]] = mine[q];
+      __syncthreads();
+      held = min(count, K);
+      if (held == K) bound = s_list[K - 1];
     }
   }
-  double d = (double)s + (double)comp;
+  if (bad) report(a.status, MK_ERR_NAN, PO_SELECT, row, chunk);
+  u64* out = a.cand + ((long long)row * a.chunks + chunk) * K;
+  for (int b = tid; b < K; b += kScanThreads) out[b] = b < held ? s_list[b] : 0ull;
+  float M = m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) s_f[warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kScanWarps; ++w) M = fmaxf(M, s_f[w]);
+  double d = 0.0;
+  if (m > -INFINITY) {
+    const float f = expf(m - M);
+    d = ((double)s + (double)comp) * (double)f;
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
   if (lane == 0) s_d[warp] = d;
@@ -165,37 +231,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(const __grid_constan
     double sum = 0.0;
 #pragma unroll
     for (int w = 0; w < kScanWarps; ++w) sum += s_d[w];
-    a.stat[(long long)row * a.chunks + chunk] = make_float4(m, (float)sum, (float)(sum - (double)(float)sum), 0.f);
-  }
-  const int count = s_n;
-  u64* out = a.cand + ((long long)row * a.chunks + chunk) * a.beams;
-  if (count <= kList) {
-    for (int e = tid; e < count; e += kScanThreads) {
-      const u64 k = s_list[e];
-      int above = 0;
-      for (int f = 0; f < count; ++f) above += s_list[f] > k;
-      if (above < a.beams) out[above] = k;
-    }
-    for (int b = count + tid; b < a.beams; b += kScanThreads) out[b] = 0ull;
-    return;
-  }
-  u64 last = ~0ull;
-  for (int b = 0; b < a.beams; ++b) {  // the largest key below the last one taken
-    u64 k = 0ull;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if (at(i) >= n) continue;
-      const u64 y = key_of(x[i], first + at(i));
-      if (y < last && y > k) k = y;
-    }
-    k = warp_max(k);
-    __syncthreads();
-    if (lane == 0) s_warp[warp] = k;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kScanWarps; ++w) k = s_warp[w] > k ? s_warp[w] : k;
-    if (tid == 0) out[b] = k;
-    last = k;
+    a.stat[(long long)row * a.chunks + chunk] = make_float4(M, (float)sum, (float)(sum - (double)(float)sum), 0.f);
   }
 }
 
@@ -305,12 +341,12 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
   }
 }
 
-// Elements of a chunk: 32 per thread when that still leaves a CTA per SM and more, else 8, so
-// that one row's logits spread over more SMs.
-constexpr int kPerLarge = 32, kPerSmall = 8;
+// Elements of a CTA's part of a row: the rows' parts fill the resident CTAs (4 per SM) once,
+// in whole groups of accesses (2048), and down to one group per CTA when there are few rows.
+constexpr int kPart = 8 * kScanThreads;
 int chunk_of(long long rows, int vocab, int n_sm) {
-  const long long large = kPerLarge * kScanThreads;
-  return rows * ((vocab + large - 1) / large) >= n_sm ? (int)large : kPerSmall * kScanThreads;
+  const long long parts = std::max(1LL, 4LL * n_sm / rows), each = ((long long)vocab + parts - 1) / parts;
+  return (int)std::min((each + kPart - 1) / kPart * kPart, 1LL << 30);
 }
 
 size_t lay_out(SelectArgs* a, void* ws, long long rows, int beams, int chunks) {
@@ -323,9 +359,7 @@ size_t lay_out(SelectArgs* a, void* ws, long long rows, int beams, int chunks) {
 
 template <typename T>
 mk_status launch_scan(const SelectArgs& a, bool vec, void* stream) {
-  const bool large = a.chunk == kPerLarge * kScanThreads;
-  auto k = large ? (vec ? scan_kernel<T, kPerLarge, true> : scan_kernel<T, kPerLarge, false>)
-                 : (vec ? scan_kernel<T, kPerSmall, true> : scan_kernel<T, kPerSmall, false>);
+  auto k = vec ? scan_kernel<T, true> : scan_kernel<T, false>;
   return launch_dependent(k, dim3((unsigned)(a.rows * a.chunks)), dim3(kScanThreads), 0, stream, "mk_beam_select", a);
 }
 
@@ -338,7 +372,7 @@ extern "C" mk_status mk_beam_select_workspace(int groups, int beams, int vocab, 
   if (groups < 1 || beams < 1 || beams > kMaxBeams || vocab < beams)
     return paged_fail(MK_ERR_INVALID, "groups must be positive, beams in [1, 32] and at most vocab");
   const long long rows = (long long)groups * beams;
-  if (rows * (vocab / (kPerSmall * kScanThreads) + 1) > 0x7fffffffLL)
+  if (rows * (vocab / kPart + 1) > 0x7fffffffLL)
     return paged_fail(MK_ERR_INVALID, "groups * beams * vocab out of range");
   int n_sm = 0;
   const mk_status s = sm_count(&n_sm);
