@@ -45,6 +45,8 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 constexpr int kMaxFreqs = 64;  // head_dim / 2 at most
+constexpr int kMaxTokens = 8;  // of a CTA
+constexpr int kCtasPerSm = 4;
 
 struct AppendArgs {
   const void *q, *k, *v;
@@ -53,124 +55,182 @@ struct AppendArgs {
   const int32_t *positions, *rows, *table;
   const double* freqs;
   int32_t* status;
-  int hq, hkv, page_size, n_pages, n_rows, width, n_freqs;
+  int n_tokens, per_cta, hq, hkv, page_size, n_pages, n_rows, width, n_freqs;
   float mscale;
 };
 
-// One CTA per token.  A head is cut into items of 16 elements, one per thread at a time: in
-// the half layout item c < n_freqs / 8 holds elements [8c, 8c + 8) and their partners
-// [n_freqs + 8c, ..), so that a rotation stays in one thread, and the others 16 consecutive
-// ones; interleaved, every item is 16 consecutive elements.  Without 16-byte alignment, or
-// when n_freqs does not fill whole items, the same work goes element pair by element pair.
-//
-// The angle position * freq is taken in 64 bits in units of pi and reduced there to
-// [-1, 1] before sine and cosine, which is what keeps far positions exact (at position 10^6
-// a 32-bit product would be off by 0.06 rad); once per pair and token, shared by all heads
-// through shared memory, 64-bit arithmetic costs nothing beside the vectors' traffic.
-template <typename T, typename C, int HD, bool INTER, bool VEC>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs a) {
-  __shared__ float s_cos[kMaxFreqs], s_sin[kMaxFreqs];
-  pdl_wait();
-  pdl_launch();
-  const int t = blockIdx.x, tid = threadIdx.x;
-  const int pos = a.positions[t];
-  if (pos < 0) return;
-  const int row = a.rows ? a.rows[t] : t;
-  const int slot = pos / a.page_size;
+// The angle position * freq is taken in 64 bits in units of pi and reduced there to [-1, 1]
+// before sine and cosine, which is what keeps far positions exact (at position 10^6 a 32-bit
+// product would be off by 0.06 rad); once per pair and token, shared by all heads through
+// shared memory, 64-bit arithmetic costs nothing beside the vectors' traffic.
+__device__ __forceinline__ void turn_of(const AppendArgs& a, int pos, int i, float* c, float* s) {
+  const double turns = (double)pos * (a.freqs[i] * 0.31830988618379067154);  // angle / pi
+  sincospif((float)(turns - 2.0 * rint(turns * 0.5)), s, c);
+  *c *= a.mscale;
+  *s *= a.mscale;
+}
+
+// where a token goes: the page and the row of it (page -1: nowhere)
+__device__ __forceinline__ int2 place_of(const AppendArgs& a, int t, int pos) {
+  const int row = a.rows ? a.rows[t] : t, slot = pos / a.page_size;
   int page = -1;
   if ((unsigned)row < (unsigned)a.n_rows && slot < a.width) page = a.table[(long long)row * a.table_stride + slot];
-  const bool placed = (unsigned)page < (unsigned)a.n_pages;
-  if (!placed && tid == 0) report(a.status, MK_ERR_PAGES, PO_APPEND, row, pos);
-  if (tid < a.n_freqs) {
-    const double turns = (double)pos * (a.freqs[tid] * 0.31830988618379067154);  // angle / pi
-    const double r = turns - 2.0 * rint(turns * 0.5);
-    float s, c;
-    sincospif((float)r, &s, &c);
-    s_cos[tid] = c * a.mscale;
-    s_sin[tid] = s * a.mscale;
+  if ((unsigned)page >= (unsigned)a.n_pages) {
+    report(a.status, MK_ERR_PAGES, PO_APPEND, row, pos);
+    page = -1;
+  }
+  return make_int2(page, pos - slot * a.page_size);
+}
+
+// A CTA takes `per_cta` tokens.  A head is cut into items of 16 elements, one per lane: in the
+// half layout item c < n_freqs / 8 holds elements [8c, 8c + 8) and their partners
+// [n_freqs + 8c, ..), so that a rotation stays in one lane, and the others 16 consecutive
+// ones; interleaved, every item is 16 consecutive elements.  A warp takes 32 items (4 heads
+// of 128 dims, 8 of 64) of a token at a time, queries first, then keys, then values; the
+// vectors of its next turn are in flight while it works, the first ones while the CTA looks
+// up its tokens' places and angles.  Bound: the vectors' bytes, read and written once; for a
+// few tokens the chain of loads from the position over the table to the store.
+template <typename T, typename C, int HD, bool INTER>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int ITEMS = HD / 16, HPW = 32 / ITEMS, WARPS = kAppendThreads / 32;
+  __shared__ __align__(16) float s_cos[kMaxTokens][kMaxFreqs], s_sin[kMaxTokens][kMaxFreqs];
+  __shared__ int2 s_place[kMaxTokens];
+  __shared__ int s_pos[kMaxTokens];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane % ITEMS;
+  pdl_wait();
+  pdl_launch();
+  const int t0 = blockIdx.x * a.per_cta, nt = min(a.per_cta, a.n_tokens - t0);
+  const int heads = a.hq + 2 * a.hkv, blocks = (heads + HPW - 1) / HPW, jobs = nt * blocks;
+  const bool turned = c < a.n_freqs / 8;
+  const int e0 = !INTER && turned ? 8 * c : 16 * c, e1 = !INTER && turned ? a.n_freqs + 8 * c : 16 * c + 8;
+  Raw8<T> rx, ry;
+  auto load = [&](int job) {
+    const int i = job / blocks, t = t0 + i, h = (job - i * blocks) * HPW + lane / ITEMS;
+    if (h >= heads) return;
+    const T* src = h < a.hq           ? static_cast<const T*>(a.q) + t * a.q_t + h * a.q_h
+                   : h < a.hq + a.hkv ? static_cast<const T*>(a.k) + t * a.k_t + (h - a.hq) * a.k_h
+                                      : static_cast<const T*>(a.v) + t * a.v_t + (h - a.hq - a.hkv) * a.v_h;
+    rx.load(src + e0);
+    ry.load(src + e1);
+  };
+  if (warp < jobs) load(warp);
+  for (int i = tid; i < nt; i += kAppendThreads) {
+    const int pos = a.positions[t0 + i];
+    s_pos[i] = pos;
+    s_place[i] = pos >= 0 ? place_of(a, t0 + i, pos) : make_int2(-1, 0);
+  }
+  for (int x = tid; x < nt * kMaxFreqs; x += kAppendThreads) {
+    const int i = x / kMaxFreqs, f = x % kMaxFreqs;
+    if (f < a.n_freqs) turn_of(a, a.positions[t0 + i], f, &s_cos[i][f], &s_sin[i][f]);
   }
   __syncthreads();
-  const long long in_page = (long long)page * a.page_stride + (long long)(pos - slot * a.page_size) * HD;
-  C* kc = static_cast<C*>(a.kc) + in_page;
-  C* vc = static_cast<C*>(a.vc) + in_page;
-  // heads in the order queries, keys, values; a token without a place has its queries only
-  const int heads = a.hq + (placed ? 2 * a.hkv : 0);
-  constexpr int PER = VEC ? HD / 16 : HD / 2;  // items, or pairs, of a head
-  for (int i = tid; i < heads * PER; i += kAppendThreads) {
-    const int h = i / PER, c = i % PER;
+  for (int job = warp; job < jobs; job += WARPS) {
+    const int i = job / blocks, t = t0 + i, h = (job - i * blocks) * HPW + lane / ITEMS;
+    float x[8], y[8];
+    rx.up(x);
+    ry.up(y);
+    if (job + WARPS < jobs) load(job + WARPS);
+    const int2 place = s_place[i];
     const bool is_q = h < a.hq, is_v = h >= a.hq + a.hkv;
+    if (h >= heads || s_pos[i] < 0 || (!is_q && place.x < 0)) continue;
+    if (turned && !is_v) {
+      float cs[8], sn[8];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        *reinterpret_cast<float4*>(cs + 4 * q) = *reinterpret_cast<const float4*>(&s_cos[i][8 * c + 4 * q]);
+        *reinterpret_cast<float4*>(sn + 4 * q) = *reinterpret_cast<const float4*>(&s_sin[i][8 * c + 4 * q]);
+      }
+      if (INTER) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float xa = x[2 * j], ya = y[2 * j];
+          x[2 * j] = xa * cs[j] - x[2 * j + 1] * sn[j];
+          x[2 * j + 1] = x[2 * j + 1] * cs[j] + xa * sn[j];
+          y[2 * j] = ya * cs[4 + j] - y[2 * j + 1] * sn[4 + j];
+          y[2 * j + 1] = y[2 * j + 1] * cs[4 + j] + ya * sn[4 + j];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float xa = x[j];
+          x[j] = xa * cs[j] - y[j] * sn[j];
+          y[j] = y[j] * cs[j] + xa * sn[j];
+        }
+      }
+    }
+    if (is_q) {
+      T* dst = static_cast<T*>(a.qo) + t * a.o_t + h * a.o_h;
+      store8<T>(dst + e0, x);
+      store8<T>(dst + e1, y);
+    } else {
+      C* dst = static_cast<C*>(is_v ? a.vc : a.kc) + (long long)place.x * a.page_stride +
+               ((long long)(is_v ? h - a.hq - a.hkv : h - a.hq) * a.page_size + place.y) * HD;
+      store8<C>(dst + e0, x);
+      store8<C>(dst + e1, y);
+    }
+  }
+}
+
+// The same without 16-byte alignment, or when n_freqs does not fill whole items: element
+// pair by element pair, one CTA per token.
+template <typename T, typename C, int HD, bool INTER>
+__global__ void __launch_bounds__(kAppendThreads) append_pairs_kernel(const __grid_constant__ AppendArgs a) {
+  __shared__ float s_cos[kMaxFreqs], s_sin[kMaxFreqs];
+  __shared__ int2 s_place;
+  pdl_wait();
+  pdl_launch();
+  const int t = blockIdx.x, tid = threadIdx.x, pos = a.positions[t];
+  if (pos < 0) return;
+  if (tid == 0) s_place = place_of(a, t, pos);
+  if (tid < a.n_freqs) turn_of(a, pos, tid, &s_cos[tid], &s_sin[tid]);
+  __syncthreads();
+  const int2 place = s_place;
+  const int heads = a.hq + (place.x >= 0 ? 2 * a.hkv : 0);
+  for (int i = tid; i < heads * (HD / 2); i += kAppendThreads) {
+    const int h = i / (HD / 2), c = i % (HD / 2);
+    const bool is_q = h < a.hq, is_v = h >= a.hq + a.hkv, turned = c < a.n_freqs;
     const int hk = is_v ? h - a.hq - a.hkv : h - a.hq;
     const T* src = is_q   ? static_cast<const T*>(a.q) + t * a.q_t + h * a.q_h
                    : is_v ? static_cast<const T*>(a.v) + t * a.v_t + hk * a.v_h
                           : static_cast<const T*>(a.k) + t * a.k_t + hk * a.k_h;
-    T* qd = static_cast<T*>(a.qo) + t * a.o_t + h * a.o_h;
-    C* cd = (is_v ? vc : kc) + (long long)hk * a.page_size * HD;
-    if (VEC) {
-      const bool turned = c < a.n_freqs / 8;
-      // in the half layout a head's rotating items come in two pieces, for values too
-      const int e0 = !INTER && turned ? 8 * c : 16 * c, e1 = !INTER && turned ? a.n_freqs + 8 * c : 16 * c + 8;
-      float x[8], y[8];
-      load8(src + e0, x);
-      load8(src + e1, y);
-      if (turned && !is_v) {
-        if (INTER) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float c0 = s_cos[8 * c + j], s0 = s_sin[8 * c + j], c1 = s_cos[8 * c + 4 + j], s1 = s_sin[8 * c + 4 + j];
-            const float xa = x[2 * j], ya = y[2 * j];
-            x[2 * j] = xa * c0 - x[2 * j + 1] * s0;
-            x[2 * j + 1] = x[2 * j + 1] * c0 + xa * s0;
-            y[2 * j] = ya * c1 - y[2 * j + 1] * s1;
-            y[2 * j + 1] = y[2 * j + 1] * c1 + ya * s1;
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float cs = s_cos[8 * c + j], sn = s_sin[8 * c + j], xa = x[j];
-            x[j] = xa * cs - y[j] * sn;
-            y[j] = y[j] * cs + xa * sn;
-          }
-        }
-      }
-      if (is_q) {
-        store8(qd + e0, x);
-        store8(qd + e1, y);
-      } else {
-        store8(cd + e0, x);
-        store8(cd + e1, y);
-      }
+    const int e0 = !INTER && turned ? c : 2 * c, e1 = !INTER && turned ? a.n_freqs + c : 2 * c + 1;
+    float x = Conv<T>::up(src[e0]), y = Conv<T>::up(src[e1]);
+    if (turned && !is_v) {
+      const float xa = x;
+      x = xa * s_cos[c] - y * s_sin[c];
+      y = y * s_cos[c] + xa * s_sin[c];
+    }
+    if (is_q) {
+      T* dst = static_cast<T*>(a.qo) + t * a.o_t + h * a.o_h;
+      dst[e0] = Conv<T>::down(x);
+      dst[e1] = Conv<T>::down(y);
     } else {
-      const int e0 = !INTER && c < a.n_freqs ? c : 2 * c, e1 = !INTER && c < a.n_freqs ? a.n_freqs + c : 2 * c + 1;
-      float x = Conv<T>::up(src[e0]), y = Conv<T>::up(src[e1]);
-      if (c < a.n_freqs && !is_v) {
-        const float xa = x;
-        x = xa * s_cos[c] - y * s_sin[c];
-        y = y * s_cos[c] + xa * s_sin[c];
-      }
-      if (is_q) {
-        qd[e0] = Conv<T>::down(x);
-        qd[e1] = Conv<T>::down(y);
-      } else {
-        cd[e0] = Conv<C>::down(x);
-        cd[e1] = Conv<C>::down(y);
-      }
+      C* dst = static_cast<C*>(is_v ? a.vc : a.kc) + (long long)place.x * a.page_stride +
+               ((long long)hk * a.page_size + place.y) * HD;
+      dst[e0] = Conv<C>::down(x);
+      dst[e1] = Conv<C>::down(y);
     }
   }
 }
 
 template <typename T, typename C, int HD>
-mk_status launch_append(const AppendArgs& a, int n, bool inter, bool vec, void* stream) {
-  auto k = inter ? (vec ? append_kernel<T, C, HD, true, true> : append_kernel<T, C, HD, true, false>)
-                 : (vec ? append_kernel<T, C, HD, false, true> : append_kernel<T, C, HD, false, false>);
-  return launch_dependent(k, dim3(n), dim3(kAppendThreads), 0, stream, "mk_rope_append", a);
+mk_status launch_append(AppendArgs a, int n_sm, bool inter, bool vec, void* stream) {
+  const char* what = "mk_rope_append";
+  if (!vec)
+    return launch_dependent(inter ? append_pairs_kernel<T, C, HD, true> : append_pairs_kernel<T, C, HD, false>,
+                            dim3(a.n_tokens), dim3(kAppendThreads), 0, stream, what, a);
+  // a token per CTA while that leaves SMs free, then up to kMaxTokens, which spread the look-up
+  a.per_cta = std::min(kMaxTokens, std::max(1, a.n_tokens / (kCtasPerSm * n_sm)));
+  return launch_dependent(inter ? append_kernel<T, C, HD, true> : append_kernel<T, C, HD, false>,
+                          dim3((a.n_tokens + a.per_cta - 1) / a.per_cta), dim3(kAppendThreads), 0, stream, what, a);
 }
 template <typename T>
-mk_status launch_append(const AppendArgs& a, int n, int cache_dtype, int hd, bool inter, bool vec, void* stream) {
+mk_status launch_append(const AppendArgs& a, int n_sm, int cache_dtype, int hd, bool inter, bool vec, void* stream) {
   if (cache_dtype == MK_F16)
-    return hd == 64 ? launch_append<T, __half, 64>(a, n, inter, vec, stream)
-                    : launch_append<T, __half, 128>(a, n, inter, vec, stream);
-  return hd == 64 ? launch_append<T, __nv_bfloat16, 64>(a, n, inter, vec, stream)
-                  : launch_append<T, __nv_bfloat16, 128>(a, n, inter, vec, stream);
+    return hd == 64 ? launch_append<T, __half, 64>(a, n_sm, inter, vec, stream)
+                    : launch_append<T, __half, 128>(a, n_sm, inter, vec, stream);
+  return hd == 64 ? launch_append<T, __nv_bfloat16, 64>(a, n_sm, inter, vec, stream)
+                  : launch_append<T, __nv_bfloat16, 128>(a, n_sm, inter, vec, stream);
 }
 
 }  // namespace
@@ -203,7 +263,7 @@ extern "C" mk_status mk_rope_append(const mk_append_args* args, const mk_page_vi
   a.v_t = args->v_token; a.v_h = args->v_head; a.o_t = args->o_token; a.o_h = args->o_head;
   a.page_stride = cache->page_stride; a.table_stride = cache->table_stride;
   a.positions = args->positions; a.rows = args->rows; a.table = cache->table; a.freqs = args->freqs; a.status = status;
-  a.hq = args->q ? args->n_heads : 0;
+  a.n_tokens = args->n_tokens; a.hq = args->q ? args->n_heads : 0;
   a.hkv = cache->n_kv_heads; a.page_size = cache->page_size; a.n_pages = cache->n_pages; a.n_rows = cache->n_rows;
   a.width = cache->table_width; a.n_freqs = args->n_freqs; a.mscale = args->mscale;
   // 16-byte accesses need aligned vectors and whole rotating items
@@ -214,11 +274,14 @@ extern "C" mk_status mk_rope_append(const mk_append_args* args, const mk_page_vi
   if (args->q)
     for (long long s : {a.q_t, a.q_h, a.o_t, a.o_h}) vec = vec && s % per == 0;
   const bool inter = args->interleaved != 0;
+  int n_sm = 0;
+  const mk_status s = sm_count(&n_sm);
+  if (s) return s;
   if (args->dtype == MK_F32)
-    return launch_append<float>(a, args->n_tokens, cache->dtype, cache->head_dim, inter, vec, stream);
+    return launch_append<float>(a, n_sm, cache->dtype, cache->head_dim, inter, vec, stream);
   if (args->dtype == MK_F16)
-    return launch_append<__half>(a, args->n_tokens, cache->dtype, cache->head_dim, inter, vec, stream);
-  return launch_append<__nv_bfloat16>(a, args->n_tokens, cache->dtype, cache->head_dim, inter, vec, stream);
+    return launch_append<__half>(a, n_sm, cache->dtype, cache->head_dim, inter, vec, stream);
+  return launch_append<__nv_bfloat16>(a, n_sm, cache->dtype, cache->head_dim, inter, vec, stream);
 }
 
 extern "C" mk_status mk_rope_freqs(const mk_rope_desc* d, double* freqs, float* mscale) {

@@ -113,18 +113,6 @@ __device__ __forceinline__ long long share_of(const AttendArgs& a, long long uni
 }
 
 template <typename T>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi);
-template <>
-__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <>
-__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <typename T>
 __device__ __forceinline__ float2 unpack2(uint32_t w);
 template <>
 __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {

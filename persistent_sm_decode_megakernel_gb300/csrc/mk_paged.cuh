@@ -80,22 +80,40 @@ struct Conv<__nv_bfloat16> {
   static __device__ __forceinline__ __nv_bfloat16 down(float x) { return __float2bfloat16_rn(x); }
 };
 
-// 8 consecutive elements between memory (16-byte aligned) and floats
+// 8 consecutive elements of memory (16-byte aligned), as they lie there
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
-  alignas(16) T raw[8];
+struct Raw8 {
+  uint4 w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(raw)[i] = reinterpret_cast<const uint4*>(p)[i];
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void up(float (&x)[8]) const {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = Conv<T>::up(raw[i]);
+    for (int i = 0; i < 8; ++i) x[i] = Conv<T>::up(reinterpret_cast<const T*>(w)[i]);
+  }
+};
+// two floats rounded to a pair of 16-bit values in one word
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
-  alignas(16) T raw[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) raw[i] = Conv<T>::down(x[i]);
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(raw)[i];
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
+}
+template <>
+__device__ __forceinline__ void store8<float>(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 #endif
 

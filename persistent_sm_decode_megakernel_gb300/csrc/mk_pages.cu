@@ -1,11 +1,12 @@
 // Page table updates of a paged KV cache (mk_update_pages: fork, free, reserve) and its
 // compaction (mk_compact_pages), with the copies of pages over all layers.
 //
-// Both are a plan of integers and a copy.  mk_update_pages takes three launches: `count`
-// (a CTA per row) moves the holders' counts from the old table to the shared part of the new
-// one and saves the old table; `plan` (one CTA) decides who copies a page, takes the lowest
-// free pages by a scan of the counts and commits, or finds that it cannot; `apply` (all SMs)
-// writes the table rows and copies the pages -- or, after a refusal, gives the counts back.
+// Both are a plan of integers and a copy.  mk_update_pages takes three steps: `count` (a CTA
+// per row) moves the holders' counts from the old table to the shared part of the new one and
+// saves the old table; `plan` (one CTA) decides who copies a page, takes the lowest free
+// pages by a scan of the counts and commits, or finds that it cannot; `apply` (all SMs) writes
+// the table rows and copies the pages -- or, after a refusal, gives the counts back.  Tables
+// of up to kCountInPlan entries are counted by the plan's CTA itself, which saves a launch.
 // The counts are integer sums, so the order of their atomics does not show.
 #include <algorithm>
 
@@ -15,13 +16,14 @@ namespace mk {
 namespace {
 
 constexpr int kMaxRows = 4096;
-constexpr int kPlanThreads = 1024;
 constexpr int kRowThreads = 256;
 constexpr int kCopyThreads = 256;
 constexpr int kUnitBytes = kCopyThreads * 16;  // a copy's unit: one 16-byte access per thread
 constexpr int kInFlight = 4;                   // units a thread has in flight
 constexpr int kCopyCtasPerSm = 4;
-constexpr int kMost = (1 << 30) - 1;           // counts of pages saturate here
+constexpr int kNarrowThreads = 256, kWideThreads = 1024;  // of the plan: one row per thread where that will do
+constexpr int kCountInPlan = 2048;             // entries of a table that the plan counts itself
+using u64 = unsigned long long;
 
 struct PoolArgs {
   char *k, *v;
@@ -79,93 +81,102 @@ __device__ __forceinline__ bool take_of(const PoolArgs& a, int r, Take* t) {
 
 __device__ __forceinline__ int page_or_none(const PoolArgs& a, int id) { return (unsigned)id < (unsigned)a.n_pages ? id : -1; }
 
+// one entry of the table: saved, and the counts moved to what the row will hold there
+__device__ __forceinline__ void count_entry(const PoolArgs& a, int r, int i, const Take& t, bool ok) {
+  const int raw = a.table[(long long)r * a.table_stride + i], o = page_or_none(a, raw);
+  int n = -1;
+  if (ok && i < t.held) n = page_or_none(a, a.table[(long long)t.parent * a.table_stride + i]);
+  if (raw >= a.n_pages) report(a.status, MK_ERR_PAGES, PO_UPDATE, r, raw);
+  a.snap[(long long)r * a.width + i] = o;
+  if (!ok || o == n) return;
+  if (o >= 0) atomicSub(a.refs + o, 1);
+  if (n >= 0) atomicAdd(a.refs + n, 1);
+}
+
 __global__ void __launch_bounds__(kRowThreads) count_kernel(const __grid_constant__ PoolArgs a) {
   pdl_wait();
   pdl_launch();
   const int r = blockIdx.x;
   Take t;
   const bool ok = take_of(a, r, &t);
-  const int32_t* old = a.table + (long long)r * a.table_stride;
-  const int32_t* from = a.table + (long long)(ok ? max(t.parent, 0) : r) * a.table_stride;
-  for (int i = threadIdx.x; i < a.width; i += kRowThreads) {
-    const int raw = old[i], o = page_or_none(a, raw);
-    if (raw >= a.n_pages) report(a.status, MK_ERR_PAGES, PO_UPDATE, r, raw);
-    a.snap[(long long)r * a.width + i] = o;
-    if (!ok) continue;
-    const int n = i < t.held ? page_or_none(a, from[i]) : -1;
-    if (o == n) continue;
-    if (o >= 0) atomicSub(a.refs + o, 1);
-    if (n >= 0) atomicAdd(a.refs + n, 1);
-  }
+  for (int i = threadIdx.x; i < a.width; i += kRowThreads) count_entry(a, r, i, t, ok);
 }
 
-__device__ __forceinline__ int add_sat(int x, int y) { return min(x + y, kMost); }
-// exclusive prefix sum of one int in [0, kMost] per thread over the CTA; the total in *total
-// (with a saturated total the prefixes say nothing: the call is refused)
-__device__ __forceinline__ int block_scan(int x, int* sums, int* total) {
+// exclusive prefix sum of a number per thread over the CTA; the total in *total
+template <int THREADS>
+__device__ __forceinline__ u64 block_scan(u64 x, u64* sums, u64* total) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int inc = x;
+  u64 inc = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc = add_sat(inc, y);
+    const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
   }
   if (lane == 31) sums[warp] = inc;
   __syncthreads();
-  if (warp == 0) {
-    int s = sums[lane];
+  u64 base = 0, all = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s = add_sat(s, y);
-    }
-    sums[lane] = s;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w == warp) base = all;
+    all += sums[w];
   }
+  *total = all;
   __syncthreads();
-  const int base = warp ? sums[warp - 1] : 0;
-  *total = sums[31];
-  __syncthreads();
-  return add_sat(base, inc - x);
+  return base + inc - x;
 }
 
 // Appends to `out` the ids in [from, to) for which want(refs[id]) holds, ascending, until
 // `most` are found; returns how many were found (at most `most`).
-template <typename Want>
-__device__ __forceinline__ int list_pages(const int32_t* refs, int from, int to, int most, int32_t* out, int* sums,
+template <int THREADS, typename Want>
+__device__ __forceinline__ int list_pages(const int32_t* refs, int from, int to, int most, int32_t* out, u64* sums,
                                           Want want) {
   int found = 0;
-  for (int base = from; base < to && found < most; base += kPlanThreads * 4) {
+  for (int base = from; base < to && found < most; base += THREADS * 4) {
     const int p0 = base + (int)threadIdx.x * 4;
+    int held[4];
     bool is[4];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) is[x] = p0 + x < to && want(refs[p0 + x]);
-    int total;
-    int at = found + block_scan(is[0] + is[1] + is[2] + is[3], sums, &total);
+    for (int x = 0; x < 4; ++x) held[x] = p0 + x < to ? __ldcg(refs + p0 + x) : 0;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) is[x] = p0 + x < to && want(held[x]);
+    u64 total;
+    int at = found + (int)block_scan<THREADS>(is[0] + is[1] + is[2] + is[3], sums, &total);
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       if (is[x] && at < most) out[at] = p0 + x;
       at += is[x];
     }
-    found = min(most, found + total);
+    found = min(most, found + (int)total);
   }
   return found;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PoolArgs a) {
-  __shared__ int s_sums[32], s_last[kMaxRows], s_bad;
+// COUNT: the counting of the whole table as well.  (refs is read past L1: atomics change it.)
+template <int THREADS, int ROWS, bool COUNT>
+__global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ PoolArgs a) {
+  __shared__ u64 s_sums[THREADS / 32];
+  __shared__ int s_last[ROWS];
   const int tid = threadIdx.x;
   pdl_wait();
   pdl_launch();
-  if (tid == 0) s_bad = 0;
-  __syncthreads();
-  constexpr int PER = kMaxRows / kPlanThreads;
-  const int per = (a.n_rows + kPlanThreads - 1) / kPlanThreads;
+  if (COUNT) {
+    for (int x = tid; x < a.n_rows * a.width; x += THREADS) {
+      const int r = x / a.width;
+      Take t;
+      const bool ok = take_of(a, r, &t);
+      count_entry(a, r, x - r * a.width, t, ok);
+    }
+    __syncthreads();
+  }
+  constexpr int PER = (ROWS + THREADS - 1) / THREADS;
+  const int per = (a.n_rows + THREADS - 1) / THREADS;
   const int r0 = min(a.n_rows, tid * per), r1 = min(a.n_rows, r0 + per);
-  int len[PER], held[PER], ends[PER], copies[PER];
+  int len[PER], held[PER], ends[PER], copies[PER], holders[PER];
+  bool bad = false;
 #pragma unroll
   for (int x = 0; x < PER; ++x) {
     const int r = r0 + x;
-    len[x] = held[x] = ends[x] = copies[x] = 0;
+    len[x] = held[x] = ends[x] = copies[x] = holders[x] = 0;
     if (r >= r1) continue;
     Take t;
     bool ok = take_of(a, r, &t);
@@ -174,7 +185,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     if (room > 0 && e > a.width) ok = false;
     if (!ok) {
       report(a.status, MK_ERR_PAGES, PO_UPDATE, r, t.parent);
-      s_bad = 1;
+      bad = true;
       t.len = t.held = 0;
     }
     len[x] = t.len;
@@ -184,44 +195,44 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     int last = -1;
     if (ok && room > 0 && t.len % a.page_size) last = a.snap[(long long)t.parent * a.width + t.held - 1];
     s_last[r] = last;
+    if (last >= 0) holders[x] = __ldcg(a.refs + last);
   }
-  __syncthreads();
+  const bool any_bad = __syncthreads_or(bad);
   // of the rows that write into one page, each copies it while another holder is left
-  int need = 0, mine = 0;
+  u64 need = 0;
 #pragma unroll
   for (int x = 0; x < PER; ++x) {
     const int r = r0 + x;
     if (r >= r1) continue;
-    const int last = s_last[r];
-    if (last >= 0) {
-      const int holders = a.refs[last];
-      if (holders > 1) {
-        int before = 0;
-        for (int q = 0; q < r; ++q) before += s_last[q] == last;
-        copies[x] = before < holders - 1;
-      }
+    if (holders[x] > 1) {
+      const int last = s_last[r];
+      int before = 0;
+      for (int q = 0; q < r; ++q) before += s_last[q] == last;
+      copies[x] = before < holders[x] - 1;
     }
-    need = add_sat(need, copies[x] + ends[x] - held[x]);
-    mine += copies[x];
+    // pages needed (at most 4096 rows of 2^26), and the copies among them in the low 13 bits
+    need += ((u64)(copies[x] + ends[x] - held[x]) << 13) + copies[x];
   }
-  int total, n_copies;
-  int at = block_scan(need, s_sums, &total);
-  int c = block_scan(mine, s_sums, &n_copies);
-  bool refused = s_bad != 0;
-  int found = 0;
-  if (!refused && total > 0)
-    found = list_pages(a.refs, 0, a.n_pages, min(total, a.n_pages), a.fresh, s_sums, [](int n) { return n == 0; });
-  if (!refused && found < total) {
-    refused = true;
-    if (tid == 0) report(a.status, MK_ERR_PAGES, PO_UPDATE, -1, total - found);
+  u64 total;
+  const u64 before = block_scan<THREADS>(need, s_sums, &total);
+  const u64 pages = total >> 13;
+  bool refused = any_bad;
+  if (!refused && pages > 0) {
+    const int most = (int)min(pages, (u64)a.n_pages);
+    const int found = list_pages<THREADS>(a.refs, 0, a.n_pages, most, a.fresh, s_sums, [](int n) { return n == 0; });
+    if ((u64)found < pages) {
+      refused = true;
+      if (tid == 0) report(a.status, MK_ERR_PAGES, PO_UPDATE, -1, (int)min(pages - found, (u64)0x7fffffff));
+    }
   }
   if (tid == 0) {
     a.head[0] = refused;
-    a.head[1] = refused ? 0 : n_copies;
+    a.head[1] = refused ? 0 : (int)(total & 8191);
   }
   if (refused) return;
   __syncthreads();  // every read of refs is done, a.fresh is written
-  for (int i = tid; i < total; i += kPlanThreads) a.refs[a.fresh[i]] = 1;
+  for (int i = tid; i < (int)pages; i += THREADS) a.refs[a.fresh[i]] = 1;
+  int at = (int)(before >> 13), c = (int)(before & 8191);
 #pragma unroll
   for (int x = 0; x < PER; ++x) {
     const int r = r0 + x;
@@ -302,21 +313,23 @@ __global__ void __launch_bounds__(kCopyThreads) apply_kernel(const __grid_consta
   copy_pages(a, a.src, a.dst, a.head[1]);
 }
 
-__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid_constant__ PoolArgs a) {
-  __shared__ int s_sums[32];
+__global__ void __launch_bounds__(kWideThreads) compact_plan_kernel(const __grid_constant__ PoolArgs a) {
+  __shared__ u64 s_sums[kWideThreads / 32];
   const int tid = threadIdx.x;
   pdl_wait();
   pdl_launch();
-  int mine = 0, used;
-  for (int i = tid; i < a.n_pages; i += kPlanThreads) {
+  int mine = 0;
+  for (int i = tid; i < a.n_pages; i += kWideThreads) {
     mine += a.refs[i] > 0;
     a.rank[i] = -1;
   }
-  block_scan(mine, s_sums, &used);
-  const int n = list_pages(a.refs, used, a.n_pages, a.n_pages, a.src, s_sums, [](int c) { return c > 0; });
-  list_pages(a.refs, 0, used, n, a.fresh, s_sums, [](int c) { return c <= 0; });
+  u64 total;
+  block_scan<kWideThreads>(mine, s_sums, &total);
+  const int used = (int)total;
+  const int n = list_pages<kWideThreads>(a.refs, used, a.n_pages, a.n_pages, a.src, s_sums, [](int c) { return c > 0; });
+  list_pages<kWideThreads>(a.refs, 0, used, n, a.fresh, s_sums, [](int c) { return c <= 0; });
   __syncthreads();  // a.src and a.fresh are written, refs read
-  for (int i = tid; i < n; i += kPlanThreads) {
+  for (int i = tid; i < n; i += kWideThreads) {
     const int s = a.src[i];
     a.rank[s] = i;
     a.refs[a.fresh[i]] = a.refs[s];
@@ -350,7 +363,7 @@ mk_status fill(PoolArgs* a, const mk_page_pool* p, void* ws, size_t ws_bytes, in
   if (!aligned_to(p->k, 16) || !aligned_to(p->v, 16)) return paged_fail(MK_ERR_INVALID, "pages must be 16-byte aligned");
   if (p->n_layers < 1 || p->n_pages < 1 || p->n_rows < 1 || p->table_width < 1)
     return paged_fail(MK_ERR_INVALID, "n_layers, n_pages, n_rows and table_width must be positive");
-  if (p->n_pages >= kMost) return paged_fail(MK_ERR_INVALID, "n_pages out of range");
+  if (p->n_pages >= (1 << 30)) return paged_fail(MK_ERR_INVALID, "n_pages out of range");
   if (p->n_rows > kMaxRows) return paged_fail(MK_ERR_INVALID, "n_rows must be at most 4096");
   if (p->page_size < 16 || p->page_size > 1024 || p->page_size % 16)
     return paged_fail(MK_ERR_INVALID, "page_size must be a multiple of 16 in [16, 1024]");
@@ -398,9 +411,16 @@ extern "C" mk_status mk_update_pages(const mk_update_args* args, const mk_page_p
   int n_sm = 0;
   s = sm_count(&n_sm);
   if (s) return s;
-  s = launch_dependent(count_kernel, dim3(a.n_rows), dim3(kRowThreads), 0, stream, "mk_update_pages (count)", a);
-  if (s) return s;
-  s = launch_dependent(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, "mk_update_pages (plan)", a);
+  const bool narrow = a.n_rows <= kNarrowThreads;
+  if (narrow && (long long)a.n_rows * a.width <= kCountInPlan) {
+    s = launch_dependent(plan_kernel<kNarrowThreads, kNarrowThreads, true>, dim3(1), dim3(kNarrowThreads), 0, stream,
+                         "mk_update_pages (plan)", a);
+  } else {
+    s = launch_dependent(count_kernel, dim3(a.n_rows), dim3(kRowThreads), 0, stream, "mk_update_pages (count)", a);
+    if (s) return s;
+    s = launch_dependent(narrow ? plan_kernel<kNarrowThreads, kNarrowThreads, false> : plan_kernel<kWideThreads, kMaxRows, false>,
+                         dim3(1), dim3(narrow ? kNarrowThreads : kWideThreads), 0, stream, "mk_update_pages (plan)", a);
+  }
   if (s) return s;
   return launch_dependent(apply_kernel, dim3(n_sm * kCopyCtasPerSm), dim3(kCopyThreads), 0, stream,
                           "mk_update_pages (apply)", a);
@@ -415,7 +435,7 @@ extern "C" mk_status mk_compact_pages(const mk_page_pool* pool, void* workspace,
   int n_sm = 0;
   s = sm_count(&n_sm);
   if (s) return s;
-  s = launch_dependent(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, "mk_compact_pages (plan)", a);
+  s = launch_dependent(compact_plan_kernel, dim3(1), dim3(kWideThreads), 0, stream, "mk_compact_pages (plan)", a);
   if (s) return s;
   return launch_dependent(compact_apply_kernel, dim3(n_sm * kCopyCtasPerSm), dim3(kCopyThreads), 0, stream,
                           "mk_compact_pages (apply)", a);

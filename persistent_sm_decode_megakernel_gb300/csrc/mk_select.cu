@@ -20,8 +20,6 @@ namespace {
 constexpr int kMaxBeams = 32;
 constexpr int kScanThreads = 256;
 constexpr int kScanWarps = kScanThreads / 32;
-constexpr int kPickThreads = 256;
-constexpr int kPickWarps = kPickThreads / 32;
 constexpr int kIter = 16 * kScanThreads;  // elements of a step
 constexpr int kList = 1024;               // entries of a CTA's list
 
@@ -39,7 +37,10 @@ struct SelectArgs {
   int rows, beams, vocab, chunk, chunks, eos;
 };
 
-__device__ __forceinline__ u64 key_of(float x, int token) { return (u64)orderable(x) << 32 | (0xFFFFFFFFu - (unsigned)token); }
+// (-0 and +0 are one value, and so a tie)
+__device__ __forceinline__ u64 key_of(float x, int token) {
+  return (u64)orderable(x + 0.f) << 32 | (0xFFFFFFFFu - (unsigned)token);
+}
 __device__ __forceinline__ float value_of(u64 key) {
   const uint32_t u = (uint32_t)(key >> 32);
   return __uint_as_float((u & 0x80000000u) ? u & 0x7FFFFFFFu : ~u);
@@ -51,6 +52,21 @@ __device__ __forceinline__ u64 warp_max(u64 k) {
   const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
   const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
   return (u64)hi << 32 | lo;
+}
+
+// e^x for x <= 0: 2^(x log2 e) by the hardware's approximation, log2 e in two parts so that
+// the product has no systematic error
+__device__ __forceinline__ float exp_of(float x) {
+  const float hi = 1.44269502162933349609375f, lo = 1.92596299112661746887e-8f;  // their sum is log2 e to 2^-50
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaf(x, lo, x * hi)));
+  return y;
+}
+
+// a double as an unsigned number of the same order (NaN does not occur)
+__device__ __forceinline__ u64 ordered(double x) {
+  const u64 u = (u64)__double_as_longlong(x);
+  return (u >> 63) ? ~u : u | (1ull << 63);
 }
 
 // A CTA reads its part of a row once, kIter elements at a time with the next ones in flight.
@@ -104,18 +120,25 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_cons
   bool bad = false;
   float m = -INFINITY, s = 0.f, comp = 0.f;
   for (int it = 0; it < steps; ++it) {
-    float top = -INFINITY;
+    float top = -INFINITY, q = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       x[i] = next[i];
-      if (!(x[i] < INFINITY)) {  // NaN or +inf
-        bad = true;
-        x[i] = -INFINITY;
-      }
-      x[i] += 0.f;  // -0 and +0 are one value, and so a tie
       top = fmaxf(top, x[i]);
+      q = fmaf(0.f, x[i], q);  // NaN as soon as one is not finite
     }
     if (it + 1 < steps) load(it + 1, next);
+    if (q != q) {  // -inf is a value; NaN and +inf are reported and count as -inf
+      top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (!(x[i] < INFINITY)) {
+          bad = true;
+          x[i] = -INFINITY;
+        }
+        top = fmaxf(top, x[i]);
+      }
+    }
     if (it == 0) {
       // the lane's own largest key: the first element that reaches top (none in an empty tail)
       int best = -1;
@@ -145,7 +168,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_cons
     }
     if (top > m) {
       if (m > -INFINITY) {
-        const float f = expf(m - top);
+        const float f = exp_of(m - top);
         s *= f;
         comp *= f;
       }
@@ -154,7 +177,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_cons
     if (m > -INFINITY) {
 #pragma unroll
       for (int i = 0; i < PER; i += 4) {
-        const float q = (expf(x[i] - m) + expf(x[i + 1] - m)) + (expf(x[i + 2] - m) + expf(x[i + 3] - m));
+        const float q = (exp_of(x[i] - m) + exp_of(x[i + 1] - m)) + (exp_of(x[i + 2] - m) + exp_of(x[i + 3] - m));
         const float t = s + q, r = t - s;  // t + the bracket below is s + q exactly
         comp += (s - (t - r)) + (q - r);
         s = t;
@@ -220,7 +243,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_cons
   for (int w = 0; w < kScanWarps; ++w) M = fmaxf(M, s_f[w]);
   double d = 0.0;
   if (m > -INFINITY) {
-    const float f = expf(m - M);
+    const float f = exp_of(m - M);
     d = ((double)s + (double)comp) * (double)f;
   }
 #pragma unroll
@@ -235,97 +258,109 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_cons
   }
 }
 
-// One CTA per group, a warp per beam at a time: the beam's best from its chunks' lists (8 keys
-// per lane in registers, the best so far carried from batch to batch), its lse, and its
-// candidates' scores; then every candidate's place among the group's is the sum over the
-// beams of how many of that beam's sorted list are ahead of it.
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constant__ SelectArgs a) {
-  __shared__ double s_key[kMaxBeams][kMaxBeams];
-  __shared__ int s_token[kMaxBeams][kMaxBeams], s_len[kMaxBeams];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = blockIdx.x, K = a.beams;
+// One CTA per group, a warp per beam: the beam's best from its parts' lists (8 keys per lane
+// in registers, the best so far carried from batch to batch), its lse, and its candidates'
+// scores in 64 bits, kept as ordered integers; then every candidate's place among the group's
+// is the sum over the beams of how many of that beam's sorted list are ahead of it.  Bound:
+// one chain of loads, 64-bit exp and log, and the list steps; nothing here grows with vocab.
+__global__ void __launch_bounds__(32 * kMaxBeams) pick_kernel(const __grid_constant__ SelectArgs a) {
+  __shared__ u64 s_key[kMaxBeams][kMaxBeams];
+  __shared__ double s_score[kMaxBeams][kMaxBeams];
+  __shared__ int s_token[kMaxBeams][kMaxBeams], s_len[kMaxBeams], s_ended[kMaxBeams];
+  const int tid = threadIdx.x, lane = tid & 31, b = tid >> 5, group = blockIdx.x, K = a.beams;
   pdl_wait();
   pdl_launch();
-  for (int b = warp; b < K; b += kPickWarps) {
-    const int row = group * K + b;
+  {
+    const int row = group * K + b, total = a.chunks * K;
+    const float4* st = a.stat + (long long)row * a.chunks;
+    const u64* cand = a.cand + (long long)row * total;
+    // everything the beam needs is asked for at once
+    const int ended = a.ended[row];
     float sc = a.scores[row];
+    float4 part = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    u64 k[8];
+    if (!ended) {
+      if (lane < a.chunks) part = st[lane];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) k[x] = x * 32 + lane < total ? cand[x * 32 + lane] : 0ull;
+    }
     if (!(sc == sc)) {
       if (lane == 0) report(a.status, MK_ERR_NAN, PO_SELECT, row, -1);
       sc = -INFINITY;
     }
-    if (a.ended[row]) {
+    if (lane == 0) {
+      s_len[b] = ended ? 1 : K;
+      s_ended[b] = ended;
+    }
+    if (ended) {
       if (lane == 0) {
-        s_len[b] = 1;
-        s_key[b][0] = (double)sc;
+        s_score[b][0] = (double)sc;
+        s_key[b][0] = ordered((double)sc);
         s_token[b][0] = a.eos;
       }
-      continue;
-    }
-    const float4* st = a.stat + (long long)row * a.chunks;
-    float m = -INFINITY;
-    for (int c = lane; c < a.chunks; c += 32) m = fmaxf(m, st[c].x);
+    } else {
+      u64 mine = 0ull;  // lane q: the q-th best so far
+      for (int base = 0; base < total; base += 256) {
+        if (base) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    double sum = 0.0;
-    if (m > -INFINITY)
-      for (int c = lane; c < a.chunks; c += 32) {
-        const float4 s = st[c];
-        if (s.x > -INFINITY) sum += ((double)s.y + (double)s.z) * exp((double)s.x - (double)m);
-      }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const double lse = m > -INFINITY ? (double)m + log(sum) : 0.0;
-    const u64* cand = a.cand + (long long)row * a.chunks * K;
-    const long long total = (long long)a.chunks * K;
-    u64 mine = 0ull;  // lane k: the k-th best so far
-    for (long long base = 0; base < total; base += 256) {
-      u64 k[8];
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const long long e = base + x * 32 + lane;
-        k[x] = e < total ? cand[e] : 0ull;
-      }
-      u64 carry = mine;
-      for (int q = 0; q < K; ++q) {
-        u64 best = carry;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) best = k[x] > best ? k[x] : best;
-        const u64 win = warp_max(best);
-        if (win == 0ull) {
-          if (lane >= q) mine = 0ull;
-          break;
+          for (int x = 0; x < 8; ++x) k[x] = base + x * 32 + lane < total ? cand[base + x * 32 + lane] : 0ull;
         }
-        if (best == win) {  // one lane: the keys differ
-          if (carry == win) carry = 0ull;
+        const int rows = min(8, (total - base + 31) / 32);  // registers in use
+        u64 carry = mine;
+        for (int q = 0; q < K; ++q) {
+          u64 best = carry;
 #pragma unroll
           for (int x = 0; x < 8; ++x)
-            if (k[x] == win) k[x] = 0ull;
+            if (x < rows) best = k[x] > best ? k[x] : best;
+          const u64 win = warp_max(best);
+          if (win == 0ull) {
+            if (lane >= q) mine = 0ull;
+            break;
+          }
+          if (best == win) {  // one lane: the keys differ
+            if (carry == win) carry = 0ull;
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              if (k[x] == win) k[x] = 0ull;
+          }
+          if (lane == q) mine = win;
         }
-        if (lane == q) mine = win;
+      }
+      float m = part.x;
+      for (int c = lane + 32; c < a.chunks; c += 32) m = fmaxf(m, st[c].x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      double sum = 0.0;
+      for (int c = lane; c < a.chunks; c += 32) {
+        if (c >= 32) part = st[c];
+        if (part.x > -INFINITY) sum += ((double)part.y + (double)part.z) * exp((double)part.x - (double)m);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const double lse = m > -INFINITY ? (double)m + log(sum) : 0.0;
+      if (lane < K) {
+        const float v = value_of(mine);
+        double s = v > -INFINITY ? (double)sc + ((double)v - lse) : -INFINITY;
+        if (!(s == s)) s = -INFINITY;
+        s_score[b][lane] = s;
+        s_key[b][lane] = ordered(s);
+        s_token[b][lane] = token_of(mine);
       }
     }
-    if (lane < K) {
-      const float v = value_of(mine);
-      double key = v > -INFINITY ? (double)sc + ((double)v - lse) : -INFINITY;
-      if (!(key == key)) key = -INFINITY;
-      s_key[b][lane] = key;
-      s_token[b][lane] = token_of(mine);
-    }
-    if (lane == 0) s_len[b] = K;
   }
   __syncthreads();
-  for (int x = tid; x < K * K; x += kPickThreads) {
+  for (int x = tid; x < K * K; x += 32 * K) {
     const int b = x / K, e = x % K;
     if (e >= s_len[b]) continue;
-    const double key = s_key[b][e];
+    const u64 key = s_key[b][e];
     int place = e;
-    for (int o = 0; o < K && place < K; ++o) {
+    for (int o = 0; o < K; ++o) {
       if (o == b) continue;
       // how many of beam o's, best first, are ahead: larger, or as large and of a lower beam
       int lo = 0, hi = s_len[o];
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        const double y = s_key[o][mid];
-        if (y > key || (y == key && o < b))
+        if (s_key[o][mid] >= key + (o < b ? 0 : 1))
           lo = mid + 1;
         else
           hi = mid;
@@ -336,8 +371,8 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
     const int out = group * K + place, token = s_token[b][e];
     a.out_tokens[out] = token;
     a.out_parents[out] = group * K + b;
-    a.out_scores[out] = (float)key;
-    a.out_ended[out] = (a.ended[group * K + b] != 0 || token == a.eos) ? 1 : 0;
+    a.out_scores[out] = (float)s_score[b][e];
+    a.out_ended[out] = (s_ended[b] != 0 || token == a.eos) ? 1 : 0;
   }
 }
 
@@ -418,5 +453,5 @@ extern "C" mk_status mk_beam_select(const mk_select_args* args, int32_t* status,
       : args->dtype == MK_F16 ? launch_scan<__half>(a, vec, stream)
                               : launch_scan<__nv_bfloat16>(a, vec, stream);
   if (s) return s;
-  return launch_dependent(pick_kernel, dim3(args->groups), dim3(kPickThreads), 0, stream, "mk_beam_select (pick)", a);
+  return launch_dependent(pick_kernel, dim3(args->groups), dim3(32 * args->beams), 0, stream, "mk_beam_select (pick)", a);
 }
