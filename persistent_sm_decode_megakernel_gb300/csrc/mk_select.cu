@@ -3,7 +3,7 @@
 // A row's candidates are ordered by logit alone, so the log-softmax is not needed to choose
 // among them: one pass over the logits yields, per part of a row, the maximum, the sum of
 // exponentials and the part's `beams` largest logits; a second kernel (one CTA per group)
-// joins the parts -- lse = M + log sum_c S_c e^(M_c - M), in 64 bits -- and picks the best of
+// joins the parts -- lse = N ln 2 + ln sum_c S_c 2^(N_c - N) -- and picks the best of
 // score + logit - lse over the group's beams.
 //
 // Keys: a logit's bits as an ordered unsigned number, above the complement of its token, so
@@ -20,10 +20,16 @@ namespace {
 constexpr int kMaxBeams = 32;
 constexpr int kScanThreads = 256;
 constexpr int kScanWarps = kScanThreads / 32;
-constexpr int kIter = 16 * kScanThreads;  // elements of a step
+constexpr int kPerSmall = 8, kPerLarge = 16;  // elements of a step per thread: one step of few, or several
 constexpr int kList = 1024;               // entries of a CTA's list
 
 using u64 = unsigned long long;
+
+// of a part of a row: n, and the sum of 2^(x log2 e - n) in units of 2^-sum_bits
+struct __align__(16) Stat {
+  float n, unused;
+  u64 sum;
+};
 
 struct SelectArgs {
   const void* logits;
@@ -32,9 +38,9 @@ struct SelectArgs {
   int32_t *out_tokens, *out_parents, *out_ended, *status;
   float* out_scores;
   u64* cand;        // [rows][chunks][beams], best first; 0: none
-  float4* stat;     // [rows][chunks]: maximum, sum of e^(x - maximum) in two parts, unused
+  Stat* stat;       // [rows][chunks]
   long long row_stride;
-  int rows, beams, vocab, chunk, chunks, eos;
+  int rows, beams, vocab, chunk, chunks, eos, sum_bits;
 };
 
 // (-0 and +0 are one value, and so a tie)
@@ -54,82 +60,133 @@ __device__ __forceinline__ u64 warp_max(u64 k) {
   return (u64)hi << 32 | lo;
 }
 
-// e^x for x <= 0: 2^(x log2 e) by the hardware's approximation, log2 e in two parts so that
-// the product has no systematic error
-__device__ __forceinline__ float exp_of(float x) {
-  const float hi = 1.44269502162933349609375f, lo = 1.92596299112661746887e-8f;  // their sum is log2 e to 2^-50
+// 2^(x log2 e - n) by the hardware's approximation; log2 e in two parts, so that the exponent
+// is off by its own rounding alone
+constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.92596299112661746887e-8f;  // to 2^-50
+__device__ __forceinline__ float term_of(float x, float n) {
   float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaf(x, lo, x * hi)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaf(x, kLog2eLo, fmaf(x, kLog2eHi, -n))));
   return y;
 }
+// 2^d for a whole d in [-126, 127], exactly; 0 below
+__device__ __forceinline__ float power_of(float d) { return d < -126.f ? 0.f : __int_as_float((127 + (int)d) << 23); }
 
-// a double as an unsigned number of the same order (NaN does not occur)
-__device__ __forceinline__ u64 ordered(double x) {
-  const u64 u = (u64)__double_as_longlong(x);
-  return (u >> 63) ? ~u : u | (1ull << 63);
+// Numbers as a pair of floats (hi + lo, |lo| at most half a step of hi): about 48 bits, from
+// 32-bit instructions -- 64-bit log alone took 1.3 us of a launch of 5.
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair two_sum(float x, float y) {
+  const float s = x + y, r = s - x;
+  return {s, (x - (s - r)) + (y - r)};
 }
+// ln(u 2^shift), u > 0: u = 2^e f with f in [0.7, 1.42), ln f = 2 t + 2 t^3 / 3 + .. of
+// t = (f - 1) / (f + 1), |t| < 0.18.  The leading term is taken in pairs, the others (below
+// 0.004) in 32 bits: off by less than 2^-30 and the pair's own rounding.
+__device__ __forceinline__ Pair ln_of(u64 u, float shift) {
+  const int z = __clzll((long long)u);
+  const u64 m = u << z;                     // the leading bit on top
+  const bool half = (m >> 48) > 0xB504u;    // f above sqrt 2: take f / 2
+  const float unit = half ? 0x1p-24f : 0x1p-23f;
+  const float fh = (float)(unsigned)(m >> 40) * unit, fl = (float)(unsigned)((m >> 16) & 0xFFFFFFu) * (unit * 0x1p-24f);
+  const float e = (float)(63 - z + (half ? 1 : 0)) + shift;
+  const float nh = fh - 1.f;                // exact
+  const Pair den = two_sum(fh, 1.f);
+  const float inv = 1.f / den.hi, th = nh * inv;
+  const float tl = (fmaf(-th, den.hi, nh) + (fl - th * (den.lo + fl))) * inv;
+  const float w = th * th;
+  const float rest = w * fmaf(w, fmaf(w, fmaf(w, fmaf(w, fmaf(w, 2.f / 13, 2.f / 11), 2.f / 9), 2.f / 7), 2.f / 5), 2.f / 3);
+  const float l2h = 0.693147182464599609375f, l2l = -1.90465429995776804525e-9f;  // ln 2 to 2^-52
+  const float ph = e * l2h, pl = fmaf(e, l2h, -ph) + e * l2l;
+  const Pair s = two_sum(ph, 2.f * th);
+  return two_sum(s.hi, s.lo + (pl + fmaf(th, rest, 2.f * tl)));
+}
+// score + (v - lse), and a pair as an unsigned number of the same order
+__device__ __forceinline__ Pair score_of(float score, float v, Pair lse) {
+  const Pair d = two_sum(v, -lse.hi), s = two_sum(score, d.hi);
+  return two_sum(s.hi, s.lo + (d.lo - lse.lo));
+}
+__device__ __forceinline__ u64 ordered(Pair p) { return (u64)orderable(p.hi + 0.f) << 32 | orderable(p.lo + 0.f); }
 
 // A CTA reads its part of a row once, kIter elements at a time with the next ones in flight.
 // The `beams` largest are kept in a list in shared memory, entered by what lies above a bound.
 // The first bound comes from the lanes: the beams-th largest of a warp's 32 lane maxima has
 // at least `beams` elements at or above it.  From then on it is the list's beams-th key: the
-// list is cut down to its best after the first elements and whenever it has grown, each entry
-// counting how many are above it, which is its place; of a part in random order about
-// beams / i keys enter at the i-th elements.  Were one step's entries to overflow the list
-// (rising logits), they come out one block maximum at a time.  The sum of exponentials runs
-// against each thread's own maximum: fours in 32 bits, a compensated sum of them, and from
-// there on in 64 bits, so that the sum of any vocabulary is good to a few 2^-24 of its terms.
-template <typename T, bool VEC>
+// list is cut down to its best after steps 1, 2, 4, 8, .., each entry counting how many are
+// above it, which is its place; of a part in random order about `beams` keys enter between
+// two of those.  Should the list overflow (rising logits), the part is read again, once per
+// beam.  The sum of exponentials runs against whole powers of two, so that joining threads,
+// steps and parts rounds nothing: a step's in 32 bits, a compensated sum of them per thread,
+// and from there on whole numbers.  Bound: the logits' bytes for many rows (the arithmetic, one
+// exponential each, is most of that time again), the launch and the block steps for few.
+template <typename T, bool VEC, int PER>
 __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_constant__ SelectArgs a) {
   __shared__ u64 s_list[kList], s_warp[kScanWarps];
-  __shared__ double s_d[kScanWarps];
   __shared__ float s_f[kScanWarps];
-  __shared__ int s_n[3];  // entries of the step, in turn: one is cleared while one is read
+  __shared__ int s_n;
   constexpr int V = VEC ? 16 / (int)sizeof(T) : 1;  // elements of an access
-  constexpr int PER = kIter / kScanThreads;
+  constexpr int kIter = PER * kScanThreads;         // elements of a step
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = a.beams;
   const int row = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks;
   pdl_wait();
   pdl_launch();
   if (a.ended[row]) return;  // it offers one token, whatever its logits
-  const T* src = static_cast<const T*>(a.logits) + (long long)row * a.row_stride;
   const int first = chunk * a.chunk, n = min(a.chunk, a.vocab - first);
+  const T* src = static_cast<const T*>(a.logits) + (long long)row * a.row_stride + first;
   // element i * V + y of step `it` is token first + it * kIter + (i * 256 + tid) * V + y
   auto at = [&](int it, int i) { return it * kIter + ((i / V) * kScanThreads + tid) * V + i % V; };
   auto load = [&](int it, float (&x)[PER]) {
+    if (VEC && (it + 1) * kIter <= n) {
 #pragma unroll
-    for (int i = 0; i < PER; i += V) {
-      const int e = at(it, i);
-      if (VEC && e + V <= n) {
+      for (int i = 0; i < PER; i += V) {
         alignas(16) T raw[V];
-        *reinterpret_cast<uint4*>(raw) = *reinterpret_cast<const uint4*>(src + first + e);
+        *reinterpret_cast<uint4*>(raw) = *reinterpret_cast<const uint4*>(src + at(it, i));
 #pragma unroll
         for (int y = 0; y < V; ++y) x[i + y] = Conv<T>::up(raw[y]);
-      } else {
-#pragma unroll
-        for (int y = 0; y < V; ++y) x[i + y] = e + y < n ? Conv<T>::up(src[first + e + y]) : -INFINITY;
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) x[i] = at(it, i) < n ? Conv<T>::up(src[at(it, i)]) : -INFINITY;
     }
   };
-  if (tid < 3) s_n[tid] = 0;
+  if (tid == 0) s_n = 0;
   float x[PER], next[PER];
   load(0, next);
   const int steps = (n + kIter - 1) / kIter;
-  int held = 0;       // entries of the list
-  u64 bound = 0ull;   // keys above it enter
+  u64 bound = 0ull;            // keys above it enter
+  float floor_ = -INFINITY;    // its value
   bool bad = false;
-  float m = -INFINITY, s = 0.f, comp = 0.f;
+  float ref = -INFINITY, s = 0.f, comp = 0.f;  // (s + comp) 2^ref: the thread's sum of e^x
   for (int it = 0; it < steps; ++it) {
-    float top = -INFINITY, q = 0.f;
+    float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       x[i] = next[i];
       top = fmaxf(top, x[i]);
-      q = fmaf(0.f, x[i], q);  // NaN as soon as one is not finite
     }
     if (it + 1 < steps) load(it + 1, next);
-    if (q != q) {  // -inf is a value; NaN and +inf are reported and count as -inf
+    // the step's sum against a whole power of two at or above the thread's largest: sums
+    // under another power are rescaled without rounding
+    float q = 0.f;
+    auto terms = [&] {
+      const float up = ceilf(top * kLog2eHi);
+      if (up > ref) {
+        if (ref > -INFINITY) {
+          const float f = power_of(ref - up);
+          s *= f;
+          comp *= f;
+        }
+        ref = up;
+      }
+      float w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < PER; ++i) w[i % 4] += term_of(x[i], ref);
+      q = (w[0] + w[1]) + (w[2] + w[3]);
+    };
+    if (fabsf(top) < INFINITY) terms();
+    if (!(fabsf(top) < INFINITY) || q != q) {  // NaN and +inf are reported and count as -inf
       top = -INFINITY;
+      q = 0.f;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         if (!(x[i] < INFINITY)) {
@@ -138,7 +195,11 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_cons
         }
         top = fmaxf(top, x[i]);
       }
+      if (top > -INFINITY) terms();
     }
+    const float sum = s + q, r = sum - s;  // sum + the bracket below is s + q exactly
+    comp += (s - (sum - r)) + (q - r);
+    s = sum;
     if (it == 0) {
       // the lane's own largest key: the first element that reaches top (none in an empty tail)
       int best = -1;
@@ -155,45 +216,39 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_cons
       __syncthreads();
 #pragma unroll
       for (int w = 0; w < kScanWarps; ++w) bound = s_warp[w] > bound ? s_warp[w] : bound;
-      if (bound) --bound;  // that key itself enters
+      if (bound) floor_ = value_of(bound--);  // that key itself enters
     }
-    if (orderable(top) >= (uint32_t)(bound >> 32)) {
+    if (top >= floor_) {
+      unsigned hits = 0;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const u64 k = key_of(x[i], first + at(it, i));
-        if (k <= bound || at(it, i) >= n) continue;
-        const int p = held + atomicAdd(&s_n[it % 3], 1);
+      for (int i = 0; i < PER; ++i) hits |= x[i] >= floor_ ? 1u << i : 0u;
+      while (hits) {
+        const int i = __ffs(hits) - 1;
+        hits &= hits - 1;
+        const int e = at(it, i);
+        float y = x[0];
+#pragma unroll
+        for (int z = 1; z < PER; ++z) y = z == i ? x[z] : y;
+        const u64 k = key_of(y, first + e);
+        if (k <= bound || e >= n) continue;
+        const int p = atomicAdd(&s_n, 1);
         if (p < kList) s_list[p] = k;
       }
     }
-    if (top > m) {
-      if (m > -INFINITY) {
-        const float f = exp_of(m - top);
-        s *= f;
-        comp *= f;
-      }
-      m = top;
-    }
-    if (m > -INFINITY) {
-#pragma unroll
-      for (int i = 0; i < PER; i += 4) {
-        const float q = (exp_of(x[i] - m) + exp_of(x[i + 1] - m)) + (exp_of(x[i + 2] - m) + exp_of(x[i + 3] - m));
-        const float t = s + q, r = t - s;  // t + the bracket below is s + q exactly
-        comp += (s - (t - r)) + (q - r);
-        s = t;
-      }
-    }
-    if (tid == 0) s_n[(it + 1) % 3] = 0;
+    if ((it & (it + 1)) != 0 && it + 1 < steps) continue;
+    // ---- after steps 1, 2, 4, .. and the last: the list's best, in order
     __syncthreads();
-    int count = held + s_n[it % 3];
-    if (count > kList) {  // the step's entries one by one: the largest below the last one taken
+    int count = s_n;
+    if (count > kList) {  // too many: the part's largest one by one, each below the last
       u64 last = ~0ull;
+      const int seen = min(n, (it + 1) * kIter);
       for (int b = 0; b < K; ++b) {
         u64 k = 0ull;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const u64 y = key_of(x[i], first + at(it, i));
-          if (at(it, i) < n && y > bound && y < last && y > k) k = y;
+        for (int e = tid; e < seen; e += kScanThreads) {
+          float y = Conv<T>::up(src[e]);
+          if (!(y < INFINITY)) y = -INFINITY;
+          const u64 z = key_of(y, first + e);
+          if (z < last && z > k) k = z;
         }
         k = warp_max(k);
         __syncthreads();
@@ -201,90 +256,126 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_cons
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < kScanWarps; ++w) k = s_warp[w] > k ? s_warp[w] : k;
-        if (tid == 0) s_list[held + b] = k;  // held <= kList / 2
+        if (tid == 0) s_list[b] = k;
         last = k;
       }
-      count = held + K;
+      count = K;
       __syncthreads();
-    }
-    held = count;
-    if (it == 0 || it == steps - 1 || count > kList / 2) {  // the list's best, in order
+    } else {
+      // a short list takes a pair of threads per entry, each counting over one half
+      const int share = count <= kScanThreads / 2 ? 2 : 1, part = share == 2 ? tid & 1 : 0;
+      const int f0 = part ? (count + 1) / 2 : 0, f1 = share == 2 && !part ? (count + 1) / 2 : count;
       u64 mine[kList / kScanThreads];
       int place[kList / kScanThreads];
 #pragma unroll
-      for (int q = 0; q < kList / kScanThreads; ++q) {
-        const int e = q * kScanThreads + tid;
-        place[q] = K;
-        mine[q] = 0ull;
-        if (e >= count) continue;
-        mine[q] = s_list[e];
+      for (int z = 0; z < kList / kScanThreads; ++z) {
+        place[z] = K;
+        mine[z] = 0ull;
+        if (z * kScanThreads >= count) continue;  // uniform
+        const int e = z * kScanThreads + tid / share;
+        if (e < count) mine[z] = s_list[e];
         int above = 0;
-        for (int f = 0; f < count; ++f) above += s_list[f] > mine[q];
-        place[q] = above;
+#pragma unroll 4
+        for (int f = f0; f < f1; ++f) above += s_list[f] > mine[z];
+        if (share == 2) above += __shfl_xor_sync(0xffffffffu, above, 1);
+        if (mine[z]) place[z] = above;
       }
       __syncthreads();
 #pragma unroll
-      for (int q = 0; q < kList / kScanThreads; ++q)
-        if (place[q] < K) s_list[place[q]] = mine[q];
-      __syncthreads();
-      held = min(count, K);
-      if (held == K) bound = s_list[K - 1];
+      for (int z = 0; z < kList / kScanThreads; ++z)
+        if (place[z] < K) s_list[place[z]] = mine[z];
+    }
+    if (tid == 0) s_n = min(count, K);
+    __syncthreads();
+    if (count >= K) {
+      bound = s_list[K - 1];
+      floor_ = value_of(bound);
     }
   }
   if (bad) report(a.status, MK_ERR_NAN, PO_SELECT, row, chunk);
   u64* out = a.cand + ((long long)row * a.chunks + chunk) * K;
-  for (int b = tid; b < K; b += kScanThreads) out[b] = b < held ? s_list[b] : 0ull;
-  float M = m;
+  for (int b = tid; b < K; b += kScanThreads) out[b] = b < s_n ? s_list[b] : 0ull;
+  float top_ref = ref;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) s_f[warp] = M;
+  for (int o = 16; o > 0; o >>= 1) top_ref = fmaxf(top_ref, __shfl_xor_sync(0xffffffffu, top_ref, o));
+  if (lane == 0) s_f[warp] = top_ref;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kScanWarps; ++w) M = fmaxf(M, s_f[w]);
-  double d = 0.0;
-  if (m > -INFINITY) {
-    const float f = exp_of(m - M);
-    d = ((double)s + (double)comp) * (double)f;
+  for (int w = 0; w < kScanWarps; ++w) top_ref = fmaxf(top_ref, s_f[w]);
+  // the thread's sum as a whole number of units: exact sums from here on, in any order
+  u64 d = 0;
+  if (ref > -INFINITY) {
+    const float f = power_of(ref - top_ref), unit = power_of((float)a.sum_bits);
+    d = (u64)__float2ull_rn(s * f * unit) + (u64)__float2ll_rn(comp * f * unit);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-  if (lane == 0) s_d[warp] = d;
+  if (lane == 0) s_warp[warp] = d;
   __syncthreads();
   if (tid == 0) {
-    double sum = 0.0;
+    u64 all = 0;
 #pragma unroll
-    for (int w = 0; w < kScanWarps; ++w) sum += s_d[w];
-    a.stat[(long long)row * a.chunks + chunk] = make_float4(M, (float)sum, (float)(sum - (double)(float)sum), 0.f);
+    for (int w = 0; w < kScanWarps; ++w) all += s_warp[w];
+    a.stat[(long long)row * a.chunks + chunk] = Stat{top_ref, 0.f, all};
   }
+}
+
+// The warp's K largest of R keys per lane and of *best (lane q: the q-th largest so far), into
+// *best.  Keys differ, 0 is none.
+template <int R>
+__device__ __forceinline__ void take_best(u64 (&k)[8], int K, int lane, u64* best) {
+  u64 carry = *best, top = carry;  // the lane's largest, looked for again when it is taken
+#pragma unroll
+  for (int x = 0; x < R; ++x) top = k[x] > top ? k[x] : top;
+  u64 mine = 0ull;
+  for (int q = 0; q < K; ++q) {
+    const u64 win = warp_max(top);
+    if (win == 0ull) break;
+    if (lane == q) mine = win;
+    if (top == win) {
+      carry = carry == win ? 0ull : carry;
+      top = carry;
+#pragma unroll
+      for (int x = 0; x < R; ++x) {
+        k[x] = k[x] == win ? 0ull : k[x];
+        top = k[x] > top ? k[x] : top;
+      }
+    }
+  }
+  *best = mine;
 }
 
 // One CTA per group, a warp per beam: the beam's best from its parts' lists (8 keys per lane
 // in registers, the best so far carried from batch to batch), its lse, and its candidates'
-// scores in 64 bits, kept as ordered integers; then every candidate's place among the group's
-// is the sum over the beams of how many of that beam's sorted list are ahead of it.  Bound:
-// one chain of loads, 64-bit exp and log, and the list steps; nothing here grows with vocab.
+// scores as pairs of floats, compared as ordered integers; then every candidate's place among the group's
+// is the number of the other beams' candidates ahead of it.  Bound:
+// one chain of loads, the logarithm and the list steps, each instruction waiting for the last.
 __global__ void __launch_bounds__(32 * kMaxBeams) pick_kernel(const __grid_constant__ SelectArgs a) {
   __shared__ u64 s_key[kMaxBeams][kMaxBeams];
-  __shared__ double s_score[kMaxBeams][kMaxBeams];
+  __shared__ float s_score[kMaxBeams][kMaxBeams];
   __shared__ int s_token[kMaxBeams][kMaxBeams], s_len[kMaxBeams], s_ended[kMaxBeams];
   const int tid = threadIdx.x, lane = tid & 31, b = tid >> 5, group = blockIdx.x, K = a.beams;
   pdl_wait();
   pdl_launch();
   {
     const int row = group * K + b, total = a.chunks * K;
-    const float4* st = a.stat + (long long)row * a.chunks;
+    const Stat* st = a.stat + (long long)row * a.chunks;
     const u64* cand = a.cand + (long long)row * total;
-    // everything the beam needs is asked for at once
+    // everything the beam needs is asked for at once (of an ended one nothing was written,
+    // and nothing is used)
     const int ended = a.ended[row];
     float sc = a.scores[row];
-    float4 part = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    Stat part{-INFINITY, 0.f, 0ull};
     u64 k[8];
-    if (!ended) {
-      if (lane < a.chunks) part = st[lane];
+    if (lane < a.chunks) part = st[lane];
 #pragma unroll
-      for (int x = 0; x < 8; ++x) k[x] = x * 32 + lane < total ? cand[x * 32 + lane] : 0ull;
+    for (int x = 0; x < 8; ++x) k[x] = 0ull;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      if (x * 32 >= total) break;
+      if (x * 32 + lane < total) k[x] = cand[x * 32 + lane];
     }
-    if (!(sc == sc)) {
+    if (!(sc < INFINITY)) {
       if (lane == 0) report(a.status, MK_ERR_NAN, PO_SELECT, row, -1);
       sc = -INFINITY;
     }
@@ -294,91 +385,69 @@ __global__ void __launch_bounds__(32 * kMaxBeams) pick_kernel(const __grid_const
     }
     if (ended) {
       if (lane == 0) {
-        s_score[b][0] = (double)sc;
-        s_key[b][0] = ordered((double)sc);
+        s_score[b][0] = sc;
+        s_key[b][0] = ordered(Pair{sc, 0.f});
         s_token[b][0] = a.eos;
       }
     } else {
-      u64 mine = 0ull;  // lane q: the q-th best so far
-      for (int base = 0; base < total; base += 256) {
-        if (base) {
+      // the parts' sums against the largest power: whole numbers, shifted
+      float ref = part.n;
+      for (int c = lane + 32; c < a.chunks; c += 32) ref = fmaxf(ref, st[c].n);
 #pragma unroll
-          for (int x = 0; x < 8; ++x) k[x] = base + x * 32 + lane < total ? cand[base + x * 32 + lane] : 0ull;
-        }
-        const int rows = min(8, (total - base + 31) / 32);  // registers in use
-        u64 carry = mine;
-        for (int q = 0; q < K; ++q) {
-          u64 best = carry;
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            if (x < rows) best = k[x] > best ? k[x] : best;
-          const u64 win = warp_max(best);
-          if (win == 0ull) {
-            if (lane >= q) mine = 0ull;
-            break;
-          }
-          if (best == win) {  // one lane: the keys differ
-            if (carry == win) carry = 0ull;
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              if (k[x] == win) k[x] = 0ull;
-          }
-          if (lane == q) mine = win;
-        }
-      }
-      float m = part.x;
-      for (int c = lane + 32; c < a.chunks; c += 32) m = fmaxf(m, st[c].x);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      double sum = 0.0;
+      for (int o = 16; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
+      u64 sum = 0;
       for (int c = lane; c < a.chunks; c += 32) {
         if (c >= 32) part = st[c];
-        if (part.x > -INFINITY) sum += ((double)part.y + (double)part.z) * exp((double)part.x - (double)m);
+        if (part.n > ref - 64.f) sum += part.sum >> (int)(ref - part.n);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      const double lse = m > -INFINITY ? (double)m + log(sum) : 0.0;
+      const Pair lse = ref > -INFINITY ? ln_of(sum, ref - (float)a.sum_bits) : Pair{0.f, 0.f};
+      u64 mine = 0ull;  // lane q: the q-th best
+      if (total <= 32)
+        take_best<1>(k, K, lane, &mine);
+      else if (total <= 64)
+        take_best<2>(k, K, lane, &mine);
+      else
+        for (int base = 0; base < total; base += 256) {
+          if (base) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) k[x] = base + x * 32 + lane < total ? cand[base + x * 32 + lane] : 0ull;
+          }
+          take_best<8>(k, K, lane, &mine);
+        }
       if (lane < K) {
         const float v = value_of(mine);
-        double s = v > -INFINITY ? (double)sc + ((double)v - lse) : -INFINITY;
-        if (!(s == s)) s = -INFINITY;
-        s_score[b][lane] = s;
+        const Pair s = v > -INFINITY && sc > -INFINITY ? score_of(sc, v, lse) : Pair{-INFINITY, 0.f};
+        s_score[b][lane] = s.hi;
         s_key[b][lane] = ordered(s);
         s_token[b][lane] = token_of(mine);
       }
     }
   }
   __syncthreads();
-  for (int x = tid; x < K * K; x += 32 * K) {
-    const int b = x / K, e = x % K;
-    if (e >= s_len[b]) continue;
-    const u64 key = s_key[b][e];
-    int place = e;
-    for (int o = 0; o < K; ++o) {
-      if (o == b) continue;
-      // how many of beam o's, best first, are ahead: larger, or as large and of a lower beam
-      int lo = 0, hi = s_len[o];
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (s_key[o][mid] >= key + (o < b ? 0 : 1))
-          lo = mid + 1;
-        else
-          hi = mid;
-      }
-      place += lo;
-    }
-    if (place >= K) continue;
-    const int out = group * K + place, token = s_token[b][e];
-    a.out_tokens[out] = token;
-    a.out_parents[out] = group * K + b;
-    a.out_scores[out] = (float)s_score[b][e];
-    a.out_ended[out] = (s_ended[b] != 0 || token == a.eos) ? 1 : 0;
+  if (lane >= s_len[b]) return;
+  const u64 key = s_key[b][lane];
+  int place = lane;
+  for (int o = 0; o < K; ++o) {
+    if (o == b) continue;
+    // of beam o's, ahead are those larger, or as large and of a lower beam
+    const u64 least = key + (o < b ? 0 : 1);
+    const int len = s_len[o];
+#pragma unroll 4
+    for (int e = 0; e < len; ++e) place += s_key[o][e] >= least;
   }
+  if (place >= K) return;
+  const int out = group * K + place, token = s_token[b][lane];
+  a.out_tokens[out] = token;
+  a.out_parents[out] = group * K + b;
+  a.out_scores[out] = s_score[b][lane];
+  a.out_ended[out] = (s_ended[b] != 0 || token == a.eos) ? 1 : 0;
 }
 
 // Elements of a CTA's part of a row: the rows' parts fill the resident CTAs (4 per SM) once,
 // in whole groups of accesses (2048), and down to one group per CTA when there are few rows.
-constexpr int kPart = 8 * kScanThreads;
+constexpr int kPart = kPerSmall * kScanThreads;
 int chunk_of(long long rows, int vocab, int n_sm) {
   const long long parts = std::max(1LL, 4LL * n_sm / rows), each = ((long long)vocab + parts - 1) / parts;
   return (int)std::min((each + kPart - 1) / kPart * kPart, 1LL << 30);
@@ -388,13 +457,15 @@ size_t lay_out(SelectArgs* a, void* ws, long long rows, int beams, int chunks) {
   char* p = static_cast<char*>(ws);
   const size_t cand = round16(sizeof(u64) * rows * chunks * beams);
   a->cand = reinterpret_cast<u64*>(p);
-  a->stat = reinterpret_cast<float4*>(p + cand);
-  return cand + sizeof(float4) * rows * chunks;
+  a->stat = reinterpret_cast<Stat*>(p + cand);
+  return cand + sizeof(Stat) * rows * chunks;
 }
 
 template <typename T>
 mk_status launch_scan(const SelectArgs& a, bool vec, void* stream) {
-  auto k = vec ? scan_kernel<T, true> : scan_kernel<T, false>;
+  const bool small = a.chunk <= kPerSmall * kScanThreads;
+  auto k = small ? (vec ? scan_kernel<T, true, kPerSmall> : scan_kernel<T, false, kPerSmall>)
+                 : (vec ? scan_kernel<T, true, kPerLarge> : scan_kernel<T, false, kPerLarge>);
   return launch_dependent(k, dim3((unsigned)(a.rows * a.chunks)), dim3(kScanThreads), 0, stream, "mk_beam_select", a);
 }
 
@@ -447,6 +518,8 @@ extern "C" mk_status mk_beam_select(const mk_select_args* args, int32_t* status,
   a.chunk = chunk_of(a.rows, a.vocab, n_sm);
   a.chunks = (int)(((long long)a.vocab + a.chunk - 1) / a.chunk);
   a.eos = args->eos;
+  a.sum_bits = 62;  // a row's sum, at most vocab, stays below 2^63
+  while ((1LL << (62 - a.sum_bits)) < a.vocab) --a.sum_bits;
   lay_out(&a, args->workspace, a.rows, a.beams, a.chunks);
   const bool vec = aligned_to(args->logits, 16) && (args->row_stride * (long long)esz) % 16 == 0;
   s = args->dtype == MK_F32   ? launch_scan<float>(a, vec, stream)
