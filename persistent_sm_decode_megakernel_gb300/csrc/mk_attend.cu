@@ -35,7 +35,7 @@ struct AttendArgs {
   int n_rows, hq, hkv, group, len_add, window, page_size, n_pages, table_rows, width;
   int tpp;                              // tiles per page
   unsigned tpp_inverse;                 // 2^32 / tpp, rounded up
-  int n_cta, min_share;
+  int n_cta;
   int by_segment;                       // joins[row * hkv + kv head] (they fit), else joins[first CTA]
   float scale, softcap;                 // scores to units of log 2: scale s, or softcap tanh(scale s)
 };
@@ -63,53 +63,81 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int r, bool tell) {
   return s;
 }
 
-// Of the rows' tiles, times hkv: returns the total; the thread whose rows hold unit `at` leaves
-// that row and the units before it in *row and *before (shared memory; the caller syncs).
-__device__ __forceinline__ long long share_of(const AttendArgs& a, long long units);
-__device__ __forceinline__ long long find_row(const AttendArgs& a, long long* sums, int* row, long long* before) {
+// The line of work, in units: every segment counts its tiles and `lead` units in front of them
+// for what a piece costs besides its tiles (the query, the table, the merge).  CTA c takes
+// [c share, (c + 1) share).  Of what a CTA takes, a segment's lead is where it begins: the
+// segment's first tiles are of the CTA that holds their units, whoever holds the lead.
+//   lead: with fewer tiles than the wave's warps the latency of a piece is all there is, and
+//     equal tiles are best; else kLead, without which a CTA that meets a dozen segments of two
+//     tiles each ran twice as long as the others (61 ragged rows of up to 700 positions).
+constexpr int kLead = 8;
+struct Line {
+  long long units, share;
+  int lead;
+};
+__device__ __forceinline__ long long row_units(const AttendArgs& a, int n, int lead) {
+  return n > 0 ? (long long)(n + lead) * a.hkv : 0LL;
+}
+// The line, and in *row and *before (shared memory; the caller syncs) the row that holds this
+// CTA's first unit and the units before it.
+__device__ __forceinline__ Line find_row(const AttendArgs& a, long long (*sums)[2], int* row, long long* before) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.n_rows + kAttThreads - 1) / kAttThreads;
   const int r0 = min(a.n_rows, tid * per), r1 = min(a.n_rows, r0 + per);
-  long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += span_of(a, r, blockIdx.x == 0).n;
-  long long inc = mine;
+  long long tiles = 0;
+  int rows = 0;  // with positions
+  for (int r = r0; r < r1; ++r) {
+    const int n = span_of(a, r, blockIdx.x == 0).n;
+    tiles += n;
+    rows += n > 0;
+  }
+  long long ti = tiles;
+  int ri = rows;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += x;
+    const long long x = __shfl_up_sync(0xffffffffu, ti, o);
+    const int y = __shfl_up_sync(0xffffffffu, ri, o);
+    if (lane >= o) {
+      ti += x;
+      ri += y;
+    }
   }
-  if (lane == 31) sums[warp] = inc;
+  if (lane == 31) {
+    sums[warp][0] = ti;
+    sums[warp][1] = ri;
+  }
   __syncthreads();
-  long long base = 0, total = 0;
+  long long all_tiles = 0, all_rows = 0;
 #pragma unroll
   for (int w = 0; w < kAttWarps; ++w) {
-    if (w < warp) base += sums[w];
-    total += sums[w];
+    if (w == warp) {
+      ti += all_tiles - tiles;  // before this thread's rows
+      ri += (int)all_rows - rows;
+    }
+    all_tiles += sums[w][0];
+    all_rows += sums[w][1];
   }
-  total *= a.hkv;
-  const long long at = share_of(a, total) * blockIdx.x;
-  long long b = (base + inc - mine) * a.hkv;
-  if (at >= b && at < b + mine * a.hkv)
+  Line l;
+  l.lead = all_tiles * a.hkv <= (long long)a.n_cta * kAttWarps ? 0 : kLead;
+  l.units = (all_tiles + all_rows * l.lead) * a.hkv;
+  l.share = max((long long)kAttWarps, (l.units + a.n_cta - 1) / a.n_cta);
+  const long long at = l.share * blockIdx.x;
+  long long b = (ti + (long long)ri * l.lead) * a.hkv;
+  if (at >= b && at < b + (tiles + (long long)rows * l.lead) * a.hkv)
     for (int r = r0; r < r1; ++r) {
-      const long long n = (per == 1 ? mine : (long long)span_of(a, r, false).n) * a.hkv;
+      const long long n = row_units(a, per == 1 ? (int)tiles : span_of(a, r, false).n, l.lead);
       if (at >= b && at < b + n) {
         *row = r;
         *before = b;
       }
       b += n;
     }
-  return total;
+  return l;
 }
 
 // the page a tile lies in: t / tpp by a multiplication (exact for t <= 2^26, tpp <= 64)
 __device__ __forceinline__ int page_index(const AttendArgs& a, int t) {
   return a.tpp == 1 ? t : (int)__umulhi((unsigned)t, a.tpp_inverse);
-}
-
-// units (tiles of one kv head) a CTA takes: equal shares of one wave, but no fewer than
-// min_share, so that a short call is not cut into pieces whose join costs more than they save
-__device__ __forceinline__ long long share_of(const AttendArgs& a, long long units) {
-  return max((long long)a.min_share, (units + a.n_cta - 1) / a.n_cta);
 }
 
 template <typename T>
@@ -161,8 +189,8 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
 // (WIDE: [part][chunk][2 row halves][32 lanes]), then the warps' partials for the CTA's merge.
 struct AttState {
   long long at, end, share, before;  // next unit, end of the CTA's units, share; units before `row`
-  long long sums[kAttWarps];
-  int row, head, slot, bad, bad_page;
+  long long sums[kAttWarps][2];
+  int row, head, slot, lead, bad, bad_page;
 };
 template <int HD, bool WIDE, int NQ>
 struct AttSmem {
@@ -204,8 +232,7 @@ __global__ void __launch_bounds__(kAttThreads, kCtasPerSm) attend_kernel(const _
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   pdl_wait();
   pdl_launch();
-  const long long units = find_row(a, st->sums, &st->row, &st->before);
-  const long long share = share_of(a, units);
+  const Line line = find_row(a, st->sums, &st->row, &st->before);
   // rows without positions: zeros
   for (int r = blockIdx.x; r < a.n_rows; r += gridDim.x) {
     if (span_of(a, r, false).n != 0) continue;
@@ -217,14 +244,15 @@ __global__ void __launch_bounds__(kAttThreads, kCtasPerSm) attend_kernel(const _
     }
   }
   if (tid == 0 && !a.by_segment) a.joins[blockIdx.x] = make_int4(0, -1, 0, 0);
-  if (share * blockIdx.x >= units) return;
+  if (line.share * blockIdx.x >= line.units) return;
   __syncthreads();
   // what a piece needs again at its end lives in shared memory: the loop over the tiles has
   // few registers to spare
   if (tid == 0) {
-    st->at = share * blockIdx.x;
-    st->end = min(units, share * (blockIdx.x + 1LL));
-    st->share = share;
+    st->at = line.share * blockIdx.x;
+    st->end = min(line.units, line.share * (blockIdx.x + 1LL));
+    st->share = line.share;
+    st->lead = line.lead;
     st->bad = 0;
   }
   __syncthreads();
@@ -232,33 +260,42 @@ __global__ void __launch_bounds__(kAttThreads, kCtasPerSm) attend_kernel(const _
     int base, cnt, mine, lo, hi;  // this warp's tiles: base, + kAttWarps, ...
     const int32_t* trow;
     {
-      long long rbase = st->before, in_row;
-      int r = st->row;
+      long long rbase = st->before, at = st->at, seg;  // seg: the segment's first unit
+      int r = st->row, j, first;
       Span sp;
       while (true) {
         sp = span_of(a, r, false);
-        in_row = st->at - rbase;
-        if (in_row < (long long)sp.n * a.hkv) break;  // rows without positions have no units
-        rbase += (long long)sp.n * a.hkv;
-        ++r;
+        const long long n = row_units(a, sp.n, st->lead);
+        if (at < rbase + n) {
+          const int each = sp.n + st->lead;
+          j = (int)((at - rbase) / each);
+          seg = rbase + (long long)j * each;
+          const long long stop = min(st->end, seg + each);
+          first = (int)max(0LL, at - seg - st->lead);
+          cnt = (int)(stop - seg - st->lead) - first;  // tiles of this piece
+          at = stop;
+          if (cnt > 0 || at >= st->end) break;  // (no tiles: of a segment's lead alone)
+        } else {
+          rbase += n;
+          ++r;
+        }
       }
-      const int j = (int)(in_row / sp.n), first = (int)(in_row - (long long)j * sp.n);
-      cnt = (int)min((long long)(sp.n - first), st->end - st->at);  // tiles of this piece
       __syncthreads();  // the state is read
+      if (cnt <= 0) return;
       if (tid == 0) {
-        const bool whole = first == 0 && cnt == sp.n;
+        const bool whole = cnt == sp.n;
         st->row = r;
         st->before = rbase;
         st->head = j;
         st->slot = whole ? 2 : first == 0;  // 0: continues a segment, 1: begins one, 2: is one
         if (first == 0) {  // the segment's begin knows where it ends
-          const int last = (int)((st->at + sp.n - 1) / st->share);
+          const int last = (int)((seg + st->lead + sp.n - 1) / st->share);
           if (a.by_segment)
             a.joins[r * a.hkv + j] = whole ? make_int4(0, -1, 0, 0) : make_int4(blockIdx.x, last, r, j);
           else if (!whole)
             a.joins[blockIdx.x] = make_int4(blockIdx.x, last, r, j);
         }
-        st->at += cnt;
+        st->at = at;
       }
       base = sp.t0 + first + warp;
       mine = cnt > warp ? (cnt - warp + kAttWarps - 1) / kAttWarps : 0;
@@ -703,7 +740,6 @@ extern "C" mk_status mk_paged_attention(const mk_attend_args* args, const mk_pag
   a.n_cta = n_sm * kCtasPerSm;
   a.part = reinterpret_cast<float*>(a.joins + a.n_cta);
   a.by_segment = (long long)a.n_rows * a.hkv <= a.n_cta;
-  a.min_share = kAttWarps;
   a.scale = args->softcap > 0.f ? args->scale / args->softcap : args->scale * kLog2e;
   a.softcap = args->softcap * kLog2e;
   // 16-bit queries of the cache's type are exact in one part.  Other queries are split into

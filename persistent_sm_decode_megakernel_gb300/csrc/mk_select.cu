@@ -110,8 +110,7 @@ __device__ __forceinline__ u64 ordered(Pair p) { return (u64)orderable(p.hi + 0.
 
 // A CTA reads its part of a row once, kIter elements at a time with the next ones in flight.
 // The `beams` largest are kept in a list in shared memory, entered by what lies above a bound.
-// The first bound comes from the lanes: the beams-th largest of a warp's 32 lane maxima has
-// at least `beams` elements at or above it.  From then on it is the list's beams-th key: the
+// The first bound comes from the lanes' maxima.  From then on it is the list's beams-th key: the
 // list is cut down to its best after steps 1, 2, 4, 8, .., each entry counting how many are
 // above it, which is its place; of a part in random order about `beams` keys enter between
 // two of those.  Should the list overflow (rising logits), the part is read again, once per
@@ -153,8 +152,8 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_cons
   float x[PER], next[PER];
   load(0, next);
   const int steps = (n + kIter - 1) / kIter;
-  u64 bound = 0ull;            // keys above it enter
-  float floor_ = -INFINITY;    // its value
+  u64 bound = 0ull;            // keys above it enter, if their logit is not below
+  float floor_ = -INFINITY;    // this
   bool bad = false;
   float ref = -INFINITY, s = 0.f, comp = 0.f;  // (s + comp) 2^ref: the thread's sum of e^x
   for (int it = 0; it < steps; ++it) {
@@ -201,22 +200,20 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_cons
     comp += (s - (sum - r)) + (q - r);
     s = sum;
     if (it == 0) {
-      // the lane's own largest key: the first element that reaches top (none in an empty tail)
-      int best = -1;
-#pragma unroll
-      for (int i = PER - 1; i >= 0; --i)
-        if (x[i] == top && at(0, i) < n) best = at(0, i);
-      u64 left = best >= 0 ? key_of(top, first + best) : 0ull, kth = 0ull;
-      for (int b = 0; b < K; ++b) {
-        kth = warp_max(left);
-        if (kth == 0ull) break;  // fewer lanes with elements than beams: no bound from this warp
-        if (left == kth) left = 0ull;
+      // a warp's r-th largest lane maximum, r = beams / 8 rounded up: the least of the warps'
+      // has at least `beams` elements at or above it (a warp with fewer lanes sets no bound)
+      float left = at(0, 0) < n ? top : -INFINITY, kth = -INFINITY;
+      for (int b = 0; b < (K + kScanWarps - 1) / kScanWarps; ++b) {
+        const uint32_t u = __reduce_max_sync(0xffffffffu, orderable(left));
+        kth = value_of((u64)u << 32);
+        const unsigned who = __ballot_sync(0xffffffffu, orderable(left) == u);
+        if (lane == __ffs(who) - 1) left = -INFINITY;
       }
-      if (lane == 0) s_warp[warp] = kth;
+      if (lane == 0) s_f[warp] = kth;
       __syncthreads();
+      floor_ = s_f[0];
 #pragma unroll
-      for (int w = 0; w < kScanWarps; ++w) bound = s_warp[w] > bound ? s_warp[w] : bound;
-      if (bound) floor_ = value_of(bound--);  // that key itself enters
+      for (int w = 1; w < kScanWarps; ++w) floor_ = fminf(floor_, s_f[w]);
     }
     if (top >= floor_) {
       unsigned hits = 0;
@@ -368,12 +365,11 @@ __global__ void __launch_bounds__(32 * kMaxBeams) pick_kernel(const __grid_const
     Stat part{-INFINITY, 0.f, 0ull};
     u64 k[8];
     if (lane < a.chunks) part = st[lane];
+    k[0] = lane < total ? cand[lane] : 0ull;
+    k[1] = 32 + lane < total ? cand[32 + lane] : 0ull;
+    if (total > 64) {
 #pragma unroll
-    for (int x = 0; x < 8; ++x) k[x] = 0ull;
-#pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      if (x * 32 >= total) break;
-      if (x * 32 + lane < total) k[x] = cand[x * 32 + lane];
+      for (int x = 2; x < 8; ++x) k[x] = x * 32 + lane < total ? cand[x * 32 + lane] : 0ull;
     }
     if (!(sc < INFINITY)) {
       if (lane == 0) report(a.status, MK_ERR_NAN, PO_SELECT, row, -1);
@@ -393,8 +389,7 @@ __global__ void __launch_bounds__(32 * kMaxBeams) pick_kernel(const __grid_const
       // the parts' sums against the largest power: whole numbers, shifted
       float ref = part.n;
       for (int c = lane + 32; c < a.chunks; c += 32) ref = fmaxf(ref, st[c].n);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
+      ref = value_of((u64)__reduce_max_sync(0xffffffffu, orderable(ref)) << 32);
       u64 sum = 0;
       for (int c = lane; c < a.chunks; c += 32) {
         if (c >= 32) part = st[c];
