@@ -7,7 +7,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <c10/core/TensorImpl.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -99,6 +99,31 @@ void* stream_of(at::Device dev) { return c10::cuda::getCurrentCUDAStream(dev.ind
 struct Workspace {
   c10::DataPtr p;
   explicit Workspace(size_t bytes) : p(c10::cuda::CUDACachingAllocator::get()->allocate(bytes)) {}
+};
+
+// New contiguous tensors of one allocation, without the dispatcher's part of at::empty
+struct Fresh {
+  c10::Storage storage;
+  at::Device dev;
+  int64_t at = 0;
+  Fresh(int64_t bytes, at::Device d) : dev(d) {
+    c10::Allocator* a = c10::cuda::CUDACachingAllocator::get();
+    storage = c10::Storage(c10::Storage::use_byte_size_t(), bytes, a->allocate(bytes), a, /*resizable=*/false);
+  }
+  at::Tensor take(at::IntArrayRef sizes, at::ScalarType type) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(storage), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                            c10::scalarTypeToTypeMeta(type));
+    const int64_t e = (int64_t)t.dtype().itemsize();
+    t.unsafeGetTensorImpl()->set_storage_offset(at / e);
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+    at += t.numel() * e;
+    return t;
+  }
+  static at::Tensor one(at::IntArrayRef sizes, at::ScalarType type, at::Device d) {
+    int64_t n = (int64_t)c10::elementSize(type);
+    for (int64_t s : sizes) n *= s;
+    return Fresh(n, d).take(sizes, type);
+  }
 };
 
 void table_of(PyObject* o, at::Device dev, int32_t** p, int* rows, int* width, long long* stride) {
@@ -196,7 +221,7 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
       const at::Tensor& q = tensor(a[0], "q");
       need(q.dim() == 3, "q must be [tokens, heads, head_dim]");
       heads_of(q, "q", n, q.size(1), view.head_dim, k.scalar_type(), dev, &x.q_token, &x.q_head);
-      out = a[11] == Py_None ? at::empty(q.sizes(), q.options()) : tensor(a[11], "q_out");
+      out = a[11] == Py_None ? Fresh::one(q.sizes(), q.scalar_type(), dev) : tensor(a[11], "q_out");
       heads_of(out, "q_out", n, q.size(1), view.head_dim, k.scalar_type(), dev, &x.o_token, &x.o_head);
       x.n_heads = size32(q.size(1), "heads");
       x.q = q.data_ptr();
@@ -233,7 +258,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const int64_t n = q.size(0), hq = q.size(1);
     heads_of(q, "q", n, hq, view.head_dim, q.scalar_type(), dev, &x.q_row, &x.q_head);
     const c10::cuda::CUDAGuard guard(dev);
-    const at::Tensor out = a[10] == Py_None ? at::empty(q.sizes(), q.options()) : tensor(a[10], "out");
+    const at::Tensor out = a[10] == Py_None ? Fresh::one(q.sizes(), q.scalar_type(), dev) : tensor(a[10], "out");
     heads_of(out, "out", n, hq, view.head_dim, q.scalar_type(), dev, &x.o_row, &x.o_head);
     x.q = q.data_ptr();
     x.out = out.data_ptr();
@@ -248,7 +273,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const int with_lse = PyObject_IsTrue(a[11]);
     at::Tensor lse;
     if (with_lse > 0) {
-      lse = at::empty({n, hq}, q.options().dtype(at::kFloat));
+      lse = Fresh::one({n, hq}, at::kFloat, dev);
       x.lse = lse.data_ptr<float>();
     }
     int32_t* status = status_of(a[12], dev);
@@ -348,9 +373,9 @@ PyObject* beam_select(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     check(mk_beam_select_workspace(x.groups, x.beams, x.vocab, &x.workspace_bytes), "mk_beam_select_workspace");
     const Workspace ws(x.workspace_bytes);
     x.workspace = ws.p.get();
-    const at::TensorOptions ints = scores.options().dtype(at::kInt);
-    const at::Tensor token = at::empty({groups, beams}, ints), parent = at::empty({groups, beams}, ints),
-                     done = at::empty({groups, beams}, ints), best = at::empty({groups, beams}, scores.options());
+    Fresh fresh(4 * 4 * groups * beams, dev);  // the four results share one allocation
+    const at::Tensor token = fresh.take({groups, beams}, at::kInt), parent = fresh.take({groups, beams}, at::kInt),
+                     done = fresh.take({groups, beams}, at::kInt), best = fresh.take({groups, beams}, at::kFloat);
     x.out_tokens = token.data_ptr<int32_t>();
     x.out_parents = parent.data_ptr<int32_t>();
     x.out_ended = done.data_ptr<int32_t>();
