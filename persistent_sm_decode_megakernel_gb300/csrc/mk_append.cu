@@ -45,8 +45,7 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 constexpr int kMaxFreqs = 64;  // head_dim / 2 at most
-constexpr int kMaxTokens = 8;  // of a CTA
-constexpr int kCtasPerSm = 4;
+constexpr int kCtasPerSm = 3, kWarpsPerSm = kCtasPerSm * kAppendThreads / 32;
 
 struct AppendArgs {
   const void *q, *k, *v;
@@ -55,118 +54,138 @@ struct AppendArgs {
   const int32_t *positions, *rows, *table;
   const double* freqs;
   int32_t* status;
-  int n_tokens, per_cta, hq, hkv, page_size, n_pages, n_rows, width, n_freqs;
+  int n_tokens, share, hq, hkv, page_size, n_pages, n_rows, width, n_freqs;
   float mscale;
 };
 
-// The angle position * freq is taken in 64 bits in units of pi and reduced there to [-1, 1]
-// before sine and cosine, which is what keeps far positions exact (at position 10^6 a 32-bit
-// product would be off by 0.06 rad); once per pair and token, shared by all heads through
-// shared memory, 64-bit arithmetic costs nothing beside the vectors' traffic.
+// The angle position * freq is taken in turns, as a whole number of 2^-64: the frequency's
+// mantissa times 1 / (2 pi) to 64 bits, shifted, times the position; whole turns fall off the
+// top, what is left is good to 2^-33 of a turn at any position and goes to sine and cosine in
+// units of pi.  A 32-bit product would be off by 0.06 rad at position 10^6, and 64-bit floating
+// point has so little throughput here that it alone cost 8 of 42 us of a long prompt.
 __device__ __forceinline__ void turn_of(const AppendArgs& a, int pos, int i, float* c, float* s) {
-  const double turns = (double)pos * (a.freqs[i] * 0.31830988618379067154);  // angle / pi
-  sincospif((float)(turns - 2.0 * rint(turns * 0.5)), s, c);
+  const unsigned long long bits = (unsigned long long)__double_as_longlong(a.freqs[i]);
+  const int exponent = (int)(bits >> 52 & 2047) - 1023;               // freq = m 2^(exponent - 52)
+  const unsigned long long m = (bits & 0xFFFFFFFFFFFFFull) | 1ull << 52;
+  constexpr unsigned long long kInv = 0xa2f9836e4e441529ull;                // 2^66 / (2 pi)
+  const unsigned long long hi = __umul64hi(m, kInv), lo = m * kInv;
+  const int shift = 54 - exponent;                                     // freq 2^64 / (2 pi) = (hi, lo) 2^-shift
+  unsigned long long turns = 0;                                        // (frequencies of 2^54 and more: none)
+  if (shift >= 64 && shift < 128)
+    turns = hi >> (shift - 64);
+  else if (shift > 0 && shift < 64)
+    turns = hi << (64 - shift) | lo >> shift;
+  turns *= (unsigned long long)pos;
+  if (bits >> 63) turns = 0ull - turns;
+  sincospif((float)(int)(turns >> 32) * 0x1p-31f, s, c);
   *c *= a.mscale;
   *s *= a.mscale;
 }
 
 // where a token goes: the page and the row of it (page -1: nowhere)
-__device__ __forceinline__ int2 place_of(const AppendArgs& a, int t, int pos) {
+__device__ __forceinline__ int2 place_of(const AppendArgs& a, int t, int pos, bool tell) {
   const int row = a.rows ? a.rows[t] : t, slot = pos / a.page_size;
   int page = -1;
   if ((unsigned)row < (unsigned)a.n_rows && slot < a.width) page = a.table[(long long)row * a.table_stride + slot];
   if ((unsigned)page >= (unsigned)a.n_pages) {
-    report(a.status, MK_ERR_PAGES, PO_APPEND, row, pos);
+    if (tell) report(a.status, MK_ERR_PAGES, PO_APPEND, row, pos);
     page = -1;
   }
   return make_int2(page, pos - slot * a.page_size);
 }
 
-// A CTA takes `per_cta` tokens.  A head is cut into items of 16 elements, one per lane: in the
-// half layout item c < n_freqs / 8 holds elements [8c, 8c + 8) and their partners
-// [n_freqs + 8c, ..), so that a rotation stays in one lane, and the others 16 consecutive
-// ones; interleaved, every item is 16 consecutive elements.  A warp takes 32 items (4 heads
-// of 128 dims, 8 of 64) of a token at a time, queries first, then keys, then values; the
-// vectors of its next turn are in flight while it works, the first ones while the CTA looks
-// up its tokens' places and angles.  Bound: the vectors' bytes, read and written once; for a
-// few tokens the chain of loads from the position over the table to the store.
+// A token is taken by 2^share warps, no warp waiting for another.  A head is cut into items of 16
+// elements, one per lane: in the half layout item c < n_freqs / 8 holds elements [8c, 8c + 8) and
+// their partners [n_freqs + 8c, ..), so that a rotation stays in one lane, and the others 16
+// consecutive ones; interleaved, every item is 16 consecutive elements.  A lane has the same
+// item of every head it takes (4 heads of 128 dims per turn of the warp, 8 of 64: queries
+// first, then keys, then values), so its cosines and sines stay in registers.  The vectors of
+// the next turns are in flight while it works, the first ones while the warp looks up its
+// token's place and angles.  Bound: the vectors' bytes, read and written once; for a few tokens
+// the chain of loads from the position over the table to the store.
 template <typename T, typename C, int HD, bool INTER>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs a) {
-  constexpr int ITEMS = HD / 16, HPW = 32 / ITEMS, WARPS = kAppendThreads / 32;
-  __shared__ __align__(16) float s_cos[kMaxTokens][kMaxFreqs], s_sin[kMaxTokens][kMaxFreqs];
-  __shared__ int2 s_place[kMaxTokens];
-  __shared__ int s_pos[kMaxTokens];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane % ITEMS;
+__global__ void __launch_bounds__(kAppendThreads, kCtasPerSm) append_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int ITEMS = HD / 16, HPW = 32 / ITEMS, WARPS = kAppendThreads / 32, U = 2;
+  __shared__ __align__(16) float s_turn[WARPS][2][kMaxFreqs];  // cosines and sines of a warp's token
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane % ITEMS;
   pdl_wait();
   pdl_launch();
-  const int t0 = blockIdx.x * a.per_cta, nt = min(a.per_cta, a.n_tokens - t0);
-  const int heads = a.hq + 2 * a.hkv, blocks = (heads + HPW - 1) / HPW, jobs = nt * blocks;
+  const int unit = blockIdx.x * WARPS + warp, t = unit >> a.share, parts = 1 << a.share;
+  if (t >= a.n_tokens) return;
+  const int heads = a.hq + 2 * a.hkv, first = (unit & (parts - 1)) * HPW + lane / ITEMS, step = parts * HPW;
   const bool turned = c < a.n_freqs / 8;
   const int e0 = !INTER && turned ? 8 * c : 16 * c, e1 = !INTER && turned ? a.n_freqs + 8 * c : 16 * c + 8;
-  Raw8<T> rx, ry;
-  auto load = [&](int job) {
-    const int i = job / blocks, t = t0 + i, h = (job - i * blocks) * HPW + lane / ITEMS;
+  const int qh = (int)a.q_h, kh = (int)a.k_h, vh = (int)a.v_h, oh = (int)a.o_h, hk = a.hq + a.hkv;
+  const T* qs = static_cast<const T*>(a.q) + t * a.q_t + e0;
+  const T* ks = static_cast<const T*>(a.k) + t * a.k_t - a.hq * a.k_h + e0;
+  const T* vs = static_cast<const T*>(a.v) + t * a.v_t - hk * a.v_h + e0;
+  Raw8<T> rx[U], ry[U];
+  auto load = [&](int u, int h) {
     if (h >= heads) return;
-    const T* src = h < a.hq           ? static_cast<const T*>(a.q) + t * a.q_t + h * a.q_h
-                   : h < a.hq + a.hkv ? static_cast<const T*>(a.k) + t * a.k_t + (h - a.hq) * a.k_h
-                                      : static_cast<const T*>(a.v) + t * a.v_t + (h - a.hq - a.hkv) * a.v_h;
-    rx.load(src + e0);
-    ry.load(src + e1);
+    const T* base = h < a.hq ? qs : h < hk ? ks : vs;
+    const int each = h < a.hq ? qh : h < hk ? kh : vh;
+    const T* src = base + (long long)h * each;
+    rx[u].load(src);
+    ry[u].load(src + (e1 - e0));
   };
-  if (warp < jobs) load(warp);
-  for (int i = tid; i < nt; i += kAppendThreads) {
-    const int pos = a.positions[t0 + i];
-    s_pos[i] = pos;
-    s_place[i] = pos >= 0 ? place_of(a, t0 + i, pos) : make_int2(-1, 0);
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(u, first + u * step);
+  const int pos = a.positions[t];
+  if (pos < 0) return;
+  int2 place = make_int2(0, 0);
+  if (lane == 0) place = place_of(a, t, pos, (unit & (parts - 1)) == 0);
+  for (int f = lane; f < a.n_freqs; f += 32) turn_of(a, pos, f, &s_turn[warp][0][f], &s_turn[warp][1][f]);
+  place.x = __shfl_sync(0xffffffffu, place.x, 0);
+  place.y = __shfl_sync(0xffffffffu, place.y, 0);
+  __syncwarp();
+  float cs[8], sn[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    cs[j] = turned ? s_turn[warp][0][8 * c + j] : 1.f;
+    sn[j] = turned ? s_turn[warp][1][8 * c + j] : 0.f;
   }
-  for (int x = tid; x < nt * kMaxFreqs; x += kAppendThreads) {
-    const int i = x / kMaxFreqs, f = x % kMaxFreqs;
-    if (f < a.n_freqs) turn_of(a, a.positions[t0 + i], f, &s_cos[i][f], &s_sin[i][f]);
-  }
-  __syncthreads();
-  for (int job = warp; job < jobs; job += WARPS) {
-    const int i = job / blocks, t = t0 + i, h = (job - i * blocks) * HPW + lane / ITEMS;
-    float x[8], y[8];
-    rx.up(x);
-    ry.up(y);
-    if (job + WARPS < jobs) load(job + WARPS);
-    const int2 place = s_place[i];
-    const bool is_q = h < a.hq, is_v = h >= a.hq + a.hkv;
-    if (h >= heads || s_pos[i] < 0 || (!is_q && place.x < 0)) continue;
-    if (turned && !is_v) {
-      float cs[8], sn[8];
+  T* qd = static_cast<T*>(a.qo) + t * a.o_t + e0;
+  const long long row = (long long)place.x * a.page_stride + (long long)place.y * HD + e0;
+  const int head = a.page_size * HD;
+  C* kd = static_cast<C*>(a.kc) + row - (long long)a.hq * head;
+  C* vd = static_cast<C*>(a.vc) + row - (long long)hk * head;
+  for (int h0 = first; h0 - lane / ITEMS < heads; h0 += U * step) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        *reinterpret_cast<float4*>(cs + 4 * q) = *reinterpret_cast<const float4*>(&s_cos[i][8 * c + 4 * q]);
-        *reinterpret_cast<float4*>(sn + 4 * q) = *reinterpret_cast<const float4*>(&s_sin[i][8 * c + 4 * q]);
-      }
-      if (INTER) {
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * step;
+      if (h >= heads) break;
+      float x[8], y[8];
+      rx[u].up(x);
+      ry[u].up(y);
+      load(u, h + U * step);
+      if (turned && h < hk) {
+        if (INTER) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float xa = x[2 * j], ya = y[2 * j];
-          x[2 * j] = xa * cs[j] - x[2 * j + 1] * sn[j];
-          x[2 * j + 1] = x[2 * j + 1] * cs[j] + xa * sn[j];
-          y[2 * j] = ya * cs[4 + j] - y[2 * j + 1] * sn[4 + j];
-          y[2 * j + 1] = y[2 * j + 1] * cs[4 + j] + ya * sn[4 + j];
-        }
-      } else {
+          for (int j = 0; j < 4; ++j) {
+            const float xa = x[2 * j], ya = y[2 * j];
+            x[2 * j] = xa * cs[j] - x[2 * j + 1] * sn[j];
+            x[2 * j + 1] = x[2 * j + 1] * cs[j] + xa * sn[j];
+            y[2 * j] = ya * cs[4 + j] - y[2 * j + 1] * sn[4 + j];
+            y[2 * j + 1] = y[2 * j + 1] * cs[4 + j] + ya * sn[4 + j];
+          }
+        } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float xa = x[j];
-          x[j] = xa * cs[j] - y[j] * sn[j];
-          y[j] = y[j] * cs[j] + xa * sn[j];
+          for (int j = 0; j < 8; ++j) {
+            const float xa = x[j];
+            x[j] = xa * cs[j] - y[j] * sn[j];
+            y[j] = y[j] * cs[j] + xa * sn[j];
+          }
         }
       }
-    }
-    if (is_q) {
-      T* dst = static_cast<T*>(a.qo) + t * a.o_t + h * a.o_h;
-      store8<T>(dst + e0, x);
-      store8<T>(dst + e1, y);
-    } else {
-      C* dst = static_cast<C*>(is_v ? a.vc : a.kc) + (long long)place.x * a.page_stride +
-               ((long long)(is_v ? h - a.hq - a.hkv : h - a.hq) * a.page_size + place.y) * HD;
-      store8<C>(dst + e0, x);
-      store8<C>(dst + e1, y);
+      if (h < a.hq) {
+        T* dst = qd + (long long)h * oh;
+        store8<T>(dst, x);
+        store8<T>(dst + (e1 - e0), y);
+      } else if (place.x >= 0) {
+        C* dst = (h < hk ? kd : vd) + (long long)h * head;
+        store8<C>(dst, x);
+        store8<C>(dst + (e1 - e0), y);
+      }
     }
   }
 }
@@ -181,7 +200,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_pairs_kernel(const __gr
   pdl_launch();
   const int t = blockIdx.x, tid = threadIdx.x, pos = a.positions[t];
   if (pos < 0) return;
-  if (tid == 0) s_place = place_of(a, t, pos);
+  if (tid == 0) s_place = place_of(a, t, pos, true);
   if (tid < a.n_freqs) turn_of(a, pos, tid, &s_cos[tid], &s_sin[tid]);
   __syncthreads();
   const int2 place = s_place;
@@ -219,10 +238,15 @@ mk_status launch_append(AppendArgs a, int n_sm, bool inter, bool vec, void* stre
   if (!vec)
     return launch_dependent(inter ? append_pairs_kernel<T, C, HD, true> : append_pairs_kernel<T, C, HD, false>,
                             dim3(a.n_tokens), dim3(kAppendThreads), 0, stream, what, a);
-  // a token per CTA while that leaves SMs free, then up to kMaxTokens, which spread the look-up
-  a.per_cta = std::min(kMaxTokens, std::max(1, a.n_tokens / (kCtasPerSm * n_sm)));
-  return launch_dependent(inter ? append_kernel<T, C, HD, true> : append_kernel<T, C, HD, false>,
-                          dim3((a.n_tokens + a.per_cta - 1) / a.per_cta), dim3(kAppendThreads), 0, stream, what, a);
+  // a warp takes at least four turns of a token, or down to one while warps are free
+  constexpr int WARPS = kAppendThreads / 32, HPW = 512 / HD;
+  const int turns = (a.hq + 2 * a.hkv + HPW - 1) / HPW;
+  while ((8LL << a.share) <= turns ||
+         ((2LL << a.share) <= turns && ((long long)a.n_tokens << (a.share + 1)) <= (long long)kWarpsPerSm * n_sm))
+    ++a.share;
+  const long long ctas = (((long long)a.n_tokens << a.share) + WARPS - 1) / WARPS;
+  return launch_dependent(inter ? append_kernel<T, C, HD, true> : append_kernel<T, C, HD, false>, dim3((unsigned)ctas),
+                          dim3(kAppendThreads), 0, stream, what, a);
 }
 template <typename T>
 mk_status launch_append(const AppendArgs& a, int n_sm, int cache_dtype, int hd, bool inter, bool vec, void* stream) {
@@ -266,8 +290,9 @@ extern "C" mk_status mk_rope_append(const mk_append_args* args, const mk_page_vi
   a.n_tokens = args->n_tokens; a.hq = args->q ? args->n_heads : 0;
   a.hkv = cache->n_kv_heads; a.page_size = cache->page_size; a.n_pages = cache->n_pages; a.n_rows = cache->n_rows;
   a.width = cache->table_width; a.n_freqs = args->n_freqs; a.mscale = args->mscale;
-  // 16-byte accesses need aligned vectors and whole rotating items
+  // 16-byte accesses need aligned vectors and whole rotating items (and head strides of 32 bits)
   bool vec = args->n_freqs % 8 == 0;
+  for (long long s : {a.q_h, a.k_h, a.v_h, a.o_h}) vec = vec && s >= INT32_MIN && s <= INT32_MAX;
   const long long per = 16 / (long long)esz;
   for (const void* p : {args->q, args->k, args->v, (const void*)args->q_out}) vec = vec && aligned_to(p, 16);
   for (long long s : {a.k_t, a.k_h, a.v_t, a.v_h}) vec = vec && s % per == 0;

@@ -176,15 +176,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// keys and values are read once: they need not stay in L1
-__device__ __forceinline__ uint4 ldg_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
 // Shared memory of the kernel: the query as A fragments [part][32-dim chunk][32 lanes][16 B]
 // (WIDE: [part][chunk][2 row halves][32 lanes]), then the warps' partials for the CTA's merge.
 struct AttState {

@@ -80,13 +80,22 @@ struct Conv<__nv_bfloat16> {
   static __device__ __forceinline__ __nv_bfloat16 down(float x) { return __float2bfloat16_rn(x); }
 };
 
+// what is read once need not stay in L1
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 // 8 consecutive elements of memory (16-byte aligned), as they lie there
 template <typename T>
 struct Raw8 {
   uint4 w[sizeof(T) / 2];
   __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = ldg_stream(reinterpret_cast<const uint4*>(p) + i);
   }
   __device__ __forceinline__ void up(float (&x)[8]) const {
 #pragma unroll
