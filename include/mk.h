@@ -488,6 +488,36 @@ typedef struct {
 mk_status mk_beam_select(const mk_select_args* args, int32_t* status, void* stream);
 mk_status mk_beam_select_workspace(int groups, int beams, int vocab, size_t* bytes);
 
+/* A decoder over a paged cache: mk_create's model (weights, batches and dtypes as there) with
+ * the cache in pages, so that sequences share pages, grow page by page and are forked by
+ * mk_update_pages.  A step runs as one launch per op (the multi-launch control), with
+ * mk_rope_append and mk_paged_attention in place of each layer's split-KV units.  rope NULL:
+ * the whole head at desc->rope_theta, unscaled; else its n_rot is at most head_dim.
+ * desc->max_ctx is not used.  Keys are rounded to the cache's type before their rotation and
+ * once more after it.  The pages, table and whatever the calls below are given belong to the
+ * caller. */
+typedef struct {
+  void *k, *v;             /* layer 0's pages, as in mk_page_view                           */
+  long long layer_stride;  /* elements from one layer to the next, a multiple of 8          */
+  long long page_stride;
+  int n_pages, page_size;
+  const int32_t* table;
+  int n_rows, table_width;
+  long long table_stride;
+} mk_paged_kv;
+mk_status mk_create_paged(const mk_model_desc* desc, const mk_weights* weights, const mk_paged_kv* pages,
+                          const mk_rope_desc* rope, int interleaved, const mk_options* opts, void* stream, mk_ctx** out);
+
+/* One step of a paged context, its inputs and outputs in device memory: step row i is token
+ * tok[i] at position pos[i] of table row rows[i] (NULL: row i) and attends to positions
+ * 0..pos[i] -- rows of one call may be consecutive positions of one sequence (a prompt).  Every
+ * position needs its page in the table before the call.  out_tok [B] (or NULL) receives the
+ * argmax, logits [B][vocab] (or NULL) the logits.  Asynchronous; mk_synchronize reports what
+ * went wrong on the device (a bad page or row as MK_ERR_PAGES: nothing is cached for it, and
+ * it is masked).  Not for stream capture. */
+mk_status mk_decode_step_paged(mk_ctx* ctx, const int32_t* tok, const int32_t* pos, const int32_t* rows, int B,
+                               int32_t* out_tok, float* logits);
+
 /* Reads the device status word back (synchronises the stream): MK_OK, or the code found,
  * with its text in mk_last_error.  The word is cleared. */
 mk_status mk_paged_status(int32_t* status, void* stream);

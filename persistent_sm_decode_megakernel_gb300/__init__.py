@@ -114,6 +114,12 @@ class mk_select_args(ctypes.Structure):
                 ("workspace_bytes", c_size_t)]
 
 
+class mk_paged_kv(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("layer_stride", c_ll), ("page_stride", c_ll), ("n_pages", c_int),
+                ("page_size", c_int), ("table", c_void_p), ("n_rows", c_int), ("table_width", c_int),
+                ("table_stride", c_ll)]
+
+
 def _fn(name, argtypes, restype=c_int):
     f = getattr(lib, name)
     f.argtypes = argtypes
@@ -157,6 +163,10 @@ mk_compact_pages = _fn("mk_compact_pages", [ctypes.POINTER(mk_page_pool), c_void
 mk_update_pages_workspace = _fn("mk_update_pages_workspace", [c_int, c_int, c_int, P_size])
 mk_beam_select = _fn("mk_beam_select", [ctypes.POINTER(mk_select_args), c_void_p, c_void_p])
 mk_beam_select_workspace = _fn("mk_beam_select_workspace", [c_int, c_int, c_int, P_size])
+mk_create_paged = _fn("mk_create_paged", [ctypes.POINTER(mk_model_desc), ctypes.POINTER(mk_weights),
+                                          ctypes.POINTER(mk_paged_kv), ctypes.POINTER(mk_rope_desc), c_int,
+                                          ctypes.POINTER(mk_options), c_void_p, ctypes.POINTER(c_void_p)])
+mk_decode_step_paged = _fn("mk_decode_step_paged", [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p])
 mk_paged_status = _fn("mk_paged_status", [c_void_p, c_void_p])
 mk_last_error = _fn("mk_last_error", [], ctypes.c_char_p)
 mk_status_string = _fn("mk_status_string", [c_int], ctypes.c_char_p)

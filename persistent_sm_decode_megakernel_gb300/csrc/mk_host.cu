@@ -18,6 +18,9 @@
 #include "mk_kernels.h"
 #include "mk_plan.h"
 
+namespace mk {
+std::string check_view(const mk_page_view* c);  // mk_append.cu
+}
 using namespace mk;
 
 namespace {
@@ -82,6 +85,21 @@ struct PrefillState {
   std::map<int, std::unique_ptr<Sched>> scheds;
 };
 
+// A context over a paged cache (mk_create_paged): the per-op launches of the multi-launch
+// control, with the append and the paged attention in place of each layer's split-KV units.
+// The QKV op sees a cache of one position (its staging, never read) and so rotates by
+// position 0; its fp32 q, k and v go through mk_rope_append.  The attention writes where a
+// sequence's single split partial lies, as (output, maximum 0, sum 1), and the merge op
+// carries it on to the O projection in the form that takes.
+struct PagedState {
+  mk_page_view view{};       // layer 0
+  long long layer_stride = 0;  // elements
+  int n_freqs = 0, interleaved = 0;
+  float mscale = 1.f;
+  DevBuf staging, freqs, status, work;
+  size_t work_bytes = 0;
+};
+
 struct mk_ctx {
   ModelShape m{};
   mk_options opts{};
@@ -107,6 +125,7 @@ struct mk_ctx {
   bool broken = false;
   int last_B = 1;
   PrefillState pf;
+  std::unique_ptr<PagedState> paged;
   const void* last_arena = nullptr;  // activation arena of the last launch (NaN sentinels)
   ~mk_ctx() {
     if (host_ctl) cudaFreeHost(host_ctl);
@@ -156,7 +175,8 @@ mk_status get_sched_in(mk_ctx* ctx, const ModelShape& m, const Geometry& geo,
   // small batches merge the KV splits inside the O-proj staging; otherwise counter mode
   // merges them in the last-arriving split and sentinel mode keeps the separate
   // ATTN_REDUCE op (it has no atomics to elect a last arriver)
-  const int merge = choose_merge(m, geo, B, ctx->opts.sync_mode == MK_SYNC_COUNTER, ctx->opts.attn_merge);
+  const int merge = ctx->paged ? (int)MERGE_OP
+                               : choose_merge(m, geo, B, ctx->opts.sync_mode == MK_SYNC_COUNTER, ctx->opts.attn_merge);
   const bool pool = ctx->opts.attn_pool == 1 && ctx->opts.exec_mode == MK_EXEC_PERSISTENT;
   std::string e = build_plan(m, geo, ctx->n_cta, B, ctx->opts.fault_drop_signal, merge, &sc->plan, pool);
   if (!e.empty()) return fail(MK_ERR_INVALID, "schedule: " + e);
@@ -397,7 +417,22 @@ mk_status ensure_prefill(mk_ctx* ctx) {
   return MK_OK;
 }
 
+// (maximum 0, sum 1) of every row and head of every layer's single split: the paged attention
+// writes the output before them
+mk_status init_paged_partials(mk_ctx* ctx) {
+  const ModelShape& m = ctx->m;
+  const DevState& S = ctx->st;
+  const size_t rows = (size_t)m.max_batch * m.Hq;
+  std::vector<float> one(2 * rows);
+  for (size_t i = 0; i < rows; ++i) one[2 * i + 1] = 1.f;
+  for (int l = 0; l < m.L; ++l)
+    MK_CUDA(cudaMemcpy2D(S.act + S.act_off[ACT_PART] + l * S.act_stride[ACT_PART] + m.hd, sizeof(float) * (m.hd + kPartExtra),
+                         one.data(), 2 * sizeof(float), 2 * sizeof(float), rows, cudaMemcpyHostToDevice));
+  return MK_OK;
+}
+
 mk_status check_step_args(mk_ctx* ctx, const int32_t* tok, const int32_t* pos, int B) {
+  if (ctx->paged) return fail(MK_ERR_INVALID, "a paged context steps through mk_decode_step_paged");
   if (ctx->broken) return fail(MK_ERR_STATE, "context needs mk_reset after a device error");
   if (B < 1 || B > ctx->m.max_batch) return fail(MK_ERR_INVALID, "B out of range");
   if (!pos) return fail(MK_ERR_INVALID, "pos is NULL");
@@ -463,8 +498,8 @@ mk_status mk_plan(const mk_model_desc* desc, const mk_options* opts, int n_ctas,
   return MK_OK;
 }
 
-mk_status mk_create(const mk_model_desc* desc, const mk_weights* w, const mk_kv* kv, const mk_options* opts,
-                    void* stream, mk_ctx** out) {
+static mk_status create_context(const mk_model_desc* desc, const mk_weights* w, const mk_kv* kv, const mk_options* opts,
+                                void* stream, std::unique_ptr<PagedState> paged, mk_ctx** out) {
   if (!out) return fail(MK_ERR_INVALID, "out is NULL");
   *out = nullptr;
   std::string e = check_desc(desc);
@@ -476,6 +511,7 @@ mk_status mk_create(const mk_model_desc* desc, const mk_weights* w, const mk_kv*
 
   auto ctx = std::make_unique<mk_ctx>();
   ctx->m = m;
+  ctx->paged = std::move(paged);
   if (opts) ctx->opts = *opts;
   mk_options& o = ctx->opts;
   if (o.wait_timeout_s <= 0) o.wait_timeout_s = 2.0;
@@ -618,6 +654,147 @@ mk_status mk_create(const mk_model_desc* desc, const mk_weights* w, const mk_kv*
   return MK_OK;
 }
 
+mk_status mk_create(const mk_model_desc* desc, const mk_weights* w, const mk_kv* kv, const mk_options* opts,
+                    void* stream, mk_ctx** out) {
+  return create_context(desc, w, kv, opts, stream, nullptr, out);
+}
+
+mk_status mk_create_paged(const mk_model_desc* desc, const mk_weights* w, const mk_paged_kv* pages, const mk_rope_desc* rope,
+                          int interleaved, const mk_options* opts, void* stream, mk_ctx** out) {
+  if (!out) return fail(MK_ERR_INVALID, "out is NULL");
+  *out = nullptr;
+  std::string e = check_desc(desc);
+  if (!e.empty()) return fail(MK_ERR_INVALID, e);
+  if (!pages) return fail(MK_ERR_INVALID, "pages is NULL");
+  if (opts && opts->exec_mode != MK_EXEC_PERSISTENT && opts->exec_mode != MK_EXEC_MULTILAUNCH)
+    return fail(MK_ERR_INVALID, "a paged context runs one launch per op");
+  auto ps = std::make_unique<PagedState>();
+  mk_page_view& v = ps->view;
+  v.k = pages->k; v.v = pages->v; v.page_stride = pages->page_stride; v.n_pages = pages->n_pages;
+  v.n_kv_heads = desc->n_kv_heads; v.page_size = pages->page_size; v.head_dim = desc->head_dim; v.dtype = desc->dtype;
+  v.table = pages->table; v.n_rows = pages->n_rows; v.table_width = pages->table_width; v.table_stride = pages->table_stride;
+  e = check_view(&v);
+  if (!e.empty()) return fail(MK_ERR_INVALID, e);
+  if (desc->n_layers > 1 && (pages->layer_stride < v.n_kv_heads * (long long)v.page_size * v.head_dim || pages->layer_stride % 8))
+    return fail(MK_ERR_INVALID, "layer_stride must hold a page and be a multiple of 8");
+  ps->layer_stride = pages->layer_stride;
+  mk_rope_desc plain{};
+  plain.theta = desc->rope_theta;
+  plain.n_rot = desc->head_dim;
+  if (!rope) rope = &plain;
+  if (rope->n_rot > desc->head_dim) return fail(MK_ERR_INVALID, "n_rot must be at most head_dim");
+  if (interleaved != 0 && interleaved != 1) return fail(MK_ERR_INVALID, "interleaved must be 0 or 1");
+  double freqs[64];
+  mk_status s = mk_rope_freqs(rope, freqs, &ps->mscale);
+  if (s) return s;
+  ps->n_freqs = rope->n_rot / 2;
+  ps->interleaved = interleaved;
+  mk_model_desc d = *desc;  // the step kernel's view: a cache of one position
+  d.max_ctx = 1;
+  mk_options o{};
+  if (opts) o = *opts;
+  o.sync_mode = MK_SYNC_COUNTER;
+  o.exec_mode = MK_EXEC_MULTILAUNCH;
+  o.kv_splits = 1;
+  o.attn_merge = 1;
+  o.attn_pool = 0;
+  o.attn_tensor_cores = -1;
+  s = upload(ps->freqs, freqs, sizeof(double) * ps->n_freqs);
+  if (s) return s;
+  MK_CUDA(cudaMalloc(&ps->staging.p, 2ull * desc->max_batch * desc->n_kv_heads * desc->head_dim));
+  MK_CUDA(cudaMalloc(&ps->status.p, 16));
+  MK_CUDA(cudaMemset(ps->status.p, 0, 16));
+  s = mk_paged_attention_workspace(desc->n_heads, desc->n_kv_heads, desc->head_dim, &ps->work_bytes);
+  if (s) return s;
+  MK_CUDA(cudaMalloc(&ps->work.p, ps->work_bytes));
+  std::vector<void*> stage(desc->n_layers, ps->staging.p);
+  const mk_kv kv{stage.data(), stage.data()};
+  mk_ctx* c = nullptr;
+  s = create_context(&d, w, &kv, &o, stream, std::move(ps), &c);
+  if (s) return s;
+  std::unique_ptr<mk_ctx> ctx(c);
+  const size_t phases = ctx->scheds.begin()->second->plan.phase_queues.size();
+  if (phases != 2 + 6 * (size_t)d.n_layers) return fail(MK_ERR_INVALID, "schedule: a paged context needs every op's phase");
+  s = init_paged_partials(c);
+  if (s) return s;
+  MK_CUDA(cudaDeviceSynchronize());
+  *out = ctx.release();
+  return MK_OK;
+}
+
+mk_status mk_decode_step_paged(mk_ctx* ctx, const int32_t* tok, const int32_t* pos, const int32_t* rows, int B,
+                               int32_t* out_tok, float* logits) {
+  if (!ctx) return fail(MK_ERR_INVALID, "ctx is NULL");
+  if (!ctx->paged) return fail(MK_ERR_INVALID, "not a paged context (mk_create_paged)");
+  if (!tok || !pos) return fail(MK_ERR_INVALID, "tok/pos NULL");
+  if (B < 1 || B > ctx->m.max_batch) return fail(MK_ERR_INVALID, "B out of range");
+  if (ctx->broken) return fail(MK_ERR_STATE, "context needs mk_reset after a device error");
+  Sched* sc = nullptr;
+  mk_status s = get_sched(ctx, B, &sc);
+  if (s) return s;
+  const PagedState& ps = *ctx->paged;
+  const ModelShape& m = ctx->m;
+  DevState S = ctx->st;
+  S.trace = ctx->st.trace;
+  S.trace_cap = ctx->st.trace_cap;
+  S.counters = reinterpret_cast<uint32_t*>(sc->counters.p);
+  S.n_counters = sc->plan.n_counters;
+  StepArgs A{};
+  A.step = ctx->step;
+  A.B = B;
+  A.flags = SF_TOK_FROM_DEVICE | SF_NO_SYNC | (ctx->opts.trace ? SF_TRACE : 0);
+  for (int b = 0; b < B; ++b) A.seq[b] = b;
+  A.logits = logits;
+  A.tok_hist = out_tok;
+  const void* fn = S.tc ? ctx->kernel_tc : ctx->kernel;
+  int32_t* status = reinterpret_cast<int32_t*>(ps.status.p);
+  if (ctx->opts.trace) MK_CUDA(cudaMemsetAsync(&reinterpret_cast<Ctl*>(ctx->ctl.p)->trace_n, 0, 4, ctx->stream));
+  MK_CUDA(cudaMemcpyAsync(reinterpret_cast<Ctl*>(ctx->ctl.p)->tok, tok, sizeof(int32_t) * B, cudaMemcpyDeviceToDevice,
+                          ctx->stream));
+  for (size_t k = 0; k < sc->ph_instr.size(); ++k) {
+    const int l = (int)((k - 1) / 6);
+    if (k > 0 && (k - 1) % 6 == OP_ATTN - OP_QKV && l < m.L) {
+      float* q = S.act + S.act_off[ACT_Q] + l * S.act_stride[ACT_Q];
+      const float* kvn = S.act + S.act_off[ACT_KVN] + l * S.act_stride[ACT_KVN];
+      mk_page_view view = ps.view;
+      view.k = static_cast<uint16_t*>(view.k) + l * ps.layer_stride;
+      view.v = static_cast<uint16_t*>(view.v) + l * ps.layer_stride;
+      mk_append_args ap{};
+      ap.q = q; ap.q_out = q; ap.k = kvn; ap.v = kvn + (size_t)m.Hkv * m.hd;
+      ap.dtype = MK_F32; ap.n_tokens = B; ap.n_heads = m.Hq;
+      ap.q_token = ap.o_token = (long long)m.Hq * m.hd;
+      ap.k_token = ap.v_token = 2LL * m.Hkv * m.hd;
+      ap.q_head = ap.o_head = ap.k_head = ap.v_head = m.hd;
+      ap.positions = pos; ap.rows = rows;
+      ap.freqs = reinterpret_cast<const double*>(ps.freqs.p);
+      ap.n_freqs = ps.n_freqs; ap.interleaved = ps.interleaved; ap.mscale = ps.mscale;
+      s = mk_rope_append(&ap, &view, status, ctx->stream);
+      if (s) return s;
+      mk_attend_args at{};
+      at.q = q; at.dtype = MK_F32; at.n_rows = B; at.n_heads = m.Hq;
+      at.q_row = (long long)m.Hq * m.hd; at.q_head = m.hd;
+      at.out = S.act + S.act_off[ACT_PART] + l * S.act_stride[ACT_PART];  // one split: [row][head][hd + kPartExtra]
+      at.o_row = (long long)m.Hq * (m.hd + kPartExtra); at.o_head = m.hd + kPartExtra;
+      at.lens = pos; at.len_add = 1; at.rows = rows;
+      at.scale = (float)(1.0 / std::sqrt((double)m.hd));
+      at.workspace = ps.work.p; at.workspace_bytes = ps.work_bytes;
+      s = mk_paged_attention(&at, &view, status, ctx->stream);
+      if (s) return s;
+      continue;
+    }
+    StepArgs Ak = A;
+    if (k == 0) Ak.flags |= SF_RESET_ARGMAX;
+    Ak.instr = reinterpret_cast<const Instr*>(sc->ph_instr[k].p);
+    Ak.q_start = reinterpret_cast<const int32_t*>(sc->ph_qstart[k].p);
+    s = launch(ctx, fn, S, Ak, false);
+    if (s) return s;
+  }
+  ++sc->epoch;
+  ++ctx->step;
+  ctx->last_B = B;
+  return MK_OK;
+}
+
 mk_status mk_destroy(mk_ctx* ctx) {
   if (!ctx) return MK_OK;
   cudaStreamSynchronize(ctx->stream);
@@ -644,6 +821,7 @@ mk_status mk_info(const mk_ctx* ctx, mk_info_t* info) {
     info->n_counters = it->second->plan.n_counters;
     info->launches_per_step =
         ctx->opts.exec_mode != MK_EXEC_PERSISTENT ? (int)it->second->plan.phase_queues.size() : 1;
+    if (ctx->paged) info->launches_per_step += 2 * ctx->m.L;  // append, attention and its join for the split-KV phase
     info->weight_bytes_per_step = it->second->plan.weight_bytes;
   }
   return MK_OK;
@@ -712,11 +890,14 @@ mk_status mk_decode_steps(mk_ctx* ctx, const int32_t* in_tok, const int32_t* pos
 
 mk_status mk_synchronize(mk_ctx* ctx) {
   if (!ctx) return fail(MK_ERR_INVALID, "ctx is NULL");
-  return read_status(ctx);
+  const mk_status s = read_status(ctx);
+  if (s || !ctx->paged) return s;
+  return mk_paged_status(reinterpret_cast<int32_t*>(ctx->paged->status.p), ctx->stream);
 }
 
 mk_status mk_prefill(mk_ctx* ctx, const int32_t* tokens, int B, int P, int32_t* next_tok, float* logits) {
   if (!ctx) return fail(MK_ERR_INVALID, "ctx is NULL");
+  if (ctx->paged) return fail(MK_ERR_INVALID, "a paged context takes its prompts through mk_decode_step_paged");
   if (!tokens || !next_tok || P < 1) return fail(MK_ERR_INVALID, "tokens/next_tok NULL or P < 1");
   if (P > ctx->m.max_ctx) return fail(MK_ERR_INVALID, "P exceeds max_ctx");
   if (B < 1 || B > ctx->m.max_batch) return fail(MK_ERR_INVALID, "B out of range");
@@ -795,6 +976,11 @@ mk_status mk_reset(mk_ctx* ctx) {
   MK_CUDA(cudaMemset(ctx->ctl.p, 0, sizeof(Ctl)));
   MK_CUDA(cudaMemset(ctx->argkeys.p, 0, sizeof(unsigned long long) * 2 * kMaxBatch));
   MK_CUDA(cudaMemset(ctx->act.p, 0xFF, sizeof(float) * 2 * ctx->st.act_floats));
+  if (ctx->paged) {
+    MK_CUDA(cudaMemset(ctx->paged->status.p, 0, 16));
+    const mk_status s = init_paged_partials(ctx);
+    if (s) return s;
+  }
   MK_CUDA(cudaDeviceSynchronize());
   ctx->step = 0;
   ctx->broken = false;

@@ -167,3 +167,147 @@ class Decoder:
         check(mk_get_trace(self.h, buf, max_records, ctypes.byref(n)), "mk_get_trace")
         return [(r.cta, r.pc, r.op, r.layer, r.t_fetch, r.t_ready, r.t_end, *list(r.t_mark))
                 for r in buf[: n.value]]
+
+
+class PagedDecoder:
+    """A decoder whose KV cache lies in pages (mk_create_paged), for several sequences that share,
+    fork and free them, and a beam search over it.
+
+    n_rows sequences (rows of the page table) of up to max_positions each, n_pages pages of
+    page_size positions; a step takes up to dm.max_batch rows.  dm's own contiguous cache is not
+    used (max_ctx=1 keeps it small).  rope: keyword arguments of paged.rope_freqs (theta, n_rot,
+    kind, factor, ..) where the model's rotary positions are not plain."""
+
+    def __init__(self, dm: DeviceModel, n_rows, n_pages, max_positions, page_size=64, rope=None, interleaved=False,
+                 stream=None):
+        from . import MK_BF16, mk_create_paged, mk_paged_kv, mk_rope_desc, paged
+        c = dm.cfg
+        self.dm, self.paged, self.page_size, self.max_positions = dm, paged, page_size, max_positions
+        self.stream = stream if stream is not None else torch.cuda.current_stream(dm.device)
+        dtype = torch.bfloat16 if dm.desc().dtype == MK_BF16 else torch.float16
+        with torch.cuda.stream(self.stream):
+            pages = torch.zeros((2, c.n_layers, n_pages, c.n_kv_heads, page_size, c.head_dim), dtype=dtype, device=dm.device)
+            self.k, self.v = pages[0], pages[1]
+            self.table = torch.full((n_rows, -(-max_positions // page_size)), -1, dtype=torch.int32, device=dm.device)
+            self.lens = torch.zeros(n_rows, dtype=torch.int32, device=dm.device)
+            self.refs = torch.zeros(n_pages, dtype=torch.int32, device=dm.device)
+            self.status = torch.zeros(4, dtype=torch.int32, device=dm.device)
+        d = dm.desc()
+        w, _, _keep = dm.abi_structs()
+        pk = mk_paged_kv(self.k.data_ptr(), self.v.data_ptr(), self.k.stride(0), self.k.stride(1), n_pages, page_size,
+                         self.table.data_ptr(), n_rows, self.table.shape[1], self.table.stride(0))
+        r = None
+        if rope is not None:
+            kw = {"theta": c.rope_theta, "n_rot": c.head_dim, "kind": "none", "factor": 1.0, "original": 0.0,
+                  "beta_fast": 0.0, "beta_slow": 0.0, **rope}
+            r = ctypes.byref(mk_rope_desc(kw["theta"], kw["n_rot"], paged.ROPE_KINDS[kw["kind"]], kw["factor"],
+                                          kw["original"], kw["beta_fast"], kw["beta_slow"]))
+        h = ctypes.c_void_p()
+        check(mk_create_paged(ctypes.byref(d), ctypes.byref(w), ctypes.byref(pk), r, int(interleaved), None,
+                              ctypes.c_void_p(self.stream.cuda_stream), ctypes.byref(h)), "mk_create_paged")
+        self.h = h
+
+    def close(self):
+        if getattr(self, "h", None):
+            mk_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _int32(self, x):
+        return torch.as_tensor(x, dtype=torch.int32, device=self.dm.device)
+
+    def synchronize(self):
+        """Waits for the stream and raises MkError for what a step or a page update reported."""
+        with torch.cuda.stream(self.stream):
+            self.paged.check_status(self.status)
+        check(mk_synchronize(self.h), "mk_synchronize")
+
+    def update(self, parents=None, reserve=None):
+        """Every row continues row parents[r] (-1: it is freed) and reserves pages for reserve[r] more
+        positions (mk_update_pages)."""
+        with torch.cuda.stream(self.stream):
+            self.paged.update_pages(self.k, self.v, self.table, self.lens, self.refs,
+                                    None if parents is None else self._int32(parents),
+                                    None if reserve is None else self._int32(reserve), self.status)
+
+    def step(self, tokens, positions, rows=None, logits=None):
+        """One step of device int32 tensors: token i at positions[i] of table row rows[i] (default i).  The
+        argmax tokens; positions need their pages (update).  lens is the caller's to advance."""
+        from . import mk_decode_step_paged
+        out = torch.empty(len(tokens), dtype=torch.int32, device=self.dm.device)
+        check(mk_decode_step_paged(self.h, tokens.data_ptr(), positions.data_ptr(), rows.data_ptr() if rows is not None else None,
+                                   len(tokens), out.data_ptr(), logits.data_ptr() if logits is not None else None),
+              "mk_decode_step_paged")
+        return out
+
+    def prefill(self, prompts, logits=None):
+        """Appends prompts {row: tokens} to their rows, up to dm.max_batch positions per step.  Returns
+        {row: next token} (device int32 [1] each); logits {row: float32 [vocab]} receives the last ones."""
+        with torch.cuda.stream(self.stream):
+            n_rows, V = self.table.shape[0], self.dm.cfg.vocab
+            reserve = [0] * n_rows
+            for r, p in prompts.items():
+                reserve[r] = len(p)
+            self.update(reserve=reserve)
+            start = self.lens.tolist()
+            jobs = [(int(t), start[r] + i, r, i == len(p) - 1) for r, p in prompts.items() for i, t in enumerate(p)]
+            last = {}
+            for at in range(0, len(jobs), self.dm.max_batch):
+                part = jobs[at: at + self.dm.max_batch]
+                tok, pos, row = (self._int32([j[x] for j in part]) for x in range(3))
+                z = torch.empty((len(part), V), dtype=torch.float32, device=self.dm.device) if logits is not None else None
+                out = self.step(tok, pos, row, z)
+                for i, j in enumerate(part):
+                    if j[3]:
+                        last[j[2]] = out[i: i + 1]
+                        if logits is not None:
+                            logits[j[2]].copy_(z[i])
+            self.lens += self._int32(reserve)
+        return last
+
+    def beam_search(self, prompt, beams, n_new, eos=-1):
+        """The `beams` best continuations of up to n_new tokens of one prompt by their summed log probability,
+        best first: (tokens [beams, n_new] int32, scores [beams]) on the host; a beam that ended repeats eos.
+        Uses table rows 0..beams-1, which are freed before and after."""
+        dev, c = self.dm.device, self.dm.cfg
+        n_rows = self.table.shape[0]
+        if not 1 <= beams <= min(32, self.dm.max_batch, n_rows):
+            raise ValueError("beams must be in [1, 32] and at most max_batch and n_rows")
+        if n_new < 1 or len(prompt) < 1 or len(prompt) + n_new - 1 > self.max_positions:
+            raise ValueError("the prompt and the new tokens must be positive and fit max_positions")
+        keep = list(range(n_rows))
+        with torch.cuda.stream(self.stream):
+            self.update(parents=[-1] * beams + keep[beams:])
+            first = {0: torch.empty(c.vocab, dtype=torch.float32, device=dev)}
+            self.prefill({0: prompt}, first)
+            logits = first[0].expand(beams, c.vocab).contiguous()
+            scores = torch.full((1, beams), -float("inf"), device=dev)
+            scores[0, 0] = 0.0                        # one beam until the first choice tells them apart
+            ended = torch.zeros((1, beams), dtype=torch.int32, device=dev)
+            parents, reserve = self._int32(keep), torch.zeros(n_rows, dtype=torch.int32, device=dev)
+            reserve[:beams] = 1
+            history = []
+            for i in range(n_new):
+                tokens, par, scores, ended = self.paged.beam_select(logits, scores, ended, eos, self.status)
+                history.append((tokens[0], par[0]))
+                if i + 1 == n_new:
+                    break
+                # beam 0 holds the prompt for all of them at first
+                parents[:beams] = par[0] if i else 0
+                self.update(parents, reserve)
+                self.step(tokens[0].contiguous(), self.lens[:beams].contiguous(), None, logits)
+                self.lens[:beams] += 1
+            self.update(parents=[-1] * beams + keep[beams:])
+            self.synchronize()
+            seqs = np.zeros((beams, n_new), dtype=np.int32)
+            at = np.arange(beams)
+            for i in reversed(range(n_new)):          # back along the parents
+                tokens, par = (x.cpu().numpy() for x in history[i])
+                seqs[:, i] = tokens[at]
+                at = par[at]
+            return seqs, scores[0].cpu().numpy()

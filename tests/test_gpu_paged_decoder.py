@@ -1,0 +1,245 @@
+"""The decoder over a paged cache (PagedDecoder: mk_create_paged, mk_decode_step_paged) against the
+fp64 oracle and the contiguous decoder, its forks, and its beam search."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import synth
+from helpers import LOGIT_RTOL, assert_parity, oracle_run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import __graft_entry__
+    __graft_entry__.build()
+    from persistent_sm_decode_megakernel_gb300 import model
+    return model
+
+
+def _paged(lib, cfg, w, max_batch, n_rows, positions, page_size=16, n_pages=None, **kw):
+    dm = lib.DeviceModel(cfg, w, max_batch=max_batch, max_ctx=1)
+    n_pages = n_pages or n_rows * (-(-positions // page_size)) + 2
+    return lib.PagedDecoder(dm, n_rows=n_rows, n_pages=n_pages, max_positions=positions, page_size=page_size, **kw)
+
+
+def _forced(dec, prompt, toks, n_new, rows):
+    """Prefill, then steps fed the given tokens: logits [B, n_new, V] and tokens [B, n_new]."""
+    B, P = prompt.shape
+    V = dec.dm.cfg.vocab
+    z0 = {r: torch.zeros(V, device=dec.dm.device) for r in rows}
+    first = dec.prefill({r: prompt[b] for b, r in enumerate(rows)}, z0)
+    out, z = [torch.cat([first[r] for r in rows])], [torch.stack([z0[r] for r in rows])]
+    row = dec._int32(rows)
+    for t in range(P, P + n_new - 1):
+        reserve = [0] * len(dec.lens)
+        for r in rows:
+            reserve[r] = 1
+        dec.update(reserve=reserve)
+        lg = torch.zeros((B, V), device=dec.dm.device)
+        out.append(dec.step(dec._int32(toks[:, t]), dec.lens[row.long()], row, lg))
+        dec.lens[row.long()] += 1
+        z.append(lg)
+    dec.synchronize()
+    return torch.stack(z, 1).cpu().numpy(), torch.stack(out, 1).cpu().numpy()
+
+
+@pytest.mark.parametrize("name,B,max_batch", [("tiny", 1, 1), ("tiny", 2, 2), ("tiny", 3, 4), ("tiny", 11, 16), ("tiny-g4", 2, 2),
+                                              ("tiny-g4", 5, 8)])
+def test_paged_decoder_matches_the_oracle(lib, name, B, max_batch):
+    """Prompts in chunks of up to max_batch rows, then forced steps, rows in an order of their own."""
+    cfg = synth.CONFIGS[name]
+    w = synth.gen_weights(cfg)
+    P, n_new = 37, 9
+    prompt = synth.gen_prompts(cfg, B, P)
+    toks, zref = oracle_run(cfg, w, prompt, n_new)
+    dec = _paged(lib, cfg, w, max_batch, B + 1, P + n_new)
+    z, tg = _forced(dec, prompt, toks, n_new, [(b + 1) % (B + 1) for b in range(B)])
+    dec.close()
+    assert assert_parity(z, tg, zref, toks, P) < 5e-3
+
+
+def test_paged_decoder_next_to_the_contiguous_one(lib):
+    """The same prompt and tokens through both: logits apart by the key's second rounding only."""
+    cfg = synth.CONFIGS["tiny-g4"]
+    w = synth.gen_weights(cfg)
+    P = 300
+    prompt = synth.gen_prompts(cfg, 1, P)
+    a = lib.DeviceModel(cfg, w, max_batch=4, max_ctx=P + 1)
+    dec = lib.Decoder(a)
+    za = torch.zeros((1, cfg.vocab), device=a.device)
+    ta = dec.prefill(prompt, logits=za)
+    b = _paged(lib, cfg, w, 4, 1, P + 1, page_size=48)
+    zb = {0: torch.zeros(cfg.vocab, device=a.device)}
+    tb = b.prefill({0: prompt[0]}, zb)
+    b.synchronize()
+    scale = za.abs().max().item()
+    assert (za[0] - zb[0]).abs().max().item() <= 5e-3 * scale
+    top = za[0].topk(2).values
+    if (top[0] - top[1]).item() > 1e-2 * scale:
+        assert int(ta[0]) == int(tb[0])
+    dec.close()
+    b.close()
+
+
+@pytest.mark.parametrize("factor", [2.0, 8.0])
+def test_paged_decoder_scaled_rotary_base(lib, factor):
+    """Rotary positions with the scaled base are those of a model whose theta is the scaled one."""
+    cfg = synth.CONFIGS["tiny"]
+    w = synth.gen_weights(cfg)
+    other = synth.with_overrides(cfg, rope_theta=cfg.rope_theta * factor ** (cfg.head_dim / (cfg.head_dim - 2)))
+    prompt = synth.gen_prompts(cfg, 1, 60)
+    toks, zref = oracle_run(other, w, prompt, 3)
+    dec = _paged(lib, cfg, w, 4, 1, 64, rope=dict(kind="base", factor=factor))
+    z, tg = _forced(dec, prompt, toks, 3, [0])
+    dec.close()
+    assert_parity(z, tg, zref, toks, 60)
+
+
+def test_forked_rows_go_their_own_ways(lib):
+    """A row forked in the middle of a page: parent and child get different tokens and match the oracle's two
+    sequences, while the pages of their common prompt stay shared."""
+    cfg = synth.CONFIGS["tiny"]
+    w = synth.gen_weights(cfg)
+    P, n = 40, 12
+    prompt = synth.gen_prompts(cfg, 1, P)
+    tails = synth.gen_prompts(cfg, 2, n)
+    m = oracle.Model(cfg, w)
+    cache = oracle.KVCache(cfg, 2, P + n)
+    oracle.prefill(m, np.repeat(prompt, 2, 0), cache)
+    want = [oracle.decode_step(m, cache, tails[:, t], [P + t] * 2) for t in range(n)]
+    dec = _paged(lib, cfg, w, 4, 3, P + n)
+    dec.prefill({1: prompt[0]})
+    dec.update(parents=[1, 1, -1], reserve=[n, n, 0])
+    assert torch.equal(dec.table[0, :2], dec.table[1, :2]) and dec.table[0, 2] != dec.table[1, 2]
+    assert int((dec.refs == 2).sum()) == 2
+    for t in range(n):
+        lg = torch.zeros((2, cfg.vocab), device=dec.dm.device)
+        dec.step(dec._int32(tails[:, t]), dec.lens[:2].contiguous(), None, lg)
+        dec.lens[:2] += 1
+        z = lg.cpu().numpy()
+        for b in range(2):
+            assert np.abs(z[b] - want[t][b]).max() <= LOGIT_RTOL * np.abs(want[t][b]).max(), (t, b)
+    dec.synchronize()
+    dec.update(parents=[-1, -1, -1])
+    assert int(dec.refs.sum()) == 0
+    dec.close()
+
+
+def test_beam_search_of_one_beam_is_greedy(lib):
+    cfg = synth.CONFIGS["tiny"]
+    w = synth.gen_weights(cfg)
+    prompt = synth.gen_prompts(cfg, 1, 21)
+    dec = _paged(lib, cfg, w, 4, 4, 64)
+    seqs, scores = dec.beam_search(prompt[0], 1, 10)
+    tok = dec.prefill({2: prompt[0]})[2]
+    greedy = [int(tok)]
+    for _ in range(9):
+        dec.update(reserve=[0, 0, 1, 0])
+        tok = dec.step(tok, dec.lens[2:3].contiguous(), dec._int32([2]))
+        dec.lens[2] += 1
+        greedy.append(int(tok))
+    dec.synchronize()
+    dec.close()
+    assert seqs[0].tolist() == greedy and scores[0] < 0
+
+
+@pytest.mark.parametrize("beams,eos", [(4, -1), (16, -1), (5, 7)])
+def test_beam_search_scores_are_the_sequences_log_probabilities(lib, beams, eos):
+    """Each returned sequence's score is what the oracle gives that sequence, they come best first, and no
+    continuation that the oracle ranks clearly higher under the same pruning is missing: its own search, in
+    64 bits, has the same scores."""
+    cfg = synth.CONFIGS["tiny"]
+    w = synth.gen_weights(cfg)
+    P, n = 30, 6
+    prompt = synth.gen_prompts(cfg, 1, P)
+    dec = _paged(lib, cfg, w, 16, 16, P + n)
+    seqs, scores = dec.beam_search(prompt[0], beams, n, eos=eos)
+    again = dec.beam_search(prompt[0], beams, n, eos=eos)
+    assert int(dec.refs.sum()) == 0
+    dec.close()
+    assert np.array_equal(seqs, again[0]) and np.array_equal(scores, again[1])   # and rows are reusable
+    assert np.all(np.diff(scores) <= 0) and len({tuple(s) for s in seqs}) == beams
+
+    def logp(z):
+        z = z - z.max(-1, keepdims=True)
+        return z - np.log(np.exp(z).sum(-1, keepdims=True))
+
+    m = oracle.Model(cfg, w)
+    cache = oracle.KVCache(cfg, beams, P + n)
+    z0 = oracle.prefill(m, np.repeat(prompt, beams, 0), cache)[:, -1]
+    # a logit is off by at most LOGIT_RTOL of the largest, its log probability by twice that, per step
+    tol = 2 * LOGIT_RTOL * np.abs(z0).max() * n
+    got, z, done = np.zeros(beams), logp(z0), np.zeros(beams, bool)
+    for i in range(n):
+        t = seqs[:, i]
+        got += np.where(done, 0.0, z[np.arange(beams), t])
+        done |= t == eos
+        if i + 1 < n:
+            z = logp(oracle.decode_step(m, cache, t, [P + i] * beams))
+    assert np.abs(got - scores).max() <= tol
+    # the oracle's own beam search: its scores, place by place
+    hist = [((), 0.0)]
+    for i in range(n):
+        grown = []
+        cache = oracle.KVCache(cfg, len(hist), P + n)
+        z = oracle.prefill(m, np.array([list(prompt[0]) + list(h) for h, _ in hist]), cache)[:, -1]
+        for (h, s), lp in zip(hist, logp(z)):
+            if eos in h:
+                grown.append((s, h + (eos,)))
+            else:
+                grown += [(s + lp[t], h + (int(t),)) for t in np.argsort(-lp, kind="stable")[:beams]]
+        grown.sort(key=lambda g: -g[0])
+        hist = [(h, s) for s, h in grown[:beams]]
+    assert np.abs(np.array([s for _, s in hist]) - scores).max() <= tol
+
+
+def test_paged_steps_report_what_is_not_there(lib):
+    """A step whose position has no page, and one whose row is none, end in MK_ERR_PAGES; the context goes on."""
+    from persistent_sm_decode_megakernel_gb300 import MK_ERR_PAGES, MkError
+    cfg = synth.CONFIGS["tiny"]
+    w = synth.gen_weights(cfg)
+    prompt = synth.gen_prompts(cfg, 1, 16)
+    dec = _paged(lib, cfg, w, 4, 2, 64)
+    want = int(dec.prefill({0: prompt[0]})[0])
+    one = dec._int32([want])
+    for pos, row in ((16, 0), (0, 9), (64, 0)):
+        dec.step(one, dec._int32([pos]), dec._int32([row]))
+        with pytest.raises(MkError) as e:
+            dec.synchronize()
+        assert e.value.status == MK_ERR_PAGES
+    dec.update(parents=[-1, -1])
+    assert int(dec.prefill({1: prompt[0]})[1]) == want
+    dec.update(reserve=[0, 100])                       # past the table
+    with pytest.raises(MkError):
+        dec.synchronize()
+    dec.synchronize()
+    dec.close()
+
+
+def test_entry_points_keep_to_their_context(lib):
+    from persistent_sm_decode_megakernel_gb300 import MK_ERR_INVALID, mk_decode_step_paged
+    cfg = synth.CONFIGS["tiny"]
+    w = synth.gen_weights(cfg)
+    dec = _paged(lib, cfg, w, 2, 1, 16)
+    plain = lib.Decoder(lib.DeviceModel(cfg, w, max_batch=1, max_ctx=8))
+    one = torch.zeros(1, dtype=torch.int32, device=dec.dm.device)
+    assert lib.Decoder.decode_step_status(dec, [1], [0])[0] == MK_ERR_INVALID
+    t, tp = lib._i32([1])
+    out, op = lib._i32([0])
+    assert lib.mk_prefill(dec.h, tp, 1, 1, op, None) == MK_ERR_INVALID
+    assert lib.mk_decode_steps(dec.h, tp, tp, 1, 1, None) == MK_ERR_INVALID
+    assert mk_decode_step_paged(plain.h, one.data_ptr(), one.data_ptr(), None, 1, None, None) == MK_ERR_INVALID
+    for B in (0, 3):
+        assert mk_decode_step_paged(dec.h, one.data_ptr(), one.data_ptr(), None, B, None, None) == MK_ERR_INVALID
+    assert mk_decode_step_paged(dec.h, None, one.data_ptr(), None, 1, None, None) == MK_ERR_INVALID
+    with pytest.raises(ValueError):
+        dec.beam_search([1, 2], 2, 4)
+    with pytest.raises(ValueError):
+        dec.beam_search([1, 2], 1, 16)
+    dec.close()
+    plain.close()

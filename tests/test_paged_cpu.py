@@ -223,3 +223,32 @@ def test_plain_pages_keep_their_invariants():
                     assert p.refs[p.table[r, t // ps]] == 1
                 p.lens[r] += rng.integers(0, reserve[r] + 1)
     assert 20 < refused < 380
+
+
+@pytest.mark.parametrize("bad", [dict(k=None), dict(table=None), dict(page_size=24), dict(n_pages=0), dict(layer_stride=64),
+                                 dict(page_stride=64), dict(table_width=0)], ids=str)
+def test_bad_paged_contexts_are_refused(mk, bad):
+    """mk_create_paged checks the descriptor, pages and rotary frequencies before any CUDA call."""
+    import synth
+    c = synth.CONFIGS["tiny"]
+    page = c.n_kv_heads * 16 * c.head_dim
+
+    def create(pages, rope=None, interleaved=0, exec_mode=0, **desc):
+        d = mk.mk_model_desc(c.n_layers, c.d_model, c.n_heads, c.n_kv_heads, c.head_dim, c.ffn_dim, c.vocab, mk.MK_BF16,
+                             c.rms_eps, c.rope_theta, 4, 1)
+        for k, x in desc.items():
+            setattr(d, k, x)
+        o, h = mk.mk_options(exec_mode=exec_mode), ctypes.c_void_p()
+        return mk.mk_create_paged(ctypes.byref(d), None, ctypes.byref(pages) if pages else None,
+                                  ctypes.byref(rope) if rope else None, interleaved, ctypes.byref(o), None, ctypes.byref(h))
+
+    good = dict(k=P, v=P, layer_stride=8 * page, page_stride=page, n_pages=8, page_size=16, table=P, n_rows=2, table_width=4,
+                table_stride=4)
+    assert create(mk.mk_paged_kv(**{**good, **bad})) == mk.MK_ERR_INVALID
+    ok = mk.mk_paged_kv(**good)
+    assert create(None) == mk.MK_ERR_INVALID
+    assert create(ok, vocab=0) == mk.MK_ERR_INVALID
+    assert create(ok, interleaved=2) == mk.MK_ERR_INVALID
+    assert create(ok, exec_mode=2) == mk.MK_ERR_INVALID
+    assert create(ok, rope=mk.mk_rope_desc(10000.0, 128, 0, 1.0, 0, 0, 0)) == mk.MK_ERR_INVALID
+    assert create(ok, rope=mk.mk_rope_desc(10000.0, 64, 1, 0.5, 0, 0, 0)) == mk.MK_ERR_INVALID
