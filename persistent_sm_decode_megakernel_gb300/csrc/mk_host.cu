@@ -740,6 +740,7 @@ mk_status mk_decode_step_paged(mk_ctx* ctx, const int32_t* tok, const int32_t* p
   S.counters = reinterpret_cast<uint32_t*>(sc->counters.p);
   S.n_counters = sc->plan.n_counters;
   StepArgs A{};
+  A.epoch = sc->epoch;
   A.step = ctx->step;
   A.B = B;
   A.flags = SF_TOK_FROM_DEVICE | SF_NO_SYNC | (ctx->opts.trace ? SF_TRACE : 0);
