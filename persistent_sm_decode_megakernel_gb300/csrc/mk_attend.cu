@@ -17,7 +17,8 @@ namespace {
 constexpr int kTile = 16;               // positions per tile: the k extent of the value product
 constexpr int kAttWarps = 4;
 constexpr int kAttThreads = 32 * kAttWarps;
-constexpr int kCtasPerSm = 3;           // 168 registers a thread
+// CTAs of one wave per SM: 168 registers a thread at 128 dims, 128 at 64
+constexpr int ctas_per_sm(int hd) { return hd == 128 ? 3 : 4; }
 constexpr int kJoinThreads = 256;
 constexpr int kMaxGroup = 16;           // query heads per kv head
 constexpr float kLog2e = 1.4426950408889634f;
@@ -211,9 +212,9 @@ struct AttSmem {
 //
 // A warp takes NT tiles at a time: with 64 dims two, so that as many bytes are in flight.
 template <typename C, typename Q, int HD, bool WIDE, int NQ, int NP>
-__global__ void __launch_bounds__(kAttThreads, kCtasPerSm) attend_kernel(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(kAttThreads, ctas_per_sm(HD)) attend_kernel(const __grid_constant__ AttendArgs a) {
   using SM = AttSmem<HD, WIDE, NQ>;
-  constexpr int CH = HD / 32, VH = HD / 64, HEADS = SM::kHeads, ROW = SM::kRow, NT = HD == 64 ? 2 : 1;
+  constexpr int CH = HD / 32, VH = HD / 64, HEADS = SM::kHeads, ROW = SM::kRow, NT = 1;
   constexpr int RH = WIDE ? 2 : 1;  // row halves that are heads of their own
   extern __shared__ __align__(16) unsigned char att_smem[];
   uint4* s_q = reinterpret_cast<uint4*>(att_smem);
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  constexpr int U = 4;  // pieces in flight per warp
+  constexpr int U = 8;  // pieces in flight per warp
   for (int b = c0 + warp; b <= c1; b += W * U) {
     float pm[U], pl[U], po[U][E];
 #pragma unroll
@@ -685,7 +686,7 @@ extern "C" mk_status mk_paged_attention_workspace(int n_heads, int n_kv_heads, i
   int n_sm = 0;
   const mk_status s = sm_count(&n_sm);
   if (s) return s;
-  const size_t n_cta = (size_t)n_sm * kCtasPerSm;
+  const size_t n_cta = (size_t)n_sm * ctas_per_sm(head_dim);
   *bytes = n_cta * (sizeof(int4) + 2 * (n_heads / n_kv_heads) * (head_dim + 4) * sizeof(float));
   return MK_OK;
 }
@@ -728,7 +729,7 @@ extern "C" mk_status mk_paged_attention(const mk_attend_args* args, const mk_pag
   a.table_rows = cache->n_rows; a.width = cache->table_width;
   a.tpp = a.page_size / kTile;
   a.tpp_inverse = a.tpp > 1 ? (unsigned)(((1ULL << 32) + a.tpp - 1) / a.tpp) : 0;
-  a.n_cta = n_sm * kCtasPerSm;
+  a.n_cta = n_sm * ctas_per_sm(cache->head_dim);
   a.part = reinterpret_cast<float*>(a.joins + a.n_cta);
   a.by_segment = (long long)a.n_rows * a.hkv <= a.n_cta;
   a.scale = args->softcap > 0.f ? args->scale / args->softcap : args->scale * kLog2e;
