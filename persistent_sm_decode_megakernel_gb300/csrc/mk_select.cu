@@ -111,9 +111,9 @@ __device__ __forceinline__ u64 ordered(Pair p) { return (u64)orderable(p.hi + 0.
 // A CTA reads its part of a row once, kIter elements at a time with the next ones in flight.
 // The `beams` largest are kept in a list in shared memory, entered by what lies above a bound.
 // The first bound comes from the lanes' maxima.  From then on it is the list's beams-th key: the
-// list is cut down to its best after steps 1, 2, 4, 8, .., each entry counting how many are
-// above it, which is its place; of a part in random order about `beams` keys enter between
-// two of those.  Should the list overflow (rising logits), the part is read again, once per
+// list is cut down to its best after steps 1, 4, 16, .., each entry counting how many are
+// above it, which is its place; of a part in random order about three times `beams` keys
+// enter between two of those.  Should the list overflow (rising logits), the part is read again, once per
 // beam.  The sum of exponentials runs against whole powers of two, so that joining threads,
 // steps and parts rounds nothing: a step's in 32 bits, a compensated sum of them per thread,
 // and from there on whole numbers.  Bound: the logits' bytes for many rows (the arithmetic, one
@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_cons
   const int steps = (n + kIter - 1) / kIter;
   u64 bound = 0ull;            // keys above it enter, if their logit is not below
   float floor_ = -INFINITY;    // this
+  int cut = 1;                 // the list is cut down after this many steps
   bool bad = false;
   float ref = -INFINITY, s = 0.f, comp = 0.f;  // (s + comp) 2^ref: the thread's sum of e^x
   for (int it = 0; it < steps; ++it) {
@@ -232,8 +233,11 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_cons
         if (p < kList) s_list[p] = k;
       }
     }
-    if ((it & (it + 1)) != 0 && it + 1 < steps) continue;
-    // ---- after steps 1, 2, 4, .. and the last: the list's best, in order
+    if (it + 1 == cut)
+      cut *= 4;
+    else if (it + 1 < steps)
+      continue;
+    // ---- after steps 1, 4, 16, .. and the last: the list's best, in order
     __syncthreads();
     int count = s_n;
     if (count > kList) {  // too many: the part's largest one by one, each below the last
@@ -270,12 +274,14 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_cons
         mine[z] = 0ull;
         if (z * kScanThreads >= count) continue;  // uniform
         const int e = z * kScanThreads + tid / share;
-        if (e < count) mine[z] = s_list[e];
         int above = 0;
+        if (e < count) {
+          mine[z] = s_list[e];
 #pragma unroll 4
-        for (int f = f0; f < f1; ++f) above += s_list[f] > mine[z];
+          for (int f = f0; f < f1; ++f) above += s_list[f] > mine[z];
+        }
         if (share == 2) above += __shfl_xor_sync(0xffffffffu, above, 1);
-        if (mine[z]) place[z] = above;
+        if (e < count) place[z] = above;
       }
       __syncthreads();
 #pragma unroll
