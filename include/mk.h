@@ -467,9 +467,9 @@ mk_status mk_update_pages_workspace(int n_rows, int table_width, int n_pages, si
  * offers token `eos` at its own score.  The `beams` best of the group are chosen, best
  * first: tokens, parents (the row chosen from: what mk_update_pages takes), scores, ended.
  * Within a beam the order is by logit, ties to the lowest token; between beams by the score
- * to about 2^-30 (before it is rounded to 32 bits), ties to the lower beam.  Finite logits
- * lie within +-2^126.  A NaN or +inf logit or score is reported (MK_ERR_NAN) and counts as
- * -inf; a token at -inf is only chosen when nothing else is left.  Outputs must not overlap
+ * to about 2^-30 (before it is rounded to 32 bits), ties to the lower beam.  A logit above
+ * 2^126 is taken for +inf, one below -2^126 may be for -inf.  A NaN or +inf logit or score is
+ * reported (MK_ERR_NAN) and counts as -inf; a token at -inf is only chosen when nothing else is left.  Outputs must not overlap
  * the inputs. */
 typedef struct {
   const void* logits;      /* [groups * beams][row_stride], the first vocab entries used    */

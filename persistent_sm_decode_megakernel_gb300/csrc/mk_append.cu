@@ -263,116 +263,122 @@ mk_status launch_append(const AppendArgs& a, int n_sm, int cache_dtype, int hd, 
 extern "C" mk_status mk_rope_append(const mk_append_args* args, const mk_page_view* cache, int32_t* status,
                                     void* stream) {
   using namespace mk;
-  const std::string e = check_view(cache);
-  if (!e.empty()) return paged_fail(MK_ERR_INVALID, e);
-  if (!args || !args->k || !args->v || !args->positions) return paged_fail(MK_ERR_INVALID, "NULL argument");
-  if (!args->q != !args->q_out) return paged_fail(MK_ERR_INVALID, "q and q_out must both be given or both be NULL");
-  if (args->dtype < MK_F16 || args->dtype > MK_F32) return paged_fail(MK_ERR_INVALID, "dtype");
-  if (args->n_tokens < 0 || args->n_heads < 0 || args->n_heads > 65535 || (args->q && args->n_heads < 1))
-    return paged_fail(MK_ERR_INVALID, "n_tokens or n_heads out of range");
-  if (args->n_freqs < 0 || 2 * (long long)args->n_freqs > cache->head_dim)
-    return paged_fail(MK_ERR_INVALID, "n_freqs must be in [0, head_dim / 2]");
-  if (args->n_freqs && !args->freqs) return paged_fail(MK_ERR_INVALID, "freqs is NULL");
-  if (args->interleaved != 0 && args->interleaved != 1) return paged_fail(MK_ERR_INVALID, "interleaved must be 0 or 1");
-  const size_t esz = args->dtype == MK_F32 ? 4 : 2;
-  for (const void* p : {args->q, args->k, args->v, (const void*)args->q_out})
-    if (!aligned_to(p, esz)) return paged_fail(MK_ERR_INVALID, "q, k, v and q_out must be aligned to their type");
-  if (args->q == args->q_out && args->q && (args->q_token != args->o_token || args->q_head != args->o_head))
-    return paged_fail(MK_ERR_INVALID, "q_out in the place of q needs q's strides");
-  if (args->n_tokens == 0) return MK_OK;
-  AppendArgs a{};
-  a.q = args->q; a.k = args->k; a.v = args->v; a.qo = args->q_out;
-  a.kc = cache->k; a.vc = cache->v;
-  a.q_t = args->q_token; a.q_h = args->q_head; a.k_t = args->k_token; a.k_h = args->k_head;
-  a.v_t = args->v_token; a.v_h = args->v_head; a.o_t = args->o_token; a.o_h = args->o_head;
-  a.page_stride = cache->page_stride; a.table_stride = cache->table_stride;
-  a.positions = args->positions; a.rows = args->rows; a.table = cache->table; a.freqs = args->freqs; a.status = status;
-  a.n_tokens = args->n_tokens; a.hq = args->q ? args->n_heads : 0;
-  a.hkv = cache->n_kv_heads; a.page_size = cache->page_size; a.n_pages = cache->n_pages; a.n_rows = cache->n_rows;
-  a.width = cache->table_width; a.n_freqs = args->n_freqs; a.mscale = args->mscale;
-  // 16-byte accesses need aligned vectors and whole rotating items (and head strides of 32 bits)
-  bool vec = args->n_freqs % 8 == 0;
-  for (long long s : {a.q_h, a.k_h, a.v_h, a.o_h}) vec = vec && s >= INT32_MIN && s <= INT32_MAX;
-  const long long per = 16 / (long long)esz;
-  for (const void* p : {args->q, args->k, args->v, (const void*)args->q_out}) vec = vec && aligned_to(p, 16);
-  for (long long s : {a.k_t, a.k_h, a.v_t, a.v_h}) vec = vec && s % per == 0;
-  if (args->q)
-    for (long long s : {a.q_t, a.q_h, a.o_t, a.o_h}) vec = vec && s % per == 0;
-  const bool inter = args->interleaved != 0;
-  int n_sm = 0;
-  const mk_status s = sm_count(&n_sm);
-  if (s) return s;
-  if (args->dtype == MK_F32)
-    return launch_append<float>(a, n_sm, cache->dtype, cache->head_dim, inter, vec, stream);
-  if (args->dtype == MK_F16)
-    return launch_append<__half>(a, n_sm, cache->dtype, cache->head_dim, inter, vec, stream);
-  return launch_append<__nv_bfloat16>(a, n_sm, cache->dtype, cache->head_dim, inter, vec, stream);
+  return c_entry([&]() -> mk_status {
+    const std::string e = check_view(cache);
+    if (!e.empty()) return paged_fail(MK_ERR_INVALID, e);
+    if (!args || !args->k || !args->v || !args->positions) return paged_fail(MK_ERR_INVALID, "NULL argument");
+    if (!args->q != !args->q_out) return paged_fail(MK_ERR_INVALID, "q and q_out must both be given or both be NULL");
+    if (args->dtype < MK_F16 || args->dtype > MK_F32) return paged_fail(MK_ERR_INVALID, "dtype");
+    if (args->n_tokens < 0 || args->n_heads < 0 || args->n_heads > 65535 || (args->q && args->n_heads < 1))
+      return paged_fail(MK_ERR_INVALID, "n_tokens or n_heads out of range");
+    if (args->n_freqs < 0 || 2 * (long long)args->n_freqs > cache->head_dim)
+      return paged_fail(MK_ERR_INVALID, "n_freqs must be in [0, head_dim / 2]");
+    if (args->n_freqs && !args->freqs) return paged_fail(MK_ERR_INVALID, "freqs is NULL");
+    if (args->interleaved != 0 && args->interleaved != 1) return paged_fail(MK_ERR_INVALID, "interleaved must be 0 or 1");
+    const size_t esz = args->dtype == MK_F32 ? 4 : 2;
+    for (const void* p : {args->q, args->k, args->v, (const void*)args->q_out})
+      if (!aligned_to(p, esz)) return paged_fail(MK_ERR_INVALID, "q, k, v and q_out must be aligned to their type");
+    if (args->q == args->q_out && args->q && (args->q_token != args->o_token || args->q_head != args->o_head))
+      return paged_fail(MK_ERR_INVALID, "q_out in the place of q needs q's strides");
+    if (args->n_tokens == 0) return MK_OK;
+    AppendArgs a{};
+    a.q = args->q; a.k = args->k; a.v = args->v; a.qo = args->q_out;
+    a.kc = cache->k; a.vc = cache->v;
+    a.q_t = args->q_token; a.q_h = args->q_head; a.k_t = args->k_token; a.k_h = args->k_head;
+    a.v_t = args->v_token; a.v_h = args->v_head; a.o_t = args->o_token; a.o_h = args->o_head;
+    a.page_stride = cache->page_stride; a.table_stride = cache->table_stride;
+    a.positions = args->positions; a.rows = args->rows; a.table = cache->table; a.freqs = args->freqs; a.status = status;
+    a.n_tokens = args->n_tokens; a.hq = args->q ? args->n_heads : 0;
+    a.hkv = cache->n_kv_heads; a.page_size = cache->page_size; a.n_pages = cache->n_pages; a.n_rows = cache->n_rows;
+    a.width = cache->table_width; a.n_freqs = args->n_freqs; a.mscale = args->mscale;
+    // 16-byte accesses need aligned vectors and whole rotating items (and head strides of 32 bits)
+    bool vec = args->n_freqs % 8 == 0;
+    for (long long s : {a.q_h, a.k_h, a.v_h, a.o_h}) vec = vec && s >= INT32_MIN && s <= INT32_MAX;
+    const long long per = 16 / (long long)esz;
+    for (const void* p : {args->q, args->k, args->v, (const void*)args->q_out}) vec = vec && aligned_to(p, 16);
+    for (long long s : {a.k_t, a.k_h, a.v_t, a.v_h}) vec = vec && s % per == 0;
+    if (args->q)
+      for (long long s : {a.q_t, a.q_h, a.o_t, a.o_h}) vec = vec && s % per == 0;
+    const bool inter = args->interleaved != 0;
+    int n_sm = 0;
+    const mk_status s = sm_count(&n_sm);
+    if (s) return s;
+    if (args->dtype == MK_F32)
+      return launch_append<float>(a, n_sm, cache->dtype, cache->head_dim, inter, vec, stream);
+    if (args->dtype == MK_F16)
+      return launch_append<__half>(a, n_sm, cache->dtype, cache->head_dim, inter, vec, stream);
+    return launch_append<__nv_bfloat16>(a, n_sm, cache->dtype, cache->head_dim, inter, vec, stream);
+  });
 }
 
 extern "C" mk_status mk_rope_freqs(const mk_rope_desc* d, double* freqs, float* mscale) {
   using namespace mk;
-  if (!d || !freqs || !mscale) return paged_fail(MK_ERR_INVALID, "NULL argument");
-  if (!(d->theta > 0) || !std::isfinite(d->theta)) return paged_fail(MK_ERR_INVALID, "theta must be positive");
-  if (d->n_rot < 2 || d->n_rot % 2 || d->n_rot > 128) return paged_fail(MK_ERR_INVALID, "n_rot must be even, in [2, 128]");
-  if (d->kind < 0 || d->kind > 4) return paged_fail(MK_ERR_INVALID, "kind must be 0..4");
-  if (d->kind && (!(d->factor >= 1) || !std::isfinite(d->factor)))
-    return paged_fail(MK_ERR_INVALID, "factor must be at least 1");
-  if (d->kind == 2 && d->n_rot < 4) return paged_fail(MK_ERR_INVALID, "the scaled base needs n_rot >= 4");
-  const double pi = 3.14159265358979323846;
-  double fast = d->beta_fast, slow = d->beta_slow;
-  if (d->kind >= 3) {
-    if (!(d->original > 0) || !std::isfinite(d->original)) return paged_fail(MK_ERR_INVALID, "original must be positive");
-    if (fast == 0) fast = d->kind == 3 ? 32 : 4;
-    if (slow == 0) slow = 1;
-    if (!(fast > slow) || !(slow > 0))
-      return paged_fail(MK_ERR_INVALID, "beta_fast must be above beta_slow, both positive");
-    if (d->kind == 3 && !(d->theta > 1)) return paged_fail(MK_ERR_INVALID, "the blend needs theta above 1");
-  }
-  const int n = d->n_rot / 2;
-  const double theta = d->kind == 2 ? d->theta * std::pow(d->factor, (double)d->n_rot / (d->n_rot - 2)) : d->theta;
-  // the (fractional) pair index that turns `turns` times within `original` positions
-  auto index_of = [&](double turns) {
-    return d->n_rot * std::log(d->original / (turns * 2 * pi)) / (2 * std::log(d->theta));
-  };
-  double lo = 0, hi = 0;
-  if (d->kind == 3) {
-    lo = std::max(0.0, std::floor(index_of(fast)));
-    hi = std::min((double)d->n_rot - 1, std::ceil(index_of(slow)));
-    if (hi <= lo) hi = lo + 0.001;
-  }
-  for (int i = 0; i < n; ++i) {
-    const double f = std::pow(theta, -2.0 * i / d->n_rot);
-    double r = f;
-    if (d->kind == 1) r = f / d->factor;
+  return c_entry([&]() -> mk_status {
+    if (!d || !freqs || !mscale) return paged_fail(MK_ERR_INVALID, "NULL argument");
+    if (!(d->theta > 0) || !std::isfinite(d->theta)) return paged_fail(MK_ERR_INVALID, "theta must be positive");
+    if (d->n_rot < 2 || d->n_rot % 2 || d->n_rot > 128) return paged_fail(MK_ERR_INVALID, "n_rot must be even, in [2, 128]");
+    if (d->kind < 0 || d->kind > 4) return paged_fail(MK_ERR_INVALID, "kind must be 0..4");
+    if (d->kind && (!(d->factor >= 1) || !std::isfinite(d->factor)))
+      return paged_fail(MK_ERR_INVALID, "factor must be at least 1");
+    if (d->kind == 2 && d->n_rot < 4) return paged_fail(MK_ERR_INVALID, "the scaled base needs n_rot >= 4");
+    const double pi = 3.14159265358979323846;
+    double fast = d->beta_fast, slow = d->beta_slow;
+    if (d->kind >= 3) {
+      if (!(d->original > 0) || !std::isfinite(d->original)) return paged_fail(MK_ERR_INVALID, "original must be positive");
+      if (fast == 0) fast = d->kind == 3 ? 32 : 4;
+      if (slow == 0) slow = 1;
+      if (!(fast > slow) || !(slow > 0))
+        return paged_fail(MK_ERR_INVALID, "beta_fast must be above beta_slow, both positive");
+      if (d->kind == 3 && !(d->theta > 1)) return paged_fail(MK_ERR_INVALID, "the blend needs theta above 1");
+    }
+    const int n = d->n_rot / 2;
+    const double theta = d->kind == 2 ? d->theta * std::pow(d->factor, (double)d->n_rot / (d->n_rot - 2)) : d->theta;
+    // the (fractional) pair index that turns `turns` times within `original` positions
+    auto index_of = [&](double turns) {
+      return d->n_rot * std::log(d->original / (turns * 2 * pi)) / (2 * std::log(d->theta));
+    };
+    double lo = 0, hi = 0;
     if (d->kind == 3) {
-      const double far = std::min(1.0, std::max(0.0, (i - lo) / (hi - lo)));  // share of the divided frequency
-      r = f * (1 - far) + f / d->factor * far;
+      lo = std::max(0.0, std::floor(index_of(fast)));
+      hi = std::min((double)d->n_rot - 1, std::ceil(index_of(slow)));
+      if (hi <= lo) hi = lo + 0.001;
     }
-    if (d->kind == 4) {
-      const double turns = d->original * f / (2 * pi);  // original / wavelength
-      const double near = std::min(1.0, std::max(0.0, (turns - slow) / (fast - slow)));
-      r = f * near + f / d->factor * (1 - near);
+    for (int i = 0; i < n; ++i) {
+      const double f = std::pow(theta, -2.0 * i / d->n_rot);
+      double r = f;
+      if (d->kind == 1) r = f / d->factor;
+      if (d->kind == 3) {
+        const double far = std::min(1.0, std::max(0.0, (i - lo) / (hi - lo)));  // share of the divided frequency
+        r = f * (1 - far) + f / d->factor * far;
+      }
+      if (d->kind == 4) {
+        const double turns = d->original * f / (2 * pi);  // original / wavelength
+        const double near = std::min(1.0, std::max(0.0, (turns - slow) / (fast - slow)));
+        r = f * near + f / d->factor * (1 - near);
+      }
+      freqs[i] = r;
     }
-    freqs[i] = r;
-  }
-  *mscale = d->kind == 3 ? (float)(0.1 * std::log(d->factor) + 1.0) : 1.0f;
-  return MK_OK;
+    *mscale = d->kind == 3 ? (float)(0.1 * std::log(d->factor) + 1.0) : 1.0f;
+    return MK_OK;
+  });
 }
 
 extern "C" mk_status mk_paged_status(int32_t* status, void* stream) {
   using namespace mk;
-  if (!status) return paged_fail(MK_ERR_INVALID, "status is NULL");
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  int32_t got[4] = {};
-  cudaError_t e = cudaMemcpyAsync(got, status, sizeof got, cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess && got[0]) e = cudaMemsetAsync(status, 0, sizeof got, s);
-  if (e != cudaSuccess) return paged_fail(MK_ERR_CUDA, std::string("mk_paged_status: ") + cudaGetErrorString(e));
-  if (!got[0]) return MK_OK;
-  static const char* const ops[] = {"?", "append", "attention", "page update", "compaction", "selection"};
-  char buf[160];
-  snprintf(buf, sizeof buf, "%s: %s at row %d, value %d", ops[got[1] >= 1 && got[1] <= 5 ? got[1] : 0],
-           got[0] == MK_ERR_NAN ? "a NaN or infinite logit" : "a bad page, row, length or parent, or too few free pages",
-           got[2], got[3]);
-  return paged_fail((mk_status)got[0], buf);
+  return c_entry([&]() -> mk_status {
+    if (!status) return paged_fail(MK_ERR_INVALID, "status is NULL");
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int32_t got[4] = {};
+    cudaError_t e = cudaMemcpyAsync(got, status, sizeof got, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess && got[0]) e = cudaMemsetAsync(status, 0, sizeof got, s);
+    if (e != cudaSuccess) return paged_fail(MK_ERR_CUDA, std::string("mk_paged_status: ") + cudaGetErrorString(e));
+    if (!got[0]) return MK_OK;
+    static const char* const ops[] = {"?", "append", "attention", "page update", "compaction", "selection"};
+    char buf[160];
+    snprintf(buf, sizeof buf, "%s: %s at row %d, value %d", ops[got[1] >= 1 && got[1] <= 5 ? got[1] : 0],
+             got[0] == MK_ERR_NAN ? "a NaN or infinite logit" : "a bad page, row, length or parent, or too few free pages",
+             got[2], got[3]);
+    return paged_fail((mk_status)got[0], buf);
+  });
 }

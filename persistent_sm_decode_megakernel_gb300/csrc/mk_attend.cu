@@ -679,70 +679,74 @@ mk_status launch_attend(const AttendArgs& a, int hd, void* stream) {
 
 extern "C" mk_status mk_paged_attention_workspace(int n_heads, int n_kv_heads, int head_dim, size_t* bytes) {
   using namespace mk;
-  if (!bytes) return paged_fail(MK_ERR_INVALID, "bytes is NULL");
-  if (n_kv_heads < 1 || n_heads < 1 || n_heads % n_kv_heads || n_heads / n_kv_heads > kMaxGroup)
-    return paged_fail(MK_ERR_INVALID, "n_heads / n_kv_heads must be a whole number in [1, 16]");
-  if (head_dim != 64 && head_dim != 128) return paged_fail(MK_ERR_INVALID, "head_dim must be 64 or 128");
-  int n_sm = 0;
-  const mk_status s = sm_count(&n_sm);
-  if (s) return s;
-  const size_t n_cta = (size_t)n_sm * ctas_per_sm(head_dim);
-  *bytes = n_cta * (sizeof(int4) + 2 * (n_heads / n_kv_heads) * (head_dim + 4) * sizeof(float));
-  return MK_OK;
+  return c_entry([&]() -> mk_status {
+    if (!bytes) return paged_fail(MK_ERR_INVALID, "bytes is NULL");
+    if (n_kv_heads < 1 || n_heads < 1 || n_heads % n_kv_heads || n_heads / n_kv_heads > kMaxGroup)
+      return paged_fail(MK_ERR_INVALID, "n_heads / n_kv_heads must be a whole number in [1, 16]");
+    if (head_dim != 64 && head_dim != 128) return paged_fail(MK_ERR_INVALID, "head_dim must be 64 or 128");
+    int n_sm = 0;
+    const mk_status s = sm_count(&n_sm);
+    if (s) return s;
+    const size_t n_cta = (size_t)n_sm * ctas_per_sm(head_dim);
+    *bytes = n_cta * (sizeof(int4) + 2 * (n_heads / n_kv_heads) * (head_dim + 4) * sizeof(float));
+    return MK_OK;
+  });
 }
 
 extern "C" mk_status mk_paged_attention(const mk_attend_args* args, const mk_page_view* cache, int32_t* status,
                                         void* stream) {
   using namespace mk;
-  const std::string e = check_view(cache);
-  if (!e.empty()) return paged_fail(MK_ERR_INVALID, e);
-  if (!args || !args->q || !args->out || !args->lens) return paged_fail(MK_ERR_INVALID, "NULL argument");
-  if (args->dtype < MK_F16 || args->dtype > MK_F32) return paged_fail(MK_ERR_INVALID, "dtype");
-  if (args->n_heads < 1 || args->n_heads % cache->n_kv_heads || args->n_heads / cache->n_kv_heads > kMaxGroup)
-    return paged_fail(MK_ERR_INVALID, "n_heads / n_kv_heads must be a whole number in [1, 16]");
-  if (args->n_rows < 0 || (long long)args->n_rows * args->n_heads > 0x7fffffffLL)
-    return paged_fail(MK_ERR_INVALID, "n_rows out of range");
-  if (args->window < 0) return paged_fail(MK_ERR_INVALID, "window must not be negative");
-  if (!(args->softcap >= 0.f) || !(args->scale == args->scale)) return paged_fail(MK_ERR_INVALID, "scale or softcap");
-  const size_t esz = args->dtype == MK_F32 ? 4 : 2;
-  if (!aligned_to(args->q, esz) || !aligned_to(args->out, esz))
-    return paged_fail(MK_ERR_INVALID, "q and out must be aligned to their type");
-  if (!args->workspace || !aligned_to(args->workspace, 16))
-    return paged_fail(MK_ERR_INVALID, "the workspace is missing or unaligned");
-  if (args->n_rows == 0) return MK_OK;
-  size_t need = 0;
-  mk_status s = mk_paged_attention_workspace(args->n_heads, cache->n_kv_heads, cache->head_dim, &need);
-  if (s) return s;
-  if (args->workspace_bytes < need)
-    return paged_fail(MK_ERR_INVALID, "the workspace is too small (mk_paged_attention_workspace)");
-  int n_sm = 0;
-  s = sm_count(&n_sm);
-  if (s) return s;
-  AttendArgs a{};
-  a.q = args->q; a.k = cache->k; a.v = cache->v; a.out = args->out; a.lse = args->lse;
-  a.joins = static_cast<int4*>(args->workspace);
-  a.lens = args->lens; a.rows = args->rows; a.table = cache->table; a.status = status;
-  a.q_row = args->q_row; a.q_head = args->q_head; a.o_row = args->o_row; a.o_head = args->o_head;
-  a.page_stride = cache->page_stride; a.table_stride = cache->table_stride;
-  a.n_rows = args->n_rows; a.hq = args->n_heads; a.hkv = cache->n_kv_heads; a.group = args->n_heads / cache->n_kv_heads;
-  a.len_add = args->len_add; a.window = args->window; a.page_size = cache->page_size; a.n_pages = cache->n_pages;
-  a.table_rows = cache->n_rows; a.width = cache->table_width;
-  a.tpp = a.page_size / kTile;
-  a.tpp_inverse = a.tpp > 1 ? (unsigned)(((1ULL << 32) + a.tpp - 1) / a.tpp) : 0;
-  a.n_cta = n_sm * ctas_per_sm(cache->head_dim);
-  a.part = reinterpret_cast<float*>(a.joins + a.n_cta);
-  a.by_segment = (long long)a.n_rows * a.hkv <= a.n_cta;
-  a.scale = args->softcap > 0.f ? args->scale / args->softcap : args->scale * kLog2e;
-  a.softcap = args->softcap * kLog2e;
-  // 16-bit queries of the cache's type are exact in one part.  Other queries are split into
-  // 2 parts of fp16 (22 bits) or 3 of bf16 (24 bits); probabilities likewise, 2 parts of
-  // bf16 (16 bits) being enough for an output of 16 bits.
-  if (cache->dtype == MK_F16) {
-    if (args->dtype == MK_F16) return launch_attend<__half, __half, 1, 2>(a, cache->head_dim, stream);
-    if (args->dtype == MK_BF16) return launch_attend<__half, __nv_bfloat16, 2, 2>(a, cache->head_dim, stream);
-    return launch_attend<__half, float, 2, 2>(a, cache->head_dim, stream);
-  }
-  if (args->dtype == MK_BF16) return launch_attend<__nv_bfloat16, __nv_bfloat16, 1, 2>(a, cache->head_dim, stream);
-  if (args->dtype == MK_F16) return launch_attend<__nv_bfloat16, __half, 2, 2>(a, cache->head_dim, stream);
-  return launch_attend<__nv_bfloat16, float, 3, 3>(a, cache->head_dim, stream);
+  return c_entry([&]() -> mk_status {
+    const std::string e = check_view(cache);
+    if (!e.empty()) return paged_fail(MK_ERR_INVALID, e);
+    if (!args || !args->q || !args->out || !args->lens) return paged_fail(MK_ERR_INVALID, "NULL argument");
+    if (args->dtype < MK_F16 || args->dtype > MK_F32) return paged_fail(MK_ERR_INVALID, "dtype");
+    if (args->n_heads < 1 || args->n_heads % cache->n_kv_heads || args->n_heads / cache->n_kv_heads > kMaxGroup)
+      return paged_fail(MK_ERR_INVALID, "n_heads / n_kv_heads must be a whole number in [1, 16]");
+    if (args->n_rows < 0 || (long long)args->n_rows * args->n_heads > 0x7fffffffLL)
+      return paged_fail(MK_ERR_INVALID, "n_rows out of range");
+    if (args->window < 0) return paged_fail(MK_ERR_INVALID, "window must not be negative");
+    if (!(args->softcap >= 0.f && args->softcap < INFINITY) || !(fabsf(args->scale) < INFINITY)) return paged_fail(MK_ERR_INVALID, "scale or softcap");
+    const size_t esz = args->dtype == MK_F32 ? 4 : 2;
+    if (!aligned_to(args->q, esz) || !aligned_to(args->out, esz))
+      return paged_fail(MK_ERR_INVALID, "q and out must be aligned to their type");
+    if (!args->workspace || !aligned_to(args->workspace, 16))
+      return paged_fail(MK_ERR_INVALID, "the workspace is missing or unaligned");
+    if (args->n_rows == 0) return MK_OK;
+    size_t need = 0;
+    mk_status s = mk_paged_attention_workspace(args->n_heads, cache->n_kv_heads, cache->head_dim, &need);
+    if (s) return s;
+    if (args->workspace_bytes < need)
+      return paged_fail(MK_ERR_INVALID, "the workspace is too small (mk_paged_attention_workspace)");
+    int n_sm = 0;
+    s = sm_count(&n_sm);
+    if (s) return s;
+    AttendArgs a{};
+    a.q = args->q; a.k = cache->k; a.v = cache->v; a.out = args->out; a.lse = args->lse;
+    a.joins = static_cast<int4*>(args->workspace);
+    a.lens = args->lens; a.rows = args->rows; a.table = cache->table; a.status = status;
+    a.q_row = args->q_row; a.q_head = args->q_head; a.o_row = args->o_row; a.o_head = args->o_head;
+    a.page_stride = cache->page_stride; a.table_stride = cache->table_stride;
+    a.n_rows = args->n_rows; a.hq = args->n_heads; a.hkv = cache->n_kv_heads; a.group = args->n_heads / cache->n_kv_heads;
+    a.len_add = args->len_add; a.window = args->window; a.page_size = cache->page_size; a.n_pages = cache->n_pages;
+    a.table_rows = cache->n_rows; a.width = cache->table_width;
+    a.tpp = a.page_size / kTile;
+    a.tpp_inverse = a.tpp > 1 ? (unsigned)(((1ULL << 32) + a.tpp - 1) / a.tpp) : 0;
+    a.n_cta = n_sm * ctas_per_sm(cache->head_dim);
+    a.part = reinterpret_cast<float*>(a.joins + a.n_cta);
+    a.by_segment = (long long)a.n_rows * a.hkv <= a.n_cta;
+    a.scale = args->softcap > 0.f ? args->scale / args->softcap : args->scale * kLog2e;
+    a.softcap = args->softcap * kLog2e;
+    // 16-bit queries of the cache's type are exact in one part.  Other queries are split into
+    // 2 parts of fp16 (22 bits) or 3 of bf16 (24 bits); probabilities likewise, 2 parts of
+    // bf16 (16 bits) being enough for an output of 16 bits.
+    if (cache->dtype == MK_F16) {
+      if (args->dtype == MK_F16) return launch_attend<__half, __half, 1, 2>(a, cache->head_dim, stream);
+      if (args->dtype == MK_BF16) return launch_attend<__half, __nv_bfloat16, 2, 2>(a, cache->head_dim, stream);
+      return launch_attend<__half, float, 2, 2>(a, cache->head_dim, stream);
+    }
+    if (args->dtype == MK_BF16) return launch_attend<__nv_bfloat16, __nv_bfloat16, 1, 2>(a, cache->head_dim, stream);
+    if (args->dtype == MK_F16) return launch_attend<__nv_bfloat16, __half, 2, 2>(a, cache->head_dim, stream);
+    return launch_attend<__nv_bfloat16, float, 3, 3>(a, cache->head_dim, stream);
+  });
 }

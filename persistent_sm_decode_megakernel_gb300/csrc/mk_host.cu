@@ -18,9 +18,8 @@
 #include "mk_kernels.h"
 #include "mk_plan.h"
 
-namespace mk {
-std::string check_view(const mk_page_view* c);  // mk_append.cu
-}
+#include "mk_paged.cuh"
+
 using namespace mk;
 
 namespace {
@@ -661,139 +660,143 @@ mk_status mk_create(const mk_model_desc* desc, const mk_weights* w, const mk_kv*
 
 mk_status mk_create_paged(const mk_model_desc* desc, const mk_weights* w, const mk_paged_kv* pages, const mk_rope_desc* rope,
                           int interleaved, const mk_options* opts, void* stream, mk_ctx** out) {
-  if (!out) return fail(MK_ERR_INVALID, "out is NULL");
-  *out = nullptr;
-  std::string e = check_desc(desc);
-  if (!e.empty()) return fail(MK_ERR_INVALID, e);
-  if (!pages) return fail(MK_ERR_INVALID, "pages is NULL");
-  if (opts && opts->exec_mode != MK_EXEC_PERSISTENT && opts->exec_mode != MK_EXEC_MULTILAUNCH)
-    return fail(MK_ERR_INVALID, "a paged context runs one launch per op");
-  auto ps = std::make_unique<PagedState>();
-  mk_page_view& v = ps->view;
-  v.k = pages->k; v.v = pages->v; v.page_stride = pages->page_stride; v.n_pages = pages->n_pages;
-  v.n_kv_heads = desc->n_kv_heads; v.page_size = pages->page_size; v.head_dim = desc->head_dim; v.dtype = desc->dtype;
-  v.table = pages->table; v.n_rows = pages->n_rows; v.table_width = pages->table_width; v.table_stride = pages->table_stride;
-  e = check_view(&v);
-  if (!e.empty()) return fail(MK_ERR_INVALID, e);
-  if (desc->n_layers > 1 && (pages->layer_stride < v.n_kv_heads * (long long)v.page_size * v.head_dim || pages->layer_stride % 8))
-    return fail(MK_ERR_INVALID, "layer_stride must hold a page and be a multiple of 8");
-  ps->layer_stride = pages->layer_stride;
-  mk_rope_desc plain{};
-  plain.theta = desc->rope_theta;
-  plain.n_rot = desc->head_dim;
-  if (!rope) rope = &plain;
-  if (rope->n_rot > desc->head_dim) return fail(MK_ERR_INVALID, "n_rot must be at most head_dim");
-  if (interleaved != 0 && interleaved != 1) return fail(MK_ERR_INVALID, "interleaved must be 0 or 1");
-  double freqs[64];
-  mk_status s = mk_rope_freqs(rope, freqs, &ps->mscale);
-  if (s) return s;
-  ps->n_freqs = rope->n_rot / 2;
-  ps->interleaved = interleaved;
-  mk_model_desc d = *desc;  // the step kernel's view: a cache of one position
-  d.max_ctx = 1;
-  mk_options o{};
-  if (opts) o = *opts;
-  o.sync_mode = MK_SYNC_COUNTER;
-  o.exec_mode = MK_EXEC_MULTILAUNCH;
-  o.kv_splits = 1;
-  o.attn_merge = 1;
-  o.attn_pool = 0;
-  o.attn_tensor_cores = -1;
-  s = upload(ps->freqs, freqs, sizeof(double) * ps->n_freqs);
-  if (s) return s;
-  MK_CUDA(cudaMalloc(&ps->staging.p, 2ull * desc->max_batch * desc->n_kv_heads * desc->head_dim));
-  MK_CUDA(cudaMalloc(&ps->status.p, 16));
-  MK_CUDA(cudaMemset(ps->status.p, 0, 16));
-  s = mk_paged_attention_workspace(desc->n_heads, desc->n_kv_heads, desc->head_dim, &ps->work_bytes);
-  if (s) return s;
-  MK_CUDA(cudaMalloc(&ps->work.p, ps->work_bytes));
-  std::vector<void*> stage(desc->n_layers, ps->staging.p);
-  const mk_kv kv{stage.data(), stage.data()};
-  mk_ctx* c = nullptr;
-  s = create_context(&d, w, &kv, &o, stream, std::move(ps), &c);
-  if (s) return s;
-  std::unique_ptr<mk_ctx> ctx(c);
-  const size_t phases = ctx->scheds.begin()->second->plan.phase_queues.size();
-  if (phases != 2 + 6 * (size_t)d.n_layers) return fail(MK_ERR_INVALID, "schedule: a paged context needs every op's phase");
-  s = init_paged_partials(c);
-  if (s) return s;
-  MK_CUDA(cudaDeviceSynchronize());
-  *out = ctx.release();
-  return MK_OK;
+  return c_entry([&]() -> mk_status {
+    if (!out) return fail(MK_ERR_INVALID, "out is NULL");
+    *out = nullptr;
+    std::string e = check_desc(desc);
+    if (!e.empty()) return fail(MK_ERR_INVALID, e);
+    if (!pages) return fail(MK_ERR_INVALID, "pages is NULL");
+    if (opts && opts->exec_mode != MK_EXEC_PERSISTENT && opts->exec_mode != MK_EXEC_MULTILAUNCH)
+      return fail(MK_ERR_INVALID, "a paged context runs one launch per op");
+    auto ps = std::make_unique<PagedState>();
+    mk_page_view& v = ps->view;
+    v.k = pages->k; v.v = pages->v; v.page_stride = pages->page_stride; v.n_pages = pages->n_pages;
+    v.n_kv_heads = desc->n_kv_heads; v.page_size = pages->page_size; v.head_dim = desc->head_dim; v.dtype = desc->dtype;
+    v.table = pages->table; v.n_rows = pages->n_rows; v.table_width = pages->table_width; v.table_stride = pages->table_stride;
+    e = check_view(&v);
+    if (!e.empty()) return fail(MK_ERR_INVALID, e);
+    if (desc->n_layers > 1 && (pages->layer_stride < v.n_kv_heads * (long long)v.page_size * v.head_dim || pages->layer_stride % 8))
+      return fail(MK_ERR_INVALID, "layer_stride must hold a page and be a multiple of 8");
+    ps->layer_stride = pages->layer_stride;
+    mk_rope_desc plain{};
+    plain.theta = desc->rope_theta;
+    plain.n_rot = desc->head_dim;
+    if (!rope) rope = &plain;
+    if (rope->n_rot > desc->head_dim) return fail(MK_ERR_INVALID, "n_rot must be at most head_dim");
+    if (interleaved != 0 && interleaved != 1) return fail(MK_ERR_INVALID, "interleaved must be 0 or 1");
+    double freqs[64];
+    mk_status s = mk_rope_freqs(rope, freqs, &ps->mscale);
+    if (s) return s;
+    ps->n_freqs = rope->n_rot / 2;
+    ps->interleaved = interleaved;
+    mk_model_desc d = *desc;  // the step kernel's view: a cache of one position
+    d.max_ctx = 1;
+    mk_options o{};
+    if (opts) o = *opts;
+    o.sync_mode = MK_SYNC_COUNTER;
+    o.exec_mode = MK_EXEC_MULTILAUNCH;
+    o.kv_splits = 1;
+    o.attn_merge = 1;
+    o.attn_pool = 0;
+    o.attn_tensor_cores = -1;
+    s = upload(ps->freqs, freqs, sizeof(double) * ps->n_freqs);
+    if (s) return s;
+    MK_CUDA(cudaMalloc(&ps->staging.p, 2ull * desc->max_batch * desc->n_kv_heads * desc->head_dim));
+    MK_CUDA(cudaMalloc(&ps->status.p, 16));
+    MK_CUDA(cudaMemset(ps->status.p, 0, 16));
+    s = mk_paged_attention_workspace(desc->n_heads, desc->n_kv_heads, desc->head_dim, &ps->work_bytes);
+    if (s) return s;
+    MK_CUDA(cudaMalloc(&ps->work.p, ps->work_bytes));
+    std::vector<void*> stage(desc->n_layers, ps->staging.p);
+    const mk_kv kv{stage.data(), stage.data()};
+    mk_ctx* c = nullptr;
+    s = create_context(&d, w, &kv, &o, stream, std::move(ps), &c);
+    if (s) return s;
+    std::unique_ptr<mk_ctx> ctx(c);
+    const size_t phases = ctx->scheds.begin()->second->plan.phase_queues.size();
+    if (phases != 2 + 6 * (size_t)d.n_layers) return fail(MK_ERR_INVALID, "schedule: a paged context needs every op's phase");
+    s = init_paged_partials(c);
+    if (s) return s;
+    MK_CUDA(cudaDeviceSynchronize());
+    *out = ctx.release();
+    return MK_OK;
+  });
 }
 
 mk_status mk_decode_step_paged(mk_ctx* ctx, const int32_t* tok, const int32_t* pos, const int32_t* rows, int B,
                                int32_t* out_tok, float* logits) {
-  if (!ctx) return fail(MK_ERR_INVALID, "ctx is NULL");
-  if (!ctx->paged) return fail(MK_ERR_INVALID, "not a paged context (mk_create_paged)");
-  if (!tok || !pos) return fail(MK_ERR_INVALID, "tok/pos NULL");
-  if (B < 1 || B > ctx->m.max_batch) return fail(MK_ERR_INVALID, "B out of range");
-  if (ctx->broken) return fail(MK_ERR_STATE, "context needs mk_reset after a device error");
-  Sched* sc = nullptr;
-  mk_status s = get_sched(ctx, B, &sc);
-  if (s) return s;
-  const PagedState& ps = *ctx->paged;
-  const ModelShape& m = ctx->m;
-  DevState S = ctx->st;
-  S.trace = ctx->st.trace;
-  S.trace_cap = ctx->st.trace_cap;
-  S.counters = reinterpret_cast<uint32_t*>(sc->counters.p);
-  S.n_counters = sc->plan.n_counters;
-  StepArgs A{};
-  A.epoch = sc->epoch;
-  A.step = ctx->step;
-  A.B = B;
-  A.flags = SF_TOK_FROM_DEVICE | SF_NO_SYNC | (ctx->opts.trace ? SF_TRACE : 0);
-  for (int b = 0; b < B; ++b) A.seq[b] = b;
-  A.logits = logits;
-  A.tok_hist = out_tok;
-  const void* fn = S.tc ? ctx->kernel_tc : ctx->kernel;
-  int32_t* status = reinterpret_cast<int32_t*>(ps.status.p);
-  if (ctx->opts.trace) MK_CUDA(cudaMemsetAsync(&reinterpret_cast<Ctl*>(ctx->ctl.p)->trace_n, 0, 4, ctx->stream));
-  MK_CUDA(cudaMemcpyAsync(reinterpret_cast<Ctl*>(ctx->ctl.p)->tok, tok, sizeof(int32_t) * B, cudaMemcpyDeviceToDevice,
-                          ctx->stream));
-  for (size_t k = 0; k < sc->ph_instr.size(); ++k) {
-    const int l = (int)((k - 1) / 6);
-    if (k > 0 && (k - 1) % 6 == OP_ATTN - OP_QKV && l < m.L) {
-      float* q = S.act + S.act_off[ACT_Q] + l * S.act_stride[ACT_Q];
-      const float* kvn = S.act + S.act_off[ACT_KVN] + l * S.act_stride[ACT_KVN];
-      mk_page_view view = ps.view;
-      view.k = static_cast<uint16_t*>(view.k) + l * ps.layer_stride;
-      view.v = static_cast<uint16_t*>(view.v) + l * ps.layer_stride;
-      mk_append_args ap{};
-      ap.q = q; ap.q_out = q; ap.k = kvn; ap.v = kvn + (size_t)m.Hkv * m.hd;
-      ap.dtype = MK_F32; ap.n_tokens = B; ap.n_heads = m.Hq;
-      ap.q_token = ap.o_token = (long long)m.Hq * m.hd;
-      ap.k_token = ap.v_token = 2LL * m.Hkv * m.hd;
-      ap.q_head = ap.o_head = ap.k_head = ap.v_head = m.hd;
-      ap.positions = pos; ap.rows = rows;
-      ap.freqs = reinterpret_cast<const double*>(ps.freqs.p);
-      ap.n_freqs = ps.n_freqs; ap.interleaved = ps.interleaved; ap.mscale = ps.mscale;
-      s = mk_rope_append(&ap, &view, status, ctx->stream);
-      if (s) return s;
-      mk_attend_args at{};
-      at.q = q; at.dtype = MK_F32; at.n_rows = B; at.n_heads = m.Hq;
-      at.q_row = (long long)m.Hq * m.hd; at.q_head = m.hd;
-      at.out = S.act + S.act_off[ACT_PART] + l * S.act_stride[ACT_PART];  // one split: [row][head][hd + kPartExtra]
-      at.o_row = (long long)m.Hq * (m.hd + kPartExtra); at.o_head = m.hd + kPartExtra;
-      at.lens = pos; at.len_add = 1; at.rows = rows;
-      at.scale = (float)(1.0 / std::sqrt((double)m.hd));
-      at.workspace = ps.work.p; at.workspace_bytes = ps.work_bytes;
-      s = mk_paged_attention(&at, &view, status, ctx->stream);
-      if (s) return s;
-      continue;
-    }
-    StepArgs Ak = A;
-    if (k == 0) Ak.flags |= SF_RESET_ARGMAX;
-    Ak.instr = reinterpret_cast<const Instr*>(sc->ph_instr[k].p);
-    Ak.q_start = reinterpret_cast<const int32_t*>(sc->ph_qstart[k].p);
-    s = launch(ctx, fn, S, Ak, false);
+  return c_entry([&]() -> mk_status {
+    if (!ctx) return fail(MK_ERR_INVALID, "ctx is NULL");
+    if (!ctx->paged) return fail(MK_ERR_INVALID, "not a paged context (mk_create_paged)");
+    if (!tok || !pos) return fail(MK_ERR_INVALID, "tok/pos NULL");
+    if (B < 1 || B > ctx->m.max_batch) return fail(MK_ERR_INVALID, "B out of range");
+    if (ctx->broken) return fail(MK_ERR_STATE, "context needs mk_reset after a device error");
+    Sched* sc = nullptr;
+    mk_status s = get_sched(ctx, B, &sc);
     if (s) return s;
-  }
-  ++sc->epoch;
-  ++ctx->step;
-  ctx->last_B = B;
-  return MK_OK;
+    const PagedState& ps = *ctx->paged;
+    const ModelShape& m = ctx->m;
+    DevState S = ctx->st;
+    S.trace = ctx->st.trace;
+    S.trace_cap = ctx->st.trace_cap;
+    S.counters = reinterpret_cast<uint32_t*>(sc->counters.p);
+    S.n_counters = sc->plan.n_counters;
+    StepArgs A{};
+    A.epoch = sc->epoch;
+    A.step = ctx->step;
+    A.B = B;
+    A.flags = SF_TOK_FROM_DEVICE | SF_NO_SYNC | (ctx->opts.trace ? SF_TRACE : 0);
+    for (int b = 0; b < B; ++b) A.seq[b] = b;
+    A.logits = logits;
+    A.tok_hist = out_tok;
+    const void* fn = S.tc ? ctx->kernel_tc : ctx->kernel;
+    int32_t* status = reinterpret_cast<int32_t*>(ps.status.p);
+    if (ctx->opts.trace) MK_CUDA(cudaMemsetAsync(&reinterpret_cast<Ctl*>(ctx->ctl.p)->trace_n, 0, 4, ctx->stream));
+    MK_CUDA(cudaMemcpyAsync(reinterpret_cast<Ctl*>(ctx->ctl.p)->tok, tok, sizeof(int32_t) * B, cudaMemcpyDeviceToDevice,
+                            ctx->stream));
+    for (size_t k = 0; k < sc->ph_instr.size(); ++k) {
+      const int l = (int)((k - 1) / 6);
+      if (k > 0 && (k - 1) % 6 == OP_ATTN - OP_QKV && l < m.L) {
+        float* q = S.act + S.act_off[ACT_Q] + l * S.act_stride[ACT_Q];
+        const float* kvn = S.act + S.act_off[ACT_KVN] + l * S.act_stride[ACT_KVN];
+        mk_page_view view = ps.view;
+        view.k = static_cast<uint16_t*>(view.k) + l * ps.layer_stride;
+        view.v = static_cast<uint16_t*>(view.v) + l * ps.layer_stride;
+        mk_append_args ap{};
+        ap.q = q; ap.q_out = q; ap.k = kvn; ap.v = kvn + (size_t)m.Hkv * m.hd;
+        ap.dtype = MK_F32; ap.n_tokens = B; ap.n_heads = m.Hq;
+        ap.q_token = ap.o_token = (long long)m.Hq * m.hd;
+        ap.k_token = ap.v_token = 2LL * m.Hkv * m.hd;
+        ap.q_head = ap.o_head = ap.k_head = ap.v_head = m.hd;
+        ap.positions = pos; ap.rows = rows;
+        ap.freqs = reinterpret_cast<const double*>(ps.freqs.p);
+        ap.n_freqs = ps.n_freqs; ap.interleaved = ps.interleaved; ap.mscale = ps.mscale;
+        s = mk_rope_append(&ap, &view, status, ctx->stream);
+        if (s) return s;
+        mk_attend_args at{};
+        at.q = q; at.dtype = MK_F32; at.n_rows = B; at.n_heads = m.Hq;
+        at.q_row = (long long)m.Hq * m.hd; at.q_head = m.hd;
+        at.out = S.act + S.act_off[ACT_PART] + l * S.act_stride[ACT_PART];  // one split: [row][head][hd + kPartExtra]
+        at.o_row = (long long)m.Hq * (m.hd + kPartExtra); at.o_head = m.hd + kPartExtra;
+        at.lens = pos; at.len_add = 1; at.rows = rows;
+        at.scale = (float)(1.0 / std::sqrt((double)m.hd));
+        at.workspace = ps.work.p; at.workspace_bytes = ps.work_bytes;
+        s = mk_paged_attention(&at, &view, status, ctx->stream);
+        if (s) return s;
+        continue;
+      }
+      StepArgs Ak = A;
+      if (k == 0) Ak.flags |= SF_RESET_ARGMAX;
+      Ak.instr = reinterpret_cast<const Instr*>(sc->ph_instr[k].p);
+      Ak.q_start = reinterpret_cast<const int32_t*>(sc->ph_qstart[k].p);
+      s = launch(ctx, fn, S, Ak, false);
+      if (s) return s;
+    }
+    ++sc->epoch;
+    ++ctx->step;
+    ctx->last_B = B;
+    return MK_OK;
+  });
 }
 
 mk_status mk_destroy(mk_ctx* ctx) {

@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <exception>
 #include <string>
 
 #include "../../include/mk.h"
@@ -18,6 +19,22 @@ enum PagedOp : int { PO_APPEND = 1, PO_ATTEND = 2, PO_UPDATE = 3, PO_COMPACT = 4
 inline mk_status paged_fail(mk_status s, const std::string& m) {
   set_last_error(m);
   return s;
+}
+
+// The body of a C entry point: whatever it throws (memory that a descriptor asks for and the
+// host does not have) becomes a status.
+template <typename F>
+inline mk_status c_entry(F&& body) noexcept {
+  try {
+    return body();
+  } catch (const std::exception& e) {
+    try {
+      set_last_error(std::string("host: ") + e.what());
+    } catch (...) {
+    }
+  } catch (...) {
+  }
+  return MK_ERR_INVALID;
 }
 
 inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

@@ -401,52 +401,58 @@ mk_status fill(PoolArgs* a, const mk_page_pool* p, void* ws, size_t ws_bytes, in
 
 extern "C" mk_status mk_update_pages_workspace(int n_rows, int table_width, int n_pages, size_t* bytes) {
   using namespace mk;
-  if (!bytes) return paged_fail(MK_ERR_INVALID, "bytes is NULL");
-  if (n_rows < 1 || n_rows > kMaxRows || table_width < 1 || n_pages < 1)
-    return paged_fail(MK_ERR_INVALID, "n_rows must be in [1, 4096], table_width and n_pages positive");
-  PoolArgs a{};
-  *bytes = lay_out(&a, nullptr, n_rows, table_width, n_pages);
-  return MK_OK;
+  return c_entry([&]() -> mk_status {
+    if (!bytes) return paged_fail(MK_ERR_INVALID, "bytes is NULL");
+    if (n_rows < 1 || n_rows > kMaxRows || table_width < 1 || n_pages < 1)
+      return paged_fail(MK_ERR_INVALID, "n_rows must be in [1, 4096], table_width and n_pages positive");
+    PoolArgs a{};
+    *bytes = lay_out(&a, nullptr, n_rows, table_width, n_pages);
+    return MK_OK;
+  });
 }
 
 extern "C" mk_status mk_update_pages(const mk_update_args* args, const mk_page_pool* pool, int32_t* status, void* stream) {
   using namespace mk;
-  if (!args || !args->lens) return paged_fail(MK_ERR_INVALID, "NULL argument");
-  PoolArgs a{};
-  mk_status s = fill(&a, pool, args->workspace, args->workspace_bytes, status);
-  if (s) return s;
-  a.lens = args->lens;
-  a.parents = args->parents;
-  a.reserve = args->reserve;
-  int n_sm = 0;
-  s = sm_count(&n_sm);
-  if (s) return s;
-  const bool narrow = a.n_rows <= kNarrowThreads;
-  if (narrow && (long long)a.n_rows * a.width <= kCountInPlan) {
-    s = launch_dependent(plan_kernel<kNarrowThreads, kNarrowThreads, true>, dim3(1), dim3(kNarrowThreads), 0, stream,
-                         "mk_update_pages (plan)", a);
-  } else {
-    s = launch_dependent(count_kernel, dim3(a.n_rows), dim3(kRowThreads), 0, stream, "mk_update_pages (count)", a);
+  return c_entry([&]() -> mk_status {
+    if (!args || !args->lens) return paged_fail(MK_ERR_INVALID, "NULL argument");
+    PoolArgs a{};
+    mk_status s = fill(&a, pool, args->workspace, args->workspace_bytes, status);
     if (s) return s;
-    s = launch_dependent(narrow ? plan_kernel<kNarrowThreads, kNarrowThreads, false> : plan_kernel<kWideThreads, kMaxRows, false>,
-                         dim3(1), dim3(narrow ? kNarrowThreads : kWideThreads), 0, stream, "mk_update_pages (plan)", a);
-  }
-  if (s) return s;
-  return launch_dependent(apply_kernel, dim3(n_sm * kCopyCtasPerSm), dim3(kCopyThreads), 0, stream,
-                          "mk_update_pages (apply)", a);
+    a.lens = args->lens;
+    a.parents = args->parents;
+    a.reserve = args->reserve;
+    int n_sm = 0;
+    s = sm_count(&n_sm);
+    if (s) return s;
+    const bool narrow = a.n_rows <= kNarrowThreads;
+    if (narrow && (long long)a.n_rows * a.width <= kCountInPlan) {
+      s = launch_dependent(plan_kernel<kNarrowThreads, kNarrowThreads, true>, dim3(1), dim3(kNarrowThreads), 0, stream,
+                           "mk_update_pages (plan)", a);
+    } else {
+      s = launch_dependent(count_kernel, dim3(a.n_rows), dim3(kRowThreads), 0, stream, "mk_update_pages (count)", a);
+      if (s) return s;
+      s = launch_dependent(narrow ? plan_kernel<kNarrowThreads, kNarrowThreads, false> : plan_kernel<kWideThreads, kMaxRows, false>,
+                           dim3(1), dim3(narrow ? kNarrowThreads : kWideThreads), 0, stream, "mk_update_pages (plan)", a);
+    }
+    if (s) return s;
+    return launch_dependent(apply_kernel, dim3(n_sm * kCopyCtasPerSm), dim3(kCopyThreads), 0, stream,
+                            "mk_update_pages (apply)", a);
+  });
 }
 
 extern "C" mk_status mk_compact_pages(const mk_page_pool* pool, void* workspace, size_t workspace_bytes, int32_t* status,
                                       void* stream) {
   using namespace mk;
-  PoolArgs a{};
-  mk_status s = fill(&a, pool, workspace, workspace_bytes, status);
-  if (s) return s;
-  int n_sm = 0;
-  s = sm_count(&n_sm);
-  if (s) return s;
-  s = launch_dependent(compact_plan_kernel, dim3(1), dim3(kWideThreads), 0, stream, "mk_compact_pages (plan)", a);
-  if (s) return s;
-  return launch_dependent(compact_apply_kernel, dim3(n_sm * kCopyCtasPerSm), dim3(kCopyThreads), 0, stream,
-                          "mk_compact_pages (apply)", a);
+  return c_entry([&]() -> mk_status {
+    PoolArgs a{};
+    mk_status s = fill(&a, pool, workspace, workspace_bytes, status);
+    if (s) return s;
+    int n_sm = 0;
+    s = sm_count(&n_sm);
+    if (s) return s;
+    s = launch_dependent(compact_plan_kernel, dim3(1), dim3(kWideThreads), 0, stream, "mk_compact_pages (plan)", a);
+    if (s) return s;
+    return launch_dependent(compact_apply_kernel, dim3(n_sm * kCopyCtasPerSm), dim3(kCopyThreads), 0, stream,
+                            "mk_compact_pages (apply)", a);
+  });
 }

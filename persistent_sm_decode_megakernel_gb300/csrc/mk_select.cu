@@ -18,6 +18,7 @@ namespace mk {
 namespace {
 
 constexpr int kMaxBeams = 32;
+constexpr float kLargest = 0x1p126f;  // of a logit: beyond it lies infinity
 constexpr int kScanThreads = 256;
 constexpr int kScanWarps = kScanThreads / 32;
 constexpr int kPerSmall = 8, kPerLarge = 16;  // elements of a step per thread: one step of few, or several
@@ -183,16 +184,17 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_cons
       for (int i = 0; i < PER; ++i) w[i % 4] += term_of(x[i], ref);
       q = (w[0] + w[1]) + (w[2] + w[3]);
     };
-    if (fabsf(top) < INFINITY) terms();
-    if (!(fabsf(top) < INFINITY) || q != q) {  // NaN and +inf are reported and count as -inf
+    if (fabsf(top) <= kLargest) terms();
+    if (!(fabsf(top) <= kLargest) || q != q) {  // NaN and +inf are reported and count as -inf
       top = -INFINITY;
       q = 0.f;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        if (!(x[i] < INFINITY)) {
+        if (!(x[i] <= kLargest)) {
           bad = true;
           x[i] = -INFINITY;
         }
+        if (x[i] < -kLargest) x[i] = -INFINITY;
         top = fmaxf(top, x[i]);
       }
       if (top > -INFINITY) terms();
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_cons
         u64 k = 0ull;
         for (int e = tid; e < seen; e += kScanThreads) {
           float y = Conv<T>::up(src[e]);
-          if (!(y < INFINITY)) y = -INFINITY;
+          if (!(y <= kLargest)) y = -INFINITY;
           const u64 z = key_of(y, first + e);
           if (z < last && z > k) k = z;
         }
@@ -475,57 +477,61 @@ mk_status launch_scan(const SelectArgs& a, bool vec, void* stream) {
 
 extern "C" mk_status mk_beam_select_workspace(int groups, int beams, int vocab, size_t* bytes) {
   using namespace mk;
-  if (!bytes) return paged_fail(MK_ERR_INVALID, "bytes is NULL");
-  if (groups < 1 || beams < 1 || beams > kMaxBeams || vocab < beams)
-    return paged_fail(MK_ERR_INVALID, "groups must be positive, beams in [1, 32] and at most vocab");
-  const long long rows = (long long)groups * beams;
-  if (rows * (vocab / kPart + 1) > 0x7fffffffLL)
-    return paged_fail(MK_ERR_INVALID, "groups * beams * vocab out of range");
-  int n_sm = 0;
-  const mk_status s = sm_count(&n_sm);
-  if (s) return s;
-  const int chunk = chunk_of(rows, vocab, n_sm);
-  SelectArgs a{};
-  *bytes = lay_out(&a, nullptr, rows, beams, (int)(((long long)vocab + chunk - 1) / chunk));
-  return MK_OK;
+  return c_entry([&]() -> mk_status {
+    if (!bytes) return paged_fail(MK_ERR_INVALID, "bytes is NULL");
+    if (groups < 1 || beams < 1 || beams > kMaxBeams || vocab < beams)
+      return paged_fail(MK_ERR_INVALID, "groups must be positive, beams in [1, 32] and at most vocab");
+    const long long rows = (long long)groups * beams;
+    if (rows * (vocab / kPart + 1) > 0x7fffffffLL)
+      return paged_fail(MK_ERR_INVALID, "groups * beams * vocab out of range");
+    int n_sm = 0;
+    const mk_status s = sm_count(&n_sm);
+    if (s) return s;
+    const int chunk = chunk_of(rows, vocab, n_sm);
+    SelectArgs a{};
+    *bytes = lay_out(&a, nullptr, rows, beams, (int)(((long long)vocab + chunk - 1) / chunk));
+    return MK_OK;
+  });
 }
 
 extern "C" mk_status mk_beam_select(const mk_select_args* args, int32_t* status, void* stream) {
   using namespace mk;
-  if (!args || !args->logits || !args->scores || !args->ended || !args->out_tokens || !args->out_parents ||
-      !args->out_scores || !args->out_ended)
-    return paged_fail(MK_ERR_INVALID, "NULL argument");
-  if (args->dtype < MK_F16 || args->dtype > MK_F32) return paged_fail(MK_ERR_INVALID, "dtype");
-  if (args->eos < -1 || args->eos >= args->vocab) return paged_fail(MK_ERR_INVALID, "eos must be a token or -1");
-  if (args->row_stride < args->vocab) return paged_fail(MK_ERR_INVALID, "row_stride is smaller than vocab");
-  const size_t esz = args->dtype == MK_F32 ? 4 : 2;
-  if (!aligned_to(args->logits, esz)) return paged_fail(MK_ERR_INVALID, "logits must be aligned to their type");
-  if ((const void*)args->out_scores == (const void*)args->scores || args->out_ended == args->ended)
-    return paged_fail(MK_ERR_INVALID, "outputs must not overlap the inputs");
-  if (!args->workspace || !aligned_to(args->workspace, 16))
-    return paged_fail(MK_ERR_INVALID, "the workspace is missing or unaligned");
-  size_t need = 0;
-  mk_status s = mk_beam_select_workspace(args->groups, args->beams, args->vocab, &need);
-  if (s) return s;
-  if (args->workspace_bytes < need) return paged_fail(MK_ERR_INVALID, "the workspace is too small (mk_beam_select_workspace)");
-  int n_sm = 0;
-  s = sm_count(&n_sm);
-  if (s) return s;
-  SelectArgs a{};
-  a.logits = args->logits; a.scores = args->scores; a.ended = args->ended;
-  a.out_tokens = args->out_tokens; a.out_parents = args->out_parents; a.out_scores = args->out_scores;
-  a.out_ended = args->out_ended; a.status = status;
-  a.row_stride = args->row_stride; a.rows = args->groups * args->beams; a.beams = args->beams; a.vocab = args->vocab;
-  a.chunk = chunk_of(a.rows, a.vocab, n_sm);
-  a.chunks = (int)(((long long)a.vocab + a.chunk - 1) / a.chunk);
-  a.eos = args->eos;
-  a.sum_bits = 62;  // a row's sum, at most vocab, stays below 2^63
-  while ((1LL << (62 - a.sum_bits)) < a.vocab) --a.sum_bits;
-  lay_out(&a, args->workspace, a.rows, a.beams, a.chunks);
-  const bool vec = aligned_to(args->logits, 16) && (args->row_stride * (long long)esz) % 16 == 0;
-  s = args->dtype == MK_F32   ? launch_scan<float>(a, vec, stream)
-      : args->dtype == MK_F16 ? launch_scan<__half>(a, vec, stream)
-                              : launch_scan<__nv_bfloat16>(a, vec, stream);
-  if (s) return s;
-  return launch_dependent(pick_kernel, dim3(args->groups), dim3(32 * args->beams), 0, stream, "mk_beam_select (pick)", a);
+  return c_entry([&]() -> mk_status {
+    if (!args || !args->logits || !args->scores || !args->ended || !args->out_tokens || !args->out_parents ||
+        !args->out_scores || !args->out_ended)
+      return paged_fail(MK_ERR_INVALID, "NULL argument");
+    if (args->dtype < MK_F16 || args->dtype > MK_F32) return paged_fail(MK_ERR_INVALID, "dtype");
+    if (args->eos < -1 || args->eos >= args->vocab) return paged_fail(MK_ERR_INVALID, "eos must be a token or -1");
+    if (args->row_stride < args->vocab) return paged_fail(MK_ERR_INVALID, "row_stride is smaller than vocab");
+    const size_t esz = args->dtype == MK_F32 ? 4 : 2;
+    if (!aligned_to(args->logits, esz)) return paged_fail(MK_ERR_INVALID, "logits must be aligned to their type");
+    if ((const void*)args->out_scores == (const void*)args->scores || args->out_ended == args->ended)
+      return paged_fail(MK_ERR_INVALID, "outputs must not overlap the inputs");
+    if (!args->workspace || !aligned_to(args->workspace, 16))
+      return paged_fail(MK_ERR_INVALID, "the workspace is missing or unaligned");
+    size_t need = 0;
+    mk_status s = mk_beam_select_workspace(args->groups, args->beams, args->vocab, &need);
+    if (s) return s;
+    if (args->workspace_bytes < need) return paged_fail(MK_ERR_INVALID, "the workspace is too small (mk_beam_select_workspace)");
+    int n_sm = 0;
+    s = sm_count(&n_sm);
+    if (s) return s;
+    SelectArgs a{};
+    a.logits = args->logits; a.scores = args->scores; a.ended = args->ended;
+    a.out_tokens = args->out_tokens; a.out_parents = args->out_parents; a.out_scores = args->out_scores;
+    a.out_ended = args->out_ended; a.status = status;
+    a.row_stride = args->row_stride; a.rows = args->groups * args->beams; a.beams = args->beams; a.vocab = args->vocab;
+    a.chunk = chunk_of(a.rows, a.vocab, n_sm);
+    a.chunks = (int)(((long long)a.vocab + a.chunk - 1) / a.chunk);
+    a.eos = args->eos;
+    a.sum_bits = 62;  // a row's sum, at most vocab, stays below 2^63
+    while ((1LL << (62 - a.sum_bits)) < a.vocab) --a.sum_bits;
+    lay_out(&a, args->workspace, a.rows, a.beams, a.chunks);
+    const bool vec = aligned_to(args->logits, 16) && (args->row_stride * (long long)esz) % 16 == 0;
+    s = args->dtype == MK_F32   ? launch_scan<float>(a, vec, stream)
+        : args->dtype == MK_F16 ? launch_scan<__half>(a, vec, stream)
+                                : launch_scan<__nv_bfloat16>(a, vec, stream);
+    if (s) return s;
+    return launch_dependent(pick_kernel, dim3(args->groups), dim3(32 * args->beams), 0, stream, "mk_beam_select (pick)", a);
+  });
 }

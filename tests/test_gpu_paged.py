@@ -646,6 +646,79 @@ def test_select_reports_nan_and_plus_infinity(paged, bad):
     _check_select(got, logits, scores, ended, -1)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_select_wide_ranges(paged, dtype):
+    """Logits of thousands (all but one of the exponentials vanish), all far below zero, and one above 2^126,
+    which is reported."""
+    from persistent_sm_decode_megakernel_gb300 import MkError
+    logits, scores, ended = _select_inputs(3, 3, 3000, dtype)
+    logits[:3] *= 2000
+    logits[3:6] -= 20000
+    _check_select(paged.beam_select(logits, scores, ended), logits, scores, ended, -1)
+    logits[7, 5] = 2e38
+    st = status()
+    got = paged.beam_select(logits, scores, ended, status=st)
+    with pytest.raises(MkError):
+        paged.check_status(st)
+    logits[7, 5] = -math.inf
+    _check_select(got, logits, scores, ended, -1)
+    logits[6:9] = -3e38                       # a row below -2^126: like one at -inf
+    got = paged.beam_select(logits, scores, ended, status=st)
+    paged.check_status(st)
+    logits[6:9] = -math.inf
+    _check_select(got, logits, scores, ended, -1)
+
+
+# ------------------------------------------------------------------------------ refusals
+def test_tensors_that_do_not_fit_are_refused(paged):
+    """Shapes, types, layouts and devices, each refused before anything is enqueued."""
+    from persistent_sm_decode_megakernel_gb300 import MK_ERR_INVALID, MkError
+    pages = torch.zeros(2, 4, 2, 16, 64, dtype=torch.bfloat16, device=DEV)
+    k, v = pages
+    table, lens, pos = ints([[0, 1], [2, 3]]), ints([5, 6]), ints([1, 2])
+    q, kv = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device=DEV), torch.zeros(2, 2, 64, dtype=torch.bfloat16, device=DEV)
+    f = torch.zeros(32, dtype=torch.float64, device=DEV)
+    append = lambda **a: paged.rope_append(**{**dict(q=q, k=kv, v=kv, k_pages=k, v_pages=v, table=table, positions=pos), **a})
+    for bad in (dict(q=q.float()), dict(q=q[:1]), dict(q=q[..., :32]), dict(k=kv[:, :1]), dict(v=kv.half()),
+                dict(k=kv.transpose(1, 2)), dict(positions=pos.long()), dict(positions=pos[:1]), dict(positions=pos.cpu()),
+                dict(rows=pos.float()), dict(freqs=f.float()), dict(freqs=f.cpu()), dict(freqs=f[None]), dict(table=table.long()),
+                dict(table=table[0]), dict(table=table.t()), dict(v_pages=v[:2]), dict(k_pages=k.float(), v_pages=v.float()),
+                dict(k_pages=k.transpose(1, 2), v_pages=v.transpose(1, 2)), dict(q_out=q.float()), dict(q=None, q_out=q),
+                dict(status=torch.zeros(3, dtype=torch.int32, device=DEV)), dict(k=kv.cpu()), dict(k=3), dict(q=[1])):
+        with pytest.raises(ValueError):
+            append(**bad)
+    with pytest.raises(MkError) as e:
+        append(freqs=torch.zeros(33, dtype=torch.float64, device=DEV))
+    assert e.value.status == MK_ERR_INVALID
+    attend_ = lambda **a: paged.paged_attention(**{**dict(q=q, k_pages=k, v_pages=v, table=table, lens=lens), **a})
+    for bad in (dict(q=q[0]), dict(q=q.double()), dict(lens=lens[:1]), dict(lens=lens.long()), dict(out=q.float()),
+                dict(out=q[:1]), dict(rows=lens[:1]), dict(window=2 ** 40), dict(q=q.to_sparse())):
+        with pytest.raises(ValueError):
+            attend_(**bad)
+    for bad in (dict(window=-1), dict(softcap=-2.0), dict(scale=math.nan), dict(q=q[:, :3])):
+        with pytest.raises(MkError):
+            attend_(**bad)
+    refs = ints([1] * 4)
+    update = lambda **a: paged.update_pages(**{**dict(k=k[None], v=v[None], table=table, lens=lens, refs=refs), **a})
+    for bad in (dict(k=k), dict(refs=refs[:3]), dict(lens=lens[:1]), dict(parents=lens.long()), dict(reserve=lens[:1]),
+                dict(v=v[None].half())):
+        with pytest.raises(ValueError):
+            update(**bad)
+    x = torch.zeros(6, 10, device=DEV)
+    s, n = torch.zeros(2, 3, device=DEV), torch.zeros(2, 3, dtype=torch.int32, device=DEV)
+    for bad in ((x[:5], s, n), (x.t(), s, n), (x, s.double(), n), (x, s, n.long()), (x, s[:, :2], n), (x.long(), s, n), (x, s.t(), n)):
+        with pytest.raises(ValueError):
+            paged.beam_select(*bad)
+    with pytest.raises(MkError):
+        paged.beam_select(x[:, :2], s, n)
+    with pytest.raises(MkError):
+        paged.beam_select(x, s, n, eos=10)
+    assert paged.paged_attention(q[:0], k, v, table, lens[:0]).shape == (0, 4, 64)
+    assert paged.rope_append(q[:0], kv[:0], kv[:0], k, v, table, pos[:0]).shape == (0, 4, 64)
+    torch.cuda.synchronize()
+    assert pages.abs().sum() == 0
+
+
 # ------------------------------------------------------------------------------ all of them
 def test_a_beam_search_of_the_four_operators_captured(paged):
     """Steps as a beam search makes them -- reserve and fork, append, attend, select -- eagerly and as one

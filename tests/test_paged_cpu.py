@@ -84,7 +84,7 @@ def test_bad_append_arguments_are_refused(mk, bad):
 
 @pytest.mark.parametrize("bad", [dict(q=None), dict(out=None), dict(lens=None), dict(dtype=3), dict(n_heads=3),
                                  dict(n_heads=0), dict(n_heads=34), dict(n_rows=-1), dict(window=-1), dict(softcap=-1.0),
-                                 dict(softcap=math.nan), dict(scale=math.nan), dict(q=P + 1), dict(workspace=None),
+                                 dict(softcap=math.nan), dict(softcap=math.inf), dict(scale=math.nan), dict(scale=math.inf), dict(q=P + 1), dict(workspace=None),
                                  dict(workspace=P + 4)], ids=str)
 def test_bad_attention_arguments_are_refused(mk, bad):
     assert _attend(mk, _view(mk), **bad) == mk.MK_ERR_INVALID
