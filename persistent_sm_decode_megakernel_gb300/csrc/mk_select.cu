@@ -21,7 +21,9 @@ constexpr int kMaxBeams = 32;
 constexpr float kLargest = 0x1p126f;  // of a logit: beyond it lies infinity
 constexpr int kScanThreads = 256;
 constexpr int kScanWarps = kScanThreads / 32;
-constexpr int kPerSmall = 8, kPerLarge = 16;  // elements of a step per thread: one step of few, or several
+// elements of a step per thread, and CTAs per SM: one short step, or several long ones (a step
+// costs about 90 instructions beside its 6 per element)
+constexpr int kPerSmall = 8, kCtasSmall = 4, kPerLarge = 32, kCtasLarge = 2;
 constexpr int kList = 1024;               // entries of a CTA's list
 
 using u64 = unsigned long long;
@@ -85,7 +87,7 @@ __device__ __forceinline__ Pair two_sum(float x, float y) {
 // t = (f - 1) / (f + 1), |t| < 0.18.  The leading term is taken in pairs, the others (below
 // 0.004) in 32 bits: off by less than 2^-30 and the pair's own rounding.
 __device__ __forceinline__ Pair ln_of(u64 u, float shift) {
-  const int z = __clzll((long long)u);
+  const int z = __clzll((long long)(u | 1));
   const u64 m = u << z;                     // the leading bit on top
   const bool half = (m >> 48) > 0xB504u;    // f above sqrt 2: take f / 2
   const float unit = half ? 0x1p-24f : 0x1p-23f;
@@ -93,7 +95,9 @@ __device__ __forceinline__ Pair ln_of(u64 u, float shift) {
   const float e = (float)(63 - z + (half ? 1 : 0)) + shift;
   const float nh = fh - 1.f;                // exact
   const Pair den = two_sum(fh, 1.f);
-  const float inv = 1.f / den.hi, th = nh * inv;
+  float inv;  // approximate: what it leaves over goes into tl
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(den.hi));
+  const float th = nh * inv;
   const float tl = (fmaf(-th, den.hi, nh) + (fl - th * (den.lo + fl))) * inv;
   const float w = th * th;
   const float rest = w * fmaf(w, fmaf(w, fmaf(w, fmaf(w, fmaf(w, 2.f / 13, 2.f / 11), 2.f / 9), 2.f / 7), 2.f / 5), 2.f / 3);
@@ -120,7 +124,7 @@ __device__ __forceinline__ u64 ordered(Pair p) { return (u64)orderable(p.hi + 0.
 // and from there on whole numbers.  Bound: the logits' bytes for many rows (the arithmetic, one
 // exponential each, is most of that time again), the launch and the block steps for few.
 template <typename T, bool VEC, int PER>
-__global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_constant__ SelectArgs a) {
+__global__ void __launch_bounds__(kScanThreads, PER == kPerLarge ? kCtasLarge : kCtasSmall) scan_kernel(const __grid_constant__ SelectArgs a) {
   __shared__ u64 s_list[kList], s_warp[kScanWarps];
   __shared__ float s_f[kScanWarps];
   __shared__ int s_n;
@@ -333,18 +337,16 @@ __device__ __forceinline__ void take_best(u64 (&k)[8], int K, int lane, u64* bes
 #pragma unroll
   for (int x = 0; x < R; ++x) top = k[x] > top ? k[x] : top;
   u64 mine = 0ull;
-  for (int q = 0; q < K; ++q) {
+#pragma unroll 1
+  for (int q = 0; q < K; ++q) {  // (without branches: twice as fast)
     const u64 win = warp_max(top);
-    if (win == 0ull) break;
-    if (lane == q) mine = win;
-    if (top == win) {
-      carry = carry == win ? 0ull : carry;
-      top = carry;
+    mine = lane == q ? win : mine;
+    carry = carry == win ? 0ull : carry;
+    top = carry;
 #pragma unroll
-      for (int x = 0; x < R; ++x) {
-        k[x] = k[x] == win ? 0ull : k[x];
-        top = k[x] > top ? k[x] : top;
-      }
+    for (int x = 0; x < R; ++x) {
+      k[x] = k[x] == win ? 0ull : k[x];
+      top = k[x] > top ? k[x] : top;
     }
   }
   *best = mine;
@@ -352,108 +354,106 @@ __device__ __forceinline__ void take_best(u64 (&k)[8], int K, int lane, u64* bes
 
 // One CTA per group, a warp per beam: the beam's best from its parts' lists (8 keys per lane
 // in registers, the best so far carried from batch to batch), its lse, and its candidates'
-// scores as pairs of floats, compared as ordered integers; then every candidate's place among the group's
-// is the number of the other beams' candidates ahead of it.  Bound:
-// one chain of loads, the logarithm and the list steps, each instruction waiting for the last.
+// scores as pairs of floats, compared as ordered integers; then the beams' lists, each sorted,
+// are merged, a lane per beam.  Bound: one chain of loads, the logarithm and the list steps,
+// each instruction waiting for the last.  Every warp goes through all of it, ended beam or not:
+// inside a branch that the compiler cannot see to be the same for a whole warp, a shuffle took
+// 285 cycles and a reduction 700, in place of 17 and 22 (the kernel 9500, in place of 3500).
 __global__ void __launch_bounds__(32 * kMaxBeams) pick_kernel(const __grid_constant__ SelectArgs a) {
   __shared__ u64 s_key[kMaxBeams][kMaxBeams];
   __shared__ float s_score[kMaxBeams][kMaxBeams];
   __shared__ int s_token[kMaxBeams][kMaxBeams], s_len[kMaxBeams], s_ended[kMaxBeams];
-  const int tid = threadIdx.x, lane = tid & 31, b = tid >> 5, group = blockIdx.x, K = a.beams;
+  const int lane = threadIdx.x & 31, b = threadIdx.x >> 5, group = blockIdx.x, K = a.beams;
+  const int row = group * K + b, total = a.chunks * K;
+  const Stat* st = a.stat + (long long)row * a.chunks;
+  const u64* cand = a.cand + (long long)row * total;
   pdl_wait();
   pdl_launch();
-  {
-    const int row = group * K + b, total = a.chunks * K;
-    const Stat* st = a.stat + (long long)row * a.chunks;
-    const u64* cand = a.cand + (long long)row * total;
-    // everything the beam needs is asked for at once (of an ended one nothing was written,
-    // and nothing is used)
-    const int ended = a.ended[row];
-    float sc = a.scores[row];
-    Stat part{-INFINITY, 0.f, 0ull};
-    u64 k[8];
-    if (lane < a.chunks) part = st[lane];
-    k[0] = lane < total ? cand[lane] : 0ull;
-    k[1] = 32 + lane < total ? cand[32 + lane] : 0ull;
-    if (total > 64) {
+  // everything the beam needs is asked for at once (of an ended one nothing was written, and
+  // what is computed from that is not used)
+  const int ended = a.ended[row];
+  float sc = a.scores[row];
+  Stat part{-INFINITY, 0.f, 0ull};
+  if (lane < a.chunks) part = st[lane];
+  u64 k[8];
+  k[0] = lane < total ? cand[lane] : 0ull;
+  k[1] = 32 + lane < total ? cand[32 + lane] : 0ull;
+  if (total > 64) {
 #pragma unroll
-      for (int x = 2; x < 8; ++x) k[x] = x * 32 + lane < total ? cand[x * 32 + lane] : 0ull;
-    }
-    if (!(sc < INFINITY)) {
-      if (lane == 0) report(a.status, MK_ERR_NAN, PO_SELECT, row, -1);
-      sc = -INFINITY;
-    }
-    if (lane == 0) {
-      s_len[b] = ended ? 1 : K;
-      s_ended[b] = ended;
-    }
-    if (ended) {
-      if (lane == 0) {
-        s_score[b][0] = sc;
-        s_key[b][0] = ordered(Pair{sc, 0.f});
-        s_token[b][0] = a.eos;
-      }
-    } else {
-      // the parts' sums against the largest power: whole numbers, shifted
-      float ref = part.n;
-      for (int c = lane + 32; c < a.chunks; c += 32) ref = fmaxf(ref, st[c].n);
-      ref = value_of((u64)__reduce_max_sync(0xffffffffu, orderable(ref)) << 32);
-      u64 sum = 0;
-      for (int c = lane; c < a.chunks; c += 32) {
-        if (c >= 32) part = st[c];
-        if (part.n > ref - 64.f) sum += part.sum >> (int)(ref - part.n);
-      }
+    for (int x = 2; x < 8; ++x) k[x] = x * 32 + lane < total ? cand[x * 32 + lane] : 0ull;
+  }
+  const bool no_score = !(sc < INFINITY);
+  sc = no_score ? -INFINITY : sc;
+  // the parts' sums against the largest power: whole numbers, shifted
+  float ref = part.n;
+  for (int c = 32; c < a.chunks; c += 32) ref = fmaxf(ref, c + lane < a.chunks ? st[c + lane].n : -INFINITY);
+  ref = value_of((u64)__reduce_max_sync(0xffffffffu, orderable(ref)) << 32);
+  auto share = [&](const Stat& s) { return s.n > ref - 64.f ? s.sum >> (int)(ref - s.n) : 0ull; };
+  u64 sum = share(part);
+  for (int c = 32; c < a.chunks; c += 32) sum += share(c + lane < a.chunks ? st[c + lane] : Stat{-INFINITY, 0.f, 0ull});
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      const Pair lse = ref > -INFINITY ? ln_of(sum, ref - (float)a.sum_bits) : Pair{0.f, 0.f};
-      u64 mine = 0ull;  // lane q: the q-th best
-      if (total <= 32)
-        take_best<1>(k, K, lane, &mine);
-      else if (total <= 64)
-        take_best<2>(k, K, lane, &mine);
-      else
-        for (int base = 0; base < total; base += 256) {
-          if (base) {
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const Pair lse = ln_of(sum, ref - (float)a.sum_bits);
+  u64 mine = 0ull;  // lane q: the q-th best
+  if (total <= 64)
+    take_best<2>(k, K, lane, &mine);
+  else
+    for (int base = 0; base < total; base += 256) {
+      if (base) {
 #pragma unroll
-            for (int x = 0; x < 8; ++x) k[x] = base + x * 32 + lane < total ? cand[base + x * 32 + lane] : 0ull;
-          }
-          take_best<8>(k, K, lane, &mine);
-        }
-      if (lane < K) {
-        const float v = value_of(mine);
-        const Pair s = v > -INFINITY && sc > -INFINITY ? score_of(sc, v, lse) : Pair{-INFINITY, 0.f};
-        s_score[b][lane] = s.hi;
-        s_key[b][lane] = ordered(s);
-        s_token[b][lane] = token_of(mine);
+        for (int x = 0; x < 8; ++x) k[x] = base + x * 32 + lane < total ? cand[base + x * 32 + lane] : 0ull;
       }
+      take_best<8>(k, K, lane, &mine);
     }
+  if (lane < K) {
+    const float v = value_of(mine);
+    Pair s = ref > -INFINITY && v > -INFINITY && sc > -INFINITY ? score_of(sc, v, lse) : Pair{-INFINITY, 0.f};
+    if (ended) s = Pair{sc, 0.f};
+    s_score[b][lane] = s.hi;
+    s_key[b][lane] = ordered(s);
+    s_token[b][lane] = ended ? a.eos : token_of(mine);
+  }
+  if (lane == 0) {
+    s_len[b] = ended ? 1 : K;
+    s_ended[b] = ended;
+    if (no_score) report(a.status, MK_ERR_NAN, PO_SELECT, row, -1);
   }
   __syncthreads();
-  if (lane >= s_len[b]) return;
-  const u64 key = s_key[b][lane];
-  int place = lane;
-  for (int o = 0; o < K; ++o) {
-    if (o == b) continue;
-    // of beam o's, ahead are those larger, or as large and of a lower beam
-    const u64 least = key + (o < b ? 0 : 1);
-    const int len = s_len[o];
-#pragma unroll 4
-    for (int e = 0; e < len; ++e) place += s_key[o][e] >= least;
+  // lane o holds beam o's best that is not yet taken (every warp alike)
+  u64 head = lane < K ? s_key[lane][0] : 0ull;
+  int next = 1, from = 0, entry = 0;
+  const int len = lane < K ? s_len[lane] : 0;
+#pragma unroll 1
+  for (int q = 0; q < K; ++q) {
+    const u64 win = warp_max(head);
+    const int who = __ffs(__ballot_sync(0xffffffffu, head == win)) - 1;  // ties: the lowest beam
+    const int taken = __shfl_sync(0xffffffffu, next, who) - 1;
+    from = lane == q ? who : from;
+    entry = lane == q ? taken : entry;
+    if (lane == who) {
+      head = next < len ? s_key[lane][next] : 0ull;
+      ++next;
+    }
   }
-  if (place >= K) return;
-  const int out = group * K + place, token = s_token[b][lane];
-  a.out_tokens[out] = token;
-  a.out_parents[out] = group * K + b;
-  a.out_scores[out] = s_score[b][lane];
-  a.out_ended[out] = (s_ended[b] != 0 || token == a.eos) ? 1 : 0;
+  if (b == 0 && lane < K) {
+    const int out = group * K + lane, token = s_token[from][entry];
+    a.out_tokens[out] = token;
+    a.out_parents[out] = group * K + from;
+    a.out_scores[out] = s_score[from][entry];
+    a.out_ended[out] = (s_ended[from] != 0 || token == a.eos) ? 1 : 0;
+  }
 }
 
-// Elements of a CTA's part of a row: the rows' parts fill the resident CTAs (4 per SM) once,
-// in whole groups of accesses (2048), and down to one group per CTA when there are few rows.
+// Elements of a CTA's part of a row: the rows' parts fill the resident CTAs once -- of long steps
+// when a part is then longer than one of their steps, else of one short step each (2048
+// elements), so that few rows still spread over many SMs.
 constexpr int kPart = kPerSmall * kScanThreads;
 int chunk_of(long long rows, int vocab, int n_sm) {
-  const long long parts = std::max(1LL, 4LL * n_sm / rows), each = ((long long)vocab + parts - 1) / parts;
-  return (int)std::min((each + kPart - 1) / kPart * kPart, 1LL << 30);
+  const long long parts = std::max(1LL, (long long)kCtasLarge * n_sm / rows), each = ((long long)vocab + parts - 1) / parts;
+  if (each > kPerLarge * kScanThreads) return (int)std::min((each + kPart - 1) / kPart * kPart, 1LL << 30);
+  const long long most = std::max(1LL, (long long)kCtasSmall * n_sm / rows);
+  const long long one = ((long long)vocab + most - 1) / most;
+  return one <= kPart ? kPart : (int)((one + kPart - 1) / kPart * kPart);
 }
 
 size_t lay_out(SelectArgs* a, void* ws, long long rows, int beams, int chunks) {
