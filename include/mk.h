@@ -401,7 +401,9 @@ mk_status mk_rope_append(const mk_append_args* args, const mk_page_view* cache, 
  * them reported (MK_ERR_PAGES).  A query that is not of the cache's type must lie within
  * the cache type's range.  A NaN or infinite value inside the range makes that row's results
  * NaN or infinite, as does a NaN key; an infinite key does, unless the query is of the
- * cache's type and the scores stay below +inf.  Results do not depend on timing. */
+ * cache's type and the scores stay below +inf.  Results do not depend on timing.
+ * n_rows * n_kv_heads * (positions / 16 + 9) must be below 2^31 - 2^24, positions being the
+ * table's width in positions or the window + 16, if that is less. */
 typedef struct {
   const void* q;           /* [n_rows][n_heads][head_dim], element strides below            */
   void* out;

@@ -7,6 +7,9 @@
 // in one CTA is finished there; the pieces of one that spans CTAs go to the workspace as
 // (running maximum, sum, weighted values) and a second small kernel joins them in order:
 //   M = max M_i,  L = sum L_i 2^(M_i - M),  out = sum O_i 2^(M_i - M) / L.
+#include <algorithm>
+#include <type_traits>
+
 #include "mk_internal.h"
 #include "mk_device.cuh"
 #include "mk_paged.cuh"
@@ -33,10 +36,11 @@ struct AttendArgs {
   const int32_t *lens, *rows, *table;
   int32_t* status;
   long long q_row, q_head, o_row, o_head, page_stride, table_stride;
-  int n_rows, hq, hkv, group, len_add, window, page_size, n_pages, table_rows, width;
+  int n_rows, hq, hkv, group, len_add, window, page_size, n_pages, table_rows, cap;  // cap: positions of a table row
   int tpp;                              // tiles per page
   unsigned tpp_inverse;                 // 2^32 / tpp, rounded up
   int n_cta;
+  int q_vec;                            // q in accesses of 16 bytes
   int by_segment;                       // joins[row * hkv + kv head] (they fit), else joins[first CTA]
   float scale, softcap;                 // scores to units of log 2: scale s, or softcap tanh(scale s)
 };
@@ -45,23 +49,45 @@ struct AttendArgs {
 struct Span {
   int lo, hi, t0, n, trow;
 };
-__device__ __forceinline__ Span span_of(const AttendArgs& a, int r, bool tell) {
+__device__ __forceinline__ int length_of(const AttendArgs& a, int r) {
+  int len;
+  asm("add.sat.s32 %0, %1, %2;" : "=r"(len) : "r"(a.lens[r]), "r"(a.len_add));
+  return len;
+}
+__device__ __forceinline__ Span span_of(const AttendArgs& a, int r) {
   Span s;
   s.trow = a.rows ? a.rows[r] : r;
-  long long len = (long long)a.lens[r] + a.len_add;
-  const long long cap = (long long)a.width * a.page_size;
-  if ((unsigned)s.trow >= (unsigned)a.table_rows) {
-    if (tell && len > 0) report(a.status, MK_ERR_PAGES, PO_ATTEND, r, s.trow);
-    len = 0;
-  }
-  if (tell && len > cap) report(a.status, MK_ERR_PAGES, PO_ATTEND, r, (int)min(len, 0x7fffffffLL));
+  const int len = (unsigned)s.trow < (unsigned)a.table_rows ? max(0, length_of(a, r)) : 0;
   // the window counts from the row's own end, also where the table ends earlier
-  const long long lo = a.window > 0 ? max(0LL, len - a.window) : 0LL;
-  s.hi = (int)max(0LL, min(len, cap));
-  s.lo = (int)min(lo, (long long)s.hi);
+  s.hi = min(len, a.cap);
+  s.lo = a.window > 0 ? min(max(0, len - a.window), s.hi) : 0;
   s.t0 = s.lo / kTile;
   s.n = s.hi > s.lo ? (s.hi + kTile - 1) / kTile - s.t0 : 0;
   return s;
+}
+// Rows that have no row of the table, and lengths beyond it, are reported.
+__device__ __noinline__ void check_rows(const AttendArgs& a) {
+  for (int r = threadIdx.x; r < a.n_rows; r += kAttThreads) {
+    const int len = length_of(a, r), trow = a.rows ? a.rows[r] : r;
+    if ((unsigned)trow >= (unsigned)a.table_rows) {
+      if (len > 0) report(a.status, MK_ERR_PAGES, PO_ATTEND, r, trow);
+    } else if (len > a.cap) {
+      report(a.status, MK_ERR_PAGES, PO_ATTEND, r, len);
+    }
+  }
+}
+// Rows without positions: zeros.
+template <typename Q>
+__device__ __noinline__ void fill_rows(const AttendArgs& a, int hd) {
+  for (int r = blockIdx.x; r < a.n_rows; r += gridDim.x) {
+    if (span_of(a, r).n != 0) continue;
+    for (int x = threadIdx.x; x < a.hq * hd; x += kAttThreads)
+      static_cast<Q*>(a.out)[(long long)r * a.o_row + (long long)(x / hd) * a.o_head + x % hd] = Conv<Q>::down(0.f);
+    for (int h = threadIdx.x; h < a.hq; h += kAttThreads) {
+      if (a.lse) a.lse[(long long)r * a.hq + h] = -INFINITY;
+      if (a.by_segment && h < a.hkv) a.joins[r * a.hkv + h] = make_int4(0, -1, 0, 0);
+    }
+  }
 }
 
 // The line of work, in units: every segment counts its tiles and `lead` units in front of them
@@ -71,33 +97,39 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int r, bool tell) {
 //   lead: with fewer tiles than the wave's warps the latency of a piece is all there is, and
 //     equal tiles are best; else kLead, without which a CTA that meets a dozen segments of two
 //     tiles each ran twice as long as the others (61 ragged rows of up to 700 positions).
+//   pitch: the units of every segment, its lead being what its tiles leave, so that each is
+//     whole in a CTA of its own; 0: n + lead.  Taken when there is a CTA for each and the longest is
+//     no longer than an equal share and the lead that a second piece would add (61 ragged rows
+//     of up to 700 positions: 14.5 us, in equal shares 15.6).
 constexpr int kLead = 8;
 struct Line {
-  long long units, share;
-  int lead;
+  int units, share, lead, pitch;
+  bool gaps;  // rows without positions
 };
-__device__ __forceinline__ long long row_units(const AttendArgs& a, int n, int lead) {
-  return n > 0 ? (long long)(n + lead) * a.hkv : 0LL;
+__device__ __forceinline__ int segment_units(int n, int lead, int pitch) { return pitch ? pitch : n + lead; }
+__device__ __forceinline__ int row_units(const AttendArgs& a, int n, int lead, int pitch) {
+  return n > 0 ? segment_units(n, lead, pitch) * a.hkv : 0;
 }
 // The line, and in *row and *before (shared memory; the caller syncs) the row that holds this
-// CTA's first unit and the units before it.
-__device__ __forceinline__ Line find_row(const AttendArgs& a, long long (*sums)[2], int* row, long long* before) {
+// CTA's first unit and the units before it.  What stands before the first load is as short as
+// it can be, all of it in 32 bits (the host refuses longer lines): executed once, it waits for
+// its instructions, 7 cycles for each.
+__device__ __forceinline__ Line find_row(const AttendArgs& a, int (*sums)[3], int* row, int* before) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.n_rows + kAttThreads - 1) / kAttThreads;
   const int r0 = min(a.n_rows, tid * per), r1 = min(a.n_rows, r0 + per);
-  long long tiles = 0;
-  int rows = 0;  // with positions
+  int tiles = 0, rows = 0, most = 0;  // rows: with positions; most: the longest
   for (int r = r0; r < r1; ++r) {
-    const int n = span_of(a, r, blockIdx.x == 0).n;
+    const int n = span_of(a, r).n;
     tiles += n;
     rows += n > 0;
+    most = max(most, n);
   }
-  long long ti = tiles;
-  int ri = rows;
+  int ti = tiles, ri = rows;
+  most = __reduce_max_sync(0xffffffffu, most);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, ti, o);
-    const int y = __shfl_up_sync(0xffffffffu, ri, o);
+    const int x = __shfl_up_sync(0xffffffffu, ti, o), y = __shfl_up_sync(0xffffffffu, ri, o);
     if (lane >= o) {
       ti += x;
       ri += y;
@@ -106,27 +138,39 @@ __device__ __forceinline__ Line find_row(const AttendArgs& a, long long (*sums)[
   if (lane == 31) {
     sums[warp][0] = ti;
     sums[warp][1] = ri;
+    sums[warp][2] = most;
   }
   __syncthreads();
-  long long all_tiles = 0, all_rows = 0;
+  ti -= tiles;  // before this thread's rows
+  ri -= rows;
+  int all_tiles = 0, all_rows = 0;
 #pragma unroll
   for (int w = 0; w < kAttWarps; ++w) {
-    if (w == warp) {
-      ti += all_tiles - tiles;  // before this thread's rows
-      ri += (int)all_rows - rows;
-    }
-    all_tiles += sums[w][0];
-    all_rows += sums[w][1];
+    const int x = sums[w][0], y = sums[w][1];
+    ti += w < warp ? x : 0;
+    ri += w < warp ? y : 0;
+    all_tiles += x;
+    all_rows += y;
+    most = max(most, sums[w][2]);
   }
   Line l;
-  l.lead = all_tiles * a.hkv <= (long long)a.n_cta * kAttWarps ? 0 : kLead;
-  l.units = (all_tiles + all_rows * l.lead) * a.hkv;
-  l.share = max((long long)kAttWarps, (l.units + a.n_cta - 1) / a.n_cta);
-  const long long at = l.share * blockIdx.x;
-  long long b = (ti + (long long)ri * l.lead) * a.hkv;
-  if (at >= b && at < b + (tiles + (long long)rows * l.lead) * a.hkv)
+  const int segments = all_rows * a.hkv;
+  l.lead = all_tiles * a.hkv <= a.n_cta * kAttWarps ? 0 : kLead;
+  l.units = all_tiles * a.hkv + segments * l.lead;
+  l.share = max(kAttWarps, (int)((unsigned)(l.units + a.n_cta - 1) / (unsigned)a.n_cta));
+  l.gaps = all_rows < a.n_rows;
+  l.pitch = 0;
+  if (l.lead && segments <= a.n_cta && most <= l.share + kLead) {
+    l.pitch = most;
+    l.share = most;
+    l.units = segments * most;
+  }
+  auto units = [&](int tiles, int rows) { return (l.pitch ? rows * l.pitch : tiles + rows * l.lead) * a.hkv; };
+  const int at = min(l.units, l.share * (int)blockIdx.x);  // (n_cta shares pass the line by less than 2^20)
+  int b = units(ti, ri);
+  if (at >= b && at < b + units(tiles, rows))
     for (int r = r0; r < r1; ++r) {
-      const long long n = row_units(a, per == 1 ? (int)tiles : span_of(a, r, false).n, l.lead);
+      const int n = row_units(a, per == 1 ? tiles : span_of(a, r).n, l.lead, l.pitch);
       if (at >= b && at < b + n) {
         *row = r;
         *before = b;
@@ -170,6 +214,11 @@ constexpr float kProbShift = 0.f;
 template <>
 constexpr float kProbShift<__half> = 14.f;
 
+// four bytes from global to shared memory, without a register between
+__device__ __forceinline__ void cp_async4(int* dst, const int* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+
 // 2^x by the hardware's approximation (2 ulp; results below the normal range become 0)
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -180,9 +229,11 @@ __device__ __forceinline__ float ex2(float x) {
 // Shared memory of the kernel: the query as A fragments [part][32-dim chunk][32 lanes][16 B]
 // (WIDE: [part][chunk][2 row halves][32 lanes]), then the warps' partials for the CTA's merge.
 struct AttState {
-  long long at, end, share, before;  // next unit, end of the CTA's units, share; units before `row`
-  long long sums[kAttWarps][2];
-  int row, head, slot, lead, bad, bad_page;
+  const int32_t* table;        // the row's pages
+  int at, end, share, before;  // next unit, end of the CTA's units, share; units before `row`
+  int sums[kAttWarps][3];
+  int row, head, slot, lead, pitch, bad, bad_page;
+  int pages[kAttWarps][64];    // of a warp's tiles: the k-th one's at k mod 64
 };
 template <int HD, bool WIDE, int NQ>
 struct AttSmem {
@@ -209,12 +260,10 @@ struct AttSmem {
 // So every load is 16 bytes, a warp's rows are read in whole 64- and 128-byte runs, no
 // barrier stands between the loads and the products, and the warps of an SM hide each
 // other's latency.
-//
-// A warp takes NT tiles at a time: with 64 dims two, so that as many bytes are in flight.
 template <typename C, typename Q, int HD, bool WIDE, int NQ, int NP>
 __global__ void __launch_bounds__(kAttThreads, ctas_per_sm(HD)) attend_kernel(const __grid_constant__ AttendArgs a) {
   using SM = AttSmem<HD, WIDE, NQ>;
-  constexpr int CH = HD / 32, VH = HD / 64, HEADS = SM::kHeads, ROW = SM::kRow, NT = 1;
+  constexpr int CH = HD / 32, VH = HD / 64, HEADS = SM::kHeads, ROW = SM::kRow;
   constexpr int RH = WIDE ? 2 : 1;  // row halves that are heads of their own
   extern __shared__ __align__(16) unsigned char att_smem[];
   uint4* s_q = reinterpret_cast<uint4*>(att_smem);
@@ -225,46 +274,39 @@ __global__ void __launch_bounds__(kAttThreads, ctas_per_sm(HD)) attend_kernel(co
   pdl_wait();
   pdl_launch();
   const Line line = find_row(a, st->sums, &st->row, &st->before);
-  // rows without positions: zeros
-  for (int r = blockIdx.x; r < a.n_rows; r += gridDim.x) {
-    if (span_of(a, r, false).n != 0) continue;
-    for (int x = tid; x < a.hq * HD; x += kAttThreads)
-      static_cast<Q*>(a.out)[(long long)r * a.o_row + (long long)(x / HD) * a.o_head + x % HD] = Conv<Q>::down(0.f);
-    for (int h = tid; h < a.hq; h += kAttThreads) {
-      if (a.lse) a.lse[(long long)r * a.hq + h] = -INFINITY;
-      if (a.by_segment && h < a.hkv) a.joins[r * a.hkv + h] = make_int4(0, -1, 0, 0);
-    }
-  }
+  if (blockIdx.x == gridDim.x - 1) check_rows(a);
+  if (line.gaps) fill_rows<Q>(a, HD);
   if (tid == 0 && !a.by_segment) a.joins[blockIdx.x] = make_int4(0, -1, 0, 0);
-  if (line.share * blockIdx.x >= line.units) return;
-  __syncthreads();
+  const int begin = line.share * (int)blockIdx.x;
+  if (begin >= line.units) return;
   // what a piece needs again at its end lives in shared memory: the loop over the tiles has
   // few registers to spare
   if (tid == 0) {
-    st->at = line.share * blockIdx.x;
-    st->end = min(line.units, line.share * (blockIdx.x + 1LL));
+    st->at = begin;
+    st->end = min(line.units, begin + line.share);
     st->share = line.share;
     st->lead = line.lead;
+    st->pitch = line.pitch;
     st->bad = 0;
   }
   __syncthreads();
   while (true) {
     int base, cnt, mine, lo, hi;  // this warp's tiles: base, + kAttWarps, ...
-    const int32_t* trow;
     {
-      long long rbase = st->before, at = st->at, seg;  // seg: the segment's first unit
-      int r = st->row, j, first;
+      int rbase = st->before, at = st->at, seg;  // seg: the segment's first unit
+      int r = st->row, j, first, each;
       Span sp;
       while (true) {
-        sp = span_of(a, r, false);
-        const long long n = row_units(a, sp.n, st->lead);
+        sp = span_of(a, r);
+        const int n = row_units(a, sp.n, st->lead, st->pitch);
         if (at < rbase + n) {
-          const int each = sp.n + st->lead;
-          j = (int)((at - rbase) / each);
-          seg = rbase + (long long)j * each;
-          const long long stop = min(st->end, seg + each);
-          first = (int)max(0LL, at - seg - st->lead);
-          cnt = (int)(stop - seg - st->lead) - first;  // tiles of this piece
+          each = segment_units(sp.n, st->lead, st->pitch);
+          const int lead = each - sp.n;
+          j = (int)((unsigned)(at - rbase) / (unsigned)each);
+          seg = rbase + j * each;
+          const int stop = min(st->end, seg + each);
+          first = max(0, at - seg - lead);
+          cnt = stop - seg - lead - first;  // tiles of this piece
           at = stop;
           if (cnt > 0 || at >= st->end) break;  // (no tiles: of a segment's lead alone)
         } else {
@@ -279,9 +321,10 @@ __global__ void __launch_bounds__(kAttThreads, ctas_per_sm(HD)) attend_kernel(co
         st->row = r;
         st->before = rbase;
         st->head = j;
+        st->table = a.table + (long long)sp.trow * a.table_stride;
         st->slot = whole ? 2 : first == 0;  // 0: continues a segment, 1: begins one, 2: is one
         if (first == 0) {  // the segment's begin knows where it ends
-          const int last = (int)((seg + st->lead + sp.n - 1) / st->share);
+          const int last = (int)((unsigned)(seg + each - 1) / (unsigned)st->share);
           if (a.by_segment)
             a.joins[r * a.hkv + j] = whole ? make_int4(0, -1, 0, 0) : make_int4(blockIdx.x, last, r, j);
           else if (!whole)
@@ -293,73 +336,89 @@ __global__ void __launch_bounds__(kAttThreads, ctas_per_sm(HD)) attend_kernel(co
       mine = cnt > warp ? (cnt - warp + kAttWarps - 1) / kAttWarps : 0;
       lo = sp.lo;
       hi = sp.hi;
-      trow = a.table + (long long)sp.trow * a.table_stride;
     }
     __syncthreads();
-    // lane i holds the page of this warp's (32 b + i)-th tile; the next 32 are fetched ahead
-    auto page_of = [&](int k) -> int { return k < mine ? trow[page_index(a, base + k * kAttWarps)] : -1; };
-    int pages = page_of(lane), pages_next = -1;
-    // the query's fragments: chunk i, lane (g, c): dims [32 i + 8 c, + 8) of head g
-#pragma unroll 1
-    for (int y = tid; y < CH * HEADS * 4; y += kAttThreads) {
-      const int h = (y >> 2) % HEADS, i = y / (4 * HEADS);
+    // the pages of this warp's first 32 tiles; from then on the next 32 are fetched ahead
+    int* pages = st->pages[warp];
+    auto entry = [&](int k) { return st->table + page_index(a, base + k * kAttWarps); };
+    const int page0 = lane < mine ? *entry(lane) : -1;
+    // the query's fragments: chunk i, lane (g, c): dims [32 i + 8 c, + 8) of head g.  Asked for
+    // here, stored behind the first keys' loads, which need not wait for them.
+    constexpr int kAsk = CH * HEADS * 4 / kAttThreads > 0 ? CH * HEADS * 4 / kAttThreads : 1;
+    Raw8<Q> ask[kAsk];
+#pragma unroll
+    for (int z = 0; z < kAsk; ++z) {
+      const int y = tid + z * kAttThreads, h = (y >> 2) % HEADS, i = y / (4 * HEADS);
       const Q* src = static_cast<const Q*>(a.q) + (long long)st->row * a.q_row +
-                     (long long)(st->head * a.group + min(h, a.group - 1)) * a.q_head + 32 * i + 8 * (y & 3);
-      float v[8];
+                     (long long)(st->head * a.group + h) * a.q_head + 32 * i + 8 * (y & 3);
+      ask[z] = {};
+      if (i < CH && h < a.group) {
+        if (a.q_vec)
+          ask[z].load(src);
+        else
+          ask[z].gather(src);
+      }
+    }
+    const long long plane = (long long)st->head * a.page_size * HD;  // the kv head's part of a page
+    // a tile's offset in the pages, and the positions [p0, p1) of it that count
+    long long off;
+    int p0, p1;
+    auto locate = [&](int k) {
+      const int t = base + k * kAttWarps;
+      const int page = pages[k & 63];
+      p0 = max(0, lo - t * kTile);
+      p1 = min(kTile, hi - t * kTile);
+      off = (long long)page * a.page_stride + plane + (t - page_index(a, t) * a.tpp) * (kTile * HD);
+      if ((unsigned)page >= (unsigned)a.n_pages) {  // its positions are masked, and reported at the end
+        st->bad_page = page;
+        st->bad = 1;
+        p0 = p1 = 0;
+        off = 0;
+      }
+    };
+    uint4 kf[2][CH];
+    auto load_k = [&]() {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = h < a.group ? Conv<Q>::up(src[e]) : 0.f;
+      for (int n = 0; n < 2; ++n) {
+        const int p = n * 8 + g;
+        const C* src = static_cast<const C*>(a.k) + off + p * HD + 8 * c;
+        if (p1 - p0 == kTile) {  // a whole tile: nothing to fill in
+#pragma unroll
+          for (int i = 0; i < CH; ++i) kf[n][i] = ldg_stream(src + 32 * i);
+        } else {
+#pragma unroll
+          for (int i = 0; i < CH; ++i)
+            kf[n][i] = p >= p0 && p < p1 ? ldg_stream(src + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+    };
+    pages[lane] = page0;
+    __syncwarp();
+    if (mine > 0) {
+      locate(0);
+      load_k();
+    }
+#pragma unroll
+    for (int z = 0; z < kAsk; ++z) {
+      const int y = tid + z * kAttThreads, h = (y >> 2) % HEADS, i = y / (4 * HEADS);
+      if (i >= CH) continue;
       uint32_t w[4][NQ];
+      if constexpr (std::is_same<C, Q>::value) {
+        w[0][0] = ask[z].w[0].x;
+        w[1][0] = ask[z].w[0].y;
+        w[2][0] = ask[z].w[0].z;
+        w[3][0] = ask[z].w[0].w;
+      } else {
+        float v[8];
+        ask[z].up(v);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) split2<C, NQ>(v[2 * e], v[2 * e + 1], w[e]);
+        for (int e = 0; e < 4; ++e) split2<C, NQ>(v[2 * e], v[2 * e + 1], w[e]);
+      }
 #pragma unroll
       for (int p = 0; p < NQ; ++p) {
         const int slot = WIDE ? ((p * CH + i) * 2 + (h >> 3)) * 32 : (p * CH + i) * 32;
         s_q[slot + (h & 7) * 4 + (y & 3)] = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
       }
-    }
-    const long long plane = (long long)st->head * a.page_size * HD;  // the kv head's part of a page
-    // a tile's offset in the pages, and the positions [p0, p1) of it that count
-    long long off[NT];
-    int p0[NT], p1[NT];
-    auto locate = [&](int k) {
-#pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        const int t = base + (k + x) * kAttWarps;
-        const int page = __shfl_sync(0xffffffffu, pages, (k + x) & 31);
-        p0[x] = max(0, lo - t * kTile);
-        p1[x] = min(kTile, hi - t * kTile);
-        off[x] = (long long)page * a.page_stride + plane + (t - page_index(a, t) * a.tpp) * (kTile * HD);
-        if ((unsigned)page >= (unsigned)a.n_pages || k + x >= mine) {
-          if (k + x < mine) {  // no such page: its positions are masked, and reported at the end
-            st->bad_page = page;
-            st->bad = 1;
-          }
-          p0[x] = p1[x] = 0;
-          off[x] = 0;
-        }
-      }
-    };
-    uint4 kf[NT][2][CH];
-    auto load_k = [&]() {
-#pragma unroll
-      for (int x = 0; x < NT; ++x)
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int p = n * 8 + g;
-          const C* src = static_cast<const C*>(a.k) + off[x] + p * HD + 8 * c;
-          if (p1[x] - p0[x] == kTile) {  // a whole tile: nothing to fill in
-#pragma unroll
-            for (int i = 0; i < CH; ++i) kf[x][n][i] = ldg_stream(src + 32 * i);
-          } else {
-#pragma unroll
-            for (int i = 0; i < CH; ++i)
-              kf[x][n][i] = p >= p0[x] && p < p1[x] ? ldg_stream(src + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
-          }
-        }
-    };
-    if (mine > 0) {
-      locate(0);
-      load_k();
     }
     float o[VH][8][4];
 #pragma unroll
@@ -375,39 +434,35 @@ __global__ void __launch_bounds__(kAttThreads, ctas_per_sm(HD)) attend_kernel(co
       l[h] = 0.f;
     }
     __syncthreads();
-    for (int k = 0; k < mine; k += NT) {
-      if ((k & 31) == 0) pages_next = page_of(k + 32 + lane);
-      int q0[NT], q1[NT];
-      // values of these tiles: in flight while the scores are computed
-      uint4 vf[NT][VH][4];
+    for (int k = 0; k < mine; ++k) {
+      if ((k & 31) == 0) {
+        __syncwarp();  // what is overwritten was read
+        if (k + 32 + lane < mine) cp_async4(pages + ((k + 32 + lane) & 63), entry(k + 32 + lane));
+      }
+      const int q0 = p0, q1 = p1;
+      // the tile's values: in flight while the scores are computed
+      uint4 vf[VH][4];
+      const C* src = static_cast<const C*>(a.v) + off + 2 * c * HD + 8 * g;
+      if (q1 - q0 == kTile) {
 #pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        q0[x] = p0[x];
-        q1[x] = p1[x];
-        const C* src = static_cast<const C*>(a.v) + off[x] + 2 * c * HD + 8 * g;
-        if (p1[x] - p0[x] == kTile) {
+        for (int y = 0; y < 4; ++y)
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
+          for (int h = 0; h < VH; ++h) vf[h][y] = ldg_stream(src + ((y & 1) + 8 * (y >> 1)) * HD + 64 * h);
+      } else {
 #pragma unroll
-            for (int h = 0; h < VH; ++h) vf[x][h][y] = ldg_stream(src + ((y & 1) + 8 * (y >> 1)) * HD + 64 * h);
-        } else {
+        for (int y = 0; y < 4; ++y) {
+          const int p = 2 * c + (y & 1) + 8 * (y >> 1);
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int p = 2 * c + (y & 1) + 8 * (y >> 1);
-#pragma unroll
-            for (int h = 0; h < VH; ++h)
-              vf[x][h][y] = p >= p0[x] && p < p1[x] ? ldg_stream(src + ((y & 1) + 8 * (y >> 1)) * HD + 64 * h)
-                                                    : make_uint4(0u, 0u, 0u, 0u);
-          }
+          for (int h = 0; h < VH; ++h)
+            vf[h][y] = p >= q0 && p < q1 ? ldg_stream(src + ((y & 1) + 8 * (y >> 1)) * HD + 64 * h)
+                                         : make_uint4(0u, 0u, 0u, 0u);
         }
       }
-      float s[NT][2][4];
+      float s[2][4];
 #pragma unroll
-      for (int x = 0; x < NT; ++x)
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[x][n][e] = 0.f;
+        for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
 #pragma unroll
@@ -421,48 +476,45 @@ __global__ void __launch_bounds__(kAttThreads, ctas_per_sm(HD)) attend_kernel(co
             w = p + 1 < NQ ? s_q[((p + 1) * CH + i) * 32 + lane] : make_uint4(0u, 0u, 0u, 0u);
           }
 #pragma unroll
-          for (int x = 0; x < NT; ++x)
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              Mma<C>::run(s[x][n], make_uint4(u.x, w.x, u.y, w.y), kf[x][n][i].x, kf[x][n][i].y);
-              Mma<C>::run(s[x][n], make_uint4(u.z, w.z, u.w, w.w), kf[x][n][i].z, kf[x][n][i].w);
-            }
+          for (int n = 0; n < 2; ++n) {
+            Mma<C>::run(s[n], make_uint4(u.x, w.x, u.y, w.y), kf[n][i].x, kf[n][i].y);
+            Mma<C>::run(s[n], make_uint4(u.z, w.z, u.w, w.w), kf[n][i].z, kf[n][i].w);
+          }
         }
       }
-      // the next tiles' keys
-      if (((k + NT) & 31) == 0) pages = pages_next;
-      if (k + NT < mine) {
-        locate(k + NT);
+      // the next tile's keys
+      if (k + 1 < mine) {
+        if (((k + 1) & 31) == 0) {
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          __syncwarp();
+        }
+        locate(k + 1);
         load_k();
       }
-      // ---- softmax of the tiles, in units of log 2; lane (g, c): columns 2c, 2c + 1 of each half
-      uint32_t ph[NT][RH][2][NP];  // [tile][row half][column half][part]
+      // ---- softmax of the tile, in units of log 2; lane (g, c): columns 2c, 2c + 1 of each half
+      uint32_t ph[RH][2][NP];  // [row half][column half][part]
 #pragma unroll
       for (int h = 0; h < RH; ++h) {
-        float x[NT][4], top = -INFINITY;
+        float x[4];
 #pragma unroll
-        for (int z = 0; z < NT; ++z) {
+        for (int e = 0; e < 4; ++e) {
+          float y = s[e >> 1][2 * h + (e & 1)];
+          // the second part's row; one part has none, and there 0 times an infinite key is NaN
+          if (!WIDE && NQ > 1) y += s[e >> 1][2 + (e & 1)];
+          x[e] = y * a.scale;
+        }
+        if (a.softcap > 0.f) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = a.softcap * tanhf(x[e]);
+        }
+        if (q1 - q0 != kTile) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float y = s[z][e >> 1][2 * h + (e & 1)];
-            // the second part's row; one part has none, and there 0 times an infinite key is NaN
-            if (!WIDE && NQ > 1) y += s[z][e >> 1][2 + (e & 1)];
-            x[z][e] = y * a.scale;
+            const int p = 2 * c + (e & 1) + 8 * (e >> 1);
+            if (p < q0 || p >= q1) x[e] = -INFINITY;
           }
-          if (a.softcap > 0.f) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[z][e] = a.softcap * tanhf(x[z][e]);
-          }
-          if (q1[z] - q0[z] != kTile) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int p = 2 * c + (e & 1) + 8 * (e >> 1);
-              if (p < q0[z] || p >= q1[z]) x[z][e] = -INFINITY;
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = fmaxf(top, x[z][e]);
         }
+        float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const float mn = fmaxf(m[h], top), ms = mn == -INFINITY ? 0.f : mn;
@@ -482,44 +534,38 @@ __global__ void __launch_bounds__(kAttThreads, ctas_per_sm(HD)) attend_kernel(co
             }
           m[h] = mn;
         }
+        float p[4];
 #pragma unroll
-        for (int z = 0; z < NT; ++z) {
-          float p[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            p[e] = ex2(x[z][e] - ms + kProbShift<C>);
-            l[h] += p[e];
-          }
-          split2<C, NP>(p[0], p[1], ph[z][h][0]);
-          split2<C, NP>(p[2], p[3], ph[z][h][1]);
+        for (int e = 0; e < 4; ++e) {
+          p[e] = ex2(x[e] - ms + kProbShift<C>);
+          l[h] += p[e];
         }
+        split2<C, NP>(p[0], p[1], ph[h][0]);
+        split2<C, NP>(p[2], p[3], ph[h][1]);
       }
       // ---- values: pair the positions (2c, 2c + 1) and (2c + 8, 2c + 9) of every dim
 #pragma unroll
-      for (int z = 0; z < NT; ++z)
+      for (int d = 0; d < VH; ++d) {
+        const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&vf[d][0]);
+        const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&vf[d][1]);
+        const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vf[d][2]);
+        const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&vf[d][3]);
 #pragma unroll
-        for (int d = 0; d < VH; ++d) {
-          const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&vf[z][d][0]);
-          const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&vf[z][d][1]);
-          const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vf[z][d][2]);
-          const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&vf[z][d][3]);
+        for (int y = 0; y < 8; ++y) {
+          const uint32_t sel = y & 1 ? 0x7632u : 0x5410u;
+          const uint32_t b0 = __byte_perm(v0[y >> 1], v1[y >> 1], sel), b1 = __byte_perm(v2[y >> 1], v3[y >> 1], sel);
 #pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            const uint32_t sel = y & 1 ? 0x7632u : 0x5410u;
-            const uint32_t b0 = __byte_perm(v0[y >> 1], v1[y >> 1], sel), b1 = __byte_perm(v2[y >> 1], v3[y >> 1], sel);
-#pragma unroll
-            for (int p = 0; p < NP; p += WIDE ? 1 : 2) {
-              if (WIDE) {
-                Mma<C>::run(o[d][y], make_uint4(ph[z][0][0][p], ph[z][RH - 1][0][p], ph[z][0][1][p], ph[z][RH - 1][1][p]),
-                            b0, b1);
-              } else {
-                const int p2 = p + 1 < NP ? p + 1 : 0;
-                Mma<C>::run(o[d][y], make_uint4(ph[z][0][0][p], p2 ? ph[z][0][0][p2] : 0u, ph[z][0][1][p],
-                                                p2 ? ph[z][0][1][p2] : 0u), b0, b1);
-              }
+          for (int p = 0; p < NP; p += WIDE ? 1 : 2) {
+            if (WIDE) {
+              Mma<C>::run(o[d][y], make_uint4(ph[0][0][p], ph[RH - 1][0][p], ph[0][1][p], ph[RH - 1][1][p]), b0, b1);
+            } else {
+              const int p2 = p + 1 < NP ? p + 1 : 0;
+              Mma<C>::run(o[d][y], make_uint4(ph[0][0][p], p2 ? ph[0][0][p2] : 0u, ph[0][1][p], p2 ? ph[0][1][p2] : 0u),
+                          b0, b1);
             }
           }
         }
+      }
     }
     // ---- merge the warps' pieces in shared memory, fixed order
 #pragma unroll
@@ -710,6 +756,11 @@ extern "C" mk_status mk_paged_attention(const mk_attend_args* args, const mk_pag
     const size_t esz = args->dtype == MK_F32 ? 4 : 2;
     if (!aligned_to(args->q, esz) || !aligned_to(args->out, esz))
       return paged_fail(MK_ERR_INVALID, "q and out must be aligned to their type");
+    // the line of work counts in 32 bits
+    const long long cap = (long long)cache->table_width * cache->page_size;
+    const long long most = (args->window > 0 ? std::min(cap, (long long)args->window + kTile) : cap) / kTile + 1 + kLead;
+    if (most * args->n_rows > 0x7f000000LL / cache->n_kv_heads)
+      return paged_fail(MK_ERR_INVALID, "n_rows * n_kv_heads * (the table's positions / 16 + 9) must be below 2^31 - 2^24");
     if (!args->workspace || !aligned_to(args->workspace, 16))
       return paged_fail(MK_ERR_INVALID, "the workspace is missing or unaligned");
     if (args->n_rows == 0) return MK_OK;
@@ -729,11 +780,12 @@ extern "C" mk_status mk_paged_attention(const mk_attend_args* args, const mk_pag
     a.page_stride = cache->page_stride; a.table_stride = cache->table_stride;
     a.n_rows = args->n_rows; a.hq = args->n_heads; a.hkv = cache->n_kv_heads; a.group = args->n_heads / cache->n_kv_heads;
     a.len_add = args->len_add; a.window = args->window; a.page_size = cache->page_size; a.n_pages = cache->n_pages;
-    a.table_rows = cache->n_rows; a.width = cache->table_width;
+    a.table_rows = cache->n_rows; a.cap = cache->table_width * cache->page_size;  // at most 2^30
     a.tpp = a.page_size / kTile;
     a.tpp_inverse = a.tpp > 1 ? (unsigned)(((1ULL << 32) + a.tpp - 1) / a.tpp) : 0;
     a.n_cta = n_sm * ctas_per_sm(cache->head_dim);
     a.part = reinterpret_cast<float*>(a.joins + a.n_cta);
+    a.q_vec = aligned_to(a.q, 16) && a.q_row * (long long)esz % 16 == 0 && a.q_head * (long long)esz % 16 == 0;
     a.by_segment = (long long)a.n_rows * a.hkv <= a.n_cta;
     a.scale = args->softcap > 0.f ? args->scale / args->softcap : args->scale * kLog2e;
     a.softcap = args->softcap * kLog2e;

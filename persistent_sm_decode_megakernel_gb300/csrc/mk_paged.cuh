@@ -114,6 +114,10 @@ struct Raw8 {
 #pragma unroll
     for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = ldg_stream(reinterpret_cast<const uint4*>(p) + i);
   }
+  __device__ __forceinline__ void gather(const T* p) {  // wherever p lies
+#pragma unroll
+    for (int i = 0; i < 8; ++i) reinterpret_cast<T*>(w)[i] = p[i];
+  }
   __device__ __forceinline__ void up(float (&x)[8]) const {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = Conv<T>::up(reinterpret_cast<const T*>(w)[i]);

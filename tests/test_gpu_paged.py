@@ -280,6 +280,25 @@ def test_attention_rows_share_tables(paged):
     _check_attend(q, kp, vp, table, [n + 1 for n in lens], out, lse, 1 / math.sqrt(128), rows=rows)
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attention_many_tiles_of_a_warp(paged, hd):
+    """Queries long enough together that a warp's part passes 32 and 64 tiles, of one table row."""
+    g = torch.Generator(device=DEV).manual_seed(6)
+    kp, vp, table = _make_cache(g, [20011], 8, hd, 16, "f16")
+    lens = [20011 - 13 * i for i in range(16)]
+    q = torch.randn(16, 8, hd, generator=g, device=DEV).half()
+    out, lse = paged.paged_attention(q, kp, vp, ints(table), ints(lens), rows=ints([0] * 16), return_lse=True)
+    _check_attend(q, kp, vp, table, lens, out, lse, 1 / math.sqrt(hd), rows=[0] * 16)
+
+
+@pytest.mark.parametrize("longest", [150, 400, 900])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attention_of_as_many_segments_as_ctas(paged, longest, hd):
+    """About a CTA per (row, kv head), rows without positions among them: each whole, or in equal shares."""
+    lens = [0 if i % 9 == 4 else longest - (17 * i) % (longest // 3) for i in range(52)]
+    _attend_case(paged, lens, 8, 8, hd, 32, "bf16", "bf16")
+
+
 @pytest.mark.parametrize("what", ["page", "negative page", "row", "length"])
 def test_attention_reports_and_masks_what_is_not_there(paged, what):
     from persistent_sm_decode_megakernel_gb300 import MK_ERR_PAGES, MkError

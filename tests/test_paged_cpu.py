@@ -91,6 +91,12 @@ def test_bad_attention_arguments_are_refused(mk, bad):
     assert mk.mk_last_error()
 
 
+def test_attention_over_more_tiles_than_it_counts_is_refused(mk):
+    view = _view(mk, table_width=1 << 26, table_stride=1 << 26)
+    assert _attend(mk, view, n_rows=16) == mk.MK_ERR_INVALID
+    assert b"2^31" in mk.mk_last_error()
+
+
 def test_calls_without_tokens_or_rows_do_nothing(mk):
     assert _append(mk, _view(mk), n_tokens=0) == mk.MK_OK
     assert _attend(mk, _view(mk), n_rows=0) == mk.MK_OK
