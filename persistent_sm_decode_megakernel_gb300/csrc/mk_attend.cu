@@ -100,7 +100,7 @@ __device__ __noinline__ void fill_rows(const AttendArgs& a, int hd) {
 //   pitch: the units of every segment, its lead being what its tiles leave, so that each is
 //     whole in a CTA of its own; 0: n + lead.  Taken when there is a CTA for each and the longest is
 //     no longer than an equal share and the lead that a second piece would add (61 ragged rows
-//     of up to 700 positions: 14.5 us, in equal shares 15.6).
+//     of up to 700 positions: 13.7 us; in equal shares 1.1 more).
 constexpr int kLead = 8;
 struct Line {
   int units, share, lead, pitch;
@@ -259,7 +259,11 @@ struct AttSmem {
 //     positions, and column n of the j-th instruction is dim 64 h + 8 n + j.
 // So every load is 16 bytes, a warp's rows are read in whole 64- and 128-byte runs, no
 // barrier stands between the loads and the products, and the warps of an SM hide each
-// other's latency.
+// other's latency.  Bound: the keys' and values' bytes (16 rows of 16384 to 32768 positions,
+// 1.67 GB: 245 us, 6.8 TB/s), of short rows the chain from the lengths over the table to the
+// first keys, 3 us of it, and a tile after another of a warp, 1 us each (one row of 512: 6.7 us
+// with the join, one of 32768: 28.5).  The pages of a warp's tiles lie in shared memory and
+// come there without a register between: held by the lanes, they cost the long rows 2 %.
 template <typename C, typename Q, int HD, bool WIDE, int NQ, int NP>
 __global__ void __launch_bounds__(kAttThreads, ctas_per_sm(HD)) attend_kernel(const __grid_constant__ AttendArgs a) {
   using SM = AttSmem<HD, WIDE, NQ>;
@@ -638,7 +642,8 @@ __global__ void __launch_bounds__(kAttThreads, ctas_per_sm(HD)) attend_kernel(co
 }
 
 // Joins the pieces of the segments that span CTAs: one CTA per (segment, head of its group);
-// warps take the pieces in turn, each lane HD / 32 dims.
+// warps take the pieces in turn, each lane HD / 32 dims.  Bound: the launch and two dependent
+// loads, 1.2 us behind one row of 512 positions, 2 us when nothing is to be joined in 2000 CTAs.
 template <typename Q, int HD>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttendArgs a, float shift) {
   constexpr int W = kJoinThreads / 32, E = HD / 32, ROW = HD + 4;
