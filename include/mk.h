@@ -516,7 +516,7 @@ mk_status mk_create_paged(const mk_model_desc* desc, const mk_weights* weights, 
  * position needs its page in the table before the call.  out_tok [B] (or NULL) receives the
  * argmax, logits [B][vocab] (or NULL) the logits.  Asynchronous; mk_synchronize reports what
  * went wrong on the device (a bad page or row as MK_ERR_PAGES: nothing is cached for it, and
- * it is masked).  Not for stream capture. */
+ * it is masked).  Not for stream capture (MK_ERR_STATE). */
 mk_status mk_decode_step_paged(mk_ctx* ctx, const int32_t* tok, const int32_t* pos, const int32_t* rows, int B,
                                int32_t* out_tok, float* logits);
 

@@ -726,6 +726,15 @@ mk_status launch_attend(const AttendArgs& a, int hd, void* stream) {
 }
 
 }  // namespace
+
+// the line of work counts in 32 bits
+std::string check_line(const mk_page_view* c, long long n_rows, int window) {
+  const long long cap = (long long)c->table_width * c->page_size;
+  const long long most = (window > 0 ? std::min(cap, (long long)window + kTile) : cap) / kTile + 1 + kLead;
+  if (most * n_rows > 0x7f000000LL / c->n_kv_heads)
+    return "n_rows * n_kv_heads * (the table's positions / 16 + 9) must be below 2^31 - 2^24";
+  return "";
+}
 }  // namespace mk
 
 extern "C" mk_status mk_paged_attention_workspace(int n_heads, int n_kv_heads, int head_dim, size_t* bytes) {
@@ -761,11 +770,8 @@ extern "C" mk_status mk_paged_attention(const mk_attend_args* args, const mk_pag
     const size_t esz = args->dtype == MK_F32 ? 4 : 2;
     if (!aligned_to(args->q, esz) || !aligned_to(args->out, esz))
       return paged_fail(MK_ERR_INVALID, "q and out must be aligned to their type");
-    // the line of work counts in 32 bits
-    const long long cap = (long long)cache->table_width * cache->page_size;
-    const long long most = (args->window > 0 ? std::min(cap, (long long)args->window + kTile) : cap) / kTile + 1 + kLead;
-    if (most * args->n_rows > 0x7f000000LL / cache->n_kv_heads)
-      return paged_fail(MK_ERR_INVALID, "n_rows * n_kv_heads * (the table's positions / 16 + 9) must be below 2^31 - 2^24");
+    const std::string line = check_line(cache, args->n_rows, args->window);
+    if (!line.empty()) return paged_fail(MK_ERR_INVALID, line);
     if (!args->workspace || !aligned_to(args->workspace, 16))
       return paged_fail(MK_ERR_INVALID, "the workspace is missing or unaligned");
     if (args->n_rows == 0) return MK_OK;

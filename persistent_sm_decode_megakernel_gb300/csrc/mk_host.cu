@@ -674,6 +674,7 @@ mk_status mk_create_paged(const mk_model_desc* desc, const mk_weights* w, const 
     v.n_kv_heads = desc->n_kv_heads; v.page_size = pages->page_size; v.head_dim = desc->head_dim; v.dtype = desc->dtype;
     v.table = pages->table; v.n_rows = pages->n_rows; v.table_width = pages->table_width; v.table_stride = pages->table_stride;
     e = check_view(&v);
+    if (e.empty()) e = check_line(&v, desc->max_batch, 0);
     if (!e.empty()) return fail(MK_ERR_INVALID, e);
     if (desc->n_layers > 1 && (pages->layer_stride < v.n_kv_heads * (long long)v.page_size * v.head_dim || pages->layer_stride % 8))
       return fail(MK_ERR_INVALID, "layer_stride must hold a page and be a multiple of 8");
@@ -731,9 +732,14 @@ mk_status mk_decode_step_paged(mk_ctx* ctx, const int32_t* tok, const int32_t* p
     if (!tok || !pos) return fail(MK_ERR_INVALID, "tok/pos NULL");
     if (B < 1 || B > ctx->m.max_batch) return fail(MK_ERR_INVALID, "B out of range");
     if (ctx->broken) return fail(MK_ERR_STATE, "context needs mk_reset after a device error");
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    MK_CUDA(cudaStreamIsCapturing(ctx->stream, &capture));
+    if (capture != cudaStreamCaptureStatusNone)  // a replay would count its arrivals from the captured step's on
+      return fail(MK_ERR_STATE, "mk_decode_step_paged cannot be captured");
     Sched* sc = nullptr;
     mk_status s = get_sched(ctx, B, &sc);
     if (s) return s;
+    ctx->broken = true;  // until all of it is enqueued
     const PagedState& ps = *ctx->paged;
     const ModelShape& m = ctx->m;
     DevState S = ctx->st;
@@ -795,6 +801,7 @@ mk_status mk_decode_step_paged(mk_ctx* ctx, const int32_t* tok, const int32_t* p
     ++sc->epoch;
     ++ctx->step;
     ctx->last_B = B;
+    ctx->broken = false;
     return MK_OK;
   });
 }

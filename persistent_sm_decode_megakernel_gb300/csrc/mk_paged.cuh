@@ -65,6 +65,8 @@ inline mk_status launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 blo
 mk_status sm_count(int* n);
 // the checks on a page view that every operator over pages applies: "" when usable
 std::string check_view(const mk_page_view* c);
+// whether the attention can count its work over that many rows of the table: "" when it can
+std::string check_line(const mk_page_view* c, long long n_rows, int window);
 
 #ifdef __CUDACC__
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -237,24 +237,38 @@ class PagedDecoder:
 
     def step(self, tokens, positions, rows=None, logits=None):
         """One step of device int32 tensors: token i at positions[i] of table row rows[i] (default i).  The
-        argmax tokens; positions need their pages (update).  lens is the caller's to advance."""
+        argmax tokens; positions need their pages (update).  lens is the caller's to advance.  It runs on
+        self.stream, where its tensors have to be ready."""
         from . import mk_decode_step_paged
-        out = torch.empty(len(tokens), dtype=torch.int32, device=self.dm.device)
-        check(mk_decode_step_paged(self.h, tokens.data_ptr(), positions.data_ptr(), rows.data_ptr() if rows is not None else None,
-                                   len(tokens), out.data_ptr(), logits.data_ptr() if logits is not None else None),
-              "mk_decode_step_paged")
+        n = len(tokens)
+        for name, t, shape, dtype in (("tokens", tokens, (n,), torch.int32), ("positions", positions, (n,), torch.int32),
+                                      ("rows", rows, (n,), torch.int32),
+                                      ("logits", logits, (n, self.dm.cfg.vocab), torch.float32)):
+            if t is None and name in ("rows", "logits"):
+                continue
+            if tuple(t.shape) != shape or t.dtype != dtype or t.device != self.k.device or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor of {shape} on {self.k.device}")
+        with torch.cuda.stream(self.stream):
+            out = torch.empty(n, dtype=torch.int32, device=self.k.device)
+            check(mk_decode_step_paged(self.h, tokens.data_ptr(), positions.data_ptr(),
+                                       rows.data_ptr() if rows is not None else None, n, out.data_ptr(),
+                                       logits.data_ptr() if logits is not None else None), "mk_decode_step_paged")
         return out
 
     def prefill(self, prompts, logits=None):
         """Appends prompts {row: tokens} to their rows, up to dm.max_batch positions per step.  Returns
-        {row: next token} (device int32 [1] each); logits {row: float32 [vocab]} receives the last ones."""
+        {row: next token} (device int32 [1] each); logits {row: float32 [vocab]} receives the last ones.  Raises
+        ValueError for a prompt that does not fit and MkError when the pages run out, before any of it."""
         with torch.cuda.stream(self.stream):
             n_rows, V = self.table.shape[0], self.dm.cfg.vocab
+            start = self.lens.tolist()
             reserve = [0] * n_rows
             for r, p in prompts.items():
+                if not 0 <= r < n_rows or len(p) < 1 or start[r] + len(p) > self.max_positions:
+                    raise ValueError("a prompt must be of a row of the table, not empty and fit max_positions")
                 reserve[r] = len(p)
             self.update(reserve=reserve)
-            start = self.lens.tolist()
+            self.synchronize()
             jobs = [(int(t), start[r] + i, r, i == len(p) - 1) for r, p in prompts.items() for i, t in enumerate(p)]
             last = {}
             for at in range(0, len(jobs), self.dm.max_batch):

@@ -221,6 +221,53 @@ def test_paged_steps_report_what_is_not_there(lib):
     dec.close()
 
 
+def test_prompts_that_do_not_fit_leave_the_rows_as_they_were(lib):
+    """Too long a prompt, an empty one, no such row, too few pages: refused before any step, and the rows go on."""
+    from persistent_sm_decode_megakernel_gb300 import MK_ERR_PAGES, MkError
+    cfg = synth.CONFIGS["tiny"]
+    w = synth.gen_weights(cfg)
+    prompt = synth.gen_prompts(cfg, 1, 33)[0]
+    dec = _paged(lib, cfg, w, 4, 3, 48, n_pages=4)
+    want = int(dec.prefill({0: prompt})[0])            # three of four pages
+    before = dec.lens.tolist(), dec.table.tolist(), dec.refs.tolist()
+    for bad in ({1: [1] * 49}, {0: [1] * 16}, {1: []}, {3: [1]}, {-1: [1]}):
+        with pytest.raises(ValueError):
+            dec.prefill(bad)
+    with pytest.raises(MkError) as e:
+        dec.prefill({1: prompt})
+    assert e.value.status == MK_ERR_PAGES
+    assert before == (dec.lens.tolist(), dec.table.tolist(), dec.refs.tolist())
+    dec.update(parents=[-1, -1, -1])
+    assert int(dec.prefill({1: prompt})[1]) == want
+    dec.close()
+
+
+def test_steps_refuse_tensors_that_do_not_fit_and_capture(lib):
+    from persistent_sm_decode_megakernel_gb300 import MK_ERR_STATE, mk_decode_step_paged
+    cfg = synth.CONFIGS["tiny"]
+    w = synth.gen_weights(cfg)
+    dec = _paged(lib, cfg, w, 2, 2, 32, stream=torch.cuda.Stream())
+    want = int(dec.prefill({0: [5, 6, 7]})[0])
+    one, two = dec._int32([want]), dec._int32([3, 4])
+    wide = torch.zeros(4, dtype=torch.int32, device=one.device)
+    z = torch.zeros(2, cfg.vocab + 1, device=one.device)
+    for args in ((one.long(), one), (one, one.long()), (one, two), (one, one, two), (one, one, one.cpu()), (wide[::2], two),
+                 (two, two, None, z), (two, two, None, z[:, 1:]), (two, two, None, z[:, 1:].half().contiguous())):
+        with pytest.raises(ValueError):
+            dec.step(*args)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=dec.stream):
+        junk = one + 1                                 # a graph of something
+        status = mk_decode_step_paged(dec.h, one.data_ptr(), one.data_ptr(), None, 1, None, None)
+    assert status == MK_ERR_STATE
+    dec.update(reserve=[1, 0])
+    torch.cuda.synchronize()
+    assert int(dec.step(one, dec._int32([3]))[0]) >= 0
+    dec.synchronize()
+    dec.close()
+
+
 def test_entry_points_keep_to_their_context(lib):
     from persistent_sm_decode_megakernel_gb300 import MK_ERR_INVALID, mk_decode_step_paged
     cfg = synth.CONFIGS["tiny"]
