@@ -7,6 +7,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/core/TensorImpl.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -44,6 +45,8 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) value_error(std::string(name) + " must be a tensor");
   const at::Tensor& t = THPVariable_Unpack(o);
   if (t.layout() != at::kStrided) value_error(std::string(name) + " must be a dense tensor");
+  if (t.requires_grad() && c10::GradMode::is_enabled())
+    value_error(std::string(name) + " requires a gradient, and none is recorded here (torch.no_grad())");
   return t;
 }
 const at::Tensor& on_gpu(PyObject* o, const char* name) {

@@ -258,3 +258,16 @@ def test_bad_paged_contexts_are_refused(mk, bad):
     assert create(ok, exec_mode=2) == mk.MK_ERR_INVALID
     assert create(ok, rope=mk.mk_rope_desc(10000.0, 128, 0, 1.0, 0, 0, 0)) == mk.MK_ERR_INVALID
     assert create(ok, rope=mk.mk_rope_desc(10000.0, 64, 1, 0.5, 0, 0, 0)) == mk.MK_ERR_INVALID
+
+
+def test_tensors_that_require_a_gradient_are_refused():
+    import torch
+    from persistent_sm_decode_megakernel_gb300 import paged
+    pages, ids = torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16), torch.zeros(1, 2, dtype=torch.int32)
+    q = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="gradient"):
+        paged.paged_attention(q, pages.clone().requires_grad_(), pages, ids, ids[:, 0])
+    with pytest.raises(ValueError, match="gradient"):
+        paged.beam_select(torch.zeros(2, 8, requires_grad=True), torch.zeros(1, 2), ids)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+        paged.beam_select(torch.zeros(2, 8, requires_grad=True), torch.zeros(1, 2), ids)
