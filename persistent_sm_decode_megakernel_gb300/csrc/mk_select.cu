@@ -57,6 +57,12 @@ __device__ __forceinline__ float value_of(u64 key) {
 }
 __device__ __forceinline__ int token_of(u64 key) { return (int)(0xFFFFFFFFu - (unsigned)key); }
 
+// the least float above x (x not +inf)
+__device__ __forceinline__ float above(float x) {
+  const uint32_t u = orderable(x + 0.f) + 1u;
+  return value_of((u64)(x == -INFINITY ? orderable(-0x1.fffffep127f) : u) << 32);
+}
+
 // the largest of the warp's keys (each lane's own, 0: none)
 __device__ __forceinline__ u64 warp_max(u64 k) {
   const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
@@ -120,8 +126,9 @@ __device__ __forceinline__ u64 ordered(Pair p) { return (u64)orderable(p.hi + 0.
 // list is cut down to its best after steps 1, 4, 16, .., each entry counting how many are
 // above it, which is its place; of a part in random order about three times `beams` keys
 // enter between two of those (no cut after the first step: 24.8 us for 128 rows of 128256, in
-// place of 18.7; one after every step: 22.3).  Should the list overflow (rising logits), the
-// part is read again, once per beam.  The sum of exponentials runs against whole powers of two, so that joining threads,
+// place of 18.7; one after every step: 22.3).  Should the list overflow (rising
+// logits, or equal ones in the first step), what came since the last cut is read again, once
+// per beam.  The sum of exponentials runs against whole powers of two, so that joining threads,
 // steps and parts rounds nothing: a step's in 32 bits, a compensated sum of them per thread,
 // and from there on whole numbers.  Bound: the logits' bytes for many rows (the arithmetic, one
 // exponential each, is most of that time again), the launch and the block steps for few.
@@ -151,18 +158,29 @@ __global__ void __launch_bounds__(kScanThreads, PER == kPerLarge ? kCtasLarge : 
 #pragma unroll
         for (int y = 0; y < V; ++y) x[i + y] = Conv<T>::up(raw[y]);
       }
-    } else {
+    } else {  // a part's last step: what lies in it
 #pragma unroll
-      for (int i = 0; i < PER; ++i) x[i] = at(it, i) < n ? Conv<T>::up(src[at(it, i)]) : -INFINITY;
+      for (int i = 0; i < PER; i += V) {
+        const int e = at(it, i);
+        if (VEC && e + V <= n) {
+          alignas(16) T raw[V];
+          *reinterpret_cast<uint4*>(raw) = *reinterpret_cast<const uint4*>(src + e);
+#pragma unroll
+          for (int y = 0; y < V; ++y) x[i + y] = Conv<T>::up(raw[y]);
+        } else {
+#pragma unroll
+          for (int y = 0; y < V; ++y) x[i + y] = e + y < n ? Conv<T>::up(src[e + y]) : -INFINITY;
+        }
+      }
     }
   };
   if (tid == 0) s_n = 0;
   float x[PER], next[PER];
   load(0, next);
   const int steps = (n + kIter - 1) / kIter;
-  u64 bound = 0ull;            // keys above it enter, if their logit is not below
-  float floor_ = -INFINITY;    // this
+  float floor_ = -INFINITY;    // logits below it do not enter
   int cut = 1;                 // the list is cut down after this many steps
+  int kept = 0, from = 0;      // entries of the list after the last cut, and elements before it
   bool bad = false;
   float ref = -INFINITY, s = 0.f, comp = 0.f;  // (s + comp) 2^ref: the thread's sum of e^x
   for (int it = 0; it < steps; ++it) {
@@ -236,8 +254,8 @@ __global__ void __launch_bounds__(kScanThreads, PER == kPerLarge ? kCtasLarge : 
         float y = x[0];
 #pragma unroll
         for (int z = 1; z < PER; ++z) y = z == i ? x[z] : y;
+        if (e >= n) continue;
         const u64 k = key_of(y, first + e);
-        if (k <= bound || e >= n) continue;
         const int p = atomicAdd(&s_n, 1);
         if (p < kList) s_list[p] = k;
       }
@@ -249,12 +267,13 @@ __global__ void __launch_bounds__(kScanThreads, PER == kPerLarge ? kCtasLarge : 
     // ---- after steps 1, 4, 16, .. and the last: the list's best, in order
     __syncthreads();
     int count = s_n;
-    if (count > kList) {  // too many: the part's largest one by one, each below the last
+    const int seen = min(n, (it + 1) * kIter);
+    if (count > kList) {  // too many: the largest since the last cut and of its list one by one, each below the last
       u64 last = ~0ull;
-      const int seen = min(n, (it + 1) * kIter);
       for (int b = 0; b < K; ++b) {
-        u64 k = 0ull;
-        for (int e = tid; e < seen; e += kScanThreads) {
+        u64 k = tid < kept && s_list[tid] < last ? s_list[tid] : 0ull;
+#pragma unroll 16
+        for (int e = from + tid; e < seen; e += kScanThreads) {
           float y = Conv<T>::up(src[e]);
           if (!(y <= kLargest)) y = -INFINITY;
           const u64 z = key_of(y, first + e);
@@ -266,10 +285,12 @@ __global__ void __launch_bounds__(kScanThreads, PER == kPerLarge ? kCtasLarge : 
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < kScanWarps; ++w) k = s_warp[w] > k ? s_warp[w] : k;
-        if (tid == 0) s_list[b] = k;
+        if (tid == 0) s_list[kList - K + b] = k;  // (what entered there is in memory still)
         last = k;
       }
       count = K;
+      __syncthreads();
+      if (tid < K) s_list[tid] = s_list[kList - K + tid];
       __syncthreads();
     } else {
       // a short list takes a pair of threads per entry, each counting over one half
@@ -299,10 +320,10 @@ __global__ void __launch_bounds__(kScanThreads, PER == kPerLarge ? kCtasLarge : 
     }
     if (tid == 0) s_n = min(count, K);
     __syncthreads();
-    if (count >= K) {
-      bound = s_list[K - 1];
-      floor_ = value_of(bound);
-    }
+    kept = min(count, K);
+    from = seen;
+    // of what follows, equal logits lose to the list's, whose tokens are lower
+    if (count >= K) floor_ = above(value_of(s_list[K - 1]));
   }
   if (bad) report(a.status, MK_ERR_NAN, PO_SELECT, row, chunk);
   u64* out = a.cand + ((long long)row * a.chunks + chunk) * K;
@@ -469,7 +490,7 @@ size_t lay_out(SelectArgs* a, void* ws, long long rows, int beams, int chunks) {
 
 template <typename T>
 mk_status launch_scan(const SelectArgs& a, bool vec, void* stream) {
-  const bool small = a.chunk <= kPerSmall * kScanThreads;
+  const bool small = a.chunk <= kPerLarge * kScanThreads;  // (a long step would not be full)
   auto k = small ? (vec ? scan_kernel<T, true, kPerSmall> : scan_kernel<T, false, kPerSmall>)
                  : (vec ? scan_kernel<T, true, kPerLarge> : scan_kernel<T, false, kPerLarge>);
   return launch_dependent(k, dim3((unsigned)(a.rows * a.chunks)), dim3(kScanThreads), 0, stream, "mk_beam_select", a);
