@@ -628,6 +628,28 @@ def test_select_ties_and_layouts_of_the_large_logits(paged, kind, beams, groups)
     _check_select(paged.beam_select(logits, scores, ended), logits, scores, ended, -1)
 
 
+@pytest.mark.parametrize("kind", ["few allowed", "half masked", "others lowest", "thin mask", "rising", "best first, then rising"])
+@pytest.mark.parametrize("groups,beams,vocab", [(16, 8, 70000), (2, 32, 32000), (1, 4, 9001)])
+def test_select_masked_and_rising_parts_of_several_steps(paged, kind, groups, beams, vocab):
+    """Masks that leave few tokens, none of the first half, one of a thousand, the type's lowest in the place of
+    -inf; logits of which ever more enter the list, with and without its first entries staying the best."""
+    logits, scores, ended = _select_inputs(groups, beams, vocab, "f32", seed=9)
+    i = torch.arange(vocab, device=DEV)
+    if kind == "few allowed":
+        logits[:, (i < 100) | (i >= 105)] = -math.inf
+    elif kind == "half masked":
+        logits[:, : vocab // 2] = -math.inf
+    elif kind == "others lowest":
+        logits[:, 5 + beams:] = torch.finfo(torch.float32).min
+    elif kind == "thin mask":
+        logits[:, i % 1000 != 7] = -math.inf
+    else:
+        logits[:] = -5.0 + i / 16384.0 + (logits - logits.min()) * 1e-7
+        if kind != "rising":
+            logits[:, : beams - 1] = 60.0 - i[: beams - 1] / 8.0
+    _check_select(paged.beam_select(logits, scores, ended), logits, scores, ended, -1)
+
+
 def test_select_minus_infinity(paged):
     """Masked tokens, a row with fewer finite logits than beams, a row without any, beams that are not alive yet
     (score -inf, as at the first step), and ended beams among them."""
