@@ -22,7 +22,7 @@ constexpr float kLargest = 0x1p126f;  // of a logit: beyond it lies infinity
 constexpr int kScanThreads = 256;
 constexpr int kScanWarps = kScanThreads / 32;
 // elements of a step per thread, and CTAs per SM: one short step, or several long ones (a step
-// costs about 90 instructions beside its 6 per element; 128 rows of 128256: 18.7 us, steps of
+// costs about 90 instructions beside its 6 per element; 128 rows of 128256: 18.4 us, steps of
 // half the length in twice the CTAs 20.2, CTAs of 128 threads 19.8 to 24)
 constexpr int kPerSmall = 8, kCtasSmall = 4, kPerLarge = 32, kCtasLarge = 2;
 constexpr int kList = 1024;               // entries of a CTA's list
@@ -126,13 +126,13 @@ __device__ __forceinline__ u64 ordered(Pair p) { return (u64)orderable(p.hi + 0.
 // list is cut down to its best after steps 1, 4, 16, .., each entry counting how many are
 // above it, which is its place; of a part in random order about three times `beams` keys
 // enter between two of those (no cut after the first step: 24.8 us for 128 rows of 128256, in
-// place of 18.7; one after every step: 22.3).  Should the list overflow (rising
+// place of 18.4; one after every step: 22.3).  Should the list overflow (rising
 // logits, or equal ones in the first step), what came since the last cut is read again, once
 // per beam.  The sum of exponentials runs against whole powers of two, so that joining threads,
 // steps and parts rounds nothing: a step's in 32 bits, a compensated sum of them per thread,
 // and from there on whole numbers.  Bound: the logits' bytes for many rows (the arithmetic, one
 // exponential each, is most of that time again), the launch and the block steps for few.
-// (Both kernels, 4 rows of 32000: 5.1 us; 128 of 128256, 66 MB: 18.7 us, 3.5 TB/s.)
+// (Both kernels, 4 rows of 32000: 5.1 us; 128 of 128256, 66 MB: 18.4 us, 3.6 TB/s.)
 template <typename T, bool VEC, int PER>
 __global__ void __launch_bounds__(kScanThreads, PER == kPerLarge ? kCtasLarge : kCtasSmall) scan_kernel(const __grid_constant__ SelectArgs a) {
   __shared__ u64 s_list[kList], s_warp[kScanWarps];
@@ -477,8 +477,8 @@ __global__ void __launch_bounds__(32 * kMaxBeams) pick_kernel(const __grid_const
 }
 
 // Elements of a CTA's part of a row: the rows' parts fill the resident CTAs once -- of long steps
-// when a part is then longer than one of their steps, else of one short step each (2048
-// elements), so that few rows still spread over many SMs.
+// when a part is then longer than one of them, else of short steps (2048 elements; one each where
+// there are CTAs for it), so that few rows still spread over many SMs.
 constexpr int kPart = kPerSmall * kScanThreads;
 int chunk_of(long long rows, int vocab, int n_sm) {
   const long long parts = std::max(1LL, (long long)kCtasLarge * n_sm / rows), each = ((long long)vocab + parts - 1) / parts;
