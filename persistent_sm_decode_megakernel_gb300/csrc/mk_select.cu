@@ -19,6 +19,9 @@ namespace {
 
 constexpr int kMaxBeams = 32;
 constexpr float kLargest = 0x1p126f;  // of a logit: beyond it lies infinity
+// Up to here x log2 e, rounded to a whole number n in 32 bits, is off by less than 0.1, so that
+// 2^(x log2 e - n) is at most about 1; from 2^32 on the rounding alone is worth 128 powers of two
+constexpr float kNear = 0x1p20f;
 constexpr int kScanThreads = 256;
 constexpr int kScanWarps = kScanThreads / 32;
 // elements of a step per thread, and CTAs per SM: one short step, or several long ones (a step
@@ -29,9 +32,11 @@ constexpr int kList = 1024;               // entries of a CTA's list
 
 using u64 = unsigned long long;
 
-// of a part of a row: n, and the sum of 2^(x log2 e - n) in units of 2^-sum_bits
+// of a part of a row: n, and the sum of 2^(x log2 e - n) in units of 2^-sum_bits; far: n is the
+// part's largest logit, and the sum that of e^(x - n)
 struct __align__(16) Stat {
-  float n, unused;
+  float n;
+  int far;
   u64 sum;
 };
 
@@ -78,6 +83,8 @@ __device__ __forceinline__ float term_of(float x, float n) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaf(x, kLog2eLo, fmaf(x, kLog2eHi, -n))));
   return y;
 }
+// the same of a natural exponent y, the difference of two logits
+__device__ __forceinline__ float exp_of(float y) { return term_of(y, 0.f); }
 // 2^d for a whole d in [-126, 127], exactly; 0 below
 __device__ __forceinline__ float power_of(float d) { return d < -126.f ? 0.f : __int_as_float((127 + (int)d) << 23); }
 
@@ -132,7 +139,12 @@ __device__ __forceinline__ u64 ordered(Pair p) { return (u64)orderable(p.hi + 0.
 // steps and parts rounds nothing: a step's in 32 bits, a compensated sum of them per thread,
 // and from there on whole numbers.  Bound: the logits' bytes for many rows (the arithmetic, one
 // exponential each, is most of that time again), the launch and the block steps for few.
-// (Both kernels, 4 rows of 32000: 5.1 us; 128 of 128256, 66 MB: 18.4 us, 3.6 TB/s.)
+// That holds for logits up to kNear in magnitude.  A step of a thread whose largest logit lies
+// beyond takes no part: it counts for nothing beside a part whose largest logit is within, and
+// a part whose largest logit is beyond (all masked by a large finite number; it is known after
+// the last cut) is read once more, its sum against that logit itself, x - max being exact where
+// it matters.
+// (Both kernels, 4 rows of 32000: 5.3 us; 128 of 128256, 66 MB: 18.4 us, 3.6 TB/s.)
 template <typename T, bool VEC, int PER>
 __global__ void __launch_bounds__(kScanThreads, PER == kPerLarge ? kCtasLarge : kCtasSmall) scan_kernel(const __grid_constant__ SelectArgs a) {
   __shared__ u64 s_list[kList], s_warp[kScanWarps];
@@ -209,7 +221,12 @@ __global__ void __launch_bounds__(kScanThreads, PER == kPerLarge ? kCtasLarge : 
       for (int i = 0; i < PER; ++i) w[i % 4] += term_of(x[i], ref);
       q = (w[0] + w[1]) + (w[2] + w[3]);
     };
-    if (fabsf(top) <= kLargest) terms();
+    if (fabsf(top) <= kNear) {
+      terms();
+    } else if (fabsf(top) <= kLargest) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) q = fmaf(x[i], 0.f, q);  // 0, or NaN where something is to be looked at
+    }
     if (!(fabsf(top) <= kLargest) || q != q) {  // NaN and +inf are reported and count as -inf
       top = -INFINITY;
       q = 0.f;
@@ -222,7 +239,7 @@ __global__ void __launch_bounds__(kScanThreads, PER == kPerLarge ? kCtasLarge : 
         if (x[i] < -kLargest) x[i] = -INFINITY;
         top = fmaxf(top, x[i]);
       }
-      if (top > -INFINITY) terms();
+      if (fabsf(top) <= kNear) terms();
     }
     const float sum = s + q, r = sum - s;  // sum + the bracket below is s + q exactly
     comp += (s - (sum - r)) + (q - r);
@@ -328,6 +345,24 @@ __global__ void __launch_bounds__(kScanThreads, PER == kPerLarge ? kCtasLarge : 
   if (bad) report(a.status, MK_ERR_NAN, PO_SELECT, row, chunk);
   u64* out = a.cand + ((long long)row * a.chunks + chunk) * K;
   for (int b = tid; b < K; b += kScanThreads) out[b] = b < s_n ? s_list[b] : 0ull;
+  const float largest = value_of(s_list[0]);
+  // (256 below the bound: what is left out then is less than e^-256 of the part's largest term)
+  const bool far = fabsf(largest) > kNear - 256.f && fabsf(largest) <= kLargest;
+  if (far) {
+    ref = s = comp = 0.f;
+    for (int it = 0; it < steps; ++it) {
+      load(it, x);
+      float q = 0.f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const float y = x[i] <= kLargest ? exp_of(x[i] - largest) : 0.f;
+        q += y;
+      }
+      const float sum = s + q, r = sum - s;
+      comp += (s - (sum - r)) + (q - r);
+      s = sum;
+    }
+  }
   float top_ref = ref;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top_ref = fmaxf(top_ref, __shfl_xor_sync(0xffffffffu, top_ref, o));
@@ -349,7 +384,7 @@ __global__ void __launch_bounds__(kScanThreads, PER == kPerLarge ? kCtasLarge : 
     u64 all = 0;
 #pragma unroll
     for (int w = 0; w < kScanWarps; ++w) all += s_warp[w];
-    a.stat[(long long)row * a.chunks + chunk] = Stat{top_ref, 0.f, all};
+    a.stat[(long long)row * a.chunks + chunk] = Stat{far ? largest : top_ref, far, all};
   }
 }
 
@@ -404,7 +439,7 @@ __global__ void __launch_bounds__(32 * kMaxBeams) pick_kernel(const __grid_const
   // what is computed from that is not used)
   const int ended = a.ended[row];
   float sc = a.scores[row];
-  Stat part{-INFINITY, 0.f, 0ull};
+  Stat part{-INFINITY, 0, 0ull};
   if (lane < a.chunks) part = st[lane];
   u64 k[8];
   k[0] = lane < total ? cand[lane] : 0ull;
@@ -421,10 +456,31 @@ __global__ void __launch_bounds__(32 * kMaxBeams) pick_kernel(const __grid_const
   ref = value_of((u64)__reduce_max_sync(0xffffffffu, orderable(ref)) << 32);
   auto share = [&](const Stat& s) { return s.n > ref - 64.f ? s.sum >> (int)(ref - s.n) : 0ull; };
   u64 sum = share(part);
-  for (int c = 32; c < a.chunks; c += 32) sum += share(c + lane < a.chunks ? st[c + lane] : Stat{-INFINITY, 0.f, 0ull});
+  for (int c = 32; c < a.chunks; c += 32) sum += share(c + lane < a.chunks ? st[c + lane] : Stat{-INFINITY, 0, 0ull});
+  int far = part.far;
+  for (int c = 32; c < a.chunks; c += 32) far |= c + lane < a.chunks ? st[c + lane].far : 0;
+  far = __any_sync(0xffffffffu, far);
+  float base = 0.f;  // the row's sum is e^base 2^shift times the whole number
+  if (far) {
+    // a part against its largest logit: the row's sum against the row's, natural exponents
+    base = -INFINITY;
+    for (int c = lane; c < a.chunks; c += 32) base = fmaxf(base, value_of(cand[c * K]));
+    base = value_of((u64)__reduce_max_sync(0xffffffffu, orderable(base)) << 32);
+    sum = 0ull;
+    for (int c = lane; c < a.chunks; c += 32) {
+      const Stat p = st[c];
+      const float f = p.far ? exp_of(p.n - base) : p.n > -INFINITY ? term_of(-base, -p.n) : 0.f;
+      sum += __double2ull_rn(__ull2double_rn(p.sum) * f);
+    }
+    ref = 0.f;
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const Pair lse = ln_of(sum, ref - (float)a.sum_bits);
+  Pair lse = ln_of(sum, ref - (float)a.sum_bits);
+  if (far) {
+    const Pair p = two_sum(base, lse.hi);
+    lse = two_sum(p.hi, p.lo + lse.lo);
+  }
   u64 mine = 0ull;  // lane q: the q-th best
   if (total <= 64)
     take_best<2>(k, K, lane, &mine);

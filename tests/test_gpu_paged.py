@@ -710,6 +710,100 @@ def test_select_wide_ranges(paged, dtype):
     _check_select(got, logits, scores, ended, -1)
 
 
+# --------------------------------------------------------------- selection over finite masks
+def _select_exact(logits, scores, ended, eos):
+    """The selection in 64 bits on the GPU, with log softmax as (x - max) - log sum e^(x - max): the maximum of a
+    row of large logits takes nothing from the sum."""
+    groups, beams = scores.shape
+    x = logits.double()
+    top = x.amax(-1, keepdim=True)
+    top = torch.where(top == -math.inf, 0.0, top)
+    lsum = torch.exp(x - top).sum(-1, keepdim=True).log()
+    best, token = torch.sort(x, dim=-1, descending=True, stable=True)
+    best, token = best[:, :beams], token[:, :beams]
+    s, done = scores.double().view(-1, 1), ended.view(-1, 1) != 0
+    key = torch.where(best == -math.inf, -math.inf, s + ((best - top) - lsum))
+    first = torch.arange(beams, device=DEV)[None] == 0
+    key = torch.where(done, torch.where(first, s, -math.inf), key).view(groups, -1)
+    token = torch.where(done, eos, token).view(groups, -1)
+    key, at = torch.sort(key, dim=-1, descending=True, stable=True)
+    key, at = key[:, :beams], at[:, :beams]
+    return token.gather(1, at), torch.arange(groups, device=DEV)[:, None] * beams + at // beams, key
+
+
+def _check_select_exact(got, logits, scores, ended, eos=-1):
+    """As _check_select, against _select_exact."""
+    token, parent, key = _select_exact(logits, scores, ended, eos)
+    assert torch.equal(got[0].long(), token)
+    assert torch.equal(got[1].long(), parent)
+    off, same = (got[2].double() - key).abs(), got[2].double() == key
+    assert torch.all(same | (off <= 2.0 ** -24 * key.abs() + 2.0 ** -19)), off[~same].max()
+
+
+MASKS = [-1e4, -1e9, -1e10, -1e12, -1e18, -1e20, -1e30]
+
+
+@pytest.mark.parametrize("mask", MASKS)
+@pytest.mark.parametrize("kind", ["allowed first", "allowed last", "half", "three quarters", "thin"])
+@pytest.mark.parametrize("groups,beams,vocab,dtype", [(16, 8, 70000, "f32"), (16, 8, 70001, "bf16"), (2, 32, 32000, "f32"),
+                                                      (1, 4, 9001, "f32"), (1, 4, 9001, "bf16")])
+def test_select_finite_masks(paged, mask, kind, groups, beams, vocab, dtype):
+    """A mask that is a large negative number, in parts of one step and of several, with the allowed tokens in
+    the first or in the last step, behind masked steps, or in between: a masked logit's exponential is 0."""
+    logits, scores, ended = _select_inputs(groups, beams, vocab, dtype, seed=3)
+    i = torch.arange(vocab, device=DEV)
+    allowed = {"allowed first": (i >= 3) & (i < 43), "allowed last": i >= vocab - 41, "half": i >= vocab // 2,
+               "three quarters": i >= vocab * 3 // 4, "thin": i % 500 == 7}[kind]
+    if kind == "thin" and vocab < 500 * beams:
+        allowed = i % 50 == 7
+    logits[:, ~allowed] = mask
+    _check_select_exact(paged.beam_select(logits, scores, ended), logits, scores, ended)
+
+
+@pytest.mark.parametrize("value", MASKS + [1e9, 1e10, 1e18, 8e37, -8e37])
+@pytest.mark.parametrize("groups,beams,vocab,dtype", [(16, 8, 70000, "f32"), (16, 8, 70000, "bf16"), (1, 4, 9001, "f32"),
+                                                      (2, 3, 50, "bf16")])
+def test_select_rows_of_one_large_value(paged, value, groups, beams, vocab, dtype):
+    """Rows whose every logit is one value offer each token at -ln(vocab), whatever the value; live rows among them."""
+    logits, scores, ended = _select_inputs(groups, beams, vocab, dtype, seed=4)
+    logits[::2] = value
+    _check_select_exact(paged.beam_select(logits, scores, ended), logits, scores, ended)
+
+
+@pytest.mark.parametrize("value", [1e9, 1e10, 1e18, 1e30])
+@pytest.mark.parametrize("at", [0, 5000, 69999])
+def test_select_one_large_logit(paged, value, at):
+    """One logit far above the others takes the whole sum, in a part of its own or not."""
+    logits, scores, ended = _select_inputs(16, 8, 70000, "f32", seed=5)
+    logits[:, at] = value
+    _check_select_exact(paged.beam_select(logits, scores, ended), logits, scores, ended)
+
+
+@pytest.mark.parametrize("power", [12, 18, 20, 21, 22])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_select_rows_around_a_power_of_two(paged, power, sign):
+    """Rows that lie within a few hundred of +-2^power: their largest logits are a step of 32 bits apart there, and
+    count for the sum on both sides of it.  (Ties are frequent; they go to the lowest token and beam.)"""
+    g = torch.Generator(device=DEV).manual_seed(power)
+    x = (torch.rand(24, 40000, generator=g, device=DEV, dtype=torch.float64) - 0.5) * 600 + sign * 2.0 ** power
+    x[:, ::1000] = sign * 2.0 ** power + 300 + torch.arange(40, device=DEV)
+    x[1::3, :30000] -= 2000
+    scores = -20 * torch.rand(6, 4, generator=g, device=DEV)
+    ended = torch.zeros(6, 4, dtype=torch.int32, device=DEV)
+    logits = x.float()
+    _check_select_exact(paged.beam_select(logits, scores, ended), logits, scores, ended)
+
+
+def test_select_large_steps_that_rise(paged):
+    """A row whose steps' largest logits go from -1e30 over -1e9, 0 and 1e9 to 1e30, a few equal ones in each."""
+    logits, scores, ended = _select_inputs(8, 4, 90000, "f32", seed=6)
+    for k, v in enumerate([-1e30, -1e9, None, 1e9, 1e30]):
+        if v is not None:
+            logits[:, 18000 * k: 18000 * (k + 1)] = v
+    for top in (5, 4, 3, 2, 1):
+        _check_select_exact(paged.beam_select(logits[:, : 18000 * top], scores, ended), logits[:, : 18000 * top], scores, ended)
+
+
 # ------------------------------------------------------------------------------ refusals
 def test_tensors_that_do_not_fit_are_refused(paged):
     """Shapes, types, layouts and devices, each refused before anything is enqueued."""
