@@ -470,7 +470,7 @@ mk_status mk_update_pages_workspace(int n_rows, int table_width, int n_pages, si
  * first: tokens, parents (the row chosen from: what mk_update_pages takes), scores, ended.
  * Within a beam the order is by logit, ties to the lowest token; between beams by the score
  * to about 2^-30 (before it is rounded to 32 bits), ties to the lower beam.  A logit above
- * 2^126 is taken for +inf, one below -2^126 may be for -inf.  A NaN or +inf logit or score is
+ * 2^126 counts as +inf, one below -2^126 as -inf.  A NaN or +inf logit or score is
  * reported (MK_ERR_NAN) and counts as -inf; a token at -inf is only chosen when nothing else is left.  Outputs must not overlap
  * the inputs. */
 typedef struct {

@@ -62,10 +62,10 @@ __device__ __forceinline__ float value_of(u64 key) {
 }
 __device__ __forceinline__ int token_of(u64 key) { return (int)(0xFFFFFFFFu - (unsigned)key); }
 
-// the least float above x (x not +inf)
+// the least logit above x (x not +inf): what lies below -kLargest is -inf
 __device__ __forceinline__ float above(float x) {
   const uint32_t u = orderable(x + 0.f) + 1u;
-  return value_of((u64)(x == -INFINITY ? orderable(-0x1.fffffep127f) : u) << 32);
+  return value_of((u64)(x == -INFINITY ? orderable(-kLargest) : u) << 32);
 }
 
 // the largest of the warp's keys (each lane's own, 0: none)
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kScanThreads, PER == kPerLarge ? kCtasLarge : 
 #pragma unroll
         for (int z = 1; z < PER; ++z) y = z == i ? x[z] : y;
         if (e >= n) continue;
-        const u64 k = key_of(y, first + e);
+        const u64 k = key_of(y < -kLargest ? -INFINITY : y, first + e);
         const int p = atomicAdd(&s_n, 1);
         if (p < kList) s_list[p] = k;
       }
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kScanThreads, PER == kPerLarge ? kCtasLarge : 
 #pragma unroll 16
         for (int e = from + tid; e < seen; e += kScanThreads) {
           float y = Conv<T>::up(src[e]);
-          if (!(y <= kLargest)) y = -INFINITY;
+          if (!(y <= kLargest) || y < -kLargest) y = -INFINITY;
           const u64 z = key_of(y, first + e);
           if (z < last && z > k) k = z;
         }

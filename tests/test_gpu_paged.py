@@ -804,6 +804,25 @@ def test_select_large_steps_that_rise(paged):
         _check_select_exact(paged.beam_select(logits[:, : 18000 * top], scores, ended), logits[:, : 18000 * top], scores, ended)
 
 
+@pytest.mark.parametrize("place", [0.0, 0.3, 0.9])
+@pytest.mark.parametrize("groups,beams,vocab,dtype", [(1, 8, 1000, "f32"), (1, 8, 20000, "f32"), (16, 8, 70000, "f32"),
+                                                      (16, 8, 70000, "bf16"), (2, 3, 300, "bf16"), (2, 3, 20000, "bf16")])
+def test_select_of_fewer_tokens_than_beams_over_the_lowest_mask(paged, place, groups, beams, vocab, dtype):
+    """One live beam, two allowed tokens, the type's lowest in the place of -inf: what is below -2^126 counts as
+    -inf wherever it lies, and of equal logits the lowest tokens are chosen."""
+    logits, scores, ended = _select_inputs(groups, beams, vocab, dtype, seed=7)
+    i, at = torch.arange(vocab, device=DEV), int(place * vocab)
+    logits[:, (i < at) | (i >= at + 2)] = torch.finfo(logits.dtype).min
+    logits[:, (i % 2 == 1) & (i != at) & (i != at + 1)] = -math.inf
+    scores[:, 1:] = -math.inf
+    got = paged.beam_select(logits, scores, ended)
+    logits[logits < -2.0 ** 126] = -math.inf
+    _check_select_exact(got, logits, scores, ended)
+    logits[:, at: at + 2] = -math.inf
+    lowest = torch.full_like(logits, torch.finfo(logits.dtype).min)
+    _check_select_exact(paged.beam_select(lowest, scores, ended), logits, scores, ended)
+
+
 # ------------------------------------------------------------------------------ refusals
 def test_tensors_that_do_not_fit_are_refused(paged):
     """Shapes, types, layouts and devices, each refused before anything is enqueued."""
