@@ -120,10 +120,12 @@ __device__ __forceinline__ Pair ln_of(u64 u, float shift) {
   const Pair s = two_sum(ph, 2.f * th);
   return two_sum(s.hi, s.lo + (pl + fmaf(th, rest, 2.f * tl)));
 }
-// score + (v - lse), and a pair as an unsigned number of the same order
+// score + (v - lse), -inf where it lies below the floats, and a pair as an unsigned number of
+// the same order
 __device__ __forceinline__ Pair score_of(float score, float v, Pair lse) {
   const Pair d = two_sum(v, -lse.hi), s = two_sum(score, d.hi);
-  return two_sum(s.hi, s.lo + (d.lo - lse.lo));
+  const Pair t = two_sum(s.hi, s.lo + (d.lo - lse.lo));
+  return t.hi > -INFINITY ? t : Pair{-INFINITY, 0.f};  // (past the range t is NaN)
 }
 __device__ __forceinline__ u64 ordered(Pair p) { return (u64)orderable(p.hi + 0.f) << 32 | orderable(p.lo + 0.f); }
 

@@ -823,6 +823,24 @@ def test_select_of_fewer_tokens_than_beams_over_the_lowest_mask(paged, place, gr
     _check_select_exact(paged.beam_select(lowest, scores, ended), logits, scores, ended)
 
 
+@pytest.mark.parametrize("vocab", [500, 20000])
+def test_select_sums_beyond_the_range_of_32_bits(paged, vocab):
+    """Scores and logits whose sum lies below the lowest float: such a candidate's score is -inf, and not NaN."""
+    logits, scores, ended = _select_inputs(2, 4, vocab, "f32", seed=8)
+    scores[:] = -3.3e38 + torch.arange(4, device=DEV) * 1e37
+    logits[:, 3:] = -8e37
+    logits[4:, 1:] = -8e37
+    got = paged.beam_select(logits, scores, ended)
+    token, parent, key = _select_exact(logits, scores, ended, -1)
+    assert torch.equal(got[0].long(), token) and torch.equal(got[1].long(), parent)
+    assert torch.equal(got[2], key.float())
+    scores[:, 1:] = -math.inf
+    got = paged.beam_select(logits, scores, ended)
+    token, parent, key = _select_exact(logits, scores, ended, -1)
+    assert torch.equal(got[0].long(), token) and torch.equal(got[1].long(), parent)
+    assert torch.equal(got[2], key.float()) and key.float().isneginf().any()
+
+
 # ------------------------------------------------------------------------------ refusals
 def test_tensors_that_do_not_fit_are_refused(paged):
     """Shapes, types, layouts and devices, each refused before anything is enqueued."""
