@@ -469,10 +469,13 @@ mk_status mk_update_pages_workspace(int n_rows, int table_width, int n_pages, si
  * offers token `eos` at its own score.  The `beams` best of the group are chosen, best
  * first: tokens, parents (the row chosen from: what mk_update_pages takes), scores, ended.
  * Within a beam the order is by logit, ties to the lowest token; between beams by the score
- * to about 2^-30 (before it is rounded to 32 bits), ties to the lower beam.  A logit above
- * 2^126 counts as +inf, one below -2^126 as -inf.  A NaN or +inf logit or score is
- * reported (MK_ERR_NAN) and counts as -inf; a token at -inf is only chosen when nothing else is left.  Outputs must not overlap
- * the inputs. */
+ * before it is rounded to 32 bits, ties to the lower beam.  That score holds a log-sum-exp good
+ * to 2^-19 (32-bit exponentials by the hardware's approximation, 2 ulp): beams whose exact
+ * scores are closer than twice that may come in either order, always the same one for the same
+ * inputs, and beams of identical rows and scores in the order of their numbers.  A logit above
+ * 2^126 counts as +inf, one below -2^126 as -inf.  A NaN or +inf logit or score is reported
+ * (MK_ERR_NAN) and counts as -inf; a token at -inf is only chosen when nothing else is left.
+ * Outputs must not overlap the inputs. */
 typedef struct {
   const void* logits;      /* [groups * beams][row_stride], the first vocab entries used    */
   int dtype;               /* MK_F16, MK_BF16 or MK_F32                                     */

@@ -88,7 +88,9 @@ __device__ __forceinline__ float exp_of(float y) { return term_of(y, 0.f); }
 // 2^d for a whole d in [-126, 127], exactly; 0 below
 __device__ __forceinline__ float power_of(float d) { return d < -126.f ? 0.f : __int_as_float((127 + (int)d) << 23); }
 
-// Numbers as a pair of floats (hi + lo, |lo| at most half a step of hi): about 48 bits, from
+// Numbers as a pair of floats (hi + lo, |lo| at most half a step of hi), so that scores are
+// compared before they are rounded to 32 bits (a score of -100 has steps of 2^-17 there; the
+// log-sum-exp in it is good to 2^-19, so that no more than that is decided): 48 bits, from
 // 32-bit instructions -- 64-bit log alone took 1.3 us of a launch of 5.
 struct Pair {
   float hi, lo;

@@ -841,6 +841,33 @@ def test_select_sums_beyond_the_range_of_32_bits(paged, vocab):
     assert torch.equal(got[2], key.float()) and key.float().isneginf().any()
 
 
+def test_select_orders_beams_up_to_the_accuracy_of_their_sums(paged):
+    """Beams of identical rows and equal scores tie: the lower beam's tokens come first.  Rows that are permutations of
+    one another have the same exact log-sum-exp, which each of them sees to 2^-19 (as _check_select says): their
+    beams come in order once the scores are further apart than twice that, and below in an order of their own, with
+    scores that are right all the same."""
+    logits, _, _ = _select_inputs(1, 1, 30000, "f32", seed=10)
+    ended = torch.zeros(3, 4, dtype=torch.int32, device=DEV)
+    rows = logits.expand(12, -1).contiguous()
+    scores = torch.full((3, 4), -3.25, device=DEV)
+    token, parent, best, _ = paged.beam_select(rows, scores, ended)
+    top = int(logits.argmax())
+    assert token.tolist() == [[top] * 4] * 3 and parent.tolist() == [[0, 1, 2, 3], [4, 5, 6, 7], [8, 9, 10, 11]]
+    assert torch.all(best == best[0, 0])
+    g = torch.Generator(device=DEV).manual_seed(11)
+    perms = [torch.randperm(30000, generator=g, device=DEV) for _ in range(12)]
+    rows = torch.stack([logits[0][p] for p in perms])
+    want = (logits.double().amax() - torch.logsumexp(logits.double(), -1)).item() - 3.25
+    for gap in (0.0, 2.0 ** -24, 2.0 ** -16):
+        scores = torch.full((3, 4), -3.25, device=DEV) + gap * torch.arange(4, device=DEV)
+        token, parent, best, _ = paged.beam_select(rows, scores, ended)
+        assert torch.all((best.double() - want - (scores.double() + 3.25).gather(1, parent.long() % 4)).abs() <= 2.0 ** -24 * 16 + 2.0 ** -19)
+        assert sorted(parent.flatten().tolist()) == list(range(12))
+        assert all(int(perms[p][t]) == top for p, t in zip(parent.flatten().tolist(), token.flatten().tolist()))
+        if gap > 2.0 ** -18:
+            assert parent.tolist() == [[3, 2, 1, 0], [7, 6, 5, 4], [11, 10, 9, 8]]
+
+
 # ------------------------------------------------------------------------------ refusals
 def test_tensors_that_do_not_fit_are_refused(paged):
     """Shapes, types, layouts and devices, each refused before anything is enqueued."""
