@@ -398,8 +398,9 @@ mk_status mk_rope_append(const mk_append_args* args, const mk_page_view* cache, 
  * scores are all -inf gets zeros and lse -inf.  Nothing outside that range is read for its
  * value: whatever lies there, NaN included, has no effect.  A row outside the table counts
  * as empty, positions past the table are dropped and those on a bad page masked, each of
- * them reported (MK_ERR_PAGES).  A query that is not of the cache's type must lie within
- * the cache type's range.  A NaN or infinite value inside the range makes that row's results
+ * them reported (MK_ERR_PAGES).  A query that is not of the cache's type is taken to 22 bits
+ * of its head's largest element over an fp16 cache, to all of its bits over a bf16 cache, at
+ * any size below 2^127.  A NaN or infinite value inside the range makes that row's results
  * NaN or infinite, as does a NaN key; an infinite key does, unless the query is of the
  * cache's type and the scores stay below +inf.  Results do not depend on timing.
  * n_rows * n_kv_heads * (positions / 16 + 9) must be below 2^31 - 2^24, positions being the

@@ -214,6 +214,18 @@ constexpr float kProbShift = 0.f;
 template <>
 constexpr float kProbShift<__half> = 14.f;
 
+// A query that is split into fp16 parts is first brought near the top of their range, every head
+// by a power of two of its own (2^shift times its largest element lies in [2^14, 2^15)) that the
+// score's factor takes back: else the second part of an element below 1/8 was a subnormal
+// number, and one below 2^-25 or above 65504 lost altogether.
+template <typename C, typename Q>
+constexpr bool kScaled = std::is_same<C, __half>::value && !std::is_same<Q, __half>::value;
+__device__ __forceinline__ int shift_of(float largest) {
+  const int e = __float_as_int(largest) >> 23;  // (largest >= 0; zeros, infinities and NaN stay as they are)
+  return e == 0 || e == 255 ? 0 : min(127 + 14 - e, 126);
+}
+__device__ __forceinline__ float power_of(int e) { return __int_as_float((127 + e) << 23); }  // 2^e, |e| <= 126
+
 // four bytes from global to shared memory, without a register between
 __device__ __forceinline__ void cp_async4(int* dst, const int* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
@@ -233,6 +245,7 @@ struct AttState {
   int at, end, share, before;  // next unit, end of the CTA's units, share; units before `row`
   int sums[kAttWarps][3];
   int row, head, slot, lead, pitch, bad, bad_page;
+  float scale[kMaxGroup];      // kScaled: a head's factor from products to scores
   int pages[kAttWarps][64];    // of a warp's tiles: the k-th one's at k mod 64
 };
 template <int HD, bool WIDE, int NQ>
@@ -349,10 +362,12 @@ __global__ void __launch_bounds__(kAttThreads, ctas_per_sm(HD)) attend_kernel(co
     // the query's fragments: chunk i, lane (g, c): dims [32 i + 8 c, + 8) of head g.  Asked for
     // here, stored behind the first keys' loads, which need not wait for them.
     constexpr int kAsk = CH * HEADS * 4 / kAttThreads > 0 ? CH * HEADS * 4 / kAttThreads : 1;
+    constexpr bool SCALED = kScaled<C, Q>;  // a head's chunks are then in neighbouring lanes of one warp
     Raw8<Q> ask[kAsk];
 #pragma unroll
     for (int z = 0; z < kAsk; ++z) {
-      const int y = tid + z * kAttThreads, h = (y >> 2) % HEADS, i = y / (4 * HEADS);
+      const int y = tid + z * kAttThreads, h = SCALED ? y / (4 * CH) : (y >> 2) % HEADS;
+      const int i = SCALED ? (y >> 2) % CH : y / (4 * HEADS);
       const Q* src = static_cast<const Q*>(a.q) + (long long)st->row * a.q_row +
                      (long long)(st->head * a.group + h) * a.q_head + 32 * i + 8 * (y & 3);
       ask[z] = {};
@@ -404,8 +419,9 @@ __global__ void __launch_bounds__(kAttThreads, ctas_per_sm(HD)) attend_kernel(co
     }
 #pragma unroll
     for (int z = 0; z < kAsk; ++z) {
-      const int y = tid + z * kAttThreads, h = (y >> 2) % HEADS, i = y / (4 * HEADS);
-      if (i >= CH) continue;
+      const int y = tid + z * kAttThreads, h = SCALED ? y / (4 * CH) : (y >> 2) % HEADS;
+      const int i = SCALED ? (y >> 2) % CH : y / (4 * HEADS);
+      if (SCALED ? h >= HEADS : i >= CH) continue;  // (whole warps)
       uint32_t w[4][NQ];
       if constexpr (std::is_same<C, Q>::value) {
         w[0][0] = ask[z].w[0].x;
@@ -415,6 +431,18 @@ __global__ void __launch_bounds__(kAttThreads, ctas_per_sm(HD)) attend_kernel(co
       } else {
         float v[8];
         ask[z].up(v);
+        if constexpr (SCALED) {
+          float most = fabsf(v[0]);
+#pragma unroll
+          for (int e = 1; e < 8; ++e) most = fmaxf(most, fabsf(v[e]));
+#pragma unroll
+          for (int x = 1; x < 4 * CH; x <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
+          const int shift = shift_of(most);
+          const float up = power_of(shift);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] *= up;
+          if (y % (4 * CH) == 0) st->scale[h] = a.scale * power_of(-shift);
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) split2<C, NQ>(v[2 * e], v[2 * e + 1], w[e]);
       }
@@ -438,6 +466,9 @@ __global__ void __launch_bounds__(kAttThreads, ctas_per_sm(HD)) attend_kernel(co
       l[h] = 0.f;
     }
     __syncthreads();
+    float scale[RH];  // of row g (WIDE: and row g + 8)
+#pragma unroll
+    for (int h = 0; h < RH; ++h) scale[h] = SCALED ? st->scale[g + 8 * h] : a.scale;
     for (int k = 0; k < mine; ++k) {
       if ((k & 31) == 0) {
         __syncwarp();  // what is overwritten was read
@@ -505,7 +536,7 @@ __global__ void __launch_bounds__(kAttThreads, ctas_per_sm(HD)) attend_kernel(co
           float y = s[e >> 1][2 * h + (e & 1)];
           // the second part's row; one part has none, and there 0 times an infinite key is NaN
           if (!WIDE && NQ > 1) y += s[e >> 1][2 + (e & 1)];
-          x[e] = y * a.scale;
+          x[e] = y * scale[h];
         }
         if (a.softcap > 0.f) {
 #pragma unroll
@@ -801,7 +832,8 @@ extern "C" mk_status mk_paged_attention(const mk_attend_args* args, const mk_pag
     a.scale = args->softcap > 0.f ? args->scale / args->softcap : args->scale * kLog2e;
     a.softcap = args->softcap * kLog2e;
     // 16-bit queries of the cache's type are exact in one part.  Other queries are split into
-    // 2 parts of fp16 (22 bits) or 3 of bf16 (24 bits); probabilities likewise, 2 parts of
+    // 2 parts of fp16 (22 bits, each head at a power of two of its own) or 3 of bf16 (24 bits);
+    // probabilities likewise, 2 parts of
     // bf16 (16 bits) being enough for an output of 16 bits.
     if (cache->dtype == MK_F16) {
       if (args->dtype == MK_F16) return launch_attend<__half, __half, 1, 2>(a, cache->head_dim, stream);

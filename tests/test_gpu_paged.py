@@ -237,6 +237,42 @@ def test_attention_types(paged, cache, vec, hq, hkv, hd):
     _attend_case(paged, [700, 3, 0, 1025, 128], hq, hkv, hd, 32, cache, vec, strided=True)
 
 
+@pytest.mark.parametrize("vec", ["f32", "bf16"])
+@pytest.mark.parametrize("power", [-100, -40, -24, -16, 8, 20, 60])
+@pytest.mark.parametrize("hq,hkv,hd", [(8, 2, 64), (4, 2, 128), (16, 1, 128), (12, 1, 64)])
+def test_attention_small_and_large_queries_over_fp16_pages(paged, vec, power, hq, hkv, hd):
+    """Queries far from 1 in size, with a scale that makes up for it: the same results as at size 1, bit for bit, as
+    a power of two is no rounding."""
+    g = torch.Generator(device=DEV).manual_seed(13)
+    lens = [300, 17, 0, 1]
+    kp, vp, table = _make_cache(g, lens, hkv, hd, 16, "f16")
+    q = torch.randn(4, hq, hd, generator=g, device=DEV).mul_(1.5).to(TYPES[vec])
+    want = paged.paged_attention(q, kp, vp, ints(table), ints(lens), scale=0.125, return_lse=True)
+    got = paged.paged_attention((q.float() * 2.0 ** power).to(q.dtype), kp, vp, ints(table), ints(lens),
+                                scale=0.125 * 2.0 ** -power, return_lse=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    _check_attend(q, kp, vp, table, lens, *want, 0.125)
+
+
+@pytest.mark.parametrize("vec", ["f32", "bf16"])
+def test_attention_queries_of_unlike_heads_over_fp16_pages(paged, vec):
+    """Heads, and elements of a head, of sizes from 1e-9 to 1e5 in one query, zeros and empty heads among them."""
+    g = torch.Generator(device=DEV).manual_seed(14)
+    lens = [200, 64, 33]
+    kp, vp, table = _make_cache(g, lens, 2, 128, 16, "f16")
+    q = torch.randn(3, 16, 128, generator=g, device=DEV)
+    q[0] *= 10.0 ** -torch.arange(16, device=DEV)[:, None] / 2
+    q[1, :, ::3] *= 1e-5
+    q[1, :, 1::3] = 0.0
+    q[2, 3:6] = 0.0
+    q = q.to(TYPES[vec])
+    out, lse = paged.paged_attention(q, kp, vp, ints(table), ints(lens), scale=0.2, return_lse=True)
+    _check_attend(q, kp, vp, table, lens, out, lse, 0.2)
+    q *= 2.0 ** 17
+    out, lse = paged.paged_attention(q, kp, vp, ints(table), ints(lens), scale=0.2 * 2.0 ** -17, return_lse=True)
+    _check_attend(q, kp, vp, table, lens, out, lse, 0.2 * 2.0 ** -17)
+
+
 @pytest.mark.parametrize("window,cap", [(1, 0.0), (16, 0.0), (100, 5.0), (1000000, 0.0), (0, 2.0), (33, 30.0)])
 @pytest.mark.parametrize("ps", [16, 48, 1024])
 def test_attention_windows_caps_and_pages(paged, window, cap, ps):
