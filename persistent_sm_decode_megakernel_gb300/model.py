@@ -222,10 +222,18 @@ class PagedDecoder:
         return torch.as_tensor(x, dtype=torch.int32, device=self.dm.device)
 
     def synchronize(self):
-        """Waits for the stream and raises MkError for what a step or a page update reported."""
+        """Waits for the stream and raises MkError for what a page update or a step reported: the update's where
+        both did, and neither report is left for a later call."""
+        from . import MkError
+        first = None
         with torch.cuda.stream(self.stream):
-            self.paged.check_status(self.status)
-        check(mk_synchronize(self.h), "mk_synchronize")
+            for read in (lambda: self.paged.check_status(self.status), lambda: check(mk_synchronize(self.h), "mk_synchronize")):
+                try:
+                    read()
+                except MkError as e:
+                    first = first or e
+        if first is not None:
+            raise first
 
     def update(self, parents=None, reserve=None):
         """Every row continues row parents[r] (-1: it is freed) and reserves pages for reserve[r] more

@@ -242,6 +242,31 @@ def test_prompts_that_do_not_fit_leave_the_rows_as_they_were(lib):
     dec.close()
 
 
+def test_a_refused_search_leaves_no_error_behind(lib):
+    """A beam search that runs out of pages raises once: what its steps reported besides (positions without a page)
+    does not come up in the next call."""
+    from persistent_sm_decode_megakernel_gb300 import MK_ERR_PAGES, MkError
+    cfg = synth.CONFIGS["tiny"]
+    w = synth.gen_weights(cfg)
+    prompt = synth.gen_prompts(cfg, 1, 30)[0]
+    dec = _paged(lib, cfg, w, 4, 4, 64, n_pages=6)
+    want = int(dec.prefill({0: prompt})[0])
+    with pytest.raises(MkError) as e:
+        dec.beam_search(prompt, 4, 20)             # four beams of 49 positions over six pages
+    assert e.value.status == MK_ERR_PAGES
+    assert int(dec.refs.sum()) == 0 and not dec.lens.any()
+    assert int(dec.prefill({1: prompt})[1]) == want
+    dec.synchronize()
+    dec.update(reserve=[0, 1000, 0, 0])            # refused, and a step of a row that has no page: both, one error
+    one = dec._int32([1])
+    dec.step(one, dec._int32([40]), dec._int32([3]))
+    with pytest.raises(MkError) as e:
+        dec.synchronize()
+    assert e.value.status == MK_ERR_PAGES
+    dec.synchronize()
+    dec.close()
+
+
 def test_steps_refuse_tensors_that_do_not_fit_and_capture(lib):
     from persistent_sm_decode_megakernel_gb300 import MK_ERR_STATE, mk_decode_step_paged
     cfg = synth.CONFIGS["tiny"]
