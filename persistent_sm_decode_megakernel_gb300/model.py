@@ -221,6 +221,12 @@ class PagedDecoder:
     def _int32(self, x):
         return torch.as_tensor(x, dtype=torch.int32, device=self.dm.device)
 
+    def _used(self, t):
+        """A caller's tensor that self.stream reads or writes: its memory is not given to anyone else before that."""
+        if t is not None and t.is_cuda:
+            t.record_stream(self.stream)
+        return t
+
     def synchronize(self):
         """Waits for the stream and raises MkError for what a page update or a step reported: the update's where
         both did, and neither report is left for a later call."""
@@ -237,16 +243,15 @@ class PagedDecoder:
 
     def update(self, parents=None, reserve=None):
         """Every row continues row parents[r] (-1: it is freed) and reserves pages for reserve[r] more
-        positions (mk_update_pages)."""
+        positions (mk_update_pages).  It runs on self.stream, where tensors given have to be ready."""
         with torch.cuda.stream(self.stream):
-            self.paged.update_pages(self.k, self.v, self.table, self.lens, self.refs,
-                                    None if parents is None else self._int32(parents),
-                                    None if reserve is None else self._int32(reserve), self.status)
+            parents, reserve = (None if x is None else self._used(self._int32(x)) for x in (parents, reserve))
+            self.paged.update_pages(self.k, self.v, self.table, self.lens, self.refs, parents, reserve, self.status)
 
     def step(self, tokens, positions, rows=None, logits=None):
         """One step of device int32 tensors: token i at positions[i] of table row rows[i] (default i).  The
         argmax tokens; positions need their pages (update).  lens is the caller's to advance.  It runs on
-        self.stream, where its tensors have to be ready."""
+        self.stream, where its tensors have to be ready; they may be dropped as soon as it returns."""
         from . import mk_decode_step_paged
         n = len(tokens)
         for name, t, shape, dtype in (("tokens", tokens, (n,), torch.int32), ("positions", positions, (n,), torch.int32),
@@ -257,6 +262,8 @@ class PagedDecoder:
             if tuple(t.shape) != shape or t.dtype != dtype or t.device != self.k.device or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {dtype} tensor of {shape} on {self.k.device}")
         with torch.cuda.stream(self.stream):
+            for t in (tokens, positions, rows, logits):
+                self._used(t)
             out = torch.empty(n, dtype=torch.int32, device=self.k.device)
             check(mk_decode_step_paged(self.h, tokens.data_ptr(), positions.data_ptr(),
                                        rows.data_ptr() if rows is not None else None, n, out.data_ptr(),
@@ -288,7 +295,7 @@ class PagedDecoder:
                     if j[3]:
                         last[j[2]] = out[i: i + 1]
                         if logits is not None:
-                            logits[j[2]].copy_(z[i])
+                            self._used(logits[j[2]]).copy_(z[i])
             self.lens += self._int32(reserve)
         return last
 

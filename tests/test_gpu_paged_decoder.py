@@ -267,6 +267,69 @@ def test_a_refused_search_leaves_no_error_behind(lib):
     dec.close()
 
 
+def _busy(stream):
+    """Some tens of milliseconds of work on a stream."""
+    with torch.cuda.stream(stream):
+        x = torch.randn(4096, 4096, device="cuda:0")
+        for _ in range(60):
+            x = x @ x * 1e-3
+
+
+def test_tensors_of_another_stream_live_until_they_were_read(lib):
+    """Tokens, positions, rows, logits, parents and reservations that the caller drops as soon as step and update
+    return, the decoder's stream being busy with something else: what the caller allocates next is other memory."""
+    cfg = synth.CONFIGS["tiny"]
+    w = synth.gen_weights(cfg)
+    prompt = synth.gen_prompts(cfg, 1, 20)[0]
+    got = []
+    for drop in (False, True):
+        dec = _paged(lib, cfg, w, 4, 4, 64, stream=torch.cuda.Stream())
+        dec.prefill({0: prompt, 2: prompt[:7]})
+        dec.synchronize()
+        torch.cuda.synchronize()
+        held, over = [], []
+
+        def ints(x):
+            t = dec._int32(x)
+            torch.cuda.current_stream().synchronize()  # ready before the other stream looks at it
+            if not drop:
+                held.append(t)
+            return t
+
+        def others(n):
+            for _ in range(8):                         # the next taker of what was dropped
+                over.append(torch.full((n,), 1, dtype=torch.int32, device=dec.dm.device))
+
+        _busy(dec.stream)
+        dec.update(ints([0, 0, 2, 2]), ints([3, 2, 1, 1]))
+        others(4)
+        z = torch.zeros(3, cfg.vocab, device=dec.dm.device)
+        torch.cuda.current_stream().synchronize()
+        out = dec.step(ints([5, 6, 7]), ints([20, 20, 7]), ints([0, 1, 2]), z)
+        others(3)
+        torch.cuda.synchronize()
+        dec.synchronize()
+        got.append((dec.table.clone(), dec.refs.clone(), out.clone(), z.clone()))
+        dec.close()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    # logits that are dropped do not become the caller's next tensor before they are written
+    dec = _paged(lib, cfg, w, 4, 1, 64, stream=torch.cuda.Stream())
+    dec.prefill({0: prompt})
+    dec.update(reserve=[3])
+    dec.synchronize()
+    one, pos = dec._int32([5]), dec._int32([20])
+    torch.cuda.synchronize()
+    _busy(dec.stream)
+    dec.step(one, pos, None, torch.empty(1, cfg.vocab, device=dec.dm.device))
+    mine = [torch.zeros(1, cfg.vocab, device=dec.dm.device) for _ in range(4)]
+    dec.synchronize()
+    assert not any(t.any() for t in mine)
+    dec.update(parents=[-1])
+    dec.prefill({0: prompt}, {0: torch.empty(cfg.vocab, device=dec.dm.device)})
+    dec.synchronize()
+    dec.close()
+
+
 def test_steps_refuse_tensors_that_do_not_fit_and_capture(lib):
     from persistent_sm_decode_megakernel_gb300 import MK_ERR_STATE, mk_decode_step_paged
     cfg = synth.CONFIGS["tiny"]
