@@ -203,13 +203,15 @@ class PagedDecoder:
             r = ctypes.byref(mk_rope_desc(kw["theta"], kw["n_rot"], paged.ROPE_KINDS[kw["kind"]], kw["factor"],
                                           kw["original"], kw["beta_fast"], kw["beta_slow"]))
         h = ctypes.c_void_p()
-        check(mk_create_paged(ctypes.byref(d), ctypes.byref(w), ctypes.byref(pk), r, int(interleaved), None,
-                              ctypes.c_void_p(self.stream.cuda_stream), ctypes.byref(h)), "mk_create_paged")
+        with torch.cuda.device(dm.device):
+            check(mk_create_paged(ctypes.byref(d), ctypes.byref(w), ctypes.byref(pk), r, int(interleaved), None,
+                                  ctypes.c_void_p(self.stream.cuda_stream), ctypes.byref(h)), "mk_create_paged")
         self.h = h
 
     def close(self):
         if getattr(self, "h", None):
-            mk_destroy(self.h)
+            with torch.cuda.device(self.dm.device):
+                mk_destroy(self.h)
             self.h = None
 
     def __del__(self):

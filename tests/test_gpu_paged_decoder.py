@@ -330,6 +330,31 @@ def test_tensors_of_another_stream_live_until_they_were_read(lib):
     dec.close()
 
 
+def test_contexts_are_made_and_freed_on_their_models_device(lib, monkeypatch):
+    """Whatever device is current: the calls that allocate and free run with the model's."""
+    import persistent_sm_decode_megakernel_gb300 as pkg
+    inside, seen = [], []
+
+    class Device(torch.cuda.device):
+        def __enter__(self):
+            inside.append(torch.device("cuda", self.idx))
+            return super().__enter__()
+
+        def __exit__(self, *a):
+            inside.pop()
+            return super().__exit__(*a)
+
+    cfg = synth.CONFIGS["tiny"]
+    w = synth.gen_weights(cfg)
+    create, destroy = pkg.mk_create_paged, lib.mk_destroy
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(pkg, "mk_create_paged", lambda *a: (seen.append(list(inside)), create(*a))[1])
+    monkeypatch.setattr(lib, "mk_destroy", lambda *a: (seen.append(list(inside)), destroy(*a))[1])
+    dec = _paged(lib, cfg, w, 1, 1, 16)
+    dec.close()
+    assert len(seen) == 2 and all(s and s[-1] == dec.dm.device for s in seen)
+
+
 def test_steps_refuse_tensors_that_do_not_fit_and_capture(lib):
     from persistent_sm_decode_megakernel_gb300 import MK_ERR_STATE, mk_decode_step_paged
     cfg = synth.CONFIGS["tiny"]
