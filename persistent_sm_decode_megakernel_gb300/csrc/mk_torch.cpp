@@ -49,6 +49,19 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
     value_error(std::string(name) + " requires a gradient, and none is recorded here (torch.no_grad())");
   return t;
 }
+// A tensor that the call writes in place counts as changed, as after torch's own operators (one
+// of inference mode has no count)
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(PyObject* o) {
+  if (o != Py_None) written(THPVariable_Unpack(o));
+}
+template <typename... Objects>
+void written(PyObject* o, Objects... more) {
+  written(o);
+  written(more...);
+}
 const at::Tensor& on_gpu(PyObject* o, const char* name) {
   const at::Tensor& t = tensor(o, name);
   if (!t.is_cuda()) value_error(std::string(name) + " must be a CUDA tensor");
@@ -242,7 +255,10 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     x.interleaved = PyObject_IsTrue(a[9]);
     x.mscale = (float)number(a[10]);
     int32_t* status = status_of(a[12], dev);
-    if (n > 0) check(mk_rope_append(&x, &view, status, stream_of(dev)), "mk_rope_append");
+    if (n > 0) {
+      check(mk_rope_append(&x, &view, status, stream_of(dev)), "mk_rope_append");
+      written(a[3], a[4], a[11], a[12]);
+    }
     if (a[0] == Py_None) Py_RETURN_NONE;
     return a[11] == Py_None ? wrap(out) : given(a[11]);
   });
@@ -286,6 +302,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
       const Workspace ws(x.workspace_bytes);
       x.workspace = ws.p.get();
       check(mk_paged_attention(&x, &view, status, stream_of(dev)), "mk_paged_attention");
+      written(a[10], a[12]);
     }
     PyObject* o = a[10] == Py_None ? wrap(out) : given(a[10]);
     if (with_lse <= 0 || !o) return o;
@@ -329,6 +346,7 @@ PyObject* update_pages(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const Workspace ws(x.workspace_bytes);
     x.workspace = ws.p.get();
     check(mk_update_pages(&x, &pool, status, stream_of(dev)), "mk_update_pages");
+    written(a[0], a[1], a[2], a[3], a[4], a[7]);
     Py_RETURN_NONE;
   });
 }
@@ -345,6 +363,7 @@ PyObject* compact_pages(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     check(mk_update_pages_workspace(pool.n_rows, pool.table_width, pool.n_pages, &bytes), "mk_update_pages_workspace");
     const Workspace ws(bytes);
     check(mk_compact_pages(&pool, ws.p.get(), bytes, status, stream_of(dev)), "mk_compact_pages");
+    written(a[0], a[1], a[2], a[3], a[4]);
     Py_RETURN_NONE;
   });
 }
@@ -384,6 +403,7 @@ PyObject* beam_select(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     x.out_ended = done.data_ptr<int32_t>();
     x.out_scores = best.data_ptr<float>();
     check(mk_beam_select(&x, status, stream_of(dev)), "mk_beam_select");
+    written(a[4]);
     return Py_BuildValue("(NNNN)", wrap(token), wrap(parent), wrap(best), wrap(done));
   });
 }
@@ -399,6 +419,7 @@ PyObject* check_status(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     Py_BEGIN_ALLOW_THREADS
     s = mk_paged_status(status, stream_of(dev));
     Py_END_ALLOW_THREADS
+    if (s != MK_OK) written(a[0]);  // cleared
     check(s, "paged status");
     Py_RETURN_NONE;
   });

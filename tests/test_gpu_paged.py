@@ -954,6 +954,44 @@ def test_tensors_that_do_not_fit_are_refused(paged):
     assert pages.abs().sum() == 0
 
 
+def test_what_is_written_in_place_counts_as_changed(paged):
+    """The version of every tensor a call writes goes up, and of no other, so that torch refuses a backward pass over
+    what a call has changed since; tensors of inference mode have none and are taken as they are."""
+    g = torch.Generator(device=DEV).manual_seed(15)
+    pages = torch.randn(2, 1, 6, 2, 16, 64, generator=g, device=DEV).bfloat16()
+    k, v = pages[0].clone(), pages[1].clone()
+    table, lens, refs, st = ints([[0, 1], [2, 3]]), ints([5, 20]), ints([1, 1, 1, 1, 0, 0]), status()
+    q, kv = torch.randn(2, 4, 64, generator=g, device=DEV).bfloat16(), torch.randn(2, 2, 64, generator=g, device=DEV).bfloat16()
+    out, pos, rows = torch.zeros_like(q), ints([1, 2]), ints([0, 1])
+    logits, scores, ended = torch.randn(2, 50, generator=g, device=DEV), torch.zeros(1, 2, device=DEV), ints([[0, 0]])
+    named = dict(k=k, v=v, table=table, lens=lens, refs=refs, st=st, q=q, kv=kv, out=out, pos=pos, rows=rows,
+                 logits=logits, scores=scores, ended=ended)
+
+    def written(call):
+        before = {n: t._version for n, t in named.items()}
+        call()
+        return {n for n, t in named.items() if t._version > before[n]}
+
+    assert written(lambda: paged.rope_append(q, kv, kv, k[0], v[0], table, pos, rows=rows)) == {"k", "v"}
+    assert written(lambda: paged.rope_append(q, kv, kv, k[0], v[0], table, pos, q_out=out, status=st)) == {"k", "v", "out", "st"}
+    assert written(lambda: paged.rope_append(q[:0], kv[:0], kv[:0], k[0], v[0], table, pos[:0], q_out=out[:0], status=st)) == set()
+    assert written(lambda: paged.paged_attention(q, k[0], v[0], table, lens)) == set()
+    assert written(lambda: paged.paged_attention(q, k[0], v[0], table, lens, out=out, status=st)) == {"out", "st"}
+    assert written(lambda: paged.update_pages(k, v, table, lens, refs)) == {"k", "v", "table", "lens", "refs"}
+    assert written(lambda: paged.compact_pages(k, v, table, refs, status=st)) == {"k", "v", "table", "refs", "st"}
+    assert written(lambda: paged.beam_select(logits, scores, ended)) == set()
+    assert written(lambda: paged.check_status(st)) == set()
+    w = torch.ones(64, device=DEV, dtype=torch.bfloat16, requires_grad=True)
+    y = (w * k).sum()                          # its backward pass wants k as it is now
+    paged.rope_append(None, kv, kv, k[0], v[0], table, pos)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():
+        k2, v2 = pages[0].clone(), pages[1].clone()
+    paged.rope_append(None, kv, kv, k2[0], v2[0], table, pos)
+    assert torch.equal(k2[0, 0, :, 1], kv[0])
+
+
 # ------------------------------------------------------------------------------ all of them
 def test_a_beam_search_of_the_four_operators_captured(paged):
     """Steps as a beam search makes them -- reserve and fork, append, attend, select -- eagerly and as one
