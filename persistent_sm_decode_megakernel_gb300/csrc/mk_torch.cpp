@@ -7,6 +7,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/core/TensorImpl.h>
 #include <c10/cuda/CUDACachingAllocator.h>
@@ -47,6 +48,8 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
   if (t.layout() != at::kStrided) value_error(std::string(name) + " must be a dense tensor");
   if (t.requires_grad() && c10::GradMode::is_enabled())
     value_error(std::string(name) + " requires a gradient, and none is recorded here (torch.no_grad())");
+  if (t._fw_grad(0).defined() && c10::AutogradState::get_tls_state().get_fw_grad_mode())
+    value_error(std::string(name) + " has a forward-mode tangent, and none is computed here");
   return t;
 }
 // A tensor that the call writes in place counts as changed, as after torch's own operators (one

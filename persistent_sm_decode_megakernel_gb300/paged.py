@@ -11,8 +11,10 @@ be captured into a CUDA graph.  Wrong arguments raise before anything is enqueue
 for tensors, MkError with the C status otherwise); what only the device can see goes to the
 `status` tensor (int32 [4], zeroed by the caller), which `check_status` reads.  A call's
 workspace is allocated per call by torch, so calls on different streams or in different
-captured graphs do not share one.  These are operators of generation: they have no backward
-pass, and refuse tensors that require a gradient (ValueError) unless gradients are switched off.
+captured graphs do not share one.  What a call writes in place counts as changed, as after torch's
+own operators.  These are operators of generation: they have no backward pass and no
+forward-mode derivative, and refuse tensors that require a gradient or have a tangent (ValueError)
+unless gradients or that mode are switched off.
 """
 import ctypes
 

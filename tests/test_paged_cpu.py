@@ -271,3 +271,24 @@ def test_tensors_that_require_a_gradient_are_refused():
         paged.beam_select(torch.zeros(2, 8, requires_grad=True), torch.zeros(1, 2), ids)
     with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
         paged.beam_select(torch.zeros(2, 8, requires_grad=True), torch.zeros(1, 2), ids)
+
+
+def test_tensors_with_a_forward_tangent_are_refused():
+    """A tangent of forward-mode differentiation would be dropped: refused, unless that mode is off."""
+    import torch.autograd.forward_ad as fwd
+    from persistent_sm_decode_megakernel_gb300 import paged
+    ids, q = torch.zeros(1, 2, dtype=torch.int32), torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    pages = torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16)
+    with fwd.dual_level():
+        x = fwd.make_dual(torch.zeros(2, 8), torch.ones(2, 8))
+        with pytest.raises(ValueError, match="tangent"):
+            paged.beam_select(x, torch.zeros(1, 2), ids)
+        p = fwd.make_dual(pages, torch.ones_like(pages))
+        with pytest.raises(ValueError, match="tangent"):
+            paged.paged_attention(q, p, pages, ids, ids[:, 0])
+        with torch.no_grad(), pytest.raises(ValueError, match="tangent"):
+            paged.beam_select(x, torch.zeros(1, 2), ids)
+        with fwd._set_fwd_grad_enabled(False), pytest.raises(ValueError, match="CUDA"):
+            paged.beam_select(x, torch.zeros(1, 2), ids)
+    with pytest.raises(ValueError, match="CUDA"):
+        paged.beam_select(torch.zeros(2, 8), torch.zeros(1, 2), ids)
