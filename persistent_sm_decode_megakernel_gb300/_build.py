@@ -3,9 +3,12 @@
 The translation units compile in parallel; the shared library links the CUDA runtime
 statically, so loading it needs no CUDA driver (host-only entry points such as
 mk_plan work on a machine without a GPU).  Beside it a small extension module passes torch
-tensors to the paged operators.
+tensors to the paged operators; it wants g++ and a torch with CUDA, and where either is missing
+libmk.so is built alone (paged.py then does not import).
 """
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
@@ -44,6 +47,23 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
+def _torch_of():
+    """(folder, what identifies it) of the torch an extension would be built against, or (None, why there is none)."""
+    try:
+        spec = importlib.util.find_spec("torch")
+    except (ImportError, ValueError):
+        spec = None
+    if spec is None or not spec.submodule_search_locations:
+        return None, "torch is not installed"
+    root = list(spec.submodule_search_locations)[0]
+    if not os.path.exists(os.path.join(root, "lib", "libc10_cuda.so")):
+        return None, "torch is without CUDA"
+    if shutil.which("g++") is None:
+        return None, "g++ is missing"
+    with open(os.path.join(root, "version.py")) as f:
+        return root, f"{sys.version_info[:2]} {root}\n{f.read()}"
+
+
 def _extension_command(nvcc):
     """The compile of the torch extension module (host code; torch's headers, libmk.so linked after)."""
     import sysconfig
@@ -63,9 +83,16 @@ def _extension_command(nvcc):
 
 
 def build(force=False, verbose=False, ptxas_info=False):
-    """Compile and link libmk.so if any source changed; returns the library path."""
+    """Compile and link libmk.so, and the torch extension where it can be, if any source (or torch) changed; returns
+    the library's path."""
     deps = _deps()
-    if not force and not _stale(LIB, deps) and not _stale(EXT, deps):
+    root, torch_id = _torch_of()
+    stamp = os.path.join(OBJ, "mk_torch.stamp")  # the torch that the extension was built against
+    need_lib = force or _stale(LIB, deps)
+    need_ext = root is not None and (force or _stale(EXT, deps) or not os.path.exists(stamp) or open(stamp).read() != torch_id)
+    if need_lib and root is None:
+        print(f"the torch extension of the paged operators (paged.py) is not built: {torch_id}", file=sys.stderr)
+    if not need_lib and not need_ext:
         return LIB
     os.makedirs(OBJ, exist_ok=True)
     nvcc = _nvcc()
@@ -83,25 +110,31 @@ def build(force=False, verbose=False, ptxas_info=False):
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stdout + r.stderr
 
-    ext_compile, ext_link = _extension_command(nvcc)
+    logs = ""
     with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        ext = ex.submit(subprocess.run, ext_compile, capture_output=True, text=True)
-        results = list(ex.map(compile_one, SOURCES))
+        if need_ext:
+            ext_compile, ext_link = _extension_command(nvcc)
+            ext = ex.submit(subprocess.run, ext_compile, capture_output=True, text=True)
+        results = list(ex.map(compile_one, SOURCES)) if need_lib else []
+    if need_lib:
+        logs = "".join(r[1] for r in results)
+        if verbose and logs:
+            print(logs, file=sys.stderr)
+        tmp = LIB + ".tmp"
+        cmd = [nvcc, "-shared"] + ARCH + ["-o", tmp] + [r[0] for r in results]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, LIB)
+    if need_ext:  # (libmk.so is in place by now, whatever becomes of it)
         if ext.result().returncode != 0:
             raise RuntimeError(f"g++ failed on mk_torch.cpp:\n{ext.result().stdout}\n{ext.result().stderr}")
-    logs = "".join(r[1] for r in results)
-    if verbose and logs:
-        print(logs, file=sys.stderr)
-    tmp = LIB + ".tmp"
-    cmd = [nvcc, "-shared"] + ARCH + ["-o", tmp] + [r[0] for r in results]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    r = subprocess.run(ext_link, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link of the torch extension failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(EXT + ".tmp", EXT)
+        r = subprocess.run(ext_link, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link of the torch extension failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(EXT + ".tmp", EXT)
+        with open(stamp, "w") as f:
+            f.write(torch_id)
     return (LIB, logs) if ptxas_info else LIB
 
 

@@ -21,7 +21,11 @@ import ctypes
 import torch
 
 from . import MkError, check, mk_rope_desc, mk_rope_freqs
-from . import _mk_torch
+try:
+    from . import _mk_torch
+except ImportError as e:
+    raise ImportError("the torch extension of the paged operators is not built or does not fit this torch: run "
+                      "__graft_entry__.build() with g++ and a torch with CUDA") from e
 
 _mk_torch.set_error(MkError)
 ROPE_KINDS = {"none": 0, "linear": 1, "base": 2, "blended": 3, "wavelength": 4}
