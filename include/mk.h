@@ -377,7 +377,7 @@ mk_status mk_rope_freqs(const mk_rope_desc* desc, double* freqs, float* mscale);
 typedef struct {
   const void *q, *k, *v;   /* [n_tokens][heads][head_dim], element strides below; q and
                               q_out NULL: no queries                                        */
-  void* q_out;             /* may be q itself (same strides)                                */
+  void* q_out;             /* may be q itself (same strides); its vectors must not overlap  */
   int dtype;               /* of q, k, v and q_out: MK_F16, MK_BF16 or MK_F32               */
   int n_tokens, n_heads;
   long long q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
@@ -411,7 +411,7 @@ mk_status mk_rope_append(const mk_append_args* args, const mk_page_view* cache, 
  * table's width in positions or the window + 16, if that is less. */
 typedef struct {
   const void* q;           /* [n_rows][n_heads][head_dim], element strides below            */
-  void* out;
+  void* out;               /* its vectors must not overlap                                  */
   float* lse;              /* [n_rows][n_heads] or NULL                                     */
   int dtype;               /* of q and out: MK_F16, MK_BF16 or MK_F32                       */
   int n_rows, n_heads;     /* n_heads / n_kv_heads: 1..16                                   */

@@ -281,6 +281,8 @@ extern "C" mk_status mk_rope_append(const mk_append_args* args, const mk_page_vi
       if (!aligned_to(p, esz)) return paged_fail(MK_ERR_INVALID, "q, k, v and q_out must be aligned to their type");
     if (args->q == args->q_out && args->q && (args->q_token != args->o_token || args->q_head != args->o_head))
       return paged_fail(MK_ERR_INVALID, "q_out in the place of q needs q's strides");
+    if (args->q && overlaps(args->n_tokens, args->o_token, args->n_heads, args->o_head, cache->head_dim))
+      return paged_fail(MK_ERR_INVALID, "the vectors of q_out overlap");
     if (args->n_tokens == 0) return MK_OK;
     AppendArgs a{};
     a.q = args->q; a.k = args->k; a.v = args->v; a.qo = args->q_out;

@@ -801,6 +801,8 @@ extern "C" mk_status mk_paged_attention(const mk_attend_args* args, const mk_pag
     const size_t esz = args->dtype == MK_F32 ? 4 : 2;
     if (!aligned_to(args->q, esz) || !aligned_to(args->out, esz))
       return paged_fail(MK_ERR_INVALID, "q and out must be aligned to their type");
+    if (overlaps(args->n_rows, args->o_row, args->n_heads, args->o_head, cache->head_dim))
+      return paged_fail(MK_ERR_INVALID, "the vectors of out overlap");
     const std::string line = check_line(cache, args->n_rows, args->window);
     if (!line.empty()) return paged_fail(MK_ERR_INVALID, line);
     if (!args->workspace || !aligned_to(args->workspace, 16))

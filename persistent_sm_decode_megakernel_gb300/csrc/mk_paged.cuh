@@ -38,6 +38,11 @@ inline mk_status c_entry(F&& body) noexcept {
 }
 
 inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+// whether vectors of `dim` elements at strides s0 (n0 of them) and s1 (n1) lie over one another for certain
+inline bool overlaps(long long n0, long long s0, long long n1, long long s1, long long dim) {
+  const long long a0 = s0 < 0 ? -s0 : s0, a1 = s1 < 0 ? -s1 : s1;
+  return (n0 > 1 && a0 < dim) || (n1 > 1 && a1 < dim) || (n0 > 1 && n1 > 1 && a0 == a1);
+}
 inline size_t round16(size_t x) { return (x + 15) & ~size_t(15); }
 
 // Every kernel of these operators is launched as a programmatic dependent of what precedes

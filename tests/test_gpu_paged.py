@@ -992,6 +992,22 @@ def test_what_is_written_in_place_counts_as_changed(paged):
     assert torch.equal(k2[0, 0, :, 1], kv[0])
 
 
+def test_outputs_that_share_memory_are_refused(paged):
+    """An expanded q_out or out, whose rows are one and the same memory."""
+    from persistent_sm_decode_megakernel_gb300 import MkError
+    pages = torch.zeros(2, 4, 2, 16, 64, dtype=torch.bfloat16, device=DEV)
+    q, kv = torch.ones(3, 4, 64, dtype=torch.bfloat16, device=DEV), torch.ones(3, 2, 64, dtype=torch.bfloat16, device=DEV)
+    table, pos = ints([[0], [1], [2]]), ints([1, 2, 3])
+    for out in (q[:1].clone().expand(3, 4, 64), q[:, :1].clone().expand(3, 4, 64)):
+        with pytest.raises(MkError):
+            paged.rope_append(q, kv, kv, *pages, table, pos, q_out=out)
+        with pytest.raises(MkError):
+            paged.paged_attention(q, *pages, table, pos, out=out)
+    torch.cuda.synchronize()
+    assert not pages.any()
+    assert torch.equal(paged.rope_append(q[:1], kv[:1], kv[:1], *pages, table, pos[:1]), q[:1])
+
+
 # ------------------------------------------------------------------------------ all of them
 def test_a_beam_search_of_the_four_operators_captured(paged):
     """Steps as a beam search makes them -- reserve and fork, append, attend, select -- eagerly and as one

@@ -292,3 +292,24 @@ def test_tensors_with_a_forward_tangent_are_refused():
             paged.beam_select(x, torch.zeros(1, 2), ids)
     with pytest.raises(ValueError, match="CUDA"):
         paged.beam_select(torch.zeros(2, 8), torch.zeros(1, 2), ids)
+
+
+@pytest.mark.parametrize("bad", [dict(o_token=0), dict(o_head=0), dict(o_head=32, o_token=512), dict(o_head=-32),
+                                 dict(o_token=63), dict(q=2 * P, q_out=2 * P, q_token=0, o_token=0)], ids=str)
+def test_rotated_queries_that_share_memory_are_refused(mk, bad):
+    """An output whose heads or tokens lie over one another (an expanded tensor) would hold whichever came last."""
+    assert _append(mk, _view(mk), **{**dict(q_out=3 * P), **bad}) == mk.MK_ERR_INVALID
+    assert b"overlap" in mk.mk_last_error()
+
+
+@pytest.mark.parametrize("bad", [dict(o_row=0), dict(o_head=0), dict(o_head=63), dict(o_row=-32)], ids=str)
+def test_attention_outputs_that_share_memory_are_refused(mk, bad):
+    assert _attend(mk, _view(mk), **bad) == mk.MK_ERR_INVALID
+    assert b"overlap" in mk.mk_last_error()
+
+
+def test_strides_of_a_single_token_or_head_do_not_count(mk):
+    """(n_tokens and n_rows 0: the checks are passed, and nothing is enqueued)"""
+    assert _append(mk, _view(mk), n_tokens=0, o_token=0, q_out=3 * P) == mk.MK_OK
+    assert _attend(mk, _view(mk), n_rows=0, o_row=0) == mk.MK_OK
+    assert _append(mk, _view(mk, n_kv_heads=1, page_stride=16 * 64), n_tokens=0, n_heads=1, o_head=0, q_out=3 * P) == mk.MK_OK
