@@ -503,9 +503,8 @@ mk_status mk_beam_select_workspace(int groups, int beams, int vocab, size_t* byt
  * mk_update_pages.  A step runs as one launch per op (the multi-launch control), with
  * mk_rope_append and mk_paged_attention in place of each layer's split-KV units.  rope NULL:
  * the whole head at desc->rope_theta, unscaled; else its n_rot is at most head_dim.
- * desc->max_ctx is not used.  Keys are rounded to the cache's type before their rotation and
- * once more after it.  The pages, table and whatever the calls below are given belong to the
- * caller. */
+ * desc->max_ctx is not used.  Keys are rotated in fp32 and, like values, rounded once to the
+ * cache's type.  The pages, table and whatever the calls below are given belong to the caller. */
 typedef struct {
   void *k, *v;             /* layer 0's pages, as in mk_page_view                           */
   long long layer_stride;  /* elements from one layer to the next, a multiple of 8          */

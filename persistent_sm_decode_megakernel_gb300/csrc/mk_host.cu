@@ -87,7 +87,9 @@ struct PrefillState {
 // A context over a paged cache (mk_create_paged): the per-op launches of the multi-launch
 // control, with the append and the paged attention in place of each layer's split-KV units.
 // The QKV op sees a cache of one position (its staging, never read) and so rotates by
-// position 0; its fp32 q, k and v go through mk_rope_append.  The attention writes where a
+// position 0.  Its keys are computed as further query heads, as those stay in fp32 (the op rounds
+// keys and values to the cache's type): q and k of a token lie in `qk`, [row][Hq + Hkv][hd], and
+// go with the values through mk_rope_append, which rounds the rotated keys once.  The attention writes where a
 // sequence's single split partial lies, as (output, maximum 0, sum 1), and the merge op
 // carries it on to the O projection in the form that takes.
 struct PagedState {
@@ -95,7 +97,7 @@ struct PagedState {
   long long layer_stride = 0;  // elements
   int n_freqs = 0, interleaved = 0;
   float mscale = 1.f;
-  DevBuf staging, freqs, status, work;
+  DevBuf staging, qk, freqs, status, work;
   size_t work_bytes = 0;
 };
 
@@ -207,6 +209,14 @@ mk_status get_sched_in(mk_ctx* ctx, const ModelShape& m, const Geometry& geo,
   if (s) return s;
   MK_CUDA(cudaMalloc(&sc->counters.p, sizeof(uint32_t) * std::max(1, sc->plan.n_counters)));
   MK_CUDA(cudaMemset(sc->counters.p, 0, sizeof(uint32_t) * std::max(1, sc->plan.n_counters)));
+  if (ctx->paged)  // key heads as the query heads behind the query's own
+    for (auto& ph : sc->plan.phase_queues)
+      for (auto& q : ph)
+        for (Instr& in : q)
+          if (in.op == OP_QKV && in.a[0] == 1) {
+            in.a[0] = 0;
+            in.a[1] += m.Hq;
+          }
   if (ctx->opts.exec_mode != MK_EXEC_PERSISTENT) {
     const size_t np = sc->plan.phase_queues.size();
     sc->ph_instr.resize(np);
@@ -702,6 +712,7 @@ mk_status mk_create_paged(const mk_model_desc* desc, const mk_weights* w, const 
     o.attn_tensor_cores = -1;
     s = upload(ps->freqs, freqs, sizeof(double) * ps->n_freqs);
     if (s) return s;
+    MK_CUDA(cudaMalloc(&ps->qk.p, 4ull * desc->max_batch * (desc->n_heads + desc->n_kv_heads) * desc->head_dim));
     MK_CUDA(cudaMalloc(&ps->staging.p, 2ull * desc->max_batch * desc->n_kv_heads * desc->head_dim));
     MK_CUDA(cudaMalloc(&ps->status.p, 16));
     MK_CUDA(cudaMemset(ps->status.p, 0, 16));
@@ -764,15 +775,17 @@ mk_status mk_decode_step_paged(mk_ctx* ctx, const int32_t* tok, const int32_t* p
       const int l = (int)((k - 1) / 6);
       if (k > 0 && (k - 1) % 6 == OP_ATTN - OP_QKV && l < m.L) {
         float* q = S.act + S.act_off[ACT_Q] + l * S.act_stride[ACT_Q];
+        const float* qk = reinterpret_cast<const float*>(ps.qk.p);
         const float* kvn = S.act + S.act_off[ACT_KVN] + l * S.act_stride[ACT_KVN];
         mk_page_view view = ps.view;
         view.k = static_cast<uint16_t*>(view.k) + l * ps.layer_stride;
         view.v = static_cast<uint16_t*>(view.v) + l * ps.layer_stride;
         mk_append_args ap{};
-        ap.q = q; ap.q_out = q; ap.k = kvn; ap.v = kvn + (size_t)m.Hkv * m.hd;
+        ap.q = qk; ap.q_out = q; ap.k = qk + (size_t)m.Hq * m.hd; ap.v = kvn + (size_t)m.Hkv * m.hd;
         ap.dtype = MK_F32; ap.n_tokens = B; ap.n_heads = m.Hq;
-        ap.q_token = ap.o_token = (long long)m.Hq * m.hd;
-        ap.k_token = ap.v_token = 2LL * m.Hkv * m.hd;
+        ap.o_token = (long long)m.Hq * m.hd;
+        ap.q_token = ap.k_token = (long long)(m.Hq + m.Hkv) * m.hd;
+        ap.v_token = 2LL * m.Hkv * m.hd;
         ap.q_head = ap.o_head = ap.k_head = ap.v_head = m.hd;
         ap.positions = pos; ap.rows = rows;
         ap.freqs = reinterpret_cast<const double*>(ps.freqs.p);
@@ -795,7 +808,13 @@ mk_status mk_decode_step_paged(mk_ctx* ctx, const int32_t* tok, const int32_t* p
       if (k == 0) Ak.flags |= SF_RESET_ARGMAX;
       Ak.instr = reinterpret_cast<const Instr*>(sc->ph_instr[k].p);
       Ak.q_start = reinterpret_cast<const int32_t*>(sc->ph_qstart[k].p);
-      s = launch(ctx, fn, S, Ak, false);
+      DevState Sk = S;
+      if (k > 0 && (k - 1) % 6 == 0 && l < m.L) {  // the QKV op: Hq + Hkv heads into qk
+        Sk.Hq = m.Hq + m.Hkv;
+        Sk.act_off[ACT_Q] = ((int64_t)reinterpret_cast<uintptr_t>(ps.qk.p) - (int64_t)reinterpret_cast<uintptr_t>(S.act)) /
+                                (int64_t)sizeof(float) - l * S.act_stride[ACT_Q];
+      }
+      s = launch(ctx, fn, Sk, Ak, false);
       if (s) return s;
     }
     ++sc->epoch;

@@ -86,6 +86,33 @@ def test_paged_decoder_next_to_the_contiguous_one(lib):
     b.close()
 
 
+@pytest.mark.parametrize("name,max_batch", [("tiny", 1), ("tiny-g4", 2), ("tiny-g4", 16)])
+def test_keys_are_rounded_once(lib, name, max_batch):
+    """The first layer's keys in the pages are the contiguous decoder's: both come from the same products, rotated in
+    32 bits and rounded once, so that only a key within 2^-20 of a rounding border (2^-8 of them over 16-bit
+    types of up to 11 bits, doubled for products summed in another order) may differ, and then by one step.  Of
+    keys rounded before their rotation as well, a third differs."""
+    cfg = synth.CONFIGS[name]
+    w = synth.gen_weights(cfg)
+    P = 200
+    prompt = synth.gen_prompts(cfg, 1, P)
+    a = lib.DeviceModel(cfg, w, max_batch=max_batch, max_ctx=P)
+    plain = lib.Decoder(a)
+    plain.prefill(prompt)
+    dec = _paged(lib, cfg, w, max_batch, 1, P)
+    dec.prefill({0: prompt[0]})
+    dec.synchronize()
+    at = dec.table[0].long()
+    for got, want, share in ((dec.k, a.k_cache, 2.0 ** -6), (dec.v, a.v_cache, 2.0 ** -6)):
+        got = got[0][at].transpose(0, 1).reshape(cfg.n_kv_heads, -1, cfg.head_dim)[:, :P].float()
+        want = want[0][0].view(dec.k.dtype).float()
+        step = torch.finfo(dec.k.dtype).eps * want.abs()
+        assert torch.all((got - want).abs() <= step + 2.0 ** -14)
+        assert (got != want).float().mean().item() <= share
+    dec.close()
+    plain.close()
+
+
 @pytest.mark.parametrize("factor", [2.0, 8.0])
 def test_paged_decoder_scaled_rotary_base(lib, factor):
     """Rotary positions with the scaled base are those of a model whose theta is the scaled one."""
