@@ -111,8 +111,10 @@ __global__ void __launch_bounds__(kAppendThreads, kCtasPerSm) append_kernel(cons
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane % ITEMS;
   pdl_wait();
   pdl_launch();
-  const int unit = blockIdx.x * WARPS + warp, t = unit >> a.share, parts = 1 << a.share;
-  if (t >= a.n_tokens) return;
+  const unsigned unit = blockIdx.x * WARPS + warp;  // below 2^32: the host sees to it
+  const int parts = 1 << a.share;
+  if ((unit >> a.share) >= (unsigned)a.n_tokens) return;
+  const int t = (int)(unit >> a.share);
   const int heads = a.hq + 2 * a.hkv, first = (unit & (parts - 1)) * HPW + lane / ITEMS, step = parts * HPW;
   const bool turned = c < a.n_freqs / 8;
   const int e0 = !INTER && turned ? 8 * c : 16 * c, e1 = !INTER && turned ? a.n_freqs + 8 * c : 16 * c + 8;
@@ -242,8 +244,10 @@ mk_status launch_append(AppendArgs a, int n_sm, bool inter, bool vec, void* stre
   // a warp takes at least four turns of a token, or down to one while warps are free
   constexpr int WARPS = kAppendThreads / 32, HPW = 512 / HD;
   const int turns = (a.hq + 2 * a.hkv + HPW - 1) / HPW;
-  while ((8LL << a.share) <= turns ||
-         ((2LL << a.share) <= turns && ((long long)a.n_tokens << (a.share + 1)) <= (long long)kWarpsPerSm * n_sm))
+  // (the warps are counted in 32 bits)
+  while (((long long)a.n_tokens << (a.share + 1)) <= 0xFFFFFFF0LL &&
+         ((8LL << a.share) <= turns ||
+          ((2LL << a.share) <= turns && ((long long)a.n_tokens << (a.share + 1)) <= (long long)kWarpsPerSm * n_sm)))
     ++a.share;
   const long long ctas = (((long long)a.n_tokens << a.share) + WARPS - 1) / WARPS;
   return launch_dependent(inter ? append_kernel<T, C, HD, true> : append_kernel<T, C, HD, false>, dim3((unsigned)ctas),

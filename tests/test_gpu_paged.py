@@ -144,6 +144,26 @@ def test_append_reports_a_place_that_is_none(paged, what, row, pos, page):
     assert torch.equal(pages, want)
 
 
+def test_append_of_more_shares_of_tokens_than_31_bits_count(paged):
+    """Many tokens of very many heads (expanded: they take no memory), nearly all of them skipped: each token's heads are
+    dealt to 4096 warps, 2.2e9 in all.  The last token and one in the middle are where they belong."""
+    heads, tokens = 65535, 530000
+    pages = torch.zeros(2, 2, heads, 16, 128, dtype=torch.bfloat16, device=DEV)
+    k = torch.randn(1, heads, 128, device=DEV).bfloat16()
+    pos = torch.full((tokens,), -1, dtype=torch.int32, device=DEV)
+    row = torch.zeros(tokens, dtype=torch.int32, device=DEV)
+    pos[tokens // 2], pos[-1], row[-1] = 3, 7, 1
+    st = status()
+    paged.rope_append(None, k.expand(tokens, heads, 128), k.expand(tokens, heads, 128), pages[0], pages[1], ints([[0], [1]]), pos,
+                      rows=row, status=st)
+    paged.check_status(st)
+    for p in pages:
+        assert torch.equal(p[0, :, 3], k[0]) and torch.equal(p[1, :, 7], k[0])
+        p[0, :, 3] = 0
+        p[1, :, 7] = 0
+        assert not p.any()
+
+
 # ------------------------------------------------------------------------------- attention
 def _make_cache(g, lens, hkv, hd, ps, cache, extra=3, poison=True):
     """Pages with random order whose places behind a sequence's end hold NaN, infinities and large values."""
