@@ -797,7 +797,9 @@ extern "C" mk_status mk_paged_attention(const mk_attend_args* args, const mk_pag
     if (args->n_rows < 0 || (long long)args->n_rows * args->n_heads > 0x7fffffffLL)
       return paged_fail(MK_ERR_INVALID, "n_rows out of range");
     if (args->window < 0) return paged_fail(MK_ERR_INVALID, "window must not be negative");
-    if (!(args->softcap >= 0.f && args->softcap < INFINITY) || !(fabsf(args->scale) < INFINITY)) return paged_fail(MK_ERR_INVALID, "scale or softcap");
+    const float factor = args->softcap > 0.f ? args->scale / args->softcap : args->scale * kLog2e;
+    if (!(args->softcap >= 0.f && args->softcap * kLog2e < INFINITY) || !(fabsf(factor) < INFINITY))
+      return paged_fail(MK_ERR_INVALID, "scale or softcap is not finite, too large, or softcap negative or too small for scale");
     const size_t esz = args->dtype == MK_F32 ? 4 : 2;
     if (!aligned_to(args->q, esz) || !aligned_to(args->out, esz))
       return paged_fail(MK_ERR_INVALID, "q and out must be aligned to their type");
@@ -831,7 +833,7 @@ extern "C" mk_status mk_paged_attention(const mk_attend_args* args, const mk_pag
     a.part = reinterpret_cast<float*>(a.joins + a.n_cta);
     a.q_vec = aligned_to(a.q, 16) && a.q_row * (long long)esz % 16 == 0 && a.q_head * (long long)esz % 16 == 0;
     a.by_segment = (long long)a.n_rows * a.hkv <= a.n_cta;
-    a.scale = args->softcap > 0.f ? args->scale / args->softcap : args->scale * kLog2e;
+    a.scale = factor;
     a.softcap = args->softcap * kLog2e;
     // 16-bit queries of the cache's type are exact in one part.  Other queries are split into
     // 2 parts of fp16 (22 bits, each head at a power of two of its own) or 3 of bf16 (24 bits);

@@ -313,3 +313,11 @@ def test_strides_of_a_single_token_or_head_do_not_count(mk):
     assert _append(mk, _view(mk), n_tokens=0, o_token=0, q_out=3 * P) == mk.MK_OK
     assert _attend(mk, _view(mk), n_rows=0, o_row=0) == mk.MK_OK
     assert _append(mk, _view(mk, n_kv_heads=1, page_stride=16 * 64), n_tokens=0, n_heads=1, o_head=0, q_out=3 * P) == mk.MK_OK
+
+
+@pytest.mark.parametrize("bad", [dict(scale=3e38), dict(scale=-3e38), dict(softcap=1e-38, scale=100.0), dict(softcap=1e-45),
+                                 dict(softcap=3e38)], ids=str)
+def test_attention_factors_beyond_the_floats_are_refused(mk, bad):
+    """scale log2 e, scale / softcap and softcap log2 e are factors of the kernel: infinite ones give NaN at a score of 0."""
+    assert _attend(mk, _view(mk), **bad) == mk.MK_ERR_INVALID
+    assert b"scale" in mk.mk_last_error()
