@@ -46,6 +46,7 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) value_error(std::string(name) + " must be a tensor");
   const at::Tensor& t = THPVariable_Unpack(o);
   if (t.layout() != at::kStrided) value_error(std::string(name) + " must be a dense tensor");
+  if (t.is_neg()) value_error(std::string(name) + " must not be a negated view (resolve_neg())");
   if (t.requires_grad() && c10::GradMode::is_enabled())
     value_error(std::string(name) + " requires a gradient, and none is recorded here (torch.no_grad())");
   if (t._fw_grad(0).defined() && c10::AutogradState::get_tls_state().get_fw_grad_mode())

@@ -321,3 +321,12 @@ def test_attention_factors_beyond_the_floats_are_refused(mk, bad):
     """scale log2 e, scale / softcap and softcap log2 e are factors of the kernel: infinite ones give NaN at a score of 0."""
     assert _attend(mk, _view(mk), **bad) == mk.MK_ERR_INVALID
     assert b"scale" in mk.mk_last_error()
+
+
+def test_negated_views_are_refused():
+    """A tensor whose values are the negatives of what lies in its memory (imaginary part of a conjugate)."""
+    from persistent_sm_decode_megakernel_gb300 import paged
+    scores = torch.complex(torch.zeros(1, 1), torch.ones(1, 1)).conj().imag
+    assert scores.is_neg() and scores.is_contiguous()
+    with pytest.raises(ValueError, match="negated"):
+        paged.beam_select(scores, scores, torch.zeros(1, 1, dtype=torch.int32))
