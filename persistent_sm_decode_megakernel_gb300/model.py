@@ -272,21 +272,29 @@ class PagedDecoder:
                                        logits.data_ptr() if logits is not None else None), "mk_decode_step_paged")
         return out
 
+    def _tokens(self, prompt):
+        tokens = [int(t) for t in prompt]
+        if any(not 0 <= t < self.dm.cfg.vocab for t in tokens):
+            raise ValueError("a prompt's tokens must be in [0, vocab)")
+        return tokens
+
     def prefill(self, prompts, logits=None):
         """Appends prompts {row: tokens} to their rows, up to dm.max_batch positions per step.  Returns
         {row: next token} (device int32 [1] each); logits {row: float32 [vocab]} receives the last ones.  Raises
-        ValueError for a prompt that does not fit and MkError when the pages run out, before any of it."""
+        ValueError for a prompt that does not fit or a token that is none, and MkError when the pages run out,
+        before any of it."""
         with torch.cuda.stream(self.stream):
             n_rows, V = self.table.shape[0], self.dm.cfg.vocab
             start = self.lens.tolist()
             reserve = [0] * n_rows
+            prompts = {r: self._tokens(p) for r, p in prompts.items()}
             for r, p in prompts.items():
                 if not 0 <= r < n_rows or len(p) < 1 or start[r] + len(p) > self.max_positions:
                     raise ValueError("a prompt must be of a row of the table, not empty and fit max_positions")
                 reserve[r] = len(p)
             self.update(reserve=reserve)
             self.synchronize()
-            jobs = [(int(t), start[r] + i, r, i == len(p) - 1) for r, p in prompts.items() for i, t in enumerate(p)]
+            jobs = [(t, start[r] + i, r, i == len(p) - 1) for r, p in prompts.items() for i, t in enumerate(p)]
             last = {}
             for at in range(0, len(jobs), self.dm.max_batch):
                 part = jobs[at: at + self.dm.max_batch]

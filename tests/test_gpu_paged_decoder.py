@@ -382,6 +382,25 @@ def test_contexts_are_made_and_freed_on_their_models_device(lib, monkeypatch):
     assert len(seen) == 2 and all(s and s[-1] == dec.dm.device for s in seen)
 
 
+def test_a_prompt_with_a_token_that_is_none_is_refused(lib):
+    """A token outside the vocabulary, in any of the prompts, raises before anything is changed."""
+    cfg = synth.CONFIGS["tiny"]
+    w = synth.gen_weights(cfg)
+    prompt = synth.gen_prompts(cfg, 1, 20)[0]
+    dec = _paged(lib, cfg, w, 4, 2, 48)
+    want = int(dec.prefill({0: prompt})[0])
+    before = dec.lens.tolist(), dec.table.tolist(), dec.refs.tolist()
+    for bad in (-1, cfg.vocab):
+        with pytest.raises(ValueError):
+            dec.prefill({1: [1, 2, bad]})
+        with pytest.raises(ValueError):
+            dec.prefill({0: [3], 1: [bad]})
+    assert before == (dec.lens.tolist(), dec.table.tolist(), dec.refs.tolist())
+    assert int(dec.prefill({1: prompt})[1]) == want
+    dec.synchronize()
+    dec.close()
+
+
 def test_steps_refuse_tensors_that_do_not_fit_and_capture(lib):
     from persistent_sm_decode_megakernel_gb300 import MK_ERR_STATE, mk_decode_step_paged
     cfg = synth.CONFIGS["tiny"]
