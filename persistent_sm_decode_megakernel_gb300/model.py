@@ -243,6 +243,12 @@ class PagedDecoder:
         if first is not None:
             raise first
 
+    def reset(self):
+        """Makes the context usable again after an error of a step (a token that is none, a NaN logit, a timeout).
+        Rows, pages and their counts stay as they are."""
+        with torch.cuda.device(self.dm.device):
+            check(mk_reset(self.h), "mk_reset")
+
     def update(self, parents=None, reserve=None):
         """Every row continues row parents[r] (-1: it is freed) and reserves pages for reserve[r] more
         positions (mk_update_pages).  It runs on self.stream, where tensors given have to be ready."""

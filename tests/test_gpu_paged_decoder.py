@@ -401,6 +401,35 @@ def test_a_prompt_with_a_token_that_is_none_is_refused(lib):
     dec.close()
 
 
+def test_a_context_in_error_goes_on_after_reset(lib):
+    """A device token outside the vocabulary stops the context until reset(), as it does a contiguous one's; rows and
+    pages are the caller's and stay."""
+    from persistent_sm_decode_megakernel_gb300 import MK_ERR_STATE, MkError
+    cfg = synth.CONFIGS["tiny"]
+    w = synth.gen_weights(cfg)
+    prompt = synth.gen_prompts(cfg, 1, 20)[0]
+    dec = _paged(lib, cfg, w, 4, 2, 48)
+    tok = dec.prefill({0: prompt})[0]
+    dec.update(parents=[0, 0], reserve=[2, 2])
+    z = torch.zeros(2, cfg.vocab, device=dec.dm.device)
+    dec.step(torch.cat((tok, tok)), dec.lens.clone(), None, z)
+    dec.synchronize()
+    for bad in (-1, cfg.vocab):
+        dec.step(dec._int32([bad]), dec._int32([21]))
+        with pytest.raises(MkError) as e:
+            dec.synchronize()
+        assert e.value.status == MK_ERR_STATE
+        with pytest.raises(MkError):
+            dec.step(tok, dec._int32([20]))
+        dec.reset()
+        dec.synchronize()
+        z2 = torch.zeros_like(z)
+        dec.step(torch.cat((tok, tok)), dec.lens.clone(), None, z2)
+        dec.synchronize()
+        assert torch.equal(z, z2)
+    dec.close()
+
+
 def test_steps_refuse_tensors_that_do_not_fit_and_capture(lib):
     from persistent_sm_decode_megakernel_gb300 import MK_ERR_STATE, mk_decode_step_paged
     cfg = synth.CONFIGS["tiny"]
