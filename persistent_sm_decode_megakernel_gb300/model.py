@@ -325,6 +325,9 @@ class PagedDecoder:
             raise ValueError("beams must be in [1, 32] and at most max_batch and n_rows")
         if n_new < 1 or len(prompt) < 1 or len(prompt) + n_new - 1 > self.max_positions:
             raise ValueError("the prompt and the new tokens must be positive and fit max_positions")
+        if beams > c.vocab or not -1 <= eos < c.vocab:
+            raise ValueError("beams must be at most vocab, eos a token or -1")
+        prompt = self._tokens(prompt)
         keep = list(range(n_rows))
         with torch.cuda.stream(self.stream):
             self.update(parents=[-1] * beams + keep[beams:])

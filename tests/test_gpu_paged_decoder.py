@@ -430,6 +430,25 @@ def test_a_context_in_error_goes_on_after_reset(lib):
     dec.close()
 
 
+def test_a_beam_search_that_cannot_be_leaves_the_rows(lib):
+    """An eos or a token that is none, more beams than tokens: refused before the rows are freed."""
+    cfg = synth.CONFIGS["tiny"]
+    w = synth.gen_weights(cfg)
+    prompt = synth.gen_prompts(cfg, 1, 20)[0]
+    dec = _paged(lib, cfg, w, 4, 4, 48)
+    dec.prefill({0: prompt, 3: prompt[:5]})
+    before = dec.lens.tolist(), dec.table.tolist(), dec.refs.tolist()
+    for kw in (dict(eos=cfg.vocab), dict(eos=-2)):
+        with pytest.raises(ValueError):
+            dec.beam_search(prompt, 2, 4, **kw)
+    for bad in (-1, cfg.vocab):
+        with pytest.raises(ValueError):
+            dec.beam_search([1, bad], 2, 4)
+    assert before == (dec.lens.tolist(), dec.table.tolist(), dec.refs.tolist())
+    dec.synchronize()
+    dec.close()
+
+
 def test_steps_refuse_tensors_that_do_not_fit_and_capture(lib):
     from persistent_sm_decode_megakernel_gb300 import MK_ERR_STATE, mk_decode_step_paged
     cfg = synth.CONFIGS["tiny"]
