@@ -199,7 +199,12 @@ class PagedDecoder:
         r = None
         if rope is not None:
             kw = {"theta": c.rope_theta, "n_rot": c.head_dim, "kind": "none", "factor": 1.0, "original": 0.0,
-                  "beta_fast": 0.0, "beta_slow": 0.0, **rope}
+                  "beta_fast": 0.0, "beta_slow": 0.0}
+            if not set(rope) <= set(kw):
+                raise ValueError(f"rope's arguments are {sorted(kw)}")
+            kw.update(rope)
+            if kw["kind"] not in paged.ROPE_KINDS:
+                raise ValueError(f"kind must be one of {sorted(paged.ROPE_KINDS)}")
             r = ctypes.byref(mk_rope_desc(kw["theta"], kw["n_rot"], paged.ROPE_KINDS[kw["kind"]], kw["factor"],
                                           kw["original"], kw["beta_fast"], kw["beta_slow"]))
         h = ctypes.c_void_p()

@@ -449,6 +449,15 @@ def test_a_beam_search_that_cannot_be_leaves_the_rows(lib):
     dec.close()
 
 
+def test_rope_arguments_that_are_none_are_refused(lib):
+    """A misspelt word or kind of the rotary positions is not left out in silence."""
+    cfg = synth.CONFIGS["tiny"]
+    w = synth.gen_weights(cfg)
+    for bad in (dict(factr=8.0), dict(kind="base", factor=2.0, orignal=4096.0), dict(kind="bases")):
+        with pytest.raises(ValueError):
+            _paged(lib, cfg, w, 1, 1, 16, rope=bad)
+
+
 def test_steps_refuse_tensors_that_do_not_fit_and_capture(lib):
     from persistent_sm_decode_megakernel_gb300 import MK_ERR_STATE, mk_decode_step_paged
     cfg = synth.CONFIGS["tiny"]
