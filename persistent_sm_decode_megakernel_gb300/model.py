@@ -343,7 +343,6 @@ class PagedDecoder:
             scores[0, 0] = 0.0                        # one beam until the first choice tells them apart
             ended = torch.zeros((1, beams), dtype=torch.int32, device=dev)
             parents, reserve = self._int32(keep), torch.zeros(n_rows, dtype=torch.int32, device=dev)
-            reserve[:beams] = 1
             history = []
             for i in range(n_new):
                 tokens, par, scores, ended = self.paged.beam_select(logits, scores, ended, eos, self.status)
@@ -352,9 +351,11 @@ class PagedDecoder:
                     break
                 # beam 0 holds the prompt for all of them at first
                 parents[:beams] = par[0] if i else 0
+                live = 1 - ended[0]                   # an ended beam has no further positions
+                reserve[:beams] = live
                 self.update(parents, reserve)
-                self.step(tokens[0].contiguous(), self.lens[:beams].contiguous(), None, logits)
-                self.lens[:beams] += 1
+                self.step(tokens[0].contiguous(), torch.where(live != 0, self.lens[:beams], -1), None, logits)
+                self.lens[:beams] += live
             self.update(parents=[-1] * beams + keep[beams:])
             self.synchronize()
             seqs = np.zeros((beams, n_new), dtype=np.int32)

@@ -458,6 +458,27 @@ def test_rope_arguments_that_are_none_are_refused(lib):
             _paged(lib, cfg, w, 1, 1, 16, rope=bad)
 
 
+def test_ended_beams_take_no_more_pages(lib):
+    """Beams that ended need no positions: a search whose beams all end at once fits the prompt's own pages, and one
+    that ends in between has the scores it has with room to spare."""
+    cfg = synth.CONFIGS["tiny"]
+    w = synth.gen_weights(cfg)
+    prompt = synth.gen_prompts(cfg, 1, 16)[0]
+    dec = _paged(lib, cfg, w, 4, 4, 64, n_pages=2)
+    eos = int(dec.beam_search(prompt, 1, 1)[0][0, 0])
+    want = dec.beam_search(prompt, 1, 1, eos=eos)
+    seqs, scores = dec.beam_search(prompt, 1, 40, eos=eos)
+    assert seqs.tolist() == [[eos] * 40] and scores[0] == want[1][0]
+    dec.close()
+    few, many = (_paged(lib, cfg, w, 4, 4, 64, n_pages=n) for n in (10, 16))
+    first = many.beam_search(prompt, 4, 3)[0]
+    for eos in sorted({int(t) for t in first.reshape(-1)})[:4]:
+        a, b = many.beam_search(prompt, 4, 20, eos=eos), few.beam_search(prompt, 4, 20, eos=eos)
+        assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+    few.close()
+    many.close()
+
+
 def test_steps_refuse_tensors_that_do_not_fit_and_capture(lib):
     from persistent_sm_decode_megakernel_gb300 import MK_ERR_STATE, mk_decode_step_paged
     cfg = synth.CONFIGS["tiny"]
