@@ -275,7 +275,7 @@ struct AttSmem {
 // other's latency.  Bound: the keys' and values' bytes (16 rows of 16384 to 32768 positions,
 // 1.67 GB: 245 us, 6.8 TB/s), of short rows the chain from the lengths over the table to the
 // first keys, 3 us of it, and a tile after another of a warp, 1 us each (one row of 512: 6.7 us
-// with the join, one of 32768: 28.5).  The pages of a warp's tiles lie in shared memory and
+// with the join, one of 32768: 29.0).  The pages of a warp's tiles lie in shared memory and
 // come there without a register between: held by the lanes, they cost the long rows 2 %.
 template <typename C, typename Q, int HD, bool WIDE, int NQ, int NP>
 __global__ void __launch_bounds__(kAttThreads, ctas_per_sm(HD)) attend_kernel(const __grid_constant__ AttendArgs a) {
