@@ -403,9 +403,10 @@ mk_status mk_rope_append(const mk_append_args* args, const mk_page_view* cache, 
  * any size below 2^127.  A NaN or infinite value inside the range makes that row's results
  * NaN or infinite, as does a NaN key; an infinite key does, unless the query is of the
  * cache's type and the scores stay below +inf.  Results do not depend on timing.
- * Scores, maxima, sums and weighted values are held in 32 bits; a warp adds its tiles of 16
- * positions one after another in the tensor cores, which do not round to nearest (5e-6 of the
- * output at some 200 tiles).  An exponential is the hardware's approximation (2 ulp, 0 below
+ * Scores, maxima, sums and weighted values are held in 32 bits.  Weighted values add up tile by
+ * tile (16 positions) in the tensor cores, which truncate: 32-bit outputs of up to 8 heads per
+ * kv head are off by less than 4e-6 for it at any length, others by up to 5e-8 per tile that a
+ * warp takes (4.3e-5 at 128 rows of 32768 positions and 8 kv heads).  An exponential is the hardware's approximation (2 ulp, 0 below
  * 2^-126 of its piece's largest).  In the products
  * with the values a probability has 22 bits over an fp16 cache, 24 over a bf16 cache with
  * 32-bit outputs, 16 over a bf16 cache with 16-bit outputs.

@@ -275,7 +275,7 @@ struct AttSmem {
 // other's latency.  Bound: the keys' and values' bytes (16 rows of 16384 to 32768 positions,
 // 1.67 GB: 245 us, 6.8 TB/s), of short rows the chain from the lengths over the table to the
 // first keys, 3 us of it, and a tile after another of a warp, 1 us each (one row of 512: 6.7 us
-// with the join, one of 32768: 29.0).  The pages of a warp's tiles lie in shared memory and
+// with the join, one of 32768: 29.2).  The pages of a warp's tiles lie in shared memory and
 // come there without a register between: held by the lanes, they cost the long rows 2 %.
 template <typename C, typename Q, int HD, bool WIDE, int NQ, int NP>
 __global__ void __launch_bounds__(kAttThreads, ctas_per_sm(HD)) attend_kernel(const __grid_constant__ AttendArgs a) {
@@ -469,9 +469,58 @@ __global__ void __launch_bounds__(kAttThreads, ctas_per_sm(HD)) attend_kernel(co
     float scale[RH];  // of row g (WIDE: and row g + 8)
 #pragma unroll
     for (int h = 0; h < RH; ++h) scale[h] = SCALED ? st->scale[g + 8 * h] : a.scale;
+    // The warp's sums of weighted values to shared memory.  The tensor cores truncate what they add
+    // up: a sum of n tiles comes out too small, by 2.5e-8 n of itself, or 5e-8 n where the values have one
+    // sign (128 rows of 32768 positions, 862 tiles a warp: 4.3e-5).  Where 32-bit outputs show it, it is added every 32 tiles to what lies
+    // there, rounded to nearest and brought to the new maximum (below 3.8e-6, in the same time).  Outputs of 16
+    // bits round at 2^-12 and 2^-9, and with over 8 heads the registers that it takes cost 15 to 20 %
+    // of the time: there the sum stays in the tensor cores.
+    constexpr bool FLUSH = std::is_same<Q, float>::value && !WIDE;
+    auto flush = [&](bool first) {
+#pragma unroll
+      for (int h = 0; h < RH; ++h) {
+        const int head = g + 8 * h;
+        float* ml = s_ml + (warp * HEADS + head) * 2;
+        const float ms = m[h] == -INFINITY ? 0.f : m[h], f = first ? 0.f : ex2(ml[0] - ms);
+        float* dst = s_part + (warp * HEADS + head) * ROW;
+#pragma unroll
+        for (int d = 0; d < VH; ++d)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {  // columns 2c + e: dims 64 d + 16 c + 8 e + y
+            float4* p = reinterpret_cast<float4*>(dst + 64 * d + 16 * c + 8 * e);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              float w[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                w[y] = WIDE ? o[d][4 * q + y][2 * h + e] : o[d][4 * q + y][e] + o[d][4 * q + y][2 + e];
+              if (!first) {
+                const float4 v = p[q];
+                w[0] = fmaf(f, v.x, w[0]);
+                w[1] = fmaf(f, v.y, w[1]);
+                w[2] = fmaf(f, v.z, w[2]);
+                w[3] = fmaf(f, v.w, w[3]);
+              }
+              p[q] = make_float4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        __syncwarp();
+        if (c == 0) ml[0] = m[h];
+      }
+    };
     for (int k = 0; k < mine; ++k) {
       if ((k & 31) == 0) {
         __syncwarp();  // what is overwritten was read
+        if (FLUSH && k > 0) {
+          flush(k == 32);
+#pragma unroll
+          for (int h = 0; h < VH; ++h)
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[h][x][e] = 0.f;
+          __syncwarp();
+        }
         if (k + 32 + lane < mine) cp_async4(pages + ((k + 32 + lane) & 63), entry(k + 32 + lane));
       }
       const int q0 = p0, q1 = p1;
@@ -603,28 +652,13 @@ __global__ void __launch_bounds__(kAttThreads, ctas_per_sm(HD)) attend_kernel(co
       }
     }
     // ---- merge the warps' pieces in shared memory, fixed order
+    flush(!FLUSH || mine <= 32);
 #pragma unroll
     for (int h = 0; h < RH; ++h) {
       float lh = l[h];
       lh += __shfl_xor_sync(0xffffffffu, lh, 1);
       lh += __shfl_xor_sync(0xffffffffu, lh, 2);
-      const int head = g + 8 * h;
-      if (c == 0) {
-        s_ml[(warp * HEADS + head) * 2] = m[h];
-        s_ml[(warp * HEADS + head) * 2 + 1] = lh;
-      }
-      float* dst = s_part + (warp * HEADS + head) * ROW;
-#pragma unroll
-      for (int d = 0; d < VH; ++d)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {  // columns 2c + e: dims 64 d + 16 c + 8 e + y
-          float w[8];
-#pragma unroll
-          for (int y = 0; y < 8; ++y) w[y] = WIDE ? o[d][y][2 * h + e] : o[d][y][e] + o[d][y][2 + e];
-          float4* p = reinterpret_cast<float4*>(dst + 64 * d + 16 * c + 8 * e);
-          p[0] = make_float4(w[0], w[1], w[2], w[3]);
-          p[1] = make_float4(w[4], w[5], w[6], w[7]);
-        }
+      if (c == 0) s_ml[(warp * HEADS + g + 8 * h) * 2 + 1] = lh;
     }
     __syncthreads();
     const int r = st->row, j = st->head, slot = st->slot;

@@ -347,6 +347,27 @@ def test_attention_many_tiles_of_a_warp(paged, hd):
     _check_attend(q, kp, vp, table, lens, out, lse, 1 / math.sqrt(hd), rows=[0] * 16)
 
 
+@pytest.mark.parametrize("cache,hd", [("bf16", 64), ("f16", 64), ("bf16", 128), ("f16", 128)])
+def test_attention_of_long_batches_does_not_shrink(paged, cache, hd):
+    """Many rows over one long sequence, some 900 tiles a warp, 32-bit outputs.  The tensor cores truncate: each of at most
+    two products per tile takes up to 2^-23 of the sum so far, half of which 32 tiles have on average before it is
+    put away rounded to nearest, 32 * 2^-23 in all, and the rest of the arithmetic is not biased."""
+    g = torch.Generator(device=DEV).manual_seed(16)
+    R, n = 128, 32768
+    kp, vp, table = _make_cache(g, [n], 8, hd, 64, cache, poison=False)
+    vp.abs_()                                  # outputs that do not cancel
+    q = torch.randn(R, 16, hd, generator=g, device=DEV)
+    out, lse = paged.paged_attention(q, kp, vp, ints(table), ints([n] * R), rows=ints([0] * R), return_lse=True)
+    at = ints(table)[0, : n // 64].long()
+    k, v = (p[at].double().permute(1, 0, 2, 3).reshape(8, n, hd) for p in (kp, vp))
+    for r in range(0, R, 32):
+        s = torch.einsum("jgd,jtd->jgt", q[r].double().view(8, 2, hd), k) / math.sqrt(hd)
+        want = torch.einsum("jgt,jtd->jgd", torch.softmax(s, -1), v).reshape(16, hd)
+        shrink = ((out[r].double() * want).sum() / (want * want).sum()).item() - 1
+        assert abs(shrink) <= 32 * 2.0 ** -23, (r, shrink)
+        assert (lse[r].double() - torch.logsumexp(s, -1).reshape(-1)).abs().max().item() <= 2.0 ** -18
+
+
 @pytest.mark.parametrize("longest", [150, 400, 900])
 @pytest.mark.parametrize("hd", [64, 128])
 def test_attention_of_as_many_segments_as_ctas(paged, longest, hd):
