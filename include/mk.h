@@ -333,7 +333,8 @@ mk_status mk_stream_bench(int page_bytes, int n_pages, int mode, int hint, long 
  *
  * What only the device can see is reported through `status`, a device int32[4] the caller
  * zeroes (NULL: not reported): the first error found is kept as {mk_status, operator, row,
- * value} (operator: 1 append, 2 attention, 3 update, 4 compaction, 5 selection) and
+ * value} (operator: 1 append, 2 attention, 3 update, 4 compaction, 5 selection, 6 tree, 7
+ * acceptance, 8 bounds, 9 page scores, 10 chosen pages) and
  * mk_paged_status reads it back.  A bad index is never followed: each call says what it
  * does instead. */
 typedef struct {
@@ -389,6 +390,12 @@ typedef struct {
   float mscale;            /* factor of cos and sin                                         */
 } mk_append_args;
 mk_status mk_rope_append(const mk_append_args* args, const mk_page_view* cache, int32_t* status, void* stream);
+/* The same with the place of every token's key and value apart from its position: slots device
+ * [n_tokens] (NULL: the positions).  What is said of a position past the table holds for a slot,
+ * and for one below 0.  The nodes of a drafted tree lie in slots of their own at positions that
+ * siblings share. */
+mk_status mk_rope_append_at(const mk_append_args* args, const int32_t* slots, const mk_page_view* cache, int32_t* status,
+                            void* stream);
 
 /* Attention of one new query per row over its paged positions:
  *   s_t = cap(scale * q . k_t),  cap(x) = softcap * tanh(x / softcap) (softcap 0: x),
@@ -500,6 +507,107 @@ typedef struct {
 } mk_select_args;
 mk_status mk_beam_select(const mk_select_args* args, int32_t* status, void* stream);
 mk_status mk_beam_select_workspace(int groups, int beams, int vocab, size_t* bytes);
+
+/* ---------------------------------------------------------------------------------------
+ * Drafted tokens.  A row's tree has n_nodes nodes: node i's parent is parents[r][i], a lower node
+ * or -1 (a root, which follows the row's cached positions); any other value means that the node
+ * is absent, and so are the nodes below it.  Node i's key and value lie in slot lens[r] + i of the
+ * row (mk_rope_append_at puts them there), its position is lens[r] + the number of its ancestors.
+ *
+ * Attention of every node over the row's slots [0, lens[r]) and over its ancestors and itself:
+ * scores, softmax and log-sum-exp as mk_paged_attention's.  window > 0: only positions above the
+ * node's own minus window.  An absent node, and every node of a row whose lens is negative or
+ * that is outside the table, gets zeros and lse -inf.  Nothing that a node does not see is read
+ * for its value: whatever lies there, NaN included, has no effect on it.  Slots past the table are
+ * dropped and those on a bad page masked, each reported (MK_ERR_PAGES).  A NaN or infinite value
+ * that a node sees makes its results NaN or infinite. */
+typedef struct {
+  const void* q;           /* [n_rows][n_nodes][n_heads][head_dim], element strides below    */
+  void* out;               /* its vectors must not overlap                                  */
+  float* lse;              /* [n_rows][n_nodes][n_heads] or NULL                            */
+  int dtype;               /* of q and out: MK_F16, MK_BF16 or MK_F32                       */
+  int n_rows, n_nodes, n_heads;  /* n_nodes 1..128; n_heads / n_kv_heads: 1..16             */
+  long long q_row, q_node, q_head, o_row, o_node, o_head;
+  const int32_t* lens;     /* [n_rows]                                                      */
+  const int32_t* parents;  /* [n_rows][n_nodes]                                             */
+  const int32_t* rows;     /* table row of each; NULL: row r                                */
+  float scale, softcap;
+  int window;
+  void* workspace;         /* 16-byte aligned                                               */
+  size_t workspace_bytes;
+} mk_tree_args;
+mk_status mk_tree_attention(const mk_tree_args* args, const mk_page_view* cache, int32_t* status, void* stream);
+/* Bytes of workspace a call needs on the current device. */
+mk_status mk_tree_attention_workspace(int n_heads, int n_kv_heads, int head_dim, size_t* bytes);
+
+/* Acceptance: node 0 (parent -1) is the token that was chosen before and stands; from there on, of
+ * a node's children the lowest one is accepted whose token is the node's choice (what the model
+ * chose after it).  The accepted nodes' keys and values move, in every layer, from slot lens[r] +
+ * node to the row's next slots in order, and lens[r] grows by their number.  out_path [r] holds the
+ * accepted nodes in order, out_tokens their choices (the next tokens, the last of them not yet
+ * in the cache), both -1 behind out_count[r].  A row whose node 0 is absent or whose lens is
+ * negative accepts nothing.  So does one that would reach past the table or onto a bad page, which
+ * is reported (MK_ERR_PAGES).  The pages that a row's tree lies in have to be its own. */
+typedef struct {
+  int32_t* lens;           /* [rows of the table] in and out                                */
+  int n_kv_heads, n_nodes; /* n_nodes 1..128                                                */
+  const int32_t *tokens, *parents, *choices;  /* [rows of the table][n_nodes]               */
+  int32_t *out_tokens, *out_path;             /* [rows of the table][n_nodes]               */
+  int32_t* out_count;      /* [rows of the table]                                           */
+} mk_accept_args;
+/* The pool's refs are not used (NULL will do); a page is [n_kv_heads][page_size][vector], the vectors
+ * of a multiple of 16 bytes up to 256. */
+mk_status mk_accept_drafts(const mk_accept_args* args, const mk_page_pool* pool, int32_t* status, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Attention over chosen pages.  bounds [n_pages][n_kv_heads][2][head_dim], of the cache's type,
+ * 16-byte aligned: the least and the greatest value of every element among a page's keys.
+ *
+ * mk_update_bounds takes the bounds of every page that holds one of the last n_new positions of a
+ * row from the page's keys up to the row's end (NaN where a key is NaN).  Lengths past the table
+ * are cut, bad pages skipped, both reported (MK_ERR_PAGES).  Of a page that rows of different
+ * lengths share, the bounds are those of one of them, element by element. */
+typedef struct {
+  void* bounds;
+  const int32_t* lens;     /* [n_rows]                                                      */
+  const int32_t* rows;     /* table row of each; NULL: row r                                */
+  int n_rows, n_new;       /* n_new >= 1                                                    */
+} mk_bounds_args;
+/* Of the cache only k is read. */
+mk_status mk_update_bounds(const mk_bounds_args* args, const mk_page_view* cache, int32_t* status, void* stream);
+
+/* scores [n_rows][n_kv_heads][table_width]: of the heads of a group the greatest
+ * sum_d max(q_d low_d, q_d high_d), which no key within the page's bounds exceeds; in 32 bits.
+ * -inf for table entries behind a row's last page, for bad pages (reported) and for rows
+ * outside the table (reported).  NaN in a query or a page's bounds makes the score NaN. */
+typedef struct {
+  const void* q;           /* [n_rows][n_heads][head_dim], element strides below            */
+  int dtype;               /* of q: MK_F16, MK_BF16 or MK_F32                               */
+  int n_rows, n_heads;     /* n_heads / n_kv_heads: 1..16                                   */
+  long long q_row, q_head;
+  const void* bounds;
+  const int32_t *lens, *rows;
+  float* scores;
+} mk_scores_args;
+/* Of the cache only the shape, the type and the table are used. */
+mk_status mk_page_scores(const mk_scores_args* args, const mk_page_view* cache, int32_t* status, void* stream);
+
+/* mk_paged_attention over n_blocks pages of each row, chosen apart for every kv head: the first
+ * `first` and the last `last` ones and those with the greatest scores of the others, ties to the
+ * lower page; NaN counts as +inf.  All of them where a row has no more.  pages (or NULL)
+ * [n_rows][n_kv_heads][n_blocks] receives their numbers within the row in rising order, -1 behind
+ * them.  attend->window must be 0 and attend->len_add is not used; lengths past the table are cut
+ * (reported).  Workspace: mk_sparse_attention_workspace. */
+typedef struct {
+  const float* scores;     /* [n_rows][n_kv_heads][scores_head], the first table_width used  */
+  long long scores_row, scores_head;  /* strides                                            */
+  int n_blocks;            /* first + last .. 65536                                         */
+  int first, last;         /* first >= 0, last >= 1                                         */
+  int32_t* pages;
+} mk_sparse_args;
+mk_status mk_sparse_attention(const mk_attend_args* attend, const mk_sparse_args* args, const mk_page_view* cache,
+                              int32_t* status, void* stream);
+mk_status mk_sparse_attention_workspace(int n_rows, int n_heads, int n_kv_heads, int head_dim, int n_blocks, size_t* bytes);
 
 /* A decoder over a paged cache: mk_create's model (weights, batches and dtypes as there) with
  * the cache in pages, so that sequences share pages, grow page by page and are forked by

@@ -114,6 +114,33 @@ class mk_select_args(ctypes.Structure):
                 ("workspace_bytes", c_size_t)]
 
 
+class mk_tree_args(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("out", c_void_p), ("lse", c_void_p), ("dtype", c_int), ("n_rows", c_int),
+                ("n_nodes", c_int), ("n_heads", c_int), ("q_row", c_ll), ("q_node", c_ll), ("q_head", c_ll),
+                ("o_row", c_ll), ("o_node", c_ll), ("o_head", c_ll), ("lens", c_void_p), ("parents", c_void_p),
+                ("rows", c_void_p), ("scale", c_float), ("softcap", c_float), ("window", c_int), ("workspace", c_void_p),
+                ("workspace_bytes", c_size_t)]
+
+
+class mk_accept_args(ctypes.Structure):
+    _fields_ = [("lens", c_void_p), ("n_kv_heads", c_int), ("n_nodes", c_int), ("tokens", c_void_p), ("parents", c_void_p),
+                ("choices", c_void_p), ("out_tokens", c_void_p), ("out_path", c_void_p), ("out_count", c_void_p)]
+
+
+class mk_bounds_args(ctypes.Structure):
+    _fields_ = [("bounds", c_void_p), ("lens", c_void_p), ("rows", c_void_p), ("n_rows", c_int), ("n_new", c_int)]
+
+
+class mk_scores_args(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("dtype", c_int), ("n_rows", c_int), ("n_heads", c_int), ("q_row", c_ll),
+                ("q_head", c_ll), ("bounds", c_void_p), ("lens", c_void_p), ("rows", c_void_p), ("scores", c_void_p)]
+
+
+class mk_sparse_args(ctypes.Structure):
+    _fields_ = [("scores", c_void_p), ("scores_row", c_ll), ("scores_head", c_ll), ("n_blocks", c_int), ("first", c_int),
+                ("last", c_int), ("pages", c_void_p)]
+
+
 class mk_paged_kv(ctypes.Structure):
     _fields_ = [("k", c_void_p), ("v", c_void_p), ("layer_stride", c_ll), ("page_stride", c_ll), ("n_pages", c_int),
                 ("page_size", c_int), ("table", c_void_p), ("n_rows", c_int), ("table_width", c_int),
@@ -155,6 +182,8 @@ mk_decode_step_noalloc = _fn("mk_decode_step_noalloc", [ctypes.POINTER(mk_model_
 P_size = ctypes.POINTER(c_size_t)
 mk_rope_freqs = _fn("mk_rope_freqs", [ctypes.POINTER(mk_rope_desc), ctypes.POINTER(c_double), P_f32])
 mk_rope_append = _fn("mk_rope_append", [ctypes.POINTER(mk_append_args), ctypes.POINTER(mk_page_view), c_void_p, c_void_p])
+mk_rope_append_at = _fn("mk_rope_append_at", [ctypes.POINTER(mk_append_args), c_void_p, ctypes.POINTER(mk_page_view),
+                                              c_void_p, c_void_p])
 mk_paged_attention = _fn("mk_paged_attention", [ctypes.POINTER(mk_attend_args), ctypes.POINTER(mk_page_view), c_void_p,
                                                 c_void_p])
 mk_paged_attention_workspace = _fn("mk_paged_attention_workspace", [c_int, c_int, c_int, P_size])
@@ -163,6 +192,15 @@ mk_compact_pages = _fn("mk_compact_pages", [ctypes.POINTER(mk_page_pool), c_void
 mk_update_pages_workspace = _fn("mk_update_pages_workspace", [c_int, c_int, c_int, P_size])
 mk_beam_select = _fn("mk_beam_select", [ctypes.POINTER(mk_select_args), c_void_p, c_void_p])
 mk_beam_select_workspace = _fn("mk_beam_select_workspace", [c_int, c_int, c_int, P_size])
+mk_tree_attention = _fn("mk_tree_attention", [ctypes.POINTER(mk_tree_args), ctypes.POINTER(mk_page_view), c_void_p,
+                                              c_void_p])
+mk_tree_attention_workspace = _fn("mk_tree_attention_workspace", [c_int, c_int, c_int, P_size])
+mk_accept_drafts = _fn("mk_accept_drafts", [ctypes.POINTER(mk_accept_args), ctypes.POINTER(mk_page_pool), c_void_p, c_void_p])
+mk_update_bounds = _fn("mk_update_bounds", [ctypes.POINTER(mk_bounds_args), ctypes.POINTER(mk_page_view), c_void_p, c_void_p])
+mk_page_scores = _fn("mk_page_scores", [ctypes.POINTER(mk_scores_args), ctypes.POINTER(mk_page_view), c_void_p, c_void_p])
+mk_sparse_attention = _fn("mk_sparse_attention", [ctypes.POINTER(mk_attend_args), ctypes.POINTER(mk_sparse_args),
+                                                  ctypes.POINTER(mk_page_view), c_void_p, c_void_p])
+mk_sparse_attention_workspace = _fn("mk_sparse_attention_workspace", [c_int, c_int, c_int, c_int, c_int, P_size])
 mk_create_paged = _fn("mk_create_paged", [ctypes.POINTER(mk_model_desc), ctypes.POINTER(mk_weights),
                                           ctypes.POINTER(mk_paged_kv), ctypes.POINTER(mk_rope_desc), c_int,
                                           ctypes.POINTER(mk_options), c_void_p, ctypes.POINTER(c_void_p)])

@@ -23,7 +23,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = [f"mk_k_{d}_{s}{m}{t}.cu" for d in ("f16", "bf16") for s in ("counter", "sentinel") for m in ("", "_ms")
            for t in ("", "_am", "_tc")] + ["mk_kernel.cu", "mk_host.cu", "mk_plan.cpp", "mk_tmap.cpp", "mk_noalloc.cu",
-                                           "mk_append.cu", "mk_attend.cu", "mk_pages.cu", "mk_select.cu"]
+                                           "mk_append.cu", "mk_attend.cu", "mk_pages.cu", "mk_select.cu",
+                                           "mk_tree.cu", "mk_accept.cu", "mk_blocks.cu"]
 
 
 def _nvcc():

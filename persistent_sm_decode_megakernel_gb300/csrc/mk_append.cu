@@ -51,7 +51,7 @@ struct AppendArgs {
   const void *q, *k, *v;
   void *qo, *kc, *vc;
   long long q_t, q_h, k_t, k_h, v_t, v_h, o_t, o_h, page_stride, table_stride;
-  const int32_t *positions, *rows, *table;
+  const int32_t *positions, *slots, *rows, *table;
   const double* freqs;
   int32_t* status;
   int n_tokens, share, hq, hkv, page_size, n_pages, n_rows, width, n_freqs;
@@ -84,9 +84,11 @@ __device__ __forceinline__ void turn_of(const AppendArgs& a, int pos, int i, flo
 
 // where a token goes: the page and the row of it (page -1: nowhere)
 __device__ __forceinline__ int2 place_of(const AppendArgs& a, int t, int pos, bool tell) {
-  const int row = a.rows ? a.rows[t] : t, slot = pos / a.page_size;
+  const int row = a.rows ? a.rows[t] : t;
+  if (a.slots) pos = a.slots[t];
+  const int slot = pos / a.page_size;  // (of the table; pos is below 0 where a slot given is)
   int page = -1;
-  if ((unsigned)row < (unsigned)a.n_rows && slot < a.width) page = a.table[(long long)row * a.table_stride + slot];
+  if ((unsigned)row < (unsigned)a.n_rows && pos >= 0 && slot < a.width) page = a.table[(long long)row * a.table_stride + slot];
   if ((unsigned)page >= (unsigned)a.n_pages) {
     if (tell) report(a.status, MK_ERR_PAGES, PO_APPEND, row, pos);
     page = -1;
@@ -267,6 +269,11 @@ mk_status launch_append(const AppendArgs& a, int n_sm, int cache_dtype, int hd, 
 
 extern "C" mk_status mk_rope_append(const mk_append_args* args, const mk_page_view* cache, int32_t* status,
                                     void* stream) {
+  return mk_rope_append_at(args, nullptr, cache, status, stream);
+}
+
+extern "C" mk_status mk_rope_append_at(const mk_append_args* args, const int32_t* slots, const mk_page_view* cache,
+                                       int32_t* status, void* stream) {
   using namespace mk;
   return c_entry([&]() -> mk_status {
     const std::string e = check_view(cache);
@@ -294,7 +301,7 @@ extern "C" mk_status mk_rope_append(const mk_append_args* args, const mk_page_vi
     a.q_t = args->q_token; a.q_h = args->q_head; a.k_t = args->k_token; a.k_h = args->k_head;
     a.v_t = args->v_token; a.v_h = args->v_head; a.o_t = args->o_token; a.o_h = args->o_head;
     a.page_stride = cache->page_stride; a.table_stride = cache->table_stride;
-    a.positions = args->positions; a.rows = args->rows; a.table = cache->table; a.freqs = args->freqs; a.status = status;
+    a.positions = args->positions; a.slots = slots; a.rows = args->rows; a.table = cache->table; a.freqs = args->freqs; a.status = status;
     a.n_tokens = args->n_tokens; a.hq = args->q ? args->n_heads : 0;
     a.hkv = cache->n_kv_heads; a.page_size = cache->page_size; a.n_pages = cache->n_pages; a.n_rows = cache->n_rows;
     a.width = cache->table_width; a.n_freqs = args->n_freqs; a.mscale = args->mscale;
@@ -381,9 +388,10 @@ extern "C" mk_status mk_paged_status(int32_t* status, void* stream) {
     if (e == cudaSuccess && got[0]) e = cudaMemsetAsync(status, 0, sizeof got, s);
     if (e != cudaSuccess) return paged_fail(MK_ERR_CUDA, std::string("mk_paged_status: ") + cudaGetErrorString(e));
     if (!got[0]) return MK_OK;
-    static const char* const ops[] = {"?", "append", "attention", "page update", "compaction", "selection"};
+    static const char* const ops[] = {"?", "append", "attention", "page update", "compaction", "selection",
+                                      "tree attention", "acceptance", "bounds", "page scores", "chosen pages"};
     char buf[160];
-    snprintf(buf, sizeof buf, "%s: %s at row %d, value %d", ops[got[1] >= 1 && got[1] <= 5 ? got[1] : 0],
+    snprintf(buf, sizeof buf, "%s: %s at row %d, value %d", ops[got[1] >= 1 && got[1] <= 10 ? got[1] : 0],
              got[0] == MK_ERR_NAN ? "a NaN or infinite logit" : "a bad page, row, length or parent, or too few free pages",
              got[2], got[3]);
     return paged_fail((mk_status)got[0], buf);

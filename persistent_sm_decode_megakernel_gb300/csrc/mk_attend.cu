@@ -10,6 +10,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "mk_attend.h"
 #include "mk_internal.h"
 #include "mk_device.cuh"
 #include "mk_paged.cuh"
@@ -36,6 +37,7 @@ struct AttendArgs {
   const int32_t *lens, *rows, *table;
   int32_t* status;
   long long q_row, q_head, o_row, o_head, page_stride, table_stride;
+  long long table_head;                 // from a kv head's table row to the next's; 0: the heads share one
   int n_rows, hq, hkv, group, len_add, window, page_size, n_pages, table_rows, cap;  // cap: positions of a table row
   int tpp;                              // tiles per page
   unsigned tpp_inverse;                 // 2^32 / tpp, rounded up
@@ -338,7 +340,7 @@ __global__ void __launch_bounds__(kAttThreads, ctas_per_sm(HD)) attend_kernel(co
         st->row = r;
         st->before = rbase;
         st->head = j;
-        st->table = a.table + (long long)sp.trow * a.table_stride;
+        st->table = a.table + (long long)sp.trow * a.table_stride + j * a.table_head;
         st->slot = whole ? 2 : first == 0;  // 0: continues a segment, 1: begins one, 2: is one
         if (first == 0) {  // the segment's begin knows where it ends
           const int last = (int)((unsigned)(seg + each - 1) / (unsigned)st->share);
@@ -824,64 +826,78 @@ extern "C" mk_status mk_paged_attention(const mk_attend_args* args, const mk_pag
   return c_entry([&]() -> mk_status {
     const std::string e = check_view(cache);
     if (!e.empty()) return paged_fail(MK_ERR_INVALID, e);
-    if (!args || !args->q || !args->out || !args->lens) return paged_fail(MK_ERR_INVALID, "NULL argument");
-    if (args->dtype < MK_F16 || args->dtype > MK_F32) return paged_fail(MK_ERR_INVALID, "dtype");
-    if (args->n_heads < 1 || args->n_heads % cache->n_kv_heads || args->n_heads / cache->n_kv_heads > kMaxGroup)
-      return paged_fail(MK_ERR_INVALID, "n_heads / n_kv_heads must be a whole number in [1, 16]");
-    if (args->n_rows < 0 || (long long)args->n_rows * args->n_heads > 0x7fffffffLL)
-      return paged_fail(MK_ERR_INVALID, "n_rows out of range");
-    if (args->window < 0) return paged_fail(MK_ERR_INVALID, "window must not be negative");
-    const float factor = args->softcap > 0.f ? args->scale / args->softcap : args->scale * kLog2e;
-    if (!(args->softcap >= 0.f && args->softcap * kLog2e < INFINITY) || !(fabsf(factor) < INFINITY))
-      return paged_fail(MK_ERR_INVALID, "scale or softcap is not finite, too large, or softcap negative or too small for scale");
-    const size_t esz = args->dtype == MK_F32 ? 4 : 2;
-    if (!aligned_to(args->q, esz) || !aligned_to(args->out, esz))
-      return paged_fail(MK_ERR_INVALID, "q and out must be aligned to their type");
-    if (overlaps(args->n_rows, args->o_row, args->n_heads, args->o_head, cache->head_dim))
-      return paged_fail(MK_ERR_INVALID, "the vectors of out overlap");
-    const std::string line = check_line(cache, args->n_rows, args->window);
-    if (!line.empty()) return paged_fail(MK_ERR_INVALID, line);
-    if (!args->workspace || !aligned_to(args->workspace, 16))
-      return paged_fail(MK_ERR_INVALID, "the workspace is missing or unaligned");
-    if (args->n_rows == 0) return MK_OK;
-    size_t need = 0;
-    mk_status s = mk_paged_attention_workspace(args->n_heads, cache->n_kv_heads, cache->head_dim, &need);
-    if (s) return s;
-    if (args->workspace_bytes < need)
-      return paged_fail(MK_ERR_INVALID, "the workspace is too small (mk_paged_attention_workspace)");
-    int n_sm = 0;
-    s = sm_count(&n_sm);
-    if (s) return s;
-    AttendArgs a{};
-    a.q = args->q; a.k = cache->k; a.v = cache->v; a.out = args->out; a.lse = args->lse;
-    a.joins = static_cast<int4*>(args->workspace);
-    a.lens = args->lens; a.rows = args->rows; a.table = cache->table; a.status = status;
-    a.q_row = args->q_row; a.q_head = args->q_head; a.o_row = args->o_row; a.o_head = args->o_head;
-    a.page_stride = cache->page_stride; a.table_stride = cache->table_stride;
-    a.n_rows = args->n_rows; a.hq = args->n_heads; a.hkv = cache->n_kv_heads; a.group = args->n_heads / cache->n_kv_heads;
-    a.len_add = args->len_add; a.window = args->window; a.page_size = cache->page_size; a.n_pages = cache->n_pages;
-    a.table_rows = cache->n_rows; a.cap = cache->table_width * cache->page_size;  // at most 2^30
-    a.tpp = a.page_size / kTile;
-    a.tpp_inverse = a.tpp > 1 ? (unsigned)(((1ULL << 32) + a.tpp - 1) / a.tpp) : 0;
-    a.n_cta = n_sm * ctas_per_sm(cache->head_dim);
-    a.part = reinterpret_cast<float*>(a.joins + a.n_cta);
-    a.q_vec = aligned_to(a.q, 16) && a.q_row * (long long)esz % 16 == 0 && a.q_head * (long long)esz % 16 == 0;
-    a.by_segment = (long long)a.n_rows * a.hkv <= a.n_cta;
-    a.scale = factor;
-    a.softcap = args->softcap * kLog2e;
-    // 16-bit queries of the cache's type are exact in one part.  Other queries are split into
-    // 2 parts of fp16 (22 bits, each head at a power of two of its own) or 3 of bf16 (24 bits);
-    // probabilities likewise, 2 parts of
-    // bf16 (16 bits) being enough for an output of 16 bits: 16 rows of 16384 to 32768 positions
-    // lie 1.66e-3 (all of it the output's rounding) from the 64-bit result with 2 parts and
-    // with 3, and a batch of 61 short rows takes 13.7 us with 2, 14.3 with 3.
-    if (cache->dtype == MK_F16) {
-      if (args->dtype == MK_F16) return launch_attend<__half, __half, 1, 2>(a, cache->head_dim, stream);
-      if (args->dtype == MK_BF16) return launch_attend<__half, __nv_bfloat16, 2, 2>(a, cache->head_dim, stream);
-      return launch_attend<__half, float, 2, 2>(a, cache->head_dim, stream);
-    }
-    if (args->dtype == MK_BF16) return launch_attend<__nv_bfloat16, __nv_bfloat16, 1, 2>(a, cache->head_dim, stream);
-    if (args->dtype == MK_F16) return launch_attend<__nv_bfloat16, __half, 2, 2>(a, cache->head_dim, stream);
-    return launch_attend<__nv_bfloat16, float, 3, 3>(a, cache->head_dim, stream);
+    if (!args) return paged_fail(MK_ERR_INVALID, "NULL argument");
+    return attend_pages(*args, *cache, 0, status, stream, nullptr);
   });
 }
+
+namespace mk {
+mk_status attend_pages(const mk_attend_args& attend, const mk_page_view& view, long long head_stride, int32_t* status,
+                       void* stream, const std::function<mk_status()>& before) {
+  const mk_attend_args* args = &attend;
+  const mk_page_view* cache = &view;
+  if (!args->q || !args->out || !args->lens) return paged_fail(MK_ERR_INVALID, "NULL argument");
+  if (args->dtype < MK_F16 || args->dtype > MK_F32) return paged_fail(MK_ERR_INVALID, "dtype");
+  if (args->n_heads < 1 || args->n_heads % cache->n_kv_heads || args->n_heads / cache->n_kv_heads > kMaxGroup)
+    return paged_fail(MK_ERR_INVALID, "n_heads / n_kv_heads must be a whole number in [1, 16]");
+  if (args->n_rows < 0 || (long long)args->n_rows * args->n_heads > 0x7fffffffLL)
+    return paged_fail(MK_ERR_INVALID, "n_rows out of range");
+  if (args->window < 0) return paged_fail(MK_ERR_INVALID, "window must not be negative");
+  const float factor = args->softcap > 0.f ? args->scale / args->softcap : args->scale * kLog2e;
+  if (!(args->softcap >= 0.f && args->softcap * kLog2e < INFINITY) || !(fabsf(factor) < INFINITY))
+    return paged_fail(MK_ERR_INVALID, "scale or softcap is not finite, too large, or softcap negative or too small for scale");
+  const size_t esz = args->dtype == MK_F32 ? 4 : 2;
+  if (!aligned_to(args->q, esz) || !aligned_to(args->out, esz))
+    return paged_fail(MK_ERR_INVALID, "q and out must be aligned to their type");
+  if (overlaps(args->n_rows, args->o_row, args->n_heads, args->o_head, cache->head_dim))
+    return paged_fail(MK_ERR_INVALID, "the vectors of out overlap");
+  const std::string line = check_line(cache, args->n_rows, args->window);
+  if (!line.empty()) return paged_fail(MK_ERR_INVALID, line);
+  if (!args->workspace || !aligned_to(args->workspace, 16))
+    return paged_fail(MK_ERR_INVALID, "the workspace is missing or unaligned");
+  if (args->n_rows == 0) return MK_OK;
+  size_t need = 0;
+  mk_status s = mk_paged_attention_workspace(args->n_heads, cache->n_kv_heads, cache->head_dim, &need);
+  if (s) return s;
+  if (args->workspace_bytes < need)
+    return paged_fail(MK_ERR_INVALID, "the workspace is too small (mk_paged_attention_workspace)");
+  int n_sm = 0;
+  s = sm_count(&n_sm);
+  if (s) return s;
+  AttendArgs a{};
+  a.q = args->q; a.k = cache->k; a.v = cache->v; a.out = args->out; a.lse = args->lse;
+  a.joins = static_cast<int4*>(args->workspace);
+  a.lens = args->lens; a.rows = args->rows; a.table = cache->table; a.status = status;
+  a.q_row = args->q_row; a.q_head = args->q_head; a.o_row = args->o_row; a.o_head = args->o_head;
+  a.page_stride = cache->page_stride; a.table_stride = cache->table_stride; a.table_head = head_stride;
+  a.n_rows = args->n_rows; a.hq = args->n_heads; a.hkv = cache->n_kv_heads; a.group = args->n_heads / cache->n_kv_heads;
+  a.len_add = args->len_add; a.window = args->window; a.page_size = cache->page_size; a.n_pages = cache->n_pages;
+  a.table_rows = cache->n_rows; a.cap = cache->table_width * cache->page_size;  // at most 2^30
+  a.tpp = a.page_size / kTile;
+  a.tpp_inverse = a.tpp > 1 ? (unsigned)(((1ULL << 32) + a.tpp - 1) / a.tpp) : 0;
+  a.n_cta = n_sm * ctas_per_sm(cache->head_dim);
+  a.part = reinterpret_cast<float*>(a.joins + a.n_cta);
+  a.q_vec = aligned_to(a.q, 16) && a.q_row * (long long)esz % 16 == 0 && a.q_head * (long long)esz % 16 == 0;
+  a.by_segment = (long long)a.n_rows * a.hkv <= a.n_cta;
+  a.scale = factor;
+  a.softcap = args->softcap * kLog2e;
+  if (before) {
+    s = before();
+    if (s) return s;
+  }
+  // 16-bit queries of the cache's type are exact in one part.  Other queries are split into
+  // 2 parts of fp16 (22 bits, each head at a power of two of its own) or 3 of bf16 (24 bits);
+  // probabilities likewise, 2 parts of
+  // bf16 (16 bits) being enough for an output of 16 bits: 16 rows of 16384 to 32768 positions
+  // lie 1.66e-3 (all of it the output's rounding) from the 64-bit result with 2 parts and
+  // with 3, and a batch of 61 short rows takes 13.7 us with 2, 14.3 with 3.
+  if (cache->dtype == MK_F16) {
+    if (args->dtype == MK_F16) return launch_attend<__half, __half, 1, 2>(a, cache->head_dim, stream);
+    if (args->dtype == MK_BF16) return launch_attend<__half, __nv_bfloat16, 2, 2>(a, cache->head_dim, stream);
+    return launch_attend<__half, float, 2, 2>(a, cache->head_dim, stream);
+  }
+  if (args->dtype == MK_BF16) return launch_attend<__nv_bfloat16, __nv_bfloat16, 1, 2>(a, cache->head_dim, stream);
+  if (args->dtype == MK_F16) return launch_attend<__nv_bfloat16, __half, 2, 2>(a, cache->head_dim, stream);
+  return launch_attend<__nv_bfloat16, float, 3, 3>(a, cache->head_dim, stream);
+}
+}  // namespace mk

@@ -14,7 +14,8 @@ namespace mk {
 
 void set_last_error(const std::string& msg);  // defined beside mk_last_error
 
-enum PagedOp : int { PO_APPEND = 1, PO_ATTEND = 2, PO_UPDATE = 3, PO_COMPACT = 4, PO_SELECT = 5 };
+enum PagedOp : int { PO_APPEND = 1, PO_ATTEND = 2, PO_UPDATE = 3, PO_COMPACT = 4, PO_SELECT = 5, PO_TREE = 6, PO_ACCEPT = 7, PO_BOUNDS = 8,
+                     PO_SCORES = 9, PO_SPARSE = 10 };
 
 inline mk_status paged_fail(mk_status s, const std::string& m) {
   set_last_error(m);

@@ -217,9 +217,9 @@ PyObject* given(PyObject* o) {
   return o;
 }
 
-// (q, k, v, k_pages, v_pages, table, positions, rows, freqs, interleaved, mscale, q_out, status)
+// (q, k, v, k_pages, v_pages, table, positions, rows, freqs, interleaved, mscale, q_out, status, slots)
 PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
-  if (!count_is(n_args, 13)) return nullptr;
+  if (!count_is(n_args, 14)) return nullptr;
   return guarded([&]() -> PyObject* {
     at::Device dev(at::kCPU);
     const mk_page_view view = view_of(a[3], a[4], a[5], &dev);
@@ -259,8 +259,9 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     x.interleaved = PyObject_IsTrue(a[9]);
     x.mscale = (float)number(a[10]);
     int32_t* status = status_of(a[12], dev);
+    const int32_t* slots = int32s(a[13], "slots", dev, n, -1, true);
     if (n > 0) {
-      check(mk_rope_append(&x, &view, status, stream_of(dev)), "mk_rope_append");
+      check(mk_rope_append_at(&x, slots, &view, status, stream_of(dev)), "mk_rope_append");
       written(a[3], a[4], a[11], a[12]);
     }
     if (a[0] == Py_None) Py_RETURN_NONE;
@@ -314,6 +315,199 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
+// [n, nodes, heads, dim] of one type and device with contiguous dims; its strides
+void nodes_of(const at::Tensor& t, const char* name, at::IntArrayRef sizes, at::ScalarType type, at::Device dev, long long* s0,
+              long long* s1, long long* s2) {
+  if (t.dim() != 4 || t.sizes() != sizes || t.scalar_type() != type || t.device() != dev || t.stride(3) != 1)
+    value_error(std::string(name) + " must be [rows, nodes, heads, head_dim], of the queries' type, on " + dev.str() +
+                ", its last dim contiguous");
+  *s0 = t.stride(0);
+  *s1 = t.stride(1);
+  *s2 = t.stride(2);
+}
+// strides of dims of one element do not count
+long long stride_of(const at::Tensor& t, int dim) { return t.size(dim) > 1 ? t.stride(dim) : 0; }
+
+// (q, k_pages, v_pages, table, lens, parents, rows, scale, softcap, window, out, return_lse, status)
+PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  if (!count_is(n_args, 13)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    at::Device dev(at::kCPU);
+    const mk_page_view view = view_of(a[1], a[2], a[3], &dev);
+    const at::Tensor& q = tensor(a[0], "q");
+    need(q.dim() == 4 && q.size(3) == view.head_dim, "q must be [rows, nodes, heads, head_dim], head_dim the pages'");
+    mk_tree_args x{};
+    x.dtype = dtype_of(q, "q");
+    const int64_t n = q.size(0), nodes = q.size(1), hq = q.size(2);
+    nodes_of(q, "q", q.sizes(), q.scalar_type(), dev, &x.q_row, &x.q_node, &x.q_head);
+    const c10::cuda::CUDAGuard guard(dev);
+    const at::Tensor out = a[10] == Py_None ? Fresh::one(q.sizes(), q.scalar_type(), dev) : tensor(a[10], "out");
+    nodes_of(out, "out", q.sizes(), q.scalar_type(), dev, &x.o_row, &x.o_node, &x.o_head);
+    x.q = q.data_ptr();
+    x.out = out.data_ptr();
+    x.n_rows = size32(n, "rows");
+    x.n_nodes = size32(nodes, "nodes");
+    x.n_heads = size32(hq, "heads");
+    x.lens = int32s(a[4], "lens", dev, n);
+    x.parents = int32s(a[5], "parents", dev, n, nodes);
+    x.rows = int32s(a[6], "rows", dev, n, -1, true);
+    x.scale = a[7] == Py_None ? (float)(1.0 / std::sqrt((double)view.head_dim)) : (float)number(a[7]);
+    x.softcap = (float)number(a[8]);
+    x.window = integer(a[9], "window");
+    const int with_lse = PyObject_IsTrue(a[11]);
+    at::Tensor lse;
+    if (with_lse > 0) {
+      lse = Fresh::one({n, nodes, hq}, at::kFloat, dev);
+      x.lse = lse.data_ptr<float>();
+    }
+    int32_t* status = status_of(a[12], dev);
+    if (n > 0) {
+      check(mk_tree_attention_workspace(x.n_heads, view.n_kv_heads, view.head_dim, &x.workspace_bytes),
+            "mk_tree_attention_workspace");
+      const Workspace ws(x.workspace_bytes);
+      x.workspace = ws.p.get();
+      check(mk_tree_attention(&x, &view, status, stream_of(dev)), "mk_tree_attention");
+      written(a[10], a[12]);
+    }
+    PyObject* o = a[10] == Py_None ? wrap(out) : given(a[10]);
+    if (with_lse <= 0 || !o) return o;
+    return Py_BuildValue("(NN)", o, wrap(lse));
+  });
+}
+
+// (q, k_pages, v_pages, table, lens, scores, n_blocks, rows, first, last, scale, softcap, out, return_lse, return_pages,
+// status)
+PyObject* sparse_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  if (!count_is(n_args, 16)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    at::Device dev(at::kCPU);
+    const mk_page_view view = view_of(a[1], a[2], a[3], &dev);
+    const at::Tensor &q = tensor(a[0], "q"), &scores = tensor(a[5], "scores");
+    need(q.dim() == 3, "q must be [rows, heads, head_dim]");
+    mk_attend_args x{};
+    mk_sparse_args y{};
+    x.dtype = dtype_of(q, "q");
+    const int64_t n = q.size(0), hq = q.size(1);
+    heads_of(q, "q", n, hq, view.head_dim, q.scalar_type(), dev, &x.q_row, &x.q_head);
+    need(scores.dim() == 3 && scores.scalar_type() == at::kFloat && scores.device() == dev && scores.size(0) == n &&
+             scores.size(1) == view.n_kv_heads && scores.size(2) == view.table_width &&
+             (scores.stride(2) == 1 || scores.size(2) == 1),
+         "scores must be float32 [rows, kv heads, the table's width] on the pages' device, the last dim contiguous");
+    y.scores = scores.data_ptr<float>();
+    y.scores_row = stride_of(scores, 0);
+    y.scores_head = stride_of(scores, 1);
+    y.n_blocks = integer(a[6], "n_blocks");
+    y.first = integer(a[8], "first");
+    y.last = integer(a[9], "last");
+    const c10::cuda::CUDAGuard guard(dev);
+    const at::Tensor out = a[12] == Py_None ? Fresh::one(q.sizes(), q.scalar_type(), dev) : tensor(a[12], "out");
+    heads_of(out, "out", n, hq, view.head_dim, q.scalar_type(), dev, &x.o_row, &x.o_head);
+    x.q = q.data_ptr();
+    x.out = out.data_ptr();
+    x.n_rows = size32(n, "rows");
+    x.n_heads = size32(hq, "heads");
+    x.lens = int32s(a[4], "lens", dev, n);
+    x.rows = int32s(a[7], "rows", dev, n, -1, true);
+    x.scale = a[10] == Py_None ? (float)(1.0 / std::sqrt((double)view.head_dim)) : (float)number(a[10]);
+    x.softcap = (float)number(a[11]);
+    const int with_lse = PyObject_IsTrue(a[13]), with_pages = PyObject_IsTrue(a[14]);
+    at::Tensor lse, pages;
+    if (with_lse > 0) {
+      lse = Fresh::one({n, hq}, at::kFloat, dev);
+      x.lse = lse.data_ptr<float>();
+    }
+    int32_t* status = status_of(a[15], dev);
+    check(mk_sparse_attention_workspace(x.n_rows, x.n_heads, view.n_kv_heads, view.head_dim, y.n_blocks, &x.workspace_bytes),
+          "mk_sparse_attention_workspace");
+    if (with_pages > 0) {
+      pages = Fresh::one({n, view.n_kv_heads, y.n_blocks}, at::kInt, dev);
+      y.pages = pages.data_ptr<int32_t>();
+    }
+    if (n > 0) {
+      const Workspace ws(x.workspace_bytes);
+      x.workspace = ws.p.get();
+      check(mk_sparse_attention(&x, &y, &view, status, stream_of(dev)), "mk_sparse_attention");
+      written(a[12], a[15]);
+    }
+    PyObject* o = a[12] == Py_None ? wrap(out) : given(a[12]);
+    if (!o || (with_lse <= 0 && with_pages <= 0)) return o;
+    if (with_lse > 0 && with_pages > 0) return Py_BuildValue("(NNN)", o, wrap(lse), wrap(pages));
+    return Py_BuildValue("(NN)", o, wrap(with_lse > 0 ? lse : pages));
+  });
+}
+
+// the bounds of pages [n_pages, kv heads, .., dim] of one type
+void* bounds_of(PyObject* o, at::Device dev, int64_t n_pages, int64_t hkv, int64_t hd, at::ScalarType type) {
+  const at::Tensor& b = tensor(o, "bounds");
+  need(b.dim() == 4 && b.size(0) == n_pages && b.size(1) == hkv && b.size(2) == 2 && b.size(3) == hd && b.scalar_type() == type &&
+           b.device() == dev && b.is_contiguous(),
+       "bounds must be a contiguous [n_pages, kv heads, 2, head_dim] tensor of the pages' type and device");
+  return b.data_ptr();
+}
+
+// (k_pages, bounds, table, lens, rows, new, status)
+PyObject* update_bounds(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  if (!count_is(n_args, 7)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    at::Device dev(at::kCPU);
+    const mk_page_view view = view_of(a[0], a[0], a[2], &dev);
+    mk_bounds_args x{};
+    x.bounds = bounds_of(a[1], dev, view.n_pages, view.n_kv_heads, view.head_dim, THPVariable_Unpack(a[0]).scalar_type());
+    const at::Tensor& lens = tensor(a[3], "lens");
+    need(lens.dim() == 1, "lens must have one dim");
+    x.lens = int32s(a[3], "lens", dev, lens.size(0));
+    x.rows = int32s(a[4], "rows", dev, lens.size(0), -1, true);
+    x.n_rows = size32(lens.size(0), "rows");
+    x.n_new = integer(a[5], "new");
+    int32_t* status = status_of(a[6], dev);
+    const c10::cuda::CUDAGuard guard(dev);
+    check(mk_update_bounds(&x, &view, status, stream_of(dev)), "mk_update_bounds");
+    written(a[1], a[6]);
+    Py_RETURN_NONE;
+  });
+}
+
+// (q, bounds, table, lens, page_size, rows, status)
+PyObject* page_scores(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  if (!count_is(n_args, 7)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor &q = on_gpu(a[0], "q"), &b = tensor(a[1], "bounds");
+    const at::Device dev = q.device();
+    need(q.dim() == 3 && b.dim() == 4, "q must be [rows, heads, head_dim], bounds [n_pages, kv heads, 2, head_dim]");
+    need(b.scalar_type() == at::kHalf || b.scalar_type() == at::kBFloat16, "bounds must be float16 or bfloat16");
+    mk_scores_args x{};
+    mk_page_view view{};
+    x.bounds = bounds_of(a[1], dev, b.size(0), b.size(1), b.size(3), b.scalar_type());
+    view.k = view.v = const_cast<void*>(x.bounds);
+    view.n_pages = size32(b.size(0), "n_pages");
+    view.n_kv_heads = size32(b.size(1), "n_kv_heads");
+    view.head_dim = size32(b.size(3), "head_dim");
+    view.page_size = integer(a[4], "page_size");
+    view.page_stride = (long long)view.n_kv_heads * view.page_size * view.head_dim;
+    view.dtype = dtype_of(b, "bounds");
+    int32_t* p = nullptr;
+    table_of(a[2], dev, &p, &view.n_rows, &view.table_width, &view.table_stride);
+    view.table = p;
+    x.dtype = dtype_of(q, "q");
+    const int64_t n = q.size(0), hq = q.size(1);
+    heads_of(q, "q", n, hq, view.head_dim, q.scalar_type(), dev, &x.q_row, &x.q_head);
+    x.q = q.data_ptr();
+    x.n_rows = size32(n, "rows");
+    x.n_heads = size32(hq, "heads");
+    x.lens = int32s(a[3], "lens", dev, n);
+    x.rows = int32s(a[5], "rows", dev, n, -1, true);
+    int32_t* status = status_of(a[6], dev);
+    const c10::cuda::CUDAGuard guard(dev);
+    const at::Tensor scores = Fresh::one({n, view.n_kv_heads, view.table_width}, at::kFloat, dev);
+    x.scores = scores.data_ptr<float>();
+    if (n > 0) {
+      check(mk_page_scores(&x, &view, status, stream_of(dev)), "mk_page_scores");
+      written(a[6]);
+    }
+    return wrap(scores);
+  });
+}
+
 mk_page_pool pool_of(PyObject* ko, PyObject* vo, PyObject* table, PyObject* refs, at::Device* dev) {
   const at::Tensor &k = on_gpu(ko, "k"), &v = on_gpu(vo, "v");
   pages_of(k, v, 5);
@@ -329,8 +523,38 @@ mk_page_pool pool_of(PyObject* ko, PyObject* vo, PyObject* table, PyObject* refs
   p.page_stride = k.size(1) > 1 ? k.stride(1) * e : page;
   p.layer_stride = k.size(0) > 1 ? k.stride(0) * e : page;
   table_of(table, *dev, &p.table, &p.n_rows, &p.table_width, &p.table_stride);
-  p.refs = int32s(refs, "refs", *dev, k.size(1));
+  if (refs) p.refs = int32s(refs, "refs", *dev, k.size(1));
   return p;
+}
+
+// (k, v, table, lens, tokens, parents, choices, status)
+PyObject* accept_drafts(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  if (!count_is(n_args, 8)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    at::Device dev(at::kCPU);
+    const mk_page_pool pool = pool_of(a[0], a[1], a[2], nullptr, &dev);
+    const at::Tensor& tokens = tensor(a[4], "tokens");
+    need(tokens.dim() == 2, "tokens must be [rows of the table, nodes]");
+    const int64_t n = pool.n_rows, nodes = tokens.size(1);
+    mk_accept_args x{};
+    x.n_kv_heads = size32(THPVariable_Unpack(a[0]).size(2), "n_kv_heads");
+    x.n_nodes = size32(nodes, "nodes");
+    x.lens = int32s(a[3], "lens", dev, n);
+    x.tokens = int32s(a[4], "tokens", dev, n, nodes);
+    x.parents = int32s(a[5], "parents", dev, n, nodes);
+    x.choices = int32s(a[6], "choices", dev, n, nodes);
+    int32_t* status = status_of(a[7], dev);
+    const c10::cuda::CUDAGuard guard(dev);
+    Fresh fresh(4 * n * (2 * nodes + 1), dev);  // the three results share one allocation
+    const at::Tensor token = fresh.take({n, nodes}, at::kInt), path = fresh.take({n, nodes}, at::kInt),
+                     count = fresh.take({n}, at::kInt);
+    x.out_tokens = token.data_ptr<int32_t>();
+    x.out_path = path.data_ptr<int32_t>();
+    x.out_count = count.data_ptr<int32_t>();
+    check(mk_accept_drafts(&x, &pool, status, stream_of(dev)), "mk_accept_drafts");
+    written(a[0], a[1], a[3], a[7]);
+    return Py_BuildValue("(NNN)", wrap(token), wrap(path), wrap(count));
+  });
 }
 
 // (k, v, table, lens, refs, parents, reserve, status)
@@ -439,7 +663,9 @@ PyObject* set_error(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
 
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {FAST(rope_append),   FAST(paged_attention), FAST(update_pages), FAST(compact_pages),
-                           FAST(beam_select),   FAST(check_status),    FAST(set_error),    {nullptr, nullptr, 0, nullptr}};
+                           FAST(beam_select),   FAST(check_status),    FAST(set_error),    FAST(tree_attention),
+                           FAST(accept_drafts), FAST(update_bounds),   FAST(page_scores),  FAST(sparse_attention),
+                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_mk_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

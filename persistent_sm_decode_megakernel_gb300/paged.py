@@ -1,8 +1,9 @@
-"""Operators over a paged KV cache, and the selection of a beam search, on torch tensors.
+"""Operators over a paged KV cache, trees of drafted tokens and the selection of a beam search, on torch tensors.
 
 PyTorch is used for device memory and streams only; the work runs in libmk.so, through the
 C ABI of include/mk.h (mk_rope_append, mk_paged_attention, mk_update_pages, mk_compact_pages,
-mk_beam_select), whose comments define each operator.  Layout: a layer's keys and values are
+mk_beam_select, mk_tree_attention, mk_accept_drafts, mk_update_bounds, mk_page_scores,
+mk_sparse_attention), whose comments define each operator.  Layout: a layer's keys and values are
 [n_pages, n_kv_heads, page_size, head_dim]; position t of table row r lies in page
 table[r, t // page_size] at row t % page_size.
 
@@ -43,12 +44,13 @@ def rope_freqs(theta, n_rot, kind="none", factor=1.0, original=0.0, beta_fast=0.
 
 
 def rope_append(q, k, v, k_pages, v_pages, table, positions, rows=None, freqs=None, interleaved=False, mscale=1.0,
-                q_out=None, status=None):
+                q_out=None, status=None, slots=None):
     """Rotates q and k ([tokens, heads, head_dim], any strides with contiguous dims) at `positions`
     and writes k and v into the pages of table rows `rows` (default: token t is row t).  Returns the
-    rotated queries (`q_out`, which may be q; None without q).  freqs None: nothing is rotated."""
+    rotated queries (`q_out`, which may be q; None without q).  freqs None: nothing is rotated.  slots
+    (int32 [tokens]): where in its row a token's key and value go, if not to its position."""
     return _mk_torch.rope_append(q, k, v, k_pages, v_pages, table, positions, rows, freqs, interleaved, mscale, q_out,
-                                 status)
+                                 status, slots)
 
 
 def paged_attention(q, k_pages, v_pages, table, lens, rows=None, scale=None, softcap=0.0, window=0, len_add=0, out=None,
@@ -58,6 +60,46 @@ def paged_attention(q, k_pages, v_pages, table, lens, rows=None, scale=None, sof
     1 / sqrt(head_dim).  Returns the output, with return_lse also the float32 log-sum-exp."""
     return _mk_torch.paged_attention(q, k_pages, v_pages, table, lens, rows, scale, softcap, window, len_add, out,
                                      return_lse, status)
+
+
+def tree_attention(q, k_pages, v_pages, table, lens, parents, rows=None, scale=None, softcap=0.0, window=0, out=None,
+                   return_lse=False, status=None):
+    """Attention of trees of drafted tokens (mk_tree_attention): q [rows, nodes, heads, head_dim], parents int32
+    [rows, nodes] (a lower node, -1 for a root, else the node is absent).  Node i, whose key and value lie in
+    slot lens[r] + i of table row `rows` (default: r), sees slots 0..lens[r] - 1, its ancestors and itself.
+    Returns the output, with return_lse also the float32 log-sum-exp [rows, nodes, heads]."""
+    return _mk_torch.tree_attention(q, k_pages, v_pages, table, lens, parents, rows, scale, softcap, window, out,
+                                    return_lse, status)
+
+
+def accept_drafts(k, v, table, lens, tokens, parents, choices, status=None):
+    """Takes over the drafted tokens that the model chose (mk_accept_drafts): tokens, parents and choices (the model's
+    token after each node) int32 [rows of the table, nodes], node 0 being the token that stands.  In place: the
+    accepted nodes' keys and values of every layer (k and v as in update_pages) and lens.  Returns the choices of the
+    accepted nodes, the nodes (both [rows, nodes], -1 behind the last) and their number [rows]."""
+    return _mk_torch.accept_drafts(k, v, table, lens, tokens, parents, choices, status)
+
+
+def update_bounds(k_pages, bounds, table, lens, rows=None, new=1, status=None):
+    """The least and greatest elements of the keys of every page that holds one of the last `new` positions of table
+    rows `rows` (mk_update_bounds), into bounds [n_pages, n_kv_heads, 2, head_dim]."""
+    _mk_torch.update_bounds(k_pages, bounds, table, lens, rows, new, status)
+
+
+def page_scores(q, bounds, table, lens, page_size, rows=None, status=None):
+    """What the product of q ([rows, heads, head_dim]) with a key within a page's bounds can be at most, the greatest of
+    the heads of a kv head: float32 [rows, kv heads, table width], -inf where a row has no page."""
+    return _mk_torch.page_scores(q, bounds, table, lens, page_size, rows, status)
+
+
+def sparse_attention(q, k_pages, v_pages, table, lens, scores, n_blocks, rows=None, first=1, last=1, scale=None,
+                     softcap=0.0, out=None, return_lse=False, return_pages=False, status=None):
+    """paged_attention over n_blocks pages of each row and kv head (mk_sparse_attention): the first `first`, the last
+    `last` and of the others those with the greatest scores ([rows, kv heads, table width]), ties to the lower page.
+    Returns the output, with return_lse also the log-sum-exp, with return_pages also the pages' numbers in the row
+    (int32 [rows, kv heads, n_blocks], rising, -1 behind them)."""
+    return _mk_torch.sparse_attention(q, k_pages, v_pages, table, lens, scores, n_blocks, rows, first, last, scale, softcap,
+                                      out, return_lse, return_pages, status)
 
 
 def update_pages(k, v, table, lens, refs, parents=None, reserve=None, status=None):
