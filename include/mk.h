@@ -538,7 +538,7 @@ typedef struct {
 } mk_tree_args;
 mk_status mk_tree_attention(const mk_tree_args* args, const mk_page_view* cache, int32_t* status, void* stream);
 /* Bytes of workspace a call needs on the current device. */
-mk_status mk_tree_attention_workspace(int n_heads, int n_kv_heads, int head_dim, size_t* bytes);
+mk_status mk_tree_attention_workspace(int n_nodes, int n_heads, int n_kv_heads, int head_dim, size_t* bytes);
 
 /* Acceptance: node 0 (parent -1) is the token that was chosen before and stands; from there on, of
  * a node's children the lowest one is accepted whose token is the node's choice (what the model

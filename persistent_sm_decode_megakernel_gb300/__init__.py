@@ -194,7 +194,7 @@ mk_beam_select = _fn("mk_beam_select", [ctypes.POINTER(mk_select_args), c_void_p
 mk_beam_select_workspace = _fn("mk_beam_select_workspace", [c_int, c_int, c_int, P_size])
 mk_tree_attention = _fn("mk_tree_attention", [ctypes.POINTER(mk_tree_args), ctypes.POINTER(mk_page_view), c_void_p,
                                               c_void_p])
-mk_tree_attention_workspace = _fn("mk_tree_attention_workspace", [c_int, c_int, c_int, P_size])
+mk_tree_attention_workspace = _fn("mk_tree_attention_workspace", [c_int, c_int, c_int, c_int, P_size])
 mk_accept_drafts = _fn("mk_accept_drafts", [ctypes.POINTER(mk_accept_args), ctypes.POINTER(mk_page_pool), c_void_p, c_void_p])
 mk_update_bounds = _fn("mk_update_bounds", [ctypes.POINTER(mk_bounds_args), ctypes.POINTER(mk_page_view), c_void_p, c_void_p])
 mk_page_scores = _fn("mk_page_scores", [ctypes.POINTER(mk_scores_args), ctypes.POINTER(mk_page_view), c_void_p, c_void_p])

@@ -25,8 +25,6 @@ constexpr int kAttThreads = 32 * kAttWarps;
 constexpr int ctas_per_sm(int hd) { return hd == 128 ? 3 : 4; }
 constexpr int kJoinThreads = 256;
 constexpr int kMaxGroup = 16;           // query heads per kv head
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.69314718055994531f;
 
 struct AttendArgs {
   const void *q, *k, *v;
@@ -187,28 +185,6 @@ __device__ __forceinline__ int page_index(const AttendArgs& a, int t) {
   return a.tpp == 1 ? t : (int)__umulhi((unsigned)t, a.tpp_inverse);
 }
 
-template <typename T>
-__device__ __forceinline__ float2 unpack2(uint32_t w);
-template <>
-__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-template <>
-__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
-  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
-}
-// two floats as PARTS packed pairs whose sums are the floats: each part is the rest rounded
-template <typename T, int PARTS>
-__device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[PARTS]) {
-#pragma unroll
-  for (int i = 0; i < PARTS; ++i) {
-    p[i] = pack2<T>(x, y);
-    const float2 r = unpack2<T>(p[i]);
-    x -= r.x;
-    y -= r.y;
-  }
-}
-
 // fp16 probabilities are held times 2^14 so that small ones stay normal numbers; bf16 has
 // the range of fp32
 template <typename T>
@@ -216,28 +192,9 @@ constexpr float kProbShift = 0.f;
 template <>
 constexpr float kProbShift<__half> = 14.f;
 
-// A query that is split into fp16 parts is first brought near the top of their range, every head
-// by a power of two of its own (2^shift times its largest element lies in [2^14, 2^15)) that the
-// score's factor takes back: else the second part of an element below 1/8 was a subnormal
-// number, and one below 2^-25 or above 65504 lost altogether.
-template <typename C, typename Q>
-constexpr bool kScaled = std::is_same<C, __half>::value && !std::is_same<Q, __half>::value;
-__device__ __forceinline__ int shift_of(float largest) {
-  const int e = __float_as_int(largest) >> 23;  // (largest >= 0; zeros, infinities and NaN stay as they are)
-  return e == 0 || e == 255 ? 0 : min(127 + 14 - e, 126);
-}
-__device__ __forceinline__ float power_of(int e) { return __int_as_float((127 + e) << 23); }  // 2^e, |e| <= 126
-
 // four bytes from global to shared memory, without a register between
 __device__ __forceinline__ void cp_async4(int* dst, const int* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
-}
-
-// 2^x by the hardware's approximation (2 ulp; results below the normal range become 0)
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // Shared memory of the kernel: the query as A fragments [part][32-dim chunk][32 lanes][16 B]

@@ -7,6 +7,7 @@
 
 #include <exception>
 #include <string>
+#include <type_traits>
 
 #include "../../include/mk.h"
 
@@ -73,6 +74,9 @@ mk_status sm_count(int* n);
 std::string check_view(const mk_page_view* c);
 // whether the attention can count its work over that many rows of the table: "" when it can
 std::string check_line(const mk_page_view* c, long long n_rows, int window);
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994531f;
 
 #ifdef __CUDACC__
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -152,6 +156,47 @@ template <>
 __device__ __forceinline__ void store8<float>(float* p, const float (&x)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+}
+// two floats as PARTS packed pairs whose sums are the floats: each part is the rest rounded
+template <typename T, int PARTS>
+__device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[PARTS]) {
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i) {
+    p[i] = pack2<T>(x, y);
+    const float2 r = unpack2<T>(p[i]);
+    x -= r.x;
+    y -= r.y;
+  }
+}
+
+// A query that is split into fp16 parts is first brought near the top of their range, every head
+// by a power of two of its own (2^shift times its largest element lies in [2^14, 2^15)) that the
+// score's factor takes back: else the second part of an element below 1/8 was a subnormal
+// number, and one below 2^-25 or above 65504 lost altogether.
+template <typename C, typename Q>
+constexpr bool kScaled = std::is_same<C, __half>::value && !std::is_same<Q, __half>::value;
+__device__ __forceinline__ int shift_of(float largest) {
+  const int e = __float_as_int(largest) >> 23;  // (largest >= 0; zeros, infinities and NaN stay as they are)
+  return e == 0 || e == 255 ? 0 : min(127 + 14 - e, 126);
+}
+__device__ __forceinline__ float power_of(int e) { return __int_as_float((127 + e) << 23); }  // 2^e, |e| <= 126
+
+// 2^x by the hardware's approximation (2 ulp; results below the normal range become 0)
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 #endif
 

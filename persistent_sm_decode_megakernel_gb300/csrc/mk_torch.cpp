@@ -362,7 +362,7 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     }
     int32_t* status = status_of(a[12], dev);
     if (n > 0) {
-      check(mk_tree_attention_workspace(x.n_heads, view.n_kv_heads, view.head_dim, &x.workspace_bytes),
+      check(mk_tree_attention_workspace(x.n_nodes, x.n_heads, view.n_kv_heads, view.head_dim, &x.workspace_bytes),
             "mk_tree_attention_workspace");
       const Workspace ws(x.workspace_bytes);
       x.workspace = ws.p.get();
