@@ -29,21 +29,20 @@ namespace {
 constexpr int kMaxNodes = 128, kMaxGroup = 16;
 constexpr int kRows = 128;               // rows of a block: the tensor cores' M
 constexpr int kGroupThreads = 128;       // a softmax warpgroup: a thread per row
-constexpr int kTreeThreads = 3 * kGroupThreads;  // two of them, and one with a warp for the copies, one for the products
-// registers of a thread: 168 at the launch (384 threads), of which the third group gives its share to the others
-constexpr int kMoreRegs = 216, kFewRegs = 72;
-static_assert(2 * kMoreRegs + kFewRegs <= 3 * 168, "registers");
+constexpr int kTreeThreads = 2 * kGroupThreads + 64;  // two of them, a warp for the copies, one for the products
+constexpr int kTile = 64;                // slots that are copied, multiplied and weighted at a time
+constexpr int kMaxStages = 10;
 constexpr int kCopyWarp = 8, kMmaWarp = 9;
 constexpr int kSmemBytes = 227 * 1024;
-constexpr int kLead = 2;                 // tiles that a piece costs besides its own
+constexpr int kLead = 4;                 // tiles that a piece costs besides its own
 constexpr int kJoinThreads = 256;
-constexpr unsigned long long kWaitNs = 2000000000ull;  // limit of a wait inside the kernel
+constexpr long long kWaitCycles = 4000000000ll;  // limit of a wait inside the kernel: two seconds
 
 struct TreeArgs {
   const void *q, *k, *v;
   void* out;
   float* lse;
-  float* part;                           // [CTA][2][rows][HD + 4]: weighted values, maximum, sum
+  float* part;                           // [CTA][2][HD + 2][rows]: weighted values, maximum, sum
   int4* joins;                           // [CTA]: first and last share, row, kv head
   const int32_t *lens, *parents, *rows, *table;
   int32_t* status;
@@ -63,7 +62,6 @@ struct TreeArgs {
 struct Span {
   int lo, hi, t0, n, trow, len;
 };
-template <int TILE>
 __device__ __forceinline__ Span span_of(const TreeArgs& a, int r) {
   Span s;
   s.trow = a.rows ? a.rows[r] : r;
@@ -71,8 +69,8 @@ __device__ __forceinline__ Span span_of(const TreeArgs& a, int r) {
   const bool there = s.len >= 0 && (unsigned)s.trow < (unsigned)a.table_rows;
   s.hi = there ? (int)min((unsigned)s.len + (unsigned)a.n_nodes, (unsigned)a.cap) : 0;
   s.lo = there && a.window > 0 ? max(0, s.len - a.window + 1) : 0;  // the roots' first position
-  s.t0 = s.lo / TILE;
-  s.n = s.hi > s.lo ? (s.hi + TILE - 1) / TILE - s.t0 : 0;
+  s.t0 = s.lo / kTile;
+  s.n = s.hi > s.lo ? (s.hi + kTile - 1) / kTile - s.t0 : 0;
   return s;
 }
 
@@ -86,10 +84,9 @@ struct Piece {
   int last_share;                         // the share its segment ends in
   bool whole;
 };
-template <int TILE>
 __device__ __forceinline__ bool next_piece(const TreeArgs& a, Walk& w, Piece& p) {
   while (w.at < w.end) {
-    p.sp = span_of<TILE>(a, w.row);
+    p.sp = span_of(a, w.row);
     const int each = p.sp.n > 0 ? p.sp.n + w.lead : 0, units = each * a.hkv;
     if (w.at >= w.before + units) {
       w.before += units;
@@ -112,29 +109,39 @@ __device__ __forceinline__ bool next_piece(const TreeArgs& a, Walk& w, Piece& p)
 // C: the cache's type.  Q: the queries' and outputs' type.  NQ parts of C make up a query element, NP a
 // probability.  PAIR: the CTA takes two blocks of rows, a warpgroup each, against the same tiles; else one
 // block, the warpgroups taking turns at the tiles and joining at a piece's end.
-template <typename C, int HD, int NQ, int NP, bool PAIR>
+//
+// Tensor memory, 256 columns a warpgroup: 128 of scores, 128 of O.  The scores have two buffers of a tile, so that
+// the tensor cores work on one while the warpgroup is at the other (one buffer where P has three parts: it
+// takes the place of the scores it comes from).
+template <typename C, typename Q, int HD, int NQ, int NP, bool PAIR>
 struct Shape {
-  static constexpr int TILE = NP == 3 ? 64 : 128;  // slots: S and all parts of P lie in the same 128 columns
+  static constexpr int BUFFERS = NP == 3 ? 1 : 2;
+  static constexpr int AHEAD = PAIR ? BUFFERS : 2 * BUFFERS;  // tiles whose scores are asked for before the first values
   static constexpr int BLOCKS = PAIR ? 2 : 1;
   static constexpr int kQPart = kRows * HD * 2, kQBytes = BLOCKS * NQ * kQPart;
-  static constexpr int kStage = TILE * HD * 2;
+  static_assert(kQBytes >= BLOCKS * kRows * HD * (int)sizeof(Q), "the outputs go through the queries' place");
+  static constexpr int kStage = kTile * HD * 2;
   struct State {
-    uint64_t full[8], empty[8], s_full[2], p_full[2], o_done[2], q_full, finished;
+    uint64_t full[kMaxStages], empty[kMaxStages], s_full[2][2], p_full[2][2], o_done[2][2], q_full, finished;  // [warpgroup][buffer]
     uint32_t tmem;
     int abort;
     Walk walk;
     int sums[kTreeThreads / 32][2];
     int parents[kMaxNodes];
     unsigned char bad[16];                // of the last tiles: groups of 16 slots on a bad page
-    unsigned odd[2][4];                   // slots whose values are not all finite, of a warpgroup's tile (PAIR: of two tiles in turn)
-    float scale[BLOCKS][kRows];
+    unsigned odd[4][2];                   // slots whose values are not all finite, of the last tiles
+    float scale[BLOCKS * kRows];
     float ml[2][kRows][2];
   };
   static constexpr int kRoom = kSmemBytes - 1024 - (int)sizeof(State) - kQBytes;
-  static constexpr int kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
-  static constexpr int kBytes = 1024 + kQBytes + kStages * kStage + (int)sizeof(State);
-  static_assert(kStages >= 3, "shared memory");
-  static_assert(kBytes <= kSmemBytes && kBytes > kSmemBytes / 2, "one CTA per SM: it takes all of the tensor memory");
+  static constexpr int kStages = kRoom / kStage < kMaxStages ? kRoom / kStage : kMaxStages;
+  // (more than half of an SM's: there is one CTA on it, which takes all of the tensor memory)
+  static constexpr int kUsed = 1024 + kQBytes + kStages * kStage + (int)sizeof(State);
+  static constexpr int kBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
+  static_assert(kStages >= 4 && kBytes <= kSmemBytes, "shared memory");
+  // the place of tile i's keys and values among a piece's `count` tiles' copies: K0 .. K(AHEAD - 1), V0, K(AHEAD), V1, ..
+  static __device__ __forceinline__ unsigned k_load(int i) { return i < AHEAD ? i : 2 * i - AHEAD + 1; }
+  static __device__ __forceinline__ unsigned v_load(int i, int count) { return i + min(count, AHEAD + i); }
 };
 
 template <typename T>
@@ -149,10 +156,10 @@ constexpr float kSlack<__half> = 5.f;
 // Waits for a phase of a barrier: a wait that takes too long sets *abort, and from then on none waits.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* abort) {
   if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long begin = globaltimer_ns();
+  const long long begin = clock64();
   while (!mbar_wait_hint(bar, parity, 100000)) {
     if (*(volatile int*)abort) return false;
-    if (globaltimer_ns() - begin > kWaitNs) {
+    if (clock64() - begin > kWaitCycles) {
       *(volatile int*)abort = 1;
       return false;
     }
@@ -194,44 +201,63 @@ __device__ __forceinline__ unsigned ones(int x, int y) {
   return y > x ? to & ~from : 0u;
 }
 
+// two sums or products at a time
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+
 template <typename C, typename Q, int HD, int NQ, int NP, bool PAIR>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_constant__ TreeArgs a,
                                                                 const __grid_constant__ CUtensorMap k_map,
                                                                 const __grid_constant__ CUtensorMap v_map) {
-  using SH = Shape<C, HD, NQ, NP, PAIR>;
+  using SH = Shape<C, Q, HD, NQ, NP, PAIR>;
   using State = typename SH::State;
-  constexpr int TILE = SH::TILE, ST = SH::kStages, HALVES = HD / 64, WORDS = TILE / 32;
+  constexpr int ST = SH::kStages, HALVES = HD / 64, AHEAD = SH::AHEAD;
   constexpr uint32_t kType = std::is_same<C, __half>::value ? 0 : 1;
   extern __shared__ unsigned char tree_smem[];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(tree_smem) + 1023) & ~uintptr_t(1023));
   unsigned char *s_q = base, *s_kv = base + SH::kQBytes;
   State* st = reinterpret_cast<State*>(s_kv + ST * SH::kStage);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int share = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
-  if (tid == 0) {
-    for (int i = 0; i < ST; ++i) {
-      mbar_init(&st->full[i], 1);
-      mbar_init(&st->empty[i], 1);
+  if (warp == kCopyWarp) {
+    if (lane < ST) {
+      mbar_init(&st->full[lane], 1);
+      mbar_init(&st->empty[lane], 1);
+    } else if (lane < ST + 2) {
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&st->s_full[lane - ST][b], 1);
+        mbar_init(&st->p_full[lane - ST][b], kGroupThreads);
+        mbar_init(&st->o_done[lane - ST][b], 1);
+      }
+    } else if (lane == ST + 2) {
+      mbar_init(&st->q_full, 2 * kGroupThreads);
+      mbar_init(&st->finished, 1);
+      st->abort = 0;
     }
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(&st->s_full[w], 1);
-      mbar_init(&st->p_full[w], kGroupThreads);
-      mbar_init(&st->o_done[w], 1);
-    }
-    mbar_init(&st->q_full, 2 * kGroupThreads);
-    mbar_init(&st->finished, 1);
-    st->abort = 0;
     mbar_fence_init();
     fence_proxy_async();
   }
   pdl_wait();
   // ---- this CTA's share of the line
-  const int per = (a.n_rows + kTreeThreads - 1) / kTreeThreads;
-  const int r0 = min(a.n_rows, tid * per), r1 = min(a.n_rows, r0 + per);
   {
+    const int per = (a.n_rows + kTreeThreads - 1) / kTreeThreads;
+    const int r0 = min(a.n_rows, tid * per), r1 = min(a.n_rows, r0 + per);
     int tiles = 0, rows = 0;
     for (int r = r0; r < r1; ++r) {
-      const int n = span_of<TILE>(a, r).n;
+      const int n = span_of(a, r).n;
       tiles += n;
       rows += n > 0;
     }
@@ -265,26 +291,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     const int lead = all_tiles * a.hkv <= a.shares ? 0 : kLead;
     const int units = (all_tiles + all_rows * lead) * a.hkv, each = max(1, (units + a.shares - 1) / a.shares);
     const int at = min(units, each * share);
-    if (tid == 0) {
-      st->walk = Walk{at, min(units, at + each), each, lead, a.n_rows, 0};
-      a.joins[blockIdx.x] = make_int4(0, -1, 0, 0);
-    }
-    __syncthreads();
     int b = (ti + ri * lead) * a.hkv;
     const int mine = (tiles + rows * lead) * a.hkv;
-    if (at < units && at >= b && at < b + mine)
+    if (at < units && at >= b && at < b + mine) {
       for (int r = r0; r < r1; ++r) {
-        const int n = span_of<TILE>(a, r).n, u = n > 0 ? (n + lead) * a.hkv : 0;
-        if (at >= b && at < b + u) {
-          st->walk.row = r;
-          st->walk.before = b;
-        }
+        const int n = span_of(a, r).n, u = n > 0 ? (n + lead) * a.hkv : 0;
+        if (at >= b && at < b + u) st->walk = Walk{at, min(units, at + each), each, lead, r, b};
         b += u;
       }
+    }
+    if (tid == 0) {
+      if (at >= units) st->walk = Walk{at, at, each, lead, a.n_rows, 0};
+      a.joins[blockIdx.x] = make_int4(0, -1, 0, 0);
+    }
     // rows without slots: zeros; what is not there is reported
     if (all_rows < a.n_rows)
       for (int r = blockIdx.x; r < a.n_rows; r += gridDim.x) {
-        if (span_of<TILE>(a, r).n != 0) continue;
+        if (span_of(a, r).n != 0) continue;
         for (int x = tid; x < a.n_nodes * a.hq * HD; x += kTreeThreads) {
           const int h = x / HD;
           static_cast<Q*>(a.out)[r * a.o_row + h / a.hq * a.o_node + h % a.hq * a.o_head + x % HD] = Conv<Q>::down(0.f);
@@ -294,38 +317,39 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       }
     if (blockIdx.x == gridDim.x - 1)
       for (int r = tid; r < a.n_rows; r += kTreeThreads) {
-        const Span s = span_of<TILE>(a, r);
+        const Span s = span_of(a, r);
         if (s.len >= 0 && (unsigned)s.trow >= (unsigned)a.table_rows)
           report(a.status, MK_ERR_PAGES, PO_TREE, r, s.trow);
         else if (s.len >= 0 && (unsigned)s.len + (unsigned)a.n_nodes > (unsigned)a.cap)
           report(a.status, MK_ERR_PAGES, PO_TREE, r, s.len);
       }
   }
+  tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
   pdl_launch();
-  const uint32_t tmem = st->tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, st->tmem, 0);
   Walk w = st->walk;
+  w = Walk{__shfl_sync(0xffffffffu, w.at, 0), __shfl_sync(0xffffffffu, w.end, 0), __shfl_sync(0xffffffffu, w.share, 0),
+           __shfl_sync(0xffffffffu, w.lead, 0), __shfl_sync(0xffffffffu, w.row, 0), __shfl_sync(0xffffffffu, w.before, 0)};
   Piece p;
   unsigned loads = 0;                     // tiles of keys or values asked for, or used
 
-  if (warp >= kCopyWarp) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
   if (warp == kCopyWarp) {
     // ------------------------------------------------------------------------- copies
-    // in the order in which the products take them: K0 (K1) V0 K2 V1 .. or, PAIR, K0 V0 K1 V1 ..
     unsigned tiles = 0;
     bool run = true;
-    while (run && next_piece<TILE>(a, w, p)) {
-      const int boxes = TILE / a.box, mine = lane / boxes;  // a lane per copy: 64 dims of some positions
-      const int at0 = (p.sp.t0 + p.first) * TILE + lane % boxes * a.box;
-      const bool on = mine < HALVES;
-      auto page_of = [&](int i) {          // the page of this lane's part of tile i, n_pages where nothing is to be read
-        const int t = at0 + i * TILE;
+    while (run && next_piece(a, w, p)) {
+      const int boxes = kTile / a.box, half = lane / boxes;  // a lane per copy: 64 dims of some positions
+      const int at0 = (p.sp.t0 + p.first) * kTile + lane % boxes * a.box;
+      const bool on = half < HALVES;
+      // the page of this lane's part of tile i: n_pages where nothing is to be read, -1 where it is none
+      auto page_of = [&](int i) {
+        const int t = at0 + i * kTile;
         if (i >= p.count || !on || t >= p.sp.hi || t + a.box <= p.sp.lo) return a.n_pages;
         const int page = a.table[(long long)p.sp.trow * a.table_stride + t / a.page_size];
         if ((unsigned)page < (unsigned)a.n_pages) return page;
-        if (mine == 0) report(a.status, MK_ERR_PAGES, PO_TREE, p.r, page);
+        if (half == 0) report(a.status, MK_ERR_PAGES, PO_TREE, p.r, page);
         return -1;
       };
       auto copy = [&](const CUtensorMap* map, int i, int page) {
@@ -333,154 +357,170 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         if (!wait_phase(&st->empty[s], (loads / ST & 1) ^ 1, &st->abort)) return false;
         if (lane == 0) mbar_arrive_expect_tx(&st->full[s], SH::kStage);
         __syncwarp();
-        const uint32_t dst = smem_addr(s_kv + s * SH::kStage) + mine * TILE * 128 + lane % boxes * a.box * 128;
-        if (on)
-          tma_box_4d(dst, map, 64 * mine, page < 0 || page >= a.n_pages ? 0 : (at0 + i * TILE) % a.page_size, p.head,
+        const uint32_t dst = smem_addr(s_kv + s * SH::kStage) + half * kTile * 128 + lane % boxes * a.box * 128;
+        if (on)  // (a page outside the map: zeros)
+          tma_box_4d(dst, map, 64 * half, page < 0 || page >= a.n_pages ? 0 : (at0 + i * kTile) % a.page_size, p.head,
                      page < 0 ? a.n_pages : page, &st->full[s]);
         ++loads;
         return true;
       };
-      auto note = [&](int page) {          // the groups of 16 slots of a tile on a bad page
-        unsigned bad = on && mine == 0 && page < 0 ? ((1u << (a.box / 16)) - 1) << (lane % boxes * (a.box / 16)) : 0u;
-        bad = __reduce_or_sync(0xffffffffu, bad);
+      // the pages of the next tiles: the keys' is AHEAD tiles before the values'
+      int page[AHEAD + 2];
+#pragma unroll
+      for (int i = 0; i < AHEAD + 1; ++i) page[i] = page_of(i);
+      auto keys = [&](int i, int pg) {
+        unsigned bad = on && half == 0 && pg < 0 ? ((1u << (a.box / 16)) - 1) << (lane % boxes * (a.box / 16)) : 0u;
+        bad = __reduce_or_sync(0xffffffffu, bad);  // the groups of 16 slots on a bad page
         if (lane == 0) st->bad[tiles % 16] = (unsigned char)bad;
         __syncwarp();
         ++tiles;
+        run = run && copy(&k_map, i, pg);
       };
-      int now = page_of(0), ahead = page_of(1);
-      note(now);
-      run = copy(&k_map, 0, now);
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i)
+        if (i < p.count) keys(i, page[i]);
       for (int i = 0; i < p.count && run; ++i) {
-        const int later = page_of(i + 2);
-        if (PAIR) run = copy(&v_map, i, now);
-        if (run && i + 1 < p.count) {
-          note(ahead);
-          run = copy(&k_map, i + 1, ahead);
-        }
-        if (!PAIR && run) run = copy(&v_map, i, now);
-        now = ahead;
-        ahead = later;
+        page[AHEAD + 1] = page_of(i + AHEAD + 1);
+        run = copy(&v_map, i, page[0]);
+        if (i + AHEAD < p.count) keys(i + AHEAD, page[AHEAD]);
+#pragma unroll
+        for (int y = 0; y < AHEAD + 1; ++y) page[y] = page[y + 1];
       }
     }
     // every copy has landed before the CTA ends
     for (unsigned i = loads > ST ? loads - ST : 0; i < loads; ++i) wait_phase(&st->full[i % ST], i / ST & 1, &st->abort);
   } else if (warp == kMmaWarp) {
     // ----------------------------------------------------------------------- products
-    if (lane == 0) {
-      const uint32_t q0 = smem_addr(s_q), kv0 = smem_addr(s_kv);
-      unsigned p_count[2] = {0, 0}, pieces = 0;
-      while (next_piece<TILE>(a, w, p)) {
-        const int n = PAIR ? 2 * p.count : p.count;
-        auto k_load = [&](int i) { return loads + (PAIR ? 2 * i : i == 0 ? 0 : 2 * i - 1); };
-        auto v_load = [&](int i) { return loads + (PAIR ? 2 * i + 1 : i + 1 < p.count ? 2 * i + 2 : 2 * p.count - 1); };
-        wait_phase(&st->q_full, pieces & 1, &st->abort);
-        ++pieces;
+    // (the whole warp walks, so that what the instructions take stays in uniform registers; one lane issues)
+    const uint64_t q_desc = smem_desc(smem_addr(s_q), 16, 1024), k_desc = smem_desc(smem_addr(s_kv), 16, 1024);
+    const uint64_t v_desc = smem_desc(smem_addr(s_kv), kTile * 128, 1024);
+    unsigned p_phase = 0, pieces = 0;     // p_phase: a bit per warpgroup and buffer
+    int stage = -1;                       // tiles are used in the order of their copies
+    unsigned lap = 1;
+    auto next_stage = [&]() {
+      if (++stage == ST) stage = 0;
+      if (stage == 0) lap ^= 1;
+      wait_phase(&st->full[stage], lap, &st->abort);
+      return stage;
+    };
+    int k_at = 0, v_at = 0;
+    while (next_piece(a, w, p)) {
+      const int n = PAIR ? 2 * p.count : p.count;  // jobs: a tile of one warpgroup
+      wait_phase(&st->q_full, pieces & 1, &st->abort);
+      ++pieces;
+      // job x is warpgroup x & 1's, in its buffer x >> 1 & 1.  The tensor cores take what one thread issues in
+      // order, so that a buffer's next scores come after the product that read its P.
+      auto turn_of = [&](int x) { return SH::BUFFERS == 2 ? x >> 1 & 1 : 0; };
+      auto scores = [&](int x) {
+        const int g = x & 1;
+        if (!PAIR || g == 0) k_at = next_stage();
         tmem_fence_after();
-        auto scores = [&](int x) {
-          const int i = PAIR ? x >> 1 : x, g = x & 1;
-          const unsigned l = k_load(i), s = l % ST;
-          wait_phase(&st->full[s], l / ST & 1, &st->abort);
-          tmem_fence_after();
-          const uint32_t d = tmem + g * 256, kb = kv0 + s * SH::kStage, qb = q0 + (PAIR ? g : 0) * NQ * SH::kQPart;
+        if (elect_one()) {
+          const uint32_t d = tmem + g * 256 + turn_of(x) * kTile;
+          const uint64_t qd = q_desc + (PAIR ? g : 0) * (NQ * SH::kQPart / 16), kd = k_desc + k_at * (SH::kStage / 16);
 #pragma unroll
           for (int y = 0; y < NQ; ++y)
 #pragma unroll
-            for (int c = 0; c < HD / 16; ++c)
-              mma_ss(d, smem_desc(qb + y * SH::kQPart + (c >> 2) * kRows * 128 + (c & 3) * 32, 16, 1024),
-                     smem_desc(kb + (c >> 2) * TILE * 128 + (c & 3) * 32, 16, 1024), mma_desc(kType, false, kRows, TILE), y + c > 0);
-          mma_commit(&st->s_full[g]);
-          if (!PAIR || g == 1) mma_commit(&st->empty[s]);
-        };
-        auto values = [&](int x) {
-          const int i = PAIR ? x >> 1 : x, g = x & 1;
-          const unsigned l = v_load(i), s = l % ST;
-          wait_phase(&st->full[s], l / ST & 1, &st->abort);
-          wait_phase(&st->p_full[g], p_count[g]++ & 1, &st->abort);
-          tmem_fence_after();
-          const uint32_t d = tmem + g * 256 + 128, pa = tmem + g * 256, vb = kv0 + s * SH::kStage;
+            for (int c = 0; c < HD / 16; ++c)  // (the address counts in 16 bytes)
+              mma_ss(d, qd + (y * SH::kQPart + (c >> 2) * kRows * 128 + (c & 3) * 32) / 16,
+                     kd + ((c >> 2) * kTile * 128 + (c & 3) * 32) / 16, mma_desc(kType, false, kRows, kTile), y + c > 0);
+          mma_commit(&st->s_full[g][turn_of(x)]);
+          if (!PAIR || g == 1) mma_commit(&st->empty[k_at]);
+        }
+        __syncwarp();
+      };
+      auto values = [&](int x) {
+        const int g = x & 1, b = turn_of(x), bit = 2 * g + b;
+        if (!PAIR || g == 0) v_at = next_stage();
+        wait_phase(&st->p_full[g][b], p_phase >> bit & 1, &st->abort);
+        p_phase ^= 1u << bit;
+        tmem_fence_after();
+        if (elect_one()) {
+          const uint32_t d = tmem + g * 256 + 128, pa = tmem + g * 256 + b * kTile;
+          const uint64_t vd = v_desc + v_at * (SH::kStage / 16);
 #pragma unroll
           for (int y = 0; y < NP; ++y)
 #pragma unroll
-            for (int c = 0; c < TILE / 16; ++c)
-              mma_ts(d, pa + y * (TILE / 2) + c * 8, smem_desc(vb + c * 2048, TILE * 128, 1024), mma_desc(kType, true, kRows, HD), true);
-          mma_commit(&st->o_done[g]);
-          if (!PAIR || g == 1) mma_commit(&st->empty[s]);
-        };
-        scores(0);
-        if (n > 1) scores(1);
-        for (int x = 0; x < n; ++x) {
-          values(x);
-          if (x + 2 < n) scores(x + 2);
+            for (int c = 0; c < kTile / 16; ++c)
+              mma_ts(d, pa + y * (kTile / 2) + c * 8, vd + c * 2048 / 16, mma_desc(kType, true, kRows, HD), true);
+          mma_commit(&st->o_done[g][b]);
+          if (!PAIR || g == 1) mma_commit(&st->empty[v_at]);
         }
-        loads += 2 * p.count;
+        __syncwarp();
+      };
+      constexpr int FIRST = 2 * SH::BUFFERS;
+      for (int x = 0; x < min(n, FIRST); ++x) scores(x);
+      for (int x = 0; x < n; ++x) {
+        values(x);
+        if (x + FIRST < n) scores(x + FIRST);
       }
-      mma_commit(&st->finished);
-      wait_phase(&st->finished, 0, &st->abort);
     }
-  }
+    if (elect_one()) mma_commit(&st->finished);
+    __syncwarp();
+    wait_phase(&st->finished, 0, &st->abort);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMoreRegs));
     // ------------------------------------------------------------------------ softmax
     const int g = warp >> 2, row = tid & (kGroupThreads - 1);  // warpgroup, row of its block
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;         // this warp's lanes of the tensor memory
-    const uint32_t t_s = tmem + g * 256 + lanes, t_o = t_s + 128;
-    const int block = PAIR ? 2 * part + g : part;
-    const int node = block * a.nodes_per_block + row / a.group, h = row % a.group;
+    const uint32_t t_s0 = tmem + g * 256 + lanes, t_o = t_s0 + 128;
+    const int first_node = (PAIR ? 2 * part : part) * a.nodes_per_block;
+    const int node = first_node + (PAIR ? g * a.nodes_per_block : 0) + row / a.group, h = row % a.group;
     const bool valid = row < a.nodes_per_block * a.group && node < a.n_nodes;
     const bool warp_valid = __any_sync(0xffffffffu, valid);
-    unsigned tiles = 0, mine = 0;         // tiles of the CTA, and of this warpgroup
+    unsigned tiles = 0, s_phase = 0;      // tiles of the CTA; a bit per buffer: the next phase of its scores
     int row_of = -1;                      // whose tree `seen` is of
     unsigned seen[4] = {0, 0, 0, 0};
     int depth = 0;
     bool there = false;
-    while (next_piece<TILE>(a, w, p)) {
+    while (next_piece(a, w, p)) {
       groups_sync();                      // what the last piece left in shared and tensor memory was read
       if (p.r != row_of)
         for (int i = tid; i < a.n_nodes; i += 2 * kGroupThreads) st->parents[i] = a.parents[(long long)p.r * a.n_nodes + i];
-      // ---- the queries, K-major, 128-byte swizzled
-      if (PAIR || g == 0) {
-        const Q* src = static_cast<const Q*>(a.q) + p.r * a.q_row + node * a.q_node + (long long)(p.head * a.group + h) * a.q_head;
-        unsigned char* dst = s_q + (PAIR ? g : 0) * NQ * SH::kQPart + row * 128;
-        constexpr bool SCALED = kScaled<C, Q>;
-        float up = a.q_sign;
-        if (SCALED) {
-          float most = 0.f;
-          if (valid)
-#pragma unroll 4
-            for (int c = 0; c < HD / 8; ++c) {
-              Raw8<Q> raw;
+      // ---- the queries, K-major, 128-byte swizzled; neighbouring lanes take neighbouring chunks of a row
+      {
+        constexpr int CH = HD / 8, ITEMS = SH::BLOCKS * kRows * CH / (2 * kGroupThreads), U = ITEMS < 8 ? ITEMS : 8;
+        const int c = tid % CH;
+        const Q* src = static_cast<const Q*>(a.q) + p.r * a.q_row + (long long)p.head * a.group * a.q_head + 8 * c;
+#pragma unroll 1
+        for (int z0 = 0; z0 < ITEMS; z0 += U) {
+          Raw8<Q> raw[U];
+#pragma unroll
+          for (int z = 0; z < U; ++z) {
+            const int x = tid / CH + (z0 + z) * (2 * kGroupThreads / CH), y = x % kRows;  // row of all blocks, of its own
+            const int nd = y / a.group, at = first_node + x / kRows * a.nodes_per_block + nd;
+            raw[z] = {};
+            if (nd < a.nodes_per_block && at < a.n_nodes) {
+              const Q* from = src + at * a.q_node + (y - nd * a.group) * a.q_head;
               if (a.q_vec)
-                raw.load(src + 8 * c);
+                raw[z].load(from);
               else
-                raw.gather(src + 8 * c);
-              float v[8];
-              raw.up(v);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(v[e]));
+                raw[z].gather(from);
             }
-          const int shift = shift_of(most);
-          up *= power_of(shift);
-          st->scale[PAIR ? g : 0][row] = a.scale * power_of(-shift);
-        }
-#pragma unroll 4
-        for (int c = 0; c < HD / 8; ++c) {
-          Raw8<Q> raw = {};
-          if (valid) {
-            if (a.q_vec)
-              raw.load(src + 8 * c);
-            else
-              raw.gather(src + 8 * c);
           }
-          float v[8];
-          raw.up(v);
-          uint32_t x[4][NQ];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            split2<C, NQ>(valid ? v[2 * e] * up : 0.f, valid ? v[2 * e + 1] * up : 0.f, x[e]);
+          for (int z = 0; z < U; ++z) {
+            const int x = tid / CH + (z0 + z) * (2 * kGroupThreads / CH), y = x % kRows;
+            float v[8];
+            raw[z].up(v);
+            float up = a.q_sign;
+            if constexpr (kScaled<C, Q>) {  // the chunks of a row are in neighbouring lanes
+              float most = fabsf(v[0]);
 #pragma unroll
-          for (int y = 0; y < NQ; ++y)
-            *reinterpret_cast<uint4*>(dst + y * SH::kQPart + (c >> 3) * kRows * 128 + (((c & 7) ^ (row & 7)) << 4)) =
-                make_uint4(x[0][y], x[1][y], x[2][y], x[3][y]);
+              for (int e = 1; e < 8; ++e) most = fmaxf(most, fabsf(v[e]));
+#pragma unroll
+              for (int o = 1; o < CH; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+              const int shift = shift_of(most);
+              up *= power_of(shift);
+              if (c == 0) st->scale[x] = a.scale * power_of(-shift);
+            }
+            uint32_t parts[4][NQ];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split2<C, NQ>(v[2 * e] * up, v[2 * e + 1] * up, parts[e]);
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+              *reinterpret_cast<uint4*>(s_q + ((x / kRows) * NQ + n) * SH::kQPart + (c >> 3) * kRows * 128 + y * 128 +
+                                        (((c & 7) ^ (y & 7)) << 4)) = make_uint4(parts[0][n], parts[1][n], parts[2][n], parts[3][n]);
+          }
         }
       }
       {
@@ -495,7 +535,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       tmem_fence_before();
       mbar_arrive(&st->q_full);
       groups_sync();                      // parents and scales are there
-      const float scale = kScaled<C, Q> ? st->scale[PAIR ? g : 0][row] : a.scale;
+      const float scale = kScaled<C, Q> ? st->scale[(PAIR ? g * kRows : 0) + row] : a.scale;
       if (p.r != row_of) {                // the node's ancestors that its window holds
         row_of = p.r;
 #pragma unroll
@@ -524,48 +564,58 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       const int lo = there ? from(depth) : p.sp.len;
       const int plain_lo = from(a.n_nodes - 1);  // tiles in [plain_lo, len) are seen by all nodes whole
       float m = -INFINITY, l = 0.f;
-      for (int i = PAIR ? 0 : g; i < p.count; i += PAIR ? 1 : 2) {
-        const int t0 = (p.sp.t0 + p.first + i) * TILE;
-        wait_phase(&st->s_full[g], mine & 1, &st->abort);
+      int turn = 0;                       // tiles of the piece that this warpgroup has taken
+      for (int i = PAIR ? 0 : g; i < p.count; i += PAIR ? 1 : 2, ++turn) {
+        const int t0 = (p.sp.t0 + p.first + i) * kTile;
+        const int buf = SH::BUFFERS == 2 ? turn & 1 : 0;
+        const uint32_t t_s = t_s0 + buf * kTile;
+        wait_phase(&st->s_full[g][buf], s_phase >> buf & 1, &st->abort);
+        s_phase ^= 1u << buf;
         tmem_fence_after();
-        const unsigned bad_tile = *(volatile unsigned char*)&st->bad[(tiles + i) % 16];
-        const bool partial = t0 < plain_lo || t0 + TILE > min(p.sp.len, p.sp.hi) || bad_tile != 0;
-        unsigned vis[WORDS];
+        const unsigned bad = *(volatile unsigned char*)&st->bad[(tiles + i) % 16];
+        const bool partial = t0 < plain_lo || t0 + kTile > min(p.sp.len, p.sp.hi) || bad != 0;
+        unsigned vis[2], odd[2] = {0, 0};
         if (partial) {
 #pragma unroll
-          for (int x = 0; x < WORDS; ++x) {
+          for (int x = 0; x < 2; ++x) {
             const int b = t0 + 32 * x;
             vis[x] = ones(lo - b, p.sp.len - b) | bits_at(seen, b - p.sp.len);
             vis[x] &= ones(0, p.sp.hi - b);
-            if (bad_tile >> (2 * x) & 1) vis[x] &= 0xffff0000u;
-            if (bad_tile >> (2 * x) & 2) vis[x] &= 0x0000ffffu;
+            if (bad >> (2 * x) & 1) vis[x] &= 0xffff0000u;
+            if (bad >> (2 * x) & 2) vis[x] &= 0x0000ffffu;
           }
           // values that are not finite must not meet the zero of one who does not see them: they are taken
-          // out of the tile and added for those who do
-          if (row < 4) st->odd[PAIR ? i & 1 : g][row] = 0;
+          // out of the tile and added for those who do.  (A set is used again when all who read it are through
+          // its tile: the scores they wait for come after the products of the tiles before.)
+          unsigned* found = st->odd[PAIR ? i & 3 : 2 * g + (turn & 1)];
+          if (row < 2) found[row] = 0;
           tile_sync<PAIR>(g);
-          const unsigned v_at = loads + (PAIR ? 2 * i + 1 : i + 1 < p.count ? 2 * i + 2 : 2 * p.count - 1);
+          const unsigned v_at = loads + SH::v_load(i, p.count);
           wait_phase(&st->full[v_at % ST], v_at / ST & 1, &st->abort);
           uint4* v = reinterpret_cast<uint4*>(s_kv + v_at % ST * SH::kStage);
           constexpr int step = PAIR ? 2 * kGroupThreads : kGroupThreads;
-          for (int x = PAIR ? tid : row; x < SH::kStage / 16; x += step) {
-            uint4 y = v[x];
+#pragma unroll
+          for (int z = 0; z < SH::kStage / 16 / step; ++z) {
+            const int x = (PAIR ? tid : row) + z * step;
+            const uint4 y = v[x];
             const uint32_t o0 = odd_mask<C>(y.x), o1 = odd_mask<C>(y.y), o2 = odd_mask<C>(y.z), o3 = odd_mask<C>(y.w);
             if (o0 | o1 | o2 | o3) {
               v[x] = make_uint4(y.x & ~o0, y.y & ~o1, y.z & ~o2, y.w & ~o3);
-              const int slot = x / 8 % TILE;
-              atomicOr(&st->odd[PAIR ? i & 1 : g][slot >> 5], 1u << (slot & 31));
+              const int slot = x / 8 % kTile;
+              atomicOr(&found[slot >> 5], 1u << (slot & 31));
             }
           }
           fence_proxy_async();
           tile_sync<PAIR>(g);
+          odd[0] = found[0];
+          odd[1] = found[1];
         }
         if (warp_valid) {
           float factor = scale;
           if (a.softcap > 0.f) {
             factor = 1.f;
 #pragma unroll 1
-            for (int x = 0; x < TILE / 16; ++x) {
+            for (int x = 0; x < kTile / 16; ++x) {
               uint32_t y[16];
               tmem_ld(t_s + 16 * x, y);
               tmem_wait_ld();
@@ -575,24 +625,31 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             }
             tmem_wait_st();
           }
-          uint32_t s[WORDS][32];
-#pragma unroll
-          for (int x = 0; x < WORDS; ++x) tmem_ld(t_s + 32 * x, s[x]);
+          uint32_t s[2][32];
+          tmem_ld(t_s, s[0]);
+          tmem_ld(t_s + 32, s[1]);
           tmem_wait_ld();
           if (partial) {
 #pragma unroll
-            for (int x = 0; x < WORDS; ++x)
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
               for (int y = 0; y < 32; ++y) s[x][y] = vis[x] >> y & 1 ? s[x][y] : 0xff800000u;
           }
           float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int x = 0; x < TILE; ++x) tops[x & 3] = fmaxf(tops[x & 3], __uint_as_float(s[x >> 5][x & 31]));
+          for (int x = 0; x < kTile; x += 2)
+            tops[x >> 1 & 3] = fmaxf(fmaxf(tops[x >> 1 & 3], __uint_as_float(s[x >> 5][x & 31])), __uint_as_float(s[x >> 5][(x & 31) + 1]));
           const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * factor;
           // what was summed under a smaller maximum is brought to the new one, where it is much smaller
           const bool grown = top > m + kSlack<C>;
           const float to = grown ? top : m;
-          if (__any_sync(0xffffffffu, grown && m > -INFINITY)) {
+          const bool rescale = __any_sync(0xffffffffu, grown && m > -INFINITY);
+          if (rescale || (odd[0] | odd[1])) {  // the sums so far are touched: the last product is done
+            // (of this buffer's it is: these scores came after it)
+            if (SH::BUFFERS == 2) wait_phase(&st->o_done[g][buf ^ 1], (s_phase >> (buf ^ 1) & 1) ^ 1, &st->abort);
+            tmem_fence_after();
+          }
+          if (rescale) {
             const float f = grown ? ex2(m - to) : 1.f;
             l *= f;
 #pragma unroll 1
@@ -607,69 +664,63 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
           }
           m = to;
           const float less = kShift<C> - (m == -INFINITY ? 0.f : m);
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const float2 factor2 = make_float2(factor, factor), less2 = make_float2(less, less);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          uint32_t parts[NP][32];
 #pragma unroll
-          for (int b = 0; b < WORDS; ++b) {
-            uint32_t parts[NP][16];
+          for (int x = 0; x < 32; ++x) {
+            float2 y = make_float2(__uint_as_float(s[x >> 4][2 * (x & 15)]), __uint_as_float(s[x >> 4][2 * (x & 15) + 1]));
+            y = fma2(y, factor2, less2);
+            y.x = ex2(y.x);
+            y.y = ex2(y.y);
+            sum[x & 1] = add2(sum[x & 1], y);
+            uint32_t z[NP];
+            split2<C, NP>(y.x, y.y, z);
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const float p0 = ex2(fmaf(__uint_as_float(s[b][2 * x]), factor, less));
-              const float p1 = ex2(fmaf(__uint_as_float(s[b][2 * x + 1]), factor, less));
-              sum[2 * (x & 1)] += p0;
-              sum[2 * (x & 1) + 1] += p1;
-              uint32_t y[NP];
-              split2<C, NP>(p0, p1, y);
-#pragma unroll
-              for (int z = 0; z < NP; ++z) parts[z][x] = y[z];
-            }
-#pragma unroll
-            for (int z = 0; z < NP; ++z) tmem_st(t_s + z * (TILE / 2) + 16 * b, parts[z]);
+            for (int e = 0; e < NP; ++e) parts[e][x] = z[e];
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tmem_wait_st();
-          if (partial) {
-#pragma unroll 1
-            for (int x = 0; x < TILE; ++x) {
-              if (!(st->odd[PAIR ? i & 1 : g][x >> 5] >> (x & 31) & 1)) continue;
-              unsigned word = 0;
 #pragma unroll
-              for (int y = 0; y < WORDS; ++y) word = (x >> 5) == y ? vis[y] : word;
-              const bool sees = word >> (x & 31) & 1;
+          for (int e = 0; e < NP; ++e) tmem_st(t_s + e * (kTile / 2), parts[e]);
+          const float2 both = add2(sum[0], sum[1]);
+          l += both.x + both.y;
+          tmem_wait_st();
+#pragma unroll 1
+          for (int x2 = 0; x2 < 2; ++x2) {
+            for (unsigned rest = x2 ? odd[1] : odd[0]; rest; rest &= rest - 1) {
+              const int x = 32 * x2 + __ffs(rest) - 1, t = t0 + x;
+              const bool sees = (x2 ? vis[1] : vis[0]) >> (x & 31) & 1;
               if (!__any_sync(0xffffffffu, sees)) continue;
-              const int t = t0 + x;
-              int page = -1;
-              if (t < p.sp.hi) page = a.table[(long long)p.sp.trow * a.table_stride + t / a.page_size];
-              if ((unsigned)page >= (unsigned)a.n_pages) continue;
-              const C* src = static_cast<const C*>(a.v) + (long long)page * a.page_stride +
+              // (who sees it has its page)
+              const C* src = static_cast<const C*>(a.v) +
+                             (long long)a.table[(long long)p.sp.trow * a.table_stride + t / a.page_size] * a.page_stride +
                              ((long long)p.head * a.page_size + t % a.page_size) * HD;
               float pr = 0.f;
 #pragma unroll
               for (int z = 0; z < NP; ++z) {
-                const uint32_t y = tmem_ld1(t_s + z * (TILE / 2) + (x >> 1));
+                const uint32_t y = tmem_ld1(t_s + z * (kTile / 2) + (x >> 1));
                 tmem_wait_ld();
-                const float2 both = unpack2<C>(y);
-                pr += x & 1 ? both.y : both.x;
+                const float2 pair = unpack2<C>(y);
+                pr += x & 1 ? pair.y : pair.x;
               }
-              for (int c = 0; c < HD / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld(t_o + 32 * c, o);
+              for (int c = 0; c < HD / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld(t_o + 16 * c, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int y = 0; y < 32; ++y) {
-                  const float v = Conv<C>::up(src[32 * c + y]);
+                for (int y = 0; y < 16; ++y) {
+                  const float v = Conv<C>::up(src[16 * c + y]);
                   if (sees && !(fabsf(v) < INFINITY)) o[y] = __float_as_uint(fmaf(pr, v, __uint_as_float(o[y])));
                 }
-                tmem_st(t_o + 32 * c, o);
+                tmem_st(t_o + 16 * c, o);
                 tmem_wait_st();
               }
             }
           }
         }
         tmem_fence_before();
-        mbar_arrive(&st->p_full[g]);
-        ++mine;
+        mbar_arrive(&st->p_full[g][buf]);
       }
-      if (mine) wait_phase(&st->o_done[g], (mine - 1) & 1, &st->abort);
+      for (int b = 0; b < SH::BUFFERS; ++b) wait_phase(&st->o_done[g][b], (s_phase >> b & 1) ^ 1, &st->abort);
       tiles += p.count;
       loads += 2 * p.count;
       // ---- the piece's result
@@ -684,6 +735,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         groups_sync();
       }
       tmem_fence_after();
+      if (tid == 0 && !p.whole && p.first == 0) a.joins[blockIdx.x] = make_int4(share, p.last_share, p.r, p.head);
       if (!warp_valid) continue;
       float M = m, L = l, f0 = 1.f, f1 = 0.f;
       if (!PAIR) {
@@ -694,55 +746,80 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         f1 = ex2(m1 - Ms);
         L = fmaf(f0, st->ml[0][row][1], f1 * st->ml[1][row][1]);
       }
-      const float Ms = M == -INFINITY ? 0.f : M;
-      const long long at = ((long long)p.r * a.n_nodes + node) * a.hq + p.head * a.group + h;
-      Q* dst = static_cast<Q*>(a.out) + p.r * a.o_row + node * a.o_node + (long long)(p.head * a.group + h) * a.o_head;
       const int slot = p.first == 0;      // 0: continues a segment, 1: begins one
-      float* keep = a.part + (((size_t)blockIdx.x * 2 + slot) * a.part_rows + (PAIR ? g : 0) * kRows + row) * (HD + 4);
+      float* keep = a.part + (size_t)(blockIdx.x * 2 + slot) * a.part_rows * (HD + 2) + (PAIR ? g * kRows : 0) + row;
       const float inv = L == 0.f ? 0.f : 1.f / L;
-      constexpr int CHUNKS = PAIR ? HD / 32 : HD / 64;  // of this thread: all of the dims, or the warpgroup's half
+      // this thread's dims: all of them, or the warpgroup's half.  What is whole goes through the queries' place
+      // in shared memory (read by now), a warp's rows in rows of its own, so that whole runs are written.
+      constexpr int DIMS = PAIR ? HD : HD / 2, kRun = DIMS * (int)sizeof(Q), RCH = kRun / 16, kTwist = RCH < 8 ? RCH - 1 : 7;
+      const int d0 = PAIR ? 0 : g * DIMS;
+      unsigned char* run = s_q + ((PAIR ? g : 0) * kRows + (warp & 3) * 32) * HD * sizeof(Q) + (PAIR ? 0 : g) * 32 * kRun;
 #pragma unroll
-      for (int c = 0; c < CHUNKS; ++c) {
-        const int d = 32 * ((PAIR ? 0 : g * CHUNKS) + c);
+      for (int c = 0; c < DIMS / 32; ++c) {
         uint32_t o[32];
         if (PAIR) {
-          tmem_ld(t_o + d, o);
+          tmem_ld(t_o + 32 * c, o);
           tmem_wait_ld();
         } else {
           uint32_t o1[32];
-          tmem_ld(tmem + lanes + 128 + d, o);
-          tmem_ld(tmem + lanes + 256 + 128 + d, o1);
+          tmem_ld(tmem + lanes + 128 + d0 + 32 * c, o);
+          tmem_ld(tmem + lanes + 256 + 128 + d0 + 32 * c, o1);
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             o[e] = __float_as_uint(fmaf(f0, __uint_as_float(o[e]), f1 * __uint_as_float(o1[e])));
         }
-        if (!valid) continue;
         if (p.whole) {
-          float x[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = L == 0.f ? 0.f : __uint_as_float(o[e]) * inv;
+          for (int e = 0; e < 4; ++e) {
+            float x[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) x[y] = L == 0.f ? 0.f : __uint_as_float(o[8 * e + y]) * inv;
+            union {
+              Q q[8];
+              uint4 v[sizeof(Q) / 2];
+            } to;
+#pragma unroll
+            for (int y = 0; y < 8; ++y) to.q[y] = Conv<Q>::down(x[y]);
+#pragma unroll
+            for (int y = 0; y < (int)sizeof(Q) / 2; ++y) {
+              const int ch = (4 * c + e) * ((int)sizeof(Q) / 2) + y;
+              *reinterpret_cast<uint4*>(run + lane * kRun + ((ch ^ (lane & kTwist)) << 4)) = to.v[y];
+            }
+          }
+        } else if (valid) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) keep[(size_t)(d0 + 32 * c + e) * a.part_rows] = __uint_as_float(o[e]);
+        }
+      }
+      if (p.whole) {
+        __syncwarp();
+        Q* out = static_cast<Q*>(a.out) + p.r * a.o_row + (long long)p.head * a.group * a.o_head + d0;
+#pragma unroll 4
+        for (int x = lane; x < 32 * RCH; x += 32) {
+          const int y = (warp & 3) * 32 + x / RCH, ch = x % RCH, nd = y / a.group;
+          const int at = first_node + (PAIR ? g * a.nodes_per_block : 0) + nd;
+          if (nd >= a.nodes_per_block || at >= a.n_nodes) continue;
+          const uint4 v = *reinterpret_cast<const uint4*>(run + x / RCH * kRun + ((ch ^ (x / RCH & kTwist)) << 4));
+          Q* dst = out + at * a.o_node + (y - nd * a.group) * a.o_head + ch * (16 / sizeof(Q));
           if (a.o_vec) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) store8<Q>(dst + d + 8 * e, *reinterpret_cast<const float(*)[8]>(x + 8 * e));
+            *reinterpret_cast<uint4*>(dst) = v;
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) dst[d + e] = Conv<Q>::down(x[e]);
+            for (int e = 0; e < 16 / (int)sizeof(Q); ++e) dst[e] = reinterpret_cast<const Q*>(&v)[e];
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) reinterpret_cast<uint4*>(keep + d)[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       }
       if (valid && (PAIR || g == 0)) {
         if (p.whole) {
-          if (a.lse) a.lse[at] = (Ms - kShift<C> + log2f(L)) * kLn2;
+          if (a.lse)
+            a.lse[((long long)p.r * a.n_nodes + node) * a.hq + p.head * a.group + h] =
+                ((M == -INFINITY ? 0.f : M) - kShift<C> + log2f(L)) * kLn2;
         } else {
-          keep[HD] = M;
-          keep[HD + 1] = L;
+          keep[(size_t)HD * a.part_rows] = M;
+          keep[(size_t)(HD + 1) * a.part_rows] = L;
         }
       }
-      if (tid == 0 && !p.whole && p.first == 0) a.joins[blockIdx.x] = make_int4(share, p.last_share, p.r, p.head);
     }
   }
   __syncwarp();
@@ -753,19 +830,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   if (warp == kMmaWarp) tmem_free_all(tmem);
 }
 
-// Joins the pieces of the segments that span CTAs: a warp per row of a block, a lane HD / 32 dims.
+// Joins the pieces of the segments that span CTAs: a CTA per 32 rows and 32 dims of a block, a lane per row, a
+// warp 4 dims; the pieces in order, eight of them in flight.
 template <typename Q, int HD>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs a, float shift) {
-  constexpr int E = HD / 32, ROW = HD + 4, U = 8;
+  constexpr int W = kJoinThreads / 32, E = 32 / W, U = 8;
+  __shared__ float s_o[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_launch();
   const int4 job = a.joins[blockIdx.x];
-  const int part = blockIdx.x % a.parts, row = blockIdx.y * (kJoinThreads / 32) + warp;
-  if (job.y < 0 || row >= a.part_rows) return;
-  const int per = a.part_rows > kRows ? 2 : 1, block = part * per + row / kRows, x = row % kRows;
-  const int node = block * a.nodes_per_block + x / a.group, head = job.w * a.group + x % a.group, r = job.z;
-  if (x >= a.nodes_per_block * a.group || node >= a.n_nodes) return;
+  if (job.y < 0) return;
+  const int part = blockIdx.x % a.parts, row0 = blockIdx.y * 32, d0 = blockIdx.z * 32;
+  const int per = a.part_rows > kRows ? 2 : 1, r = job.z;
+  const int row = min(row0 + lane, a.part_rows - 1);  // (past the last: loaded and not used)
   float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
@@ -773,12 +851,12 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     float pm[U], pl[U], po[U][E];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int y = min(b + u, job.y);     // past the last: loaded and not used
-      const float* src = a.part + (((size_t)(y * a.parts + part) * 2 + (y == job.x)) * a.part_rows + row) * ROW;
+      const int y = min(b + u, job.y);
+      const float* src = a.part + (size_t)((y * a.parts + part) * 2 + (y == job.x)) * a.part_rows * (HD + 2) + row;
+      pm[u] = src[(size_t)HD * a.part_rows];
+      pl[u] = src[(size_t)(HD + 1) * a.part_rows];
 #pragma unroll
-      for (int e = 0; e < E; ++e) po[u][e] = src[32 * e + lane];
-      pm[u] = src[HD];
-      pl[u] = src[HD + 1];
+      for (int e = 0; e < E; ++e) po[u][e] = src[(size_t)(d0 + warp * E + e) * a.part_rows];
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -791,11 +869,25 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
       m = mn;
     }
   }
-  Q* out = static_cast<Q*>(a.out) + r * a.o_row + node * a.o_node + head * a.o_head;
 #pragma unroll
-  for (int e = 0; e < E; ++e) out[32 * e + lane] = Conv<Q>::down(l == 0.f ? 0.f : o[e] / l);
-  if (lane == 0 && a.lse)
+  for (int e = 0; e < E; ++e) s_o[lane][warp * E + e] = l == 0.f ? 0.f : o[e] / l;
+  // where row x of the blocks goes: its node and head, or no node
+  auto place = [&](int x, int* node, int* head) {
+    const int y = x % kRows, nd = y / a.group;
+    *node = (part * per + x / kRows) * a.nodes_per_block + nd;
+    *head = job.w * a.group + y - nd * a.group;
+    return x < a.part_rows && nd < a.nodes_per_block && *node < a.n_nodes;
+  };
+  int node, head;
+  if (warp == 0 && d0 == 0 && a.lse && place(row0 + lane, &node, &head))
     a.lse[((long long)r * a.n_nodes + node) * a.hq + head] = ((m == -INFINITY ? 0.f : m) - shift + log2f(l)) * kLn2;
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int x = warp * E + e;
+    if (place(row0 + x, &node, &head))
+      static_cast<Q*>(a.out)[r * a.o_row + node * a.o_node + head * a.o_head + d0 + lane] = Conv<Q>::down(s_o[x][lane]);
+  }
 }
 
 // --------------------------------------------------------------------------------- host
@@ -842,9 +934,9 @@ Deal deal(int n_nodes, int group, bool same_type) {
 
 template <typename C, typename Q, int HD, int NQ, int NP, bool PAIR>
 mk_status launch_tree(TreeArgs& a, const mk_page_view& view, void* stream) {
-  using SH = Shape<C, HD, NQ, NP, PAIR>;
+  using SH = Shape<C, Q, HD, NQ, NP, PAIR>;
   a.box = 16;
-  while (a.box < SH::TILE && a.page_size % (2 * a.box) == 0) a.box *= 2;
+  while (a.box < kTile && a.page_size % (2 * a.box) == 0) a.box *= 2;
   CUtensorMap k_map, v_map;
   mk_status s = page_map(&k_map, view, view.k, a.box);
   if (!s) s = page_map(&v_map, view, view.v, a.box);
@@ -854,9 +946,8 @@ mk_status launch_tree(TreeArgs& a, const mk_page_view& view, void* stream) {
   if (e != cudaSuccess) return paged_fail(MK_ERR_CUDA, std::string("mk_tree_attention: ") + cudaGetErrorString(e));
   s = launch_dependent(kernel, dim3(a.shares * a.parts), dim3(kTreeThreads), SH::kBytes, stream, "mk_tree_attention", a, k_map, v_map);
   if (s) return s;
-  const int per = kJoinThreads / 32;
-  return launch_dependent(tree_join_kernel<Q, HD>, dim3(a.shares * a.parts, (a.part_rows + per - 1) / per), dim3(kJoinThreads), 0,
-                          stream, "mk_tree_attention (join)", a, kShift<C>);
+  return launch_dependent(tree_join_kernel<Q, HD>, dim3(a.shares * a.parts, (a.part_rows + 31) / 32, HD / 32), dim3(kJoinThreads),
+                          0, stream, "mk_tree_attention (join)", a, kShift<C>);
 }
 template <typename C, typename Q, int NQ, int NP>
 mk_status launch_tree(TreeArgs& a, const mk_page_view& view, bool pair, void* stream) {
@@ -885,7 +976,7 @@ extern "C" mk_status mk_tree_attention_workspace(int n_nodes, int n_heads, int n
     if (s) return s;
     size_t rows = 0;
     for (bool same : {false, true}) rows = std::max<size_t>(rows, deal(n_nodes, n_heads / n_kv_heads, same).part_rows);
-    *bytes = (size_t)n_sm * (sizeof(int4) + 2 * rows * (head_dim + 4) * sizeof(float));
+    *bytes = (size_t)n_sm * (sizeof(int4) + 2 * rows * (head_dim + 2) * sizeof(float));
     return MK_OK;
   });
 }
@@ -915,9 +1006,9 @@ extern "C" mk_status mk_tree_attention(const mk_tree_args* args, const mk_page_v
       return paged_fail(MK_ERR_INVALID, "the vectors of out overlap");
     // the line of work counts in 32 bits, in tiles of 64 at the least
     const long long cap = (long long)cache->table_width * cache->page_size;
-    const long long most = (args->window > 0 ? std::min(cap, (long long)args->window + kMaxNodes + 64) : cap) / 64 + 2 + kLead;
+    const long long most = (args->window > 0 ? std::min(cap, (long long)args->window + kMaxNodes + kTile) : cap) / kTile + 2 + kLead;
     if (most * rn > 0x7f000000LL / cache->n_kv_heads)
-      return paged_fail(MK_ERR_INVALID, "n_rows * n_kv_heads * (the table's positions / 64 + 4) must be below 2^31 - 2^24");
+      return paged_fail(MK_ERR_INVALID, "n_rows * n_kv_heads * (the table's positions / 64 + 6) must be below 2^31 - 2^24");
     if (!args->workspace || !aligned_to(args->workspace, 16)) return paged_fail(MK_ERR_INVALID, "the workspace is missing or unaligned");
     if (args->n_rows == 0) return MK_OK;
     size_t need = 0;
