@@ -29,7 +29,7 @@ namespace {
 constexpr int kMaxNodes = 128, kMaxGroup = 16;
 constexpr int kRows = 128;               // rows of a block: the tensor cores' M
 constexpr int kGroupThreads = 128;       // a softmax warpgroup: a thread per row
-constexpr int kTreeThreads = 2 * kGroupThreads + 64;  // two of them, a warp for the copies, one for the products
+constexpr int kTreeThreads = 2 * kGroupThreads + 96;  // two of them, a warp for the copies, one for each one's products
 constexpr int kTile = 64;                // slots that are copied, multiplied and weighted at a time
 constexpr int kMaxStages = 10;
 constexpr int kCopyWarp = 8, kMmaWarp = 9;
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   if (warp == kCopyWarp) {
     if (lane < ST) {
       mbar_init(&st->full[lane], 1);
-      mbar_init(&st->empty[lane], 1);
+      mbar_init(&st->empty[lane], SH::BLOCKS);
     } else if (lane < ST + 2) {
       for (int b = 0; b < 2; ++b) {
         mbar_init(&st->s_full[lane - ST][b], 1);
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       }
     } else if (lane == ST + 2) {
       mbar_init(&st->q_full, 2 * kGroupThreads);
-      mbar_init(&st->finished, 1);
+      mbar_init(&st->finished, 2);
       st->abort = 0;
     }
     mbar_fence_init();
@@ -389,71 +389,65 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     }
     // every copy has landed before the CTA ends
     for (unsigned i = loads > ST ? loads - ST : 0; i < loads; ++i) wait_phase(&st->full[i % ST], i / ST & 1, &st->abort);
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kMmaWarp) {
     // ----------------------------------------------------------------------- products
-    // (the whole warp walks, so that what the instructions take stays in uniform registers; one lane issues)
-    const uint64_t q_desc = smem_desc(smem_addr(s_q), 16, 1024), k_desc = smem_desc(smem_addr(s_kv), 16, 1024);
-    const uint64_t v_desc = smem_desc(smem_addr(s_kv), kTile * 128, 1024);
-    unsigned p_phase = 0, pieces = 0;     // p_phase: a bit per warpgroup and buffer
-    int stage = -1;                       // tiles are used in the order of their copies
-    unsigned lap = 1;
-    auto next_stage = [&]() {
-      if (++stage == ST) stage = 0;
-      if (stage == 0) lap ^= 1;
-      wait_phase(&st->full[stage], lap, &st->abort);
-      return stage;
-    };
-    int k_at = 0, v_at = 0;
+    // A warp for each warpgroup: one alone takes longer to issue a job than the tensor cores to do it.  The whole
+    // warp walks, so that what the instructions take stays in uniform registers; one lane issues.
+    const int g = warp - kMmaWarp;
+    const uint64_t q_desc = smem_desc(smem_addr(s_q) + (PAIR ? g : 0) * NQ * SH::kQPart, 16, 1024);
+    const uint64_t k_desc = smem_desc(smem_addr(s_kv), 16, 1024), v_desc = smem_desc(smem_addr(s_kv), kTile * 128, 1024);
+    const uint32_t t_s = tmem + g * 256, t_o = t_s + 128;
+    unsigned p_phase = 0, pieces = 0;     // p_phase: a bit per buffer
     while (next_piece(a, w, p)) {
-      const int n = PAIR ? 2 * p.count : p.count;  // jobs: a tile of one warpgroup
+      const int n = PAIR ? p.count : (p.count - g + 1) / 2;  // jobs: this warpgroup's tiles
       wait_phase(&st->q_full, pieces & 1, &st->abort);
       ++pieces;
-      // job x is warpgroup x & 1's, in its buffer x >> 1 & 1.  The tensor cores take what one thread issues in
-      // order, so that a buffer's next scores come after the product that read its P.
-      auto turn_of = [&](int x) { return SH::BUFFERS == 2 ? x >> 1 & 1 : 0; };
+      auto tile = [&](int x) { return PAIR ? x : 2 * x + g; };
+      // The tensor cores take what one thread issues in order: a buffer's next scores come after the product
+      // that read its P.
       auto scores = [&](int x) {
-        const int g = x & 1;
-        if (!PAIR || g == 0) k_at = next_stage();
+        const unsigned l = loads + SH::k_load(tile(x)), s = l % ST;
+        const int b = SH::BUFFERS == 2 ? x & 1 : 0;
+        wait_phase(&st->full[s], l / ST & 1, &st->abort);
         tmem_fence_after();
         if (elect_one()) {
-          const uint32_t d = tmem + g * 256 + turn_of(x) * kTile;
-          const uint64_t qd = q_desc + (PAIR ? g : 0) * (NQ * SH::kQPart / 16), kd = k_desc + k_at * (SH::kStage / 16);
+          const uint64_t kd = k_desc + s * (SH::kStage / 16);
 #pragma unroll
           for (int y = 0; y < NQ; ++y)
 #pragma unroll
             for (int c = 0; c < HD / 16; ++c)  // (the address counts in 16 bytes)
-              mma_ss(d, qd + (y * SH::kQPart + (c >> 2) * kRows * 128 + (c & 3) * 32) / 16,
+              mma_ss(t_s + b * kTile, q_desc + (y * SH::kQPart + (c >> 2) * kRows * 128 + (c & 3) * 32) / 16,
                      kd + ((c >> 2) * kTile * 128 + (c & 3) * 32) / 16, mma_desc(kType, false, kRows, kTile), y + c > 0);
-          mma_commit(&st->s_full[g][turn_of(x)]);
-          if (!PAIR || g == 1) mma_commit(&st->empty[k_at]);
+          mma_commit(&st->s_full[g][b]);
+          mma_commit(&st->empty[s]);
         }
         __syncwarp();
       };
       auto values = [&](int x) {
-        const int g = x & 1, b = turn_of(x), bit = 2 * g + b;
-        if (!PAIR || g == 0) v_at = next_stage();
-        wait_phase(&st->p_full[g][b], p_phase >> bit & 1, &st->abort);
-        p_phase ^= 1u << bit;
+        const unsigned l = loads + SH::v_load(tile(x), p.count), s = l % ST;
+        const int b = SH::BUFFERS == 2 ? x & 1 : 0;
+        wait_phase(&st->full[s], l / ST & 1, &st->abort);
+        wait_phase(&st->p_full[g][b], p_phase >> b & 1, &st->abort);
+        p_phase ^= 1u << b;
         tmem_fence_after();
         if (elect_one()) {
-          const uint32_t d = tmem + g * 256 + 128, pa = tmem + g * 256 + b * kTile;
-          const uint64_t vd = v_desc + v_at * (SH::kStage / 16);
+          const uint64_t vd = v_desc + s * (SH::kStage / 16);
 #pragma unroll
           for (int y = 0; y < NP; ++y)
 #pragma unroll
             for (int c = 0; c < kTile / 16; ++c)
-              mma_ts(d, pa + y * (kTile / 2) + c * 8, vd + c * 2048 / 16, mma_desc(kType, true, kRows, HD), true);
+              mma_ts(t_o, t_s + b * kTile + y * (kTile / 2) + c * 8, vd + c * 2048 / 16, mma_desc(kType, true, kRows, HD), true);
           mma_commit(&st->o_done[g][b]);
-          if (!PAIR || g == 1) mma_commit(&st->empty[v_at]);
+          mma_commit(&st->empty[s]);
         }
         __syncwarp();
       };
-      constexpr int FIRST = 2 * SH::BUFFERS;
-      for (int x = 0; x < min(n, FIRST); ++x) scores(x);
+      for (int x = 0; x < min(n, SH::BUFFERS); ++x) scores(x);
       for (int x = 0; x < n; ++x) {
         values(x);
-        if (x + FIRST < n) scores(x + FIRST);
+        if (x + SH::BUFFERS < n) scores(x + SH::BUFFERS);
       }
+      loads += 2 * p.count;
     }
     if (elect_one()) mma_commit(&st->finished);
     __syncwarp();
