@@ -56,6 +56,8 @@ struct TreeArgs {
   int q_vec, o_vec;                      // 16-byte accesses
   float scale, softcap;                  // scores to units of log 2: scale s, or softcap tanh(scale s)
   float q_sign;                          // -1: queries are negated (the scale was negative), 0: they are zero
+  uint32_t q_and, q_xor;                 // the same for a pair of 16-bit ones
+  int group_inverse;                     // 2^16 / group, rounded up
 };
 
 // Slots [lo, hi) of a row that some node may see, its tiles [t0, t0 + n).
@@ -152,6 +154,9 @@ template <typename T>
 constexpr float kSlack = 8.f;             // a maximum may be passed by this much before what is summed is rescaled
 template <>
 constexpr float kSlack<__half> = 5.f;
+
+// the node of a block that a row of it is of: row / group, exact for rows below 128 and groups up to 16
+__device__ __forceinline__ int node_of(const TreeArgs& a, int row) { return row * a.group_inverse >> 16; }
 
 // Waits for a phase of a barrier: a wait that takes too long sets *abort, and from then on none waits.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* abort) {
@@ -338,8 +343,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   if (warp == kCopyWarp) {
     // ------------------------------------------------------------------------- copies
     unsigned tiles = 0;
-    bool run = true;
+    bool run = true, begun = false;
     while (run && next_piece(a, w, p)) {
+      if (begun) {  // the queries of a piece to come: to L2 while the one before it is worked on
+        constexpr int LINES = HD * (int)sizeof(Q) / 128;
+        const int nodes = min(SH::BLOCKS * a.nodes_per_block, a.n_nodes - part * SH::BLOCKS * a.nodes_per_block);
+        for (int x = lane; x < nodes * a.group * LINES; x += 32) {
+          const int y = x / LINES, nd = y / a.group;  // (of both blocks)
+          prefetch_l2_line(static_cast<const Q*>(a.q) + p.r * a.q_row + (long long)(part * SH::BLOCKS * a.nodes_per_block + nd) * a.q_node +
+                           (long long)(p.head * a.group + y - nd * a.group) * a.q_head + x % LINES * (128 / sizeof(Q)));
+        }
+      }
       const int boxes = kTile / a.box, half = lane / boxes;  // a lane per copy: 64 dims of some positions
       const int at0 = (p.sp.t0 + p.first) * kTile + lane % boxes * a.box;
       const bool on = half < HALVES;
@@ -379,6 +393,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i)
         if (i < p.count) keys(i, page[i]);
+      // (the first queries do not queue behind the keys and values that fill the ring)
+      if (!begun) wait_phase(&st->q_full, 0, &st->abort);
+      begun = true;
       for (int i = 0; i < p.count && run; ++i) {
         page[AHEAD + 1] = page_of(i + AHEAD + 1);
         run = copy(&v_map, i, page[0]);
@@ -458,7 +475,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;         // this warp's lanes of the tensor memory
     const uint32_t t_s0 = tmem + g * 256 + lanes, t_o = t_s0 + 128;
     const int first_node = (PAIR ? 2 * part : part) * a.nodes_per_block;
-    const int node = first_node + (PAIR ? g * a.nodes_per_block : 0) + row / a.group, h = row % a.group;
+    const int node = first_node + (PAIR ? g * a.nodes_per_block : 0) + node_of(a, row), h = row - node_of(a, row) * a.group;
+    // the rows that hold queries, rounded up to whole warps' worth; the others of the blocks stay zero
+    const int q_rows = PAIR ? 2 * kRows : min(kRows, (min(a.nodes_per_block, a.n_nodes - first_node) * a.group + 31) / 32 * 32);
+    for (int x = q_rows * 8 + tid; x < kRows * 8; x += 2 * kGroupThreads)
+      for (int y = 0; y < NQ * HALVES; ++y) reinterpret_cast<uint4*>(s_q)[y * kRows * 8 + x] = make_uint4(0u, 0u, 0u, 0u);
+    if (row >= q_rows && !PAIR && g == 0) st->scale[row] = 1.f;
     const bool valid = row < a.nodes_per_block * a.group && node < a.n_nodes;
     const bool warp_valid = __any_sync(0xffffffffu, valid);
     unsigned tiles = 0, s_phase = 0;      // tiles of the CTA; a bit per buffer: the next phase of its scores
@@ -470,21 +492,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       groups_sync();                      // what the last piece left in shared and tensor memory was read
       if (p.r != row_of)
         for (int i = tid; i < a.n_nodes; i += 2 * kGroupThreads) st->parents[i] = a.parents[(long long)p.r * a.n_nodes + i];
-      // ---- the queries, K-major, 128-byte swizzled; neighbouring lanes take neighbouring chunks of a row
+      // ---- the queries, K-major, 128-byte swizzled; neighbouring lanes take neighbouring chunks of a row.  (What
+      // is executed once or twice waits for its instructions: the loop is short, and ends with the rows.)
       {
-        constexpr int CH = HD / 8, ITEMS = SH::BLOCKS * kRows * CH / (2 * kGroupThreads), U = ITEMS < 8 ? ITEMS : 8;
+        constexpr int CH = HD / 8, STEP = 2 * kGroupThreads / CH, U = NQ == 1 ? 4 : sizeof(Q) == 2 ? 2 : 1;
         const int c = tid % CH;
         const Q* src = static_cast<const Q*>(a.q) + p.r * a.q_row + (long long)p.head * a.group * a.q_head + 8 * c;
 #pragma unroll 1
-        for (int z0 = 0; z0 < ITEMS; z0 += U) {
+        for (int x0 = tid / CH; x0 < q_rows; x0 += U * STEP) {
           Raw8<Q> raw[U];
 #pragma unroll
           for (int z = 0; z < U; ++z) {
-            const int x = tid / CH + (z0 + z) * (2 * kGroupThreads / CH), y = x % kRows;  // row of all blocks, of its own
-            const int nd = y / a.group, at = first_node + x / kRows * a.nodes_per_block + nd;
+            const int x = x0 + z * STEP, y = x % kRows, nd = node_of(a, y);  // row of all blocks, of its own
             raw[z] = {};
-            if (nd < a.nodes_per_block && at < a.n_nodes) {
-              const Q* from = src + at * a.q_node + (y - nd * a.group) * a.q_head;
+            if (x < q_rows && nd < a.nodes_per_block && x / kRows * a.nodes_per_block + nd < a.n_nodes - first_node) {
+              const Q* from = src + (first_node + x / kRows * a.nodes_per_block + nd) * a.q_node + (y - nd * a.group) * a.q_head;
               if (a.q_vec)
                 raw[z].load(from);
               else
@@ -493,27 +515,35 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
           }
 #pragma unroll
           for (int z = 0; z < U; ++z) {
-            const int x = tid / CH + (z0 + z) * (2 * kGroupThreads / CH), y = x % kRows;
-            float v[8];
-            raw[z].up(v);
-            float up = a.q_sign;
-            if constexpr (kScaled<C, Q>) {  // the chunks of a row are in neighbouring lanes
-              float most = fabsf(v[0]);
-#pragma unroll
-              for (int e = 1; e < 8; ++e) most = fmaxf(most, fabsf(v[e]));
-#pragma unroll
-              for (int o = 1; o < CH; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-              const int shift = shift_of(most);
-              up *= power_of(shift);
-              if (c == 0) st->scale[x] = a.scale * power_of(-shift);
-            }
+            const int x = x0 + z * STEP, y = x % kRows;
             uint32_t parts[4][NQ];
+            if constexpr (std::is_same<C, Q>::value) {
+              parts[0][0] = (raw[z].w[0].x & a.q_and) ^ a.q_xor;
+              parts[1][0] = (raw[z].w[0].y & a.q_and) ^ a.q_xor;
+              parts[2][0] = (raw[z].w[0].z & a.q_and) ^ a.q_xor;
+              parts[3][0] = (raw[z].w[0].w & a.q_and) ^ a.q_xor;
+            } else {
+              float v[8];
+              raw[z].up(v);
+              float up = a.q_sign;
+              if constexpr (kScaled<C, Q>) {  // the chunks of a row are in neighbouring lanes
+                float most = fabsf(v[0]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) split2<C, NQ>(v[2 * e] * up, v[2 * e + 1] * up, parts[e]);
+                for (int e = 1; e < 8; ++e) most = fmaxf(most, fabsf(v[e]));
 #pragma unroll
-            for (int n = 0; n < NQ; ++n)
-              *reinterpret_cast<uint4*>(s_q + ((x / kRows) * NQ + n) * SH::kQPart + (c >> 3) * kRows * 128 + y * 128 +
-                                        (((c & 7) ^ (y & 7)) << 4)) = make_uint4(parts[0][n], parts[1][n], parts[2][n], parts[3][n]);
+                for (int o = 1; o < CH; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                const int shift = shift_of(most);
+                up *= power_of(shift);
+                if (c == 0 && x < q_rows) st->scale[x] = a.scale * power_of(-shift);
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) split2<C, NQ>(v[2 * e] * up, v[2 * e + 1] * up, parts[e]);
+            }
+            if (x < q_rows)
+#pragma unroll
+              for (int n = 0; n < NQ; ++n)
+                *reinterpret_cast<uint4*>(s_q + ((x / kRows) * NQ + n) * SH::kQPart + (c >> 3) * kRows * 128 + y * 128 +
+                                          (((c & 7) ^ (y & 7)) << 4)) = make_uint4(parts[0][n], parts[1][n], parts[2][n], parts[3][n]);
           }
         }
       }
@@ -558,6 +588,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       const int lo = there ? from(depth) : p.sp.len;
       const int plain_lo = from(a.n_nodes - 1);  // tiles in [plain_lo, len) are seen by all nodes whole
       float m = -INFINITY, l = 0.f;
+      // before the sums so far are touched: the last product is done (of the buffer at hand it is: its scores came after it)
+      auto sums_done = [&](int buf) {
+        if (SH::BUFFERS == 2) wait_phase(&st->o_done[g][buf ^ 1], (s_phase >> (buf ^ 1) & 1) ^ 1, &st->abort);
+        tmem_fence_after();
+      };
       int turn = 0;                       // tiles of the piece that this warpgroup has taken
       for (int i = PAIR ? 0 : g; i < p.count; i += PAIR ? 1 : 2, ++turn) {
         const int t0 = (p.sp.t0 + p.first + i) * kTile;
@@ -568,42 +603,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         tmem_fence_after();
         const unsigned bad = *(volatile unsigned char*)&st->bad[(tiles + i) % 16];
         const bool partial = t0 < plain_lo || t0 + kTile > min(p.sp.len, p.sp.hi) || bad != 0;
-        unsigned vis[2], odd[2] = {0, 0};
-        if (partial) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int b = t0 + 32 * x;
-            vis[x] = ones(lo - b, p.sp.len - b) | bits_at(seen, b - p.sp.len);
-            vis[x] &= ones(0, p.sp.hi - b);
-            if (bad >> (2 * x) & 1) vis[x] &= 0xffff0000u;
-            if (bad >> (2 * x) & 2) vis[x] &= 0x0000ffffu;
-          }
-          // values that are not finite must not meet the zero of one who does not see them: they are taken
-          // out of the tile and added for those who do.  (A set is used again when all who read it are through
-          // its tile: the scores they wait for come after the products of the tiles before.)
-          unsigned* found = st->odd[PAIR ? i & 3 : 2 * g + (turn & 1)];
-          if (row < 2) found[row] = 0;
-          tile_sync<PAIR>(g);
-          const unsigned v_at = loads + SH::v_load(i, p.count);
-          wait_phase(&st->full[v_at % ST], v_at / ST & 1, &st->abort);
-          uint4* v = reinterpret_cast<uint4*>(s_kv + v_at % ST * SH::kStage);
-          constexpr int step = PAIR ? 2 * kGroupThreads : kGroupThreads;
-#pragma unroll
-          for (int z = 0; z < SH::kStage / 16 / step; ++z) {
-            const int x = (PAIR ? tid : row) + z * step;
-            const uint4 y = v[x];
-            const uint32_t o0 = odd_mask<C>(y.x), o1 = odd_mask<C>(y.y), o2 = odd_mask<C>(y.z), o3 = odd_mask<C>(y.w);
-            if (o0 | o1 | o2 | o3) {
-              v[x] = make_uint4(y.x & ~o0, y.y & ~o1, y.z & ~o2, y.w & ~o3);
-              const int slot = x / 8 % kTile;
-              atomicOr(&found[slot >> 5], 1u << (slot & 31));
-            }
-          }
-          fence_proxy_async();
-          tile_sync<PAIR>(g);
-          odd[0] = found[0];
-          odd[1] = found[1];
-        }
+        unsigned vis[2] = {0, 0};
         if (warp_valid) {
           float factor = scale;
           if (a.softcap > 0.f) {
@@ -625,9 +625,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
           tmem_wait_ld();
           if (partial) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < 2; ++x) {
+              const int b = t0 + 32 * x;
+              vis[x] = ones(lo - b, p.sp.len - b) | bits_at(seen, b - p.sp.len);
+              vis[x] &= ones(0, p.sp.hi - b);
+              if (bad >> (2 * x) & 1) vis[x] &= 0xffff0000u;
+              if (bad >> (2 * x) & 2) vis[x] &= 0x0000ffffu;
 #pragma unroll
               for (int y = 0; y < 32; ++y) s[x][y] = vis[x] >> y & 1 ? s[x][y] : 0xff800000u;
+            }
           }
           float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -638,12 +644,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
           const bool grown = top > m + kSlack<C>;
           const float to = grown ? top : m;
           const bool rescale = __any_sync(0xffffffffu, grown && m > -INFINITY);
-          if (rescale || (odd[0] | odd[1])) {  // the sums so far are touched: the last product is done
-            // (of this buffer's it is: these scores came after it)
-            if (SH::BUFFERS == 2) wait_phase(&st->o_done[g][buf ^ 1], (s_phase >> (buf ^ 1) & 1) ^ 1, &st->abort);
-            tmem_fence_after();
-          }
           if (rescale) {
+            sums_done(buf);
             const float f = grown ? ex2(m - to) : 1.f;
             l *= f;
 #pragma unroll 1
@@ -678,6 +680,33 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
           const float2 both = add2(sum[0], sum[1]);
           l += both.x + both.y;
           tmem_wait_st();
+        }
+        if (partial) {
+          // Values that are not finite must not meet the zero of one who does not see them: they are taken
+          // out of the tile and added for those who do.  (A set of them is used again when all who read it are
+          // through its tile: the scores they wait for come after the products of the tiles before.)
+          unsigned* found = st->odd[PAIR ? i & 3 : 2 * g + (turn & 1)];
+          if (row < 2) found[row] = 0;
+          tile_sync<PAIR>(g);
+          const unsigned v_at = loads + SH::v_load(i, p.count);
+          wait_phase(&st->full[v_at % ST], v_at / ST & 1, &st->abort);
+          uint4* v = reinterpret_cast<uint4*>(s_kv + v_at % ST * SH::kStage);
+          constexpr int step = PAIR ? 2 * kGroupThreads : kGroupThreads;
+#pragma unroll
+          for (int z = 0; z < SH::kStage / 16 / step; ++z) {
+            const int x = (PAIR ? tid : row) + z * step;
+            const uint4 y = v[x];
+            const uint32_t o0 = odd_mask<C>(y.x), o1 = odd_mask<C>(y.y), o2 = odd_mask<C>(y.z), o3 = odd_mask<C>(y.w);
+            if (o0 | o1 | o2 | o3) {
+              v[x] = make_uint4(y.x & ~o0, y.y & ~o1, y.z & ~o2, y.w & ~o3);
+              const int slot = x / 8 % kTile;
+              atomicOr(&found[slot >> 5], 1u << (slot & 31));
+            }
+          }
+          fence_proxy_async();
+          tile_sync<PAIR>(g);
+          const unsigned odd[2] = {found[0], found[1]};
+          if (odd[0] | odd[1]) sums_done(buf);
 #pragma unroll 1
           for (int x2 = 0; x2 < 2; ++x2) {
             for (unsigned rest = x2 ? odd[1] : odd[0]; rest; rest &= rest - 1) {
@@ -748,7 +777,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       constexpr int DIMS = PAIR ? HD : HD / 2, kRun = DIMS * (int)sizeof(Q), RCH = kRun / 16, kTwist = RCH < 8 ? RCH - 1 : 7;
       const int d0 = PAIR ? 0 : g * DIMS;
       unsigned char* run = s_q + ((PAIR ? g : 0) * kRows + (warp & 3) * 32) * HD * sizeof(Q) + (PAIR ? 0 : g) * 32 * kRun;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < DIMS / 32; ++c) {
         uint32_t o[32];
         if (PAIR) {
@@ -789,9 +818,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       if (p.whole) {
         __syncwarp();
         Q* out = static_cast<Q*>(a.out) + p.r * a.o_row + (long long)p.head * a.group * a.o_head + d0;
-#pragma unroll 4
+#pragma unroll 2
         for (int x = lane; x < 32 * RCH; x += 32) {
-          const int y = (warp & 3) * 32 + x / RCH, ch = x % RCH, nd = y / a.group;
+          const int y = (warp & 3) * 32 + x / RCH, ch = x % RCH, nd = node_of(a, y);
           const int at = first_node + (PAIR ? g * a.nodes_per_block : 0) + nd;
           if (nd >= a.nodes_per_block || at >= a.n_nodes) continue;
           const uint4 v = *reinterpret_cast<const uint4*>(run + x / RCH * kRun + ((ch ^ (x / RCH & kTwist)) << 4));
@@ -867,7 +896,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
   for (int e = 0; e < E; ++e) s_o[lane][warp * E + e] = l == 0.f ? 0.f : o[e] / l;
   // where row x of the blocks goes: its node and head, or no node
   auto place = [&](int x, int* node, int* head) {
-    const int y = x % kRows, nd = y / a.group;
+    const int y = x % kRows, nd = node_of(a, y);
     *node = (part * per + x / kRows) * a.nodes_per_block + nd;
     *head = job.w * a.group + y - nd * a.group;
     return x < a.part_rows && nd < a.nodes_per_block && *node < a.n_nodes;
@@ -1032,6 +1061,9 @@ extern "C" mk_status mk_tree_attention(const mk_tree_args* args, const mk_page_v
     a.o_vec = aligned_to(a.out, 16) && a.o_row % per == 0 && a.o_node % per == 0 && a.o_head % per == 0;
     a.scale = factor == 0.f ? 1.f : std::abs(factor);
     a.q_sign = factor == 0.f ? 0.f : factor < 0.f ? -1.f : 1.f;
+    a.q_and = factor == 0.f ? 0u : 0xffffffffu;
+    a.q_xor = factor < 0.f ? 0x80008000u : 0u;
+    a.group_inverse = (65536 + a.group - 1) / a.group;
     a.softcap = args->softcap * kLog2e;
     // 16-bit queries of the cache's type are exact in one part, others are split into 2 parts of fp16 (22
     // bits, each head at a power of two of its own) or 3 of bf16 (24 bits).  A probability has one part where the
