@@ -25,10 +25,10 @@ struct AcceptArgs {
   int n_layers, n_pages, page_size, width, hkv, n_nodes, vec;  // vec: 16-byte pieces of a vector
 };
 
-__global__ void __cluster_dims__(kAcceptCluster, 1, 1) __launch_bounds__(kAcceptThreads)
+__global__ void __cluster_dims__(kAcceptCluster, 1, 1) __launch_bounds__(kAcceptThreads, 4)
 accept_kernel(const __grid_constant__ AcceptArgs a) {
   __shared__ int s_token[kMaxNodes], s_parent[kMaxNodes], s_choice[kMaxNodes], s_path[kMaxNodes], s_count;
-  __shared__ int s_src[kMaxNodes][2], s_dst[kMaxNodes][2];  // page and position in it
+  __shared__ long long s_src[kMaxNodes], s_dst[kMaxNodes];  // bytes from a plane's begin to the vectors of its first head
   const int tid = threadIdx.x, lane = tid & 31, r = blockIdx.x / kAcceptCluster, rank = blockIdx.x % kAcceptCluster;
   const int n = a.n_nodes;
   pdl_wait();
@@ -75,9 +75,7 @@ accept_kernel(const __grid_constant__ AcceptArgs a) {
         bad = true;
         told = (int)t;
       }
-      int(*place)[2] = w ? s_dst : s_src;
-      place[j][0] = page;
-      place[j][1] = (int)(t - (long long)i * a.page_size);
+      (w ? s_dst : s_src)[j] = page * a.page_stride + (t - (long long)i * a.page_size) * a.vec * 16;
     }
   }
   if (__syncthreads_or(bad)) {
@@ -85,7 +83,7 @@ accept_kernel(const __grid_constant__ AcceptArgs a) {
     count = 0;
   }
   const int planes = 2 * a.n_layers * a.hkv, vec = a.vec;
-  constexpr int U = 8;  // vectors in flight
+  constexpr int U = 6;  // vectors in flight
   for (int x = rank * kAcceptThreads + tid; x < planes * vec && count > 1; x += kAcceptCluster * kAcceptThreads) {
     const int piece = x % vec, plane = x / vec, head = plane % a.hkv, l = plane / a.hkv;
     char* base = (l & 1 ? a.v : a.k) + (long long)(l >> 1) * a.layer_stride + (long long)head * a.page_size * vec * 16 + piece * 16;
@@ -94,11 +92,11 @@ accept_kernel(const __grid_constant__ AcceptArgs a) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (j0 + u < count)
-          got[u] = *reinterpret_cast<const uint4*>(base + s_src[j0 + u][0] * a.page_stride + (long long)s_src[j0 + u][1] * vec * 16);
+          got[u] = *reinterpret_cast<const uint4*>(base + s_src[j0 + u]);
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (j0 + u < count && s_path[j0 + u] != j0 + u)
-          *reinterpret_cast<uint4*>(base + s_dst[j0 + u][0] * a.page_stride + (long long)s_dst[j0 + u][1] * vec * 16) = got[u];
+          *reinterpret_cast<uint4*>(base + s_dst[j0 + u]) = got[u];
     }
   }
   // every CTA of the row has read its length

@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(kBoundThreads) bounds_kernel(const __grid_cons
 }
 
 // ------------------------------------------------------------------------------ scores
-constexpr int kScoreThreads = 256;
+constexpr int kScoreWarps = 8, kScoreThreads = 32 * kScoreWarps;
+constexpr int kScorePages = 8;             // pages that a warp takes at a time
 
 struct ScoreArgs {
   const void *q, *bounds;
@@ -112,58 +113,215 @@ struct ScoreArgs {
   float* scores;
   int32_t* status;
   long long q_row, q_head, table_stride;
-  int n_rows, hkv, group, page_size, n_pages, table_rows, width;
+  int n_rows, hkv, group, page_size, n_pages, table_rows, width, chunk, q_vec;  // chunk: pages of a CTA
 };
 
-// A warp takes a page of one row and kv head, a lane HD / 32 elements; the heads' sums go through the lanes.
-template <typename C, typename Q, int HD>
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float z;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
+}
+
+// As q_d low_d or q_d high_d is the greater by q_d's sign alone, a score is one product of length 2 HD: of the
+// queries' negative elements and then their positive ones with a page's lower bounds and then its upper ones,
+// which lie one behind the other.  A warp takes eight pages: tensor-core tiles m16n8k16 of 16 rows of heads (up to
+// 8 heads: row g the head's first part, row g + 8 the second; more: a row per head) and 8 columns of pages, whose
+// fragments come straight from memory, 16 bytes a lane, as the elements may be summed in any order the two
+// operands share.  The lower and the upper half are summed apart, in two chains.  Where a sum is not finite (an
+// infinite bound times the zero of the other sign) the warp takes those pages once more without the tensor
+// cores.  Bound: the bounds' bytes (16 rows of 1024 to 2048 pages of 16 positions, 105 MB).
+template <typename C, typename Q, int HD, bool WIDE, int NQ>
+struct ScoreSmem {
+  static constexpr int I = HD / 16;        // chunks of 32 elements of both halves
+  static constexpr int RH = WIDE ? 2 : 1;
+  uint4 q[kScoreWarps][NQ][I][RH][32];
+  float scale[kScoreWarps][16];
+};
+template <typename C, typename Q, int HD, bool WIDE, int NQ>
 __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_constant__ ScoreArgs a) {
-  constexpr int E = HD / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, head = blockIdx.y, r = blockIdx.z;
+  using SM = ScoreSmem<C, Q, HD, WIDE, NQ>;
+  constexpr int I = SM::I, RH = SM::RH;
+  extern __shared__ __align__(16) unsigned char score_smem[];
+  SM* sm = reinterpret_cast<SM*>(score_smem);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y, g = lane >> 2, c = lane & 3;
   pdl_wait();
   pdl_launch();
-  const int j = blockIdx.x * (kScoreThreads / 32) + warp;
-  if (j >= a.width) return;
   const int trow = a.rows ? a.rows[r] : r, cap = a.width * a.page_size;
-  const bool tell = j == 0 && head == 0 && lane == 0;
-  int len = a.lens[r];
+  const bool tell = blockIdx.x == 0 && threadIdx.x == 0;
+  int len = max(0, a.lens[r]);
   if ((unsigned)trow >= (unsigned)a.table_rows) {
     if (tell && len > 0) report(a.status, MK_ERR_PAGES, PO_SCORES, r, trow);
     len = 0;
   }
-  if (len > cap && tell) report(a.status, MK_ERR_PAGES, PO_SCORES, r, len);
-  float best = -INFINITY;
-  if (len > 0 && (long long)j * a.page_size < len) {
-    const int page = a.table[(long long)trow * a.table_stride + j];
-    if ((unsigned)page >= (unsigned)a.n_pages) {
-      if (head == 0 && lane == 0) report(a.status, MK_ERR_PAGES, PO_SCORES, r, page);
-    } else {
-      const C* b = static_cast<const C*>(a.bounds) + ((long long)page * a.hkv + head) * 2 * HD + lane;
-      float lo[E], hi[E];
+  if (len > cap) {
+    if (tell) report(a.status, MK_ERR_PAGES, PO_SCORES, r, len);
+    len = cap;
+  }
+  const int pages = (len + a.page_size - 1) / a.page_size;
+  const int begin = blockIdx.x * a.chunk, end = min(a.width, begin + a.chunk);
+  const int per = min(a.hkv, kScoreWarps), subs = kScoreWarps / per, sub = warp / per;
+  if (sub >= subs) return;
+  const int32_t* table = a.table + (long long)(len > 0 ? trow : 0) * a.table_stride;
+  const int step = subs * kScorePages, first = begin + sub * kScorePages;
+  // the page of this lane's column, -1 where there is none
+  auto page_of = [&](int j, bool tell_bad) {
+    if (j >= min(pages, end)) return -1;
+    const int page = table[j];
+    if ((unsigned)page < (unsigned)a.n_pages) return page;
+    if (tell_bad && c == 0) report(a.status, MK_ERR_PAGES, PO_SCORES, r, page);
+    return -1;
+  };
+  for (int head = warp % per; head < a.hkv; head += per) {
+    float* out = a.scores + ((long long)r * a.hkv + head) * a.width;
+    const Q* q0 = static_cast<const Q*>(a.q) + (long long)r * a.q_row + (long long)head * a.group * a.q_head + 8 * c;
+    const C* b0 = static_cast<const C*>(a.bounds) + (long long)head * 2 * HD + 8 * c;
+    uint4 raw[I];
+    auto load = [&](int page) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        lo[e] = Conv<C>::up(b[32 * e]);
-        hi[e] = Conv<C>::up(b[HD + 32 * e]);
-      }
-      for (int h = 0; h < a.group; ++h) {
-        const Q* q = static_cast<const Q*>(a.q) + (long long)r * a.q_row + (long long)(head * a.group + h) * a.q_head + lane;
-        float s = 0.f;
+      for (int i = 0; i < I; ++i)
+        raw[i] = page >= 0 ? ldg_stream(b0 + (long long)page * a.hkv * 2 * HD + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    int page = page_of(first + g, head == 0), ahead = page_of(first + step + g, head == 0);
+    if (first < pages) load(page);
+    // ---- the queries' fragments: chunk i, lane (g, c): elements [32 i + 8 c, + 8) of head g
+    if (first < pages) {
+      __syncwarp();
+#pragma unroll 1
+      for (int rh = 0; rh < RH; ++rh) {
+        const int h = g + 8 * rh;
+        auto get = [&](int i, float (&v)[8]) {
+          Raw8<Q> x = {};
+          if (h < a.group) {
+            if (a.q_vec)
+              x.load(q0 + h * a.q_head + 32 * i);
+            else
+              x.gather(q0 + h * a.q_head + 32 * i);
+          }
+          x.up(v);
+        };
+        float up = 1.f;
+        if constexpr (kScaled<C, Q>) {
+          float most = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float x = Conv<Q>::up(q[32 * e]);
-          s = fmaf(x, x > 0.f ? hi[e] : lo[e], s);
+          for (int i = 0; i < I / 2; ++i) {
+            float v[8];
+            get(i, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(v[e]));
+          }
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+          const int shift = shift_of(most);
+          up = power_of(shift);
+          if (c == 0) sm->scale[warp][h] = power_of(-shift);
         }
 #pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        best = s != s || best != best ? NAN : fmaxf(best, s);
+        for (int i = 0; i < I / 2; ++i) {
+          float v[8];
+          get(i, v);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t w[4][NQ];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = v[2 * e] * up, y = v[2 * e + 1] * up;
+              split2<C, NQ>((half ? x > 0.f : x < 0.f) || x != x ? x : 0.f, (half ? y > 0.f : y < 0.f) || y != y ? y : 0.f, w[e]);
+            }
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+              sm->q[warp][n][half * (I / 2) + i][rh][lane] = make_uint4(w[0][n], w[1][n], w[2][n], w[3][n]);
+          }
+        }
       }
+      __syncwarp();
+    }
+    for (int j0 = first; j0 < end; j0 += step) {
+      float best[2] = {-INFINITY, -INFINITY};  // of pages j0 + 2 c and the next one
+      if (j0 < pages) {
+        uint4 now[I];
+#pragma unroll
+        for (int i = 0; i < I; ++i) now[i] = raw[i];
+        const int mine = page;
+        page = ahead;
+        ahead = page_of(j0 + 2 * step + g, head == 0);
+        if (j0 + step < pages) load(page);
+        constexpr int SETS = WIDE ? NQ : (NQ + 1) / 2;
+        float d[SETS][2][4];
+#pragma unroll
+        for (int n = 0; n < SETS; ++n)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[n][half][e] = 0.f;
+#pragma unroll
+            for (int i = half * (I / 2); i < (half + 1) * (I / 2); ++i) {
+              const int n0 = WIDE ? n : 2 * n;
+              const uint4 u = sm->q[warp][n0][i][0][lane];
+              const uint4 w = WIDE ? sm->q[warp][n0][i][RH - 1][lane]
+                              : n0 + 1 < NQ ? sm->q[warp][n0 + 1 < NQ ? n0 + 1 : 0][i][0][lane] : make_uint4(0u, 0u, 0u, 0u);
+              Mma<C>::run(d[n][half], make_uint4(u.x, w.x, u.y, w.y), now[i].x, now[i].y);
+              Mma<C>::run(d[n][half], make_uint4(u.z, w.z, u.w, w.w), now[i].z, now[i].w);
+            }
+          }
+        bool odd = false;
+#pragma unroll
+        for (int rh = 0; rh < RH; ++rh) {
+          const int h = g + 8 * rh;
+          const float scale = kScaled<C, Q> ? sm->scale[warp][h] : 1.f;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float s = 0.f;
+#pragma unroll
+            for (int n = SETS - 1; n >= 0; --n) {  // the smallest parts first
+              if (!WIDE && 2 * n + 1 < NQ) s += d[n][0][2 + e] + d[n][1][2 + e];
+              s += d[n][0][2 * rh + e] + d[n][1][2 * rh + e];
+            }
+            s *= scale;
+            odd = odd || !(fabsf(s) < INFINITY);
+            if (h < a.group) best[e] = fmaxf(best[e], s);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) best[e] = fmaxf(best[e], __shfl_xor_sync(0xffffffffu, best[e], o));
+        if (__any_sync(0xffffffffu, odd)) {  // the four lanes of a page together, what is not a half's to add adds nothing
+          float most = -INFINITY;
+          for (int h = 0; h < a.group; ++h) {
+            float s = 0.f;
+#pragma unroll 1
+            for (int i = 0; i < I / 2; ++i)
+              for (int e = 0; e < 8; ++e) {
+                const float x = Conv<Q>::up(q0[h * a.q_head + 32 * i + e]);
+                float lo = 0.f, hi = 0.f;
+                if (mine >= 0) {
+                  lo = Conv<C>::up(b0[(long long)mine * a.hkv * 2 * HD + 32 * i + e]);
+                  hi = Conv<C>::up(b0[(long long)mine * a.hkv * 2 * HD + HD + 32 * i + e]);
+                }
+                s += x == 0.f ? 0.f : x > 0.f ? x * hi : x * lo;
+              }
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            most = max_nan(most, s);
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) best[e] = __shfl_sync(0xffffffffu, most, 4 * (2 * c + e));
+        }
+        const unsigned there = __ballot_sync(0xffffffffu, mine >= 0);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (!(there >> (4 * (2 * c + e)) & 1)) best[e] = -INFINITY;
+      }
+      if (g == 0)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (j0 + 2 * c + e < end) out[j0 + 2 * c + e] = best[e];
     }
   }
-  if (lane == 0) a.scores[((long long)r * a.hkv + head) * a.width + j] = best;
 }
 
 // ------------------------------------------------------------------------------ choice
-constexpr int kChooseThreads = 256;
+constexpr int kChooseThreads = 512, kChooseKeys = 4;
 
 struct ChooseArgs {
   const float* scores;
@@ -177,10 +335,13 @@ struct ChooseArgs {
 __device__ __forceinline__ uint32_t key_of(float x) { return orderable(x != x ? INFINITY : x + 0.f); }
 
 // One CTA per row and kv head: the key of the last page to be taken by its bytes, from the top (a count of
-// the pages that share the bytes found so far, 256 counters a turn), then the pages in order: all with
-// a greater key and the first of those with the same.
+// the pages that share the bytes found so far, 256 counters a turn; equal bytes of a warp count at once, as the
+// first bytes of most scores are), then the pages in order: all with a greater key and the first of those
+// with the same.  Keys of up to kChooseThreads * kChooseKeys pages stay in registers.
+template <bool KEPT>
 __global__ void __launch_bounds__(kChooseThreads) choose_kernel(const __grid_constant__ ChooseArgs a) {
-  __shared__ int s_count[256], s_warp[kChooseThreads / 32][2], s_digit, s_left;
+  constexpr int W = kChooseThreads / 32;
+  __shared__ int s_count[256], s_warp[2][W][2], s_digit, s_left;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.x, head = blockIdx.y;
   pdl_wait();
   pdl_launch();
@@ -195,7 +356,7 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(const __grid_con
     if (tell) report(a.status, MK_ERR_PAGES, PO_SPARSE, r, len);
     len = cap;
   }
-  const int n = (int)(((long long)len + a.page_size - 1) / a.page_size), taken = min(n, a.n_blocks);
+  const int n = (len + a.page_size - 1) / a.page_size, taken = min(n, a.n_blocks);
   const int32_t* table = a.table + (long long)(len > 0 ? trow : 0) * a.table_stride;
   const float* score = a.scores + r * a.scores_row + head * a.scores_head;
   const long long at = ((long long)r * a.hkv + head) * a.n_blocks;
@@ -204,71 +365,103 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(const __grid_con
   const int begin = n > a.n_blocks ? a.first : 0, end = n > a.n_blocks ? n - a.last : 0;  // pages that are chosen among
   int left = n > a.n_blocks ? a.n_blocks - a.first - a.last : 0;                            // how many of them
   uint32_t limit = 0xffffffffu;  // above it: taken; at it: the first `left`
+  uint32_t kept[KEPT ? kChooseKeys : 1];
+  if (KEPT) {
+#pragma unroll
+    for (int i = 0; i < kChooseKeys; ++i) {
+      const int j = i * kChooseThreads + tid;
+      kept[i] = j >= begin && j < end && left > 0 ? key_of(score[j]) : 0u;
+    }
+  }
   if (left > 0) {
     uint32_t prefix = 0;
     for (int shift = 24; shift >= 0; shift -= 8) {
       for (int i = tid; i < 256; i += kChooseThreads) s_count[i] = 0;
       __syncthreads();
-      for (int j = begin + tid; j < end; j += kChooseThreads) {
-        const uint32_t k = key_of(score[j]);
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&s_count[k >> shift & 255], 1);
+      auto count = [&](int j, uint32_t k) {
+        const bool in = j >= begin && j < end && (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)));
+        const unsigned digit = in ? k >> shift & 255u : 256u;
+        const unsigned same = __match_any_sync(0xffffffffu, digit);
+        if (in && lane == __ffs(same) - 1) atomicAdd(&s_count[digit], __popc(same));
+      };
+      if (KEPT) {
+#pragma unroll
+        for (int i = 0; i < kChooseKeys; ++i)
+          if (i * kChooseThreads < end) count(i * kChooseThreads + tid, kept[i]);
+      } else {
+        for (int base = 0; base < end; base += kChooseThreads) count(base + tid, base + tid < end ? key_of(score[base + tid]) : 0u);
       }
       __syncthreads();
       if (tid < 32) {  // the greatest digit with at least `left` pages at or above it; a lane 8 digits
-        int mine = 0;
-        for (int e = 0; e < 8; ++e) mine += s_count[255 - (lane * 8 + e)];
+        int c[8], mine = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          c[e] = s_count[255 - (lane * 8 + e)];
+          mine += c[e];
+        }
         int before = mine;
+#pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int x = __shfl_up_sync(0xffffffffu, before, o);
           if (lane >= o) before += x;
         }
         before -= mine;
-        if (before < left && before + mine >= left)
+        if (before < left && before + mine >= left) {
+#pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int c = s_count[255 - (lane * 8 + e)];
-            if (before < left && before + c >= left) {
+            if (before < left && before + c[e] >= left) {
               s_digit = 255 - (lane * 8 + e);
               s_left = left - before;
             }
-            before += c;
+            before += c[e];
           }
+        }
       }
       __syncthreads();
       prefix |= (uint32_t)s_digit << shift;
       left = s_left;
-      __syncthreads();
     }
     limit = prefix;
   }
   int out = 0, same = 0;  // pages written, pages met at the limit
-  for (int base = 0; base < n; base += kChooseThreads) {
-    const int j = base + tid;
-    const bool among = j >= begin && j < end;
-    const uint32_t k = among && left > 0 ? key_of(score[j]) : 0;
-    const bool equal = among && left > 0 && k == limit;
-    bool in = j < n && (!among || (left > 0 && k > limit));
-    const unsigned eq = __ballot_sync(0xffffffffu, equal);
-    if (lane == 0) s_warp[warp][0] = __popc(eq);
-    __syncthreads();
-    int rank = same + __popc(eq & ((1u << lane) - 1));
-    for (int w = 0; w < kChooseThreads / 32; ++w) {
-      rank += w < warp ? s_warp[w][0] : 0;
-      same += s_warp[w][0];
+  auto take = [&](int i, uint32_t k) {
+    const int j = i * kChooseThreads + tid;
+    const bool among = j >= begin && j < end && left > 0;
+    const bool equal = among && k == limit, more = j < n && (j < begin || j >= end || (among && k > limit));
+    // those with the same key come before this one as far as they are taken: their places are counted apart
+    const unsigned eq = __ballot_sync(0xffffffffu, equal), mo = __ballot_sync(0xffffffffu, more);
+    int(*counts)[2] = s_warp[i & 1];
+    if (lane == 0) {
+      counts[warp][0] = __popc(eq);
+      counts[warp][1] = __popc(mo);
     }
-    in = in || (equal && rank < left);
-    const unsigned got = __ballot_sync(0xffffffffu, in);
-    if (lane == 0) s_warp[warp][1] = __popc(got);
     __syncthreads();
-    int place = out + __popc(got & ((1u << lane) - 1));
-    for (int w = 0; w < kChooseThreads / 32; ++w) {
-      place += w < warp ? s_warp[w][1] : 0;
-      out += s_warp[w][1];
+    int rank = same + __popc(eq & ((1u << lane) - 1)), place = out + __popc(mo & ((1u << lane) - 1));
+    int all_eq = 0, all_mo = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      rank += w < warp ? counts[w][0] : 0;
+      place += w < warp ? counts[w][1] : 0;
+      all_eq += counts[w][0];
+      all_mo += counts[w][1];
     }
-    if (in) {
+    if (more || (equal && rank < left)) {
+      place += min(rank, left);
       a.chosen[at + place] = table[j];
       if (a.pages) a.pages[at + place] = j;
     }
-    __syncthreads();
+    same += all_eq;
+    out += all_mo;
+  };
+  if (KEPT) {
+#pragma unroll
+    for (int i = 0; i < kChooseKeys; ++i)
+      if (i * kChooseThreads < n) take(i, kept[i]);
+  } else {
+    for (int i = 0; i * kChooseThreads < n; ++i) {
+      const int j = i * kChooseThreads + tid;
+      take(i, j >= begin && j < end && left > 0 ? key_of(score[j]) : 0u);
+    }
   }
   for (int i = taken + tid; i < a.n_blocks; i += kChooseThreads) {
     a.chosen[at + i] = -1;
@@ -276,12 +469,20 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(const __grid_con
   }
 }
 
-template <typename C>
-mk_status launch_scores(const ScoreArgs& a, int dtype, int hd, dim3 grid, void* stream) {
-  auto go = [&](auto kernel) { return launch_dependent(kernel, grid, dim3(kScoreThreads), 0, stream, "mk_page_scores", a); };
-  if (dtype == MK_F32) return hd == 64 ? go(scores_kernel<C, float, 64>) : go(scores_kernel<C, float, 128>);
-  if (dtype == MK_F16) return hd == 64 ? go(scores_kernel<C, __half, 64>) : go(scores_kernel<C, __half, 128>);
-  return hd == 64 ? go(scores_kernel<C, __nv_bfloat16, 64>) : go(scores_kernel<C, __nv_bfloat16, 128>);
+template <typename C, typename Q, int HD, bool WIDE, int NQ>
+mk_status launch_scores(const ScoreArgs& a, void* stream) {
+  auto kernel = scores_kernel<C, Q, HD, WIDE, NQ>;
+  constexpr int smem = sizeof(ScoreSmem<C, Q, HD, WIDE, NQ>);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return paged_fail(MK_ERR_CUDA, std::string("mk_page_scores: ") + cudaGetErrorString(e));
+  }
+  return launch_dependent(kernel, dim3((a.width + a.chunk - 1) / a.chunk, a.n_rows), dim3(kScoreThreads), smem, stream, "mk_page_scores", a);
+}
+template <typename C, typename Q, int NQ>
+mk_status launch_scores(const ScoreArgs& a, int hd, void* stream) {
+  if (a.group > 8) return hd == 64 ? launch_scores<C, Q, 64, true, NQ>(a, stream) : launch_scores<C, Q, 128, true, NQ>(a, stream);
+  return hd == 64 ? launch_scores<C, Q, 64, false, NQ>(a, stream) : launch_scores<C, Q, 128, false, NQ>(a, stream);
 }
 
 size_t choice_bytes(long long n_rows, int n_kv_heads, int n_blocks) {
@@ -335,9 +536,26 @@ extern "C" mk_status mk_page_scores(const mk_scores_args* args, const mk_page_vi
     a.table_stride = cache->table_stride; a.n_rows = args->n_rows; a.hkv = cache->n_kv_heads;
     a.group = args->n_heads / cache->n_kv_heads; a.page_size = cache->page_size; a.n_pages = cache->n_pages;
     a.table_rows = cache->n_rows; a.width = cache->table_width;
-    const dim3 grid((a.width + kScoreThreads / 32 - 1) / (kScoreThreads / 32), a.hkv, a.n_rows);
-    return cache->dtype == MK_F16 ? launch_scores<__half>(a, args->dtype, cache->head_dim, grid, stream)
-                                  : launch_scores<__nv_bfloat16>(a, args->dtype, cache->head_dim, grid, stream);
+    const long long per = args->dtype == MK_F32 ? 4 : 8;
+    a.q_vec = aligned_to(a.q, 16) && a.q_row % per == 0 && a.q_head % per == 0;
+    // pages of a CTA: as many as leave two CTAs for every SM, in whole turns of its warps
+    int n_sm = 0;
+    const mk_status s = sm_count(&n_sm);
+    if (s) return s;
+    const int turn = kScorePages * std::max(1, kScoreWarps / a.hkv);
+    const long long want = (long long)a.width * a.n_rows / (2LL * n_sm);
+    a.chunk = (int)std::min<long long>(64, std::max<long long>(1, want / turn) * turn);
+    // queries of the bounds' type are exact in one part, others are split into 2 parts of fp16 (22 bits, each head
+    // at a power of two of its own) or 3 of bf16 (24 bits; fp16 queries: 2, 16 bits and more than their 11)
+    const int d = cache->head_dim;
+    if (cache->dtype == MK_F16) {
+      if (args->dtype == MK_F16) return launch_scores<__half, __half, 1>(a, d, stream);
+      if (args->dtype == MK_BF16) return launch_scores<__half, __nv_bfloat16, 2>(a, d, stream);
+      return launch_scores<__half, float, 2>(a, d, stream);
+    }
+    if (args->dtype == MK_BF16) return launch_scores<__nv_bfloat16, __nv_bfloat16, 1>(a, d, stream);
+    if (args->dtype == MK_F16) return launch_scores<__nv_bfloat16, __half, 2>(a, d, stream);
+    return launch_scores<__nv_bfloat16, float, 3>(a, d, stream);
   });
 }
 
@@ -392,8 +610,10 @@ extern "C" mk_status mk_sparse_attention(const mk_attend_args* attend, const mk_
     const size_t used = choice_bytes(attend->n_rows, cache->n_kv_heads, args->n_blocks);
     x.workspace = static_cast<char*>(attend->workspace) + used;
     x.workspace_bytes = attend->workspace_bytes - used;
-    auto choose = [&]() { return launch_dependent(choose_kernel, dim3(c.n_rows, c.hkv), dim3(kChooseThreads), 0, stream,
-                                                  "mk_sparse_attention (choice)", c); };
+    auto choose = [&]() {
+      return launch_dependent(c.width <= kChooseThreads * kChooseKeys ? choose_kernel<true> : choose_kernel<false>,
+                              dim3(c.n_rows, c.hkv), dim3(kChooseThreads), 0, stream, "mk_sparse_attention (choice)", c);
+    };
     return attend_pages(x, view, args->n_blocks, status, stream, choose);
   });
 }
