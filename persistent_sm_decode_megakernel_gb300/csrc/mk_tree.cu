@@ -206,6 +206,14 @@ __device__ __forceinline__ unsigned ones(int x, int y) {
   return y > x ? to & ~from : 0u;
 }
 
+// cap tanh(x / (2 log2 e)) = cap - 2 cap / (2^x + 1), off by 2^-22 cap: two of the hardware's approximations (2 ulp, 1 ulp) in the
+// place of tanhf's 25 instructions, which took three times a tile's softmax
+__device__ __forceinline__ float capped(float x, float cap) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(x) + 1.f));
+  return fmaf(-2.f * cap, r, cap);
+}
+
 // two sums or products at a time
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -255,6 +263,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     mbar_fence_init();
     fence_proxy_async();
   }
+  // the rows that hold queries, rounded up to whole warps' worth; the others of the blocks stay zero
+  const int first_node = part * SH::BLOCKS * a.nodes_per_block;
+  const int q_rows = PAIR ? 2 * kRows : min(kRows, (min(a.nodes_per_block, a.n_nodes - first_node) * a.group + 31) / 32 * 32);
+  for (int x = q_rows * 8 + tid; x < kRows * 8 && !PAIR; x += kTreeThreads) {
+#pragma unroll
+    for (int y = 0; y < NQ * HALVES; ++y) reinterpret_cast<uint4*>(s_q)[y * kRows * 8 + x] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (!PAIR && tid >= q_rows && tid < kRows) st->scale[tid] = 1.f;
   pdl_wait();
   // ---- this CTA's share of the line
   {
@@ -347,10 +363,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     while (run && next_piece(a, w, p)) {
       if (begun) {  // the queries of a piece to come: to L2 while the one before it is worked on
         constexpr int LINES = HD * (int)sizeof(Q) / 128;
-        const int nodes = min(SH::BLOCKS * a.nodes_per_block, a.n_nodes - part * SH::BLOCKS * a.nodes_per_block);
+        const int nodes = min(SH::BLOCKS * a.nodes_per_block, a.n_nodes - first_node);
         for (int x = lane; x < nodes * a.group * LINES; x += 32) {
           const int y = x / LINES, nd = y / a.group;  // (of both blocks)
-          prefetch_l2_line(static_cast<const Q*>(a.q) + p.r * a.q_row + (long long)(part * SH::BLOCKS * a.nodes_per_block + nd) * a.q_node +
+          prefetch_l2_line(static_cast<const Q*>(a.q) + p.r * a.q_row + (long long)(first_node + nd) * a.q_node +
                            (long long)(p.head * a.group + y - nd * a.group) * a.q_head + x % LINES * (128 / sizeof(Q)));
         }
       }
@@ -474,13 +490,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     const int g = warp >> 2, row = tid & (kGroupThreads - 1);  // warpgroup, row of its block
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;         // this warp's lanes of the tensor memory
     const uint32_t t_s0 = tmem + g * 256 + lanes, t_o = t_s0 + 128;
-    const int first_node = (PAIR ? 2 * part : part) * a.nodes_per_block;
     const int node = first_node + (PAIR ? g * a.nodes_per_block : 0) + node_of(a, row), h = row - node_of(a, row) * a.group;
-    // the rows that hold queries, rounded up to whole warps' worth; the others of the blocks stay zero
-    const int q_rows = PAIR ? 2 * kRows : min(kRows, (min(a.nodes_per_block, a.n_nodes - first_node) * a.group + 31) / 32 * 32);
-    for (int x = q_rows * 8 + tid; x < kRows * 8; x += 2 * kGroupThreads)
-      for (int y = 0; y < NQ * HALVES; ++y) reinterpret_cast<uint4*>(s_q)[y * kRows * 8 + x] = make_uint4(0u, 0u, 0u, 0u);
-    if (row >= q_rows && !PAIR && g == 0) st->scale[row] = 1.f;
     const bool valid = row < a.nodes_per_block * a.group && node < a.n_nodes;
     const bool warp_valid = __any_sync(0xffffffffu, valid);
     unsigned tiles = 0, s_phase = 0;      // tiles of the CTA; a bit per buffer: the next phase of its scores
@@ -490,8 +500,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     bool there = false;
     while (next_piece(a, w, p)) {
       groups_sync();                      // what the last piece left in shared and tensor memory was read
-      if (p.r != row_of)
-        for (int i = tid; i < a.n_nodes; i += 2 * kGroupThreads) st->parents[i] = a.parents[(long long)p.r * a.n_nodes + i];
+      int parent = 0;                     // (asked for before the queries, stored behind them)
+      const bool other_row = p.r != row_of;
+      if (other_row && tid < a.n_nodes) parent = a.parents[(long long)p.r * a.n_nodes + tid];
       // ---- the queries, K-major, 128-byte swizzled; neighbouring lanes take neighbouring chunks of a row.  (What
       // is executed once or twice waits for its instructions: the loop is short, and ends with the rows.)
       {
@@ -555,12 +566,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         for (int i = 0; i < HD / 32; ++i) tmem_st(t_o + 32 * i, zero);
         tmem_wait_st();
       }
-      fence_proxy_async();
+      if (other_row && tid < a.n_nodes) st->parents[tid] = parent;
+      fence_proxy_async_shared();
       tmem_fence_before();
       mbar_arrive(&st->q_full);
       groups_sync();                      // parents and scales are there
       const float scale = kScaled<C, Q> ? st->scale[(PAIR ? g * kRows : 0) + row] : a.scale;
-      if (p.r != row_of) {                // the node's ancestors that its window holds
+      if (other_row) {                    // the node's ancestors that its window holds
         row_of = p.r;
 #pragma unroll
         for (int i = 0; i < 4; ++i) seen[i] = 0;
@@ -606,23 +618,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         unsigned vis[2] = {0, 0};
         if (warp_valid) {
           float factor = scale;
-          if (a.softcap > 0.f) {
-            factor = 1.f;
-#pragma unroll 1
-            for (int x = 0; x < kTile / 16; ++x) {
-              uint32_t y[16];
-              tmem_ld(t_s + 16 * x, y);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(a.softcap * tanhf(__uint_as_float(y[e]) * scale));
-              tmem_st(t_s + 16 * x, y);
-            }
-            tmem_wait_st();
-          }
           uint32_t s[2][32];
           tmem_ld(t_s, s[0]);
           tmem_ld(t_s + 32, s[1]);
           tmem_wait_ld();
+          if (a.softcap > 0.f) {
+            factor = 1.f;
+            const float twice = scale * (2.f * kLog2e);
+#pragma unroll
+            for (int x = 0; x < kTile; ++x)
+              s[x >> 5][x & 31] = __float_as_uint(capped(__uint_as_float(s[x >> 5][x & 31]) * twice, a.softcap));
+          }
           if (partial) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -703,7 +709,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
               atomicOr(&found[slot >> 5], 1u << (slot & 31));
             }
           }
-          fence_proxy_async();
+          fence_proxy_async_shared();
           tile_sync<PAIR>(g);
           const unsigned odd[2] = {found[0], found[1]};
           if (odd[0] | odd[1]) sums_done(buf);
@@ -812,7 +818,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
           }
         } else if (valid) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) keep[(size_t)(d0 + 32 * c + e) * a.part_rows] = __uint_as_float(o[e]);
+          for (int e = 0; e < 32; ++e) keep[(d0 + 32 * c + e) * a.part_rows] = __uint_as_float(o[e]);
         }
       }
       if (p.whole) {
