@@ -52,6 +52,8 @@ struct TreeArgs {
   int parts;                             // CTAs of a share: each takes one block (PAIR: two) of its segments
   int shares;
   int part_rows;                         // rows of a piece in the workspace
+  int tpp;                               // 16s of positions in a page
+  unsigned tpp_inverse;                  // 2^32 / tpp, rounded up
   int box;                               // positions of a copy
   int q_vec, o_vec;                      // 16-byte accesses
   float scale, softcap;                  // scores to units of log 2: scale s, or softcap tanh(scale s)
@@ -83,7 +85,7 @@ struct Walk {
 struct Piece {
   Span sp;
   int r, head, first, count;              // tiles [first, first + count) of the segment's
-  int last_share;                         // the share its segment ends in
+  int last_unit;                          // of its segment
   bool whole;
 };
 __device__ __forceinline__ bool next_piece(const TreeArgs& a, Walk& w, Piece& p) {
@@ -100,7 +102,7 @@ __device__ __forceinline__ bool next_piece(const TreeArgs& a, Walk& w, Piece& p)
     const int seg = w.before + p.head * each, stop = min(w.end, seg + each);
     p.first = max(0, w.at - seg - w.lead);
     p.count = stop - seg - w.lead - p.first;
-    p.last_share = (int)((unsigned)(seg + each - 1) / (unsigned)w.share);
+      p.last_unit = seg + each - 1;
     p.whole = p.count == p.sp.n;
     w.at = stop;
     if (p.count > 0) return true;         // (none: of a segment's lead alone)
@@ -154,6 +156,12 @@ template <typename T>
 constexpr float kSlack = 8.f;             // a maximum may be passed by this much before what is summed is rescaled
 template <>
 constexpr float kSlack<__half> = 5.f;
+
+// the page of a row that a slot lies in: a multiplication of the slot's number in 16s (exact below 2^26, pages of up to 64 of them)
+__device__ __forceinline__ int page_index(const TreeArgs& a, int slot) {
+  const int t = slot >> 4;
+  return a.tpp == 1 ? t : (int)__umulhi((unsigned)t, a.tpp_inverse);
+}
 
 // the node of a block that a row of it is of: row / group, exact for rows below 128 and groups up to 16
 __device__ __forceinline__ int node_of(const TreeArgs& a, int row) { return row * a.group_inverse >> 16; }
@@ -246,6 +254,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int share = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
   if (warp == kCopyWarp) {
+    if (lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &v_map : &k_map) : "memory");
     if (lane < ST) {
       mbar_init(&st->full[lane], 1);
       mbar_init(&st->empty[lane], SH::BLOCKS);
@@ -373,34 +382,41 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       const int boxes = kTile / a.box, half = lane / boxes;  // a lane per copy: 64 dims of some positions
       const int at0 = (p.sp.t0 + p.first) * kTile + lane % boxes * a.box;
       const bool on = half < HALVES;
-      // the page of this lane's part of tile i: n_pages where nothing is to be read, -1 where it is none
-      auto page_of = [&](int i) {
+      // whether anything of this lane's part of tile i is to be read, and the table's entry for it (asked for some tiles
+      // ahead, looked at when it is used)
+      auto read_of = [&](int i) {
         const int t = at0 + i * kTile;
-        if (i >= p.count || !on || t >= p.sp.hi || t + a.box <= p.sp.lo) return a.n_pages;
-        const int page = a.table[(long long)p.sp.trow * a.table_stride + t / a.page_size];
-        if ((unsigned)page < (unsigned)a.n_pages) return page;
-        if (half == 0) report(a.status, MK_ERR_PAGES, PO_TREE, p.r, page);
-        return -1;
+        return i < p.count && on && t < p.sp.hi && t + a.box > p.sp.lo;
       };
+      const int32_t* table = a.table + (long long)p.sp.trow * a.table_stride;
+      auto entry_of = [&](int i) { return read_of(i) ? table[page_index(a, at0 + i * kTile)] : 0; };
       auto copy = [&](const CUtensorMap* map, int i, int page) {
         const int s = loads % ST;
         if (!wait_phase(&st->empty[s], (loads / ST & 1) ^ 1, &st->abort)) return false;
         if (lane == 0) mbar_arrive_expect_tx(&st->full[s], SH::kStage);
         __syncwarp();
         const uint32_t dst = smem_addr(s_kv + s * SH::kStage) + half * kTile * 128 + lane % boxes * a.box * 128;
+        const int t = at0 + i * kTile;
+        const bool there = read_of(i) && (unsigned)page < (unsigned)a.n_pages;
         if (on)  // (a page outside the map: zeros)
-          tma_box_4d(dst, map, 64 * half, page < 0 || page >= a.n_pages ? 0 : (at0 + i * kTile) % a.page_size, p.head,
-                     page < 0 ? a.n_pages : page, &st->full[s]);
+          tma_box_4d(dst, map, 64 * half, there ? t - page_index(a, t) * a.page_size : 0, p.head, there ? page : a.n_pages, &st->full[s]);
         ++loads;
         return true;
       };
       // the pages of the next tiles: the keys' is AHEAD tiles before the values'
       int page[AHEAD + 2];
 #pragma unroll
-      for (int i = 0; i < AHEAD + 1; ++i) page[i] = page_of(i);
+      for (int i = 0; i < AHEAD + 1; ++i) page[i] = entry_of(i);
       auto keys = [&](int i, int pg) {
-        unsigned bad = on && half == 0 && pg < 0 ? ((1u << (a.box / 16)) - 1) << (lane % boxes * (a.box / 16)) : 0u;
-        bad = __reduce_or_sync(0xffffffffu, bad);  // the groups of 16 slots on a bad page
+        const bool none = half == 0 && read_of(i) && (unsigned)pg >= (unsigned)a.n_pages;
+        unsigned bad = 0;
+        if (__any_sync(0xffffffffu, none)) {  // the groups of 16 slots on a bad page
+          if (none) {
+            report(a.status, MK_ERR_PAGES, PO_TREE, p.r, pg);
+            bad = ((1u << (a.box / 16)) - 1) << (lane % boxes * (a.box / 16));
+          }
+          bad = __reduce_or_sync(0xffffffffu, bad);
+        }
         if (lane == 0) st->bad[tiles % 16] = (unsigned char)bad;
         __syncwarp();
         ++tiles;
@@ -413,7 +429,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       if (!begun) wait_phase(&st->q_full, 0, &st->abort);
       begun = true;
       for (int i = 0; i < p.count && run; ++i) {
-        page[AHEAD + 1] = page_of(i + AHEAD + 1);
+        page[AHEAD + 1] = entry_of(i + AHEAD + 1);
         run = copy(&v_map, i, page[0]);
         if (i + AHEAD < p.count) keys(i + AHEAD, page[AHEAD]);
 #pragma unroll
@@ -764,7 +780,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         groups_sync();
       }
       tmem_fence_after();
-      if (tid == 0 && !p.whole && p.first == 0) a.joins[blockIdx.x] = make_int4(share, p.last_share, p.r, p.head);
+      if (tid == 0 && !p.whole && p.first == 0) a.joins[blockIdx.x] = make_int4(share, (int)((unsigned)p.last_unit / (unsigned)w.share), p.r, p.head);
       if (!warp_valid) continue;
       float M = m, L = l, f0 = 1.f, f1 = 0.f;
       if (!PAIR) {
@@ -1057,6 +1073,8 @@ extern "C" mk_status mk_tree_attention(const mk_tree_args* args, const mk_page_v
     a.n_rows = args->n_rows; a.n_nodes = args->n_nodes; a.hq = args->n_heads; a.hkv = cache->n_kv_heads;
     a.group = a.hq / a.hkv; a.window = args->window; a.page_size = cache->page_size; a.n_pages = cache->n_pages;
     a.table_rows = cache->n_rows; a.cap = (int)cap;
+    a.tpp = a.page_size / 16;
+    a.tpp_inverse = a.tpp > 1 ? (unsigned)(((1ULL << 32) + a.tpp - 1) / a.tpp) : 0;
     const Deal d = deal(a.n_nodes, a.group, args->dtype == cache->dtype);
     a.nodes_per_block = d.nodes_per_block; a.blocks = d.blocks; a.parts = d.parts; a.part_rows = d.part_rows;
     a.shares = std::max(1, n_sm / d.parts);
