@@ -65,7 +65,7 @@ __device__ __forceinline__ void tmem_free_all(uint32_t base) {
 #define MK_R8(a, i) a(i), a(i + 1), a(i + 2), a(i + 3), a(i + 4), a(i + 5), a(i + 6), a(i + 7)
 #define MK_O(i) "=r"(r[i])
 #define MK_I(i) "r"(r[i])
-// 32 or 16 columns of the warp's 32 lanes (a lane a row), to and from registers; the reads are there after
+// 32, 16 or 8 columns of the warp's 32 lanes (a lane a row), to and from registers; the reads are there after
 // tmem_wait_ld
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile(
@@ -95,6 +95,10 @@ __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[16]) 
           MK_I, 0),
       MK_R8(MK_I, 8), "r"(addr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::MK_R8(MK_I, 0), "r"(addr)
+               : "memory");
 }
 #undef MK_I
 #undef MK_O

@@ -133,7 +133,7 @@ struct Shape {
     int sums[kTreeThreads / 32][2];
     int parents[kMaxNodes];
     unsigned char bad[16];                // of the last tiles: groups of 16 slots on a bad page
-    unsigned odd[4][2];                   // slots whose values are not all finite, of the last tiles
+    unsigned odd[8][2];                   // slots whose values are not all finite, of the last tiles
     float scale[BLOCKS * kRows];
     float ml[2][kRows][2];
   };
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       // ---- the queries, K-major, 128-byte swizzled; neighbouring lanes take neighbouring chunks of a row.  (What
       // is executed once or twice waits for its instructions: the loop is short, and ends with the rows.)
       {
-        constexpr int CH = HD / 8, STEP = 2 * kGroupThreads / CH, U = NQ == 1 ? 4 : sizeof(Q) == 2 ? 2 : 1;
+        constexpr int CH = HD / 8, STEP = 2 * kGroupThreads / CH, U = PAIR ? 8 : NQ == 1 ? 4 : sizeof(Q) == 2 ? 2 : 1;
         const int c = tid % CH;
         const Q* src = static_cast<const Q*>(a.q) + p.r * a.q_row + (long long)p.head * a.group * a.q_head + 8 * c;
 #pragma unroll 1
@@ -705,9 +705,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         }
         if (partial) {
           // Values that are not finite must not meet the zero of one who does not see them: they are taken
-          // out of the tile and added for those who do.  (A set of them is used again when all who read it are
-          // through its tile: the scores they wait for come after the products of the tiles before.)
-          unsigned* found = st->odd[PAIR ? i & 3 : 2 * g + (turn & 1)];
+          // out of the tile and added for those who do.  (Kept for eight tiles: one warpgroup may be ahead of the
+          // other by what the ring holds, five tiles.)
+          unsigned* found = st->odd[PAIR ? i & 7 : 2 * g + (turn & 1)];
           if (row < 2) found[row] = 0;
           tile_sync<PAIR>(g);
           const unsigned v_at = loads + SH::v_load(i, p.count);
