@@ -638,6 +638,17 @@ mk_status mk_create_paged(const mk_model_desc* desc, const mk_weights* weights, 
 mk_status mk_decode_step_paged(mk_ctx* ctx, const int32_t* tok, const int32_t* pos, const int32_t* rows, int B,
                                int32_t* out_tok, float* logits);
 
+/* One step over trees of drafted tokens, all in device memory: node i of row r is token
+ * tok[r][i] with parent parents[r][i] (mk_tree_attention's), behind the lens[r] cached positions
+ * of table row rows[r] (NULL: row r); its position is lens[r] + the number of its ancestors, its key and
+ * value go to slot lens[r] + i, which needs its page before the call.  n_rows * n_nodes is at most
+ * max_batch.  out_tok [n_rows][n_nodes] (or NULL) receives the argmax after each node, logits
+ * [n_rows][n_nodes][vocab] (or NULL) the logits; what an absent node gets means nothing (its token still has
+ * to be one).  mk_accept_drafts takes the drafts over.  Asynchronous, errors and captures as
+ * mk_decode_step_paged's. */
+mk_status mk_decode_step_tree(mk_ctx* ctx, const int32_t* tok, const int32_t* lens, const int32_t* parents,
+                              const int32_t* rows, int n_rows, int n_nodes, int32_t* out_tok, float* logits);
+
 /* Reads the device status word back (synchronises the stream): MK_OK, or the code found,
  * with its text in mk_last_error.  The word is cleared. */
 mk_status mk_paged_status(int32_t* status, void* stream);

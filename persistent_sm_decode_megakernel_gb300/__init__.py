@@ -205,6 +205,8 @@ mk_create_paged = _fn("mk_create_paged", [ctypes.POINTER(mk_model_desc), ctypes.
                                           ctypes.POINTER(mk_paged_kv), ctypes.POINTER(mk_rope_desc), c_int,
                                           ctypes.POINTER(mk_options), c_void_p, ctypes.POINTER(c_void_p)])
 mk_decode_step_paged = _fn("mk_decode_step_paged", [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p])
+mk_decode_step_tree = _fn("mk_decode_step_tree", [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_void_p,
+                                                  c_void_p])
 mk_paged_status = _fn("mk_paged_status", [c_void_p, c_void_p])
 mk_last_error = _fn("mk_last_error", [], ctypes.c_char_p)
 mk_status_string = _fn("mk_status_string", [c_int], ctypes.c_char_p)

@@ -19,6 +19,7 @@
 #include "mk_plan.h"
 
 #include "mk_paged.cuh"
+#include "mk_tree.h"
 
 using namespace mk;
 
@@ -97,7 +98,7 @@ struct PagedState {
   long long layer_stride = 0;  // elements
   int n_freqs = 0, interleaved = 0;
   float mscale = 1.f;
-  DevBuf staging, qk, freqs, status, work;
+  DevBuf staging, qk, freqs, status, work, places;  // places: positions, slots and table rows of a step over trees
   size_t work_bytes = 0;
 };
 
@@ -718,7 +719,12 @@ mk_status mk_create_paged(const mk_model_desc* desc, const mk_weights* w, const 
     MK_CUDA(cudaMemset(ps->status.p, 0, 16));
     s = mk_paged_attention_workspace(desc->n_heads, desc->n_kv_heads, desc->head_dim, &ps->work_bytes);
     if (s) return s;
+    size_t tree_bytes = 0;
+    s = mk_tree_attention_workspace(desc->max_batch, desc->n_heads, desc->n_kv_heads, desc->head_dim, &tree_bytes);
+    if (s) return s;
+    ps->work_bytes = std::max(ps->work_bytes, tree_bytes);
     MK_CUDA(cudaMalloc(&ps->work.p, ps->work_bytes));
+    MK_CUDA(cudaMalloc(&ps->places.p, 3 * sizeof(int32_t) * desc->max_batch));
     std::vector<void*> stage(desc->n_layers, ps->staging.p);
     const mk_kv kv{stage.data(), stage.data()};
     mk_ctx* c = nullptr;
@@ -735,6 +741,129 @@ mk_status mk_create_paged(const mk_model_desc* desc, const mk_weights* w, const 
   });
 }
 
+}  // extern "C"
+
+namespace {
+
+// The trees of a step: rows of nodes instead of single tokens.
+struct StepTrees {
+  const int32_t *lens, *parents, *rows;  // rows: of the table, or NULL
+  int n_rows, n_nodes;
+};
+
+// One step of a paged context over B tokens at pos of table rows `rows`, or over trees (pos and rows are then the
+// nodes' and go with `slots`).
+mk_status step_paged(mk_ctx* ctx, const int32_t* tok, const int32_t* pos, const int32_t* rows, const StepTrees* trees, int B,
+                     int32_t* out_tok, float* logits, const char* name) {
+  if (ctx->broken) return fail(MK_ERR_STATE, "context needs mk_reset after a device error");
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  MK_CUDA(cudaStreamIsCapturing(ctx->stream, &capture));
+  if (capture != cudaStreamCaptureStatusNone)  // a replay would count its arrivals from the captured step's on
+    return fail(MK_ERR_STATE, std::string(name) + " cannot be captured");
+  Sched* sc = nullptr;
+  mk_status s = get_sched(ctx, B, &sc);
+  if (s) return s;
+  ctx->broken = true;  // until all of it is enqueued
+  const PagedState& ps = *ctx->paged;
+  const ModelShape& m = ctx->m;
+  const int32_t* slots = nullptr;
+  if (trees) {
+    int32_t* places = reinterpret_cast<int32_t*>(ps.places.p);
+    s = tree_places(trees->lens, trees->parents, trees->rows, trees->n_rows, trees->n_nodes, places, places + B, places + 2 * B,
+                    ctx->stream);
+    if (s) return s;
+    pos = places;
+    slots = places + B;
+    rows = places + 2 * B;
+  }
+  DevState S = ctx->st;
+  S.trace = ctx->st.trace;
+  S.trace_cap = ctx->st.trace_cap;
+  S.counters = reinterpret_cast<uint32_t*>(sc->counters.p);
+  S.n_counters = sc->plan.n_counters;
+  StepArgs A{};
+  A.epoch = sc->epoch;
+  A.step = ctx->step;
+  A.B = B;
+  A.flags = SF_TOK_FROM_DEVICE | SF_NO_SYNC | (ctx->opts.trace ? SF_TRACE : 0);
+  for (int b = 0; b < B; ++b) A.seq[b] = b;
+  A.logits = logits;
+  A.tok_hist = out_tok;
+  const void* fn = S.tc ? ctx->kernel_tc : ctx->kernel;
+  int32_t* status = reinterpret_cast<int32_t*>(ps.status.p);
+  if (ctx->opts.trace) MK_CUDA(cudaMemsetAsync(&reinterpret_cast<Ctl*>(ctx->ctl.p)->trace_n, 0, 4, ctx->stream));
+  MK_CUDA(cudaMemcpyAsync(reinterpret_cast<Ctl*>(ctx->ctl.p)->tok, tok, sizeof(int32_t) * B, cudaMemcpyDeviceToDevice,
+                          ctx->stream));
+  for (size_t k = 0; k < sc->ph_instr.size(); ++k) {
+    const int l = (int)((k - 1) / 6);
+    if (k > 0 && (k - 1) % 6 == OP_ATTN - OP_QKV && l < m.L) {
+      float* q = S.act + S.act_off[ACT_Q] + l * S.act_stride[ACT_Q];
+      const float* qk = reinterpret_cast<const float*>(ps.qk.p);
+      const float* kvn = S.act + S.act_off[ACT_KVN] + l * S.act_stride[ACT_KVN];
+      mk_page_view view = ps.view;
+      view.k = static_cast<uint16_t*>(view.k) + l * ps.layer_stride;
+      view.v = static_cast<uint16_t*>(view.v) + l * ps.layer_stride;
+      mk_append_args ap{};
+      ap.q = qk; ap.q_out = q; ap.k = qk + (size_t)m.Hq * m.hd; ap.v = kvn + (size_t)m.Hkv * m.hd;
+      ap.dtype = MK_F32; ap.n_tokens = B; ap.n_heads = m.Hq;
+      ap.o_token = (long long)m.Hq * m.hd;
+      ap.q_token = ap.k_token = (long long)(m.Hq + m.Hkv) * m.hd;
+      ap.v_token = 2LL * m.Hkv * m.hd;
+      ap.q_head = ap.o_head = ap.k_head = ap.v_head = m.hd;
+      ap.positions = pos; ap.rows = rows;
+      ap.freqs = reinterpret_cast<const double*>(ps.freqs.p);
+      ap.n_freqs = ps.n_freqs; ap.interleaved = ps.interleaved; ap.mscale = ps.mscale;
+      s = mk_rope_append_at(&ap, slots, &view, status, ctx->stream);
+      if (s) return s;
+      if (trees) {
+        mk_tree_args ta{};
+        ta.q = q; ta.dtype = MK_F32; ta.n_rows = trees->n_rows; ta.n_nodes = trees->n_nodes; ta.n_heads = m.Hq;
+        ta.q_head = m.hd; ta.q_node = (long long)m.Hq * m.hd; ta.q_row = ta.q_node * trees->n_nodes;
+        ta.out = S.act + S.act_off[ACT_PART] + l * S.act_stride[ACT_PART];
+        ta.o_head = m.hd + kPartExtra; ta.o_node = m.Hq * ta.o_head; ta.o_row = ta.o_node * trees->n_nodes;
+        ta.lens = trees->lens; ta.parents = trees->parents; ta.rows = trees->rows;
+        ta.scale = (float)(1.0 / std::sqrt((double)m.hd));
+        ta.workspace = ps.work.p; ta.workspace_bytes = ps.work_bytes;
+        s = mk_tree_attention(&ta, &view, status, ctx->stream);
+        if (s) return s;
+        continue;
+      }
+      mk_attend_args at{};
+      at.q = q; at.dtype = MK_F32; at.n_rows = B; at.n_heads = m.Hq;
+      at.q_row = (long long)m.Hq * m.hd; at.q_head = m.hd;
+      at.out = S.act + S.act_off[ACT_PART] + l * S.act_stride[ACT_PART];  // one split: [row][head][hd + kPartExtra]
+      at.o_row = (long long)m.Hq * (m.hd + kPartExtra); at.o_head = m.hd + kPartExtra;
+      at.lens = pos; at.len_add = 1; at.rows = rows;
+      at.scale = (float)(1.0 / std::sqrt((double)m.hd));
+      at.workspace = ps.work.p; at.workspace_bytes = ps.work_bytes;
+      s = mk_paged_attention(&at, &view, status, ctx->stream);
+      if (s) return s;
+      continue;
+    }
+    StepArgs Ak = A;
+    if (k == 0) Ak.flags |= SF_RESET_ARGMAX;
+    Ak.instr = reinterpret_cast<const Instr*>(sc->ph_instr[k].p);
+    Ak.q_start = reinterpret_cast<const int32_t*>(sc->ph_qstart[k].p);
+    DevState Sk = S;
+    if (k > 0 && (k - 1) % 6 == 0 && l < m.L) {  // the QKV op: Hq + Hkv heads into qk
+      Sk.Hq = m.Hq + m.Hkv;
+      Sk.act_off[ACT_Q] = ((int64_t)reinterpret_cast<uintptr_t>(ps.qk.p) - (int64_t)reinterpret_cast<uintptr_t>(S.act)) /
+                              (int64_t)sizeof(float) - l * S.act_stride[ACT_Q];
+    }
+    s = launch(ctx, fn, Sk, Ak, false);
+    if (s) return s;
+  }
+  ++sc->epoch;
+  ++ctx->step;
+  ctx->last_B = B;
+  ctx->broken = false;
+  return MK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
 mk_status mk_decode_step_paged(mk_ctx* ctx, const int32_t* tok, const int32_t* pos, const int32_t* rows, int B,
                                int32_t* out_tok, float* logits) {
   return c_entry([&]() -> mk_status {
@@ -742,86 +871,20 @@ mk_status mk_decode_step_paged(mk_ctx* ctx, const int32_t* tok, const int32_t* p
     if (!ctx->paged) return fail(MK_ERR_INVALID, "not a paged context (mk_create_paged)");
     if (!tok || !pos) return fail(MK_ERR_INVALID, "tok/pos NULL");
     if (B < 1 || B > ctx->m.max_batch) return fail(MK_ERR_INVALID, "B out of range");
-    if (ctx->broken) return fail(MK_ERR_STATE, "context needs mk_reset after a device error");
-    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-    MK_CUDA(cudaStreamIsCapturing(ctx->stream, &capture));
-    if (capture != cudaStreamCaptureStatusNone)  // a replay would count its arrivals from the captured step's on
-      return fail(MK_ERR_STATE, "mk_decode_step_paged cannot be captured");
-    Sched* sc = nullptr;
-    mk_status s = get_sched(ctx, B, &sc);
-    if (s) return s;
-    ctx->broken = true;  // until all of it is enqueued
-    const PagedState& ps = *ctx->paged;
-    const ModelShape& m = ctx->m;
-    DevState S = ctx->st;
-    S.trace = ctx->st.trace;
-    S.trace_cap = ctx->st.trace_cap;
-    S.counters = reinterpret_cast<uint32_t*>(sc->counters.p);
-    S.n_counters = sc->plan.n_counters;
-    StepArgs A{};
-    A.epoch = sc->epoch;
-    A.step = ctx->step;
-    A.B = B;
-    A.flags = SF_TOK_FROM_DEVICE | SF_NO_SYNC | (ctx->opts.trace ? SF_TRACE : 0);
-    for (int b = 0; b < B; ++b) A.seq[b] = b;
-    A.logits = logits;
-    A.tok_hist = out_tok;
-    const void* fn = S.tc ? ctx->kernel_tc : ctx->kernel;
-    int32_t* status = reinterpret_cast<int32_t*>(ps.status.p);
-    if (ctx->opts.trace) MK_CUDA(cudaMemsetAsync(&reinterpret_cast<Ctl*>(ctx->ctl.p)->trace_n, 0, 4, ctx->stream));
-    MK_CUDA(cudaMemcpyAsync(reinterpret_cast<Ctl*>(ctx->ctl.p)->tok, tok, sizeof(int32_t) * B, cudaMemcpyDeviceToDevice,
-                            ctx->stream));
-    for (size_t k = 0; k < sc->ph_instr.size(); ++k) {
-      const int l = (int)((k - 1) / 6);
-      if (k > 0 && (k - 1) % 6 == OP_ATTN - OP_QKV && l < m.L) {
-        float* q = S.act + S.act_off[ACT_Q] + l * S.act_stride[ACT_Q];
-        const float* qk = reinterpret_cast<const float*>(ps.qk.p);
-        const float* kvn = S.act + S.act_off[ACT_KVN] + l * S.act_stride[ACT_KVN];
-        mk_page_view view = ps.view;
-        view.k = static_cast<uint16_t*>(view.k) + l * ps.layer_stride;
-        view.v = static_cast<uint16_t*>(view.v) + l * ps.layer_stride;
-        mk_append_args ap{};
-        ap.q = qk; ap.q_out = q; ap.k = qk + (size_t)m.Hq * m.hd; ap.v = kvn + (size_t)m.Hkv * m.hd;
-        ap.dtype = MK_F32; ap.n_tokens = B; ap.n_heads = m.Hq;
-        ap.o_token = (long long)m.Hq * m.hd;
-        ap.q_token = ap.k_token = (long long)(m.Hq + m.Hkv) * m.hd;
-        ap.v_token = 2LL * m.Hkv * m.hd;
-        ap.q_head = ap.o_head = ap.k_head = ap.v_head = m.hd;
-        ap.positions = pos; ap.rows = rows;
-        ap.freqs = reinterpret_cast<const double*>(ps.freqs.p);
-        ap.n_freqs = ps.n_freqs; ap.interleaved = ps.interleaved; ap.mscale = ps.mscale;
-        s = mk_rope_append(&ap, &view, status, ctx->stream);
-        if (s) return s;
-        mk_attend_args at{};
-        at.q = q; at.dtype = MK_F32; at.n_rows = B; at.n_heads = m.Hq;
-        at.q_row = (long long)m.Hq * m.hd; at.q_head = m.hd;
-        at.out = S.act + S.act_off[ACT_PART] + l * S.act_stride[ACT_PART];  // one split: [row][head][hd + kPartExtra]
-        at.o_row = (long long)m.Hq * (m.hd + kPartExtra); at.o_head = m.hd + kPartExtra;
-        at.lens = pos; at.len_add = 1; at.rows = rows;
-        at.scale = (float)(1.0 / std::sqrt((double)m.hd));
-        at.workspace = ps.work.p; at.workspace_bytes = ps.work_bytes;
-        s = mk_paged_attention(&at, &view, status, ctx->stream);
-        if (s) return s;
-        continue;
-      }
-      StepArgs Ak = A;
-      if (k == 0) Ak.flags |= SF_RESET_ARGMAX;
-      Ak.instr = reinterpret_cast<const Instr*>(sc->ph_instr[k].p);
-      Ak.q_start = reinterpret_cast<const int32_t*>(sc->ph_qstart[k].p);
-      DevState Sk = S;
-      if (k > 0 && (k - 1) % 6 == 0 && l < m.L) {  // the QKV op: Hq + Hkv heads into qk
-        Sk.Hq = m.Hq + m.Hkv;
-        Sk.act_off[ACT_Q] = ((int64_t)reinterpret_cast<uintptr_t>(ps.qk.p) - (int64_t)reinterpret_cast<uintptr_t>(S.act)) /
-                                (int64_t)sizeof(float) - l * S.act_stride[ACT_Q];
-      }
-      s = launch(ctx, fn, Sk, Ak, false);
-      if (s) return s;
-    }
-    ++sc->epoch;
-    ++ctx->step;
-    ctx->last_B = B;
-    ctx->broken = false;
-    return MK_OK;
+    return step_paged(ctx, tok, pos, rows, nullptr, B, out_tok, logits, "mk_decode_step_paged");
+  });
+}
+
+mk_status mk_decode_step_tree(mk_ctx* ctx, const int32_t* tok, const int32_t* lens, const int32_t* parents, const int32_t* rows,
+                              int n_rows, int n_nodes, int32_t* out_tok, float* logits) {
+  return c_entry([&]() -> mk_status {
+    if (!ctx) return fail(MK_ERR_INVALID, "ctx is NULL");
+    if (!ctx->paged) return fail(MK_ERR_INVALID, "not a paged context (mk_create_paged)");
+    if (!tok || !lens || !parents) return fail(MK_ERR_INVALID, "tok/lens/parents NULL");
+    if (n_rows < 1 || n_nodes < 1 || (long long)n_rows * n_nodes > ctx->m.max_batch)
+      return fail(MK_ERR_INVALID, "n_rows * n_nodes out of range");
+    const StepTrees trees{lens, parents, rows, n_rows, n_nodes};
+    return step_paged(ctx, tok, nullptr, nullptr, &trees, n_rows * n_nodes, out_tok, logits, "mk_decode_step_tree");
   });
 }
 

@@ -22,6 +22,7 @@
 #include "mk_device.cuh"
 #include "mk_paged.cuh"
 #include "mk_tmem.cuh"
+#include "mk_tree.h"
 
 namespace mk {
 namespace {
@@ -935,6 +936,32 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
   }
 }
 
+// a thread per node
+__global__ void __launch_bounds__(kMaxNodes) places_kernel(const int32_t* lens, const int32_t* parents, const int32_t* rows, int n_nodes,
+                                                            int32_t* positions, int32_t* slots, int32_t* table_rows) {
+  __shared__ int s_parent[kMaxNodes];
+  const int r = blockIdx.x, node = threadIdx.x;
+  pdl_wait();
+  pdl_launch();
+  if (node < n_nodes) s_parent[node] = parents[(long long)r * n_nodes + node];
+  const int len = lens[r];
+  __syncthreads();
+  if (node >= n_nodes) return;
+  int depth = 0, i = node;
+  bool there = len >= 0 && len <= 0x7fffffff - kMaxNodes;
+  while (there) {
+    const int up = s_parent[i];
+    if (up == -1) break;
+    there = up >= 0 && up < i;
+    i = up;
+    ++depth;
+  }
+  const long long at = (long long)r * n_nodes + node;
+  positions[at] = there ? len + depth : -1;
+  slots[at] = there ? len + node : -1;
+  table_rows[at] = rows ? rows[r] : r;
+}
+
 // --------------------------------------------------------------------------------- host
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -1006,6 +1033,13 @@ mk_status launch_tree(TreeArgs& a, const mk_page_view& view, bool pair, void* st
 }
 
 }  // namespace
+
+mk_status tree_places(const int32_t* lens, const int32_t* parents, const int32_t* rows, int n_rows, int n_nodes, int32_t* positions,
+                      int32_t* slots, int32_t* table_rows, void* stream) {
+  return launch_dependent(places_kernel, dim3(n_rows), dim3(kMaxNodes), 0, stream, "the nodes' places", lens, parents, rows, n_nodes,
+                          positions, slots, table_rows);
+}
+
 }  // namespace mk
 
 extern "C" mk_status mk_tree_attention_workspace(int n_nodes, int n_heads, int n_kv_heads, int head_dim, size_t* bytes) {

@@ -283,6 +283,87 @@ class PagedDecoder:
                                        logits.data_ptr() if logits is not None else None), "mk_decode_step_paged")
         return out
 
+    def step_tree(self, tokens, parents, lens, rows=None, logits=None):
+        """One step over trees of drafted tokens (mk_decode_step_tree): device int32 tokens and parents [rows, nodes]
+        behind the first lens [rows] positions of table rows `rows` (default i).  The argmax after each node
+        [rows, nodes]; the nodes' slots need their pages (update).  It runs on self.stream, where its tensors have to be
+        ready; they may be dropped as soon as it returns."""
+        from . import mk_decode_step_tree
+        shape = tuple(parents.shape)
+        if len(shape) != 2:
+            raise ValueError("parents must be [rows, nodes]")
+        for name, t, want, dtype in (("tokens", tokens, shape, torch.int32), ("parents", parents, shape, torch.int32),
+                                     ("lens", lens, shape[:1], torch.int32), ("rows", rows, shape[:1], torch.int32),
+                                     ("logits", logits, shape + (self.dm.cfg.vocab,), torch.float32)):
+            if t is None and name in ("rows", "logits"):
+                continue
+            if tuple(t.shape) != want or t.dtype != dtype or t.device != self.k.device or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor of {want} on {self.k.device}")
+        with torch.cuda.stream(self.stream):
+            for t in (tokens, parents, lens, rows, logits):
+                self._used(t)
+            out = torch.empty(shape, dtype=torch.int32, device=self.k.device)
+            check(mk_decode_step_tree(self.h, tokens.data_ptr(), lens.data_ptr(), parents.data_ptr(),
+                                      rows.data_ptr() if rows is not None else None, shape[0], shape[1], out.data_ptr(),
+                                      logits.data_ptr() if logits is not None else None), "mk_decode_step_tree")
+        return out
+
+    def verify(self, tokens, parents, rows, logits=None):
+        """Reserves pages for trees of drafted tokens, runs one step over them and takes over what the model agrees with
+        (paged.accept_drafts): tokens and parents [len(rows), nodes] for different table rows `rows` (numbers), node 0 of
+        each being the token that stands.  lens of the rows grows.  Returns the next tokens, the accepted nodes (both
+        [len(rows), nodes], -1 behind the last) and their number [len(rows)], on the device; synchronize reports what
+        went wrong there."""
+        n_rows = self.table.shape[0]
+        rows = [int(r) for r in rows]
+        if len(set(rows)) != len(rows) or any(not 0 <= r < n_rows for r in rows):
+            raise ValueError("rows must be different rows of the table")
+        with torch.cuda.stream(self.stream):
+            tokens, parents = self._used(self._int32(tokens)).contiguous(), self._used(self._int32(parents)).contiguous()
+            if tokens.dim() != 2 or tokens.shape[0] != len(rows) or tokens.shape[1] < 1 or parents.shape != tokens.shape:
+                raise ValueError("tokens and parents must be [rows, nodes]")
+            nodes = tokens.shape[1]
+            if len(rows) * nodes > self.dm.max_batch:
+                raise ValueError("rows * nodes must be at most max_batch")
+            reserve = [nodes if r in rows else 0 for r in range(n_rows)]
+            self.update(reserve=reserve)
+            at = self._int32(rows)
+            out = self.step_tree(tokens, parents, self.lens[at.long()], at, logits)
+            every = torch.full((3, n_rows, nodes), -2, dtype=torch.int32, device=self.k.device)   # rows without a tree: absent
+            every[:, at.long()] = torch.stack((tokens, parents, out))
+            accepted = self.paged.accept_drafts(self.k, self.v, self.table, self.lens, *every, status=self.status)
+            return tuple(x[at.long()] for x in accepted)
+
+    def generate(self, prompt, n_new, draft, eos=-1):
+        """Greedy decoding of n_new tokens after one prompt in table row 0 (freed before and after), several of them per
+        step where `draft` guesses them: draft(tokens so far) gives drafted tokens and their parents (lists; a parent is
+        a lower drafted token's number, or -1 for one that follows the tokens so far), as many as fit max_batch - 1.
+        The result is what single steps give, whatever the drafts: (tokens, number of steps); it ends with eos."""
+        n_rows = self.table.shape[0]
+        if n_new < 1 or len(prompt) < 1 or len(prompt) + n_new - 1 > self.max_positions:
+            raise ValueError("the prompt and the new tokens must be positive and fit max_positions")
+        prompt = self._tokens(prompt)
+        keep = list(range(n_rows))
+        with torch.cuda.stream(self.stream):
+            self.update(parents=[-1] + keep[1:])
+            tokens, steps = [int(self.prefill({0: prompt})[0])], 0
+            while len(tokens) < n_new and tokens[-1] != eos:
+                guessed, parents = draft(prompt + tokens)
+                room = min(self.dm.max_batch, self.max_positions - len(prompt) - len(tokens) + 1) - 1
+                guessed, parents = self._tokens(guessed)[:room], [int(p) for p in parents][:room]
+                if len(guessed) != len(parents) or any(not -1 <= p < i for i, p in enumerate(parents)):
+                    raise ValueError("a drafted token's parent must be a lower one's number or -1")
+                got, _, count = self.verify([[tokens[-1]] + guessed], [[-1] + [p + 1 for p in parents]], [0])
+                self.synchronize()
+                steps += 1
+                for t in got[0, : int(count)].tolist():
+                    tokens.append(t)
+                    if t == eos:
+                        break
+            self.update(parents=[-1] + keep[1:])
+            self.synchronize()
+        return tokens[:n_new], steps
+
     def _tokens(self, prompt):
         tokens = [int(t) for t in prompt]
         if any(not 0 <= t < self.dm.cfg.vocab for t in tokens):
