@@ -1074,7 +1074,7 @@ extern "C" mk_status mk_tree_attention(const mk_tree_args* args, const mk_page_v
       return paged_fail(MK_ERR_INVALID, "n_rows * n_nodes * n_heads * head_dim must be in [0, 2^31)");
     if (args->window < 0) return paged_fail(MK_ERR_INVALID, "window must not be negative");
     const float factor = args->softcap > 0.f ? args->scale / args->softcap : args->scale * kLog2e;
-    if (!(args->softcap >= 0.f && args->softcap * kLog2e < INFINITY) || !(std::abs(factor) < INFINITY))
+    if (!(args->softcap >= 0.f && 2.f * args->softcap * kLog2e < INFINITY) || !(std::abs(factor) * 2.f * kLog2e < INFINITY))
       return paged_fail(MK_ERR_INVALID, "scale or softcap is not finite, too large, or softcap negative or too small for scale");
     const size_t esz = args->dtype == MK_F32 ? 4 : 2;
     if (!aligned_to(args->q, esz) || !aligned_to(args->out, esz))

@@ -757,3 +757,189 @@ def test_long_decoding_over_chosen_pages_captured(paged):
             assert np.isfinite(k).all()
     paged.check_status(one.st)
     paged.check_status(two.st)
+
+
+def test_drafted_decoding_of_the_three_operators(paged):
+    """Append into slots, tree attention and acceptance, step after step, as one captured graph: what the accepted path
+    attends to and leaves in the cache is what appending its tokens one by one gives."""
+    g = gen(15)
+    hq, hkv, hd, ps, nodes, steps, L = 8, 2, 64, 16, 7, 12, 1
+    start = [33, 0, 100]
+    R = len(start)
+    width = 20
+    table = ints(torch.randperm(R * width, generator=g, device=DEV).view(R, width).cpu())
+    base = torch.randn(2, L, R * width, hkv, ps, hd, generator=g, device=DEV).half()
+    freqs, m = paged.rope_freqs(10000.0, hd, device=DEV)
+    rng = np.random.default_rng(15)
+    plans = []
+    for s in range(steps):
+        parents = trees(rng, R, nodes, "random")
+        tokens = rng.integers(0, 3, (R, nodes)).tolist()
+        choices = rng.integers(0, 3, (R, nodes)).tolist()
+        plans.append((parents, tokens, choices, torch.randn(R, nodes, hq + 2 * hkv, hd, generator=g, device=DEV).half()))
+
+    class Run:
+        def __init__(self):
+            self.k, self.v, self.n, self.st = base[0].clone(), base[1].clone(), ints(start), status()
+            self.parents, self.tokens, self.choices, self.depth = (torch.zeros(R, nodes, dtype=torch.int32, device=DEV) for _ in range(4))
+            self.x = torch.zeros_like(plans[0][3])
+            self.rows = ints([r for r in range(R) for _ in range(nodes)])
+            self.node = ints([list(range(nodes))] * R)
+
+        def load(self, plan):
+            parents, tokens, choices, x = plan
+            self.parents.copy_(ints(parents))
+            self.tokens.copy_(ints(tokens))
+            self.choices.copy_(ints(choices))
+            self.depth.copy_(ints([[-10 ** 6 if s is None else int(s[9:].sum()) - 1 for s in tree_seen(9, p)] for p in parents]))
+            self.x.copy_(x)
+
+        def step(self):
+            slots, pos = self.n[:, None] + self.node, self.n[:, None] + self.depth
+            x = self.x.view(-1, hq + 2 * hkv, hd)
+            q = paged.rope_append(x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], self.k[0], self.v[0], table, pos.view(-1).contiguous(),
+                                  rows=self.rows, freqs=freqs, mscale=m, slots=slots.view(-1).contiguous(), status=self.st)
+            out, lse = paged.tree_attention(q.view(R, nodes, hq, hd), self.k[0], self.v[0], table, self.n, self.parents, return_lse=True,
+                                            status=self.st)
+            return (out, lse, *paged.accept_drafts(self.k, self.v, table, self.n, self.tokens, self.parents, self.choices, status=self.st))
+
+    one, two = Run(), Run()
+    for r in (one, two):
+        r.load(plans[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = two.step()
+    for x, y in ((two.k, base[0]), (two.v, base[1]), (two.n, ints(start))):
+        x.copy_(y)
+    # the accepted tokens appended one by one, for comparison
+    k, v, n = base[0].clone(), base[1].clone(), list(start)
+    for plan in plans:
+        one.load(plan)
+        two.load(plan)
+        want = one.step()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        parents, tokens, choices, x = plan
+        for r in range(R):
+            path = accept(tokens[r], parents[r], choices[r])
+            assert want[3][r, : len(path)].tolist() == path
+            for i in path:
+                y = x[r, i][None]
+                q = paged.rope_append(y[:, :hq], y[:, hq:hq + hkv], y[:, hq + hkv:], k[0], v[0], table, ints([n[r]]), rows=ints([r]),
+                                      freqs=freqs, mscale=m)
+                n[r] += 1
+                ref, rl = paged.paged_attention(q, k[0], v[0], table, ints([n[r]]), rows=ints([r]), return_lse=True)
+                # both are off by their rounding, 2^-12 of values up to 4, and by that of probabilities, 2^-11 of sum p |v| < 4
+                assert (want[0][r, i].float() - ref[0].float()).abs().max().item() <= 2.0 ** -8
+                assert (want[1][r, i] - rl[0]).abs().max().item() <= 2.0 ** -17
+            t = np.arange(n[r])
+            at = table[r].cpu().numpy()[t // ps]
+            assert torch.equal(one.k[0][at, :, t % ps], k[0][at, :, t % ps]) and torch.equal(one.v[0][at, :, t % ps], v[0][at, :, t % ps])
+        assert one.n.tolist() == n
+    paged.check_status(one.st)
+    paged.check_status(two.st)
+
+
+# ------------------------------------------------------------------------------ refusals
+def _small():
+    pages = torch.zeros(2, 4, 2, 16, 64, dtype=torch.bfloat16, device=DEV)
+    q = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16, device=DEV)
+    bounds = torch.zeros(4, 2, 2, 64, dtype=torch.bfloat16, device=DEV)
+    return pages, q, bounds, ints([[0, 1], [2, 3]]), ints([5, 6]), ints([[-1, 0, 1]] * 2), torch.zeros(2, 2, 2, device=DEV)
+
+
+def test_tensors_that_do_not_fit_are_refused(paged):
+    from persistent_sm_decode_megakernel_gb300 import MkError
+    pages, q, bounds, table, lens, tree, scores = _small()
+    k, v = pages
+    call = lambda f, base: lambda **a: f(**{**base, **a})  # noqa: E731
+    attend_ = call(paged.tree_attention, dict(q=q, k_pages=k, v_pages=v, table=table, lens=lens, parents=tree))
+    accept_ = call(paged.accept_drafts, dict(k=k[None], v=v[None], table=table, lens=lens, tokens=tree, parents=tree, choices=tree))
+    bounds_ = call(paged.update_bounds, dict(k_pages=k, bounds=bounds, table=table, lens=lens))
+    scores_ = call(paged.page_scores, dict(q=q[:, 0], bounds=bounds, table=table, lens=lens, page_size=16))
+    sparse_ = call(paged.sparse_attention, dict(q=q[:, 0], k_pages=k, v_pages=v, table=table, lens=lens, scores=scores, n_blocks=2))
+    append_ = call(paged.rope_append, dict(q=q[:, 0], k=k[:2, :, 0], v=k[:2, :, 0], k_pages=k, v_pages=v, table=table, positions=lens))
+    grown = q.float().requires_grad_()
+    st3 = torch.zeros(3, dtype=torch.int32, device=DEV)
+    for f, bads in ((attend_, (dict(q=q[0]), dict(q=q.double()), dict(q=q[..., :32]), dict(q=grown), dict(q=q.cpu()), dict(q=q.transpose(2, 3)),
+                               dict(lens=lens[:1]), dict(lens=lens.long()), dict(parents=tree[:1]), dict(parents=tree.long()),
+                               dict(parents=tree.t()), dict(parents=tree[:, :2]), dict(out=q.float()), dict(out=q[:1]), dict(rows=lens[:1]),
+                               dict(window=2 ** 40), dict(status=st3), dict(v_pages=v.half()), dict(q=3), dict(lens=None))),
+                    (accept_, (dict(k=k), dict(v=v[None].half()), dict(lens=lens[:1]), dict(tokens=tree[:1]), dict(tokens=tree[0]),
+                               dict(parents=tree[:, :2]), dict(choices=tree.long()), dict(choices=tree.t()), dict(table=table.long()),
+                               dict(status=st3), dict(tokens=tree.cpu()))),
+                    (bounds_, (dict(bounds=bounds[:3]), dict(bounds=bounds.half()), dict(bounds=bounds[:, :, :1]), dict(bounds=bounds.transpose(1, 2)),
+                               dict(bounds=bounds[:1].expand(4, 2, 2, 64)), dict(lens=lens.long()), dict(lens=table), dict(rows=lens[:1]),
+                               dict(new=2 ** 40), dict(k_pages=k.float()), dict(bounds=bounds.float().requires_grad_()))),
+                    (scores_, (dict(q=q), dict(q=q[:, 0].double()), dict(q=q[:1, 0]), dict(q=q[:, 0, :, :32]), dict(bounds=bounds.float()),
+                               dict(bounds=bounds[0]), dict(bounds=bounds.transpose(0, 1)), dict(table=table[0]), dict(lens=lens[:1]),
+                               dict(bounds=bounds.cpu()), dict(q=grown[:, 0]))),
+                    (sparse_, (dict(q=q), dict(scores=scores[:1]), dict(scores=scores[..., :1]), dict(scores=scores.half()), dict(scores=scores.cpu()),
+                               dict(scores=scores.permute(0, 2, 1).contiguous().permute(0, 2, 1)), dict(scores=None), dict(out=q[:, 1].float()),
+                               dict(lens=lens.long()), dict(n_blocks=2 ** 40))),
+                    (append_, (dict(slots=lens.long()), dict(slots=lens[:1]), dict(slots=lens.cpu())))):
+        for bad in bads:
+            with pytest.raises(ValueError):
+                f(**bad)
+    for f, bads in ((attend_, (dict(window=-1), dict(softcap=-2.0), dict(scale=math.nan), dict(q=q[:, :, :3]), dict(q=q[:, :0], parents=tree[:, :0]),
+                               dict(out=q[:1].clone().expand(2, 3, 4, 64)), dict(out=q[:, :1].clone().expand(2, 3, 4, 64)),
+                               dict(out=q[:, :, :1].clone().expand(2, 3, 4, 64)),
+                               dict(q=q[:, :1].expand(2, 129, 4, 64), parents=tree[:, :1].expand(2, 129).contiguous()))),
+                    (accept_, (dict(tokens=tree[:, :0].contiguous(), parents=tree[:, :0].contiguous(), choices=tree[:, :0].contiguous()),)),
+                    (bounds_, (dict(new=0), dict(new=-1))),
+                    (scores_, (dict(page_size=8), dict(page_size=2048), dict(q=q[:, 0, :3]))),
+                    (sparse_, (dict(n_blocks=1), dict(n_blocks=0), dict(first=-1), dict(last=0), dict(first=2), dict(scale=math.inf)))):
+        for bad in bads:
+            with pytest.raises(MkError):
+                f(**bad)
+    assert attend_(q=q[:0], lens=lens[:0], parents=tree[:0]).shape == (0, 3, 4, 64)
+    assert scores_(q=q[:0, 0], lens=lens[:0]).shape == (0, 2, 2)
+    assert sparse_(q=q[:0, 0], lens=lens[:0], scores=scores[:0], return_pages=True)[1].shape == (0, 2, 2)
+    bounds_(lens=lens[:0])
+    with torch.no_grad():
+        attend_(q=grown)
+    torch.cuda.synchronize()
+    assert not pages.any() and not bounds.any() and lens.tolist() == [5, 6]
+
+
+def test_what_is_written_in_place_counts_as_changed(paged):
+    pages, q, bounds, table, lens, tree, scores = _small()
+    k, v, st, out = pages[0].clone(), pages[1].clone(), status(), torch.zeros_like(q)
+    named = dict(k=k, v=v, q=q, bounds=bounds, table=table, lens=lens, tree=tree, scores=scores, st=st, out=out)
+
+    def written(call):
+        before = {n: t._version for n, t in named.items()}
+        call()
+        return {n for n, t in named.items() if t._version > before[n]}
+
+    assert written(lambda: paged.tree_attention(q, k, v, table, lens, tree)) == set()
+    assert written(lambda: paged.tree_attention(q, k, v, table, lens, tree, out=out, status=st)) == {"out", "st"}
+    assert written(lambda: paged.update_bounds(k, bounds, table, lens)) == {"bounds"}
+    assert written(lambda: paged.page_scores(q[:, 0], bounds, table, lens, 16, status=st)) == {"st"}
+    assert written(lambda: paged.sparse_attention(q[:, 0], k, v, table, lens, scores, 2, out=out[:, 0])) == {"out"}
+    assert written(lambda: paged.accept_drafts(k[None], v[None], table, lens, tree, tree, tree)) == {"k", "v", "lens"}
+
+
+def test_one_slot_for_two_tokens_and_slots_that_are_none(paged):
+    """Tokens of one position in slots of their own; slots below 0 or past the table are reported and cache nothing."""
+    from persistent_sm_decode_megakernel_gb300 import MK_ERR_PAGES, MkError
+    pages = torch.zeros(2, 4, 2, 16, 64, dtype=torch.float16, device=DEV)
+    k = torch.randn(3, 2, 64, generator=gen(17), device=DEV).half()
+    freqs, m = paged.rope_freqs(10000.0, 64, device=DEV)
+    st = status()
+    for strided in (k, torch.cat((k, k), -1)[..., 3:67].copy_(k)):      # whole vectors, and element pairs
+        pages.zero_()
+        paged.rope_append(None, strided, strided, pages[0], pages[1], ints([[2, 0]]), ints([9, 9, 9]), rows=ints([0, 0, 0]), freqs=freqs,
+                          slots=ints([20, 9, 31]), status=st)
+        paged.check_status(st)
+        want = torch.zeros_like(pages[0])
+        paged.rope_append(None, k, k, want, torch.zeros_like(want), ints([[0, 1], [1, 2], [2, 3]]), ints([9, 9, 9]), freqs=freqs)
+        for t, (page, at) in enumerate(((0, 4), (2, 9), (0, 15))):
+            assert torch.equal(pages[0][page, :, at], want[t, :, 9]) and torch.equal(pages[1][page, :, at], k[t])
+        for bad in (-1, 32, -2 ** 31, 2 ** 31 - 1):
+            keep = pages.clone()
+            paged.rope_append(None, strided[:1], strided[:1], pages[0], pages[1], ints([[2, 0]]), ints([9]), freqs=freqs, slots=ints([bad]),
+                              status=st)
+            with pytest.raises(MkError) as e:
+                paged.check_status(st)
+            assert e.value.status == MK_ERR_PAGES and torch.equal(pages, keep)
