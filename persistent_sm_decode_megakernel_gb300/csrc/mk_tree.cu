@@ -30,7 +30,8 @@ namespace {
 constexpr int kMaxNodes = 128, kMaxGroup = 16;
 constexpr int kRows = 128;               // rows of a block: the tensor cores' M
 constexpr int kGroupThreads = 128;       // a softmax warpgroup: a thread per row
-constexpr int kTreeThreads = 2 * kGroupThreads + 96;  // two of them, a warp for the copies, one for each one's products
+// two of them, then warps: the copies, each one's products, with SOLO the second one's copies
+__host__ __device__ constexpr int tree_threads(int mode) { return 2 * kGroupThreads + (mode == 2 ? 128 : 96); }
 constexpr int kTile = 64;                // slots that are copied, multiplied and weighted at a time
 constexpr int kMaxStages = 10;
 constexpr int kCopyWarp = 8, kMmaWarp = 9;
@@ -51,8 +52,9 @@ struct TreeArgs {
   int n_rows, n_nodes, hq, hkv, group, window, page_size, n_pages, table_rows, cap;
   int nodes_per_block, blocks;           // blocks of 128 rows that a segment's rows make up
   int parts;                             // CTAs of a share: each takes one block (PAIR: two) of its segments
-  int shares;
+  int shares;                            // of the line of work: one for each CTA of a part (SOLO: two)
   int part_rows;                         // rows of a piece in the workspace
+  int q_rows;                            // rows of a block that hold queries, in whole 32s
   int tpp;                               // 16s of positions in a page
   unsigned tpp_inverse;                  // 2^32 / tpp, rounded up
   int box;                               // positions of a copy
@@ -112,38 +114,51 @@ __device__ __forceinline__ bool next_piece(const TreeArgs& a, Walk& w, Piece& p)
 }
 
 // C: the cache's type.  Q: the queries' and outputs' type.  NQ parts of C make up a query element, NP a
-// probability.  PAIR: the CTA takes two blocks of rows, a warpgroup each, against the same tiles; else one
-// block, the warpgroups taking turns at the tiles and joining at a piece's end.
+// probability.  How the two warpgroups of a CTA work:
+//   PAIR: on two blocks of rows, one each, against the same tiles;
+//   SOLO: on a share of the line each, by themselves, as two CTAs would;
+//   TURNS: on one block, taking turns at the tiles and joining at a piece's end.
 //
 // Tensor memory, 256 columns a warpgroup: 128 of scores, 128 of O.  The scores have two buffers of a tile, so that
 // the tensor cores work on one while the warpgroup is at the other (one buffer where P has three parts: it
 // takes the place of the scores it comes from).
-template <typename C, typename Q, int HD, int NQ, int NP, bool PAIR>
+enum Mode : int { TURNS = 0, PAIR_MODE = 1, SOLO_MODE = 2 };
+template <typename C, typename Q, int HD, int NQ, int NP, int MODE>
 struct Shape {
+  static constexpr bool PAIR = MODE == PAIR_MODE, SOLO = MODE == SOLO_MODE;
   static constexpr int BUFFERS = NP == 3 ? 1 : 2;
-  static constexpr int AHEAD = PAIR ? BUFFERS : 2 * BUFFERS;  // tiles whose scores are asked for before the first values
-  static constexpr int BLOCKS = PAIR ? 2 : 1;
-  static constexpr int kQPart = kRows * HD * 2, kQBytes = BLOCKS * NQ * kQPart;
-  static_assert(kQBytes >= BLOCKS * kRows * HD * (int)sizeof(Q), "the outputs go through the queries' place");
+  static constexpr int AHEAD = MODE == TURNS ? 2 * BUFFERS : BUFFERS;  // tiles whose scores are asked for before the first values
+  static constexpr int BLOCKS = PAIR ? 2 : 1;       // blocks of rows of a piece
+  static constexpr int QUERIES = MODE == TURNS ? 1 : 2;  // places of a block's queries
+  static __host__ __device__ constexpr int q_part(int rows) { return rows * HD * 2; }
+  static __host__ __device__ constexpr int q_bytes(int rows) { return QUERIES * NQ * q_part(rows); }
+  static_assert(NQ * 2 >= (int)sizeof(Q), "the outputs go through the queries' place");
   static constexpr int kStage = kTile * HD * 2;
   struct State {
-    uint64_t full[kMaxStages], empty[kMaxStages], s_full[2][2], p_full[2][2], o_done[2][2], q_full, finished;  // [warpgroup][buffer]
+    uint64_t full[kMaxStages], empty[kMaxStages], s_full[2][2], p_full[2][2], o_done[2][2], q_full[2], q_seen, finished;  // [warpgroup][buffer]
     uint32_t tmem;
     int abort;
-    Walk walk;
-    int sums[kTreeThreads / 32][2];
-    int parents[kMaxNodes];
-    unsigned char bad[16];                // of the last tiles: groups of 16 slots on a bad page
+    Walk walk[2];
+    int sums[tree_threads(MODE) / 32][2];
+    int parents[2][kMaxNodes];
+    unsigned char bad[2][16];                // of the last tiles: groups of 16 slots on a bad page
     unsigned odd[8][2];                   // slots whose values are not all finite, of the last tiles
-    float scale[BLOCKS * kRows];
+    float scale[QUERIES * kRows];
     float ml[2][kRows][2];
   };
-  static constexpr int kRoom = kSmemBytes - 1024 - (int)sizeof(State) - kQBytes;
-  static constexpr int kStages = kRoom / kStage < kMaxStages ? kRoom / kStage : kMaxStages;
+  // stages of a ring: SOLO has two of four; with SOLO only the rows that hold queries have a place (the products read
+  // on over what lies behind it, for rows that nobody looks at)
+  static constexpr int kRoom = kSmemBytes - 1024 - (int)sizeof(State) - q_bytes(kRows);
+  static constexpr int kStages = SOLO ? 4 : kRoom / kStage < kMaxStages ? kRoom / kStage : kMaxStages;
   // (more than half of an SM's: there is one CTA on it, which takes all of the tensor memory)
-  static constexpr int kUsed = 1024 + kQBytes + kStages * kStage + (int)sizeof(State);
-  static constexpr int kBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
-  static_assert(kStages >= 4 && kBytes <= kSmemBytes, "shared memory");
+  static __host__ __device__ constexpr int bytes(int rows) {
+    const int used = 1024 + q_bytes(rows) + (SOLO ? 2 : 1) * kStages * kStage + (int)sizeof(State);
+    return used > 120 * 1024 ? used : 120 * 1024;
+  }
+  static_assert(kStages >= 4 && (SOLO || bytes(kRows) <= kSmemBytes), "shared memory");
+  static_assert(!SOLO || bytes(32) <= kSmemBytes, "shared memory");
+  // what the products of the last row of queries' place read beyond it lies in the ring
+  static_assert(!SOLO || 8 * kStage >= kRows * 128, "shared memory");
   // the place of tile i's keys and values among a piece's `count` tiles' copies: K0 .. K(AHEAD - 1), V0, K(AHEAD), V1, ..
   static __device__ __forceinline__ unsigned k_load(int i) { return i < AHEAD ? i : 2 * i - AHEAD + 1; }
   static __device__ __forceinline__ unsigned v_load(int i, int count) { return i + min(count, AHEAD + i); }
@@ -167,18 +182,26 @@ __device__ __forceinline__ int page_index(const TreeArgs& a, int slot) {
 // the node of a block that a row of it is of: row / group, exact for rows below 128 and groups up to 16
 __device__ __forceinline__ int node_of(const TreeArgs& a, int row) { return row * a.group_inverse >> 16; }
 
-// Waits for a phase of a barrier: a wait that takes too long sets *abort, and from then on none waits.
+// Waits for a phase of a barrier, false where it did not come: a wait that takes too long sets *abort, and from then
+// on none waits: the work goes on over whatever lies there, within its bounds, to its end.  With abort NULL: up to
+// the limit in any case (what is in flight when a CTA ends).
+// A barrier's next phase but one never completes before everyone who waits for a phase has seen it: each is answered by
+// its waiters before it can.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* abort) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long begin = clock64();
   while (!mbar_wait_hint(bar, parity, 100000)) {
-    if (*(volatile int*)abort) return false;
+    if (abort && *(volatile int*)abort) return false;
     if (clock64() - begin > kWaitCycles) {
-      *(volatile int*)abort = 1;
+      if (abort) *(volatile int*)abort = 1;
       return false;
     }
   }
   return true;
+}
+// the same for a whole warp, which goes on together
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* abort) {
+  return __all_sync(0xffffffffu, wait_phase(bar, parity, abort));
 }
 __device__ __forceinline__ void groups_sync() { asm volatile("bar.sync 1, %0;" ::"n"(2 * kGroupThreads) : "memory"); }
 template <bool BOTH>
@@ -240,33 +263,41 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-template <typename C, typename Q, int HD, int NQ, int NP, bool PAIR>
-__global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_constant__ TreeArgs a,
+template <typename C, typename Q, int HD, int NQ, int NP, int MODE>
+__global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __grid_constant__ TreeArgs a,
                                                                 const __grid_constant__ CUtensorMap k_map,
                                                                 const __grid_constant__ CUtensorMap v_map) {
-  using SH = Shape<C, Q, HD, NQ, NP, PAIR>;
+  using SH = Shape<C, Q, HD, NQ, NP, MODE>;
   using State = typename SH::State;
-  constexpr int ST = SH::kStages, HALVES = HD / 64, AHEAD = SH::AHEAD;
+  constexpr bool PAIR = SH::PAIR, SOLO = SH::SOLO;
+  constexpr int ST = SH::kStages, HALVES = HD / 64, AHEAD = SH::AHEAD, kTreeThreads = tree_threads(MODE);
+  constexpr int WORKERS = SOLO ? kGroupThreads : 2 * kGroupThreads;  // softmax threads of a piece
   constexpr uint32_t kType = std::is_same<C, __half>::value ? 0 : 1;
   extern __shared__ unsigned char tree_smem[];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(tree_smem) + 1023) & ~uintptr_t(1023));
-  unsigned char *s_q = base, *s_kv = base + SH::kQBytes;
-  State* st = reinterpret_cast<State*>(s_kv + ST * SH::kStage);
+  const int place_rows = SOLO ? a.q_rows : kRows, q_part = SH::q_part(place_rows);
+  unsigned char *s_q = base, *s_kv = base + SH::q_bytes(place_rows);
+  State* st = reinterpret_cast<State*>(s_kv + (SOLO ? 2 : 1) * ST * SH::kStage);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const int share = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
+  const int part = blockIdx.x % a.parts;
+  // the share of warpgroup g (SOLO: the first of all CTAs come first)
+  auto share_of = [&](int g) { return (int)blockIdx.x / a.parts + (SOLO ? g * (a.shares / 2) : 0); };
   if (warp == kCopyWarp) {
     if (lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &v_map : &k_map) : "memory");
-    if (lane < ST) {
+    constexpr int ALL = (SOLO ? 2 : 1) * ST;
+    if (lane < ALL) {
       mbar_init(&st->full[lane], 1);
       mbar_init(&st->empty[lane], SH::BLOCKS);
-    } else if (lane < ST + 2) {
+    } else if (lane < ALL + 2) {
       for (int b = 0; b < 2; ++b) {
-        mbar_init(&st->s_full[lane - ST][b], 1);
-        mbar_init(&st->p_full[lane - ST][b], kGroupThreads);
-        mbar_init(&st->o_done[lane - ST][b], 1);
+        mbar_init(&st->s_full[lane - ALL][b], 1);
+        mbar_init(&st->p_full[lane - ALL][b], kGroupThreads);
+        mbar_init(&st->o_done[lane - ALL][b], 1);
       }
-    } else if (lane == ST + 2) {
-      mbar_init(&st->q_full, 2 * kGroupThreads);
+    } else if (lane == ALL + 2) {
+      mbar_init(&st->q_full[0], WORKERS);
+      mbar_init(&st->q_full[1], WORKERS);
+      mbar_init(&st->q_seen, 2);
       mbar_init(&st->finished, 2);
       st->abort = 0;
     }
@@ -275,12 +306,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   }
   // the rows that hold queries, rounded up to whole warps' worth; the others of the blocks stay zero
   const int first_node = part * SH::BLOCKS * a.nodes_per_block;
-  const int q_rows = PAIR ? 2 * kRows : min(kRows, (min(a.nodes_per_block, a.n_nodes - first_node) * a.group + 31) / 32 * 32);
-  for (int x = q_rows * 8 + tid; x < kRows * 8 && !PAIR; x += kTreeThreads) {
+  const int q_rows = PAIR ? 2 * kRows : min(place_rows, (min(a.nodes_per_block, a.n_nodes - first_node) * a.group + 31) / 32 * 32);
+  for (int x = q_rows * 8 + tid; x < kRows * 8 && MODE == TURNS; x += kTreeThreads) {
 #pragma unroll
     for (int y = 0; y < NQ * HALVES; ++y) reinterpret_cast<uint4*>(s_q)[y * kRows * 8 + x] = make_uint4(0u, 0u, 0u, 0u);
   }
-  if (!PAIR && tid >= q_rows && tid < kRows) st->scale[tid] = 1.f;
+  if (MODE == TURNS && tid >= q_rows && tid < kRows) st->scale[tid] = 1.f;
   pdl_wait();
   // ---- this CTA's share of the line
   {
@@ -321,19 +352,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     // with a CTA for every tile the latency of a piece is all there is
     const int lead = all_tiles * a.hkv <= a.shares ? 0 : kLead;
     const int units = (all_tiles + all_rows * lead) * a.hkv, each = max(1, (units + a.shares - 1) / a.shares);
-    const int at = min(units, each * share);
-    int b = (ti + ri * lead) * a.hkv;
     const int mine = (tiles + rows * lead) * a.hkv;
-    if (at < units && at >= b && at < b + mine) {
-      for (int r = r0; r < r1; ++r) {
-        const int n = span_of(a, r).n, u = n > 0 ? (n + lead) * a.hkv : 0;
-        if (at >= b && at < b + u) st->walk = Walk{at, min(units, at + each), each, lead, r, b};
-        b += u;
+#pragma unroll
+    for (int g = 0; g < (SOLO ? 2 : 1); ++g) {
+      const int share = share_of(g), at = min(units, each * share);
+      int b = (ti + ri * lead) * a.hkv;
+      if (at < units && at >= b && at < b + mine) {
+        for (int r = r0; r < r1; ++r) {
+          const int n = span_of(a, r).n, u = n > 0 ? (n + lead) * a.hkv : 0;
+          if (at >= b && at < b + u) st->walk[g] = Walk{at, min(units, at + each), each, lead, r, b};
+          b += u;
+        }
       }
-    }
-    if (tid == 0) {
-      if (at >= units) st->walk = Walk{at, at, each, lead, a.n_rows, 0};
-      a.joins[blockIdx.x] = make_int4(0, -1, 0, 0);
+      if (tid == 0) {
+        if (at >= units) st->walk[g] = Walk{at, at, each, lead, a.n_rows, 0};
+        a.joins[share * a.parts + part] = make_int4(0, -1, 0, 0);
+      }
     }
     // rows without slots: zeros; what is not there is reported
     if (all_rows < a.n_rows)
@@ -360,13 +394,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   tmem_fence_after();
   pdl_launch();
   const uint32_t tmem = __shfl_sync(0xffffffffu, st->tmem, 0);
-  Walk w = st->walk;
+  // whose share this warp works on
+  const int own = !SOLO ? 0 : warp < kCopyWarp ? warp >> 2 : warp == kCopyWarp ? 0 : warp == kMmaWarp ? 0 : 1;
+  Walk w = st->walk[own];
   w = Walk{__shfl_sync(0xffffffffu, w.at, 0), __shfl_sync(0xffffffffu, w.end, 0), __shfl_sync(0xffffffffu, w.share, 0),
            __shfl_sync(0xffffffffu, w.lead, 0), __shfl_sync(0xffffffffu, w.row, 0), __shfl_sync(0xffffffffu, w.before, 0)};
+  const int self = share_of(own) * a.parts + part;  // the place of its pieces
   Piece p;
   unsigned loads = 0;                     // tiles of keys or values asked for, or used
 
-  if (warp == kCopyWarp) {
+  s_kv += SOLO ? own * ST * SH::kStage : 0;
+  uint64_t *full = st->full + (SOLO ? own * ST : 0), *empty = st->empty + (SOLO ? own * ST : 0);
+  if (warp == kCopyWarp || (SOLO && warp == kMmaWarp + 2)) {
     // ------------------------------------------------------------------------- copies
     unsigned tiles = 0;
     bool run = true, begun = false;
@@ -393,14 +432,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       auto entry_of = [&](int i) { return read_of(i) ? table[page_index(a, at0 + i * kTile)] : 0; };
       auto copy = [&](const CUtensorMap* map, int i, int page) {
         const int s = loads % ST;
-        if (!wait_phase(&st->empty[s], (loads / ST & 1) ^ 1, &st->abort)) return false;
-        if (lane == 0) mbar_arrive_expect_tx(&st->full[s], SH::kStage);
+        if (!wait_warp(&empty[s], (loads / ST & 1) ^ 1, &st->abort)) return false;
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], SH::kStage);
         __syncwarp();
         const uint32_t dst = smem_addr(s_kv + s * SH::kStage) + half * kTile * 128 + lane % boxes * a.box * 128;
         const int t = at0 + i * kTile;
         const bool there = read_of(i) && (unsigned)page < (unsigned)a.n_pages;
         if (on)  // (a page outside the map: zeros)
-          tma_box_4d(dst, map, 64 * half, there ? t - page_index(a, t) * a.page_size : 0, p.head, there ? page : a.n_pages, &st->full[s]);
+          tma_box_4d(dst, map, 64 * half, there ? t - page_index(a, t) * a.page_size : 0, p.head, there ? page : a.n_pages, &full[s]);
         ++loads;
         return true;
       };
@@ -418,7 +457,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
           }
           bad = __reduce_or_sync(0xffffffffu, bad);
         }
-        if (lane == 0) st->bad[tiles % 16] = (unsigned char)bad;
+        if (lane == 0) st->bad[own][tiles % 16] = (unsigned char)bad;
         __syncwarp();
         ++tiles;
         run = run && copy(&k_map, i, pg);
@@ -427,7 +466,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       for (int i = 0; i < AHEAD; ++i)
         if (i < p.count) keys(i, page[i]);
       // (the first queries do not queue behind the keys and values that fill the ring)
-      if (!begun) wait_phase(&st->q_full, 0, &st->abort);
+      if (!begun) wait_phase(&st->q_full[own], 0, &st->abort);
       begun = true;
       for (int i = 0; i < p.count && run; ++i) {
         page[AHEAD + 1] = entry_of(i + AHEAD + 1);
@@ -438,27 +477,31 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       }
     }
     // every copy has landed before the CTA ends
-    for (unsigned i = loads > ST ? loads - ST : 0; i < loads; ++i) wait_phase(&st->full[i % ST], i / ST & 1, &st->abort);
+    for (unsigned i = loads > ST ? loads - ST : 0; i < loads; ++i) wait_phase(&full[i % ST], i / ST & 1, nullptr);
   } else if (warp >= kMmaWarp) {
     // ----------------------------------------------------------------------- products
     // A warp for each warpgroup: one alone takes longer to issue a job than the tensor cores to do it.  The whole
     // warp walks, so that what the instructions take stays in uniform registers; one lane issues.
     const int g = warp - kMmaWarp;
-    const uint64_t q_desc = smem_desc(smem_addr(s_q) + (PAIR ? g : 0) * NQ * SH::kQPart, 16, 1024);
+    const uint64_t q_desc = smem_desc(smem_addr(s_q) + (MODE == TURNS ? 0 : g) * NQ * q_part, 16, 1024);
     const uint64_t k_desc = smem_desc(smem_addr(s_kv), 16, 1024), v_desc = smem_desc(smem_addr(s_kv), kTile * 128, 1024);
     const uint32_t t_s = tmem + g * 256, t_o = t_s + 128;
     unsigned p_phase = 0, pieces = 0;     // p_phase: a bit per buffer
     while (next_piece(a, w, p)) {
-      const int n = PAIR ? p.count : (p.count - g + 1) / 2;  // jobs: this warpgroup's tiles
-      wait_phase(&st->q_full, pieces & 1, &st->abort);
+      const int n = MODE != TURNS ? p.count : (p.count - g + 1) / 2;  // jobs: this warpgroup's tiles
+      wait_phase(&st->q_full[own], pieces & 1, &st->abort);
       ++pieces;
-      auto tile = [&](int x) { return PAIR ? x : 2 * x + g; };
+      if (MODE == TURNS) {  // (a piece of one tile can be over before the second warp has looked: the next queries wait for both)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&st->q_seen);
+      }
+      auto tile = [&](int x) { return MODE != TURNS ? x : 2 * x + g; };
       // The tensor cores take what one thread issues in order: a buffer's next scores come after the product
       // that read its P.
       auto scores = [&](int x) {
         const unsigned l = loads + SH::k_load(tile(x)), s = l % ST;
         const int b = SH::BUFFERS == 2 ? x & 1 : 0;
-        wait_phase(&st->full[s], l / ST & 1, &st->abort);
+        wait_phase(&full[s], l / ST & 1, &st->abort);
         tmem_fence_after();
         if (elect_one()) {
           const uint64_t kd = k_desc + s * (SH::kStage / 16);
@@ -466,17 +509,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
           for (int y = 0; y < NQ; ++y)
 #pragma unroll
             for (int c = 0; c < HD / 16; ++c)  // (the address counts in 16 bytes)
-              mma_ss(t_s + b * kTile, q_desc + (y * SH::kQPart + (c >> 2) * kRows * 128 + (c & 3) * 32) / 16,
+              mma_ss(t_s + b * kTile, q_desc + (y * q_part + (c >> 2) * place_rows * 128 + (c & 3) * 32) / 16,
                      kd + ((c >> 2) * kTile * 128 + (c & 3) * 32) / 16, mma_desc(kType, false, kRows, kTile), y + c > 0);
           mma_commit(&st->s_full[g][b]);
-          mma_commit(&st->empty[s]);
+          mma_commit(&empty[s]);
         }
         __syncwarp();
       };
       auto values = [&](int x) {
         const unsigned l = loads + SH::v_load(tile(x), p.count), s = l % ST;
         const int b = SH::BUFFERS == 2 ? x & 1 : 0;
-        wait_phase(&st->full[s], l / ST & 1, &st->abort);
+        wait_phase(&full[s], l / ST & 1, &st->abort);
         wait_phase(&st->p_full[g][b], p_phase >> b & 1, &st->abort);
         p_phase ^= 1u << b;
         tmem_fence_after();
@@ -488,7 +531,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             for (int c = 0; c < kTile / 16; ++c)
               mma_ts(t_o, t_s + b * kTile + y * (kTile / 2) + c * 8, vd + c * 2048 / 16, mma_desc(kType, true, kRows, HD), true);
           mma_commit(&st->o_done[g][b]);
-          mma_commit(&st->empty[s]);
+          mma_commit(&empty[s]);
         }
         __syncwarp();
       };
@@ -501,7 +544,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     }
     if (elect_one()) mma_commit(&st->finished);
     __syncwarp();
-    wait_phase(&st->finished, 0, &st->abort);
+    wait_phase(&st->finished, 0, nullptr);
   } else {
     // ------------------------------------------------------------------------ softmax
     const int g = warp >> 2, row = tid & (kGroupThreads - 1);  // warpgroup, row of its block
@@ -510,24 +553,28 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     const int node = first_node + (PAIR ? g * a.nodes_per_block : 0) + node_of(a, row), h = row - node_of(a, row) * a.group;
     const bool valid = row < a.nodes_per_block * a.group && node < a.n_nodes;
     const bool warp_valid = __any_sync(0xffffffffu, valid);
-    unsigned tiles = 0, s_phase = 0;      // tiles of the CTA; a bit per buffer: the next phase of its scores
+    auto workers_sync = [&]() { SOLO ? tile_sync<false>(g) : groups_sync(); };
+    unsigned tiles = 0, s_phase = 0, pieces = 0;  // tiles and pieces so far; a bit per buffer: the next phase of its scores
     int row_of = -1;                      // whose tree `seen` is of
     unsigned seen[4] = {0, 0, 0, 0};
     int depth = 0;
     bool there = false;
+    const int id = SOLO ? row : tid;      // of the piece's threads
     while (next_piece(a, w, p)) {
-      groups_sync();                      // what the last piece left in shared and tensor memory was read
+      workers_sync();                      // what the last piece left in shared and tensor memory was read
+      if (MODE == TURNS && pieces > 0) wait_phase(&st->q_seen, (pieces - 1) & 1, &st->abort);
+      ++pieces;
       int parent = 0;                     // (asked for before the queries, stored behind them)
       const bool other_row = p.r != row_of;
-      if (other_row && tid < a.n_nodes) parent = a.parents[(long long)p.r * a.n_nodes + tid];
+      if (other_row && id < a.n_nodes) parent = a.parents[(long long)p.r * a.n_nodes + id];
       // ---- the queries, K-major, 128-byte swizzled; neighbouring lanes take neighbouring chunks of a row.  (What
       // is executed once or twice waits for its instructions: the loop is short, and ends with the rows.)
       {
-        constexpr int CH = HD / 8, STEP = 2 * kGroupThreads / CH, U = PAIR ? 8 : NQ == 1 ? 4 : sizeof(Q) == 2 ? 2 : 1;
-        const int c = tid % CH;
+        constexpr int CH = HD / 8, STEP = WORKERS / CH, U = PAIR ? 8 : NQ == 1 ? 4 : sizeof(Q) == 2 ? 2 : 1;
+        const int c = id % CH;
         const Q* src = static_cast<const Q*>(a.q) + p.r * a.q_row + (long long)p.head * a.group * a.q_head + 8 * c;
 #pragma unroll 1
-        for (int x0 = tid / CH; x0 < q_rows; x0 += U * STEP) {
+        for (int x0 = id / CH; x0 < q_rows; x0 += U * STEP) {
           Raw8<Q> raw[U];
 #pragma unroll
           for (int z = 0; z < U; ++z) {
@@ -562,7 +609,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 for (int o = 1; o < CH; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
                 const int shift = shift_of(most);
                 up *= power_of(shift);
-                if (c == 0 && x < q_rows) st->scale[x] = a.scale * power_of(-shift);
+                if (c == 0 && x < q_rows) st->scale[(SOLO ? g * kRows : 0) + x] = a.scale * power_of(-shift);
               }
 #pragma unroll
               for (int e = 0; e < 4; ++e) split2<C, NQ>(v[2 * e] * up, v[2 * e + 1] * up, parts[e]);
@@ -570,7 +617,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             if (x < q_rows)
 #pragma unroll
               for (int n = 0; n < NQ; ++n)
-                *reinterpret_cast<uint4*>(s_q + ((x / kRows) * NQ + n) * SH::kQPart + (c >> 3) * kRows * 128 + y * 128 +
+                *reinterpret_cast<uint4*>(s_q + ((SOLO ? g : x / kRows) * NQ + n) * q_part + (c >> 3) * place_rows * 128 + y * 128 +
                                           (((c & 7) ^ (y & 7)) << 4)) = make_uint4(parts[0][n], parts[1][n], parts[2][n], parts[3][n]);
           }
         }
@@ -583,12 +630,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         for (int i = 0; i < HD / 32; ++i) tmem_st(t_o + 32 * i, zero);
         tmem_wait_st();
       }
-      if (other_row && tid < a.n_nodes) st->parents[tid] = parent;
+      if (other_row && id < a.n_nodes) st->parents[own][id] = parent;
       fence_proxy_async_shared();
       tmem_fence_before();
-      mbar_arrive(&st->q_full);
-      groups_sync();                      // parents and scales are there
-      const float scale = kScaled<C, Q> ? st->scale[(PAIR ? g * kRows : 0) + row] : a.scale;
+      mbar_arrive(&st->q_full[own]);
+      workers_sync();                     // parents and scales are there
+      const float scale = kScaled<C, Q> ? st->scale[(MODE != TURNS ? g * kRows : 0) + row] : a.scale;
       if (other_row) {                    // the node's ancestors that its window holds
         row_of = p.r;
 #pragma unroll
@@ -599,7 +646,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
           if (a.window == 0 || depth < a.window)
 #pragma unroll
             for (int x = 0; x < 4; ++x) seen[x] |= (i >> 5) == x ? 1u << (i & 31) : 0u;
-          const int up = st->parents[i];
+          const int up = st->parents[own][i];
           if (up == -1) break;
           there = up >= 0 && up < i;
           i = up;
@@ -623,14 +670,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         tmem_fence_after();
       };
       int turn = 0;                       // tiles of the piece that this warpgroup has taken
-      for (int i = PAIR ? 0 : g; i < p.count; i += PAIR ? 1 : 2, ++turn) {
+      for (int i = MODE != TURNS ? 0 : g; i < p.count; i += MODE != TURNS ? 1 : 2, ++turn) {
         const int t0 = (p.sp.t0 + p.first + i) * kTile;
         const int buf = SH::BUFFERS == 2 ? turn & 1 : 0;
         const uint32_t t_s = t_s0 + buf * kTile;
         wait_phase(&st->s_full[g][buf], s_phase >> buf & 1, &st->abort);
         s_phase ^= 1u << buf;
         tmem_fence_after();
-        const unsigned bad = *(volatile unsigned char*)&st->bad[(tiles + i) % 16];
+        const unsigned bad = *(volatile unsigned char*)&st->bad[own][(tiles + i) % 16];
         const bool partial = t0 < plain_lo || t0 + kTile > min(p.sp.len, p.sp.hi) || bad != 0;
         unsigned vis[2] = {0, 0};
         if (warp_valid) {
@@ -712,7 +759,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
           if (row < 2) found[row] = 0;
           tile_sync<PAIR>(g);
           const unsigned v_at = loads + SH::v_load(i, p.count);
-          wait_phase(&st->full[v_at % ST], v_at / ST & 1, &st->abort);
+          wait_phase(&full[v_at % ST], v_at / ST & 1, &st->abort);
           uint4* v = reinterpret_cast<uint4*>(s_kv + v_at % ST * SH::kStage);
           constexpr int step = PAIR ? 2 * kGroupThreads : kGroupThreads;
 #pragma unroll
@@ -774,17 +821,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         m = -INFINITY;
         l = 0.f;
       }
-      if (!PAIR) {
+      if (MODE == TURNS) {
         st->ml[g][row][0] = m;
         st->ml[g][row][1] = l;
         tmem_fence_before();
         groups_sync();
       }
       tmem_fence_after();
-      if (tid == 0 && !p.whole && p.first == 0) a.joins[blockIdx.x] = make_int4(share, (int)((unsigned)p.last_unit / (unsigned)w.share), p.r, p.head);
+      if (id == 0 && !p.whole && p.first == 0)
+        a.joins[self] = make_int4(share_of(own), (int)((unsigned)p.last_unit / (unsigned)w.share), p.r, p.head);
       if (!warp_valid) continue;
       float M = m, L = l, f0 = 1.f, f1 = 0.f;
-      if (!PAIR) {
+      if (MODE == TURNS) {
         const float m0 = st->ml[0][row][0], m1 = st->ml[1][row][0];
         M = fmaxf(m0, m1);
         const float Ms = M == -INFINITY ? 0.f : M;
@@ -793,17 +841,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         L = fmaf(f0, st->ml[0][row][1], f1 * st->ml[1][row][1]);
       }
       const int slot = p.first == 0;      // 0: continues a segment, 1: begins one
-      float* keep = a.part + (size_t)(blockIdx.x * 2 + slot) * a.part_rows * (HD + 2) + (PAIR ? g * kRows : 0) + row;
+      float* keep = a.part + (size_t)(self * 2 + slot) * a.part_rows * (HD + 2) + (PAIR ? g * kRows : 0) + row;
       const float inv = L == 0.f ? 0.f : 1.f / L;
       // this thread's dims: all of them, or the warpgroup's half.  What is whole goes through the queries' place
       // in shared memory (read by now), a warp's rows in rows of its own, so that whole runs are written.
-      constexpr int DIMS = PAIR ? HD : HD / 2, kRun = DIMS * (int)sizeof(Q), RCH = kRun / 16, kTwist = RCH < 8 ? RCH - 1 : 7;
-      const int d0 = PAIR ? 0 : g * DIMS;
-      unsigned char* run = s_q + ((PAIR ? g : 0) * kRows + (warp & 3) * 32) * HD * sizeof(Q) + (PAIR ? 0 : g) * 32 * kRun;
+      constexpr int DIMS = MODE != TURNS ? HD : HD / 2, kRun = DIMS * (int)sizeof(Q), RCH = kRun / 16, kTwist = RCH < 8 ? RCH - 1 : 7;
+      const int d0 = MODE != TURNS ? 0 : g * DIMS;
+      unsigned char* run = s_q + (MODE != TURNS ? g * NQ * q_part : 0) + (warp & 3) * 32 * HD * (int)sizeof(Q) + (MODE != TURNS ? 0 : g) * 32 * kRun;
 #pragma unroll 1
       for (int c = 0; c < DIMS / 32; ++c) {
         uint32_t o[32];
-        if (PAIR) {
+        if (MODE != TURNS) {
           tmem_ld(t_o + 32 * c, o);
           tmem_wait_ld();
         } else {
@@ -856,7 +904,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
           }
         }
       }
-      if (valid && (PAIR || g == 0)) {
+      if (valid && (MODE != TURNS || g == 0)) {
         if (p.whole) {
           if (a.lse)
             a.lse[((long long)p.r * a.n_nodes + node) * a.hq + p.head * a.group + h] =
@@ -991,7 +1039,7 @@ mk_status page_map(CUtensorMap* map, const mk_page_view& c, void* base, int box)
 // How a call's rows are dealt: blocks of 128, and CTAs that take one (16-bit queries of the cache's type: two)
 // of a share's blocks.
 struct Deal {
-  int nodes_per_block, blocks, parts, part_rows;
+  int nodes_per_block, blocks, parts, part_rows, q_rows;
   bool pair;
 };
 Deal deal(int n_nodes, int group, bool same_type) {
@@ -1001,35 +1049,47 @@ Deal deal(int n_nodes, int group, bool same_type) {
   d.pair = same_type && d.blocks > 1;
   d.parts = d.pair ? (d.blocks + 1) / 2 : d.blocks;
   d.part_rows = d.pair ? 2 * kRows : d.blocks > 1 ? kRows : n_nodes * group;
+  d.q_rows = std::min(kRows, (std::min(n_nodes, d.nodes_per_block) * group + 31) / 32 * 32);
   return d;
 }
 
-template <typename C, typename Q, int HD, int NQ, int NP, bool PAIR>
-mk_status launch_tree(TreeArgs& a, const mk_page_view& view, void* stream) {
-  using SH = Shape<C, Q, HD, NQ, NP, PAIR>;
+template <typename C, typename Q, int HD, int NQ, int NP, int MODE>
+mk_status launch_mode(TreeArgs a, const mk_page_view& view, int n_sm, void* stream) {
+  using SH = Shape<C, Q, HD, NQ, NP, MODE>;
+  const int ctas = std::max(1, n_sm / a.parts) * a.parts;
+  a.shares = ctas / a.parts * (SH::SOLO ? 2 : 1);
   a.box = 16;
   while (a.box < kTile && a.page_size % (2 * a.box) == 0) a.box *= 2;
   CUtensorMap k_map, v_map;
   mk_status s = page_map(&k_map, view, view.k, a.box);
   if (!s) s = page_map(&v_map, view, view.v, a.box);
   if (s) return s;
-  auto kernel = tree_kernel<C, Q, HD, NQ, NP, PAIR>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::kBytes);
+  auto kernel = tree_kernel<C, Q, HD, NQ, NP, MODE>;
+  const int smem = SH::bytes(SH::SOLO ? a.q_rows : kRows);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return paged_fail(MK_ERR_CUDA, std::string("mk_tree_attention: ") + cudaGetErrorString(e));
-  s = launch_dependent(kernel, dim3(a.shares * a.parts), dim3(kTreeThreads), SH::kBytes, stream, "mk_tree_attention", a, k_map, v_map);
+  s = launch_dependent(kernel, dim3(ctas), dim3(tree_threads(MODE)), smem, stream, "mk_tree_attention", a, k_map, v_map);
   if (s) return s;
   return launch_dependent(tree_join_kernel<Q, HD>, dim3(a.shares * a.parts, (a.part_rows + 31) / 32, HD / 32), dim3(kJoinThreads),
                           0, stream, "mk_tree_attention (join)", a, kShift<C>);
 }
-template <typename C, typename Q, int NQ, int NP>
-mk_status launch_tree(TreeArgs& a, const mk_page_view& view, bool pair, void* stream) {
+template <typename C, typename Q, int HD, int NQ, int NP>
+mk_status launch_tree(const TreeArgs& a, const mk_page_view& view, bool pair, int n_sm, void* stream) {
   if constexpr (NQ == 1) {
-    if (pair)
-      return view.head_dim == 64 ? launch_tree<C, Q, 64, NQ, NP, true>(a, view, stream)
-                                 : launch_tree<C, Q, 128, NQ, NP, true>(a, view, stream);
+    if (pair) return launch_mode<C, Q, HD, NQ, NP, PAIR_MODE>(a, view, n_sm, stream);
   }
-  return view.head_dim == 64 ? launch_tree<C, Q, 64, NQ, NP, false>(a, view, stream)
-                             : launch_tree<C, Q, 128, NQ, NP, false>(a, view, stream);
+  // SOLO where there are segments enough for a third of the CTAs (8 nodes, 8 kv heads, bf16: 16 rows of 4500 to 9000
+  // positions 79.6 us, TURNS 98.3; 64 rows 267, 342), TURNS where there are fewer and a piece's latency counts
+  // (one row of 512 positions 12.0 us, SOLO 12.6; one of 32768 38.9, 42.0)
+  const bool solo = 3LL * a.n_rows * a.hkv * a.parts >= n_sm;
+  if (solo && Shape<C, Q, HD, NQ, NP, SOLO_MODE>::bytes(a.q_rows) <= kSmemBytes)
+    return launch_mode<C, Q, HD, NQ, NP, SOLO_MODE>(a, view, n_sm, stream);
+  return launch_mode<C, Q, HD, NQ, NP, TURNS>(a, view, n_sm, stream);
+}
+template <typename C, typename Q, int NQ, int NP>
+mk_status launch_tree(const TreeArgs& a, const mk_page_view& view, bool pair, int n_sm, void* stream) {
+  return view.head_dim == 64 ? launch_tree<C, Q, 64, NQ, NP>(a, view, pair, n_sm, stream)
+                             : launch_tree<C, Q, 128, NQ, NP>(a, view, pair, n_sm, stream);
 }
 
 }  // namespace
@@ -1053,9 +1113,12 @@ extern "C" mk_status mk_tree_attention_workspace(int n_nodes, int n_heads, int n
     int n_sm = 0;
     const mk_status s = sm_count(&n_sm);
     if (s) return s;
-    size_t rows = 0;
-    for (bool same : {false, true}) rows = std::max<size_t>(rows, deal(n_nodes, n_heads / n_kv_heads, same).part_rows);
-    *bytes = (size_t)n_sm * (sizeof(int4) + 2 * rows * (head_dim + 2) * sizeof(float));
+    size_t rows = 0;  // of a CTA's pieces at once: two shares' of one block, or one's of two
+    for (bool same : {false, true}) {
+      const Deal d = deal(n_nodes, n_heads / n_kv_heads, same);
+      rows = std::max<size_t>(rows, d.pair ? d.part_rows : 2 * d.part_rows);
+    }
+    *bytes = (size_t)n_sm * (2 * sizeof(int4) + 2 * rows * (head_dim + 2) * sizeof(float));
     return MK_OK;
   });
 }
@@ -1111,9 +1174,9 @@ extern "C" mk_status mk_tree_attention(const mk_tree_args* args, const mk_page_v
     a.tpp_inverse = a.tpp > 1 ? (unsigned)(((1ULL << 32) + a.tpp - 1) / a.tpp) : 0;
     const Deal d = deal(a.n_nodes, a.group, args->dtype == cache->dtype);
     a.nodes_per_block = d.nodes_per_block; a.blocks = d.blocks; a.parts = d.parts; a.part_rows = d.part_rows;
-    a.shares = std::max(1, n_sm / d.parts);
+    a.q_rows = d.q_rows;
     a.joins = static_cast<int4*>(args->workspace);
-    a.part = reinterpret_cast<float*>(a.joins + n_sm);
+    a.part = reinterpret_cast<float*>(a.joins + 2 * n_sm);
     const long long per = 16 / (long long)esz;
     a.q_vec = aligned_to(a.q, 16) && a.q_row % per == 0 && a.q_node % per == 0 && a.q_head % per == 0;
     a.o_vec = aligned_to(a.out, 16) && a.o_row % per == 0 && a.o_node % per == 0 && a.o_head % per == 0;
@@ -1127,12 +1190,12 @@ extern "C" mk_status mk_tree_attention(const mk_tree_args* args, const mk_page_v
     // bits, each head at a power of two of its own) or 3 of bf16 (24 bits).  A probability has one part where the
     // outputs have 16 bits, and 2 of fp16 or 3 of bf16 where they have 32.
     if (cache->dtype == MK_F16) {
-      if (args->dtype == MK_F16) return launch_tree<__half, __half, 1, 1>(a, *cache, d.pair, stream);
-      if (args->dtype == MK_BF16) return launch_tree<__half, __nv_bfloat16, 2, 1>(a, *cache, d.pair, stream);
-      return launch_tree<__half, float, 2, 2>(a, *cache, d.pair, stream);
+      if (args->dtype == MK_F16) return launch_tree<__half, __half, 1, 1>(a, *cache, d.pair, n_sm, stream);
+      if (args->dtype == MK_BF16) return launch_tree<__half, __nv_bfloat16, 2, 1>(a, *cache, d.pair, n_sm, stream);
+      return launch_tree<__half, float, 2, 2>(a, *cache, d.pair, n_sm, stream);
     }
-    if (args->dtype == MK_BF16) return launch_tree<__nv_bfloat16, __nv_bfloat16, 1, 1>(a, *cache, d.pair, stream);
-    if (args->dtype == MK_F16) return launch_tree<__nv_bfloat16, __half, 2, 1>(a, *cache, d.pair, stream);
-    return launch_tree<__nv_bfloat16, float, 3, 3>(a, *cache, d.pair, stream);
+    if (args->dtype == MK_BF16) return launch_tree<__nv_bfloat16, __nv_bfloat16, 1, 1>(a, *cache, d.pair, n_sm, stream);
+    if (args->dtype == MK_F16) return launch_tree<__nv_bfloat16, __half, 2, 1>(a, *cache, d.pair, n_sm, stream);
+    return launch_tree<__nv_bfloat16, float, 3, 3>(a, *cache, d.pair, n_sm, stream);
   });
 }
