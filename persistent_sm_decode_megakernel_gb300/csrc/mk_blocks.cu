@@ -49,13 +49,15 @@ __device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// A CTA takes one kv head of one page: a thread 16 bytes of every kBoundThreads / (HD / 8)-th key,
-// pairs of elements compared as they lie there; what the threads found is joined in shared memory.
-template <typename C, int HD>
+// A CTA takes HEADS kv heads of one page: a thread 16 bytes of every kBoundThreads / (HD / 8)-th key of each,
+// pairs of elements compared as they lie there; what the threads found is joined in shared memory.  Bound: the keys'
+// bytes; a thread has eight loads in flight, of several heads where a page has few positions (16 prompts of
+// 4096 to 8192 positions in pages of 32, 221 MB).
+template <typename C, int HD, int HEADS>
 __global__ void __launch_bounds__(kBoundThreads) bounds_kernel(const __grid_constant__ BoundArgs a) {
   constexpr int VEC = HD / 8, STEP = kBoundThreads / VEC;
-  __shared__ uint4 s_low[kBoundThreads], s_high[kBoundThreads];
-  const int tid = threadIdx.x, r = blockIdx.x / a.candidates, c = blockIdx.x % a.candidates, head = blockIdx.y;
+  __shared__ uint4 s_low[HEADS][kBoundThreads], s_high[HEADS][kBoundThreads];
+  const int tid = threadIdx.x, r = blockIdx.x / a.candidates, c = blockIdx.x % a.candidates, head = blockIdx.y * HEADS;
   pdl_wait();
   pdl_launch();
   const int trow = a.rows ? a.rows[r] : r, cap = a.width * a.page_size;
@@ -80,27 +82,45 @@ __global__ void __launch_bounds__(kBoundThreads) bounds_kernel(const __grid_cons
   const int held = min(a.page_size, len - j * a.page_size), v = tid % VEC;
   const C* src = static_cast<const C*>(a.k) + page * a.page_stride + (long long)head * a.page_size * HD + v * 8;
   constexpr uint32_t kInf = Pair<C>::kInf, kNeg = kInf | 0x80008000u;
-  uint4 low = make_uint4(kInf, kInf, kInf, kInf), high = make_uint4(kNeg, kNeg, kNeg, kNeg);
-  auto join = [&](const uint4& l, const uint4& h) {
+  auto join = [](uint4& low, uint4& high, const uint4& l, const uint4& h) {
     low = make_uint4(min2<C>(low.x, l.x), min2<C>(low.y, l.y), min2<C>(low.z, l.z), min2<C>(low.w, l.w));
     high = make_uint4(max2<C>(high.x, h.x), max2<C>(high.y, h.y), max2<C>(high.z, h.z), max2<C>(high.w, h.w));
   };
-  constexpr int U = 8;
-  for (int p = tid / VEC; p < held; p += U * STEP) {
-    uint4 x[U];
+  uint4 low[HEADS], high[HEADS];
 #pragma unroll
-    for (int u = 0; u < U; ++u) x[u] = ldg_stream(src + (long long)min(p + u * STEP, held - 1) * HD);  // the last one again: no matter
-#pragma unroll
-    for (int u = 0; u < U; ++u) join(x[u], x[u]);
+  for (int h = 0; h < HEADS; ++h) {
+    low[h] = make_uint4(kInf, kInf, kInf, kInf);
+    high[h] = make_uint4(kNeg, kNeg, kNeg, kNeg);
   }
-  s_low[tid] = low;
-  s_high[tid] = high;
+  constexpr int U = 8 / HEADS;
+  for (int p = tid / VEC; p < held; p += U * STEP) {
+    uint4 x[HEADS][U];
+#pragma unroll
+    for (int h = 0; h < HEADS; ++h)  // past the last key or head: the last one again, no matter
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        x[h][u] = ldg_stream(src + ((long long)min(h, a.hkv - 1 - head) * a.page_size + min(p + u * STEP, held - 1)) * HD);
+#pragma unroll
+    for (int h = 0; h < HEADS; ++h)
+#pragma unroll
+      for (int u = 0; u < U; ++u) join(low[h], high[h], x[h][u], x[h][u]);
+  }
+#pragma unroll
+  for (int h = 0; h < HEADS; ++h) {
+    s_low[h][tid] = low[h];
+    s_high[h][tid] = high[h];
+  }
   __syncthreads();
-  if (tid >= 2 * VEC) return;
-  const bool up = tid >= VEC;
-  for (int y = 0; y < STEP; ++y) join(s_low[y * VEC + v], s_high[y * VEC + v]);
-  C* dst = static_cast<C*>(a.bounds) + (((long long)page * a.hkv + head) * 2 + up) * HD + v * 8;
-  *reinterpret_cast<uint4*>(dst) = up ? high : low;
+  // a thread per head, bound and 16 bytes
+  for (int x = tid; x < HEADS * 2 * VEC; x += kBoundThreads) {
+    const int h = x / (2 * VEC), at = x % VEC;
+    const bool up = x / VEC % 2;
+    if (head + h >= a.hkv) break;
+    uint4 l = s_low[h][at], u = s_high[h][at];
+    for (int y = 1; y < STEP; ++y) join(l, u, s_low[h][y * VEC + at], s_high[h][y * VEC + at]);
+    C* dst = static_cast<C*>(a.bounds) + (((long long)page * a.hkv + head + h) * 2 + up) * HD + at * 8;
+    *reinterpret_cast<uint4*>(dst) = up ? u : l;
+  }
 }
 
 // ------------------------------------------------------------------------------ scores
@@ -163,12 +183,13 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_cons
   if (sub >= subs) return;
   const int32_t* table = a.table + (long long)(len > 0 ? trow : 0) * a.table_stride;
   const int step = subs * kScorePages, first = begin + sub * kScorePages;
-  // the page of this lane's column, -1 where there is none
-  auto page_of = [&](int j, bool tell_bad) {
-    if (j >= min(pages, end)) return -1;
-    const int page = table[j];
-    if ((unsigned)page < (unsigned)a.n_pages) return page;
-    if (tell_bad && c == 0) report(a.status, MK_ERR_PAGES, PO_SCORES, r, page);
+  // the table's entry for this lane's column, asked for some turns ahead, and the page it names, -1 where that is none
+  const int last = min(pages, end);
+  auto entry_of = [&](int j) { return j < last ? table[j] : 0; };
+  auto page_of = [&](int j, int entry, bool tell_bad) {
+    if (j >= last) return -1;
+    if ((unsigned)entry < (unsigned)a.n_pages) return entry;
+    if (tell_bad && c == 0) report(a.status, MK_ERR_PAGES, PO_SCORES, r, entry);
     return -1;
   };
   for (int head = warp % per; head < a.hkv; head += per) {
@@ -181,31 +202,36 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_cons
       for (int i = 0; i < I; ++i)
         raw[i] = page >= 0 ? ldg_stream(b0 + (long long)page * a.hkv * 2 * HD + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
     };
-    int page = page_of(first + g, head == 0), ahead = page_of(first + step + g, head == 0);
-    if (first < pages) load(page);
+    const int entry = entry_of(first + g);
+    int ahead = entry_of(first + step + g), page = -1;
     // ---- the queries' fragments: chunk i, lane (g, c): elements [32 i + 8 c, + 8) of head g
     if (first < pages) {
       __syncwarp();
 #pragma unroll 1
       for (int rh = 0; rh < RH; ++rh) {
         const int h = g + 8 * rh;
-        auto get = [&](int i, float (&v)[8]) {
-          Raw8<Q> x = {};
+        Raw8<Q> x[I / 2];
+#pragma unroll
+        for (int i = 0; i < I / 2; ++i) {
+          x[i] = {};
           if (h < a.group) {
             if (a.q_vec)
-              x.load(q0 + h * a.q_head + 32 * i);
+              x[i].load(q0 + h * a.q_head + 32 * i);
             else
-              x.gather(q0 + h * a.q_head + 32 * i);
+              x[i].gather(q0 + h * a.q_head + 32 * i);
           }
-          x.up(v);
-        };
+        }
+        if (rh == 0) {  // (the first bounds go out behind the queries)
+          page = page_of(first + g, entry, head == 0);
+          load(page);
+        }
         float up = 1.f;
         if constexpr (kScaled<C, Q>) {
           float most = 0.f;
 #pragma unroll
           for (int i = 0; i < I / 2; ++i) {
             float v[8];
-            get(i, v);
+            x[i].up(v);
 #pragma unroll
             for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(v[e]));
           }
@@ -218,14 +244,14 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_cons
 #pragma unroll
         for (int i = 0; i < I / 2; ++i) {
           float v[8];
-          get(i, v);
+          x[i].up(v);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t w[4][NQ];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float x = v[2 * e] * up, y = v[2 * e + 1] * up;
-              split2<C, NQ>((half ? x > 0.f : x < 0.f) || x != x ? x : 0.f, (half ? y > 0.f : y < 0.f) || y != y ? y : 0.f, w[e]);
+              const float y = v[2 * e] * up, z = v[2 * e + 1] * up;
+              split2<C, NQ>((half ? y > 0.f : y < 0.f) || y != y ? y : 0.f, (half ? z > 0.f : z < 0.f) || z != z ? z : 0.f, w[e]);
             }
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
@@ -242,8 +268,8 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_cons
 #pragma unroll
         for (int i = 0; i < I; ++i) now[i] = raw[i];
         const int mine = page;
-        page = ahead;
-        ahead = page_of(j0 + 2 * step + g, head == 0);
+        page = page_of(j0 + step + g, ahead, head == 0);
+        ahead = entry_of(j0 + 2 * step + g);
         if (j0 + step < pages) load(page);
         constexpr int SETS = WIDE ? NQ : (NQ + 1) / 2;
         float d[SETS][2][4];
@@ -341,7 +367,7 @@ __device__ __forceinline__ uint32_t key_of(float x) { return orderable(x != x ? 
 template <bool KEPT>
 __global__ void __launch_bounds__(kChooseThreads) choose_kernel(const __grid_constant__ ChooseArgs a) {
   constexpr int W = kChooseThreads / 32;
-  __shared__ int s_count[256], s_warp[2][W][2], s_digit, s_left;
+  __shared__ int s_count[256], s_warp[2][W][2], s_digit, s_left, s_whole;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.x, head = blockIdx.y;
   pdl_wait();
   pdl_launch();
@@ -365,6 +391,7 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(const __grid_con
   const int begin = n > a.n_blocks ? a.first : 0, end = n > a.n_blocks ? n - a.last : 0;  // pages that are chosen among
   int left = n > a.n_blocks ? a.n_blocks - a.first - a.last : 0;                            // how many of them
   uint32_t limit = 0xffffffffu;  // above it: taken; at it: the first `left`
+  bool whole = false;            // at or above it: taken
   uint32_t kept[KEPT ? kChooseKeys : 1];
   if (KEPT) {
 #pragma unroll
@@ -412,6 +439,7 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(const __grid_con
             if (before < left && before + c[e] >= left) {
               s_digit = 255 - (lane * 8 + e);
               s_left = left - before;
+              s_whole = c[e] == left - before;
             }
             before += c[e];
           }
@@ -420,6 +448,9 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(const __grid_con
       __syncthreads();
       prefix |= (uint32_t)s_digit << shift;
       left = s_left;
+      // all that share the bytes so far are taken: nothing is left to tell apart
+      whole = s_whole;
+      if (whole) break;
     }
     limit = prefix;
   }
@@ -427,7 +458,8 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(const __grid_con
   auto take = [&](int i, uint32_t k) {
     const int j = i * kChooseThreads + tid;
     const bool among = j >= begin && j < end && left > 0;
-    const bool equal = among && k == limit, more = j < n && (j < begin || j >= end || (among && k > limit));
+    const bool equal = among && !whole && k == limit;
+    const bool more = j < n && (j < begin || j >= end || (among && (whole ? k >= limit : k > limit)));
     // those with the same key come before this one as far as they are taken: their places are counted apart
     const unsigned eq = __ballot_sync(0xffffffffu, equal), mo = __ballot_sync(0xffffffffu, more);
     int(*counts)[2] = s_warp[i & 1];
@@ -473,10 +505,9 @@ template <typename C, typename Q, int HD, bool WIDE, int NQ>
 mk_status launch_scores(const ScoreArgs& a, void* stream) {
   auto kernel = scores_kernel<C, Q, HD, WIDE, NQ>;
   constexpr int smem = sizeof(ScoreSmem<C, Q, HD, WIDE, NQ>);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return paged_fail(MK_ERR_CUDA, std::string("mk_page_scores: ") + cudaGetErrorString(e));
-  }
+  static SmemLimit limit;
+  const mk_status s = smem > 48 * 1024 ? limit.raise(kernel, smem, "mk_page_scores") : MK_OK;
+  if (s) return s;
   return launch_dependent(kernel, dim3((a.width + a.chunk - 1) / a.chunk, a.n_rows), dim3(kScoreThreads), smem, stream, "mk_page_scores", a);
 }
 template <typename C, typename Q, int NQ>
@@ -510,10 +541,19 @@ extern "C" mk_status mk_update_bounds(const mk_bounds_args* args, const mk_page_
     if (args->n_rows < 0 || (long long)args->n_rows * a.candidates > 0x7fffffffLL)
       return paged_fail(MK_ERR_INVALID, "n_rows * the pages of n_new positions must be in [0, 2^31)");
     if (args->n_rows == 0) return MK_OK;
-    const dim3 grid(a.n_rows * a.candidates, a.hkv);
+    // two heads to a CTA where a page's keys of one are no eight loads of a thread, and CTAs are many
+    int n_sm = 0;
+    const mk_status s = sm_count(&n_sm);
+    if (s) return s;
+    const bool two = a.page_size * cache->head_dim < 8192 && (long long)a.n_rows * a.candidates * a.hkv >= 64LL * n_sm;
+    const dim3 grid(a.n_rows * a.candidates, two ? (a.hkv + 1) / 2 : a.hkv);
     auto go = [&](auto kernel) { return launch_dependent(kernel, grid, dim3(kBoundThreads), 0, stream, "mk_update_bounds", a); };
-    if (cache->dtype == MK_F16) return cache->head_dim == 64 ? go(bounds_kernel<__half, 64>) : go(bounds_kernel<__half, 128>);
-    return cache->head_dim == 64 ? go(bounds_kernel<__nv_bfloat16, 64>) : go(bounds_kernel<__nv_bfloat16, 128>);
+    auto typed = [&](auto zero) {
+      using C = decltype(zero);
+      if (cache->head_dim == 64) return two ? go(bounds_kernel<C, 64, 2>) : go(bounds_kernel<C, 64, 1>);
+      return two ? go(bounds_kernel<C, 128, 2>) : go(bounds_kernel<C, 128, 1>);
+    };
+    return cache->dtype == MK_F16 ? typed(__half()) : typed(__nv_bfloat16());
   });
 }
 

@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <exception>
 #include <string>
 #include <type_traits>
@@ -67,6 +68,21 @@ inline mk_status launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 blo
   if (e != cudaSuccess) return paged_fail(MK_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
   return MK_OK;
 }
+
+// A kernel's limit of dynamic shared memory, raised once per device (a microsecond of a call's host time)
+struct SmemLimit {
+  std::atomic<bool> done[64] = {};
+  template <typename K>
+  mk_status raise(K kernel, int bytes, const char* what) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev < 64 && done[dev]) return MK_OK;
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return paged_fail(MK_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+    if (dev < 64) done[dev] = true;
+    return MK_OK;
+  }
+};
 
 // multiprocessors of the current device (looked up once per device)
 mk_status sm_count(int* n);

@@ -341,7 +341,10 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const int64_t n = q.size(0), nodes = q.size(1), hq = q.size(2);
     nodes_of(q, "q", q.sizes(), q.scalar_type(), dev, &x.q_row, &x.q_node, &x.q_head);
     const c10::cuda::CUDAGuard guard(dev);
-    const at::Tensor out = a[10] == Py_None ? Fresh::one(q.sizes(), q.scalar_type(), dev) : tensor(a[10], "out");
+    const int with_lse = PyObject_IsTrue(a[11]);
+    // the results share one allocation (the first one's bytes are a multiple of 128)
+    Fresh fresh((a[10] == Py_None ? q.numel() * (int64_t)q.element_size() : 0) + (with_lse > 0 ? 4 * n * nodes * hq : 0), dev);
+    const at::Tensor out = a[10] == Py_None ? fresh.take(q.sizes(), q.scalar_type()) : tensor(a[10], "out");
     nodes_of(out, "out", q.sizes(), q.scalar_type(), dev, &x.o_row, &x.o_node, &x.o_head);
     x.q = q.data_ptr();
     x.out = out.data_ptr();
@@ -354,10 +357,9 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     x.scale = a[7] == Py_None ? (float)(1.0 / std::sqrt((double)view.head_dim)) : (float)number(a[7]);
     x.softcap = (float)number(a[8]);
     x.window = integer(a[9], "window");
-    const int with_lse = PyObject_IsTrue(a[11]);
     at::Tensor lse;
     if (with_lse > 0) {
-      lse = Fresh::one({n, nodes, hq}, at::kFloat, dev);
+      lse = fresh.take({n, nodes, hq}, at::kFloat);
       x.lse = lse.data_ptr<float>();
     }
     int32_t* status = status_of(a[12], dev);
@@ -400,7 +402,15 @@ PyObject* sparse_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     y.first = integer(a[8], "first");
     y.last = integer(a[9], "last");
     const c10::cuda::CUDAGuard guard(dev);
-    const at::Tensor out = a[12] == Py_None ? Fresh::one(q.sizes(), q.scalar_type(), dev) : tensor(a[12], "out");
+    const int with_lse = PyObject_IsTrue(a[13]), with_pages = PyObject_IsTrue(a[14]);
+    check(mk_sparse_attention_workspace(size32(n, "rows"), size32(hq, "heads"), view.n_kv_heads, view.head_dim, y.n_blocks,
+                                        &x.workspace_bytes),
+          "mk_sparse_attention_workspace");
+    // the results share one allocation (the first one's bytes are a multiple of 128)
+    Fresh fresh((a[12] == Py_None ? q.numel() * (int64_t)q.element_size() : 0) + (with_lse > 0 ? 4 * n * hq : 0) +
+                    (with_pages > 0 ? 4 * n * view.n_kv_heads * (int64_t)y.n_blocks : 0),
+                dev);
+    const at::Tensor out = a[12] == Py_None ? fresh.take(q.sizes(), q.scalar_type()) : tensor(a[12], "out");
     heads_of(out, "out", n, hq, view.head_dim, q.scalar_type(), dev, &x.o_row, &x.o_head);
     x.q = q.data_ptr();
     x.out = out.data_ptr();
@@ -410,17 +420,14 @@ PyObject* sparse_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     x.rows = int32s(a[7], "rows", dev, n, -1, true);
     x.scale = a[10] == Py_None ? (float)(1.0 / std::sqrt((double)view.head_dim)) : (float)number(a[10]);
     x.softcap = (float)number(a[11]);
-    const int with_lse = PyObject_IsTrue(a[13]), with_pages = PyObject_IsTrue(a[14]);
     at::Tensor lse, pages;
     if (with_lse > 0) {
-      lse = Fresh::one({n, hq}, at::kFloat, dev);
+      lse = fresh.take({n, hq}, at::kFloat);
       x.lse = lse.data_ptr<float>();
     }
     int32_t* status = status_of(a[15], dev);
-    check(mk_sparse_attention_workspace(x.n_rows, x.n_heads, view.n_kv_heads, view.head_dim, y.n_blocks, &x.workspace_bytes),
-          "mk_sparse_attention_workspace");
     if (with_pages > 0) {
-      pages = Fresh::one({n, view.n_kv_heads, y.n_blocks}, at::kInt, dev);
+      pages = fresh.take({n, view.n_kv_heads, y.n_blocks}, at::kInt);
       y.pages = pages.data_ptr<int32_t>();
     }
     if (n > 0) {

@@ -246,6 +246,22 @@ __device__ __forceinline__ float capped(float x, float cap) {
   return fmaf(-2.f * cap, r, cap);
 }
 
+// The same for 32-bit outputs, off by 2^-23 cap at most and by 2^-23 of itself up to a third of the cap: small ones by the
+// series of tanh (through x^11), the others with one step of Newton's behind the reciprocal's approximation.
+__device__ __forceinline__ float capped_fine(float x, float cap) {
+  const float d = ex2(x * (2.f * kLog2e)) + 1.f;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  r = d < 1e30f ? r * fmaf(-d, r, 2.f) : 0.f;
+  const float q = x * x;
+  float t = fmaf(q, -1382.f / 155925.f, 62.f / 2835.f);
+  t = fmaf(q, t, -17.f / 315.f);
+  t = fmaf(q, t, 2.f / 15.f);
+  t = fmaf(q, t, -1.f / 3.f);
+  t = fmaf(q * x, t, x);
+  return q < 0.09f ? cap * t : fmaf(-2.f * cap, r, cap);
+}
+
 // two sums or products at a time
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -691,7 +707,9 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
             const float twice = scale * (2.f * kLog2e);
 #pragma unroll
             for (int x = 0; x < kTile; ++x)
-              s[x >> 5][x & 31] = __float_as_uint(capped(__uint_as_float(s[x >> 5][x & 31]) * twice, a.softcap));
+              s[x >> 5][x & 31] = __float_as_uint(std::is_same<Q, float>::value
+                                                      ? capped_fine(__uint_as_float(s[x >> 5][x & 31]) * scale, a.softcap)
+                                                      : capped(__uint_as_float(s[x >> 5][x & 31]) * twice, a.softcap));
           }
           if (partial) {
 #pragma unroll
@@ -1066,8 +1084,9 @@ mk_status launch_mode(TreeArgs a, const mk_page_view& view, int n_sm, void* stre
   if (s) return s;
   auto kernel = tree_kernel<C, Q, HD, NQ, NP, MODE>;
   const int smem = SH::bytes(SH::SOLO ? a.q_rows : kRows);
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return paged_fail(MK_ERR_CUDA, std::string("mk_tree_attention: ") + cudaGetErrorString(e));
+  static SmemLimit limit;
+  s = limit.raise(kernel, SH::SOLO ? kSmemBytes : smem, "mk_tree_attention");
+  if (s) return s;
   s = launch_dependent(kernel, dim3(ctas), dim3(tree_threads(MODE)), smem, stream, "mk_tree_attention", a, k_map, v_map);
   if (s) return s;
   return launch_dependent(tree_join_kernel<Q, HD>, dim3(a.shares * a.parts, (a.part_rows + 31) / 32, HD / 32), dim3(kJoinThreads),
