@@ -51,8 +51,9 @@ __device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
 
 // A CTA takes HEADS kv heads of one page: a thread 16 bytes of every kBoundThreads / (HD / 8)-th key of each,
 // pairs of elements compared as they lie there; what the threads found is joined in shared memory.  Bound: the keys'
-// bytes; a thread has eight loads in flight, of several heads where a page has few positions (16 prompts of
-// 4096 to 8192 positions in pages of 32, 221 MB).
+// bytes; a thread has eight loads in flight, of two heads where a page has few positions (16 prompts of 4096 to
+// 8192 positions in pages of 32, 221 MB: 33.9 us, 6.5 TB/s; one head to a CTA 40.5); of a step's one page a row the
+// chain from the length over the table to the keys (2.8 us).
 template <typename C, int HD, int HEADS>
 __global__ void __launch_bounds__(kBoundThreads) bounds_kernel(const __grid_constant__ BoundArgs a) {
   constexpr int VEC = HD / 8, STEP = kBoundThreads / VEC;
@@ -149,7 +150,9 @@ __device__ __forceinline__ float max_nan(float x, float y) {
 // fragments come straight from memory, 16 bytes a lane, as the elements may be summed in any order the two
 // operands share.  The lower and the upper half are summed apart, in two chains.  Where a sum is not finite (an
 // infinite bound times the zero of the other sign) the warp takes those pages once more without the tensor
-// cores.  Bound: the bounds' bytes (16 rows of 1024 to 2048 pages of 16 positions, 105 MB).
+// cores.  Bound: the bounds' bytes (16
+// rows of 1024 to 2048 pages of 16 positions, 105 MB: 21.6 us, 4.9 TB/s; warps that multiplied on CUDA cores and added
+// up through the lanes took 84); of one row the chain from the length over the table to the bounds (3.5 us).
 template <typename C, typename Q, int HD, bool WIDE, int NQ>
 struct ScoreSmem {
   static constexpr int I = HD / 16;        // chunks of 32 elements of both halves
@@ -158,7 +161,7 @@ struct ScoreSmem {
   float scale[kScoreWarps][16];
 };
 template <typename C, typename Q, int HD, bool WIDE, int NQ>
-__global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_constant__ ScoreArgs a) {
+__global__ void __launch_bounds__(kScoreThreads, 2) scores_kernel(const __grid_constant__ ScoreArgs a) {
   using SM = ScoreSmem<C, Q, HD, WIDE, NQ>;
   constexpr int I = SM::I, RH = SM::RH;
   extern __shared__ __align__(16) unsigned char score_smem[];
@@ -363,7 +366,8 @@ __device__ __forceinline__ uint32_t key_of(float x) { return orderable(x != x ? 
 // One CTA per row and kv head: the key of the last page to be taken by its bytes, from the top (a count of
 // the pages that share the bytes found so far, 256 counters a turn; equal bytes of a warp count at once, as the
 // first bytes of most scores are), then the pages in order: all with a greater key and the first of those
-// with the same.  Keys of up to kChooseThreads * kChooseKeys pages stay in registers.
+// with the same.  Keys of up to kChooseThreads * kChooseKeys pages stay in registers.  Bound: latency, some barriers
+// a byte (128 segments of 512 to 1024 pages: about 5 of the 56 us of the whole call; one launch before the attention's).
 template <bool KEPT>
 __global__ void __launch_bounds__(kChooseThreads) choose_kernel(const __grid_constant__ ChooseArgs a) {
   constexpr int W = kChooseThreads / 32;
@@ -578,13 +582,14 @@ extern "C" mk_status mk_page_scores(const mk_scores_args* args, const mk_page_vi
     a.table_rows = cache->n_rows; a.width = cache->table_width;
     const long long per = args->dtype == MK_F32 ? 4 : 8;
     a.q_vec = aligned_to(a.q, 16) && a.q_row % per == 0 && a.q_head % per == 0;
-    // pages of a CTA: as many as leave two CTAs for every SM, in whole turns of its warps
+    // pages of a CTA: as many as leave two CTAs for every SM (one wave), in whole turns of its warps, up to 96 (16 ragged
+    // rows of up to 2048 pages: 21.6 us; 64 pages 25.7, 128 23.5, 256 34.4)
     int n_sm = 0;
     const mk_status s = sm_count(&n_sm);
     if (s) return s;
     const int turn = kScorePages * std::max(1, kScoreWarps / a.hkv);
     const long long want = (long long)a.width * a.n_rows / (2LL * n_sm);
-    a.chunk = (int)std::min<long long>(64, std::max<long long>(1, want / turn) * turn);
+    a.chunk = (int)std::min<long long>(96, std::max<long long>(1, want / turn) * turn);
     // queries of the bounds' type are exact in one part, others are split into 2 parts of fp16 (22 bits, each head
     // at a power of two of its own) or 3 of bf16 (24 bits; fp16 queries: 2, 16 bits and more than their 11)
     const int d = cache->head_dim;

@@ -8,6 +8,13 @@
 // tensor-map copies from the pages, P from the threads' registers into tensor memory, where it is the
 // second product's first operand.
 //
+// Bound: the tensor cores, next to the keys' and values' bytes.  A tile of 64 slots costs a block of 128 rows 8 products
+// for the scores, each 48 cycles (with both operands in shared memory its traffic decides: 64 columns take 48, not 32),
+// and 4 of 64 for the values at 128 dims: two blocks of 16-bit queries 1280 cycles, the tile's arrival at the copy
+// bandwidth 1100 to 1400, by the clock.  16 rows of 64 nodes over 16384 to 32768 positions, 32 heads over 8: 348 us, 4.9
+// TB/s and 1.23 PFLOP/s; one row of 16 nodes over 32768, 32-bit queries in two parts: 39 us; one of 8 nodes over 512: 12
+// us, the latency of a piece (7 us, most of it code executed for the first time) and of the join (3 us).
+//
 // The work is split as the single tokens' attention splits it: the segments (row, kv head), each of its tiles,
 // follow one another in one line; every CTA of one wave takes an equal share of it; the pieces of a segment that
 // spans CTAs go to the workspace and a second kernel joins them in order:
