@@ -518,9 +518,12 @@ mk_status mk_beam_select_workspace(int groups, int beams, int vocab, size_t* byt
  * scores, softmax and log-sum-exp as mk_paged_attention's.  window > 0: only positions above the
  * node's own minus window.  An absent node, and every node of a row whose lens is negative or
  * that is outside the table, gets zeros and lse -inf.  Nothing that a node does not see is read
- * for its value: whatever lies there, NaN included, has no effect on it.  Slots past the table are
- * dropped and those on a bad page masked, each reported (MK_ERR_PAGES).  A NaN or infinite value
- * that a node sees makes its results NaN or infinite. */
+ * for its value: whatever lies there, NaN included, has no effect on it.  Slots that a node should
+ * see but that lie past the table or on a bad page are masked and reported (MK_ERR_PAGES); those of
+ * absent nodes need no page.  A NaN or infinite value that a node sees makes its results NaN or
+ * infinite, as does a NaN key; an infinite key does, unless the query is of the cache's type and
+ * the scores stay below +inf.  A probability is rounded to the cache's type where out has 16 bits;
+ * in 32-bit outputs it has 22 bits over an fp16 cache, 24 over a bf16 cache. */
 typedef struct {
   const void* q;           /* [n_rows][n_nodes][n_heads][head_dim], element strides below    */
   void* out;               /* its vectors must not overlap                                  */

@@ -112,7 +112,7 @@ __device__ __forceinline__ bool next_piece(const TreeArgs& a, Walk& w, Piece& p)
     const int seg = w.before + p.head * each, stop = min(w.end, seg + each);
     p.first = max(0, w.at - seg - w.lead);
     p.count = stop - seg - w.lead - p.first;
-      p.last_unit = seg + each - 1;
+    p.last_unit = seg + each - 1;
     p.whole = p.count == p.sp.n;
     w.at = stop;
     if (p.count > 0) return true;         // (none: of a segment's lead alone)
@@ -134,7 +134,11 @@ template <typename C, typename Q, int HD, int NQ, int NP, int MODE>
 struct Shape {
   static constexpr bool PAIR = MODE == PAIR_MODE, SOLO = MODE == SOLO_MODE;
   static constexpr int BUFFERS = NP == 3 ? 1 : 2;
-  static constexpr int AHEAD = MODE == TURNS ? 2 * BUFFERS : BUFFERS;  // tiles whose scores are asked for before the first values
+  // A ring of stages for each that takes its tiles: a product warp must see every load of its ring, in order.  (With one
+  // ring of which each takes every second tile, one could look for a load whose stage still waits for the other's load
+  // before it: loads land in any order, and the parity of a phase but one ago reads as done.)
+  static constexpr int RINGS = PAIR ? 1 : 2;
+  static constexpr int AHEAD = BUFFERS;             // tiles of a ring whose scores are asked for before the first values
   static constexpr int BLOCKS = PAIR ? 2 : 1;       // blocks of rows of a piece
   static constexpr int QUERIES = MODE == TURNS ? 1 : 2;  // places of a block's queries
   static __host__ __device__ constexpr int q_part(int rows) { return rows * HD * 2; }
@@ -153,20 +157,20 @@ struct Shape {
     float scale[QUERIES * kRows];
     float ml[2][kRows][2];
   };
-  // stages of a ring: SOLO has two of four; with SOLO only the rows that hold queries have a place (the products read
+  // stages of a ring: with SOLO four, and only the rows that hold queries have a place (the products read
   // on over what lies behind it, for rows that nobody looks at)
   static constexpr int kRoom = kSmemBytes - 1024 - (int)sizeof(State) - q_bytes(kRows);
-  static constexpr int kStages = SOLO ? 4 : kRoom / kStage < kMaxStages ? kRoom / kStage : kMaxStages;
+  static constexpr int kAll = kRoom / kStage < kMaxStages ? kRoom / kStage : kMaxStages, kStages = SOLO ? 4 : kAll / RINGS;
   // (more than half of an SM's: there is one CTA on it, which takes all of the tensor memory)
   static __host__ __device__ constexpr int bytes(int rows) {
-    const int used = 1024 + q_bytes(rows) + (SOLO ? 2 : 1) * kStages * kStage + (int)sizeof(State);
+    const int used = 1024 + q_bytes(rows) + RINGS * kStages * kStage + (int)sizeof(State);
     return used > 120 * 1024 ? used : 120 * 1024;
   }
-  static_assert(kStages >= 4 && (SOLO || bytes(kRows) <= kSmemBytes), "shared memory");
+  static_assert(kStages >= 3 && RINGS * kStages <= kMaxStages && (SOLO || bytes(kRows) <= kSmemBytes), "shared memory");
   static_assert(!SOLO || bytes(32) <= kSmemBytes, "shared memory");
   // what the products of the last row of queries' place read beyond it lies in the ring
   static_assert(!SOLO || 8 * kStage >= kRows * 128, "shared memory");
-  // the place of tile i's keys and values among a piece's `count` tiles' copies: K0 .. K(AHEAD - 1), V0, K(AHEAD), V1, ..
+  // the place of tile i's keys and values among the copies to a ring of a piece's `count` tiles in it: K0 .. K(AHEAD - 1), V0, K(AHEAD), V1, ..
   static __device__ __forceinline__ unsigned k_load(int i) { return i < AHEAD ? i : 2 * i - AHEAD + 1; }
   static __device__ __forceinline__ unsigned v_load(int i, int count) { return i + min(count, AHEAD + i); }
 };
@@ -259,7 +263,7 @@ __device__ __forceinline__ float capped_fine(float x, float cap) {
   const float d = ex2(x * (2.f * kLog2e)) + 1.f;
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-  r = d < 1e30f ? r * fmaf(-d, r, 2.f) : 0.f;
+  r = d < 1e30f ? r * fmaf(-d, r, 2.f) : r;  // (infinity's is 0, NaN's NaN)
   const float q = x * x;
   float t = fmaf(q, -1382.f / 155925.f, 62.f / 2835.f);
   t = fmaf(q, t, -17.f / 315.f);
@@ -300,14 +304,13 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(tree_smem) + 1023) & ~uintptr_t(1023));
   const int place_rows = SOLO ? a.q_rows : kRows, q_part = SH::q_part(place_rows);
   unsigned char *s_q = base, *s_kv = base + SH::q_bytes(place_rows);
-  State* st = reinterpret_cast<State*>(s_kv + (SOLO ? 2 : 1) * ST * SH::kStage);
+  State* st = reinterpret_cast<State*>(s_kv + SH::RINGS * ST * SH::kStage);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int part = blockIdx.x % a.parts;
   // the share of warpgroup g (SOLO: the first of all CTAs come first)
   auto share_of = [&](int g) { return (int)blockIdx.x / a.parts + (SOLO ? g * (a.shares / 2) : 0); };
   if (warp == kCopyWarp) {
-    if (lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &v_map : &k_map) : "memory");
-    constexpr int ALL = (SOLO ? 2 : 1) * ST;
+    constexpr int ALL = SH::RINGS * ST;
     if (lane < ALL) {
       mbar_init(&st->full[lane], 1);
       mbar_init(&st->empty[lane], SH::BLOCKS);
@@ -408,7 +411,7 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
         const Span s = span_of(a, r);
         if (s.len >= 0 && (unsigned)s.trow >= (unsigned)a.table_rows)
           report(a.status, MK_ERR_PAGES, PO_TREE, r, s.trow);
-        else if (s.len >= 0 && (unsigned)s.len + (unsigned)a.n_nodes > (unsigned)a.cap)
+        else if (s.len > a.cap)
           report(a.status, MK_ERR_PAGES, PO_TREE, r, s.len);
       }
   }
@@ -424,12 +427,14 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
            __shfl_sync(0xffffffffu, w.lead, 0), __shfl_sync(0xffffffffu, w.row, 0), __shfl_sync(0xffffffffu, w.before, 0)};
   const int self = share_of(own) * a.parts + part;  // the place of its pieces
   Piece p;
-  unsigned loads = 0;                     // tiles of keys or values asked for, or used
-
-  s_kv += SOLO ? own * ST * SH::kStage : 0;
-  uint64_t *full = st->full + (SOLO ? own * ST : 0), *empty = st->empty + (SOLO ? own * ST : 0);
+  unsigned loads = 0, loads1 = 0;         // tiles of keys or values asked for, or used; TURNS' copies: of the second ring
+  // whose ring (TURNS' one copying warp: the first, and the second behind it)
+  const int ring = PAIR ? 0 : warp < kCopyWarp ? warp >> 2 : warp == kMmaWarp + 1 || warp == kMmaWarp + 2 ? 1 : 0;
+  s_kv += ring * ST * SH::kStage;
+  uint64_t *full = st->full + ring * ST, *empty = st->empty + ring * ST;
   if (warp == kCopyWarp || (SOLO && warp == kMmaWarp + 2)) {
     // ------------------------------------------------------------------------- copies
+    constexpr int LEAD = MODE == TURNS ? 2 * AHEAD : AHEAD;  // tiles whose keys come before the first values
     unsigned tiles = 0;
     bool run = true, begun = false;
     while (run && next_piece(a, w, p)) {
@@ -454,8 +459,10 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
       const int32_t* table = a.table + (long long)p.sp.trow * a.table_stride;
       auto entry_of = [&](int i) { return read_of(i) ? table[page_index(a, at0 + i * kTile)] : 0; };
       auto copy = [&](const CUtensorMap* map, int i, int page) {
-        const int s = loads % ST;
-        if (!wait_warp(&empty[s], (loads / ST & 1) ^ 1, &st->abort)) return false;
+        const int r = MODE == TURNS ? i & 1 : 0;
+        const unsigned l = r ? loads1 : loads;
+        const int s = r * ST + l % ST;
+        if (!wait_warp(&empty[s], (l / ST & 1) ^ 1, &st->abort)) return false;
         if (lane == 0) mbar_arrive_expect_tx(&full[s], SH::kStage);
         __syncwarp();
         const uint32_t dst = smem_addr(s_kv + s * SH::kStage) + half * kTile * 128 + lane % boxes * a.box * 128;
@@ -463,21 +470,19 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
         const bool there = read_of(i) && (unsigned)page < (unsigned)a.n_pages;
         if (on)  // (a page outside the map: zeros)
           tma_box_4d(dst, map, 64 * half, there ? t - page_index(a, t) * a.page_size : 0, p.head, there ? page : a.n_pages, &full[s]);
-        ++loads;
+        loads += 1 - r;
+        loads1 += r;
         return true;
       };
-      // the pages of the next tiles: the keys' is AHEAD tiles before the values'
-      int page[AHEAD + 2];
+      // the pages of the next tiles: the keys' is LEAD tiles before the values'
+      int page[LEAD + 2];
 #pragma unroll
-      for (int i = 0; i < AHEAD + 1; ++i) page[i] = entry_of(i);
+      for (int i = 0; i < LEAD + 1; ++i) page[i] = entry_of(i);
       auto keys = [&](int i, int pg) {
         const bool none = half == 0 && read_of(i) && (unsigned)pg >= (unsigned)a.n_pages;
         unsigned bad = 0;
         if (__any_sync(0xffffffffu, none)) {  // the groups of 16 slots on a bad page
-          if (none) {
-            report(a.status, MK_ERR_PAGES, PO_TREE, p.r, pg);
-            bad = ((1u << (a.box / 16)) - 1) << (lane % boxes * (a.box / 16));
-          }
+          if (none) bad = ((1u << (a.box / 16)) - 1) << (lane % boxes * (a.box / 16));
           bad = __reduce_or_sync(0xffffffffu, bad);
         }
         if (lane == 0) st->bad[own][tiles % 16] = (unsigned char)bad;
@@ -486,21 +491,22 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
         run = run && copy(&k_map, i, pg);
       };
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i)
+      for (int i = 0; i < LEAD; ++i)
         if (i < p.count) keys(i, page[i]);
       // (the first queries do not queue behind the keys and values that fill the ring)
       if (!begun) wait_phase(&st->q_full[own], 0, &st->abort);
       begun = true;
       for (int i = 0; i < p.count && run; ++i) {
-        page[AHEAD + 1] = entry_of(i + AHEAD + 1);
+        page[LEAD + 1] = entry_of(i + LEAD + 1);
         run = copy(&v_map, i, page[0]);
-        if (i + AHEAD < p.count) keys(i + AHEAD, page[AHEAD]);
+        if (i + LEAD < p.count) keys(i + LEAD, page[LEAD]);
 #pragma unroll
-        for (int y = 0; y < AHEAD + 1; ++y) page[y] = page[y + 1];
+        for (int y = 0; y < LEAD + 1; ++y) page[y] = page[y + 1];
       }
     }
     // every copy has landed before the CTA ends
     for (unsigned i = loads > ST ? loads - ST : 0; i < loads; ++i) wait_phase(&full[i % ST], i / ST & 1, nullptr);
+    for (unsigned i = loads1 > ST ? loads1 - ST : 0; i < loads1; ++i) wait_phase(&full[ST + i % ST], i / ST & 1, nullptr);
   } else if (warp >= kMmaWarp) {
     // ----------------------------------------------------------------------- products
     // A warp for each warpgroup: one alone takes longer to issue a job than the tensor cores to do it.  The whole
@@ -518,11 +524,10 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
         __syncwarp();
         if (lane == 0) mbar_arrive(&st->q_seen);
       }
-      auto tile = [&](int x) { return MODE != TURNS ? x : 2 * x + g; };
       // The tensor cores take what one thread issues in order: a buffer's next scores come after the product
       // that read its P.
       auto scores = [&](int x) {
-        const unsigned l = loads + SH::k_load(tile(x)), s = l % ST;
+        const unsigned l = loads + SH::k_load(x), s = l % ST;
         const int b = SH::BUFFERS == 2 ? x & 1 : 0;
         wait_phase(&full[s], l / ST & 1, &st->abort);
         tmem_fence_after();
@@ -540,7 +545,7 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
         __syncwarp();
       };
       auto values = [&](int x) {
-        const unsigned l = loads + SH::v_load(tile(x), p.count), s = l % ST;
+        const unsigned l = loads + SH::v_load(x, n), s = l % ST;
         const int b = SH::BUFFERS == 2 ? x & 1 : 0;
         wait_phase(&full[s], l / ST & 1, &st->abort);
         wait_phase(&st->p_full[g][b], p_phase >> b & 1, &st->abort);
@@ -563,7 +568,7 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
         values(x);
         if (x + SH::BUFFERS < n) scores(x + SH::BUFFERS);
       }
-      loads += 2 * p.count;
+      loads += 2 * n;
     }
     if (elect_one()) mma_commit(&st->finished);
     __syncwarp();
@@ -675,9 +680,12 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
           i = up;
           ++depth;
         }
-        if (!there)
+        if (!there) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) seen[i] = 0;
+        } else if ((unsigned)p.sp.len + (unsigned)node >= (unsigned)a.cap) {
+          report(a.status, MK_ERR_PAGES, PO_TREE, p.r, p.sp.len);
+        }
       }
       // the first position that a node of so many ancestors sees (lengths up to 2^31 - 1)
       auto from = [&](int up) {
@@ -692,7 +700,8 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
         if (SH::BUFFERS == 2) wait_phase(&st->o_done[g][buf ^ 1], (s_phase >> (buf ^ 1) & 1) ^ 1, &st->abort);
         tmem_fence_after();
       };
-      int turn = 0;                       // tiles of the piece that this warpgroup has taken
+      const int n = MODE != TURNS ? p.count : (p.count - g + 1) / 2;  // this warpgroup's tiles of the piece
+      int turn = 0;                       // those that it has taken
       for (int i = MODE != TURNS ? 0 : g; i < p.count; i += MODE != TURNS ? 1 : 2, ++turn) {
         const int t0 = (p.sp.t0 + p.first + i) * kTile;
         const int buf = SH::BUFFERS == 2 ? turn & 1 : 0;
@@ -724,8 +733,11 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
               const int b = t0 + 32 * x;
               vis[x] = ones(lo - b, p.sp.len - b) | bits_at(seen, b - p.sp.len);
               vis[x] &= ones(0, p.sp.hi - b);
-              if (bad >> (2 * x) & 1) vis[x] &= 0xffff0000u;
-              if (bad >> (2 * x) & 2) vis[x] &= 0x0000ffffu;
+              const unsigned none = (bad >> (2 * x) & 1 ? 0x0000ffffu : 0u) | (bad >> (2 * x) & 2 ? 0xffff0000u : 0u);
+              if (vis[x] & none)           // (only what some node sees is missed: the slots of absent ones need no page)
+                report(a.status, MK_ERR_PAGES, PO_TREE, p.r,
+                       a.table[(long long)p.sp.trow * a.table_stride + page_index(a, b + __ffs(vis[x] & none) - 1)]);
+              vis[x] &= ~none;
 #pragma unroll
               for (int y = 0; y < 32; ++y) s[x][y] = vis[x] >> y & 1 ? s[x][y] : 0xff800000u;
             }
@@ -783,7 +795,7 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
           unsigned* found = st->odd[PAIR ? i & 7 : 2 * g + (turn & 1)];
           if (row < 2) found[row] = 0;
           tile_sync<PAIR>(g);
-          const unsigned v_at = loads + SH::v_load(i, p.count);
+          const unsigned v_at = loads + SH::v_load(turn, n);
           wait_phase(&full[v_at % ST], v_at / ST & 1, &st->abort);
           uint4* v = reinterpret_cast<uint4*>(s_kv + v_at % ST * SH::kStage);
           constexpr int step = PAIR ? 2 * kGroupThreads : kGroupThreads;
@@ -840,7 +852,7 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
       }
       for (int b = 0; b < SH::BUFFERS; ++b) wait_phase(&st->o_done[g][b], (s_phase >> b & 1) ^ 1, &st->abort);
       tiles += p.count;
-      loads += 2 * p.count;
+      loads += 2 * n;
       // ---- the piece's result
       if (!there) {                       // (an absent node's row went through the whole tiles with the others)
         m = -INFINITY;

@@ -281,6 +281,52 @@ def test_tree_reports_and_masks_what_is_not_there(paged, what):
     paged.tree_attention(*args, rows=ints(rows))   # no status: not reported, no fault
 
 
+def test_tree_slots_of_absent_nodes_need_no_page(paged):
+    """Padded trees whose pages end with their last node: nothing is reported, and what the table holds behind is not used."""
+    g = gen(18)
+    lens, nodes = [30, 15, 48, 9], 40
+    parents = [[-1] + [i - 1 if i < m else -2 for i in range(1, nodes)] for m in (2, 1, 16, 7)]
+    ends = [n + m for n, m in zip(lens, (2, 1, 16, 7))]
+    kp, vp, table = make_cache(g, ends, 2, 64, 16, "bf16")
+    table = table[:, :4].copy()                       # 64 slots: the padding of row 2 ends past the table
+    for fill in (-1, 10 ** 6):
+        table[table < 0] = fill
+        table[table >= len(kp)] = fill
+        q = torch.randn(4, nodes, 4, 64, generator=g, device=DEV).bfloat16()
+        st = status()
+        out, lse = paged.tree_attention(q, kp, vp, ints(table), ints(lens), ints(parents), return_lse=True, status=st)
+        paged.check_status(st)
+        check_tree(q, kp, vp, table, lens, parents, out, lse, 0.125)
+
+
+@pytest.mark.parametrize("vec", ["bf16", "f32"])
+def test_tree_caps_of_nan_infinite_and_small_scores(paged, vec):
+    """A cap: NaN keys make who sees them NaN, infinite ones count as the cap (queries of the cache's type); scores far below the cap are kept to their
+    own size's accuracy, which check_tree bounds by the scores and not by the cap."""
+    g = gen(19)
+    n, nodes, parents = 90, 3, [[-1, 0, 0]]
+    kp, vp, table = make_cache(g, [n + nodes], 1, 64, 16, "bf16")
+    q = torch.randn(1, nodes, 2, 64, generator=g, device=DEV).to(TYPES[vec])
+    q[..., 0] = 1.0
+    args = (ints(table), ints([n]), ints(parents))
+    for size, cap in ((1.0, 50.0), (0.01, 5.0), (30.0, 2.0)):
+        out, lse = paged.tree_attention(q * size, kp, vp, *args, softcap=cap, return_lse=True)
+        check_tree(q * size, kp, vp, table, [n], parents, out, lse, 0.125, cap=cap)
+    at = kp[int(table[0, (n + 1) // 16]), :, (n + 1) % 16]
+    at[:, 0] = math.nan
+    out, lse = paged.tree_attention(q, kp, vp, *args, softcap=5.0, return_lse=True)
+    assert torch.isnan(lse[0, 1]).all() and torch.isnan(out[0, 1]).all()
+    assert torch.isfinite(out[0, 0]).all() and torch.isfinite(out[0, 2]).all() and torch.isfinite(lse[0, [0, 2]]).all()
+    if vec == "f32":       # (a query in several parts meets an infinite key with a part of 0)
+        return
+    at[:, 0] = math.inf
+    out, lse = paged.tree_attention(q, kp, vp, *args, softcap=5.0, return_lse=True)
+    assert torch.isfinite(out).all()
+    at[:, 0] = 1e30
+    want, wl = paged.tree_attention(q, kp, vp, *args, softcap=5.0, return_lse=True)
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
 def test_tree_extreme_lengths(paged):
     """Lengths near 2^31 (past any table) are cut to the table's positions and reported."""
     from persistent_sm_decode_megakernel_gb300 import MkError
@@ -329,6 +375,34 @@ def test_tree_offsets_past_32_bits(paged):
         paged.accept_drafts(k[0][None], k[1][None], ints([t]), n, one, ints([[-1, 0, 0]]), ints([[8, 1, 2]]))
         assert n.item() == 192
     assert torch.equal(pool[:, ids], small)
+
+
+@pytest.mark.parametrize("lens,nodes,hq,hkv,vec", [
+    ([20000], 16, 8, 2, "f32"),              # one block of rows, tiles by turns
+    ([9000, 3, 70, 0, 5000], 5, 8, 4, "bf16"),
+    ([6000, 100], 64, 32, 4, "bf16"),        # two blocks
+    ([700] * 40, 7, 16, 8, "bf16"),          # a share to a warpgroup
+])
+def test_tree_answers_stay_the_same_beside_other_traffic(paged, lens, nodes, hq, hkv, vec):
+    """Many calls while another stream moves memory, which lets the copies of a call land in other orders: the same bits."""
+    g = gen(20)
+    kp, vp, table = make_cache(g, [n + nodes for n in lens], hkv, 128, 64, "bf16")
+    q = torch.randn(len(lens), nodes, hq, 128, generator=g, device=DEV).to(TYPES[vec])
+    tree = ints(trees(np.random.default_rng(20), len(lens), nodes, "random"))
+    tb, ls, st = ints(table), ints(lens), status()
+    want = paged.tree_attention(q, kp, vp, tb, ls, tree, return_lse=True, status=st)
+    a, b = (torch.zeros(64 << 20, dtype=torch.uint8, device=DEV) for _ in range(2))
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    differ = torch.zeros((), dtype=torch.int64, device=DEV)
+    for i in range(300):
+        with torch.cuda.stream(other):
+            a.copy_(b)
+        got = paged.tree_attention(q, kp, vp, tb, ls, tree, return_lse=True, status=st)
+        differ += sum((x != y).sum() for x, y in zip(got, want))
+    torch.cuda.current_stream().wait_stream(other)
+    paged.check_status(st)
+    assert differ.item() == 0
 
 
 def test_tree_repeats_bit_for_bit_and_replays(paged):
@@ -668,6 +742,14 @@ def test_sparse_ties_nan_and_infinite_scores(paged):
     scores[2, 1] = math.nan
     for n_blocks in (2, 5, 23, 64, 257):
         check_sparse(paged, q, kp, vp, table, lens, scores, n_blocks, 1, 1)
+
+
+@pytest.mark.parametrize("pages,n_blocks", [(2049, 7), (3000, 130), (4100, 4099), (2100, 2200)])
+def test_sparse_of_more_pages_than_registers_hold(paged, pages, n_blocks):
+    lens = [16 * pages - 5, 16 * (pages // 2)]
+    q, kp, vp, table, scores = sparse_inputs(lens, 2, 1, 64, 16, "bf16", "bf16", seed=pages)
+    scores[1] = (scores[1] * 4).round()
+    check_sparse(paged, q, kp, vp, table, lens, scores, n_blocks, 1, 2)
 
 
 def test_sparse_of_all_pages_is_paged_attention(paged):
