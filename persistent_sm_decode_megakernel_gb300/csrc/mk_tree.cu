@@ -12,7 +12,7 @@
 // for the scores, each 48 cycles (with both operands in shared memory its traffic decides: 64 columns take 48, not 32),
 // and 4 of 64 for the values at 128 dims: two blocks of 16-bit queries 1280 cycles, the tile's arrival at the copy
 // bandwidth 1100 to 1400, by the clock.  16 rows of 64 nodes over 16384 to 32768 positions, 32 heads over 8: 348 us, 4.9
-// TB/s and 1.23 PFLOP/s; one row of 16 nodes over 32768, 32-bit queries in two parts: 39 us; one of 8 nodes over 512: 12
+// TB/s and 1.23 PFLOP/s; one row of 16 nodes over 32768, 32-bit queries in two parts: 39.5 us; one of 8 nodes over 512: 12.3
 // us, the latency of a piece (7 us, most of it code executed for the first time) and of the join (3 us).
 //
 // The work is split as the single tokens' attention splits it: the segments (row, kv head), each of its tiles,
@@ -196,8 +196,8 @@ __device__ __forceinline__ int node_of(const TreeArgs& a, int row) { return row 
 // Waits for a phase of a barrier, false where it did not come: a wait that takes too long sets *abort, and from then
 // on none waits: the work goes on over whatever lies there, within its bounds, to its end.  With abort NULL: up to
 // the limit in any case (what is in flight when a CTA ends).
-// A barrier's next phase but one never completes before everyone who waits for a phase has seen it: each is answered by
-// its waiters before it can.
+// A barrier tells two phases apart: nobody looks for a phase before the one before it is over, nor after the next one is.
+// Each phase is answered by its waiters before the next can end, and a ring's loads are waited for one by one, in order.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* abort) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long begin = clock64();
@@ -534,11 +534,11 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
         if (elect_one()) {
           const uint64_t kd = k_desc + s * (SH::kStage / 16);
 #pragma unroll
-          for (int y = 0; y < NQ; ++y)
+          for (int y = NQ - 1; y >= 0; --y)  // the smallest parts first: each product's sum is cut off, not rounded
 #pragma unroll
             for (int c = 0; c < HD / 16; ++c)  // (the address counts in 16 bytes)
               mma_ss(t_s + b * kTile, q_desc + (y * q_part + (c >> 2) * place_rows * 128 + (c & 3) * 32) / 16,
-                     kd + ((c >> 2) * kTile * 128 + (c & 3) * 32) / 16, mma_desc(kType, false, kRows, kTile), y + c > 0);
+                     kd + ((c >> 2) * kTile * 128 + (c & 3) * 32) / 16, mma_desc(kType, false, kRows, kTile), y < NQ - 1 || c > 0);
           mma_commit(&st->s_full[g][b]);
           mma_commit(&empty[s]);
         }
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
         if (elect_one()) {
           const uint64_t vd = v_desc + s * (SH::kStage / 16);
 #pragma unroll
-          for (int y = 0; y < NP; ++y)
+          for (int y = NP - 1; y >= 0; --y)
 #pragma unroll
             for (int c = 0; c < kTile / 16; ++c)
               mma_ts(t_o, t_s + b * kTile + y * (kTile / 2) + c * 8, vd + c * 2048 / 16, mma_desc(kType, true, kRows, HD), true);
@@ -1118,7 +1118,7 @@ mk_status launch_tree(const TreeArgs& a, const mk_page_view& view, bool pair, in
   }
   // SOLO where there are segments enough for a third of the CTAs (8 nodes, 8 kv heads, bf16: 16 rows of 4500 to 9000
   // positions 79.6 us, TURNS 98.3; 64 rows 267, 342), TURNS where there are fewer and a piece's latency counts
-  // (one row of 512 positions 12.0 us, SOLO 12.6; one of 32768 38.9, 42.0)
+  // (one row of 512 positions 12.3 us, SOLO 12.6; one of 32768 39.4, 42.0)
   const bool solo = 3LL * a.n_rows * a.hkv * a.parts >= n_sm;
   if (solo && Shape<C, Q, HD, NQ, NP, SOLO_MODE>::bytes(a.q_rows) <= kSmemBytes)
     return launch_mode<C, Q, HD, NQ, NP, SOLO_MODE>(a, view, n_sm, stream);
