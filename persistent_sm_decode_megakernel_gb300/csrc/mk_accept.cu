@@ -101,6 +101,7 @@ accept_kernel(const __grid_constant__ AcceptArgs a) {
     }
   }
   // every CTA of the row has read its length
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
   if (rank != 0) return;
   for (int j = tid; j < n; j += kAcceptThreads) {

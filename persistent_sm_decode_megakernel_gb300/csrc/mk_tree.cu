@@ -193,22 +193,25 @@ __device__ __forceinline__ int page_index(const TreeArgs& a, int slot) {
 // the node of a block that a row of it is of: row / group, exact for rows below 128 and groups up to 16
 __device__ __forceinline__ int node_of(const TreeArgs& a, int row) { return row * a.group_inverse >> 16; }
 
-// Waits for a phase of a barrier, false where it did not come: a wait that takes too long sets *abort, and from then
+// Waits for a phase of a barrier, a whole warp together (what follows may need it so), false where it did not come: a wait that takes too long sets *abort, and from then
 // on none waits: the work goes on over whatever lies there, within its bounds, to its end.  With abort NULL: up to
 // the limit in any case (what is in flight when a CTA ends).
 // A barrier tells two phases apart: nobody looks for a phase before the one before it is over, nor after the next one is.
 // Each phase is answered by its waiters before the next can end, and a ring's loads are waited for one by one, in order.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const long long begin = clock64();
-  while (!mbar_wait_hint(bar, parity, 100000)) {
-    if (abort && *(volatile int*)abort) return false;
-    if (clock64() - begin > kWaitCycles) {
-      if (abort) *(volatile int*)abort = 1;
-      return false;
+  bool come = mbar_try_wait(bar, parity);
+  if (!come) {
+    const long long begin = clock64();
+    while (!(come = mbar_wait_hint(bar, parity, 100000))) {
+      if (abort && *(volatile int*)abort) break;
+      if (clock64() - begin > kWaitCycles) {
+        if (abort) *(volatile int*)abort = 1;
+        break;
+      }
     }
   }
-  return true;
+  __syncwarp();
+  return come;
 }
 // the same for a whole warp, which goes on together
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* abort) {
