@@ -522,8 +522,8 @@ mk_status mk_beam_select_workspace(int groups, int beams, int vocab, size_t* byt
  * see but that lie past the table or on a bad page are masked and reported (MK_ERR_PAGES); those of
  * absent nodes need no page.  A NaN or infinite value that a node sees makes its results NaN or
  * infinite, as does a NaN key; an infinite key does, unless the query is of the cache's type and
- * the scores stay below +inf.  A probability is rounded to the cache's type where out has 16 bits;
- * in 32-bit outputs it has 22 bits over an fp16 cache, 24 over a bf16 cache, and the sums, which
+ * the scores stay below +inf.  A probability has 22 bits over an fp16 cache, over a bf16
+ * cache 16 where out has 16 bits and 24 where it has 32; the sums, which
  * the tensor cores cut off instead of rounding, keep them within some 5e-6 of their norm. */
 typedef struct {
   const void* q;           /* [n_rows][n_nodes][n_heads][head_dim], element strides below    */

@@ -1228,15 +1228,16 @@ extern "C" mk_status mk_tree_attention(const mk_tree_args* args, const mk_page_v
     a.group_inverse = (65536 + a.group - 1) / a.group;
     a.softcap = args->softcap * kLog2e;
     // 16-bit queries of the cache's type are exact in one part, others are split into 2 parts of fp16 (22
-    // bits, each head at a power of two of its own) or 3 of bf16 (24 bits).  A probability has one part where the
-    // outputs have 16 bits, and 2 of fp16 or 3 of bf16 where they have 32.
+    // bits, each head at a power of two of its own) or 3 of bf16 (24 bits); probabilities likewise, 2 parts of bf16 (16
+    // bits) being enough for an output of 16 bits, as for single tokens.  (One part, 8 or 11 bits, is as far off as the
+    // output's own rounding: 2.3e-3 from 64 bits where that gives 1.7e-3.)
     if (cache->dtype == MK_F16) {
-      if (args->dtype == MK_F16) return launch_tree<__half, __half, 1, 1>(a, *cache, d.pair, n_sm, stream);
-      if (args->dtype == MK_BF16) return launch_tree<__half, __nv_bfloat16, 2, 1>(a, *cache, d.pair, n_sm, stream);
+      if (args->dtype == MK_F16) return launch_tree<__half, __half, 1, 2>(a, *cache, d.pair, n_sm, stream);
+      if (args->dtype == MK_BF16) return launch_tree<__half, __nv_bfloat16, 2, 2>(a, *cache, d.pair, n_sm, stream);
       return launch_tree<__half, float, 2, 2>(a, *cache, d.pair, n_sm, stream);
     }
-    if (args->dtype == MK_BF16) return launch_tree<__nv_bfloat16, __nv_bfloat16, 1, 1>(a, *cache, d.pair, n_sm, stream);
-    if (args->dtype == MK_F16) return launch_tree<__nv_bfloat16, __half, 2, 1>(a, *cache, d.pair, n_sm, stream);
+    if (args->dtype == MK_BF16) return launch_tree<__nv_bfloat16, __nv_bfloat16, 1, 2>(a, *cache, d.pair, n_sm, stream);
+    if (args->dtype == MK_F16) return launch_tree<__nv_bfloat16, __half, 2, 2>(a, *cache, d.pair, n_sm, stream);
     return launch_tree<__nv_bfloat16, float, 3, 3>(a, *cache, d.pair, n_sm, stream);
   });
 }

@@ -1,0 +1,120 @@
+"""Tree attention on the GPU in each of the ways its kernel deals the rows, against a plain 64-bit computation (torch,
+from the definitions in include/mk.h): shares of the line to each warpgroup (many short trees), pairs of blocks (more than
+128 rows per kv head, queries of the cache's type), single blocks of several parts (queries of another type).  And the sums of
+long contexts, whose accuracy must not go with the length.
+
+Tolerances: a result rounded to a type is off by at most half a step, eps / 2 relative (plus the smallest subnormal's half
+for fp16); what the 32-bit arithmetic adds is said at the check."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from drafts_plain import tree_seen
+from test_gpu_drafts import DEV, EDGES, TYPES, gen, ints, make_cache, paged, status, trees  # noqa: F401 (paged: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def plain_tree(q, kp, vp, table, n, row, parents, scale, window=0, cap=0.0):
+    """One row's trees in 64 bits: outputs, log-sum-exps, sum p |v|, the largest scale sum |q||k|; absent nodes zeros and -inf."""
+    T, hq, hd = q.shape
+    hkv, ps = kp.shape[1], kp.shape[2]
+    lines = tree_seen(n, parents, window) if n >= 0 else [None] * T
+    there = torch.tensor([s is not None for s in lines], device=DEV)
+    out, lse = torch.zeros(T, hq, hd, dtype=torch.float64, device=DEV), torch.full((T, hq), -math.inf, dtype=torch.float64, device=DEV)
+    mass, size = torch.zeros_like(out), torch.zeros_like(lse)
+    if not there.any():
+        return out, lse, mass, size
+    seen = torch.as_tensor(np.stack([s if s is not None else np.zeros(n + T, dtype=bool) for s in lines]), device=DEV)
+    some = seen.any(0).nonzero()[:, 0]                      # the slots that any node sees
+    page = torch.as_tensor(table, device=DEV)[row, some // ps].long()
+    for j in range(hkv):
+        k, v = (x[page, j, some % ps].double() for x in (kp, vp))
+        h = slice(j * (hq // hkv), (j + 1) * (hq // hkv))
+        x = q[:, h].double()
+        s = torch.einsum("thd,ld->thl", x, k) * scale
+        big = torch.einsum("thd,ld->thl", x.abs(), k.abs()) * abs(scale)
+        if cap:
+            s = cap * torch.tanh(s / cap)
+        mask = seen[:, None, some]
+        s = torch.where(mask, s, torch.tensor(-math.inf, dtype=torch.float64, device=DEV))
+        m = s.amax(2, keepdim=True).clamp_min(-1e300)
+        p = torch.exp(s - m)
+        z = p.sum(2, keepdim=True)
+        p = torch.where(z > 0, p / z, torch.zeros_like(p))
+        out[:, h], mass[:, h] = torch.einsum("thl,ld->thd", p, v), torch.einsum("thl,ld->thd", p, v.abs())
+        lse[:, h] = (m + torch.log(z))[..., 0]
+        size[:, h] = torch.where(mask, big, torch.zeros_like(big)).amax(2)
+    return out, lse, mass, size
+
+
+def check(q, kp, vp, table, lens, parents, out, lse, window=0, cap=0.0):
+    """With A = scale sum |q||k| at its largest: a score's 32-bit products and sums are off by at most (hd + 16) 2^-23 A, its
+    query parts by 2^-17 A (bf16 cache, fp16 queries), 2^-22 A (fp16 cache, other queries) or nothing; the conversion to units
+    of log 2, exp2 and the maximum add 2^-21 (1 + |score| / 4).  A probability has parts good to 2^-17 (bf16, two parts) or 2^-22.
+    A sum of n products of up to 16 probabilities, each cut off, is off by at most n 2^-23; the maxima's slack, the pieces, the sum
+    of the probabilities and their least parts, below 2^-34 each, stay below 64 2^-23 at these lengths.  A relative error d of
+    every probability moves the output by at most 2 d sum p |v|."""
+    hd, scale = q.shape[-1], 1 / math.sqrt(q.shape[-1])
+    eps, least = torch.finfo(q.dtype).eps / 2, 2.0 ** -25 if q.dtype == torch.float16 else 0.0
+    qbits = 0.0 if q.dtype == kp.dtype else 2.0 ** -17 if (kp.dtype, q.dtype) == (torch.bfloat16, torch.float16) else 2.0 ** -22
+    pbits = 2.0 ** -17 if kp.dtype == torch.bfloat16 and q.dtype != torch.float32 else 2.0 ** -22
+    for r, n in enumerate(lens):
+        w, l, mass, size = plain_tree(q[r], kp, vp, table, n, r, parents[r], scale, window, cap)
+        d = size * ((hd + 16) * 2.0 ** -23 + qbits) + 2.0 ** -21 * (1 + (size.clamp_max(cap) if cap else size) / 4)
+        sums = (3 * max(n, 0) / 16 + 64) * 2.0 ** -23
+        off = (out[r].double() - w).abs()
+        assert torch.all(off <= w.abs() * eps + least + (2 * d[..., None] + 2 * pbits + sums) * mass), (r, (off / mass).max())
+        none = torch.isinf(l)
+        assert torch.equal(none, torch.isinf(lse[r])) and torch.all(lse[r][none] == -math.inf), r
+        assert torch.all((lse[r].double() - l).abs()[~none] <= (d + sums + 2.0 ** -22 * l.abs())[~none]), r
+
+
+def run(paged, lens, nodes, hq, hkv, hd, ps, cache, vec, window=0, cap=0.0, shape="random", seed=1, size=1.5):  # noqa: F811
+    g = gen(seed)
+    parents = trees(np.random.default_rng(seed), len(lens), nodes, shape)
+    gone = [(r, n + i) for r, n in enumerate(lens) if n >= 0 for i, s in enumerate(tree_seen(n, parents[r])) if s is None]
+    kp, vp, table = make_cache(g, [n + nodes if n >= 0 else 0 for n in lens], hkv, hd, ps, cache, skip=gone)
+    q = torch.randn(len(lens), nodes, hq, hd, generator=g, device=DEV).mul_(size).to(TYPES[vec])
+    st = status()
+    out, lse = paged.tree_attention(q, kp, vp, ints(table), ints(lens), ints(parents), window=window, softcap=cap, return_lse=True,
+                                    status=st)
+    paged.check_status(st)
+    check(q, kp, vp, table, lens, parents, out, lse, window, cap)
+
+
+PAIRS = [("f16", "f16"), ("f16", "f32"), ("f16", "bf16"), ("bf16", "bf16"), ("bf16", "f32"), ("bf16", "f16")]
+MANY = EDGES * 3 + [511, 700, 1025, 64, 191, 5]          # 45 rows: with two kv heads a share for every warpgroup
+
+
+@pytest.mark.parametrize("cache,vec", PAIRS)
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("window,cap", [(0, 0.0), (70, 20.0)])
+def test_many_rows(paged, cache, vec, hd, window, cap):  # noqa: F811
+    run(paged, MANY, 7, 8, 2, hd, 16, cache, vec, window, cap)
+
+
+@pytest.mark.parametrize("cache,vec", PAIRS)
+@pytest.mark.parametrize("nodes,hq,hkv", [(13, 8, 2), (1, 4, 4), (8, 32, 2), (20, 16, 4)])
+def test_many_rows_of_other_sizes(paged, cache, vec, nodes, hq, hkv):  # noqa: F811
+    run(paged, MANY, nodes, hq, hkv, 128, 64, cache, vec, 3, shape="chain")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("nodes,hq,hkv", [(33, 8, 2), (65, 8, 2), (128, 8, 2), (50, 6, 1), (17, 16, 1)])
+@pytest.mark.parametrize("window,cap", [(0, 0.0), (70, 20.0)])
+def test_pairs_of_blocks(paged, dtype, hd, nodes, hq, hkv, window, cap):  # noqa: F811
+    """Two, three and four blocks of rows, the last of three without a partner."""
+    run(paged, [0, 5, 130, 700, -1, 1025], nodes, hq, hkv, hd, 32, dtype, dtype, window, cap)
+
+
+@pytest.mark.parametrize("cache,vec", [p for p in PAIRS if p[0] != p[1]])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("nodes,rows", [(33, 6), (65, 6), (128, 2), (40, 45)])
+@pytest.mark.parametrize("window,cap", [(0, 0.0), (70, 20.0)])
+def test_blocks_of_other_types(paged, cache, vec, hd, nodes, rows, window, cap):  # noqa: F811
+    """More than 128 rows per kv head whose queries are in parts: a block to a CTA."""
+    run(paged, ([0, 5, 130, 700, -1, 1025] + MANY)[:rows], nodes, 8, 2, hd, 32, cache, vec, window, cap)
