@@ -523,8 +523,9 @@ mk_status mk_beam_select_workspace(int groups, int beams, int vocab, size_t* byt
  * absent nodes need no page.  A NaN or infinite value that a node sees makes its results NaN or
  * infinite, as does a NaN key; an infinite key does, unless the query is of the cache's type and
  * the scores stay below +inf.  A probability has 22 bits over an fp16 cache, over a bf16
- * cache 16 where out has 16 bits and 24 where it has 32; the sums, which
- * the tensor cores cut off instead of rounding, keep them within some 5e-6 of their norm. */
+ * cache 16 where out has 16 bits and 24 where it has 32.  The sums of values, which the tensor cores
+ * cut off instead of rounding, are off by at most 2^-16 of sum p |v| in 32-bit outputs (measured: 3e-6), by
+ * 2^-14 in fp16 ones, by 2^-11 in bf16 ones, at any length. */
 typedef struct {
   const void* q;           /* [n_rows][n_nodes][n_heads][head_dim], element strides below    */
   void* out;               /* its vectors must not overlap                                  */

@@ -45,6 +45,16 @@ constexpr int kCopyWarp = 8, kMmaWarp = 9;
 constexpr int kSmemBytes = 227 * 1024;
 constexpr int kLead = 4;                 // tiles that a piece costs besides its own
 constexpr int kJoinThreads = 256;
+// Products that are added up in tensor memory at the most.  The tensor cores cut a sum off where it is longer than 32 bits
+// instead of rounding it, always towards zero, so that a long piece's sums would fall behind by up to 2^-23 a product (32768
+// positions in one piece: 2e-4 of every value).  After so many a row's thread takes its sums out, adds them, rounded, to those
+// before, in the workspace, and begins anew.  For 16-bit outputs as many as may cost a quarter of their least half step.
+template <typename Q>
+constexpr int kSumProducts = 128;
+template <>
+constexpr int kSumProducts<__half> = 512;
+template <>
+constexpr int kSumProducts<__nv_bfloat16> = 4096;
 constexpr long long kWaitCycles = 4000000000ll;  // limit of a wait inside the kernel: two seconds
 
 struct TreeArgs {
@@ -52,6 +62,7 @@ struct TreeArgs {
   void* out;
   float* lse;
   float* part;                           // [CTA][2][HD + 2][rows]: weighted values, maximum, sum
+  float* sums;                           // [CTA][warpgroup][HD][q_rows]: weighted values of a piece's tiles so far
   int4* joins;                           // [CTA]: first and last share, row, kv head
   const int32_t *lens, *parents, *rows, *table;
   int32_t* status;
@@ -138,6 +149,8 @@ struct Shape {
   // ring of which each takes every second tile, one could look for a load whose stage still waits for the other's load
   // before it: loads land in any order, and the parity of a phase but one ago reads as done.)
   static constexpr int RINGS = PAIR ? 1 : 2;
+  // Tiles of a warpgroup whose values are summed in tensor memory before the sum is put away (kSumProducts).
+  static constexpr int kSumTiles = kSumProducts<Q> / (NP * kTile / 16);
   static constexpr int AHEAD = BUFFERS;             // tiles of a ring whose scores are asked for before the first values
   static constexpr int BLOCKS = PAIR ? 2 : 1;       // blocks of rows of a piece
   static constexpr int QUERIES = MODE == TURNS ? 1 : 2;  // places of a block's queries
@@ -274,6 +287,51 @@ __device__ __forceinline__ float capped_fine(float x, float cap) {
   t = fmaf(q, t, -1.f / 3.f);
   t = fmaf(q * x, t, x);
   return q < 0.09f ? cap * t : fmaf(-2.f * cap, r, cap);
+}
+
+// A row's sums from tensor memory to the workspace, added to `f` times those that are there (-1: none are), and zeros in their
+// place; and back, to be added once more.  (A row's words are its own thread's.  Calls, so that the loop over the tiles, which is
+// short of registers, has no part of it; what only adds does not wait for what is there.)
+template <int HD>
+__device__ __noinline__ void put_away(uint32_t t_o, float* sums, int rows, float f) {
+  const bool fresh = f < 0.f, adds = __all_sync(0xffffffffu, f == 1.f);
+#pragma unroll 1
+  for (int x = 0; x < HD / 16; ++x) {
+    uint32_t o[16];
+    tmem_ld(t_o + 16 * x, o);
+    tmem_wait_ld();
+    float* at = sums + (size_t)16 * x * rows;
+    if (adds) {
+#pragma unroll
+      for (int y = 0; y < 16; ++y) atomicAdd(at + y * rows, __uint_as_float(o[y]));
+    } else {
+      float had[16];
+#pragma unroll
+      for (int y = 0; y < 16; ++y) had[y] = fresh ? 0.f : __ldcg(at + y * rows);
+#pragma unroll
+      for (int y = 0; y < 16; ++y) __stcg(at + y * rows, fmaf(f, had[y], __uint_as_float(o[y])));
+    }
+#pragma unroll
+    for (int y = 0; y < 16; ++y) o[y] = 0;
+    tmem_st(t_o + 16 * x, o);
+  }
+  tmem_wait_st();
+}
+template <int HD>
+__device__ __noinline__ void take_back(uint32_t t_o, const float* sums, int rows, float f) {
+#pragma unroll 1
+  for (int x = 0; x < HD / 16; ++x) {
+    uint32_t o[16];
+    float had[16];
+#pragma unroll
+    for (int y = 0; y < 16; ++y) had[y] = __ldcg(sums + (size_t)(16 * x + y) * rows);
+    tmem_ld(t_o + 16 * x, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(fmaf(f, had[y], __uint_as_float(o[y])));
+    tmem_st(t_o + 16 * x, o);
+  }
+  tmem_wait_st();
 }
 
 // two sums or products at a time
@@ -591,6 +649,7 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
     int depth = 0;
     bool there = false;
     const int id = SOLO ? row : tid;      // of the piece's threads
+    float* sums = a.sums + (size_t)(blockIdx.x * 2 + g) * HD * a.q_rows + row;  // what is put away
     while (next_piece(a, w, p)) {
       workers_sync();                      // what the last piece left in shared and tensor memory was read
       if (MODE == TURNS && pieces > 0) wait_phase(&st->q_seen, (pieces - 1) & 1, &st->abort);
@@ -698,6 +757,7 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
       const int lo = there ? from(depth) : p.sp.len;
       const int plain_lo = from(a.n_nodes - 1);  // tiles in [plain_lo, len) are seen by all nodes whole
       float m = -INFINITY, l = 0.f;
+      float away = -INFINITY;             // the maximum of the sums that were put away
       // before the sums so far are touched: the last product is done (of the buffer at hand it is: its scores came after it)
       auto sums_done = [&](int buf) {
         if (SH::BUFFERS == 2) wait_phase(&st->o_done[g][buf ^ 1], (s_phase >> (buf ^ 1) & 1) ^ 1, &st->abort);
@@ -716,6 +776,11 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
         const bool partial = t0 < plain_lo || t0 + kTile > min(p.sp.len, p.sp.hi) || bad != 0;
         unsigned vis[2] = {0, 0};
         if (warp_valid) {
+          if (turn > 0 && turn % SH::kSumTiles == 0) {
+            sums_done(buf);
+            put_away<HD>(t_o, sums, a.q_rows, turn == SH::kSumTiles ? -1.f : away == m ? 1.f : ex2(away - m));
+            away = m;
+          }
           float factor = scale;
           uint32_t s[2][32];
           tmem_ld(t_s, s[0]);
@@ -857,6 +922,10 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
       tiles += p.count;
       loads += 2 * n;
       // ---- the piece's result
+      if (n > SH::kSumTiles && warp_valid) {
+        tmem_fence_after();
+        take_back<HD>(t_o, sums, a.q_rows, away == m ? 1.f : ex2(away - m));
+      }
       if (!there) {                       // (an absent node's row went through the whole tiles with the others)
         m = -INFINITY;
         l = 0.f;
@@ -1093,6 +1162,9 @@ Deal deal(int n_nodes, int group, bool same_type) {
   return d;
 }
 
+// floats of the sums that are put away
+size_t sums_count(int n_sm, int head_dim, int q_rows) { return (size_t)n_sm * 2 * head_dim * q_rows; }
+
 template <typename C, typename Q, int HD, int NQ, int NP, int MODE>
 mk_status launch_mode(TreeArgs a, const mk_page_view& view, int n_sm, void* stream) {
   using SH = Shape<C, Q, HD, NQ, NP, MODE>;
@@ -1159,7 +1231,8 @@ extern "C" mk_status mk_tree_attention_workspace(int n_nodes, int n_heads, int n
       const Deal d = deal(n_nodes, n_heads / n_kv_heads, same);
       rows = std::max<size_t>(rows, d.pair ? d.part_rows : 2 * d.part_rows);
     }
-    *bytes = (size_t)n_sm * (2 * sizeof(int4) + 2 * rows * (head_dim + 2) * sizeof(float));
+    *bytes = (size_t)n_sm * (2 * sizeof(int4) + 2 * rows * (head_dim + 2) * sizeof(float)) +
+             sums_count(n_sm, head_dim, deal(n_nodes, n_heads / n_kv_heads, true).q_rows) * sizeof(float);
     return MK_OK;
   });
 }
@@ -1217,7 +1290,8 @@ extern "C" mk_status mk_tree_attention(const mk_tree_args* args, const mk_page_v
     a.nodes_per_block = d.nodes_per_block; a.blocks = d.blocks; a.parts = d.parts; a.part_rows = d.part_rows;
     a.q_rows = d.q_rows;
     a.joins = static_cast<int4*>(args->workspace);
-    a.part = reinterpret_cast<float*>(a.joins + 2 * n_sm);
+    a.sums = reinterpret_cast<float*>(a.joins + 2 * n_sm);
+    a.part = a.sums + sums_count(n_sm, cache->head_dim, d.q_rows);
     const long long per = 16 / (long long)esz;
     a.q_vec = aligned_to(a.q, 16) && a.q_row % per == 0 && a.q_node % per == 0 && a.q_head % per == 0;
     a.o_vec = aligned_to(a.out, 16) && a.o_row % per == 0 && a.o_node % per == 0 && a.o_head % per == 0;

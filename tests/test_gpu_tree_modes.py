@@ -118,3 +118,50 @@ def test_pairs_of_blocks(paged, dtype, hd, nodes, hq, hkv, window, cap):  # noqa
 def test_blocks_of_other_types(paged, cache, vec, hd, nodes, rows, window, cap):  # noqa: F811
     """More than 128 rows per kv head whose queries are in parts: a block to a CTA."""
     run(paged, ([0, 5, 130, 700, -1, 1025] + MANY)[:rows], nodes, 8, 2, hd, 32, cache, vec, window, cap)
+
+
+def long_sums(paged, cache, vec, n, rows, nodes, hq, hkv, hd):  # noqa: F811
+    """Relative errors [some rows, nodes, heads, dims] of rows that all read one sequence of n positions, each of about the same
+    weight, the values of every dim about a mean of its own in [1, 2]."""
+    g = gen(21)
+    ps, pages = 64, -(-(n + nodes) // 64)
+    kp, vp = (torch.randn(pages, hkv, ps, hd, generator=g, device=DEV) for _ in range(2))
+    vp = vp * 0.25 + 1 + torch.rand(hkv, 1, hd, generator=g, device=DEV)
+    kp, vp = kp.to(TYPES[cache]), vp.to(TYPES[cache])
+    table = torch.randperm(pages, generator=g, device=DEV)[None].cpu().numpy().astype(np.int32)
+    q = torch.randn(rows, nodes, hq, hd, generator=g, device=DEV).mul_(0.2).to(TYPES[vec])
+    parents = [[-1] + [0] * (nodes - 1)] * rows
+    st = status()
+    out, lse = paged.tree_attention(q, kp, vp, ints(table), ints([n] * rows), ints(parents), rows=ints([0] * rows), return_lse=True,
+                                    status=st)
+    paged.check_status(st)
+    off = []
+    for r in range(0, rows, max(1, rows // 4)):
+        w, l, _, _ = plain_tree(q[r], kp, vp, table, n, 0, parents[r], 1 / math.sqrt(hd))
+        off.append((out[r].double() - w) / w)
+        # scores of 32-bit sums, exp2 and the maximum (scores below 2), the parts' rounding and sums that are rounded
+        assert (lse[r].double() - l).abs().max() <= 2.0 ** -16
+    return torch.stack(off)
+
+
+@pytest.mark.parametrize("cache,nodes,rows,hq,hkv,hd", [
+    ("f16", 4, 64, 8, 4, 64),        # a share to each warpgroup
+    ("bf16", 4, 64, 8, 4, 64),
+    ("bf16", 4, 64, 8, 4, 128),
+    ("f16", 40, 52, 16, 4, 128),     # two blocks of parts
+    ("bf16", 64, 16, 4, 2, 64),      # one block, tiles by turns
+    ("f16", 16, 2, 16, 8, 128),
+])
+def test_long_sums_of_32_bits(paged, cache, nodes, rows, hq, hkv, hd):  # noqa: F811
+    """The products of the values are cut off, not rounded: at most 128 of them are added before what they gave is put away,
+    which is off by 128 2^-23 at most.  The rest, all of it roundings that know no direction, stays below 2^-19."""
+    off = long_sums(paged, cache, "f32", 32768, rows, nodes, hq, hkv, hd)
+    assert off.abs().max() <= 128 * 2.0 ** -23 + 2.0 ** -19
+
+
+@pytest.mark.parametrize("nodes,rows", [(33, 80), (4, 160)])
+def test_long_sums_of_16_bits(paged, nodes, rows):  # noqa: F811
+    """The same with 512 products at a time, as the mean over many values, whose own roundings of up to 2^-12 cancel: 512 2^-23
+    and three deviations, 2^-12 / sqrt(3 * 256) each, of the mean over 256 dims."""
+    off = long_sums(paged, "f16", "f16", 131072, rows, nodes, 8, 2, 128)
+    assert off.mean().abs() <= 512 * 2.0 ** -23 + 3 * 2.0 ** -12 / math.sqrt(3 * 256)
