@@ -398,7 +398,7 @@ mk_status mk_rope_append_at(const mk_append_args* args, const int32_t* slots, co
                             void* stream);
 
 /* Attention of one new query per row over its paged positions:
- *   s_t = cap(scale * q . k_t),  cap(x) = softcap * tanh(x / softcap) (softcap 0: x),
+ *   s_t = cap(scale * q . k_t),  cap(x) = softcap * tanh(x / softcap) (softcap 0, or 2^64 and more: x),
  *   out = sum_t e^(s_t) v_t / sum_t e^(s_t),  lse = log sum_t e^(s_t)   (natural log)
  * over t in [max(0, n - window), n) (window 0: [0, n)), n = lens[r] + len_add.  Query head h
  * reads kv head h / (n_heads / n_kv_heads).  A row without positions (n <= 0) or whose
@@ -515,7 +515,8 @@ mk_status mk_beam_select_workspace(int groups, int beams, int vocab, size_t* byt
  * row (mk_rope_append_at puts them there), its position is lens[r] + the number of its ancestors.
  *
  * Attention of every node over the row's slots [0, lens[r]) and over its ancestors and itself:
- * scores, softmax and log-sum-exp as mk_paged_attention's.  window > 0: only positions above the
+ * scores, softmax and log-sum-exp as mk_paged_attention's (with 16-bit outputs a softcap of up to 64
+ * moves a score by up to 2^-16).  window > 0: only positions above the
  * node's own minus window.  An absent node, and every node of a row whose lens is negative or
  * that is outside the table, gets zeros and lse -inf.  Nothing that a node does not see is read
  * for its value: whatever lies there, NaN included, has no effect on it.  Slots that a node should

@@ -800,7 +800,7 @@ mk_status attend_pages(const mk_attend_args& attend, const mk_page_view& view, l
   if (args->n_rows < 0 || (long long)args->n_rows * args->n_heads > 0x7fffffffLL)
     return paged_fail(MK_ERR_INVALID, "n_rows out of range");
   if (args->window < 0) return paged_fail(MK_ERR_INVALID, "window must not be negative");
-  const float factor = args->softcap > 0.f ? args->scale / args->softcap : args->scale * kLog2e;
+  const float softcap = cap_of(args->softcap), factor = softcap > 0.f ? args->scale / softcap : args->scale * kLog2e;
   if (!(args->softcap >= 0.f && args->softcap * kLog2e < INFINITY) || !(fabsf(factor) < INFINITY))
     return paged_fail(MK_ERR_INVALID, "scale or softcap is not finite, too large, or softcap negative or too small for scale");
   const size_t esz = args->dtype == MK_F32 ? 4 : 2;
@@ -837,7 +837,7 @@ mk_status attend_pages(const mk_attend_args& attend, const mk_page_view& view, l
   a.q_vec = aligned_to(a.q, 16) && a.q_row * (long long)esz % 16 == 0 && a.q_head * (long long)esz % 16 == 0;
   a.by_segment = (long long)a.n_rows * a.hkv <= a.n_cta;
   a.scale = factor;
-  a.softcap = args->softcap * kLog2e;
+  a.softcap = softcap * kLog2e;
   if (before) {
     s = before();
     if (s) return s;

@@ -94,6 +94,10 @@ std::string check_line(const mk_page_view* c, long long n_rows, int window);
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
+// A cap of 2^64 and more is none: scores that it would change have long left all others behind, and in its units (scale / cap,
+// at a power of two of the head's own) common ones would lose bits below the normal numbers.
+inline float cap_of(float softcap) { return softcap < 0x1p64f ? softcap : 0.f; }
+
 #ifdef __CUDACC__
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

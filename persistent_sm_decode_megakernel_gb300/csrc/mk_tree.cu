@@ -266,15 +266,19 @@ __device__ __forceinline__ unsigned ones(int x, int y) {
 }
 
 // cap tanh(x / (2 log2 e)) = cap - 2 cap / (2^x + 1), off by 2^-22 cap: two of the hardware's approximations (2 ulp, 1 ulp) in the
-// place of tanhf's 25 instructions, which took three times a tile's softmax
+// place of tanhf's 25 instructions, which took three times a tile's softmax.  For 16-bit outputs and caps up to 64, where that
+// is 2^-16 of a score, a sixteenth of fp16's half step in a probability (33 rows x 7 nodes x 700, 16 heads over 8, cap 30: 35 us,
+// with the finer one below 50).
+constexpr float kCoarseCap = 64.f;
 __device__ __forceinline__ float capped(float x, float cap) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(x) + 1.f));
   return fmaf(-2.f * cap, r, cap);
 }
 
-// The same for 32-bit outputs, off by 2^-23 cap at most and by 2^-23 of itself up to a third of the cap: small ones by the
-// series of tanh (through x^11), the others with one step of Newton's behind the reciprocal's approximation.
+// cap tanh(x) for 32-bit outputs and larger caps, off by 2^-23 cap at most and by 2^-23 of itself up to a third of the cap, so
+// that a cap far above the scores costs them nothing: small ones by the series of tanh (through x^11), the others with one
+// step of Newton's behind the reciprocal's approximation.
 __device__ __forceinline__ float capped_fine(float x, float cap) {
   const float d = ex2(x * (2.f * kLog2e)) + 1.f;
   float r;
@@ -788,12 +792,16 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
           tmem_wait_ld();
           if (a.softcap > 0.f) {
             factor = 1.f;
-            const float twice = scale * (2.f * kLog2e);
+            if (std::is_same<Q, float>::value || a.softcap > kCoarseCap * kLog2e) {
 #pragma unroll
-            for (int x = 0; x < kTile; ++x)
-              s[x >> 5][x & 31] = __float_as_uint(std::is_same<Q, float>::value
-                                                      ? capped_fine(__uint_as_float(s[x >> 5][x & 31]) * scale, a.softcap)
-                                                      : capped(__uint_as_float(s[x >> 5][x & 31]) * twice, a.softcap));
+              for (int x = 0; x < kTile; ++x)
+                s[x >> 5][x & 31] = __float_as_uint(capped_fine(__uint_as_float(s[x >> 5][x & 31]) * scale, a.softcap));
+            } else {
+              const float twice = scale * (2.f * kLog2e);
+#pragma unroll
+              for (int x = 0; x < kTile; ++x)
+                s[x >> 5][x & 31] = __float_as_uint(capped(__uint_as_float(s[x >> 5][x & 31]) * twice, a.softcap));
+            }
           }
           if (partial) {
 #pragma unroll
@@ -1250,7 +1258,7 @@ extern "C" mk_status mk_tree_attention(const mk_tree_args* args, const mk_page_v
     if (args->n_rows < 0 || (long long)args->n_rows * args->n_nodes * args->n_heads > 0x7fffffffLL / cache->head_dim)
       return paged_fail(MK_ERR_INVALID, "n_rows * n_nodes * n_heads * head_dim must be in [0, 2^31)");
     if (args->window < 0) return paged_fail(MK_ERR_INVALID, "window must not be negative");
-    const float factor = args->softcap > 0.f ? args->scale / args->softcap : args->scale * kLog2e;
+    const float softcap = cap_of(args->softcap), factor = softcap > 0.f ? args->scale / softcap : args->scale * kLog2e;
     if (!(args->softcap >= 0.f && 2.f * args->softcap * kLog2e < INFINITY) || !(std::abs(factor) * 2.f * kLog2e < INFINITY))
       return paged_fail(MK_ERR_INVALID, "scale or softcap is not finite, too large, or softcap negative or too small for scale");
     const size_t esz = args->dtype == MK_F32 ? 4 : 2;
@@ -1300,7 +1308,7 @@ extern "C" mk_status mk_tree_attention(const mk_tree_args* args, const mk_page_v
     a.q_and = factor == 0.f ? 0u : 0xffffffffu;
     a.q_xor = factor < 0.f ? 0x80008000u : 0u;
     a.group_inverse = (65536 + a.group - 1) / a.group;
-    a.softcap = args->softcap * kLog2e;
+    a.softcap = softcap * kLog2e;
     // 16-bit queries of the cache's type are exact in one part, others are split into 2 parts of fp16 (22
     // bits, each head at a power of two of its own) or 3 of bf16 (24 bits); probabilities likewise, 2 parts of bf16 (16
     // bits) being enough for an output of 16 bits, as for single tokens.  (One part, 8 or 11 bits, is as far off as the

@@ -120,6 +120,32 @@ def test_blocks_of_other_types(paged, cache, vec, hd, nodes, rows, window, cap):
     run(paged, ([0, 5, 130, 700, -1, 1025] + MANY)[:rows], nodes, 8, 2, hd, 32, cache, vec, window, cap)
 
 
+@pytest.mark.parametrize("cache,vec", PAIRS)
+@pytest.mark.parametrize("cap", [0.5, 50.0, 64.0, 65.0, 1e3, 1e5, 1e8, 1e15, 1e30, 1e37])
+def test_caps_of_any_size(paged, cache, vec, cap):  # noqa: F811
+    """A capped score is as exact as an uncapped one, whatever the cap."""
+    run(paged, [0, 90, 300], 3, 4, 2, 64, 16, cache, vec, cap=cap, size=3.0)
+
+
+@pytest.mark.parametrize("cache,vec", PAIRS)
+def test_caps_beyond_all_scores_are_none(paged, cache, vec):  # noqa: F811
+    """From 2^64 on, bit for bit, here and in the attention of single tokens and of chosen pages."""
+    g = gen(26)
+    kp, vp, table = make_cache(g, [203], 2, 64, 16, cache)
+    q = torch.randn(1, 3, 4, 64, generator=g, device=DEV).to(TYPES[vec])
+    tb, n = ints(table), ints([200])
+    scores = torch.randn(1, 2, table.shape[1], generator=g, device=DEV)
+    calls = (lambda c: paged.tree_attention(q, kp, vp, tb, n, ints([[-1, 0, 1]]), softcap=c, return_lse=True),
+             lambda c: paged.paged_attention(q[:, 0], kp, vp, tb, n, softcap=c, return_lse=True),
+             lambda c: paged.sparse_attention(q[:, 0], kp, vp, tb, n, scores, 5, softcap=c, return_lse=True))
+    for call in calls:
+        want = call(0.0)
+        for cap in (2.0 ** 64, 1e37):
+            assert all(torch.equal(x, y) for x, y in zip(call(cap), want)), cap
+        w, l = call(1e19)
+        assert (w.float() - want[0].float()).abs().max() <= 2.0 ** -6 and (l - want[1]).abs().max() <= 2.0 ** -17
+
+
 def long_sums(paged, cache, vec, n, rows, nodes, hq, hkv, hd):  # noqa: F811
     """Relative errors [some rows, nodes, heads, dims] of rows that all read one sequence of n positions, each of about the same
     weight, the values of every dim about a mean of its own in [1, 2]."""
