@@ -476,8 +476,11 @@ __global__ void __launch_bounds__(tree_threads(MODE), 1) tree_kernel(const __gri
         const Span s = span_of(a, r);
         if (s.len >= 0 && (unsigned)s.trow >= (unsigned)a.table_rows)
           report(a.status, MK_ERR_PAGES, PO_TREE, r, s.trow);
-        else if (s.len > a.cap)
-          report(a.status, MK_ERR_PAGES, PO_TREE, r, s.len);
+        else if (s.len >= a.cap) {  // every node's slot is past the table (there may be no tile whose softmax could tell)
+          bool some = false;
+          for (int i = 0; i < a.n_nodes; ++i) some = some || a.parents[(long long)r * a.n_nodes + i] == -1;
+          if (some) report(a.status, MK_ERR_PAGES, PO_TREE, r, s.len);
+        }
       }
   }
   tmem_fence_before();

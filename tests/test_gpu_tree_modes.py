@@ -191,3 +191,25 @@ def test_long_sums_of_16_bits(paged, nodes, rows):  # noqa: F811
     and three deviations, 2^-12 / sqrt(3 * 256) each, of the mean over 256 dims."""
     off = long_sums(paged, "f16", "f16", 131072, rows, nodes, 8, 2, 128)
     assert off.mean().abs() <= 512 * 2.0 ** -23 + 3 * 2.0 ** -12 / math.sqrt(3 * 256)
+
+
+def test_a_window_of_one_past_a_full_table_is_reported(paged):  # noqa: F811
+    """A sequence that fills its table: every node's own slot is past it.  Nothing is seen, and it is told, unless no node is there."""
+    from persistent_sm_decode_megakernel_gb300 import MK_ERR_PAGES, MkError
+    g = gen(22)
+    kp, vp, table = make_cache(g, [64, 64], 2, 64, 16, "f16")
+    table = table[:, :4].copy()
+    q = torch.randn(2, 3, 4, 64, generator=g, device=DEV).half()
+    for window in (1, 2, 0):
+        for parents, told in (([[-2, 0, 1], [-2, 0, 1]], False), ([[-2, 0, 1], [-2, -1, 1]], True), ([[-1, 0, 1]] * 2, True)):
+            for lens in ([64, 64], [64, 100]):
+                st = status()
+                out, lse = paged.tree_attention(q, kp, vp, ints(table), ints(lens), ints(parents), window=window, return_lse=True, status=st)
+                if told:
+                    with pytest.raises(MkError) as e:
+                        paged.check_status(st)
+                    assert e.value.status == MK_ERR_PAGES and "tree" in str(e.value)
+                else:
+                    paged.check_status(st)
+                if window == 1 or not told:
+                    assert torch.all(out == 0) and torch.all(lse == -math.inf)
