@@ -336,7 +336,8 @@ mk_status mk_stream_bench(int page_bytes, int n_pages, int mode, int hint, long 
  * value} (operator: 1 append, 2 attention, 3 update, 4 compaction, 5 selection, 6 tree, 7
  * acceptance, 8 bounds, 9 page scores, 10 chosen pages) and
  * mk_paged_status reads it back.  A bad index is never followed: each call says what it
- * does instead. */
+ * does instead.  MK_ERR_TIMEOUT (tree attention; row -1, a CTA's number): a wait inside the kernel
+ * took two seconds and was given up, the call's outputs mean nothing; without a status nobody is told. */
 typedef struct {
   void *k, *v;             /* one layer's pages, 16-byte aligned                            */
   long long page_stride;   /* elements from one page to the next, a multiple of 8           */

@@ -392,7 +392,9 @@ extern "C" mk_status mk_paged_status(int32_t* status, void* stream) {
                                       "tree attention", "acceptance", "bounds", "page scores", "chosen pages"};
     char buf[160];
     snprintf(buf, sizeof buf, "%s: %s at row %d, value %d", ops[got[1] >= 1 && got[1] <= 10 ? got[1] : 0],
-             got[0] == MK_ERR_NAN ? "a NaN or infinite logit" : "a bad page, row, length or parent, or too few free pages",
+             got[0] == MK_ERR_NAN       ? "a NaN or infinite logit"
+             : got[0] == MK_ERR_TIMEOUT ? "a wait inside the kernel ran out, its outputs mean nothing,"
+                                        : "a bad page, row, length or parent, or too few free pages",
              got[2], got[3]);
     return paged_fail((mk_status)got[0], buf);
   });

@@ -213,3 +213,12 @@ def test_a_window_of_one_past_a_full_table_is_reported(paged):  # noqa: F811
                     paged.check_status(st)
                 if window == 1 or not told:
                     assert torch.all(out == 0) and torch.all(lse == -math.inf)
+
+
+def test_a_wait_that_ran_out_is_told_as_one(paged):  # noqa: F811
+    from persistent_sm_decode_megakernel_gb300 import MK_ERR_TIMEOUT, MkError
+    st = ints([MK_ERR_TIMEOUT, 6, -1, 17])
+    with pytest.raises(MkError) as e:
+        paged.check_status(st)
+    assert e.value.status == MK_ERR_TIMEOUT and "wait" in str(e.value) and "bad page" not in str(e.value)
+    paged.check_status(st)
