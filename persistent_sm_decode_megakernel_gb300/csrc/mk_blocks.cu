@@ -314,7 +314,8 @@ __global__ void __launch_bounds__(kScoreThreads, 2) scores_kernel(const __grid_c
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) best[e] = fmaxf(best[e], __shfl_xor_sync(0xffffffffu, best[e], o));
-        if (__any_sync(0xffffffffu, odd)) {  // the four lanes of a page together, what is not a half's to add adds nothing
+        // the four lanes of a page together; what is not a half's to add adds nothing, but a NaN bound is one under any query
+        if (__any_sync(0xffffffffu, odd)) {
           float most = -INFINITY;
           for (int h = 0; h < a.group; ++h) {
             float s = 0.f;
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) scores_kernel(const __grid_c
                   lo = Conv<C>::up(b0[(long long)mine * a.hkv * 2 * HD + 32 * i + e]);
                   hi = Conv<C>::up(b0[(long long)mine * a.hkv * 2 * HD + HD + 32 * i + e]);
                 }
-                s += x == 0.f ? 0.f : x > 0.f ? x * hi : x * lo;
+                s += !(lo == lo && hi == hi) ? lo + hi : x == 0.f ? 0.f : x > 0.f ? x * hi : x * lo;
               }
             s += __shfl_xor_sync(0xffffffffu, s, 1);
             s += __shfl_xor_sync(0xffffffffu, s, 2);

@@ -1025,3 +1025,25 @@ def test_one_slot_for_two_tokens_and_slots_that_are_none(paged):
             with pytest.raises(MkError) as e:
                 paged.check_status(st)
             assert e.value.status == MK_ERR_PAGES and torch.equal(pages, keep)
+
+
+
+@pytest.mark.parametrize("vec", ["bf16", "f32"])
+@pytest.mark.parametrize("hq", [2, 12])
+def test_scores_of_nan_bounds_under_any_query(paged, vec, hq):
+    """A NaN bound makes the score NaN whatever the query holds there, zeros of either sign included; an infinite one
+    under a zero adds nothing."""
+    for zero in (0.0, -0.0, 2.0, -2.0):
+        bounds = torch.stack((-torch.ones(6, 1, 64), torch.ones(6, 1, 64)), 2).to(DEV).bfloat16()
+        bounds[0, 0, :, 5], bounds[1, 0, 0, 5], bounds[2, 0, 1, 5] = math.nan, math.nan, math.nan
+        bounds[3, 0, 0, 5], bounds[3, 0, 1, 5] = -math.inf, math.inf
+        bounds[4, 0, 0, 7], bounds[4, 0, 1, 9] = math.nan, math.inf
+        q = torch.ones(1, hq, 64, device=DEV).to(TYPES[vec])
+        q[..., 5] = zero
+        got = paged.page_scores(q, bounds, ints([[0, 1, 2, 3, 4, 5]]), ints([96]), 16)[0, 0].tolist()
+        assert all(math.isnan(got[i]) for i in (0, 1, 2, 4)), got
+        assert got[3] == (63 if zero == 0 else math.inf) and got[5] == 63 + abs(zero), got
+    q[..., 5] = 0.0
+    q[0, 1, 3] = math.nan
+    got = paged.page_scores(q, bounds, ints([[0, 1, 2, 3, 4, 5]]), ints([96]), 16)[0, 0].tolist()
+    assert all(math.isnan(x) for x in got), got
