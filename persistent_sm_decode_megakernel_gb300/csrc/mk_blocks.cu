@@ -583,16 +583,18 @@ extern "C" mk_status mk_page_scores(const mk_scores_args* args, const mk_page_vi
     a.table_rows = cache->n_rows; a.width = cache->table_width;
     const long long per = args->dtype == MK_F32 ? 4 : 8;
     a.q_vec = aligned_to(a.q, 16) && a.q_row % per == 0 && a.q_head % per == 0;
-    // pages of a CTA: as many as leave two CTAs for every SM (one wave), in whole turns of its warps, up to 96 (16 ragged
-    // rows of up to 2048 pages: 21.6 us; 64 pages 25.7, 128 23.5, 256 34.4)
+    // pages of a CTA: as many as leave two CTAs for every SM (one wave), in whole turns of its warps, up to 96 or what whole
+    // turns leave of that (8 kv heads, 16 ragged rows of up to 2048 pages: 21.6 us; 64 pages 25.7, 128 23.5, 256 34.4)
     int n_sm = 0;
     const mk_status s = sm_count(&n_sm);
     if (s) return s;
     const int turn = kScorePages * std::max(1, kScoreWarps / a.hkv);
     const long long want = (long long)a.width * a.n_rows / (2LL * n_sm);
-    a.chunk = (int)std::min<long long>(96, std::max<long long>(1, want / turn) * turn);
-    // queries of the bounds' type are exact in one part, others are split into 2 parts of fp16 (22 bits, each head
-    // at a power of two of its own) or 3 of bf16 (24 bits; fp16 queries: 2, 16 bits and more than their 11)
+    a.chunk = (int)std::min<long long>(96 / turn, std::max<long long>(1, want / turn)) * turn;
+    // queries of the bounds' type are exact in one part, others are split as the attention splits them: into 2 parts of
+    // fp16 (22 bits, each head at a power of two of its own; a third part would bring 32-bit queries' scores from 2.6e-7
+    // to 1e-7 of 64 bits and take 16 rows of 24576 positions in pages of 16 from 21.6 to 29.9 us) or 3 of bf16 (24 bits; fp16
+    // queries: 2, 16 bits and more than their 11)
     const int d = cache->head_dim;
     if (cache->dtype == MK_F16) {
       if (args->dtype == MK_F16) return launch_scores<__half, __half, 1>(a, d, stream);
