@@ -584,13 +584,14 @@ typedef struct {
 mk_status mk_update_bounds(const mk_bounds_args* args, const mk_page_view* cache, int32_t* status, void* stream);
 
 /* scores [n_rows][n_kv_heads][table_width]: of the heads of a group the greatest
- * sum_d max(q_d low_d, q_d high_d), which no key within the page's bounds exceeds; in 32 bits.
+ * sum_d max(q_d low_d, q_d high_d), which no key within the page's bounds exceeds; summed in 32 bits, of
+ * queries in 32 bits or their own type, over fp16 bounds in 22 where their type is another.
  * -inf for table entries behind a row's last page, for bad pages (reported) and for rows
  * outside the table (reported).  NaN in a query or a page's bounds makes the score NaN. */
 typedef struct {
   const void* q;           /* [n_rows][n_heads][head_dim], element strides below            */
   int dtype;               /* of q: MK_F16, MK_BF16 or MK_F32                               */
-  int n_rows, n_heads;     /* n_heads / n_kv_heads: 1..16                                   */
+  int n_rows, n_heads;     /* n_rows up to 65535; n_heads / n_kv_heads: 1..16               */
   long long q_row, q_head;
   const void* bounds;
   const int32_t *lens, *rows;

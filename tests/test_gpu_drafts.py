@@ -1047,3 +1047,24 @@ def test_scores_of_nan_bounds_under_any_query(paged, vec, hq):
     q[0, 1, 3] = math.nan
     got = paged.page_scores(q, bounds, ints([[0, 1, 2, 3, 4, 5]]), ints([96]), 16)[0, 0].tolist()
     assert all(math.isnan(x) for x in got), got
+
+
+@pytest.mark.parametrize("cache,vec", [("f16", "f32"), ("bf16", "f32"), ("f16", "f16"), ("bf16", "f16")])
+@pytest.mark.parametrize("hd,hq,hkv", [(128, 16, 1), (64, 8, 2)])
+def test_scores_are_held_in_32_bits(paged, cache, vec, hd, hq, hkv):
+    """Bounds of 1 at one dim and of 0 at all others, so that a score is one element of a head, beside a large one at a dim of
+    its own.  Queries that enter whole give it exactly; of 32-bit ones over fp16 bounds, whose two parts hold 11 bits each of
+    what is left, at most 2^-12 of at most 2^-11 of it is lost."""
+    g = gen(24)
+    ps, pages = 16, 64
+    at = torch.arange(pages, device=DEV) % (hd - 1) + 1                  # the dim that page j looks at
+    bounds = torch.zeros(pages, hkv, 2, hd, device=DEV)
+    bounds.scatter_(3, at[:, None, None, None].expand(pages, hkv, 2, 1), 1.0)
+    q = torch.randn(1, hq, hd, generator=g, device=DEV).abs().add_(0.5).to(TYPES[vec])
+    q[..., 0] = 30.0
+    got = paged.page_scores(q, bounds.to(TYPES[cache]), ints([list(range(pages))]), ints([ps * pages]), ps)[0]
+    want = q[0].view(hkv, hq // hkv, hd).amax(1).float()[:, at]
+    if (cache, vec) == ("f16", "f32"):
+        assert ((got - want).abs() <= want * 2.0 ** -23).all()
+    else:
+        assert torch.equal(got, want)
