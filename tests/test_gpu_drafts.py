@@ -1027,6 +1027,22 @@ def test_one_slot_for_two_tokens_and_slots_that_are_none(paged):
             assert e.value.status == MK_ERR_PAGES and torch.equal(pages, keep)
 
 
+# --------------------------------------------------------------------- what the tests above do not look at
+def test_accept_leaves_what_lies_between_the_layers(paged):
+    """Layers that hold a page more than the pool: trees that are taken over to the end change nothing of it."""
+    rows, nodes, ps, n_pages = 3, 6, 16, 8
+    pages = torch.randn(2, 3, n_pages + 1, 2, ps, 64, generator=gen(23), device=DEV).half()
+    keep = pages.clone()
+    table = ints([[7, 0], [1, 6], [5, 2]])
+    # every second node is the chosen one's child: all of the others' vectors move
+    parents, tokens = [[-1, 0, 0, 2, 2, 4]] * rows, [[1, 9, 2, 9, 3, 4]] * rows
+    n = ints([14, 0, 26])
+    count = paged.accept_drafts(pages[0][:, :n_pages], pages[1][:, :n_pages], table, n, ints(tokens), ints(parents),
+                                ints([[2, 0, 3, 0, 4, 5]] * rows))[2]
+    assert count.tolist() == [4, 4, 4] and n.tolist() == [18, 4, 30]
+    assert torch.equal(pages[:, :, n_pages], keep[:, :, n_pages]) and not torch.equal(pages, keep)
+    assert torch.equal(pages[:, :, [3, 4]], keep[:, :, [3, 4]])          # pages of no row
+
 
 @pytest.mark.parametrize("vec", ["bf16", "f32"])
 @pytest.mark.parametrize("hq", [2, 12])
@@ -1068,3 +1084,30 @@ def test_scores_are_held_in_32_bits(paged, cache, vec, hd, hq, hkv):
         assert ((got - want).abs() <= want * 2.0 ** -23).all()
     else:
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("cache,vec,hq,hkv", [("bf16", "bf16", 8, 2), ("f16", "f32", 16, 1), ("f16", "f16", 3, 3)])
+def test_no_key_of_a_page_exceeds_its_score(paged, cache, vec, hq, hkv):
+    """Append, bounds and scores together, step after step: a page's score is no less than the product of any of the heads with
+    any key in it, but for the rounding of sums of 2 hd products of which each element is at most the bounds' greater one (as in
+    test_scores)."""
+    g = gen(25)
+    hd, ps, start, steps = 64, 16, [30, 61, 0], 20
+    kp, vp, table = make_cache(g, [n + steps for n in start], hkv, hd, ps, cache)
+    tb, n = ints(table), ints(start)
+    freqs, m = paged.rope_freqs(10000.0, hd, device=DEV)
+    bounds = torch.full((kp.shape[0], hkv, 2, hd), math.nan, dtype=kp.dtype, device=DEV)
+    paged.update_bounds(kp, bounds, tb, n, new=max(start))
+    for i in range(steps):
+        x = torch.randn(3, hq + 2 * hkv, hd, generator=g, device=DEV).to(TYPES[vec])
+        q = paged.rope_append(x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], kp, vp, tb, n, freqs=freqs, mscale=m)
+        n += 1
+        paged.update_bounds(kp, bounds, tb, n)
+        got, qd, kd = f64(paged.page_scores(q, bounds, tb, n, ps)), f64(q), f64(kp)
+        for r in range(3):
+            for j in range(-(-(start[r] + i + 1) // ps)):
+                keys = kd[table[r, j], :, : start[r] + i + 1 - j * ps]
+                for h in range(hkv):
+                    heads = qd[r, h * (hq // hkv): (h + 1) * (hq // hkv)]
+                    size = (np.abs(heads) @ np.abs(keys[h]).max(0)).max()
+                    assert got[r, h, j] >= (heads @ keys[h].T).max() - size * ((hd + 16) * 2.0 ** -23 + 2.0 ** -22), (i, r, h, j)
