@@ -256,7 +256,8 @@ class PagedDecoder:
 
     def update(self, parents=None, reserve=None):
         """Every row continues row parents[r] (-1: it is freed) and reserves pages for reserve[r] more
-        positions (mk_update_pages).  It runs on self.stream, where tensors given have to be ready."""
+        positions (mk_update_pages; pages reserved before and not filled are given back).  It runs on self.stream,
+        where tensors given have to be ready."""
         with torch.cuda.stream(self.stream):
             parents, reserve = (None if x is None else self._used(self._int32(x)) for x in (parents, reserve))
             self.paged.update_pages(self.k, self.v, self.table, self.lens, self.refs, parents, reserve, self.status)
@@ -311,8 +312,9 @@ class PagedDecoder:
     def verify(self, tokens, parents, rows, logits=None):
         """Reserves pages for trees of drafted tokens, runs one step over them and takes over what the model agrees with
         (paged.accept_drafts): tokens and parents [len(rows), nodes] for different table rows `rows` (numbers), node 0 of
-        each being the token that stands.  lens of the rows grows.  Returns the next tokens, the accepted nodes (both
-        [len(rows), nodes], -1 behind the last) and their number [len(rows)], on the device; synchronize reports what
+        each being the token that stands.  lens of the rows grows; other rows
+        keep the pages that they reserved.  Returns the next tokens, the accepted nodes (both [len(rows), nodes], -1 behind
+        the last) and their number [len(rows)], on the device.  Synchronize reports what
         went wrong there."""
         n_rows = self.table.shape[0]
         rows = [int(r) for r in rows]
@@ -325,9 +327,12 @@ class PagedDecoder:
             nodes = tokens.shape[1]
             if len(rows) * nodes > self.dm.max_batch:
                 raise ValueError("rows * nodes must be at most max_batch")
-            reserve = [nodes if r in rows else 0 for r in range(n_rows)]
-            self.update(reserve=reserve)
             at = self._int32(rows)
+            # the pages that other rows hold behind their positions are what they reserved
+            held = (self.table >= 0).sum(1, dtype=torch.int32) * self.page_size
+            reserve = torch.where(held - self.lens >= self.page_size, held - self.lens, 0)
+            reserve[at.long()] = nodes
+            self.update(reserve=reserve)
             out = self.step_tree(tokens, parents, self.lens[at.long()], at, logits)
             every = torch.full((3, n_rows, nodes), -2, dtype=torch.int32, device=self.k.device)   # rows without a tree: absent
             every[:, at.long()] = torch.stack((tokens, parents, out))

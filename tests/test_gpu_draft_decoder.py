@@ -196,3 +196,25 @@ def test_tree_steps_refuse_what_does_not_fit(lib):
     assert len(tokens) == 3
     dec.close()
     side.close()
+
+
+def test_verify_leaves_other_rows_what_they_reserved(lib):
+    """A row that reserved ahead steps on after another row's verify, and its pages stay counted."""
+    cfg = synth.CONFIGS["tiny"]
+    w = synth.gen_weights(cfg)
+    dec = _paged(lib, cfg, w, 8, 3, 96)
+    a, b = (synth.gen_prompts(cfg, 1, 14)[0], synth.gen_prompts(cfg, 1, 10)[0])
+    first = dec.prefill({0: a, 1: b})
+    dec.update(reserve=[0, 40, 0])
+    held = (dec.table[1] >= 0).sum().item()
+    assert held == 4
+    dec.verify([[int(first[0]), 5, 6]], [[-1, 0, 0]], [0])
+    dec.synchronize()
+    assert (dec.table[1] >= 0).sum().item() == held and (dec.table[2] >= 0).sum().item() == 0
+    assert dec.refs.sum().item() == (dec.table >= 0).sum().item()
+    tok = first[1]
+    for i in range(30):
+        tok = dec.step(tok.contiguous(), dec.lens[1:2].contiguous(), dec._int32([1]))
+        dec.lens[1] += 1
+    dec.synchronize()
+    dec.close()
