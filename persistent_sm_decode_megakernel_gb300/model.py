@@ -314,8 +314,8 @@ class PagedDecoder:
         (paged.accept_drafts): tokens and parents [len(rows), nodes] for different table rows `rows` (numbers), node 0 of
         each being the token that stands.  lens of the rows grows; other rows
         keep the pages that they reserved.  Returns the next tokens, the accepted nodes (both [len(rows), nodes], -1 behind
-        the last) and their number [len(rows)], on the device.  Synchronize reports what
-        went wrong there."""
+        the last) and their number [len(rows)], on the device.  Synchronize reports what went wrong there: where the pages
+        do not suffice, or an error that self.status holds is still to be read, no row takes anything over."""
         n_rows = self.table.shape[0]
         rows = [int(r) for r in rows]
         if len(set(rows)) != len(rows) or any(not 0 <= r < n_rows for r in rows):
@@ -333,6 +333,9 @@ class PagedDecoder:
             reserve = torch.where(held - self.lens >= self.page_size, held - self.lens, 0)
             reserve[at.long()] = nodes
             self.update(reserve=reserve)
+            # what the device finds wrong makes every node absent
+            right = self.status[0] == 0
+            parents = torch.where(right, parents, -2)
             out = self.step_tree(tokens, parents, self.lens[at.long()], at, logits)
             every = torch.full((3, n_rows, nodes), -2, dtype=torch.int32, device=self.k.device)   # rows without a tree: absent
             every[:, at.long()] = torch.stack((tokens, parents, out))

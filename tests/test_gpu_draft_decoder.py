@@ -218,3 +218,32 @@ def test_verify_leaves_other_rows_what_they_reserved(lib):
         dec.lens[1] += 1
     dec.synchronize()
     dec.close()
+
+
+def test_verify_without_pages_takes_nothing_over(lib):
+    """A row whose last page is shared, and no free page for its copy: the shared page, both rows and what is returned say so."""
+    from persistent_sm_decode_megakernel_gb300 import MK_ERR_PAGES, MkError
+    cfg = synth.CONFIGS["tiny"]
+    w = synth.gen_weights(cfg)
+    dec = _paged(lib, cfg, w, 8, 2, 16, n_pages=1)
+    first = dec.prefill({0: synth.gen_prompts(cfg, 1, 9)[0]})
+    dec.update(parents=[0, 0])
+    dec.synchronize()
+    keep = [x.clone() for x in (dec.k, dec.v, dec.table, dec.lens, dec.refs)]
+    got, path, count = dec.verify([[int(first[0]), 3]], [[-1, 0]], [1])
+    with pytest.raises(MkError) as e:
+        dec.synchronize()
+    assert e.value.status == MK_ERR_PAGES
+    assert count.tolist() == [0] and got.tolist() == [[-1, -1]] and path.tolist() == [[-1, -1]]
+    assert all(torch.equal(x, y) for x, y in zip(keep, (dec.k, dec.v, dec.table, dec.lens, dec.refs)))
+    # an error that nobody has read yet (a refused update, which changes nothing): nothing either, then all is as ever
+    dec.update(parents=[0, -1])
+    dec.update(reserve=[16, 0])
+    got, path, count = dec.verify([[int(first[0]), 3]], [[-1, 0]], [0])
+    assert count.tolist() == [0] and dec.lens.tolist() == [9, 0]
+    with pytest.raises(MkError):
+        dec.synchronize()
+    got, path, count = dec.verify([[int(first[0]), 3]], [[-1, 0]], [0])
+    dec.synchronize()
+    assert count.item() >= 1 and dec.lens.tolist() == [9 + count.item(), 0]
+    dec.close()
