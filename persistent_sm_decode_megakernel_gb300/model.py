@@ -303,7 +303,7 @@ class PagedDecoder:
         with torch.cuda.stream(self.stream):
             for t in (tokens, parents, lens, rows, logits):
                 self._used(t)
-            out = torch.empty(shape, dtype=torch.int32, device=self.k.device)
+            out = torch.full(shape, -1, dtype=torch.int32, device=self.k.device)   # (what a step leaves that ends early)
             check(mk_decode_step_tree(self.h, tokens.data_ptr(), lens.data_ptr(), parents.data_ptr(),
                                       rows.data_ptr() if rows is not None else None, shape[0], shape[1], out.data_ptr(),
                                       logits.data_ptr() if logits is not None else None), "mk_decode_step_tree")
@@ -312,15 +312,20 @@ class PagedDecoder:
     def verify(self, tokens, parents, rows, logits=None):
         """Reserves pages for trees of drafted tokens, runs one step over them and takes over what the model agrees with
         (paged.accept_drafts): tokens and parents [len(rows), nodes] for different table rows `rows` (numbers), node 0 of
-        each being the token that stands.  lens of the rows grows; other rows
+        each being the token that stands; absent nodes' tokens have to be some too.  lens of the rows grows; other rows
         keep the pages that they reserved.  Returns the next tokens, the accepted nodes (both [len(rows), nodes], -1 behind
         the last) and their number [len(rows)], on the device.  Synchronize reports what went wrong there: where the pages
-        do not suffice, or an error that self.status holds is still to be read, no row takes anything over."""
+        do not suffice, a token is none, the step did not come to its end or an error that self.status holds is still to be
+        read, no row takes anything over."""
         n_rows = self.table.shape[0]
         rows = [int(r) for r in rows]
         if len(set(rows)) != len(rows) or any(not 0 <= r < n_rows for r in rows):
             raise ValueError("rows must be different rows of the table")
         with torch.cuda.stream(self.stream):
+            if not torch.is_tensor(tokens):
+                tokens = torch.as_tensor(tokens, dtype=torch.int32)
+            if not tokens.is_cuda and ((tokens < 0) | (tokens >= self.dm.cfg.vocab)).any():
+                raise ValueError("tokens must be in [0, vocab)")
             tokens, parents = self._used(self._int32(tokens)).contiguous(), self._used(self._int32(parents)).contiguous()
             if tokens.dim() != 2 or tokens.shape[0] != len(rows) or tokens.shape[1] < 1 or parents.shape != tokens.shape:
                 raise ValueError("tokens and parents must be [rows, nodes]")
@@ -334,11 +339,11 @@ class PagedDecoder:
             reserve[at.long()] = nodes
             self.update(reserve=reserve)
             # what the device finds wrong makes every node absent
-            right = self.status[0] == 0
+            right = (self.status[0] == 0) & ((tokens >= 0) & (tokens < self.dm.cfg.vocab)).all()
             parents = torch.where(right, parents, -2)
             out = self.step_tree(tokens, parents, self.lens[at.long()], at, logits)
             every = torch.full((3, n_rows, nodes), -2, dtype=torch.int32, device=self.k.device)   # rows without a tree: absent
-            every[:, at.long()] = torch.stack((tokens, parents, out))
+            every[:, at.long()] = torch.stack((tokens, torch.where((out >= 0).all(), parents, -2), out))
             accepted = self.paged.accept_drafts(self.k, self.v, self.table, self.lens, *every, status=self.status)
             return tuple(x[at.long()] for x in accepted)
 

@@ -247,3 +247,28 @@ def test_verify_without_pages_takes_nothing_over(lib):
     dec.synchronize()
     assert count.item() >= 1 and dec.lens.tolist() == [9 + count.item(), 0]
     dec.close()
+
+
+def test_verify_of_tokens_that_are_none_takes_nothing_over(lib):
+    from persistent_sm_decode_megakernel_gb300 import MkError
+    cfg = synth.CONFIGS["tiny"]
+    w = synth.gen_weights(cfg)
+    dec = _paged(lib, cfg, w, 8, 2, 64)
+    first = int(dec.prefill({0: synth.gen_prompts(cfg, 1, 9)[0]})[0])
+    for bad in (-1, cfg.vocab, -2 ** 31):
+        with pytest.raises(ValueError):
+            dec.verify([[first, bad]], [[-1, 0]], [0])
+        keep = [x.clone() for x in (dec.lens, dec.k[:, :, :, :9], dec.v[:, :, :, :9])]
+        got, path, count = dec.verify(dec._int32([[first, bad]]), dec._int32([[-1, 0]]), [0])
+        with pytest.raises(MkError):
+            dec.synchronize()
+        dec.reset()
+        dec.synchronize()
+        assert count.tolist() == [0] and path.tolist() == [[-1, -1]]
+        assert all(torch.equal(x, y) for x, y in zip(keep, (dec.lens, dec.k[:, :, :, :9], dec.v[:, :, :, :9])))
+    with pytest.raises(ValueError):
+        dec.verify(torch.tensor([[first, cfg.vocab]]), [[-1, 0]], [0])
+    _, _, count = dec.verify([[first, 1]], [[-1, 0]], [0])
+    dec.synchronize()
+    assert count.item() >= 1
+    dec.close()
