@@ -351,7 +351,8 @@ class PagedDecoder:
         """Greedy decoding of n_new tokens after one prompt in table row 0 (freed before and after), several of them per
         step where `draft` guesses them: draft(tokens so far) gives drafted tokens and their parents (lists; a parent is
         a lower drafted token's number, or -1 for one that follows the tokens so far), as many as fit max_batch - 1.
-        The result is what single steps give, whatever the drafts: (tokens, number of steps); it ends with eos."""
+        The result is what single steps give, whatever the drafts, but where two logits lie as near to one another as sums
+        in another order can be: (tokens, number of steps); it ends with eos."""
         n_rows = self.table.shape[0]
         if n_new < 1 or len(prompt) < 1 or len(prompt) + n_new - 1 > self.max_positions:
             raise ValueError("the prompt and the new tokens must be positive and fit max_positions")
@@ -363,9 +364,10 @@ class PagedDecoder:
             while len(tokens) < n_new and tokens[-1] != eos:
                 guessed, parents = draft(prompt + tokens)
                 room = min(self.dm.max_batch, self.max_positions - len(prompt) - len(tokens) + 1) - 1
-                guessed, parents = self._tokens(guessed)[:room], [int(p) for p in parents][:room]
+                guessed, parents = self._tokens(guessed), [int(p) for p in parents]
                 if len(guessed) != len(parents) or any(not -1 <= p < i for i, p in enumerate(parents)):
                     raise ValueError("a drafted token's parent must be a lower one's number or -1")
+                guessed, parents = guessed[:room], parents[:room]
                 got, _, count = self.verify([[tokens[-1]] + guessed], [[-1] + [p + 1 for p in parents]], [0])
                 self.synchronize()
                 steps += 1

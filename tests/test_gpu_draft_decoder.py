@@ -272,3 +272,12 @@ def test_verify_of_tokens_that_are_none_takes_nothing_over(lib):
     dec.synchronize()
     assert count.item() >= 1
     dec.close()
+
+
+def test_drafts_of_two_lengths_are_refused_however_long(lib):
+    cfg = synth.CONFIGS["tiny"]
+    dec = _paged(lib, cfg, synth.gen_weights(cfg), 4, 1, 48)
+    for bad in (([1] * 9, [-1] * 8), ([1] * 8, [-1] * 7 + [8]), ([1] * 7 + [cfg.vocab], [-1] * 8)):
+        with pytest.raises(ValueError):
+            dec.generate([1, 2], 3, lambda t, bad=bad: bad)
+    dec.close()
