@@ -526,8 +526,8 @@ mk_status mk_beam_select_workspace(int groups, int beams, int vocab, size_t* byt
  * infinite, as does a NaN key; an infinite key does, unless the query is of the cache's type and
  * the scores stay below +inf.  A probability has 22 bits over an fp16 cache, over a bf16
  * cache 16 where out has 16 bits and 24 where it has 32.  The sums of values, which the tensor cores
- * cut off instead of rounding, are off by at most 2^-16 of sum p |v| in 32-bit outputs (measured: 3e-6), by
- * 2^-14 in fp16 ones, by 2^-11 in bf16 ones, at any length. */
+ * cut off instead of rounding, are off by at most 2^-16 of sum p |v| in 32-bit outputs (measured: 3e-6) and by
+ * 2^-14 in 16-bit ones, at any length. */
 typedef struct {
   const void* q;           /* [n_rows][n_nodes][n_heads][head_dim], element strides below    */
   void* out;               /* its vectors must not overlap                                  */

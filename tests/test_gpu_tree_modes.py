@@ -193,6 +193,22 @@ def test_long_sums_of_16_bits(paged, nodes, rows):  # noqa: F811
     assert off.mean().abs() <= 512 * 2.0 ** -23 + 3 * 2.0 ** -12 / math.sqrt(3 * 256)
 
 
+@pytest.mark.parametrize("nodes,rows", [(33, 80), (2, 160)])
+def test_long_sums_of_bf16(paged, nodes, rows):  # noqa: F811
+    """Of each 64 values 33 are 1 + 2^-7 and 31 are 1, whose mean lies 2^-13 above the middle of these neighbours; weights of about
+    the same size (a deviation of 0.2, and of the mean 2^-7 * 0.2 / 2 / sqrt(n), 2e-6) hardly move it.  Sums that lose 2^-14
+    of themselves at most leave it above, and it is rounded up."""
+    g = gen(27)
+    n, hkv, hd = 131072, 2, 64
+    kp = torch.randn(n // 64 + 1, hkv, 64, hd, generator=g, device=DEV).bfloat16()
+    vp = torch.ones_like(kp)
+    vp[:, :, torch.randperm(64, generator=g, device=DEV)[:33]] = 1 + 2.0 ** -7
+    q = torch.randn(rows, nodes, 4 * hkv, hd, generator=g, device=DEV).mul_(0.2).bfloat16()
+    out = paged.tree_attention(q, kp, vp, ints([list(range(len(kp)))]), ints([n] * rows), ints([[-1] + [0] * (nodes - 1)] * rows),
+                               rows=ints([0] * rows))
+    assert torch.all(out == 1 + 2.0 ** -7)
+
+
 def test_a_window_of_one_past_a_full_table_is_reported(paged):  # noqa: F811
     """A sequence that fills its table: every node's own slot is past it.  Nothing is seen, and it is told, unless no node is there."""
     from persistent_sm_decode_megakernel_gb300 import MK_ERR_PAGES, MkError
