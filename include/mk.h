@@ -526,8 +526,8 @@ mk_status mk_beam_select_workspace(int groups, int beams, int vocab, size_t* byt
  * infinite, as does a NaN key; an infinite key does, unless the query is of the cache's type and
  * the scores stay below +inf.  A probability has 22 bits over an fp16 cache, over a bf16
  * cache 16 where out has 16 bits and 24 where it has 32.  The sums of values, which the tensor cores
- * cut off instead of rounding, are off by at most 2^-16 of sum p |v| in 32-bit outputs (measured: 3e-6) and by
- * 2^-14 in 16-bit ones, at any length. */
+ * cut off instead of rounding, are off by at most 2^-16 of sum p |v| in 32-bit outputs (measured: up to 8e-6
+ * where all values have one sign) and by 2^-14 in 16-bit ones, at any length. */
 typedef struct {
   const void* q;           /* [n_rows][n_nodes][n_heads][head_dim], element strides below    */
   void* out;               /* its vectors must not overlap                                  */
@@ -649,8 +649,8 @@ mk_status mk_decode_step_paged(mk_ctx* ctx, const int32_t* tok, const int32_t* p
 /* One step over trees of drafted tokens, all in device memory: node i of row r is token
  * tok[r][i] with parent parents[r][i] (mk_tree_attention's), behind the lens[r] cached positions
  * of table row rows[r] (NULL: row r); its position is lens[r] + the number of its ancestors, its key and
- * value go to slot lens[r] + i, which needs its page before the call.  n_rows * n_nodes is at most
- * max_batch.  out_tok [n_rows][n_nodes] (or NULL) receives the argmax after each node, logits
+ * value go to slot lens[r] + i, which needs its page before the call; no table row may be given twice
+ * (its nodes' slots would be one another's).  n_rows * n_nodes is at most max_batch.  out_tok [n_rows][n_nodes] (or NULL) receives the argmax after each node, logits
  * [n_rows][n_nodes][vocab] (or NULL) the logits; what an absent node gets means nothing (its token still has
  * to be one).  mk_accept_drafts takes the drafts over.  Asynchronous, errors and captures as
  * mk_decode_step_paged's. */

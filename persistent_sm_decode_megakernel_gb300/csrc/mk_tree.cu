@@ -10,10 +10,11 @@
 //
 // Bound: the tensor cores, next to the keys' and values' bytes.  A tile of 64 slots costs a block of 128 rows 8 products
 // for the scores, each 48 cycles (with both operands in shared memory its traffic decides: 64 columns take 48, not 32),
-// and 4 of 64 for the values at 128 dims: two blocks of 16-bit queries 1280 cycles, the tile's arrival at the copy
-// bandwidth 1100 to 1400, by the clock.  16 rows of 64 nodes over 16384 to 32768 positions, 32 heads over 8: 348 us, 4.9
-// TB/s and 1.23 PFLOP/s; one row of 16 nodes over 32768, 32-bit queries in two parts: 39.5 us; one of 8 nodes over 512: 12.3
-// us, the latency of a piece (7 us, most of it code executed for the first time) and of the join (3 us).
+// and 4 of 64 for each part of the probabilities at 128 dims: two blocks of 16-bit queries 1792 cycles, the tile's arrival
+// at the copy bandwidth 1100 to 1400, by the clock.  16 rows of 64 nodes over 16384 to 32768 positions, 32 heads over 8: 443 us,
+// 3.8 TB/s and 0.97 PFLOP/s of the 32-bit product (half as much again is multiplied); one row of 16 nodes over 32768, 32-bit
+// queries in two parts: 38.5 us; one of 8 nodes over 512: 12.9 us, the latency of a piece (7 us, most of it code executed
+// for the first time) and of the join (3 us).
 //
 // The work is split as the single tokens' attention splits it: the segments (row, kv head), each of its tiles,
 // follow one another in one line; every CTA of one wave takes an equal share of it; the pieces of a segment that
@@ -203,9 +204,9 @@ __device__ __forceinline__ int page_index(const TreeArgs& a, int slot) {
 // the node of a block that a row of it is of: row / group, exact for rows below 128 and groups up to 16
 __device__ __forceinline__ int node_of(const TreeArgs& a, int row) { return row * a.group_inverse >> 16; }
 
-// Waits for a phase of a barrier, a whole warp together (what follows may need it so), false where it did not come: a wait that takes too long sets *abort, and from then
-// on none waits: the work goes on over whatever lies there, within its bounds, to its end.  With abort NULL: up to
-// the limit in any case (what is in flight when a CTA ends).
+// Waits for a phase of a barrier, a whole warp together (what follows may need it so), false where it did not come: a wait
+// that takes too long sets *abort, and from then on none waits: the work goes on over whatever lies there, within its bounds,
+// to its end.  With abort NULL: up to the limit in any case (what is in flight when a CTA ends).
 // A barrier tells two phases apart: nobody looks for a phase before the one before it is over, nor after the next one is.
 // Each phase is answered by its waiters before the next can end, and a ring's loads are waited for one by one, in order.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* abort) {
@@ -292,7 +293,8 @@ __device__ __forceinline__ float capped_fine(float x, float cap) {
 
 // A row's sums from tensor memory to the workspace, added to `f` times those that are there (-1: none are), and zeros in their
 // place; and back, to be added once more.  (A row's words are its own thread's.  Calls, so that the loop over the tiles, which is
-// short of registers, has no part of it; what only adds does not wait for what is there.)
+// short of registers, has no part of it.  What only adds does not wait for what is there; sums below the normal numbers it
+// takes for zero.)
 template <int HD>
 __device__ __noinline__ void put_away(uint32_t t_o, float* sums, int rows, float f) {
   const bool fresh = f < 0.f, adds = __all_sync(0xffffffffu, f == 1.f);
@@ -1200,8 +1202,8 @@ mk_status launch_tree(const TreeArgs& a, const mk_page_view& view, bool pair, in
     if (pair) return launch_mode<C, Q, HD, NQ, NP, PAIR_MODE>(a, view, n_sm, stream);
   }
   // SOLO where there are segments enough for a third of the CTAs (8 nodes, 8 kv heads, bf16: 16 rows of 4500 to 9000
-  // positions 79.6 us, TURNS 98.3; 64 rows 267, 342), TURNS where there are fewer and a piece's latency counts
-  // (one row of 512 positions 12.3 us, SOLO 12.6; one of 32768 39.4, 42.0)
+  // positions 79 us, TURNS 102; 64 rows 279, 373), TURNS where there are fewer and a piece's latency counts (32-bit queries
+  // over fp16, one row of 512 positions: 13.2 us, SOLO 13.8; one of 32768 38.7, 40.4)
   const bool solo = 3LL * a.n_rows * a.hkv * a.parts >= n_sm;
   if (solo && Shape<C, Q, HD, NQ, NP, SOLO_MODE>::bytes(a.q_rows) <= kSmemBytes)
     return launch_mode<C, Q, HD, NQ, NP, SOLO_MODE>(a, view, n_sm, stream);

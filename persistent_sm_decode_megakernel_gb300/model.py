@@ -286,7 +286,7 @@ class PagedDecoder:
 
     def step_tree(self, tokens, parents, lens, rows=None, logits=None):
         """One step over trees of drafted tokens (mk_decode_step_tree): device int32 tokens and parents [rows, nodes]
-        behind the first lens [rows] positions of table rows `rows` (default i).  The argmax after each node
+        behind the first lens [rows] positions of different table rows `rows` (default i).  The argmax after each node
         [rows, nodes]; the nodes' slots need their pages (update).  It runs on self.stream, where its tensors have to be
         ready; they may be dropped as soon as it returns."""
         from . import mk_decode_step_tree
