@@ -209,6 +209,52 @@ def test_long_sums_of_bf16(paged, nodes, rows):  # noqa: F811
     assert torch.all(out == 1 + 2.0 ** -7)
 
 
+@pytest.mark.parametrize("cache,vec,nodes,rows", [("f16", "f32", 4, 45), ("bf16", "f32", 4, 45), ("f16", "f16", 40, 45), ("bf16", "f32", 40, 25)])
+@pytest.mark.parametrize("falling", [False, True])
+def test_long_sums_under_growing_maxima(paged, cache, vec, nodes, rows, falling):  # noqa: F811
+    """Scores that rise along the sequence by far more than a maximum may be passed by, so that what was put away is worth ever
+    less, or fall, so that what comes is."""
+    g = gen(29)
+    n, hkv, hd = 24000, 4, 64
+    kp, vp, table = make_cache(g, [n + nodes], hkv, hd, 64, cache)
+    place = torch.empty(kp.shape[0], device=DEV)
+    place[ints(table[0, :-1]).long()] = torch.linspace(0, 4, table.shape[1] - 1, device=DEV)
+    kp = (kp.float() * (4 - place if falling else place)[:, None, None, None]).to(kp.dtype)
+    q = torch.randn(rows, nodes, 2 * hkv, hd, generator=g, device=DEV).mul_(2).to(TYPES[vec])
+    lens, parents = [n] * rows, [[-1] + [0] * (nodes - 1)] * rows
+    out, lse = paged.tree_attention(q, kp, vp, ints(table), ints(lens), ints(parents), rows=ints([0] * rows), return_lse=True)
+    for r in (0, rows - 1):
+        check(q[r:r + 1], kp, vp, table, lens[:1], parents[:1], out[r:r + 1], lse[r:r + 1])
+
+
+@pytest.mark.parametrize("cache,vec,nodes,rows", [("f16", "f32", 4, 40), ("bf16", "bf16", 40, 20), ("bf16", "f32", 40, 20)])
+def test_long_sums_repeat_bit_for_bit(paged, cache, vec, nodes, rows):  # noqa: F811
+    """Sums that are put away: the same call again, and two captured graphs at the same time on two streams."""
+    g = gen(28)
+    n, hkv, hd = 30000, 4, 64
+    kp, vp, table = make_cache(g, [n + nodes], hkv, hd, 64, cache)
+    tb, ls = ints(table), ints([n - 100 * r for r in range(rows)])
+    tree, at = ints(trees(np.random.default_rng(28), rows, nodes, "random")), ints([0] * rows)
+    qs = [torch.randn(rows, nodes, 4 * hkv, hd, generator=g, device=DEV).mul_(2).to(TYPES[vec]) for _ in range(2)]
+    call = lambda q: paged.tree_attention(q, kp, vp, tb, ls, tree, rows=at, return_lse=True)  # noqa: E731
+    want = [call(q) for q in qs]
+    assert all(torch.isfinite(w[0]).all() for w in want)
+    assert all(torch.equal(x, y) for x, y in zip(want[0], call(qs[0])))
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for q in qs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(call(q))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, graph in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(x, y) for x, y in zip(w, o))
+
+
 def test_a_window_of_one_past_a_full_table_is_reported(paged):  # noqa: F811
     """A sequence that fills its table: every node's own slot is past it.  Nothing is seen, and it is told, unless no node is there."""
     from persistent_sm_decode_megakernel_gb300 import MK_ERR_PAGES, MkError
